@@ -237,6 +237,123 @@ pkv_status pkv_paged_attention_decode_noalloc(
     float scale, pkv_dtype dtype, int partition_tokens, void* stream);
 
 /* ------------------------------------------------------------------ *
+ * Decoding against a bounded cache
+ *
+ * Two ways to keep a sequence's cache from growing with its context: a
+ * sliding window with sinks (blocks outside it go back to the pool,
+ * pkv_alloc_release_window), and eviction by accumulated attention weight
+ * (decode with pkv_paged_attention_decode_accumulate, evict with
+ * pkv_evict_tokens, free the blocks past the new length with
+ * pkv_alloc_truncate).  Not on the pages.
+ *
+ * These calls take grouped heads: H query heads on Hkv KV heads, H a
+ * multiple of Hkv, at most 16 query heads per KV head (PKV_ERR_UNSUPPORTED
+ * above); query head h uses KV head h / (H / Hkv).  The caches are then
+ * [NB][bs][Hkv][D], as pkv_reshape_and_cache and pkv_copy_blocks lay them
+ * out for H = Hkv.  NB * bs must fit 31 bits; S at most 32767.
+ * ------------------------------------------------------------------ */
+
+/* Bytes of workspace for pkv_paged_attention_decode_window (0 for invalid
+ * arguments); it does not depend on the context lengths. */
+size_t pkv_decode_window_workspace_size(int S, int H, int Hkv, int D);
+
+/* Decode attention with a sliding window and sinks.  With n =
+ * context_lens[s], the query of sequence s (its token n - 1) sees the tokens
+ *   j < sink_tokens  or  j >= n - window,   j < n:
+ *   out[s,h,:] = sum_j softmax_j(scale * q[s,h,:] . K_j) V_j over those j.
+ * n = 0 gives out = 0; window >= n is plain attention.  Blocks that hold no
+ * visible token are neither read nor looked up: their table entries may be
+ * anything (-1 once released).
+ *   out, q        [S][H][D] dtype
+ *   window        >= 1; sink_tokens >= 0
+ *   max_context_len  upper bound of context_lens (0 = MB*bs)
+ *   workspace     256-byte aligned device memory of at least
+ *                 pkv_decode_window_workspace_size bytes, no initial contents
+ *                 needed; one call at a time may use it
+ *   other arguments as in pkv_paged_attention_decode.
+ * Computation is fp32; attention weights enter P.V as the sum of two 16-bit
+ * numbers (relative error 2^-16 at most for bf16); one rounding to dtype at
+ * the end.  Equal inputs give equal bits.  A visible V element that is not
+ * finite makes its output elements not finite. */
+pkv_status pkv_paged_attention_decode_window(
+    void* out, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens,
+    int S, int H, int Hkv, int D, int bs, int NB, int MB, int max_context_len,
+    int window, int sink_tokens, float scale, pkv_dtype dtype,
+    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for pkv_paged_attention_decode_accumulate (0 for
+ * invalid arguments): the logits of every query head take 4 * S * H *
+ * max_context_len of them. */
+size_t pkv_decode_accumulate_workspace_size(int S, int H, int Hkv, int D, int max_context_len);
+
+/* Decode attention that also adds every token's attention weight to a
+ * running score: out as pkv_paged_attention_decode gives it (with grouped
+ * heads), and for j < n = context_lens[s]
+ *   scores[s,g,j] += sum over the query heads h of KV head g of
+ *                    softmax_j(scale * q[s,h,:] . K_j).
+ * Entries at j >= n are not touched.  A new sequence's row starts as zeros;
+ * rows belong to the sequence, not to its blocks: whoever reorders or forks
+ * sequences moves or copies their rows.
+ *   scores        [S][Hkv][score_stride] fp32 device memory
+ *   score_stride  >= max_context_len
+ *   max_context_len  upper bound of context_lens (0 = MB*bs); sizes the
+ *                 workspace
+ *   other arguments as in pkv_paged_attention_decode_window.  Each score is
+ *   added to by one thread in a fixed order: equal inputs give equal bits. */
+pkv_status pkv_paged_attention_decode_accumulate(
+    void* out, float* scores, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens,
+    int S, int H, int Hkv, int D, int bs, int NB, int MB, int max_context_len,
+    int64_t score_stride, float scale, pkv_dtype dtype,
+    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for pkv_evict_tokens (0 for invalid arguments). */
+size_t pkv_evict_workspace_size(int S, int Hkv, int budget);
+
+/* Eviction by accumulated attention weight.  For every sequence s with n =
+ * context_lens[s] > budget, and every KV head on its own: keep `budget`
+ * tokens and compact the cache to them.
+ *   position of token j: positions[s,g,j] if >= 0, else token_counts[s] - n + j
+ *     (tokens appended since the last eviction need no entry);
+ *   protected: position < sink_tokens or >= token_counts[s] - recent_tokens;
+ *   kept: the `budget` best by (protected, score, lowest j).  NaN counts as
+ *     -infinity.
+ * The i-th kept token at j >= budget (ascending) moves into the i-th evicted
+ * place below budget (ascending): K row, V row, score and position of that
+ * head.  Attention does not depend on the order of a head's tokens (rotary or
+ * other position encodings are in K already), so the heads of one token row
+ * may then hold different tokens.
+ * After: entries [budget, n) have score 0 and position -1, entries < budget
+ * their true position, new_context_lens[s] = min(n, budget).  A sequence with
+ * n <= budget keeps everything (its entries < n are copied when the outputs
+ * are other arrays).  Entries >= n are not touched; cache rows at or past
+ * budget keep their old contents.
+ *   k_cache, v_cache  [NB][bs][Hkv][D] dtype, compacted in place.  The blocks
+ *                 of an evicted sequence must be its own (refcount 1:
+ *                 pkv_alloc_unshare first)
+ *   scores, positions  [S][Hkv][score_stride] fp32 and int32; fresh rows hold
+ *                 0 and -1
+ *   scores_out, positions_out  the same shapes; each may be its input (in
+ *                 place) or an array that does not overlap it
+ *   context_lens, token_counts  [S] int32: tokens cached (at most MB*bs and
+ *                 score_stride) and tokens seen (>= context_lens[s]); others
+ *                 are clamped and set PKV_DEVERR_CONTEXT
+ *   new_context_lens  [S] int32, written; not context_lens itself
+ *   budget        >= 1, >= sink_tokens + recent_tokens
+ *   workspace     256-byte aligned, pkv_evict_workspace_size bytes; one call
+ *                 at a time may use it
+ * The call may be repeated with the same inputs (outputs in other arrays): it
+ * writes the same caches. */
+pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
+                            const int32_t* positions, const int32_t* block_tables,
+                            const int32_t* context_lens, const int32_t* token_counts,
+                            float* scores_out, int32_t* positions_out, int32_t* new_context_lens,
+                            int S, int Hkv, int D, int bs, int NB, int MB, int64_t score_stride,
+                            int budget, int recent_tokens, int sink_tokens, pkv_dtype dtype,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ *
  * Cache maintenance kernels
  * ------------------------------------------------------------------ */
 
@@ -407,6 +524,34 @@ pkv_status pkv_alloc_append_batch(pkv_allocator* a, int32_t* tables, int32_t* nu
  * release that would underflow changes nothing (PKV_ERR_INVALID_ARG). */
 pkv_status pkv_alloc_fork(pkv_allocator* a, int32_t* tables, int32_t* num_blocks, int32_t S,
                           int32_t MB, const int32_t* parents);
+
+/* The first n blocks of a row made the row's own before they are written in
+ * place (pkv_evict_tokens): every one of table[0..n) with refcount > 1 is
+ * copied-on-write, in order, as pkv_alloc_cow does; (src, dst) pairs go to
+ * pairs[2*k], pairs[2*k+1] (room for n) and *n_pairs receives their number.
+ * All-or-nothing. */
+pkv_status pkv_alloc_unshare(pkv_allocator* a, int32_t* table, int32_t n, int64_t* pairs,
+                             int32_t* n_pairs);
+
+/* Release the blocks a row no longer needs when it holds `tokens` tokens
+ * (after pkv_evict_tokens): entries from ceil(tokens/bs) on lose one holder,
+ * last first, and become -1; *num_blocks = min(*num_blocks, ceil(tokens/bs)).
+ * Entries that are -1 already (pkv_alloc_release_window) are passed over.
+ * *num_freed (may be NULL) receives the number of blocks freed.
+ * All-or-nothing. */
+pkv_status pkv_alloc_truncate(pkv_allocator* a, int32_t* table, int32_t* num_blocks,
+                              int32_t tokens, int32_t bs, int32_t* num_freed);
+
+/* Release the blocks of a row that a sliding window has passed: with
+ * context_len tokens cached and attended to, no later query sees the tokens
+ * [sink_tokens, context_len + 1 - window).  Every block that lies wholly in
+ * that range loses one holder (ascending) and its entry becomes -1;
+ * *num_blocks does not change.  A row with such entries can be appended to
+ * and truncated, not forked.  *num_freed (may be NULL) receives the number of
+ * blocks freed.  All-or-nothing. */
+pkv_status pkv_alloc_release_window(pkv_allocator* a, int32_t* table, int32_t num_blocks,
+                                    int32_t context_len, int32_t window, int32_t sink_tokens,
+                                    int32_t bs, int32_t* num_freed);
 
 /* Reference count of block id (0 = free). */
 pkv_status pkv_alloc_refcount(const pkv_allocator* a, int32_t id, int32_t* rc);

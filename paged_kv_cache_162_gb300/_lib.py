@@ -52,6 +52,7 @@ class OutOfBlocks(PkvError, MemoryError):
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 
@@ -69,6 +70,15 @@ SIGNATURES = {
                                                       _I, _I, _I, _I, _F, _I, _I, _P, _SZ, _P]),
     "pkv_paged_attention_decode_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
                                                 _I, _F, _I, _I, _P]),
+    "pkv_decode_window_workspace_size": (_SZ, [_I, _I, _I, _I]),
+    "pkv_paged_attention_decode_window": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
+                                               _I, _I, _I, _F, _I, _P, _SZ, _P]),
+    "pkv_decode_accumulate_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "pkv_paged_attention_decode_accumulate": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
+                                                   _I, _I, _I, _I64, _F, _I, _P, _SZ, _P]),
+    "pkv_evict_workspace_size": (_SZ, [_I, _I, _I]),
+    "pkv_evict_tokens": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I64,
+                              _I, _I, _I, _I, _P, _SZ, _P]),
     "pkv_compute_slot_mapping": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P]),
     "pkv_reshape_and_cache": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "pkv_copy_blocks": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
@@ -87,6 +97,9 @@ SIGNATURES = {
     "pkv_alloc_append": (_I, [_P, _P, _P, _I32, _I32, _I32, _I32, _P, _P]),
     "pkv_alloc_append_batch": (_I, [_P, _P, _P, _I32, _I32, _P, _P, _I32, _P, _I32, _P, _P]),
     "pkv_alloc_fork": (_I, [_P, _P, _P, _I32, _I32, _P]),
+    "pkv_alloc_unshare": (_I, [_P, _P, _I32, _P, _P]),
+    "pkv_alloc_truncate": (_I, [_P, _P, _P, _I32, _I32, _P]),
+    "pkv_alloc_release_window": (_I, [_P, _P, _I32, _I32, _I32, _I32, _I32, _P]),
     "pkv_alloc_refcount": (_I, [_P, _I32, _P]),
     "pkv_alloc_num_blocks": (_I32, [_P]),
     "pkv_alloc_num_free": (_I32, [_P]),
@@ -206,6 +219,55 @@ def pkv_paged_attention_decode_noalloc(out, q, k_cache, v_cache, block_tables, c
         ptr(out), ptr(q), ptr(k_cache), ptr(v_cache), ptr(block_tables), ptr(context_lens), S, H,
         D, bs, NB, MB, max_context_len, float(scale), int(dtype), partition_tokens,
         stream_handle(stream)), "paged_attention_decode_noalloc")
+
+
+def pkv_decode_window_workspace_size(S, H, Hkv, D) -> int:
+    return int(lib().pkv_decode_window_workspace_size(S, H, Hkv, D))
+
+
+def pkv_paged_attention_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, S, H,
+                                      Hkv, D, bs, NB, MB, max_context_len, window, sink_tokens,
+                                      scale, dtype, workspace, workspace_bytes,
+                                      stream=None) -> None:
+    st = lib().pkv_paged_attention_decode_window(
+        ptr(out), ptr(q), ptr(k_cache), ptr(v_cache), ptr(block_tables), ptr(context_lens), S, H,
+        Hkv, D, bs, NB, MB, max_context_len, window, sink_tokens, scale, dtype, ptr(workspace),
+        workspace_bytes, stream_handle(stream))
+    if st:
+        check(st, "paged_attention_decode_window")
+
+
+def pkv_decode_accumulate_workspace_size(S, H, Hkv, D, max_context_len) -> int:
+    return int(lib().pkv_decode_accumulate_workspace_size(S, H, Hkv, D, max_context_len))
+
+
+def pkv_paged_attention_decode_accumulate(out, scores, q, k_cache, v_cache, block_tables,
+                                          context_lens, S, H, Hkv, D, bs, NB, MB, max_context_len,
+                                          score_stride, scale, dtype, workspace, workspace_bytes,
+                                          stream=None) -> None:
+    st = lib().pkv_paged_attention_decode_accumulate(
+        ptr(out), ptr(scores), ptr(q), ptr(k_cache), ptr(v_cache), ptr(block_tables),
+        ptr(context_lens), S, H, Hkv, D, bs, NB, MB, max_context_len, score_stride, scale, dtype,
+        ptr(workspace), workspace_bytes, stream_handle(stream))
+    if st:
+        check(st, "paged_attention_decode_accumulate")
+
+
+def pkv_evict_workspace_size(S, Hkv, budget) -> int:
+    return int(lib().pkv_evict_workspace_size(S, Hkv, budget))
+
+
+def pkv_evict_tokens(k_cache, v_cache, scores, positions, block_tables, context_lens, token_counts,
+                     scores_out, positions_out, new_context_lens, S, Hkv, D, bs, NB, MB,
+                     score_stride, budget, recent_tokens, sink_tokens, dtype, workspace,
+                     workspace_bytes, stream=None) -> None:
+    st = lib().pkv_evict_tokens(
+        ptr(k_cache), ptr(v_cache), ptr(scores), ptr(positions), ptr(block_tables),
+        ptr(context_lens), ptr(token_counts), ptr(scores_out), ptr(positions_out),
+        ptr(new_context_lens), S, Hkv, D, bs, NB, MB, score_stride, budget, recent_tokens,
+        sink_tokens, dtype, ptr(workspace), workspace_bytes, stream_handle(stream))
+    if st:
+        check(st, "evict_tokens")
 
 
 def pkv_compute_slot_mapping(slot_mapping, block_tables, seq_idx, pos, T, S, MB, bs,

@@ -124,6 +124,45 @@ class BlockAllocator:
         check(lib().pkv_alloc_fork(self._h, tables.ctypes.data, nblocks.ctypes.data, S, MB,
                                    par.ctypes.data), "alloc_fork")
 
+    def unshare(self, row: np.ndarray, n: int) -> np.ndarray:
+        """The first n blocks of `row` (int32, in place) made the row's own:
+        shared ones are copied-on-write.  Returns the copy pairs [P, 2]."""
+        _need_i32(row, "row")
+        n = int(n)
+        if not 0 <= n <= len(row):
+            raise PkvError(PKV_ERR_INVALID_ARG, "unshare: n must be in [0, len(row)]")
+        pairs = np.empty(2 * max(n, 1), dtype=np.int64)
+        npairs = ctypes.c_int32(0)
+        check(lib().pkv_alloc_unshare(self._h, row.ctypes.data, n, pairs.ctypes.data,
+                                      ctypes.addressof(npairs)), "alloc_unshare")
+        return pairs[:2 * npairs.value].reshape(-1, 2)
+
+    def truncate(self, row: np.ndarray, num_blocks: int, tokens: int, block_size: int):
+        """Releases the blocks `row` (int32, in place) does not need for
+        `tokens` tokens; returns (num_blocks, blocks freed)."""
+        _need_i32(row, "row")
+        if int(num_blocks) > len(row):
+            raise PkvError(PKV_ERR_INVALID_ARG, "truncate: num_blocks is past the row")
+        nb, freed = ctypes.c_int32(int(num_blocks)), ctypes.c_int32(0)
+        check(lib().pkv_alloc_truncate(self._h, row.ctypes.data, ctypes.addressof(nb), int(tokens),
+                                       int(block_size), ctypes.addressof(freed)), "alloc_truncate")
+        return int(nb.value), int(freed.value)
+
+    def release_window(self, row: np.ndarray, num_blocks: int, context_len: int, window: int,
+                       sink_tokens: int, block_size: int) -> int:
+        """Releases the blocks of `row` (int32, in place) that no query after
+        this context sees through the window; their entries become -1.
+        Returns the number of blocks freed."""
+        _need_i32(row, "row")
+        if int(num_blocks) > len(row):
+            raise PkvError(PKV_ERR_INVALID_ARG, "release_window: num_blocks is past the row")
+        freed = ctypes.c_int32(0)
+        check(lib().pkv_alloc_release_window(self._h, row.ctypes.data, int(num_blocks),
+                                             int(context_len), int(window), int(sink_tokens),
+                                             int(block_size), ctypes.addressof(freed)),
+              "alloc_release_window")
+        return int(freed.value)
+
     def refcount(self, block: int) -> int:
         rc = ctypes.c_int32(0)
         check(lib().pkv_alloc_refcount(self._h, int(block), ctypes.addressof(rc)),

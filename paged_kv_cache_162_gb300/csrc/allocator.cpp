@@ -334,6 +334,102 @@ pkv_status pkv_alloc_fork(pkv_allocator* a, int32_t* tables, int32_t* num_blocks
     return PKV_OK;
 }
 
+pkv_status pkv_alloc_unshare(pkv_allocator* a, int32_t* table, int32_t n, int64_t* pairs,
+                             int32_t* n_pairs) {
+    PKV_TRACE("pkv_alloc_unshare");
+    pkv::clear_error();
+    if (!a || n < 0 || !n_pairs || (n && !table)) return pkv::fail(PKV_ERR_INVALID_ARG, "alloc_unshare: bad argument");
+    *n_pairs = 0;
+    int32_t shared = 0;
+    for (int32_t j = 0; j < n; ++j) {
+        if (!valid_id(a, table[j]) || a->rc[table[j]] <= 0)
+            return pkv::fail(PKV_ERR_INVALID_ARG, "alloc_unshare: table holds a block that is not held");
+        shared += a->rc[table[j]] > 1;
+    }
+    if (shared && !pairs) return pkv::fail(PKV_ERR_INVALID_ARG, "alloc_unshare: pairs is null");
+    // a block twice in the row: its second entry is its own once the first
+    // has been copied, so this count is an upper bound
+    if (a->top < shared) return pkv::fail(PKV_ERR_OOM, "alloc_unshare: out of free blocks");
+    int32_t k = 0;
+    for (int32_t j = 0; j < n; ++j) {
+        const int32_t id = table[j];
+        if (a->rc[id] <= 1) continue;
+        const int32_t nid = pop(a);
+        set_rc(a, id, a->rc[id] - 1);
+        pairs[2 * k] = id;
+        pairs[2 * k + 1] = nid;
+        ++k;
+        table[j] = nid;
+    }
+    *n_pairs = k;
+    return PKV_OK;
+}
+
+namespace {
+
+// Releases table[j] for j in [lo, hi), in that order or backwards, passing
+// over -1 entries; nothing changes unless every other entry is held often
+// enough.
+pkv_status release_entries(pkv_allocator* a, int32_t* table, int64_t lo, int64_t hi, bool backwards,
+                           const char* what, int32_t* num_freed) {
+    for (int64_t j = lo; j < hi; ++j)
+        if (table[j] != -1 && !valid_id(a, table[j])) return pkv::fail(PKV_ERR_INVALID_ARG, what);
+    bool ok = true;
+    for (int64_t j = lo; j < hi; ++j)
+        if (table[j] != -1) ok = (a->rc[table[j]] -= 1) >= 0 && ok;
+    for (int64_t j = lo; j < hi; ++j)
+        if (table[j] != -1) a->rc[table[j]] += 1;  // undo the probe
+    if (!ok) return pkv::fail(PKV_ERR_INVALID_ARG, what);
+    int32_t freed = 0;
+    for (int64_t i = lo; i < hi; ++i) {
+        const int64_t j = backwards ? hi - 1 - (i - lo) : i;
+        const int32_t id = table[j];
+        if (id == -1) continue;
+        set_rc(a, id, a->rc[id] - 1);
+        if (a->rc[id] == 0) {
+            push(a, id);
+            ++freed;
+        }
+        table[j] = -1;
+    }
+    if (num_freed) *num_freed = freed;
+    return PKV_OK;
+}
+
+}  // namespace
+
+pkv_status pkv_alloc_truncate(pkv_allocator* a, int32_t* table, int32_t* num_blocks,
+                              int32_t tokens, int32_t bs, int32_t* num_freed) {
+    PKV_TRACE("pkv_alloc_truncate");
+    pkv::clear_error();
+    if (!a || !num_blocks || *num_blocks < 0 || tokens < 0 || bs <= 0 || (*num_blocks > 0 && !table))
+        return pkv::fail(PKV_ERR_INVALID_ARG, "alloc_truncate: bad argument");
+    const int64_t need = ((int64_t)tokens + bs - 1) / bs;
+    if (num_freed) *num_freed = 0;
+    if (need >= *num_blocks) return PKV_OK;
+    const pkv_status st = release_entries(a, table, need, *num_blocks, true,
+                                          "alloc_truncate: table holds a block that is not held", num_freed);
+    if (st == PKV_OK) *num_blocks = (int32_t)need;
+    return st;
+}
+
+pkv_status pkv_alloc_release_window(pkv_allocator* a, int32_t* table, int32_t num_blocks,
+                                    int32_t context_len, int32_t window, int32_t sink_tokens,
+                                    int32_t bs, int32_t* num_freed) {
+    PKV_TRACE("pkv_alloc_release_window");
+    pkv::clear_error();
+    if (!a || num_blocks < 0 || context_len < 0 || window < 1 || sink_tokens < 0 || bs <= 0 ||
+        (num_blocks > 0 && !table) || context_len > (int64_t)num_blocks * bs)
+        return pkv::fail(PKV_ERR_INVALID_ARG, "alloc_release_window: bad argument");
+    if (num_freed) *num_freed = 0;
+    const int64_t lo = ((int64_t)sink_tokens + bs - 1) / bs;        // first block past the sinks
+    const int64_t gone = (int64_t)context_len + 1 - window;        // tokens below this are out of sight
+    const int64_t hi = gone > 0 ? gone / bs : 0;
+    if (lo >= hi) return PKV_OK;
+    return release_entries(a, table, lo, hi, false,
+                           "alloc_release_window: table holds a block that is not held", num_freed);
+}
+
 pkv_status pkv_alloc_refcount(const pkv_allocator* a, int32_t id, int32_t* rc) {
     pkv::clear_error();
     if (!a || !rc || !valid_id(a, id)) return pkv::fail(PKV_ERR_INVALID_ARG, "alloc_refcount: bad argument");

@@ -1,0 +1,891 @@
+// Decode attention for bounded caches: a sliding window with sinks, and
+// attention that adds every token's weight to a running score.
+//
+// What it computes, for sequence s, query head h, KV head g = h / G, context
+// n, with z_j = scale q_h . K_j over the tokens j the query sees:
+//   out = sum_j 2^(z'_j - M) V_j / sum_j 2^(z'_j - M),  z' = z log2(e), M = max z'
+// window:      j < sinks or j >= n - window.  The nv = min(n, sinks + window)
+//   visible tokens are numbered v = 0 .. nv-1, token j = v below the sinks and
+//   v + (n - nv) above, so the gap is skipped by one addition per row and no
+//   block inside it is looked up.
+// accumulate:  every j < n; then scores[s, g, j] += sum_{h in g} p_hj with
+//   p_hj = 2^(z'_hj - M_h) / L_h.  p needs the whole row's M and L, so the z'
+//   are written to scratch as they are computed and read back once.
+//
+// How: a unit is one sequence and `hw` neighbouring KV heads; its visible
+// tokens go in tiles of 16.  One warp takes one KV head of a tile: K and V
+// rows come through a cp.async ring in shared memory (16-byte chunks, XOR
+// swizzle by row, rows without a token zero-filled and not read), the group's
+// G <= 16 query heads are the rows of m16n8k16 products on the tensor cores.
+// Memory is the bound: 512 bytes of K and V per (token, KV head) at D = 128
+// against 32 + 16 products of 16x8x16 per 8 KB tile.
+//   S = Q K^T, then the online softmax on the accumulators, then O += P V with
+//   P as the sum of two 16-bit numbers (its rounding and the rest): P rounded
+//   once would add an error as large as the output's own rounding.
+// A CTA is four warps: hw heads times 4 / hw token splits, joined in shared
+// memory.
+//
+// Two ways to spread the units:
+//  * direct: one CTA per unit, one launch, no workspace traffic but z'.
+//  * split: the tiles of all units, in order, are cut into one equal range per
+//    resident CTA.  A unit inside one range is finished there; a unit cut by
+//    range ends leaves (M, L, unnormalised out) per piece, and a second kernel
+//    (one CTA per range, the same ranges) joins the pieces of the units that
+//    begin in its range and folds its tokens' weights into the scores.  Ranges
+//    are computed from the lengths on the device by every CTA, so a call needs
+//    no plan, no counter and no ticket, and every sum has a fixed order.
+#include <climits>
+#include <cmath>
+#include <cstdio>
+#include <mutex>
+
+#include "pagedkv.h"
+#include "pkv_device.cuh"
+#include "pkv_mma.cuh"
+
+namespace {
+
+using pkv::cp_async16_zfill;
+using pkv::cp_async_commit;
+using pkv::cp_async_wait;
+using pkv::ldsm_x4;
+using pkv::ldsm_x4_trans;
+using pkv::Mma;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTile = 16;
+constexpr int kMaxRanges = 512;    // CTAs of a split call
+constexpr int kMaxGroup = 16;      // query heads per KV head
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+constexpr int kStages = D == 128 ? 3 : 5;
+template <int D>
+constexpr int kTileBytes = kTile * D * 2;  // K (or V) of one tile and head
+template <int D>
+constexpr int kRingBytes = kStages<D> * 2 * kTileBytes<D>;  // one warp's ring
+template <int D>
+constexpr int kSmemBytes = kWarps * kRingBytes<D>;
+
+// What a range (one CTA of a split call) did, for the join kernel.
+struct RangeInfo {
+    int s, hb, tb;       // its first unit and the first tile taken of it
+    int tiles;           // tiles in the range, 0 = none
+    int first_c0;        // range where the first unit begins
+    int first_c1;        // range where the first unit ends
+    int last_c1;         // range where the last unit ends
+    int pad;
+};
+
+struct Params {
+    void* out;
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    int S, H, Hkv, G, NB, MB, bs_log2, max_ctx;
+    int window, sinks;   // accumulate: window = max_ctx
+    int hw, nsplit, HB;  // KV heads per CTA, warps per KV head, units per sequence
+    int direct;          // one CTA per unit
+    float qscale;        // scale * log2(e)
+    RangeInfo* info;     // [ranges]
+    float* part_m;       // [2 * ranges][hw * G]
+    float* part_l;
+    float* part_acc;     // [2 * ranges][hw * G][D]
+    float* row_m;        // [S][H]: M and L of units finished in one range
+    float* row_l;
+    float* z;            // [S][H][z_stride], accumulate only
+    int64_t z_stride;
+    float* scores;       // [S][Hkv][score_stride], accumulate only
+    int64_t score_stride;
+    int* err;
+};
+
+__device__ __forceinline__ int context_of(const Params& p, int s) {
+    const int n = __ldg(p.context_lens + s);
+    return n < 0 ? 0 : (n > p.max_ctx ? p.max_ctx : n);
+}
+
+__device__ __forceinline__ int visible_of(const Params& p, int n) {
+    const long long most = (long long)p.window + p.sinks;
+    return most < n ? (int)most : n;
+}
+
+// Tiles of a unit; an empty context has one, which writes zeros.
+__device__ __forceinline__ int tiles_of(const Params& p, int n) {
+    const int t = (visible_of(p, n) + kTile - 1) / kTile;
+    return t < 1 ? 1 : t;
+}
+
+// Running softmax of one warp over its tiles: rows lane/4 and lane/4 + 8 of
+// the accumulators, (m, l) per row.
+template <int D>
+struct Acc {
+    float o[D / 8][4];
+    float m[2], l[2];
+};
+
+// One warp: KV head kvh of sequence s, visible tiles first, first + step, ...
+// below te.  kWide: more than 8 query heads per KV head.
+template <class E, int D, bool kWide, bool kScores>
+__device__ __forceinline__ void attend(const Params& p, int s, int kvh, int n, int first, int te,
+                                       int step, uint32_t ring, int lane, Acc<D>& a) {
+    constexpr int NK = D / 16, NO = D / 8;
+    constexpr int ROWB = D * 2, CPR = ROWB / 16, CPL = kTile * CPR / 32;
+    constexpr int NST = kStages<D>;
+    constexpr int R = kWide ? 2 : 1;
+    const int g = lane >> 2, t = lane & 3;
+    const int nv = visible_of(p, n), shift = n - nv;
+    const int64_t row_elems = (int64_t)p.Hkv * D;
+    const int bs_mask = (1 << p.bs_log2) - 1;
+    const int32_t* bt = p.block_tables + (int64_t)s * p.MB;
+    const uint16_t* k_head = static_cast<const uint16_t*>(p.k_cache) + (int64_t)kvh * D;
+    const uint16_t* v_head = static_cast<const uint16_t*>(p.v_cache) + (int64_t)kvh * D;
+
+#pragma unroll
+    for (int j = 0; j < NO; ++j) a.o[j][0] = a.o[j][1] = a.o[j][2] = a.o[j][3] = 0.f;
+    a.m[0] = a.m[1] = -INFINITY;
+    a.l[0] = a.l[1] = 0.f;
+    if (first >= te) return;
+
+    // query fragments: rows g and g + 8 are heads kvh * G + row
+    uint32_t qa[NK][4];
+    {
+        const uint16_t* q0 = static_cast<const uint16_t*>(p.q) +
+                             ((int64_t)s * p.H + (int64_t)kvh * p.G + g) * D + 2 * t;
+        const bool r0 = g < p.G, r1 = kWide && g + 8 < p.G;
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+            qa[k][0] = r0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + 16 * k)) : 0u;
+            qa[k][1] = r1 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + 8 * D + 16 * k)) : 0u;
+            qa[k][2] = r0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + 16 * k + 8)) : 0u;
+            qa[k][3] = r1 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + 8 * D + 16 * k + 8)) : 0u;
+        }
+    }
+
+    // Row lane % 16 of tile i: its cache row, or -1 where there is no token
+    // (past the visible ones) or its block id is out of range.  NB * bs fits
+    // an int (checked on the host).
+    auto lookup = [&](int i) -> int {
+        const int v = i * kTile + (lane & 15);
+        if (i >= te || v >= nv) return -1;
+        const int tok = v < p.sinks ? v : v + shift;
+        const int phys = __ldg(bt + (tok >> p.bs_log2));
+        if ((unsigned)phys >= (unsigned)p.NB) {
+            pkv::report(p.err, PKV_DEVERR_BLOCK_ID);
+            return -1;
+        }
+        return (phys << p.bs_log2) | (tok & bs_mask);
+    };
+    unsigned mask[NST];  // rows with a token, of the tiles in flight
+    int slot = lookup(first);
+    // copies of tile i into ring stage `stage`, then the lookup for the next
+    auto issue = [&](int i, int stage) -> unsigned {
+        const unsigned rows = __ballot_sync(kFull, slot >= 0) & 0xffffu;
+        if (i < te) {
+            const uint32_t sk = ring + stage * 2 * kTileBytes<D>, sv = sk + kTileBytes<D>;
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) {
+                const int chunk = lane + 32 * j;
+                const int row = chunk / CPR, c = chunk % CPR;
+                const int sl = __shfl_sync(kFull, slot, row);
+                const int64_t off = (int64_t)(sl < 0 ? 0 : sl) * row_elems + c * 8;
+                const uint32_t dst = row * ROWB + ((c ^ (row & 7)) * 16);
+                const int bytes = sl < 0 ? 0 : 16;
+                cp_async16_zfill(sk + dst, k_head + off, bytes);
+                cp_async16_zfill(sv + dst, v_head + off, bytes);
+            }
+            slot = lookup(i + step);
+        }
+        cp_async_commit();  // empty past the end: the counting stays simple
+        return rows;
+    };
+
+#pragma unroll
+    for (int st = 0; st < NST - 1; ++st) mask[st] = issue(first + st * step, st);
+    int stage = 0;
+    for (int i = first; i < te; i += step) {
+        const int fill = stage == 0 ? NST - 1 : stage - 1;
+        mask[NST - 1] = issue(i + (NST - 1) * step, fill);
+        cp_async_wait<NST - 1>();
+        __syncwarp();
+        const uint32_t sk = ring + stage * 2 * kTileBytes<D>, sv = sk + kTileBytes<D>;
+
+        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        {
+            const int mi = lane >> 3;
+            const int row = (mi >> 1) * 8 + (lane & 7);
+#pragma unroll
+            for (int k = 0; k < NK; ++k) {
+                uint32_t b[4];
+                ldsm_x4(b, sk + row * ROWB + (((2 * k + (mi & 1)) ^ (row & 7)) * 16));
+                Mma<E>::run(sc[0], qa[k], b[0], b[1]);
+                Mma<E>::run(sc[1], qa[k], b[2], b[3]);
+            }
+        }
+        // logits in log2 units; element e of sc[j] is row g + 8 (e / 2),
+        // token 8 j + 2 t + e % 2 of the tile
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2 * R; ++e) {
+                sc[j][e] *= p.qscale;
+                if (mask[0] != 0xffffu && !((mask[0] >> (8 * j + 2 * t + (e & 1))) & 1u))
+                    sc[j][e] = -INFINITY;
+            }
+        if constexpr (kScores) {
+            float* zr = p.z + ((int64_t)s * p.H + (int64_t)kvh * p.G + g) * p.z_stride +
+                        i * kTile + 2 * t;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (g + 8 * r < p.G) {
+                    float* zp = zr + 8 * r * p.z_stride;
+                    *reinterpret_cast<float2*>(zp) = make_float2(sc[0][2 * r], sc[0][2 * r + 1]);
+                    *reinterpret_cast<float2*>(zp + 8) = make_float2(sc[1][2 * r], sc[1][2 * r + 1]);
+                }
+        }
+        float pr[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float corr[2] = {1.f, 1.f};
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float mt = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]),
+                             fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
+            mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 1));
+            mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 2));
+            const float m_new = fmaxf(a.m[r], mt);
+            const float m_use = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet
+            corr[r] = exp2f(a.m[r] - m_use);
+            a.m[r] = m_new;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) pr[j][2 * r + e] = exp2f(sc[j][2 * r + e] - m_use);
+            a.l[r] = fmaf(a.l[r], corr[r],
+                          (pr[0][2 * r] + pr[0][2 * r + 1]) + (pr[1][2 * r] + pr[1][2 * r + 1]));
+        }
+        // most tiles leave every row's maximum as it was
+        if (__any_sync(kFull, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+            for (int j = 0; j < NO; ++j) {
+                a.o[j][0] *= corr[0];
+                a.o[j][1] *= corr[0];
+                if (kWide) {
+                    a.o[j][2] *= corr[1];
+                    a.o[j][3] *= corr[1];
+                }
+            }
+        }
+        // P = its rounding to 16 bits + the rounding of what is left
+        uint32_t ph[4] = {0u, 0u, 0u, 0u}, pl[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float x = pr[j][2 * r], y = pr[j][2 * r + 1];
+                const uint32_t hi = E::from_float2(x, y);
+                const float2 back = E::to_float2(hi);
+                ph[2 * j + r] = hi;
+                pl[2 * j + r] = E::from_float2(x - back.x, y - back.y);
+            }
+        {
+            const int mi = lane >> 3;
+            const int row = (mi & 1) * 8 + (lane & 7);
+#pragma unroll
+            for (int j = 0; j < NO; j += 2) {
+                uint32_t b[4];
+                ldsm_x4_trans(b, sv + row * ROWB + (((j + (mi >> 1)) ^ (row & 7)) * 16));
+                Mma<E>::run(a.o[j], ph, b[0], b[1]);
+                Mma<E>::run(a.o[j + 1], ph, b[2], b[3]);
+                Mma<E>::run(a.o[j], pl, b[0], b[1]);
+                Mma<E>::run(a.o[j + 1], pl, b[2], b[3]);
+            }
+        }
+        __syncwarp();  // this stage is filled again by the next issue
+#pragma unroll
+        for (int st = 0; st < NST - 1; ++st) mask[st] = mask[st + 1];
+        stage = stage + 1 == NST ? 0 : stage + 1;
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        a.l[r] += __shfl_xor_sync(kFull, a.l[r], 1);
+        a.l[r] += __shfl_xor_sync(kFull, a.l[r], 2);
+    }
+}
+
+// Joins the token splits of each head in shared memory: split 0's warp ends
+// up with the whole.  `ring` is the CTA's ring memory, idle here.
+template <int D>
+__device__ __forceinline__ void join_splits(const Params& p, float* ring, int warp, int lane,
+                                            Acc<D>& a) {
+    constexpr int NO = D / 8;
+    constexpr int kSlice = kRingBytes<D> / 4;  // floats of one warp's ring
+    __syncthreads();
+    if (warp >= p.hw) {
+        float* mine = ring + warp * kSlice + lane;
+#pragma unroll
+        for (int j = 0; j < NO; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mine[(4 * j + e) * 32] = a.o[j][e];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            mine[(4 * NO + r) * 32] = a.m[r];
+            mine[(4 * NO + 2 + r) * 32] = a.l[r];
+        }
+    }
+    __syncthreads();
+    if (warp < p.hw) {
+        for (int w = warp + p.hw; w < kWarps; w += p.hw) {
+            const float* other = ring + w * kSlice + lane;
+            float wa[2], wb[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float mo = other[(4 * NO + r) * 32], lo = other[(4 * NO + 2 + r) * 32];
+                const float m_new = fmaxf(a.m[r], mo);
+                const float m_use = m_new == -INFINITY ? 0.f : m_new;
+                wa[r] = exp2f(a.m[r] - m_use);
+                wb[r] = exp2f(mo - m_use);
+                a.m[r] = m_new;
+                a.l[r] = a.l[r] * wa[r] + lo * wb[r];
+            }
+#pragma unroll
+            for (int j = 0; j < NO; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    a.o[j][e] = a.o[j][e] * wa[e >> 1] + other[(4 * j + e) * 32] * wb[e >> 1];
+        }
+    }
+    __syncthreads();  // the rings are filled again after this
+}
+
+// scores[s, kvh, j] += sum over the group's heads of 2^(z - M) / L for the
+// tokens j0 <= j < j1; s_m and s_inv hold M and 1 / L (0 for an empty row) of
+// the G heads.  Each score is added to by one thread, heads in order.
+__device__ __forceinline__ void fold_weights(const Params& p, int s, int kvh, int j0, int j1,
+                                             const float* s_m, const float* s_inv) {
+    const float* z = p.z + ((int64_t)s * p.H + (int64_t)kvh * p.G) * p.z_stride;
+    float* sc = p.scores + ((int64_t)s * p.Hkv + kvh) * p.score_stride;
+    for (int j = j0 + threadIdx.x; j < j1; j += kThreads) {
+        float w = 0.f;
+        for (int r = 0; r < p.G; ++r) {
+            const float inv = s_inv[r];
+            if (inv != 0.f) w = fmaf(exp2f(z[r * p.z_stride + j] - s_m[r]), inv, w);
+        }
+        sc[j] += w;
+    }
+}
+
+template <class E, int D, bool kWide, bool kScores>
+__global__ void __launch_bounds__(kThreads, 2) bounded_kernel(Params p) {
+    // inputs may come from the kernel before this one; the next may become
+    // resident once every CTA is here, and waits for this grid's end
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ long long s_before[kThreads + 1];  // tiles before each thread's sequences
+    __shared__ long long s_warp[kWarps];
+    __shared__ float s_m[kMaxGroup], s_inv[kMaxGroup];
+    constexpr int NO = D / 8;
+    constexpr int R = kWide ? 2 : 1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int hl = warp % p.hw, split = warp / p.hw;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kRingBytes<D>;
+    const int c = blockIdx.x;
+
+    int s, hb, tb, n;
+    long long left = LLONG_MAX;   // tiles left in this range
+    long long unit0 = 0;          // first tile of the current unit
+    long long range = 1;
+    if (p.direct) {
+        s = c / p.HB;
+        hb = c % p.HB;
+        tb = 0;
+        const int raw = __ldg(p.context_lens + s);
+        if ((raw < 0 || raw > p.max_ctx) && hb == 0 && tid == 0) pkv::report(p.err, PKV_DEVERR_CONTEXT);
+        n = context_of(p, s);
+    } else {
+        // tiles before each thread's run of sequences
+        const int per = (p.S + kThreads - 1) / kThreads;
+        long long mine = 0;
+        for (int i = 0; i < per; ++i) {
+            const int q = tid * per + i;
+            if (q < p.S) {
+                const int raw = __ldg(p.context_lens + q);
+                if ((raw < 0 || raw > p.max_ctx) && c == 0) pkv::report(p.err, PKV_DEVERR_CONTEXT);
+                mine += tiles_of(p, context_of(p, q));
+            }
+        }
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) s_warp[warp] = incl;
+        __syncthreads();
+        long long base = 0;
+        for (int w = 0; w < warp; ++w) base += s_warp[w];
+        s_before[tid] = base + incl - mine;
+        if (tid == kThreads - 1) s_before[kThreads] = base + incl;
+        __syncthreads();
+        const long long total = s_before[kThreads] * p.HB;
+        range = (total + gridDim.x - 1) / gridDim.x;
+        const long long begin = range * c;
+        if (begin >= total) {
+            if (tid == 0) p.info[c].tiles = 0;
+            return;
+        }
+        left = min(range, total - begin);
+        // the sequence holding tile `begin`: the thread run, then the sequence
+        const long long want = begin / p.HB;  // in units of one head block's tiles
+        int run = 0;
+#pragma unroll
+        for (int k = 0; k < kThreads / 32; ++k)
+            run += __popc(__ballot_sync(kFull, s_before[32 * k + lane] <= want));
+        run -= 1;  // s_before[0] = 0 <= want; equal entries are empty runs, the last one wins
+        long long before = s_before[run];
+        s = run * per;
+        for (;;) {
+            const int q = s + lane;
+            const int tl = q < p.S && q < (run + 1) * per ? tiles_of(p, context_of(p, q)) : 0;
+            long long in = tl;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long x = __shfl_up_sync(kFull, in, o);
+                if (lane >= o) in += x;
+            }
+            const unsigned past = __ballot_sync(kFull, before + in > want);
+            if (past) {
+                const int at = __ffs(past) - 1;
+                before += __shfl_sync(kFull, in - tl, at);
+                s += at;
+                break;
+            }
+            before += __shfl_sync(kFull, in, 31);
+            s += 32;
+        }
+        n = context_of(p, s);
+        const long long inside = begin - before * p.HB;
+        const int T = tiles_of(p, n);
+        hb = (int)(inside / T);
+        tb = (int)(inside % T);
+        unit0 = begin - tb;
+        if (tid == 0) {
+            RangeInfo* ri = p.info + c;
+            ri->s = s;
+            ri->hb = hb;
+            ri->tb = tb;
+            ri->tiles = (int)left;
+            ri->first_c0 = (int)(unit0 / range);
+            ri->first_c1 = (int)((unit0 + T - 1) / range);
+        }
+    }
+
+    for (;;) {
+        const int T = tiles_of(p, n);
+        const int te = (int)min((long long)T, tb + left);
+        const int kvh = hb * p.hw + hl;
+        Acc<D> a;
+        attend<E, D, kWide, kScores>(p, s, kvh, n, tb + split, te, p.nsplit, ring, lane, a);
+        if (p.nsplit > 1) join_splits<D>(p, reinterpret_cast<float*>(smem), warp, lane, a);
+        const bool whole = tb == 0 && te == T;
+        if (split == 0) {
+            if (whole) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int row = g + 8 * r;
+                    if (row < p.G) {
+                        const int64_t oh = (int64_t)s * p.H + (int64_t)kvh * p.G + row;
+                        const float inv = a.l[r] > 0.f || a.l[r] != a.l[r] ? 1.f / a.l[r] : 0.f;
+                        uint16_t* dst = static_cast<uint16_t*>(p.out) + oh * D + 2 * t;
+#pragma unroll
+                        for (int j = 0; j < NO; ++j)
+                            *reinterpret_cast<uint32_t*>(dst + 8 * j) =
+                                E::from_float2(a.o[j][2 * r] * inv, a.o[j][2 * r + 1] * inv);
+                        if (kScores && t == 0) {
+                            if (p.direct) {
+                                s_m[row] = a.m[r];
+                                s_inv[row] = inv;
+                            } else {
+                                p.row_m[oh] = a.m[r];
+                                p.row_l[oh] = a.l[r];
+                            }
+                        }
+                    }
+                }
+            } else {
+                const int64_t piece = 2 * (int64_t)c + (tb == 0 ? 1 : 0);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int row = g + 8 * r;
+                    if (row < p.G) {
+                        const int64_t at = (piece * p.hw + hl) * p.G + row;
+                        float* dst = p.part_acc + at * D + 2 * t;
+#pragma unroll
+                        for (int j = 0; j < NO; ++j)
+                            *reinterpret_cast<float2*>(dst + 8 * j) =
+                                make_float2(a.o[j][2 * r], a.o[j][2 * r + 1]);
+                        if (t == 0) {
+                            p.part_m[at] = a.m[r];
+                            p.part_l[at] = a.l[r];
+                        }
+                    }
+                }
+            }
+        }
+        if (p.direct) {
+            if (kScores) {  // the z of this unit were written by this CTA
+                __syncthreads();
+                fold_weights(p, s, hb, 0, n, s_m, s_inv);
+            }
+            return;
+        }
+        left -= te - tb;
+        if (left == 0) {
+            if (tid == 0) p.info[c].last_c1 = (int)((unit0 + T - 1) / range);
+            return;
+        }
+        unit0 += T;
+        tb = 0;
+        if (++hb == p.HB) {
+            hb = 0;
+            n = context_of(p, ++s);
+        }
+    }
+}
+
+// M and L of one row over the pieces of a cut unit: the first in range c0,
+// the last in range c1.  All lanes return them; `mine` is piece c0 + lane's
+// weight.
+__device__ __forceinline__ int64_t piece_row(const Params& p, int c, int c0, int hl, int row) {
+    return ((2 * (int64_t)c + (c == c0 ? 1 : 0)) * p.hw + hl) * p.G + row;
+}
+
+__device__ __forceinline__ void join_row(const Params& p, int c0, int c1, int hl, int row,
+                                         int lane, float& M, float& L) {
+    M = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_m[piece_row(p, c, c0, hl, row)]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    const float use = M == -INFINITY ? 0.f : M;
+    L = 0.f;
+    for (int c = c0 + lane; c <= c1; c += 32) {
+        const int64_t at = piece_row(p, c, c0, hl, row);
+        L = fmaf(exp2f(p.part_m[at] - use), p.part_l[at], L);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(kFull, L, o);
+}
+
+// After bounded_kernel, one CTA per range: joins the pieces of the unit that
+// begins in the range and ends in a later one; with scores, folds the weights
+// of the range's tokens.
+template <class E, int D, bool kScores>
+__global__ void __launch_bounds__(kThreads) join_kernel(Params p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    __shared__ float s_m[kMaxGroup], s_inv[kMaxGroup];
+    constexpr int DPL = D / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c = blockIdx.x;
+    const RangeInfo ri = p.info[c];
+    if (ri.tiles == 0) return;
+    int s = ri.s, hb = ri.hb, tb = ri.tb, left = ri.tiles;
+    bool first = true;
+    for (;;) {
+        const int n = context_of(p, s);
+        const int T = tiles_of(p, n);
+        const int te = min(T, tb + left);
+        const bool whole = tb == 0 && te == T;
+        const bool last = te - tb == left;
+        // ranges of the first and the last piece
+        const int c0 = first ? ri.first_c0 : c;
+        const int c1 = first ? ri.first_c1 : (last ? ri.last_c1 : c);
+        if (!whole && tb == 0) {  // the unit begins here: join its pieces
+            const int rows = p.hw * p.G;
+            for (int i = warp; i < rows; i += kWarps) {
+                const int hl = i / p.G, row = i % p.G;
+                float M, L;
+                join_row(p, c0, c1, hl, row, lane, M, L);
+                const float use = M == -INFINITY ? 0.f : M;
+                float o[DPL];
+#pragma unroll
+                for (int j = 0; j < DPL; ++j) o[j] = 0.f;
+                for (int cc = c0; cc <= c1; ++cc) {
+                    const int64_t at = piece_row(p, cc, c0, hl, row);
+                    const float w = exp2f(p.part_m[at] - use);
+                    const float* src = p.part_acc + at * D + lane * DPL;
+#pragma unroll
+                    for (int j = 0; j < DPL; ++j) o[j] = fmaf(w, src[j], o[j]);
+                }
+                const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+                const int64_t oh = (int64_t)s * p.H + (int64_t)(hb * p.hw + hl) * p.G + row;
+                uint16_t* dst = static_cast<uint16_t*>(p.out) + oh * D + lane * DPL;
+#pragma unroll
+                for (int j = 0; j < DPL; j += 2)
+                    *reinterpret_cast<uint32_t*>(dst + j) = E::from_float2(o[j] * inv, o[j + 1] * inv);
+            }
+        }
+        if constexpr (kScores) {
+            for (int hl = 0; hl < p.hw; ++hl) {
+                const int kvh = hb * p.hw + hl;
+                __syncthreads();  // s_m and s_inv of the head before have been read
+                for (int row = warp; row < p.G; row += kWarps) {
+                    float M, L;
+                    if (whole) {
+                        const int64_t oh = (int64_t)s * p.H + (int64_t)kvh * p.G + row;
+                        M = p.row_m[oh];
+                        L = p.row_l[oh];
+                    } else {
+                        join_row(p, c0, c1, hl, row, lane, M, L);
+                    }
+                    if (lane == 0) {
+                        s_m[row] = M;
+                        s_inv[row] = L > 0.f || L != L ? 1.f / L : 0.f;
+                    }
+                }
+                __syncthreads();
+                fold_weights(p, s, kvh, tb * kTile, min(te * kTile, n), s_m, s_inv);
+            }
+        }
+        left -= te - tb;
+        if (left == 0) return;
+        first = false;
+        tb = 0;
+        if (++hb == p.HB) {
+            hb = 0;
+            ++s;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+// A unit of at most this many visible tokens per sequence is one CTA.
+constexpr int kDirectTokens = 512;
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct Layout {
+    size_t info, m, l, acc, row_m, row_l, z, total;
+    int64_t z_stride;
+};
+
+int heads_per_cta(int Hkv) { return Hkv % 4 == 0 ? 4 : (Hkv % 2 == 0 ? 2 : 1); }
+
+// scores: with the logits of contexts up to max_ctx and the rows' M and L.
+Layout layout_of(int S, int H, int Hkv, int D, bool scores, int max_ctx) {
+    const size_t rows = (size_t)2 * kMaxRanges * heads_per_cta(Hkv) * (H / Hkv);
+    Layout L;
+    size_t o = 0;
+    L.info = o;  o = align256(o + kMaxRanges * sizeof(RangeInfo));
+    L.m = o;     o = align256(o + rows * sizeof(float));
+    L.l = o;     o = align256(o + rows * sizeof(float));
+    L.acc = o;   o = align256(o + rows * D * sizeof(float));
+    L.row_m = L.row_l = L.z = o;
+    L.z_stride = ((int64_t)max_ctx + kTile - 1) / kTile * kTile;
+    if (L.z_stride == 0) L.z_stride = kTile;
+    if (scores) {
+        o = align256(o + (size_t)S * H * sizeof(float));
+        L.row_l = o; o = align256(o + (size_t)S * H * sizeof(float));
+        L.z = o;     o = align256(o + (size_t)S * H * L.z_stride * sizeof(float));
+    }
+    L.total = o;
+    return L;
+}
+
+using KernelFn = void (*)(Params);
+
+template <class E, bool kScores>
+KernelFn pick_attend(int D, bool wide) {
+    if (D == 128) return wide ? bounded_kernel<E, 128, true, kScores> : bounded_kernel<E, 128, false, kScores>;
+    return wide ? bounded_kernel<E, 64, true, kScores> : bounded_kernel<E, 64, false, kScores>;
+}
+
+template <bool kScores>
+KernelFn pick_join(pkv_dtype dtype, int D) {
+    if (dtype == PKV_F16) return D == 128 ? join_kernel<pkv::F16, 128, kScores> : join_kernel<pkv::F16, 64, kScores>;
+    return D == 128 ? join_kernel<pkv::BF16, 128, kScores> : join_kernel<pkv::BF16, 64, kScores>;
+}
+
+// Resident CTAs per SM of an attention kernel, after allowing it its shared
+// memory (once per kernel and device); 0 if it cannot run.
+int resident_of(KernelFn fn, int smem) {
+    static std::mutex mu;
+    static struct { KernelFn fn; int dev; int n; } cache[128];
+    static int used = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    std::lock_guard<std::mutex> lk(mu);
+    for (int i = 0; i < used; ++i)
+        if (cache[i].fn == fn && cache[i].dev == dev) return cache[i].n;
+    int n = 0;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, kThreads, smem) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (used < 128) cache[used++] = {fn, dev, n};
+    return n;
+}
+
+pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_cache,
+                       const void* v_cache, const int32_t* block_tables,
+                       const int32_t* context_lens, int S, int H, int Hkv, int D, int bs, int NB,
+                       int MB, int max_context_len, int window, int sinks, float scale,
+                       pkv_dtype dtype, bool with_scores, float* scores, int64_t score_stride,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    char msg[256];
+    auto bad = [&](pkv_status st, const char* what) {
+        snprintf(msg, sizeof msg, "%s: %s", who, what);
+        return pkv::fail(st, msg);
+    };
+    if (S < 0 || H <= 0 || Hkv <= 0 || NB <= 0 || MB <= 0 || (dtype != PKV_F16 && dtype != PKV_BF16))
+        return bad(PKV_ERR_INVALID_ARG, "bad size or dtype");
+    if ((D != 64 && D != 128) || (bs != 8 && bs != 16 && bs != 32 && bs != 64))
+        return bad(PKV_ERR_UNSUPPORTED, "head_dim must be 64/128, block_size 8/16/32/64");
+    if (H % Hkv != 0) return bad(PKV_ERR_INVALID_ARG, "H must be a multiple of Hkv");
+    if (H / Hkv > kMaxGroup) return bad(PKV_ERR_UNSUPPORTED, "at most 16 query heads per KV head");
+    if (window < 1 || sinks < 0) return bad(PKV_ERR_INVALID_ARG, "window must be >= 1 and sink_tokens >= 0");
+    if (!(scale == scale) || std::isinf(scale)) return bad(PKV_ERR_INVALID_ARG, "scale must be finite");
+    if ((int64_t)NB * bs > INT32_MAX) return bad(PKV_ERR_INVALID_ARG, "NB * bs must fit 31 bits");
+    if (S > 32767) return bad(PKV_ERR_INVALID_ARG, "at most 32767 sequences");
+    const int64_t cap = (int64_t)MB * bs;
+    const int64_t max_ctx = max_context_len == 0 ? (cap < INT32_MAX - 64 ? cap : INT32_MAX - 64) : max_context_len;
+    if (max_ctx < 0 || max_ctx > cap || max_ctx > INT32_MAX - 64)
+        return bad(PKV_ERR_INVALID_ARG, "max_context_len must be in [0, MB*bs]");
+    if (S == 0) return PKV_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || (with_scores && !scores))
+        return bad(PKV_ERR_INVALID_ARG, "null pointer");
+    if (!pkv::aligned16(out) || !pkv::aligned16(q) || !pkv::aligned16(k_cache) || !pkv::aligned16(v_cache))
+        return bad(PKV_ERR_INVALID_ARG, "token pointers must be 16-byte aligned");
+    if (with_scores && (reinterpret_cast<uintptr_t>(scores) & 3u))
+        return bad(PKV_ERR_INVALID_ARG, "scores must be 4-byte aligned");
+    if (with_scores && score_stride < max_ctx)
+        return bad(PKV_ERR_INVALID_ARG, "score_stride must be at least max_context_len");
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return bad(PKV_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
+    const Layout L = layout_of(S, H, Hkv, D, with_scores, (int)max_ctx);
+    if (workspace_bytes < L.total) return bad(PKV_ERR_WORKSPACE, "workspace too small");
+
+    Params p;
+    p.out = out;
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.S = S;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.G = H / Hkv;
+    p.NB = NB;
+    p.MB = MB;
+    p.bs_log2 = bs == 8 ? 3 : (bs == 16 ? 4 : (bs == 32 ? 5 : 6));
+    p.max_ctx = (int)max_ctx;
+    p.window = window;
+    p.sinks = sinks;
+    p.qscale = scale * kLog2e;
+    char* w = static_cast<char*>(workspace);
+    p.info = reinterpret_cast<RangeInfo*>(w + L.info);
+    p.part_m = reinterpret_cast<float*>(w + L.m);
+    p.part_l = reinterpret_cast<float*>(w + L.l);
+    p.part_acc = reinterpret_cast<float*>(w + L.acc);
+    p.row_m = reinterpret_cast<float*>(w + L.row_m);
+    p.row_l = reinterpret_cast<float*>(w + L.row_l);
+    p.z = reinterpret_cast<float*>(w + L.z);
+    p.z_stride = L.z_stride;
+    p.scores = scores;
+    p.score_stride = score_stride;
+    p.err = pkv::device_error_word();
+    const int64_t most = (int64_t)window + sinks < max_ctx ? (int64_t)window + sinks : max_ctx;
+    p.direct = most <= kDirectTokens;
+    p.hw = p.direct ? 1 : heads_per_cta(Hkv);
+    p.nsplit = kWarps / p.hw;
+    p.HB = Hkv / p.hw;
+
+    const bool wide = p.G > 8;
+    KernelFn fn = dtype == PKV_F16
+                      ? (with_scores ? pick_attend<pkv::F16, true>(D, wide) : pick_attend<pkv::F16, false>(D, wide))
+                      : (with_scores ? pick_attend<pkv::BF16, true>(D, wide) : pick_attend<pkv::BF16, false>(D, wide));
+    const int smem = D == 128 ? kSmemBytes<128> : kSmemBytes<64>;
+    const int per_sm = resident_of(fn, smem);
+    if (per_sm < 1) return bad(PKV_ERR_CUDA, "the kernel cannot be resident");
+
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = pkv::as_stream(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int ranges = per_sm * pkv::sm_count();
+    if (ranges > kMaxRanges) ranges = kMaxRanges;
+    cfg.gridDim = dim3(p.direct ? (unsigned)(S * p.HB) : (unsigned)ranges);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p);
+    if (e == cudaSuccess && !p.direct) {
+        cfg.dynamicSmemBytes = 0;
+        e = cudaLaunchKernelEx(&cfg, with_scores ? pick_join<true>(dtype, D) : pick_join<false>(dtype, D), p);
+    }
+    if (e != cudaSuccess) {
+        snprintf(msg, sizeof msg, "%s launch", who);
+        return pkv::cuda_fail(e, msg);
+    }
+    return PKV_OK;
+}
+
+bool workspace_args_ok(int S, int H, int Hkv, int D) {
+    return S >= 0 && H > 0 && Hkv > 0 && H % Hkv == 0 && H / Hkv <= kMaxGroup && (D == 64 || D == 128);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pkv_decode_window_workspace_size(int S, int H, int Hkv, int D) {
+    if (!workspace_args_ok(S, H, Hkv, D)) return 0;
+    return layout_of(S, H, Hkv, D, false, 0).total;
+}
+
+pkv_status pkv_paged_attention_decode_window(
+    void* out, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens, int S, int H, int Hkv, int D, int bs,
+    int NB, int MB, int max_context_len, int window, int sink_tokens, float scale, pkv_dtype dtype,
+    void* workspace, size_t workspace_bytes, void* stream) {
+    PKV_TRACE("pkv_paged_attention_decode_window");
+    pkv::clear_error();
+    return run_bounded("paged_attention_decode_window", out, q, k_cache, v_cache, block_tables,
+                       context_lens, S, H, Hkv, D, bs, NB, MB, max_context_len, window, sink_tokens,
+                       scale, dtype, false, nullptr, 0, workspace, workspace_bytes, stream);
+}
+
+size_t pkv_decode_accumulate_workspace_size(int S, int H, int Hkv, int D, int max_context_len) {
+    if (!workspace_args_ok(S, H, Hkv, D) || max_context_len < 0 || max_context_len > INT32_MAX - 64)
+        return 0;
+    return layout_of(S, H, Hkv, D, true, max_context_len).total;
+}
+
+pkv_status pkv_paged_attention_decode_accumulate(
+    void* out, float* scores, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens, int S, int H, int Hkv, int D, int bs,
+    int NB, int MB, int max_context_len, int64_t score_stride, float scale, pkv_dtype dtype,
+    void* workspace, size_t workspace_bytes, void* stream) {
+    PKV_TRACE("pkv_paged_attention_decode_accumulate");
+    pkv::clear_error();
+    // every token is visible: a window as long as any context, no sinks
+    return run_bounded("paged_attention_decode_accumulate", out, q, k_cache, v_cache, block_tables,
+                       context_lens, S, H, Hkv, D, bs, NB, MB, max_context_len, INT32_MAX, 0, scale,
+                       dtype, true, scores, score_stride, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

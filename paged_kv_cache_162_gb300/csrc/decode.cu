@@ -69,6 +69,7 @@
 
 #include "pagedkv.h"
 #include "pkv_device.cuh"
+#include "pkv_mma.cuh"
 
 namespace {
 
@@ -80,6 +81,13 @@ constexpr int kAutoCandidates = 7;       // 64, 128, ..., 4096 tokens
 constexpr int kItemsPerCta = 6;          // automatic choice: at least this many items per CTA
 constexpr int kPlanThreads = 256;
 constexpr unsigned kFull = 0xffffffffu;
+
+using pkv::cp_async16;
+using pkv::cp_async_commit;
+using pkv::cp_async_wait;
+using pkv::ldsm_x4;
+using pkv::ldsm_x4_trans;
+using pkv::Mma;
 
 struct Workspace {
     unsigned* counter;  // next work item
@@ -947,50 +955,6 @@ __global__ void __launch_bounds__(kThreads, PKV_MIN_CTAS_PER_SM) decode_kernel(D
 // workspace slots as the decode kernel's, and the same tickets merge them.
 // ---------------------------------------------------------------------------
 constexpr int kPrefixStages = 3;
-
-template <class E>
-struct Mma;
-template <>
-struct Mma<pkv::F16> {
-    static __device__ __forceinline__ void run(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                               uint32_t b1) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-};
-template <>
-struct Mma<pkv::BF16> {
-    static __device__ __forceinline__ void run(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                               uint32_t b1) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-};
-
-__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 struct PrefixParams {
     DecodeParams d;

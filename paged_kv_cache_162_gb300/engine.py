@@ -119,6 +119,174 @@ def paged_attention_decode_shared_prefix(out, q, k_cache, v_cache, block_tables,
     return out
 
 
+def _refuse(what: str):
+    raise L.PkvError(L.PKV_ERR_INVALID_ARG, what)
+
+
+def _need(who, tensors, cache):
+    """Every (name, tensor, dtype, shape) contiguous, of that type and shape
+    (None: any), on the caches' device -- or, for q and out, in pinned host
+    memory."""
+    dev = cache.device
+    for name, t, dtype, shape in tensors:
+        if t.dtype != dtype or (shape is not None and t.shape != shape) or not t.is_contiguous():
+            _refuse(f"{who}: {name} must be contiguous {dtype} of shape "
+                    f"{tuple(shape) if shape is not None else 'any'}, got {t.dtype} {tuple(t.shape)}"
+                    f"{'' if t.is_contiguous() else ' (not contiguous)'}")
+        if t.device != dev and not (name in ("q", "out") and t.device.type == "cpu" and t.is_pinned()):
+            _refuse(f"{who}: {name} is on {t.device}, the caches on {dev}")
+
+
+def _on_device(cache, stream, call):
+    """call(stream) with the caches' device current."""
+    dev = cache.device.index
+    if dev == torch.cuda.current_device():
+        return call(stream)
+    with torch.cuda.device(dev):
+        return call(stream)
+
+
+def _attention_shapes(who, q, k_cache, block_tables):
+    if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2:
+        _refuse(f"{who}: q must be [S, H, D], the caches [NB, bs, Hkv, D], block_tables [S, MB]")
+    S, H, D = q.shape
+    NB, bs, Hkv, Dk = k_cache.shape
+    if Dk != D:
+        _refuse(f"{who}: q has head_dim {D}, the caches {Dk}")
+    return S, H, D, NB, bs, Hkv, block_tables.shape[1]
+
+
+def _workspace(who, ws, size, device, stream=None):
+    if ws is None:
+        n = size()
+        if n == 0:
+            _refuse(f"{who}: bad workspace arguments (H a multiple of Hkv, at most 16 per group?)")
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        if stream is not None:  # keeps its memory until the call's stream has passed
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            ws.record_stream(stream)
+        return ws
+    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device:
+        _refuse(f"{who}: workspace must be a contiguous uint8 tensor on {device}")
+    return ws
+
+
+def new_window_workspace(S, H, Hkv, D, device="cuda") -> torch.Tensor:
+    return _workspace("new_window_workspace", None,
+                      lambda: L.pkv_decode_window_workspace_size(S, H, Hkv, D), device)
+
+
+def new_accumulate_workspace(S, H, Hkv, D, max_context_len, device="cuda") -> torch.Tensor:
+    return _workspace("new_accumulate_workspace", None,
+                      lambda: L.pkv_decode_accumulate_workspace_size(S, H, Hkv, D,
+                                                                     max_context_len), device)
+
+
+def new_evict_workspace(S, Hkv, budget, device="cuda") -> torch.Tensor:
+    return _workspace("new_evict_workspace", None,
+                      lambda: L.pkv_evict_workspace_size(S, Hkv, budget), device)
+
+
+def paged_attention_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, window,
+                                  sink_tokens=0, scale=None, max_context_len=0, workspace=None,
+                                  stream=None):
+    """Decode attention of each sequence's newest token over its first
+    sink_tokens tokens and its last `window` tokens.
+
+    q, out: [S, H, D]; caches: [NB, bs, Hkv, D] with H a multiple of Hkv (at
+    most 16 query heads per KV head); block_tables [S, MB] int32;
+    context_lens [S] int32.  Blocks without a visible token are not looked
+    up: their table entries may be -1 (BlockAllocator.release_window).
+    workspace: new_window_workspace(S, H, Hkv, D), kept between calls.
+    """
+    who = "paged_attention_decode_window"
+    S, H, D, NB, bs, Hkv, MB = _attention_shapes(who, q, k_cache, block_tables)
+    dt = k_cache.dtype
+    _need(who, (("q", q, dt, None), ("out", out, dt, q.shape), ("k_cache", k_cache, dt, None),
+                ("v_cache", v_cache, dt, k_cache.shape),
+                ("block_tables", block_tables, torch.int32, (S, MB)),
+                ("context_lens", context_lens, torch.int32, (S,))), k_cache)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    ws = _workspace(who, workspace, lambda: L.pkv_decode_window_workspace_size(S, H, Hkv, D),
+                    k_cache.device, stream)
+    _on_device(k_cache, stream, lambda st: L.pkv_paged_attention_decode_window(
+        out, q, k_cache, v_cache, block_tables, context_lens, S, H, Hkv, D, bs, NB, MB,
+        max_context_len, window, sink_tokens, scale, dtype_code(dt), ws, ws.numel(), st))
+    return out
+
+
+def paged_attention_decode_accumulate(out, scores, q, k_cache, v_cache, block_tables, context_lens,
+                                      scale=None, max_context_len=0, workspace=None, stream=None):
+    """Decode attention over each whole context that also adds each cached
+    token's attention weight, summed over the query heads of its KV head, to
+    scores [S, Hkv, cap] fp32 (cap >= max_context_len, or MB * bs when that
+    is 0; entries past a context are left alone).  The statistic
+    evict_tokens goes by.  Other arguments as in
+    paged_attention_decode_window; workspace: new_accumulate_workspace(S, H,
+    Hkv, D, max_context_len)."""
+    who = "paged_attention_decode_accumulate"
+    S, H, D, NB, bs, Hkv, MB = _attention_shapes(who, q, k_cache, block_tables)
+    dt = k_cache.dtype
+    _need(who, (("q", q, dt, None), ("out", out, dt, q.shape), ("k_cache", k_cache, dt, None),
+                ("v_cache", v_cache, dt, k_cache.shape),
+                ("block_tables", block_tables, torch.int32, (S, MB)),
+                ("context_lens", context_lens, torch.int32, (S,)),
+                ("scores", scores, torch.float32, (S, Hkv, scores.shape[-1]))), k_cache)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    ws = _workspace(who, workspace, lambda: L.pkv_decode_accumulate_workspace_size(
+        S, H, Hkv, D, max_context_len or MB * bs), k_cache.device, stream)
+    _on_device(k_cache, stream, lambda st: L.pkv_paged_attention_decode_accumulate(
+        out, scores, q, k_cache, v_cache, block_tables, context_lens, S, H, Hkv, D, bs, NB, MB,
+        max_context_len, scores.shape[-1], scale, dtype_code(dt), ws, ws.numel(), st))
+    return out
+
+
+def evict_tokens(k_cache, v_cache, scores, positions, block_tables, context_lens, token_counts,
+                 new_context_lens, budget, recent_tokens, sink_tokens=0, scores_out=None,
+                 positions_out=None, workspace=None, stream=None):
+    """Keeps the `budget` best tokens of every (sequence, KV head) with more
+    -- the first sink_tokens positions and the last recent_tokens ones, then
+    the highest scores, ties by the lowest index -- and compacts the caches,
+    scores and positions to them in place (see pkv_evict_tokens).
+
+    scores [S, Hkv, cap] fp32 (paged_attention_decode_accumulate), positions
+    [S, Hkv, cap] int32 (-1: appended since the last eviction; a new
+    sequence's row is all -1); context_lens, token_counts [S] int32: tokens
+    cached and tokens seen; new_context_lens [S] int32 receives
+    min(context_lens, budget).  scores_out / positions_out: other arrays for
+    the results (default: in place).  The evicted sequences' blocks must be
+    their own (BlockAllocator.unshare); afterwards BlockAllocator.truncate
+    releases the blocks past the budget."""
+    who = "evict_tokens"
+    if k_cache.dim() != 4 or block_tables.dim() != 2:
+        _refuse(f"{who}: the caches must be [NB, bs, Hkv, D], block_tables [S, MB]")
+    NB, bs, Hkv, D = k_cache.shape
+    S, MB = block_tables.shape
+    if scores_out is None:
+        scores_out = scores
+    if positions_out is None:
+        positions_out = positions
+    rows = (S, Hkv, scores.shape[-1])
+    i32, dt = torch.int32, k_cache.dtype
+    _need(who, (("k_cache", k_cache, dt, None), ("v_cache", v_cache, dt, k_cache.shape),
+                ("scores", scores, torch.float32, rows), ("positions", positions, i32, rows),
+                ("scores_out", scores_out, torch.float32, rows),
+                ("positions_out", positions_out, i32, rows),
+                ("block_tables", block_tables, i32, None),
+                ("context_lens", context_lens, i32, (S,)),
+                ("token_counts", token_counts, i32, (S,)),
+                ("new_context_lens", new_context_lens, i32, (S,))), k_cache)
+    ws = _workspace(who, workspace, lambda: L.pkv_evict_workspace_size(S, Hkv, budget),
+                    k_cache.device, stream)
+    _on_device(k_cache, stream, lambda st: L.pkv_evict_tokens(
+        k_cache, v_cache, scores, positions, block_tables, context_lens, token_counts, scores_out,
+        positions_out, new_context_lens, S, Hkv, D, bs, NB, MB, rows[2], budget, recent_tokens,
+        sink_tokens, dtype_code(dt), ws, ws.numel(), st))
+
+
 def compute_slot_mapping(slot_mapping, block_tables, seq_idx, pos, block_size, stream=None):
     L.pkv_compute_slot_mapping(slot_mapping, block_tables, seq_idx, pos, seq_idx.numel(),
                                block_tables.shape[0], block_tables.shape[1], block_size, stream)
