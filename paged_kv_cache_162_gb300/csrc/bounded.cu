@@ -34,6 +34,8 @@
 //    begin in its range and folds its tokens' weights into the scores.  Ranges
 //    are computed from the lengths on the device by every CTA, so a call needs
 //    no plan, no counter and no ticket, and every sum has a fixed order.
+#include <cooperative_groups.h>
+
 #include <climits>
 #include <cmath>
 #include <cstdio>
@@ -42,6 +44,8 @@
 #include "pagedkv.h"
 #include "pkv_device.cuh"
 #include "pkv_mma.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace {
 
@@ -57,6 +61,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;
 constexpr int kMaxRanges = 512;    // CTAs of a split call
 constexpr int kMaxGroup = 16;      // query heads per KV head
+constexpr int kMaxCluster = 16;    // CTAs that share a unit in a direct call
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -69,14 +74,11 @@ constexpr int kRingBytes = kStages<D> * 2 * kTileBytes<D>;  // one warp's ring
 template <int D>
 constexpr int kSmemBytes = kWarps * kRingBytes<D>;
 
-// What a range (one CTA of a split call) did, for the join kernel.
+// The unit that begins in a range (one CTA of a split call) and ends in a
+// later one, for the join kernel.
 struct RangeInfo {
-    int s, hb, tb;       // its first unit and the first tile taken of it
-    int tiles;           // tiles in the range, 0 = none
-    int first_c0;        // range where the first unit begins
-    int first_c1;        // range where the first unit ends
-    int last_c1;         // range where the last unit ends
-    int pad;
+    int unit;  // s * HB + hb, -1: none
+    int c1;    // the range where it ends
 };
 
 struct Params {
@@ -89,9 +91,12 @@ struct Params {
     int S, H, Hkv, G, NB, MB, bs_log2, max_ctx;
     int window, sinks;   // accumulate: window = max_ctx
     int hw, nsplit, HB;  // KV heads per CTA, warps per KV head, units per sequence
-    int direct;          // one CTA per unit
+    int direct;          // one cluster per unit
+    int cs;              // direct: CTAs per cluster
+    int fold;            // split: CTAs per unit that fold weights into scores
     float qscale;        // scale * log2(e)
     RangeInfo* info;     // [ranges]
+    int2* place;         // [S * HB]: first and last range of each unit, accumulate only
     float* part_m;       // [2 * ranges][hw * G]
     float* part_l;
     float* part_acc;     // [2 * ranges][hw * G][D]
@@ -362,20 +367,140 @@ __device__ __forceinline__ void join_splits(const Params& p, float* ring, int wa
 }
 
 // scores[s, kvh, j] += sum over the group's heads of 2^(z - M) / L for the
-// tokens j0 <= j < j1; s_m and s_inv hold M and 1 / L (0 for an empty row) of
-// the G heads.  Each score is added to by one thread, heads in order.
+// tokens j0 <= j < j1 (j0 a multiple of 16) by threads tid, tid + threads, ...:
+// four tokens per thread and round.  s_m and s_inv hold M and 1 / L (0 for an
+// empty row) of the G heads.  Each score is added to by one thread, heads in
+// order.
 __device__ __forceinline__ void fold_weights(const Params& p, int s, int kvh, int j0, int j1,
-                                             const float* s_m, const float* s_inv) {
+                                             const float* s_m, const float* s_inv, int tid,
+                                             int threads) {
     const float* z = p.z + ((int64_t)s * p.H + (int64_t)kvh * p.G) * p.z_stride;
     float* sc = p.scores + ((int64_t)s * p.Hkv + kvh) * p.score_stride;
-    for (int j = j0 + threadIdx.x; j < j1; j += kThreads) {
-        float w = 0.f;
-        for (int r = 0; r < p.G; ++r) {
-            const float inv = s_inv[r];
-            if (inv != 0.f) w = fmaf(exp2f(z[r * p.z_stride + j] - s_m[r]), inv, w);
+    const bool vec = (reinterpret_cast<uintptr_t>(sc) & 15u) == 0;
+    for (int j = j0 + 4 * tid; j < j1; j += 4 * threads) {
+        const bool full = j + 4 <= j1;
+        float old[4];
+        if (vec && full) {
+            const float4 v = *reinterpret_cast<const float4*>(sc + j);
+            old[0] = v.x; old[1] = v.y; old[2] = v.z; old[3] = v.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) old[e] = j + e < j1 ? sc[j + e] : 0.f;
         }
-        sc[j] += w;
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int r = 0; r < p.G; ++r) {
+            const float4 v = *reinterpret_cast<const float4*>(z + r * p.z_stride + j);
+            const float inv = s_inv[r], m = s_m[r];
+            if (inv != 0.f) {
+                w[0] = fmaf(exp2f(v.x - m), inv, w[0]);
+                w[1] = fmaf(exp2f(v.y - m), inv, w[1]);
+                w[2] = fmaf(exp2f(v.z - m), inv, w[2]);
+                w[3] = fmaf(exp2f(v.w - m), inv, w[3]);
+            }
+        }
+        if (vec && full) {
+            *reinterpret_cast<float4*>(sc + j) =
+                make_float4(old[0] + w[0], old[1] + w[1], old[2] + w[2], old[3] + w[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (j + e < j1) sc[j + e] = old[e] + w[e];
+        }
     }
+}
+
+// Joins the CTAs of a cluster that share a unit (hw = 1): every CTA leaves its
+// rows in shared memory, then the rows are dealt out over the cluster's warps,
+// and each CTA folds its own tokens [tb, te) into the scores.
+template <class E, int D, bool kWide, bool kScores>
+__device__ __forceinline__ void join_cluster(const Params& p, int s, int kvh, int n, int tb, int te,
+                                             float* mem, int warp, int lane, const Acc<D>& a,
+                                             float* s_m, float* s_inv) {
+    constexpr int NO = D / 8, R = kWide ? 2 : 1, DPL = D / 32;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int g = lane >> 2, t = lane & 3, tid = warp * 32 + lane;
+    float* rows = mem;                      // [G][D]
+    float* ml = mem + kMaxGroup * D;        // [2][16]
+    if (warp == 0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int row = g + 8 * r;
+            if (row < p.G) {
+#pragma unroll
+                for (int j = 0; j < NO; ++j)
+                    *reinterpret_cast<float2*>(rows + row * D + 8 * j + 2 * t) =
+                        make_float2(a.o[j][2 * r], a.o[j][2 * r + 1]);
+                if (t == 0) {
+                    ml[row] = a.m[r];
+                    ml[kMaxGroup + row] = a.l[r];
+                }
+            }
+        }
+    }
+    cluster.sync();
+    // M and L of a row: lane i reads CTA i's
+    auto row_of = [&](int row, float& M, float& w, float& inv) {
+        float m = -INFINITY, l = 0.f;
+        if (lane < CS) {
+            const float* other = cluster.map_shared_rank(ml, lane);
+            m = other[row];
+            l = other[kMaxGroup + row];
+        }
+        M = m;
+#pragma unroll
+        for (int o = kMaxCluster / 2; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+        M = __shfl_sync(kFull, M, 0);
+        w = lane < CS ? exp2f(m - (M == -INFINITY ? 0.f : M)) : 0.f;
+        float L = w * l;
+#pragma unroll
+        for (int o = kMaxCluster / 2; o >= 1; o >>= 1) L += __shfl_xor_sync(kFull, L, o);
+        L = __shfl_sync(kFull, L, 0);
+        inv = L > 0.f || L != L ? 1.f / L : 0.f;
+    };
+    for (int row = rank * kWarps + warp; row < p.G; row += CS * kWarps) {
+        float M, w, inv;
+        row_of(row, M, w, inv);
+        float o[DPL];
+#pragma unroll
+        for (int j = 0; j < DPL; ++j) o[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kMaxCluster; ++i) {
+            if (i < CS) {
+                const float wi = __shfl_sync(kFull, w, i);
+                const float* src = cluster.map_shared_rank(rows, i) + row * D + lane * DPL;
+                float v[DPL];
+                if constexpr (DPL == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(src);
+                    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(src);
+                    v[0] = x.x; v[1] = x.y;
+                }
+#pragma unroll
+                for (int j = 0; j < DPL; ++j) o[j] = fmaf(wi, v[j], o[j]);
+            }
+        }
+        uint16_t* dst = static_cast<uint16_t*>(p.out) +
+                        ((int64_t)s * p.H + (int64_t)kvh * p.G + row) * D + lane * DPL;
+#pragma unroll
+        for (int j = 0; j < DPL; j += 2)
+            *reinterpret_cast<uint32_t*>(dst + j) = E::from_float2(o[j] * inv, o[j + 1] * inv);
+    }
+    if constexpr (kScores) {
+        for (int row = warp; row < p.G; row += kWarps) {
+            float M, w, inv;
+            row_of(row, M, w, inv);
+            if (lane == 0) {
+                s_m[row] = M;
+                s_inv[row] = inv;
+            }
+        }
+        __syncthreads();
+        fold_weights(p, s, kvh, tb * kTile, min(te * kTile, n), s_m, s_inv, tid, kThreads);
+    }
+    cluster.sync();  // no CTA leaves while another reads its rows
 }
 
 template <class E, int D, bool kWide, bool kScores>
@@ -400,14 +525,20 @@ __global__ void __launch_bounds__(kThreads, 2) bounded_kernel(Params p) {
     long long left = LLONG_MAX;   // tiles left in this range
     long long unit0 = 0;          // first tile of the current unit
     long long range = 1;
+    int end = 0;                  // direct: tiles [tb, end) are this CTA's
+    const int crank = p.direct ? c % p.cs : 0;
     if (p.direct) {
-        s = c / p.HB;
-        hb = c % p.HB;
-        tb = 0;
+        const int unit = c / p.cs;
+        s = unit / p.HB;
+        hb = unit % p.HB;
         const int raw = __ldg(p.context_lens + s);
-        if ((raw < 0 || raw > p.max_ctx) && hb == 0 && tid == 0) pkv::report(p.err, PKV_DEVERR_CONTEXT);
+        if ((raw < 0 || raw > p.max_ctx) && hb == 0 && crank == 0 && tid == 0)
+            pkv::report(p.err, PKV_DEVERR_CONTEXT);
         n = context_of(p, s);
-    } else {
+        const int T = tiles_of(p, n), per = (T + p.cs - 1) / p.cs;
+        tb = min(T, crank * per);
+        end = min(T, tb + per);
+        } else {
         // tiles before each thread's run of sequences
         const int per = (p.S + kThreads - 1) / kThreads;
         long long mine = 0;
@@ -436,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 2) bounded_kernel(Params p) {
         range = (total + gridDim.x - 1) / gridDim.x;
         const long long begin = range * c;
         if (begin >= total) {
-            if (tid == 0) p.info[c].tiles = 0;
+            if (tid == 0) p.info[c].unit = -1;
             return;
         }
         left = min(range, total - begin);
@@ -474,25 +605,20 @@ __global__ void __launch_bounds__(kThreads, 2) bounded_kernel(Params p) {
         hb = (int)(inside / T);
         tb = (int)(inside % T);
         unit0 = begin - tb;
-        if (tid == 0) {
-            RangeInfo* ri = p.info + c;
-            ri->s = s;
-            ri->hb = hb;
-            ri->tb = tb;
-            ri->tiles = (int)left;
-            ri->first_c0 = (int)(unit0 / range);
-            ri->first_c1 = (int)((unit0 + T - 1) / range);
-        }
     }
 
     for (;;) {
         const int T = tiles_of(p, n);
-        const int te = (int)min((long long)T, tb + left);
+        const int te = p.direct ? end : (int)min((long long)T, tb + left);
         const int kvh = hb * p.hw + hl;
         Acc<D> a;
         attend<E, D, kWide, kScores>(p, s, kvh, n, tb + split, te, p.nsplit, ring, lane, a);
         if (p.nsplit > 1) join_splits<D>(p, reinterpret_cast<float*>(smem), warp, lane, a);
         const bool whole = tb == 0 && te == T;
+        if (p.direct && p.cs > 1) {
+            join_cluster<E, D, kWide, kScores>(p, s, hb, n, tb, te, reinterpret_cast<float*>(smem), warp, lane, a, s_m, s_inv);
+            return;
+        }
         if (split == 0) {
             if (whole) {
 #pragma unroll
@@ -540,13 +666,18 @@ __global__ void __launch_bounds__(kThreads, 2) bounded_kernel(Params p) {
         if (p.direct) {
             if (kScores) {  // the z of this unit were written by this CTA
                 __syncthreads();
-                fold_weights(p, s, hb, 0, n, s_m, s_inv);
+                fold_weights(p, s, hb, 0, n, s_m, s_inv, tid, kThreads);
             }
             return;
         }
+        if (kScores && tb == 0 && tid == 0)
+            p.place[s * p.HB + hb] = make_int2(c, (int)((unit0 + T - 1) / range));
         left -= te - tb;
         if (left == 0) {
-            if (tid == 0) p.info[c].last_c1 = (int)((unit0 + T - 1) / range);
+            if (tid == 0) {
+                p.info[c].unit = tb == 0 && te < T ? s * p.HB + hb : -1;
+                p.info[c].c1 = (int)((unit0 + T - 1) / range);
+            }
             return;
         }
         unit0 += T;
@@ -581,98 +712,103 @@ __device__ __forceinline__ void join_row(const Params& p, int c0, int c1, int hl
     for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(kFull, L, o);
 }
 
-// After bounded_kernel, one CTA per range: joins the pieces of the unit that
-// begins in the range and ends in a later one; with scores, folds the weights
-// of the range's tokens.
+// After bounded_kernel.  The first ranges * join CTAs join, per range, the
+// pieces of the unit that begins in it and ends in a later one, a warp per
+// row.  With scores, `fold` CTAs per unit follow; each takes every fold-th
+// stretch of the unit's tokens, 4 tokens of a head per thread, and folds their
+// weights into the scores.  A stretch is one round of loads: the chain is
+// length and place of the unit -> M, L, z and scores -> store.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+
 template <class E, int D, bool kScores>
-__global__ void __launch_bounds__(kThreads) join_kernel(Params p) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(Params p, int ranges, int join) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    __shared__ float s_m[kMaxGroup], s_inv[kMaxGroup];
+    __shared__ float s_m[4 * kMaxGroup], s_inv[4 * kMaxGroup];
     constexpr int DPL = D / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int c = blockIdx.x;
-    const RangeInfo ri = p.info[c];
-    if (ri.tiles == 0) return;
-    int s = ri.s, hb = ri.hb, tb = ri.tb, left = ri.tiles;
-    bool first = true;
-    for (;;) {
+    const int rows = p.hw * p.G;
+    if ((int)blockIdx.x < ranges * join) {
+        const int c = blockIdx.x / join;
+        const int i = (blockIdx.x % join) * kJoinWarps + warp;
+        const RangeInfo ri = p.info[c];
+        if (ri.unit < 0 || i >= rows) return;
+        const int hl = i / p.G, row = i % p.G;
+        float M, L;
+        join_row(p, c, ri.c1, hl, row, lane, M, L);
+        const float use = M == -INFINITY ? 0.f : M;
+        float o[DPL];
+#pragma unroll
+        for (int j = 0; j < DPL; ++j) o[j] = 0.f;
+#pragma unroll 8
+        for (int cc = c; cc <= ri.c1; ++cc) {
+            const int64_t at = piece_row(p, cc, c, hl, row);
+            const float w = exp2f(p.part_m[at] - use);
+            const float* src = p.part_acc + at * D + lane * DPL;
+            if constexpr (DPL == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(src);
+                o[0] = fmaf(w, x.x, o[0]);
+                o[1] = fmaf(w, x.y, o[1]);
+                o[2] = fmaf(w, x.z, o[2]);
+                o[3] = fmaf(w, x.w, o[3]);
+            } else {
+                const float2 x = *reinterpret_cast<const float2*>(src);
+                o[0] = fmaf(w, x.x, o[0]);
+                o[1] = fmaf(w, x.y, o[1]);
+            }
+        }
+        const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+        const int64_t oh = (int64_t)(ri.unit / p.HB) * p.H + (int64_t)(ri.unit % p.HB) * rows + i;
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + oh * D + lane * DPL;
+#pragma unroll
+        for (int j = 0; j < DPL; j += 2)
+            *reinterpret_cast<uint32_t*>(dst + j) = E::from_float2(o[j] * inv, o[j + 1] * inv);
+        return;
+    }
+    if constexpr (kScores) {
+        const int f = blockIdx.x - ranges * join;
+        const int unit = f / p.fold, part = f % p.fold;
+        const int s = unit / p.HB, hb = unit % p.HB;
+        const int2 place = p.place[unit];  // the unit's first and last range
         const int n = context_of(p, s);
-        const int T = tiles_of(p, n);
-        const int te = min(T, tb + left);
-        const bool whole = tb == 0 && te == T;
-        const bool last = te - tb == left;
-        // ranges of the first and the last piece
-        const int c0 = first ? ri.first_c0 : c;
-        const int c1 = first ? ri.first_c1 : (last ? ri.last_c1 : c);
-        if (!whole && tb == 0) {  // the unit begins here: join its pieces
-            const int rows = p.hw * p.G;
-            for (int i = warp; i < rows; i += kWarps) {
-                const int hl = i / p.G, row = i % p.G;
-                float M, L;
-                join_row(p, c0, c1, hl, row, lane, M, L);
-                const float use = M == -INFINITY ? 0.f : M;
-                float o[DPL];
-#pragma unroll
-                for (int j = 0; j < DPL; ++j) o[j] = 0.f;
-                for (int cc = c0; cc <= c1; ++cc) {
-                    const int64_t at = piece_row(p, cc, c0, hl, row);
-                    const float w = exp2f(p.part_m[at] - use);
-                    const float* src = p.part_acc + at * D + lane * DPL;
-#pragma unroll
-                    for (int j = 0; j < DPL; ++j) o[j] = fmaf(w, src[j], o[j]);
-                }
-                const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-                const int64_t oh = (int64_t)s * p.H + (int64_t)(hb * p.hw + hl) * p.G + row;
-                uint16_t* dst = static_cast<uint16_t*>(p.out) + oh * D + lane * DPL;
-#pragma unroll
-                for (int j = 0; j < DPL; j += 2)
-                    *reinterpret_cast<uint32_t*>(dst + j) = E::from_float2(o[j] * inv, o[j + 1] * inv);
+        const int per = kJoinThreads / p.hw;  // threads per head
+        if (part * 4 * per >= n) return;
+        for (int i = warp; i < rows; i += kJoinWarps) {
+            float M, L;
+            if (place.x == place.y) {
+                const int64_t oh = (int64_t)s * p.H + (int64_t)hb * rows + i;
+                M = p.row_m[oh];
+                L = p.row_l[oh];
+            } else {
+                join_row(p, place.x, place.y, i / p.G, i % p.G, lane, M, L);
+            }
+            if (lane == 0) {
+                s_m[i] = M;
+                s_inv[i] = L > 0.f || L != L ? 1.f / L : 0.f;
             }
         }
-        if constexpr (kScores) {
-            for (int hl = 0; hl < p.hw; ++hl) {
-                const int kvh = hb * p.hw + hl;
-                __syncthreads();  // s_m and s_inv of the head before have been read
-                for (int row = warp; row < p.G; row += kWarps) {
-                    float M, L;
-                    if (whole) {
-                        const int64_t oh = (int64_t)s * p.H + (int64_t)kvh * p.G + row;
-                        M = p.row_m[oh];
-                        L = p.row_l[oh];
-                    } else {
-                        join_row(p, c0, c1, hl, row, lane, M, L);
-                    }
-                    if (lane == 0) {
-                        s_m[row] = M;
-                        s_inv[row] = L > 0.f || L != L ? 1.f / L : 0.f;
-                    }
-                }
-                __syncthreads();
-                fold_weights(p, s, kvh, tb * kTile, min(te * kTile, n), s_m, s_inv);
-            }
-        }
-        left -= te - tb;
-        if (left == 0) return;
-        first = false;
-        tb = 0;
-        if (++hb == p.HB) {
-            hb = 0;
-            ++s;
-        }
+        __syncthreads();
+        const int hl = tid / per;
+        for (int j = part * 4 * per; j < n; j += p.fold * 4 * per)
+            fold_weights(p, s, hb * p.hw + hl, j, min(n, j + 4 * per), s_m + hl * p.G,
+                         s_inv + hl * p.G, tid % per, per);
     }
 }
 
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-// A unit of at most this many visible tokens per sequence is one CTA.
+// Visible tokens of a direct call per CTA, and its CTAs in multiples of the
+// resident ones.
 constexpr int kDirectTokens = 512;
+constexpr int kDirectWaves = 2;
+constexpr int kFoldCtas = 8192;     // of a split call
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Layout {
-    size_t info, m, l, acc, row_m, row_l, z, total;
+    size_t info, m, l, acc, place, row_m, row_l, z, total;
     int64_t z_stride;
 };
 
@@ -687,11 +823,12 @@ Layout layout_of(int S, int H, int Hkv, int D, bool scores, int max_ctx) {
     L.m = o;     o = align256(o + rows * sizeof(float));
     L.l = o;     o = align256(o + rows * sizeof(float));
     L.acc = o;   o = align256(o + rows * D * sizeof(float));
-    L.row_m = L.row_l = L.z = o;
+    L.place = L.row_m = L.row_l = L.z = o;
     L.z_stride = ((int64_t)max_ctx + kTile - 1) / kTile * kTile;
     if (L.z_stride == 0) L.z_stride = kTile;
     if (scores) {
-        o = align256(o + (size_t)S * H * sizeof(float));
+        o = align256(o + (size_t)S * Hkv * sizeof(int2));
+        L.row_m = o; o = align256(o + (size_t)S * H * sizeof(float));
         L.row_l = o; o = align256(o + (size_t)S * H * sizeof(float));
         L.z = o;     o = align256(o + (size_t)S * H * L.z_stride * sizeof(float));
     }
@@ -700,6 +837,7 @@ Layout layout_of(int S, int H, int Hkv, int D, bool scores, int max_ctx) {
 }
 
 using KernelFn = void (*)(Params);
+using JoinFn = void (*)(Params, int, int);
 
 template <class E, bool kScores>
 KernelFn pick_attend(int D, bool wide) {
@@ -708,7 +846,7 @@ KernelFn pick_attend(int D, bool wide) {
 }
 
 template <bool kScores>
-KernelFn pick_join(pkv_dtype dtype, int D) {
+JoinFn pick_join(pkv_dtype dtype, int D) {
     if (dtype == PKV_F16) return D == 128 ? join_kernel<pkv::F16, 128, kScores> : join_kernel<pkv::F16, 64, kScores>;
     return D == 128 ? join_kernel<pkv::BF16, 128, kScores> : join_kernel<pkv::BF16, 64, kScores>;
 }
@@ -729,6 +867,7 @@ int resident_of(KernelFn fn, int smem) {
         if (cache[i].fn == fn && cache[i].dev == dev) return cache[i].n;
     int n = 0;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, kThreads, smem) != cudaSuccess) {
         cudaGetLastError();
         return 0;
@@ -757,7 +896,8 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     if (window < 1 || sinks < 0) return bad(PKV_ERR_INVALID_ARG, "window must be >= 1 and sink_tokens >= 0");
     if (!(scale == scale) || std::isinf(scale)) return bad(PKV_ERR_INVALID_ARG, "scale must be finite");
     if ((int64_t)NB * bs > INT32_MAX) return bad(PKV_ERR_INVALID_ARG, "NB * bs must fit 31 bits");
-    if (S > 32767) return bad(PKV_ERR_INVALID_ARG, "at most 32767 sequences");
+    if (S > 32767 || (int64_t)S * H > INT32_MAX / kMaxCluster)
+        return bad(PKV_ERR_INVALID_ARG, "at most 32767 sequences, and 2^27 heads in all of them");
     const int64_t cap = (int64_t)MB * bs;
     const int64_t max_ctx = max_context_len == 0 ? (cap < INT32_MAX - 64 ? cap : INT32_MAX - 64) : max_context_len;
     if (max_ctx < 0 || max_ctx > cap || max_ctx > INT32_MAX - 64)
@@ -796,6 +936,7 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     p.qscale = scale * kLog2e;
     char* w = static_cast<char*>(workspace);
     p.info = reinterpret_cast<RangeInfo*>(w + L.info);
+    p.place = reinterpret_cast<int2*>(w + L.place);
     p.part_m = reinterpret_cast<float*>(w + L.m);
     p.part_l = reinterpret_cast<float*>(w + L.l);
     p.part_acc = reinterpret_cast<float*>(w + L.acc);
@@ -807,11 +948,6 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     p.score_stride = score_stride;
     p.err = pkv::device_error_word();
     const int64_t most = (int64_t)window + sinks < max_ctx ? (int64_t)window + sinks : max_ctx;
-    p.direct = most <= kDirectTokens;
-    p.hw = p.direct ? 1 : heads_per_cta(Hkv);
-    p.nsplit = kWarps / p.hw;
-    p.HB = Hkv / p.hw;
-
     const bool wide = p.G > 8;
     KernelFn fn = dtype == PKV_F16
                       ? (with_scores ? pick_attend<pkv::F16, true>(D, wide) : pick_attend<pkv::F16, false>(D, wide))
@@ -819,23 +955,51 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     const int smem = D == 128 ? kSmemBytes<128> : kSmemBytes<64>;
     const int per_sm = resident_of(fn, smem);
     if (per_sm < 1) return bad(PKV_ERR_CUDA, "the kernel cannot be resident");
+    const int resident = per_sm * pkv::sm_count();
+    // direct: the smallest cluster that leaves kDirectTokens per CTA; more CTAs
+    // while they still fit the card at once and have a tile per warp
+    p.cs = 1;
+    while (p.cs < kMaxCluster && most > (int64_t)kDirectTokens * p.cs) p.cs *= 2;
+    p.direct = most <= (int64_t)kDirectTokens * p.cs &&
+               (int64_t)S * Hkv * p.cs <= (int64_t)kDirectWaves * resident;
+    if (p.direct)
+        while (p.cs < kMaxCluster && (int64_t)S * Hkv * p.cs * 2 <= resident &&
+               most > (int64_t)2 * kWarps * kTile * p.cs)
+            p.cs *= 2;
+    p.hw = p.direct ? 1 : heads_per_cta(Hkv);
+    p.nsplit = kWarps / p.hw;
+    p.HB = Hkv / p.hw;
+    // as many CTAs per unit as its longest context has stretches, while the
+    // grid stays within a few times the card
+    const int units = S * p.HB, stretch = 4 * kJoinThreads / p.hw;
+    p.fold = (int)((max_ctx + stretch - 1) / stretch);
+    const int most_fold = kFoldCtas / units > 1 ? kFoldCtas / units : 1;
+    if (p.fold > most_fold) p.fold = most_fold;
+    if (p.fold < 1) p.fold = 1;
 
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cs;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = pkv::as_stream(stream);
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int ranges = per_sm * pkv::sm_count();
-    if (ranges > kMaxRanges) ranges = kMaxRanges;
-    cfg.gridDim = dim3(p.direct ? (unsigned)(S * p.HB) : (unsigned)ranges);
+    cfg.numAttrs = p.direct && p.cs > 1 ? 2 : 1;
+    const int ranges = resident < kMaxRanges ? resident : kMaxRanges;
+    cfg.gridDim = dim3(p.direct ? (unsigned)(S * p.HB * p.cs) : (unsigned)ranges);
     cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p);
     if (e == cudaSuccess && !p.direct) {
+        const int join = (p.hw * p.G + kJoinWarps - 1) / kJoinWarps;
         cfg.dynamicSmemBytes = 0;
-        e = cudaLaunchKernelEx(&cfg, with_scores ? pick_join<true>(dtype, D) : pick_join<false>(dtype, D), p);
+        cfg.blockDim = dim3(kJoinThreads);
+        cfg.gridDim = dim3((unsigned)(ranges * join + (with_scores ? units * p.fold : 0)));
+        e = cudaLaunchKernelEx(&cfg, with_scores ? pick_join<true>(dtype, D) : pick_join<false>(dtype, D), p,
+                               ranges, join);
     }
     if (e != cudaSuccess) {
         snprintf(msg, sizeof msg, "%s launch", who);

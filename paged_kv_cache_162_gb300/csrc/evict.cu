@@ -12,10 +12,11 @@
 // an order-preserving compaction would copy nearly every kept row each time.
 //
 // Selection: scores become 32-bit keys that order as the scores do (safe =
-// all ones, NaN as -inf, -0 as +0), held in shared memory; four passes over
-// 8-bit digits with a 256-bin histogram find the budget-th key, and ties are
-// kept from the lowest index by counting.  All counts are integers: the result
-// does not depend on the order of the atomics.
+// all ones, NaN as -inf, -0 as +0), held in shared memory; at most four passes
+// over 8-bit digits with a 256-bin histogram find the budget-th key (fewer when
+// a bin stays as a whole), and ties are kept from the lowest index by counting.
+// All counts are integers: the result does not depend on the order of the
+// atomics.
 //
 // One cluster of 1..8 CTAs per (s, h): each CTA holds a stretch of the row,
 // histograms are summed through distributed shared memory, so few long rows
@@ -34,11 +35,12 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 256;
 constexpr int kPasses = 4;
 constexpr int kMaxCluster = 8;
+constexpr int kKeysPerCta = 4096;     // a row's CTAs: until this many keys each
 constexpr int kSmemKeys = 48 * 1024;  // keys a CTA can hold: 192 KB
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -69,41 +71,38 @@ __device__ __forceinline__ uint32_t key_of(float score, bool safe) {
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-// Sum over the block's warps of `v` below this warp, and the block's total.
-__device__ __forceinline__ int warp_offset(int v, int* s_warp, int warp, int lane, int& total) {
-    if (lane == 0) s_warp[warp] = v;
-    __syncthreads();
-    int x = lane < kWarps ? s_warp[lane] : 0;
-    int incl = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += y;
-    }
-    total = __shfl_sync(kFull, incl, kWarps - 1);
-    const int before = __shfl_sync(kFull, incl - x, warp);
-    __syncthreads();
-    return before;
+// How many tokens of a stretch lie below the budget / past it and have a key
+// above / equal to the threshold.
+struct Counts {
+    int gt_front, gt_back, eq_front, eq_back;
+};
+__device__ __forceinline__ Counts operator+(const Counts& x, const Counts& y) {
+    return {x.gt_front + y.gt_front, x.gt_back + y.gt_back, x.eq_front + y.eq_front,
+            x.eq_back + y.eq_back};
 }
 
-template <int D>
+template <int D, bool kCluster>
 __global__ void __launch_bounds__(kThreads) evict_kernel(Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     extern __shared__ uint32_t s_keys[];
     __shared__ int s_hist[kPasses][kBins];
-    __shared__ int s_warp[kWarps];
     __shared__ int s_pick[2];
-    __shared__ int s_counts[2];      // holes and movers of this CTA's stretch
+    __shared__ Counts s_warp[kWarps];
+    __shared__ Counts s_cta;         // of this CTA's stretch, read by the cluster
     cg::cluster_group cluster = cg::this_cluster();
-    const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int CS = kCluster ? (int)cluster.num_blocks() : 1;
+    const int rank = kCluster ? (int)cluster.block_rank() : 0;
+    auto sync_row = [&] {  // all the row's CTAs
+        if constexpr (kCluster) cluster.sync(); else __syncthreads();
+    };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row = blockIdx.x / CS;
     const int s = row / p.Hkv, h = row % p.Hkv;
 
     const int raw = __ldg(p.context_lens + s);
-    const int n = raw < 0 ? 0 : (raw > p.max_ctx ? p.max_ctx : raw);
     int N = __ldg(p.token_counts + s);
+    const int n = raw < 0 ? 0 : (raw > p.max_ctx ? p.max_ctx : raw);
     if (rank == 0 && h == 0 && tid == 0) {
         if (raw != n || N < n) pkv::report(p.err, PKV_DEVERR_CONTEXT);
         p.new_lens[s] = min(n, p.budget);
@@ -117,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(Params p) {
     const bool moved_pos = pos_out != stored;
     const int b = p.budget;
 
-    if (n <= b) {  // the same in every CTA of the cluster
+    if (n <= b) {  // the same in every CTA of the row
         for (int j = rank * kThreads + tid; j < n; j += CS * kThreads) {
             if (moved_out) score_out[j] = score[j];
             if (moved_pos) pos_out[j] = stored[j];
@@ -125,53 +124,80 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(Params p) {
         return;
     }
 
-    // this CTA's stretch [j0, j1), this warp's part [w0, w1)
+    // this CTA's stretch [j0, j1) of the row
     const int seg = ((n + CS - 1) / CS + 31) & ~31;
     const int j0 = min(n, rank * seg), j1 = min(n, j0 + seg);
     const bool in_smem = seg <= p.seg_cap;
     const int oldest_recent = N - p.recent;
-    auto position = [&](int j) -> int {
-        const int q = stored[j];
-        return q >= 0 ? q : N - n + j;
+    auto make_key = [&](float sc, int stored_pos, int j) -> uint32_t {
+        const int q = stored_pos >= 0 ? stored_pos : N - n + j;
+        return key_of(sc, q < p.sinks || q >= oldest_recent);
     };
-    auto make_key = [&](int j) -> uint32_t {
-        const int q = position(j);
-        return key_of(score[j], q < p.sinks || q >= oldest_recent);
+    auto key = [&](int j) -> uint32_t {
+        return in_smem ? s_keys[j - j0] : make_key(score[j], stored[j], j);
     };
-    auto key = [&](int j) -> uint32_t { return in_smem ? s_keys[j - j0] : make_key(j); };
 
     for (int i = tid; i < kPasses * kBins; i += kThreads) (&s_hist[0][0])[i] = 0;
     __syncthreads();
 
-    // the budget-th largest key, digit by digit from the top
-    uint32_t prefix = 0;
-    int want = b;        // rank still to find among the keys with the prefix
-    int ties_before = 0; // keys equal to it in the CTAs before this one
+    // the budget-th largest key T, digit by digit from the top
+    uint32_t T = 0;
+    int want = b;        // rank still to find among the keys with the digits so far
+    int pass = 0;
 #pragma unroll 1
-    for (int pass = 0; pass < kPasses; ++pass) {
+    for (;; ++pass) {
         const int shift = 24 - 8 * pass;
-        for (int j = j0 + tid; j < j1; j += kThreads) {
-            uint32_t k;
-            if (pass == 0) {
-                k = make_key(j);
-                if (in_smem) s_keys[j - j0] = k;
-            } else {
-                k = key(j);
-                if ((k >> (shift + 8)) != prefix) continue;
+        if (pass == 0) {
+            constexpr int U = 8;  // loads in flight per thread
+            for (int base = j0; base < j1; base += U * kThreads) {
+                float sc[U];
+                int q[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int j = base + u * kThreads + tid;
+                    sc[u] = j < j1 ? score[j] : 0.f;
+                    q[u] = j < j1 ? stored[j] : 0;
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int j = base + u * kThreads + tid;
+                    if (j < j1) {
+                        const uint32_t k = make_key(sc[u], q[u], j);
+                        if (in_smem) s_keys[j - j0] = k;
+                        atomicAdd(&s_hist[0][k >> 24], 1);
+                    }
+                }
             }
-            atomicAdd(&s_hist[pass][(k >> shift) & 255u], 1);
+        } else {
+            for (int j = j0 + tid; j < j1; j += kThreads) {
+                const uint32_t k = key(j);
+                if ((k >> (shift + 8)) == T) atomicAdd(&s_hist[pass][(k >> shift) & 255u], 1);
+            }
         }
-        cluster.sync();
-        // suffix counts over the bins, 8 bins per lane of warp 0
-        if (warp == 0) {
+        sync_row();
+        // suffix counts over the bins, 8 per lane; alone, every warp does it,
+        // in a cluster warp 0 reads the others' bins and tells its CTA
+        int digit = 0, rest = 0, in_bin = 0;
+        if (!kCluster || warp == 0) {
             int c[8], sum = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                c[i] = 0;
-                for (int r = 0; r < CS; ++r)
-                    c[i] += cluster.map_shared_rank(&s_hist[pass][0], r)[8 * lane + i];
-                sum += c[i];
+            for (int i = 0; i < 8; ++i) c[i] = 0;
+            if constexpr (kCluster) {
+                for (int r = 0; r < CS; ++r) {
+                    const int4* other = reinterpret_cast<const int4*>(
+                        cluster.map_shared_rank(&s_hist[pass][0], r) + 8 * lane);
+                    const int4 x = other[0], y = other[1];
+                    c[0] += x.x; c[1] += x.y; c[2] += x.z; c[3] += x.w;
+                    c[4] += y.x; c[5] += y.y; c[6] += y.z; c[7] += y.w;
+                }
+            } else {
+                const int4* own = reinterpret_cast<const int4*>(&s_hist[pass][8 * lane]);
+                const int4 x = own[0], y = own[1];
+                c[0] = x.x; c[1] = x.y; c[2] = x.z; c[3] = x.w;
+                c[4] = y.x; c[5] = y.y; c[6] = y.z; c[7] = y.w;
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += c[i];
             int above = sum;  // keys in this lane's bins and those of higher lanes
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -179,73 +205,99 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(Params p) {
                 if (lane + o < 32) above += y;
             }
             int over = above - sum;
+            bool mine = false;
 #pragma unroll
             for (int i = 7; i >= 0; --i) {
                 if (over < want && over + c[i] >= want) {
-                    s_pick[0] = 8 * lane + i;
-                    s_pick[1] = want - over;
+                    mine = true;
+                    digit = 8 * lane + i;
+                    rest = want - over;
+                    in_bin = c[i];
                 }
                 over += c[i];
             }
+            const int src = __ffs(__ballot_sync(kFull, mine)) - 1;
+            digit = __shfl_sync(kFull, digit, src);
+            rest = __shfl_sync(kFull, rest, src);
+            in_bin = __shfl_sync(kFull, in_bin, src);
+            if (kCluster && lane == 0) {
+                s_pick[0] = digit | (in_bin == rest ? 256 : 0);
+                s_pick[1] = rest;
+            }
         }
-        __syncthreads();
-        prefix = (prefix << 8) | (uint32_t)s_pick[0];
-        want = s_pick[1];
+        bool whole = in_bin == rest;
+        if constexpr (kCluster) {
+            __syncthreads();
+            digit = s_pick[0] & 255;
+            whole = (s_pick[0] & 256) != 0;
+            rest = s_pick[1];
+        }
+        T = (T << 8) | (uint32_t)digit;
+        want = rest;
+        // every key with these digits stays: the digits left do not matter
+        if (whole || pass == kPasses - 1) break;
     }
-    const uint32_t T = prefix;
-    // `want` of the keys equal to T stay, lowest index first
-    for (int r = 0; r < rank; ++r)
-        ties_before += cluster.map_shared_rank(&s_hist[kPasses - 1][0], r)[T & 255u];
+    // keys are compared by their digits so far; `want` of those equal to T
+    // stay, lowest index first
+    const int drop = 24 - 8 * pass;
 
-    const int per = ((seg / 32 + kWarps - 1) / kWarps) * 32;  // this warp's stretch
+    // count this warp's stretch [w0, w1)
+    const int per = ((seg / 32 + kWarps - 1) / kWarps) * 32;
     const int w0 = min(j1, j0 + warp * per), w1 = min(j1, w0 + per);
-    // ties before this warp
-    int ties = 0, dummy;
-    for (int j = w0 + lane; j < w1; j += 32) ties += key(j) == T;
-    ties = __reduce_add_sync(kFull, ties);
-    const int ties0 = ties_before + warp_offset(ties, s_warp, warp, lane, dummy);
-
-    // holes and movers: count, then list in order
-    int holes = 0, movers = 0, seen = ties0;
-    auto kept = [&](int j, int& seen_ties) -> bool {  // whole warp, j = base + lane
-        const uint32_t k = j < w1 ? key(j) : 0u;
-        const unsigned eq = __ballot_sync(kFull, j < w1 && k == T);
-        const bool tie_in = seen_ties + __popc(eq & ((1u << lane) - 1u)) < want;
-        seen_ties += __popc(eq);
-        return j < w1 && (k > T || (k == T && tie_in));
-    };
-    for (int base = w0; base < w1; base += 32) {
-        const int j = base + lane;
-        const bool kp = kept(j, seen);
-        holes += __popc(__ballot_sync(kFull, j < w1 && !kp && j < b));
-        movers += __popc(__ballot_sync(kFull, kp && j >= b));
+    Counts mine = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int j = w0 + lane; j < w1; j += 32) {
+        const uint32_t k = key(j) >> drop;
+        const int gt = k > T, eq = k == T, front = j < b;
+        mine.gt_front += gt & front;
+        mine.gt_back += gt & (front ^ 1);
+        mine.eq_front += eq & front;
+        mine.eq_back += eq & (front ^ 1);
     }
-    int total_holes, total_movers;
-    int hole0 = warp_offset(holes, s_warp, warp, lane, total_holes);
-    int mover0 = warp_offset(movers, s_warp, warp, lane, total_movers);
-    if (tid == 0) {
-        s_counts[0] = total_holes;
-        s_counts[1] = total_movers;
+    mine.gt_front = __reduce_add_sync(kFull, mine.gt_front);
+    mine.gt_back = __reduce_add_sync(kFull, mine.gt_back);
+    mine.eq_front = __reduce_add_sync(kFull, mine.eq_front);
+    mine.eq_back = __reduce_add_sync(kFull, mine.eq_back);
+    if (lane == 0) s_warp[warp] = mine;
+    __syncthreads();
+    Counts before = {0, 0, 0, 0}, all = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const Counts x = s_warp[w];
+        all = all + x;
+        if (w < warp) before = before + x;
     }
-    cluster.sync();
-    int all_movers = 0;
-    for (int r = 0; r < CS; ++r) {
-        const int* other = cluster.map_shared_rank(&s_counts[0], r);
-        if (r < rank) {
-            hole0 += other[0];
-            mover0 += other[1];
+    if constexpr (kCluster) {
+        if (tid == 0) s_cta = all;
+        cluster.sync();
+        for (int r = 0; r < CS; ++r) {
+            if (r == rank) continue;
+            const Counts x = *cluster.map_shared_rank(&s_cta, r);
+            all = all + x;
+            if (r < rank) before = before + x;
         }
-        all_movers += other[1];
     }
+    // tokens below the budget come before those past it, so of the ties before
+    // any point the kept ones are the first `want`, the front ones first
+    auto kept_front = [&](int eq_front) { return min(want, eq_front); };
+    const int ties0 = before.eq_front + before.eq_back;
+    int hole0 = min(w0, b) - before.gt_front - kept_front(before.eq_front);
+    int mover0 = before.gt_back + min(want, ties0) - kept_front(before.eq_front);
+    const int all_movers = all.gt_back + min(want, all.eq_front + all.eq_back) - kept_front(all.eq_front);
+
     int32_t* hole_list = p.holes + (int64_t)row * b;
     int32_t* mover_list = p.movers + (int64_t)row * b;
-    seen = ties0;
+    int seen = ties0;
     for (int base = w0; base < w1; base += 32) {
         const int j = base + lane;
-        const bool kp = kept(j, seen);
-        const bool is_hole = j < w1 && !kp && j < b, is_mover = kp && j >= b;
-        const unsigned hm = __ballot_sync(kFull, is_hole), mm = __ballot_sync(kFull, is_mover);
+        const bool in = j < w1;
+        const uint32_t k = in ? key(j) >> drop : 0u;
         const unsigned below = (1u << lane) - 1u;
+        const unsigned eq = __ballot_sync(kFull, in && k == T);
+        const bool kp = in && (k > T || (k == T && seen + __popc(eq & below) < want));
+        seen += __popc(eq);
+        const bool is_hole = in && !kp && j < b, is_mover = kp && j >= b;
+        const unsigned hm = __ballot_sync(kFull, is_hole), mm = __ballot_sync(kFull, is_mover);
         if (is_hole) hole_list[hole0 + __popc(hm & below)] = j;
         if (is_mover) mover_list[mover0 + __popc(mm & below)] = j;
         hole0 += __popc(hm);
@@ -254,54 +306,60 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(Params p) {
             const int q = stored[j];
             if (moved_out) score_out[j] = score[j];
             if (moved_pos || q < 0) pos_out[j] = q >= 0 ? q : N - n + j;
-        } else if (j < w1 && j >= b && !kp) {  // evicted, past the new length
+        } else if (in && j >= b && !kp) {  // evicted, past the new length
             score_out[j] = 0.f;
             pos_out[j] = -1;
         }
     }
-    cluster.sync();  // the lists are complete (and no CTA's memory is read after this)
+    sync_row();  // the lists are complete (and no CTA's memory is read after this)
 
-    // moves: LPR lanes take one K or V row of D elements
+    // Moves.  A warp takes up to 32 movers: lane i looks up mover i's places
+    // and moves its score and position, then LPR lanes copy each K or V row.
     constexpr int LPR = D / 8;
-    constexpr int PER_WARP = 32 / (2 * LPR);  // movers a warp takes at once
+    constexpr int PER_STEP = 32 / (2 * LPR);  // movers copied by one warp-wide load
+    constexpr int U = 8;                      // loads in flight per lane
     const int sub = lane / (2 * LPR), part = lane % (2 * LPR);
     uint4* cache = part < LPR ? p.k_cache : p.v_cache;
-    const int col = part % LPR;
+    const int64_t row_vecs = (int64_t)p.Hkv * LPR;
+    cache += (int64_t)h * LPR + part % LPR;
     const int32_t* bt = p.block_tables + (int64_t)s * p.MB;
     const int bs_mask = (1 << p.bs_log2) - 1;
-    const int step = CS * kWarps * PER_WARP;
-    constexpr int U = 4;
-    for (int i0 = (rank * kWarps + warp) * PER_WARP + sub; i0 < all_movers; i0 += U * step) {
-        uint4 v[U];
-        uint4* dst[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * step;
-            dst[u] = nullptr;
-            if (i < all_movers) {
-                const int to = hole_list[i], of = mover_list[i];
-                const int pt = __ldg(bt + (to >> p.bs_log2)), po = __ldg(bt + (of >> p.bs_log2));
-                if ((unsigned)pt < (unsigned)p.NB && (unsigned)po < (unsigned)p.NB) {
-                    const int64_t rt = ((int64_t)pt << p.bs_log2) + (to & bs_mask);
-                    const int64_t ro = ((int64_t)po << p.bs_log2) + (of & bs_mask);
-                    dst[u] = cache + (rt * p.Hkv + h) * LPR + col;
-                    v[u] = cache[(ro * p.Hkv + h) * LPR + col];
-                } else if (part == 0) {
-                    pkv::report(p.err, PKV_DEVERR_BLOCK_ID);
-                }
-                if (part == 0) {
-                    const float sv = score[of];
-                    const int q = position(of);
-                    score_out[to] = sv;
-                    pos_out[to] = q;
-                    score_out[of] = 0.f;
-                    pos_out[of] = -1;
-                }
+    const int warps = CS * kWarps;
+    const int chunk = min(32, max(PER_STEP, (all_movers + warps - 1) / warps));
+    for (int i0 = (rank * kWarps + warp) * chunk; i0 < all_movers; i0 += warps * chunk) {
+        const int count = min(chunk, all_movers - i0);
+        int slot_to = -1, slot_of = -1;
+        if (lane < count) {
+            const int to = hole_list[i0 + lane], of = mover_list[i0 + lane];
+            const int pt = __ldg(bt + (to >> p.bs_log2)), po = __ldg(bt + (of >> p.bs_log2));
+            const float sv = score[of];
+            const int q = stored[of];
+            if ((unsigned)pt < (unsigned)p.NB && (unsigned)po < (unsigned)p.NB) {
+                slot_to = (pt << p.bs_log2) | (to & bs_mask);
+                slot_of = (po << p.bs_log2) | (of & bs_mask);
+            } else {
+                pkv::report(p.err, PKV_DEVERR_BLOCK_ID);
             }
+            score_out[to] = sv;
+            pos_out[to] = q >= 0 ? q : N - n + of;
+            score_out[of] = 0.f;
+            pos_out[of] = -1;
         }
+        for (int m = 0; m < count; m += U * PER_STEP) {
+            uint4 v[U];
+            int to[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (dst[u]) *dst[u] = v[u];
+            for (int u = 0; u < U; ++u) {
+                const int i = m + u * PER_STEP + sub;
+                to[u] = __shfl_sync(kFull, slot_to, i & 31);
+                const int of = __shfl_sync(kFull, slot_of, i & 31);
+                if (i >= count) to[u] = -1;
+                if (to[u] >= 0) v[u] = cache[of * row_vecs];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (to[u] >= 0) cache[to[u] * row_vecs] = v[u];
+        }
     }
 }
 
@@ -355,6 +413,8 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
         return pkv::fail(PKV_ERR_UNSUPPORTED, "evict_tokens: head_dim must be 64/128, block_size 8/16/32/64");
     if (budget < 1 || recent_tokens < 0 || sink_tokens < 0 || (int64_t)recent_tokens + sink_tokens > budget)
         return pkv::fail(PKV_ERR_INVALID_ARG, "evict_tokens: budget must be >= 1 and hold the sinks and the recent tokens");
+    if ((int64_t)NB * bs > INT32_MAX)
+        return pkv::fail(PKV_ERR_INVALID_ARG, "evict_tokens: NB * bs must fit 31 bits");
     if ((int64_t)S * Hkv > INT32_MAX / kMaxCluster)
         return pkv::fail(PKV_ERR_INVALID_ARG, "evict_tokens: too many rows");
     if (S == 0) return PKV_OK;
@@ -396,13 +456,14 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
     p.movers = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + list_bytes(S, Hkv, budget));
     p.err = pkv::device_error_word();
 
-    // CTAs per row: while the card is not filled and a CTA has over 4096 keys
+    // CTAs per row
     const int rows = S * Hkv;
     int cs = 1;
-    while (cs < kMaxCluster && rows * cs < 2 * pkv::sm_count() && p.max_ctx / cs > 4096) cs *= 2;
+    while (cs < kMaxCluster && p.max_ctx / cs > kKeysPerCta) cs *= 2;
     const int seg = ((p.max_ctx + cs - 1) / cs + 31) & ~31;
     p.seg_cap = seg < kSmemKeys ? seg : kSmemKeys;
-    void (*fn)(Params) = D == 128 ? evict_kernel<128> : evict_kernel<64>;
+    void (*fn)(Params) = cs > 1 ? (D == 128 ? evict_kernel<128, true> : evict_kernel<64, true>)
+                                : (D == 128 ? evict_kernel<128, false> : evict_kernel<64, false>);
     if (!ready(fn, kSmemKeys * 4)) return pkv::fail(PKV_ERR_CUDA, "evict_tokens: shared memory");
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -417,7 +478,7 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
     cfg.dynamicSmemBytes = (size_t)p.seg_cap * 4;
     cfg.stream = pkv::as_stream(stream);
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = cs > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p);
     return e == cudaSuccess ? PKV_OK : pkv::cuda_fail(e, "evict_tokens launch");
 }
