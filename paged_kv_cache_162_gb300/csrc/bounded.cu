@@ -133,22 +133,131 @@ struct Acc {
     float m[2], l[2];
 };
 
-// One warp: KV head kvh of sequence s, visible tiles first, first + step, ...
-// below te.  kWide: more than 8 query heads per KV head.
+// One warp's tiles on their way through its ring: tile i of one unit after the
+// other, `step` apart, each looked up one tile ahead of its copies and copied
+// kStages - 1 tiles ahead of its use.  chain: goes on into the units that
+// follow in the range, so that a unit's end does not drain the ring.
+template <int D>
+struct Feed {
+    static constexpr int NST = kStages<D>;
+    const Params& p;
+    const uint32_t ring;
+    const int lane, hl;       // head of the CTA's hw that this warp takes
+    const int step;
+    const bool chain;
+    int s, hb, n_next, i, te, left;  // the next tile to copy, and its unit
+    int nv, shift;
+    const int32_t* bt;
+    const uint16_t* k_head;
+    int slot;                 // cache row of its row lane % 16
+    bool more;
+    unsigned mask[NST];       // rows with a token, of the tiles in the ring
+    int stage;                // of the oldest tile
+
+    __device__ __forceinline__ Feed(const Params& p_, uint32_t ring_, int lane_, int hl_, int step_,
+                                    bool chain_)
+        : p(p_), ring(ring_), lane(lane_), hl(hl_), step(step_), chain(chain_) {}
+
+    __device__ __forceinline__ void enter(int n) {  // unit (s, hb)
+        nv = visible_of(p, n);
+        shift = n - nv;
+        bt = p.block_tables + (int64_t)s * p.MB;
+        const int kvh = hb * p.hw + hl;
+        k_head = static_cast<const uint16_t*>(p.k_cache) + (int64_t)kvh * D;
+        // the unit's queries are read when its first tile is used
+        const char* q = static_cast<const char*>(p.q) +
+                        ((int64_t)s * p.H + (int64_t)kvh * p.G) * D * 2;
+        if (lane * 128 < p.G * D * 2) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + lane * 128));
+    }
+
+    // Row lane % 16 of the next tile: its cache row, or -1 where there is no
+    // token (past the visible ones) or its block id is out of range.  NB * bs
+    // fits an int (checked on the host).
+    __device__ __forceinline__ void lookup() {
+        slot = -1;
+        const int v = i * kTile + (lane & 15);
+        if (!more || v >= nv) return;
+        const int tok = v < p.sinks ? v : v + shift;
+        const int phys = __ldg(bt + (tok >> p.bs_log2));
+        if ((unsigned)phys >= (unsigned)p.NB) {
+            pkv::report(p.err, PKV_DEVERR_BLOCK_ID);
+            return;
+        }
+        slot = (phys << p.bs_log2) | (tok & ((1 << p.bs_log2) - 1));
+    }
+
+    // Tiles first, first + step, ... below te_ of unit (s_, hb_); left_: tiles
+    // up to the range's end, counted from the unit's first one.
+    __device__ __forceinline__ void begin(int s_, int hb_, int n, int first, int te_, int left_) {
+        s = s_;
+        hb = hb_;
+        i = first;
+        te = te_;
+        left = left_;
+        n_next = chain && s + 1 < p.S ? context_of(p, s + 1) : 0;
+        more = i < te;
+        enter(n);
+        lookup();
+        stage = 0;
+#pragma unroll
+        for (int st = 0; st < NST - 1; ++st) push(st, st);
+    }
+
+    // Copies the next tile into ring stage `st` and its row mask into
+    // mask[at], then looks up the one after it.
+    __device__ __forceinline__ void push(int st, int at) {
+        constexpr int ROWB = D * 2, CPR = ROWB / 16, CPL = kTile * CPR / 32;
+        mask[at] = __ballot_sync(kFull, slot >= 0) & 0xffffu;
+        if (more) {
+            const uint32_t sk = ring + st * 2 * kTileBytes<D>, sv = sk + kTileBytes<D>;
+            const int64_t row_elems = (int64_t)p.Hkv * D;
+            const int64_t to_v = static_cast<const uint16_t*>(p.v_cache) - static_cast<const uint16_t*>(p.k_cache);
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) {
+                const int chunk = lane + 32 * j;
+                const int row = chunk / CPR, c = chunk % CPR;
+                const int sl = __shfl_sync(kFull, slot, row);
+                const uint16_t* src = k_head + (int64_t)(sl < 0 ? 0 : sl) * row_elems + c * 8;
+                const uint32_t dst = row * ROWB + ((c ^ (row & 7)) * 16);
+                const int bytes = sl < 0 ? 0 : 16;
+                cp_async16_zfill(sk + dst, src, bytes);
+                cp_async16_zfill(sv + dst, src + to_v, bytes);
+            }
+            i += step;
+            if (i >= te) {
+                left -= te;
+                more = chain && left > 0;
+                if (more) {
+                    int n;
+                    if (++hb == p.HB) {
+                        hb = 0;
+                        ++s;
+                        n = n_next;
+                        n_next = s + 1 < p.S ? context_of(p, s + 1) : 0;
+                    } else {
+                        n = context_of(p, s);
+                    }
+                    enter(n);
+                    i = 0;
+                    te = min(tiles_of(p, n), left);
+                }
+            }
+            lookup();
+        }
+        cp_async_commit();  // empty past the end: the counting stays simple
+    }
+};
+
+// One warp: KV head kvh of sequence s, its tiles first, first + step, ... below
+// te out of the feed.  kWide: more than 8 query heads per KV head.
 template <class E, int D, bool kWide, bool kScores>
-__device__ __forceinline__ void attend(const Params& p, int s, int kvh, int n, int first, int te,
-                                       int step, uint32_t ring, int lane, Acc<D>& a) {
+__device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, int kvh, int first,
+                                       int te, int lane, Acc<D>& a) {
     constexpr int NK = D / 16, NO = D / 8;
-    constexpr int ROWB = D * 2, CPR = ROWB / 16, CPL = kTile * CPR / 32;
+    constexpr int ROWB = D * 2;
     constexpr int NST = kStages<D>;
     constexpr int R = kWide ? 2 : 1;
     const int g = lane >> 2, t = lane & 3;
-    const int nv = visible_of(p, n), shift = n - nv;
-    const int64_t row_elems = (int64_t)p.Hkv * D;
-    const int bs_mask = (1 << p.bs_log2) - 1;
-    const int32_t* bt = p.block_tables + (int64_t)s * p.MB;
-    const uint16_t* k_head = static_cast<const uint16_t*>(p.k_cache) + (int64_t)kvh * D;
-    const uint16_t* v_head = static_cast<const uint16_t*>(p.v_cache) + (int64_t)kvh * D;
 
 #pragma unroll
     for (int j = 0; j < NO; ++j) a.o[j][0] = a.o[j][1] = a.o[j][2] = a.o[j][3] = 0.f;
@@ -171,53 +280,13 @@ __device__ __forceinline__ void attend(const Params& p, int s, int kvh, int n, i
         }
     }
 
-    // Row lane % 16 of tile i: its cache row, or -1 where there is no token
-    // (past the visible ones) or its block id is out of range.  NB * bs fits
-    // an int (checked on the host).
-    auto lookup = [&](int i) -> int {
-        const int v = i * kTile + (lane & 15);
-        if (i >= te || v >= nv) return -1;
-        const int tok = v < p.sinks ? v : v + shift;
-        const int phys = __ldg(bt + (tok >> p.bs_log2));
-        if ((unsigned)phys >= (unsigned)p.NB) {
-            pkv::report(p.err, PKV_DEVERR_BLOCK_ID);
-            return -1;
-        }
-        return (phys << p.bs_log2) | (tok & bs_mask);
-    };
-    unsigned mask[NST];  // rows with a token, of the tiles in flight
-    int slot = lookup(first);
-    // copies of tile i into ring stage `stage`, then the lookup for the next
-    auto issue = [&](int i, int stage) -> unsigned {
-        const unsigned rows = __ballot_sync(kFull, slot >= 0) & 0xffffu;
-        if (i < te) {
-            const uint32_t sk = ring + stage * 2 * kTileBytes<D>, sv = sk + kTileBytes<D>;
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                const int chunk = lane + 32 * j;
-                const int row = chunk / CPR, c = chunk % CPR;
-                const int sl = __shfl_sync(kFull, slot, row);
-                const int64_t off = (int64_t)(sl < 0 ? 0 : sl) * row_elems + c * 8;
-                const uint32_t dst = row * ROWB + ((c ^ (row & 7)) * 16);
-                const int bytes = sl < 0 ? 0 : 16;
-                cp_async16_zfill(sk + dst, k_head + off, bytes);
-                cp_async16_zfill(sv + dst, v_head + off, bytes);
-            }
-            slot = lookup(i + step);
-        }
-        cp_async_commit();  // empty past the end: the counting stays simple
-        return rows;
-    };
-
-#pragma unroll
-    for (int st = 0; st < NST - 1; ++st) mask[st] = issue(first + st * step, st);
-    int stage = 0;
-    for (int i = first; i < te; i += step) {
-        const int fill = stage == 0 ? NST - 1 : stage - 1;
-        mask[NST - 1] = issue(i + (NST - 1) * step, fill);
+    for (int i = first; i < te; i += feed.step) {
+        const int stage = feed.stage;
+        feed.push(stage == 0 ? NST - 1 : stage - 1, NST - 1);
+        const unsigned rows = feed.mask[0];
         cp_async_wait<NST - 1>();
         __syncwarp();
-        const uint32_t sk = ring + stage * 2 * kTileBytes<D>, sv = sk + kTileBytes<D>;
+        const uint32_t sk = feed.ring + stage * 2 * kTileBytes<D>, sv = sk + kTileBytes<D>;
 
         float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
         {
@@ -238,7 +307,7 @@ __device__ __forceinline__ void attend(const Params& p, int s, int kvh, int n, i
 #pragma unroll
             for (int e = 0; e < 2 * R; ++e) {
                 sc[j][e] *= p.qscale;
-                if (mask[0] != 0xffffu && !((mask[0] >> (8 * j + 2 * t + (e & 1))) & 1u))
+                if (rows != 0xffffu && !((rows >> (8 * j + 2 * t + (e & 1))) & 1u))
                     sc[j][e] = -INFINITY;
             }
         if constexpr (kScores) {
@@ -308,12 +377,11 @@ __device__ __forceinline__ void attend(const Params& p, int s, int kvh, int n, i
                 Mma<E>::run(a.o[j + 1], pl, b[2], b[3]);
             }
         }
-        __syncwarp();  // this stage is filled again by the next issue
+        __syncwarp();  // this stage is filled again by the next push
 #pragma unroll
-        for (int st = 0; st < NST - 1; ++st) mask[st] = mask[st + 1];
-        stage = stage + 1 == NST ? 0 : stage + 1;
+        for (int st = 0; st < NST - 1; ++st) feed.mask[st] = feed.mask[st + 1];
+        feed.stage = stage + 1 == NST ? 0 : stage + 1;
     }
-    cp_async_wait<0>();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         a.l[r] += __shfl_xor_sync(kFull, a.l[r], 1);
@@ -522,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 2) bounded_kernel(Params p) {
     const int c = blockIdx.x;
 
     int s, hb, tb, n;
-    long long left = LLONG_MAX;   // tiles left in this range
+    long long left = 0;           // tiles left in this range
     long long unit0 = 0;          // first tile of the current unit
     long long range = 1;
     int end = 0;                  // direct: tiles [tb, end) are this CTA's
@@ -538,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 2) bounded_kernel(Params p) {
         const int T = tiles_of(p, n), per = (T + p.cs - 1) / p.cs;
         tb = min(T, crank * per);
         end = min(T, tb + per);
-        } else {
+    } else {
         // tiles before each thread's run of sequences
         const int per = (p.S + kThreads - 1) / kThreads;
         long long mine = 0;
@@ -607,12 +675,19 @@ __global__ void __launch_bounds__(kThreads, 2) bounded_kernel(Params p) {
         unit0 = begin - tb;
     }
 
-    for (;;) {
+    // with one warp per head the tiles of all units run through the ring
+    // without a break; token splits are joined in the ring's memory, so there
+    // every unit starts anew
+    const bool chain = !p.direct && p.nsplit == 1;
+    Feed<D> feed(p, ring, lane, hl, p.nsplit, chain);
+    for (bool first = true;; first = false) {
         const int T = tiles_of(p, n);
         const int te = p.direct ? end : (int)min((long long)T, tb + left);
         const int kvh = hb * p.hw + hl;
         Acc<D> a;
-        attend<E, D, kWide, kScores>(p, s, kvh, n, tb + split, te, p.nsplit, ring, lane, a);
+        if (!chain || first) feed.begin(s, hb, n, tb + split, te, (int)left + tb);
+        attend<E, D, kWide, kScores>(p, feed, s, kvh, tb + split, te, lane, a);
+        if (!chain) cp_async_wait<0>();
         if (p.nsplit > 1) join_splits<D>(p, reinterpret_cast<float*>(smem), warp, lane, a);
         const bool whole = tb == 0 && te == T;
         if (p.direct && p.cs > 1) {
@@ -689,32 +764,42 @@ __global__ void __launch_bounds__(kThreads, 2) bounded_kernel(Params p) {
     }
 }
 
-// M and L of one row over the pieces of a cut unit: the first in range c0,
-// the last in range c1.  All lanes return them; `mine` is piece c0 + lane's
-// weight.
+// Row `row` of head hl in the piece that range c has of a unit beginning in c0.
 __device__ __forceinline__ int64_t piece_row(const Params& p, int c, int c0, int hl, int row) {
     return ((2 * (int64_t)c + (c == c0 ? 1 : 0)) * p.hw + hl) * p.G + row;
 }
 
-__device__ __forceinline__ void join_row(const Params& p, int c0, int c1, int hl, int row,
-                                         int lane, float& M, float& L) {
+// M and L of one row over the pieces of a cut unit, ranges c0 .. c1: by one
+// thread (kWarp false), or by a warp whose lanes share the pieces.
+template <bool kWarp>
+__device__ __forceinline__ void join_row(const Params& p, int c0, int c1, int hl, int row, int lane,
+                                         float& M, float& L) {
     M = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_m[piece_row(p, c, c0, hl, row)]);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-    const float use = M == -INFINITY ? 0.f : M;
     L = 0.f;
-    for (int c = c0 + lane; c <= c1; c += 32) {
+    for (int c = kWarp ? c0 + lane : c0; c <= c1; c += kWarp ? 32 : 1) {
         const int64_t at = piece_row(p, c, c0, hl, row);
-        L = fmaf(exp2f(p.part_m[at] - use), p.part_l[at], L);
+        const float m = p.part_m[at], l = p.part_l[at];
+        const float m_new = fmaxf(M, m);
+        const float use = m_new == -INFINITY ? 0.f : m_new;
+        L = L * exp2f(M - use) + l * exp2f(m - use);
+        M = m_new;
     }
+    if constexpr (kWarp) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(kFull, L, o);
+        for (int o = 16; o >= 1; o >>= 1) {
+            const float m = __shfl_xor_sync(kFull, M, o), l = __shfl_xor_sync(kFull, L, o);
+            const float m_new = fmaxf(M, m);
+            const float use = m_new == -INFINITY ? 0.f : m_new;
+            L = L * exp2f(M - use) + l * exp2f(m - use);
+            M = m_new;
+        }
+    }
 }
 
 // After bounded_kernel.  The first ranges * join CTAs join, per range, the
-// pieces of the unit that begins in it and ends in a later one, a warp per
-// row.  With scores, `fold` CTAs per unit follow; each takes every fold-th
+// pieces of the unit that begins in it and ends in a later one: a warp per
+// row, or all the CTA's warps on one row (`wpr` of them) where a unit has many
+// pieces.  With scores, `fold` CTAs per unit follow; each takes every fold-th
 // stretch of the unit's tokens, 4 tokens of a head per thread, and folds their
 // weights into the scores.  A stretch is one round of loads: the chain is
 // length and place of the unit -> M, L, z and scores -> store.
@@ -722,41 +807,70 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
 template <class E, int D, bool kScores>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(Params p, int ranges, int join) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(Params p, int ranges, int join, int wpr) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     __shared__ float s_m[4 * kMaxGroup], s_inv[4 * kMaxGroup];
+    __shared__ __align__(16) float s_o[kJoinWarps][D];
     constexpr int DPL = D / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rows = p.hw * p.G;
     if ((int)blockIdx.x < ranges * join) {
         const int c = blockIdx.x / join;
-        const int i = (blockIdx.x % join) * kJoinWarps + warp;
-        const RangeInfo ri = p.info[c];
-        if (ri.unit < 0 || i >= rows) return;
+        const int i = (blockIdx.x % join) * (kJoinWarps / wpr) + warp / wpr;
+        if (i >= rows) return;
         const int hl = i / p.G, row = i % p.G;
+        auto load_piece = [&](int64_t at, float (&x)[DPL]) {
+            const float* src = p.part_acc + at * D + lane * DPL;
+            if constexpr (DPL == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(src);
+                x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(src);
+                x[0] = v.x; x[1] = v.y;
+            }
+        };
+        // most cut units have two pieces, whose places do not depend on the
+        // unit: their loads go out with the look at whether there is one
+        float x0[DPL], x1[DPL];
+        if (wpr == 1 && c + 1 < ranges) {
+            load_piece(piece_row(p, c, c, hl, row), x0);
+            load_piece(piece_row(p, c + 1, c, hl, row), x1);
+        }
+        const RangeInfo ri = p.info[c];
+        if (ri.unit < 0) return;  // the same for all warps of a row
         float M, L;
-        join_row(p, c, ri.c1, hl, row, lane, M, L);
+        join_row<true>(p, c, ri.c1, hl, row, lane, M, L);
         const float use = M == -INFINITY ? 0.f : M;
         float o[DPL];
 #pragma unroll
         for (int j = 0; j < DPL; ++j) o[j] = 0.f;
+        auto add = [&](int cc, const float (&x)[DPL]) {
+            const float w = exp2f(p.part_m[piece_row(p, cc, c, hl, row)] - use);
+#pragma unroll
+            for (int j = 0; j < DPL; ++j) o[j] = fmaf(w, x[j], o[j]);
+        };
+        int cc = c + warp % wpr;
+        if (wpr == 1) {
+            add(c, x0);
+            add(c + 1, x1);
+            cc = c + 2;
+        }
 #pragma unroll 8
-        for (int cc = c; cc <= ri.c1; ++cc) {
-            const int64_t at = piece_row(p, cc, c, hl, row);
-            const float w = exp2f(p.part_m[at] - use);
-            const float* src = p.part_acc + at * D + lane * DPL;
-            if constexpr (DPL == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(src);
-                o[0] = fmaf(w, x.x, o[0]);
-                o[1] = fmaf(w, x.y, o[1]);
-                o[2] = fmaf(w, x.z, o[2]);
-                o[3] = fmaf(w, x.w, o[3]);
-            } else {
-                const float2 x = *reinterpret_cast<const float2*>(src);
-                o[0] = fmaf(w, x.x, o[0]);
-                o[1] = fmaf(w, x.y, o[1]);
-            }
+        for (; cc <= ri.c1; cc += wpr) {
+            float x[DPL];
+            load_piece(piece_row(p, cc, c, hl, row), x);
+            add(cc, x);
+        }
+        if (wpr > 1) {  // one row per CTA: add the warps' sums
+#pragma unroll
+            for (int j = 0; j < DPL; ++j) s_o[warp][lane * DPL + j] = o[j];
+            __syncthreads();
+            if (warp != 0) return;
+#pragma unroll
+            for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+                for (int j = 0; j < DPL; ++j) o[j] += s_o[w][lane * DPL + j];
         }
         const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
         const int64_t oh = (int64_t)(ri.unit / p.HB) * p.H + (int64_t)(ri.unit % p.HB) * rows + i;
@@ -774,18 +888,26 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(Params p, int ranges
         const int n = context_of(p, s);
         const int per = kJoinThreads / p.hw;  // threads per head
         if (part * 4 * per >= n) return;
-        for (int i = warp; i < rows; i += kJoinWarps) {
-            float M, L;
-            if (place.x == place.y) {
-                const int64_t oh = (int64_t)s * p.H + (int64_t)hb * rows + i;
-                M = p.row_m[oh];
-                L = p.row_l[oh];
-            } else {
-                join_row(p, place.x, place.y, i / p.G, i % p.G, lane, M, L);
+        auto keep = [&](int i, float M, float L) {
+            s_m[i] = M;
+            s_inv[i] = L > 0.f || L != L ? 1.f / L : 0.f;
+        };
+        if (place.x == place.y) {
+            if (tid < rows) {
+                const int64_t oh = (int64_t)s * p.H + (int64_t)hb * rows + tid;
+                keep(tid, p.row_m[oh], p.row_l[oh]);
             }
-            if (lane == 0) {
-                s_m[i] = M;
-                s_inv[i] = L > 0.f || L != L ? 1.f / L : 0.f;
+        } else if (place.y - place.x < 4) {  // few pieces: a thread per row
+            if (tid < rows) {
+                float M, L;
+                join_row<false>(p, place.x, place.y, tid / p.G, tid % p.G, lane, M, L);
+                keep(tid, M, L);
+            }
+        } else {
+            for (int i = warp; i < rows; i += kJoinWarps) {
+                float M, L;
+                join_row<true>(p, place.x, place.y, i / p.G, i % p.G, lane, M, L);
+                if (lane == 0) keep(i, M, L);
             }
         }
         __syncthreads();
@@ -803,7 +925,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(Params p, int ranges
 // resident ones.
 constexpr int kDirectTokens = 512;
 constexpr int kDirectWaves = 2;
-constexpr int kFoldCtas = 8192;     // of a split call
+constexpr int kFoldCtas = 4096;     // of a split call
+constexpr int kMinUnits = 16;       // of a split call, else fewer KV heads per unit
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -837,7 +960,7 @@ Layout layout_of(int S, int H, int Hkv, int D, bool scores, int max_ctx) {
 }
 
 using KernelFn = void (*)(Params);
-using JoinFn = void (*)(Params, int, int);
+using JoinFn = void (*)(Params, int, int, int);
 
 template <class E, bool kScores>
 KernelFn pick_attend(int D, bool wide) {
@@ -967,6 +1090,7 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
                most > (int64_t)2 * kWarps * kTile * p.cs)
             p.cs *= 2;
     p.hw = p.direct ? 1 : heads_per_cta(Hkv);
+    while (!p.direct && p.hw > 1 && (int64_t)S * Hkv / p.hw < kMinUnits) p.hw /= 2;
     p.nsplit = kWarps / p.hw;
     p.HB = Hkv / p.hw;
     // as many CTAs per unit as its longest context has stretches, while the
@@ -994,12 +1118,14 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     cfg.gridDim = dim3(p.direct ? (unsigned)(S * p.HB * p.cs) : (unsigned)ranges);
     cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p);
     if (e == cudaSuccess && !p.direct) {
-        const int join = (p.hw * p.G + kJoinWarps - 1) / kJoinWarps;
+        // a unit of more than 16 pieces: a CTA per row
+        const int wpr = ranges > 16 * units ? kJoinWarps : 1;
+        const int join = (p.hw * p.G * wpr + kJoinWarps - 1) / kJoinWarps;
         cfg.dynamicSmemBytes = 0;
         cfg.blockDim = dim3(kJoinThreads);
         cfg.gridDim = dim3((unsigned)(ranges * join + (with_scores ? units * p.fold : 0)));
         e = cudaLaunchKernelEx(&cfg, with_scores ? pick_join<true>(dtype, D) : pick_join<false>(dtype, D), p,
-                               ranges, join);
+                               ranges, join, wpr);
     }
     if (e != cudaSuccess) {
         snprintf(msg, sizeof msg, "%s launch", who);

@@ -12,9 +12,9 @@
 // an order-preserving compaction would copy nearly every kept row each time.
 //
 // Selection: scores become 32-bit keys that order as the scores do (safe =
-// all ones, NaN as -inf, -0 as +0), held in shared memory; at most four passes
-// over 8-bit digits with a 256-bin histogram find the budget-th key (fewer when
-// a bin stays as a whole), and ties are kept from the lowest index by counting.
+// all ones, NaN as -inf, -0 as +0), held in shared memory; histograms of
+// one digit after the other find the budget-th key (the last digits are
+// skipped when a bin stays as a whole), and ties are kept from the lowest index by counting.
 // All counts are integers: the result does not depend on the order of the
 // atomics.
 //
@@ -37,11 +37,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 256;
-constexpr int kPasses = 4;
 constexpr int kMaxCluster = 8;
-constexpr int kKeysPerCta = 4096;     // a row's CTAs: until this many keys each
+constexpr int kFewKeys = 2048;        // a row of fewer is one CTA's
 constexpr int kSmemKeys = 48 * 1024;  // keys a CTA can hold: 192 KB
+constexpr int kChunk = 128;           // keys a warp takes at once, 4 per lane
 constexpr unsigned kFull = 0xffffffffu;
 
 struct Params {
@@ -59,6 +58,7 @@ struct Params {
     int64_t stride;       // of the score and position rows
     int budget, recent, sinks;
     int seg_cap;          // keys the shared memory holds
+    int vec;              // the score and position rows start on 16 bytes
     int32_t* holes;       // [S * Hkv][budget]
     int32_t* movers;      // [S * Hkv][budget]
     int* err;
@@ -81,13 +81,46 @@ __device__ __forceinline__ Counts operator+(const Counts& x, const Counts& y) {
             x.eq_back + y.eq_back};
 }
 
+// Four consecutive entries, of which the first `count` exist (the others are
+// `none`): one 16-byte load where the row allows it.
+template <class T>
+__device__ __forceinline__ void load4(const T* p, int count, bool vec, T none, T (&v)[4]) {
+    if (vec && count >= 4) {
+        const int4 x = *reinterpret_cast<const int4*>(p);
+        const int w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const T*>(&w[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = e < count ? p[e] : none;
+    }
+}
+template <class T>
+__device__ __forceinline__ void store4(T* p, int count, bool vec, const T (&v)[4]) {
+    if (vec && count >= 4) {
+        int w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const int*>(&v[e]);
+        *reinterpret_cast<int4*>(p) = make_int4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < count) p[e] = v[e];
+    }
+}
+
 template <int D, bool kCluster>
-__global__ void __launch_bounds__(kThreads) evict_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, 4) evict_kernel(Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    extern __shared__ uint32_t s_keys[];
-    __shared__ int s_hist[kPasses][kBins];
-    __shared__ int s_pick[2];
+    extern __shared__ __align__(16) uint32_t s_keys[];
+    // digits of 11 bits, or of 8 in a cluster, where every CTA reads every
+    // histogram
+    constexpr int BITS = kCluster ? 8 : 11, PASSES = (31 + BITS) / BITS;
+    constexpr int BINS = 1 << BITS, BPT = BINS / kThreads;  // bins per thread
+    __shared__ __align__(16) int s_hist[2][BINS];
+    __shared__ int s_sum[kWarps];
+    __shared__ int s_pick[3];
     __shared__ Counts s_warp[kWarps];
     __shared__ Counts s_cta;         // of this CTA's stretch, read by the cluster
     cg::cluster_group cluster = cg::this_cluster();
@@ -102,6 +135,12 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(Params p) {
 
     const int raw = __ldg(p.context_lens + s);
     int N = __ldg(p.token_counts + s);
+    auto clear = [&](int which) {
+#pragma unroll
+        for (int i = 0; i < BPT; ++i) s_hist[which][i * kThreads + tid] = 0;
+    };
+    clear(0);
+    clear(1);
     const int n = raw < 0 ? 0 : (raw > p.max_ctx ? p.max_ctx : raw);
     if (rank == 0 && h == 0 && tid == 0) {
         if (raw != n || N < n) pkv::report(p.err, PKV_DEVERR_CONTEXT);
@@ -114,18 +153,24 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(Params p) {
     int32_t* pos_out = p.positions_out + (int64_t)row * p.stride;
     const bool moved_out = score_out != score;     // results go to other arrays
     const bool moved_pos = pos_out != stored;
+    const bool vec = p.vec;
     const int b = p.budget;
 
     if (n <= b) {  // the same in every CTA of the row
-        for (int j = rank * kThreads + tid; j < n; j += CS * kThreads) {
-            if (moved_out) score_out[j] = score[j];
-            if (moved_pos) pos_out[j] = stored[j];
+        if (!moved_out && !moved_pos) return;
+        for (int j = 4 * (rank * kThreads + tid); j < n; j += 4 * CS * kThreads) {
+            float sc[4];
+            int q[4];
+            load4(score + j, n - j, vec, 0.f, sc);
+            load4(stored + j, n - j, vec, 0, q);
+            if (moved_out) store4(score_out + j, n - j, vec, sc);
+            if (moved_pos) store4(pos_out + j, n - j, vec, q);
         }
         return;
     }
 
     // this CTA's stretch [j0, j1) of the row
-    const int seg = ((n + CS - 1) / CS + 31) & ~31;
+    const int seg = ((n + CS - 1) / CS + kChunk - 1) / kChunk * kChunk;
     const int j0 = min(n, rank * seg), j1 = min(n, j0 + seg);
     const bool in_smem = seg <= p.seg_cap;
     const int oldest_recent = N - p.recent;
@@ -133,126 +178,150 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(Params p) {
         const int q = stored_pos >= 0 ? stored_pos : N - n + j;
         return key_of(sc, q < p.sinks || q >= oldest_recent);
     };
-    auto key = [&](int j) -> uint32_t {
-        return in_smem ? s_keys[j - j0] : make_key(score[j], stored[j], j);
+    // keys of tokens j .. j + 3 (j a multiple of 4 from j0 on, below j1)
+    auto keys4 = [&](int j, uint32_t (&k)[4]) {
+        if (in_smem) {
+            const uint4 x = *reinterpret_cast<const uint4*>(s_keys + (j - j0));
+            k[0] = x.x; k[1] = x.y; k[2] = x.z; k[3] = x.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) k[e] = j + e < j1 ? make_key(score[j + e], stored[j + e], j + e) : 0u;
+        }
     };
+    __syncthreads();  // the histograms are empty
 
-    for (int i = tid; i < kPasses * kBins; i += kThreads) (&s_hist[0][0])[i] = 0;
-    __syncthreads();
+    // First pass over the row: keys, their first digit, and what does not
+    // wait for the selection.  Entries below the budget keep their place
+    // unless a mover comes (written later, over this); entries past it end as
+    // 0 and -1, here where that is another array than the one movers are read
+    // from.
+    constexpr int U = 2;  // rounds of loads in flight
+    for (int base = j0 + 4 * tid; base < j1; base += 4 * U * kThreads) {
+        float sc[U][4];
+        int q[U][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = base + 4 * u * kThreads;
+            load4(score + j, j1 - j, vec, 0.f, sc[u]);
+            load4(stored + j, j1 - j, vec, 0, q[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = base + 4 * u * kThreads, count = j1 - j;
+            if (count <= 0) break;
+            uint32_t k[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                k[e] = make_key(sc[u][e], q[u][e], j + e);
+                if (e < count) atomicAdd(&s_hist[0][k[e] >> (32 - BITS)], 1);
+            }
+            if (in_smem) *reinterpret_cast<uint4*>(s_keys + (j - j0)) = make_uint4(k[0], k[1], k[2], k[3]);
+            bool fresh = false;  // a position that was not stored yet
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                fresh |= q[u][e] < 0;
+                if (j + e < b) {
+                    q[u][e] = q[u][e] >= 0 ? q[u][e] : N - n + j + e;
+                } else {
+                    sc[u][e] = 0.f;
+                    q[u][e] = -1;
+                }
+            }
+            if (moved_out) store4(score_out + j, count, vec, sc[u]);
+            if (moved_pos) store4(pos_out + j, count, vec, q[u]);
+            else if (fresh && j < b) store4(pos_out + j, min(count, b - j), vec, q[u]);
+        }
+    }
 
-    // the budget-th largest key T, digit by digit from the top
+    // the budget-th largest key T, digit by digit from the top; two histograms
+    // in turn
     uint32_t T = 0;
     int want = b;        // rank still to find among the keys with the digits so far
-    int pass = 0;
-#pragma unroll 1
-    for (;; ++pass) {
-        const int shift = 24 - 8 * pass;
-        if (pass == 0) {
-            constexpr int U = 8;  // loads in flight per thread
-            for (int base = j0; base < j1; base += U * kThreads) {
-                float sc[U];
-                int q[U];
+    int drop = 32 - BITS;  // bits below the digits so far
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int j = base + u * kThreads + tid;
-                    sc[u] = j < j1 ? score[j] : 0.f;
-                    q[u] = j < j1 ? stored[j] : 0;
-                }
+    for (int pass = 0; pass < PASSES; ++pass) {
+        sync_row();
+        // counts of the keys in higher bins: BPT bins per thread, warps, block
+        int c[BPT], sum = 0;
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int j = base + u * kThreads + tid;
-                    if (j < j1) {
-                        const uint32_t k = make_key(sc[u], q[u], j);
-                        if (in_smem) s_keys[j - j0] = k;
-                        atomicAdd(&s_hist[0][k >> 24], 1);
-                    }
-                }
-            }
-        } else {
-            for (int j = j0 + tid; j < j1; j += kThreads) {
-                const uint32_t k = key(j);
-                if ((k >> (shift + 8)) == T) atomicAdd(&s_hist[pass][(k >> shift) & 255u], 1);
+        for (int i = 0; i < BPT; ++i) c[i] = 0;
+        for (int r = 0; r < CS; ++r) {
+            const int* hist = &s_hist[pass & 1][BPT * tid];
+            if constexpr (kCluster) hist = cluster.map_shared_rank(hist, r);
+            if constexpr (BPT == 8) {
+                const int4 x = reinterpret_cast<const int4*>(hist)[0], y = reinterpret_cast<const int4*>(hist)[1];
+                c[0] += x.x; c[1] += x.y; c[2] += x.z; c[3] += x.w;
+                c[4] += y.x; c[5] += y.y; c[6] += y.z; c[7] += y.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < BPT; ++i) c[i] += hist[i];
             }
         }
-        sync_row();
-        // suffix counts over the bins, 8 per lane; alone, every warp does it,
-        // in a cluster warp 0 reads the others' bins and tells its CTA
-        int digit = 0, rest = 0, in_bin = 0;
-        if (!kCluster || warp == 0) {
-            int c[8], sum = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = 0;
-            if constexpr (kCluster) {
-                for (int r = 0; r < CS; ++r) {
-                    const int4* other = reinterpret_cast<const int4*>(
-                        cluster.map_shared_rank(&s_hist[pass][0], r) + 8 * lane);
-                    const int4 x = other[0], y = other[1];
-                    c[0] += x.x; c[1] += x.y; c[2] += x.z; c[3] += x.w;
-                    c[4] += y.x; c[5] += y.y; c[6] += y.z; c[7] += y.w;
-                }
-            } else {
-                const int4* own = reinterpret_cast<const int4*>(&s_hist[pass][8 * lane]);
-                const int4 x = own[0], y = own[1];
-                c[0] = x.x; c[1] = x.y; c[2] = x.z; c[3] = x.w;
-                c[4] = y.x; c[5] = y.y; c[6] = y.z; c[7] = y.w;
-            }
+        for (int i = 0; i < BPT; ++i) sum += c[i];
+        int above = sum;  // keys in this lane's bins and those of higher lanes
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += c[i];
-            int above = sum;  // keys in this lane's bins and those of higher lanes
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_down_sync(kFull, above, o);
+            if (lane + o < 32) above += y;
+        }
+        if (lane == 0) s_sum[warp] = above;
+        __syncthreads();
+        int over = above - sum;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_down_sync(kFull, above, o);
-                if (lane + o < 32) above += y;
-            }
-            int over = above - sum;
-            bool mine = false;
+        for (int w = 1; w < kWarps; ++w)
+            if (w > warp) over += s_sum[w];
+        if (over < want && over + sum >= want) {  // one thread's bins hold it
 #pragma unroll
-            for (int i = 7; i >= 0; --i) {
+            for (int i = BPT - 1; i >= 0; --i) {
                 if (over < want && over + c[i] >= want) {
-                    mine = true;
-                    digit = 8 * lane + i;
-                    rest = want - over;
-                    in_bin = c[i];
+                    s_pick[0] = BPT * tid + i;
+                    s_pick[1] = want - over;
+                    s_pick[2] = c[i];
                 }
                 over += c[i];
             }
-            const int src = __ffs(__ballot_sync(kFull, mine)) - 1;
-            digit = __shfl_sync(kFull, digit, src);
-            rest = __shfl_sync(kFull, rest, src);
-            in_bin = __shfl_sync(kFull, in_bin, src);
-            if (kCluster && lane == 0) {
-                s_pick[0] = digit | (in_bin == rest ? 256 : 0);
-                s_pick[1] = rest;
-            }
         }
-        bool whole = in_bin == rest;
-        if constexpr (kCluster) {
+        __syncthreads();
+        const int bits = min(BITS, 32 - BITS * pass);  // of this digit
+        T = pass == 0 ? (uint32_t)s_pick[0] : (T << bits) | (uint32_t)s_pick[0];
+        want = s_pick[1];
+        // done, or every key with these digits stays: the rest do not matter
+        if (pass == PASSES - 1 || s_pick[2] == want) break;
+        const int low = max(0, drop - BITS);           // bits below the next digit
+        if (pass >= 1) {  // the next digit goes where the one before last was
+            clear((pass + 1) & 1);
             __syncthreads();
-            digit = s_pick[0] & 255;
-            whole = (s_pick[0] & 256) != 0;
-            rest = s_pick[1];
         }
-        T = (T << 8) | (uint32_t)digit;
-        want = rest;
-        // every key with these digits stays: the digits left do not matter
-        if (whole || pass == kPasses - 1) break;
+        for (int j = j0 + 4 * tid; j < j1; j += 4 * kThreads) {
+            uint32_t k[4];
+            keys4(j, k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if ((k[e] >> drop) == T && j + e < j1)
+                    atomicAdd(&s_hist[(pass + 1) & 1][(k[e] >> low) & ((1 << (drop - low)) - 1)], 1);
+        }
+        drop = low;
     }
     // keys are compared by their digits so far; `want` of those equal to T
     // stay, lowest index first
-    const int drop = 24 - 8 * pass;
 
     // count this warp's stretch [w0, w1)
-    const int per = ((seg / 32 + kWarps - 1) / kWarps) * 32;
+    const int per = (seg / kChunk + kWarps - 1) / kWarps * kChunk;
     const int w0 = min(j1, j0 + warp * per), w1 = min(j1, w0 + per);
     Counts mine = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int j = w0 + lane; j < w1; j += 32) {
-        const uint32_t k = key(j) >> drop;
-        const int gt = k > T, eq = k == T, front = j < b;
-        mine.gt_front += gt & front;
-        mine.gt_back += gt & (front ^ 1);
-        mine.eq_front += eq & front;
-        mine.eq_back += eq & (front ^ 1);
+    for (int j = w0 + 4 * lane; j < w1; j += kChunk) {
+        uint32_t k[4];
+        keys4(j, k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool in = j + e < w1, front = j + e < b;
+            const int gt = in && (k[e] >> drop) > T, eq = in && (k[e] >> drop) == T;
+            mine.gt_front += front ? gt : 0;
+            mine.gt_back += front ? 0 : gt;
+            mine.eq_front += front ? eq : 0;
+            mine.eq_back += front ? 0 : eq;
+        }
     }
     mine.gt_front = __reduce_add_sync(kFull, mine.gt_front);
     mine.gt_back = __reduce_add_sync(kFull, mine.gt_back);
@@ -288,28 +357,63 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(Params p) {
     int32_t* hole_list = p.holes + (int64_t)row * b;
     int32_t* mover_list = p.movers + (int64_t)row * b;
     int seen = ties0;
-    for (int base = w0; base < w1; base += 32) {
-        const int j = base + lane;
-        const bool in = j < w1;
-        const uint32_t k = in ? key(j) >> drop : 0u;
-        const unsigned below = (1u << lane) - 1u;
-        const unsigned eq = __ballot_sync(kFull, in && k == T);
-        const bool kp = in && (k > T || (k == T && seen + __popc(eq & below) < want));
-        seen += __popc(eq);
-        const bool is_hole = in && !kp && j < b, is_mover = kp && j >= b;
-        const unsigned hm = __ballot_sync(kFull, is_hole), mm = __ballot_sync(kFull, is_mover);
-        if (is_hole) hole_list[hole0 + __popc(hm & below)] = j;
-        if (is_mover) mover_list[mover0 + __popc(mm & below)] = j;
-        hole0 += __popc(hm);
-        mover0 += __popc(mm);
-        if (kp && j < b) {  // stays in its place
-            const int q = stored[j];
-            if (moved_out) score_out[j] = score[j];
-            if (moved_pos || q < 0) pos_out[j] = q >= 0 ? q : N - n + j;
-        } else if (in && j >= b && !kp) {  // evicted, past the new length
-            score_out[j] = 0.f;
-            pos_out[j] = -1;
+    for (int base = w0; base < w1; base += kChunk) {
+        const int j = base + 4 * lane;
+        uint32_t k[4] = {0u, 0u, 0u, 0u};
+        if (j < w1) keys4(j, k);
+        bool kp[4], eq[4];
+        int ties = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool in = j + e < w1;
+            kp[e] = in && (k[e] >> drop) > T;
+            eq[e] = in && (k[e] >> drop) == T;
+            ties += eq[e];
         }
+        if (__any_sync(kFull, ties != 0)) {  // ranks of the ties, in order
+            int incl = ties;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, incl, o);
+                if (lane >= o) incl += y;
+            }
+            int r = seen + incl - ties;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                kp[e] |= eq[e] && r < want;
+                r += eq[e];
+            }
+            seen += __shfl_sync(kFull, incl, 31);
+        }
+        int found = 0;  // holes, and movers in the upper half
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (j + e < w1) found += j + e < b ? (kp[e] ? 0 : 1) : (kp[e] ? 0x10000 : 0);
+        if (!moved_out || !moved_pos) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (j + e < w1 && j + e >= b && !kp[e]) {  // evicted: nobody reads these any more
+                    if (!moved_out) score_out[j + e] = 0.f;
+                    if (!moved_pos) pos_out[j + e] = -1;
+                }
+        }
+        if (!__any_sync(kFull, found != 0)) continue;
+        int incl = found;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += y;
+        }
+        const int total = __shfl_sync(kFull, incl, 31);
+        int ho = hole0 + ((incl - found) & 0xffff), mo = mover0 + ((incl - found) >> 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (j + e >= w1) continue;
+            if (j + e < b && !kp[e]) hole_list[ho++] = j + e;
+            if (j + e >= b && kp[e]) mover_list[mo++] = j + e;
+        }
+        hole0 += total & 0xffff;
+        mover0 += total >> 16;
     }
     sync_row();  // the lists are complete (and no CTA's memory is read after this)
 
@@ -317,7 +421,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(Params p) {
     // and moves its score and position, then LPR lanes copy each K or V row.
     constexpr int LPR = D / 8;
     constexpr int PER_STEP = 32 / (2 * LPR);  // movers copied by one warp-wide load
-    constexpr int U = 8;                      // loads in flight per lane
+    constexpr int M = 8;                      // loads in flight per lane
     const int sub = lane / (2 * LPR), part = lane % (2 * LPR);
     uint4* cache = part < LPR ? p.k_cache : p.v_cache;
     const int64_t row_vecs = (int64_t)p.Hkv * LPR;
@@ -342,14 +446,14 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(Params p) {
             }
             score_out[to] = sv;
             pos_out[to] = q >= 0 ? q : N - n + of;
-            score_out[of] = 0.f;
-            pos_out[of] = -1;
+            if (!moved_out) score_out[of] = 0.f;
+            if (!moved_pos) pos_out[of] = -1;
         }
-        for (int m = 0; m < count; m += U * PER_STEP) {
-            uint4 v[U];
-            int to[U];
+        for (int m = 0; m < count; m += M * PER_STEP) {
+            uint4 v[M];
+            int to[M];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < M; ++u) {
                 const int i = m + u * PER_STEP + sub;
                 to[u] = __shfl_sync(kFull, slot_to, i & 31);
                 const int of = __shfl_sync(kFull, slot_of, i & 31);
@@ -357,7 +461,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(Params p) {
                 if (to[u] >= 0) v[u] = cache[of * row_vecs];
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int u = 0; u < M; ++u)
                 if (to[u] >= 0) cache[to[u] * row_vecs] = v[u];
         }
     }
@@ -456,11 +560,16 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
     p.movers = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + list_bytes(S, Hkv, budget));
     p.err = pkv::device_error_word();
 
-    // CTAs per row
+    p.vec = score_stride % 4 == 0 && pkv::aligned16(scores) && pkv::aligned16(positions) &&
+            pkv::aligned16(scores_out) && pkv::aligned16(positions_out);
+    // CTAs per row: until the card has two per SM or a CTA 2048 keys, and for
+    // rows beyond a CTA's shared memory
     const int rows = S * Hkv;
     int cs = 1;
-    while (cs < kMaxCluster && p.max_ctx / cs > kKeysPerCta) cs *= 2;
-    const int seg = ((p.max_ctx + cs - 1) / cs + 31) & ~31;
+    while (cs < kMaxCluster && ((rows * cs < 2 * pkv::sm_count() && p.max_ctx / cs > kFewKeys) ||
+                                p.max_ctx / cs > kSmemKeys))
+        cs *= 2;
+    const int seg = ((p.max_ctx + cs - 1) / cs + kChunk - 1) / kChunk * kChunk;
     p.seg_cap = seg < kSmemKeys ? seg : kSmemKeys;
     void (*fn)(Params) = cs > 1 ? (D == 128 ? evict_kernel<128, true> : evict_kernel<64, true>)
                                 : (D == 128 ? evict_kernel<128, false> : evict_kernel<64, false>);

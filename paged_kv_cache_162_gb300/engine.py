@@ -124,10 +124,12 @@ def _refuse(what: str):
 
 
 def _need(who, tensors, cache):
-    """Every (name, tensor, dtype, shape) contiguous, of that type and shape
-    (None: any), on the caches' device -- or, for q and out, in pinned host
-    memory."""
+    """Refuses unless every (name, tensor, dtype, shape) is contiguous, of
+    that type and shape (None: any), on the caches' device -- or, for q and
+    out, in pinned host memory."""
     dev = cache.device
+    if dev.type != "cuda":
+        _refuse(f"{who}: the caches must be on a CUDA device, not {dev}")
     for name, t, dtype, shape in tensors:
         if t.dtype != dtype or (shape is not None and t.shape != shape) or not t.is_contiguous():
             _refuse(f"{who}: {name} must be contiguous {dtype} of shape "
@@ -137,23 +139,45 @@ def _need(who, tensors, cache):
             _refuse(f"{who}: {name} is on {t.device}, the caches on {dev}")
 
 
-def _on_device(cache, stream, call):
-    """call(stream) with the caches' device current."""
-    dev = cache.device.index
-    if dev == torch.cuda.current_device():
-        return call(stream)
-    with torch.cuda.device(dev):
-        return call(stream)
+_I32 = torch.int32
 
 
-def _attention_shapes(who, q, k_cache, block_tables):
+def _launch(who, fn, dev, stream, *args):
+    """fn(*args, stream handle) with device `dev` current (None: torch's
+    current stream on it)."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(who, fn, dev, stream, *args)
+    st = fn(*args, L.current_stream_handle(dev) if stream is None else L.stream_handle(stream))
+    if st:
+        L.check(st, who)
+
+
+def _attention_args(who, out, q, k_cache, v_cache, block_tables, context_lens):
+    """Checks what the two attention calls share; returns the sizes."""
     if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2:
         _refuse(f"{who}: q must be [S, H, D], the caches [NB, bs, Hkv, D], block_tables [S, MB]")
-    S, H, D = q.shape
-    NB, bs, Hkv, Dk = k_cache.shape
+    shape, cshape = q.shape, k_cache.shape
+    S, H, D = shape
+    NB, bs, Hkv, Dk = cshape
+    MB = block_tables.shape[1]
     if Dk != D:
         _refuse(f"{who}: q has head_dim {D}, the caches {Dk}")
-    return S, H, D, NB, bs, Hkv, block_tables.shape[1]
+    dt, dev = k_cache.dtype, k_cache.get_device()
+    # one expression on the way through; _need says what is wrong
+    if not (dev >= 0 and q.dtype is dt and out.dtype is dt and v_cache.dtype is dt
+            and block_tables.dtype is _I32 and context_lens.dtype is _I32 and out.shape == shape
+            and v_cache.shape == cshape and block_tables.shape[0] == S
+            and context_lens.shape == (S,) and q.is_contiguous() and out.is_contiguous()
+            and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_tables.is_contiguous() and context_lens.is_contiguous()
+            and q.get_device() == dev and out.get_device() == dev and v_cache.get_device() == dev
+            and block_tables.get_device() == dev and context_lens.get_device() == dev):
+        _need(who, (("k_cache", k_cache, dt, None), ("q", q, dt, None), ("out", out, dt, shape),
+                    ("v_cache", v_cache, dt, cshape),
+                    ("block_tables", block_tables, _I32, (S, MB)),
+                    ("context_lens", context_lens, _I32, (S,))), k_cache)
+    return S, H, D, NB, bs, Hkv, MB, dev
 
 
 def _workspace(who, ws, size, device, stream=None):
@@ -201,19 +225,15 @@ def paged_attention_decode_window(out, q, k_cache, v_cache, block_tables, contex
     workspace: new_window_workspace(S, H, Hkv, D), kept between calls.
     """
     who = "paged_attention_decode_window"
-    S, H, D, NB, bs, Hkv, MB = _attention_shapes(who, q, k_cache, block_tables)
-    dt = k_cache.dtype
-    _need(who, (("q", q, dt, None), ("out", out, dt, q.shape), ("k_cache", k_cache, dt, None),
-                ("v_cache", v_cache, dt, k_cache.shape),
-                ("block_tables", block_tables, torch.int32, (S, MB)),
-                ("context_lens", context_lens, torch.int32, (S,))), k_cache)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
+    S, H, D, NB, bs, Hkv, MB, dev = _attention_args(who, out, q, k_cache, v_cache, block_tables,
+                                                    context_lens)
     ws = _workspace(who, workspace, lambda: L.pkv_decode_window_workspace_size(S, H, Hkv, D),
                     k_cache.device, stream)
-    _on_device(k_cache, stream, lambda st: L.pkv_paged_attention_decode_window(
-        out, q, k_cache, v_cache, block_tables, context_lens, S, H, Hkv, D, bs, NB, MB,
-        max_context_len, window, sink_tokens, scale, dtype_code(dt), ws, ws.numel(), st))
+    _launch(who, L.lib().pkv_paged_attention_decode_window, dev, stream, out.data_ptr(),
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+            context_lens.data_ptr(), S, H, Hkv, D, bs, NB, MB, max_context_len, window,
+            sink_tokens, 1.0 / math.sqrt(D) if scale is None else scale, dtype_code(k_cache.dtype),
+            ws.data_ptr(), ws.numel())
     return out
 
 
@@ -227,20 +247,19 @@ def paged_attention_decode_accumulate(out, scores, q, k_cache, v_cache, block_ta
     paged_attention_decode_window; workspace: new_accumulate_workspace(S, H,
     Hkv, D, max_context_len)."""
     who = "paged_attention_decode_accumulate"
-    S, H, D, NB, bs, Hkv, MB = _attention_shapes(who, q, k_cache, block_tables)
-    dt = k_cache.dtype
-    _need(who, (("q", q, dt, None), ("out", out, dt, q.shape), ("k_cache", k_cache, dt, None),
-                ("v_cache", v_cache, dt, k_cache.shape),
-                ("block_tables", block_tables, torch.int32, (S, MB)),
-                ("context_lens", context_lens, torch.int32, (S,)),
-                ("scores", scores, torch.float32, (S, Hkv, scores.shape[-1]))), k_cache)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
+    S, H, D, NB, bs, Hkv, MB, dev = _attention_args(who, out, q, k_cache, v_cache, block_tables,
+                                                    context_lens)
+    if not (scores.dtype is torch.float32 and scores.dim() == 3 and scores.shape[:2] == (S, Hkv)
+            and scores.is_contiguous() and scores.get_device() == dev):
+        _need(who, (("scores", scores, torch.float32, (S, Hkv, scores.shape[-1])),), k_cache)
+    cap = scores.shape[2]
     ws = _workspace(who, workspace, lambda: L.pkv_decode_accumulate_workspace_size(
         S, H, Hkv, D, max_context_len or MB * bs), k_cache.device, stream)
-    _on_device(k_cache, stream, lambda st: L.pkv_paged_attention_decode_accumulate(
-        out, scores, q, k_cache, v_cache, block_tables, context_lens, S, H, Hkv, D, bs, NB, MB,
-        max_context_len, scores.shape[-1], scale, dtype_code(dt), ws, ws.numel(), st))
+    _launch(who, L.lib().pkv_paged_attention_decode_accumulate, dev, stream, out.data_ptr(),
+            scores.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_tables.data_ptr(), context_lens.data_ptr(), S, H, Hkv, D, bs, NB, MB,
+            max_context_len, cap, 1.0 / math.sqrt(D) if scale is None else scale,
+            dtype_code(k_cache.dtype), ws.data_ptr(), ws.numel())
     return out
 
 
@@ -269,22 +288,41 @@ def evict_tokens(k_cache, v_cache, scores, positions, block_tables, context_lens
         scores_out = scores
     if positions_out is None:
         positions_out = positions
-    rows = (S, Hkv, scores.shape[-1])
-    i32, dt = torch.int32, k_cache.dtype
-    _need(who, (("k_cache", k_cache, dt, None), ("v_cache", v_cache, dt, k_cache.shape),
-                ("scores", scores, torch.float32, rows), ("positions", positions, i32, rows),
-                ("scores_out", scores_out, torch.float32, rows),
-                ("positions_out", positions_out, i32, rows),
-                ("block_tables", block_tables, i32, None),
-                ("context_lens", context_lens, i32, (S,)),
-                ("token_counts", token_counts, i32, (S,)),
-                ("new_context_lens", new_context_lens, i32, (S,))), k_cache)
+    f32, dt, dev = torch.float32, k_cache.dtype, k_cache.get_device()
+    rows = scores.shape
+    if not (dev >= 0 and len(rows) == 3 and rows[0] == S and rows[1] == Hkv and v_cache.dtype is dt
+            and scores.dtype is f32 and scores_out.dtype is f32 and positions.dtype is _I32
+            and positions_out.dtype is _I32 and block_tables.dtype is _I32
+            and context_lens.dtype is _I32 and token_counts.dtype is _I32
+            and new_context_lens.dtype is _I32 and v_cache.shape == k_cache.shape
+            and scores_out.shape == rows and positions.shape == rows and positions_out.shape == rows
+            and context_lens.shape == (S,) and token_counts.shape == (S,)
+            and new_context_lens.shape == (S,) and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and scores.is_contiguous() and scores_out.is_contiguous()
+            and positions.is_contiguous() and positions_out.is_contiguous()
+            and block_tables.is_contiguous() and context_lens.is_contiguous()
+            and token_counts.is_contiguous() and new_context_lens.is_contiguous()
+            and v_cache.get_device() == dev and scores.get_device() == dev
+            and scores_out.get_device() == dev and positions.get_device() == dev
+            and positions_out.get_device() == dev and block_tables.get_device() == dev
+            and context_lens.get_device() == dev and token_counts.get_device() == dev
+            and new_context_lens.get_device() == dev):
+        want = (S, Hkv, rows[-1] if len(rows) else 0)
+        _need(who, (("k_cache", k_cache, dt, None), ("v_cache", v_cache, dt, k_cache.shape),
+                    ("scores", scores, f32, want), ("positions", positions, _I32, want),
+                    ("scores_out", scores_out, f32, want),
+                    ("positions_out", positions_out, _I32, want),
+                    ("block_tables", block_tables, _I32, None),
+                    ("context_lens", context_lens, _I32, (S,)),
+                    ("token_counts", token_counts, _I32, (S,)),
+                    ("new_context_lens", new_context_lens, _I32, (S,))), k_cache)
     ws = _workspace(who, workspace, lambda: L.pkv_evict_workspace_size(S, Hkv, budget),
                     k_cache.device, stream)
-    _on_device(k_cache, stream, lambda st: L.pkv_evict_tokens(
-        k_cache, v_cache, scores, positions, block_tables, context_lens, token_counts, scores_out,
-        positions_out, new_context_lens, S, Hkv, D, bs, NB, MB, rows[2], budget, recent_tokens,
-        sink_tokens, dtype_code(dt), ws, ws.numel(), st))
+    _launch(who, L.lib().pkv_evict_tokens, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(),
+            scores.data_ptr(), positions.data_ptr(), block_tables.data_ptr(),
+            context_lens.data_ptr(), token_counts.data_ptr(), scores_out.data_ptr(),
+            positions_out.data_ptr(), new_context_lens.data_ptr(), S, Hkv, D, bs, NB, MB, rows[2],
+            budget, recent_tokens, sink_tokens, dtype_code(dt), ws.data_ptr(), ws.numel())
 
 
 def compute_slot_mapping(slot_mapping, block_tables, seq_idx, pos, block_size, stream=None):
