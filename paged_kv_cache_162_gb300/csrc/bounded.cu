@@ -26,14 +26,19 @@
 // memory.
 //
 // Two ways to spread the units:
-//  * direct: one CTA per unit, one launch, no workspace traffic but z'.
-//  * split: the tiles of all units, in order, are cut into one equal range per
-//    resident CTA.  A unit inside one range is finished there; a unit cut by
-//    range ends leaves (M, L, unnormalised out) per piece, and a second kernel
-//    (one CTA per range, the same ranges) joins the pieces of the units that
-//    begin in its range and folds its tokens' weights into the scores.  Ranges
-//    are computed from the lengths on the device by every CTA, so a call needs
-//    no plan, no counter and no ticket, and every sum has a fixed order.
+//  * direct: one CTA, or one cluster of CTAs that share the unit's tokens, per
+//    unit; the cluster joins its parts through distributed shared memory.  One
+//    launch, no workspace traffic but z'.  For few or short units.
+//  * split: the tiles of all units, in order, are cut into ranges: one large
+//    range per resident CTA, then small ones that whichever CTA is done first
+//    takes (cluster launch control: a running CTA cancels the launch of a
+//    waiting one and does its work, keeping its plan and its full ring).  A
+//    unit inside one range is finished there; a unit cut by range ends leaves
+//    (M, L, unnormalised out) per piece, and a second kernel joins the pieces
+//    and folds all weights into the scores.  Ranges are computed from the
+//    lengths on the device by every CTA: a call needs no plan kernel, no counter
+//    and no ticket, and as the cuts do not depend on who does which range,
+//    every sum has a fixed order.
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -44,6 +49,7 @@
 #include "pagedkv.h"
 #include "pkv_device.cuh"
 #include "pkv_mma.cuh"
+#include "tc_wait.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -59,7 +65,8 @@ using pkv::Mma;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;
-constexpr int kMaxRanges = 512;    // CTAs of a split call
+constexpr int kMaxRanges = 1536;   // CTAs of a split call
+constexpr int kMinRange = 8;       // tiles, more than any ring holds
 constexpr int kMaxGroup = 16;      // query heads per KV head
 constexpr int kMaxCluster = 16;    // CTAs that share a unit in a direct call
 constexpr unsigned kFull = 0xffffffffu;
@@ -74,8 +81,7 @@ constexpr int kRingBytes = kStages<D> * 2 * kTileBytes<D>;  // one warp's ring
 template <int D>
 constexpr int kSmemBytes = kWarps * kRingBytes<D>;
 
-// The unit that begins in a range (one CTA of a split call) and ends in a
-// later one, for the join kernel.
+// The unit that begins in a range and ends in a later one, for the join kernel.
 struct RangeInfo {
     int unit;  // s * HB + hb, -1: none
     int c1;    // the range where it ends
@@ -91,8 +97,8 @@ struct Params {
     int S, H, Hkv, G, NB, MB, bs_log2, max_ctx;
     int window, sinks;   // accumulate: window = max_ctx
     int hw, nsplit, HB;  // KV heads per CTA, warps per KV head, units per sequence
-    int direct;          // one cluster per unit
     int cs;              // direct: CTAs per cluster
+    int ranges0, ranges; // split: large ranges, and all of them
     int fold;            // split: CTAs per unit that fold weights into scores
     float qscale;        // scale * log2(e)
     RangeInfo* info;     // [ranges]
@@ -125,6 +131,161 @@ __device__ __forceinline__ int tiles_of(const Params& p, int n) {
     return t < 1 ? 1 : t;
 }
 
+// How the tiles of a split call are cut: ranges0 large ranges hold
+// kLargeShare / 16 of them, the others the rest, kMinRange tiles or more each
+// (the last one of each kind may hold fewer, or none).
+constexpr int kLargeShare = 14;
+constexpr int kSmallRanges = 2;    // per large one
+
+struct RangeMap {
+    long long total, large, small;
+    int n_large;
+    __device__ __forceinline__ void set(const Params& p, long long total_) {
+        total = total_;
+        n_large = p.ranges0;
+        const long long in_large = p.ranges > n_large ? total * kLargeShare / 16 : total;
+        large = max((long long)kMinRange, (in_large + n_large - 1) / n_large);
+        const long long rest = total - min(total, large * n_large);
+        const int n_small = max(1, p.ranges - n_large);
+        small = max((long long)kMinRange, (rest + n_small - 1) / n_small);
+    }
+    __device__ __forceinline__ long long begin(int c) const {
+        const long long x = c <= n_large ? large * c : large * n_large + small * (c - n_large);
+        return min(x, total);
+    }
+    __device__ __forceinline__ int of(long long tile) const {
+        const long long edge = large * n_large;
+        return tile < edge ? (int)(tile / large) : n_large + (int)((tile - edge) / small);
+    }
+};
+
+// A range's first unit and first tile of it.
+struct Range {
+    long long unit0;     // the unit's first tile, of all
+    int c, s, hb, tb, n; // range, unit (s, hb), its tile, context of s
+    int left;            // tiles in the range, 0: none
+};
+
+// The sequence whose units hold tile `want` * HB, by a whole warp.  before[i]:
+// tiles of the sequences below run i of `per` sequences.
+__device__ __forceinline__ int sequence_of(const Params& p, const long long* before, int per,
+                                           long long want, int lane, long long& first) {
+    int run = 0;
+#pragma unroll
+    for (int k = 0; k < kThreads / 32; ++k)
+        run += __popc(__ballot_sync(kFull, before[32 * k + lane] <= want));
+    run -= 1;  // before[0] = 0 <= want; equal entries are empty runs, the last one wins
+    first = before[run];
+    for (int s = run * per;; s += 32) {
+        const int q = s + lane;
+        const int tl = q < p.S && q < (run + 1) * per ? tiles_of(p, context_of(p, q)) : 0;
+        long long in = tl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(kFull, in, o);
+            if (lane >= o) in += x;
+        }
+        const unsigned past = __ballot_sync(kFull, first + in > want);
+        if (past) {
+            const int at = __ffs(past) - 1;
+            first += __shfl_sync(kFull, in - tl, at);
+            return s + at;
+        }
+        first += __shfl_sync(kFull, in, 31);
+    }
+}
+
+// Shared by the CTAs' warps in a split call.
+struct Plan {
+    long long before[kThreads + 1];   // tiles of the sequences before each thread's run
+    long long warp_sum[kWarps];
+    RangeMap map;
+    Range queue[kWarps][4];           // ranges a warp has begun to copy, not yet to use
+    __align__(16) uint4 taken[2];     // answers of the launch control, in turn
+    __align__(8) unsigned long long full[2], used[2];
+    int abort;
+};
+
+// Range c as a warp finds it (whole warp; every lane returns it).
+__device__ __forceinline__ Range range_at(const Params& p, const long long* before, const RangeMap& map,
+                                          int c, int lane) {
+    Range r;
+    const long long at = map.begin(c);
+    r.c = c;
+    r.left = (int)(map.begin(c + 1) - at);
+    if (r.left == 0) return r;
+    long long first;
+    const int per = (p.S + kThreads - 1) / kThreads;
+    r.s = sequence_of(p, before, per, at / p.HB, lane, first);
+    r.n = context_of(p, r.s);
+    const long long inside = at - first * p.HB;
+    const int T = tiles_of(p, r.n);
+    r.hb = (int)(inside / T);
+    r.tb = (int)(inside % T);
+    r.unit0 = at - r.tb;
+    return r;
+}
+
+__device__ __forceinline__ uint32_t smem_of(const void* x) {
+    return (uint32_t)__cvta_generic_to_shared(x);
+}
+
+// Asks for the range of a CTA that has not been launched: request k of this
+// CTA, by one thread.
+__device__ __noinline__ void ask_range(Plan* plan, int k) {
+    const int b = k & 1;
+    // every warp has read the answer that was here
+    if (k >= 2 && !tc_mbar_wait(smem_of(&plan->used[b]), ((k - 2) >> 1) & 1, &plan->abort)) return;
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], 16;" ::"r"(smem_of(&plan->full[b])) : "memory");
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_of(&plan->taken[b])),
+        "r"(smem_of(&plan->full[b]))
+        : "memory");
+}
+
+// The next range for a warp, into its queue's entry at; false when there is
+// none.  k: answers read so far.
+__device__ __noinline__ bool next_range(const Params& p, Plan* plan, int warp, int lane, int& k, int at) {
+    for (;;) {
+        const int b = k & 1;
+        const bool answered = tc_mbar_wait(smem_of(&plan->full[b]), (k >> 1) & 1, &plan->abort);
+        if (!__all_sync(kFull, answered)) {
+            pkv::report(p.err, PKV_DEVERR_TIMEOUT);
+            *(volatile int*)&plan->abort = 1;
+            return false;
+        }
+        uint32_t got, c;
+        asm volatile(
+            "{.reg .b128 h; .reg .pred ok;\n\t"
+            "ld.shared.b128 h, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 ok, h;\n\t"
+            "selp.u32 %0, 1, 0, ok;\n\t"
+            "mov.u32 %1, 0;\n\t"
+            "@ok clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;}"
+            : "=r"(got), "=r"(c)
+            : "r"(smem_of(&plan->taken[b]))
+            : "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_of(&plan->used[b])) : "memory");
+        ++k;
+        if (!got) return false;
+        const Range r = range_at(p, plan->before, plan->map, (int)c, lane);
+        if (r.left > 0) {
+            if (lane == 0) plan->queue[warp][at & 3] = r;
+            __syncwarp();
+            return true;
+        }
+        if (warp == 0 && lane == 0) {
+            p.info[c].unit = -1;
+            ask_range(plan, k);
+        }
+        __syncwarp();
+    }
+}
+
 // Running softmax of one warp over its tiles: rows lane/4 and lane/4 + 8 of
 // the accumulators, (m, l) per row.
 template <int D>
@@ -135,17 +296,17 @@ struct Acc {
 
 // One warp's tiles on their way through its ring: tile i of one unit after the
 // other, `step` apart, each looked up one tile ahead of its copies and copied
-// kStages - 1 tiles ahead of its use.  chain: goes on into the units that
-// follow in the range, so that a unit's end does not drain the ring.
+// kStages - 1 tiles ahead of its use.  With a plan and step 1 it goes on into
+// the units and ranges that follow, so that no end of one drains the ring.
 template <int D>
 struct Feed {
     static constexpr int NST = kStages<D>;
     const Params& p;
+    Plan* const plan;         // null: one unit (part) at a time
     const uint32_t ring;
-    const int lane, hl;       // head of the CTA's hw that this warp takes
+    const int warp, lane, hl; // hl: head of the CTA's hw that this warp takes
     const int step;
-    const bool chain;
-    int s, hb, n_next, i, te, left;  // the next tile to copy, and its unit
+    int s, hb, n_next, i, te, left;  // the next tile to copy, and its unit; left: from its tile 0 to the range's end
     int nv, shift;
     const int32_t* bt;
     const uint16_t* k_head;
@@ -153,10 +314,12 @@ struct Feed {
     bool more;
     unsigned mask[NST];       // rows with a token, of the tiles in the ring
     int stage;                // of the oldest tile
+    int asked, answers, pushed;  // requests made (warp 0), answers read, ranges queued
 
-    __device__ __forceinline__ Feed(const Params& p_, uint32_t ring_, int lane_, int hl_, int step_,
-                                    bool chain_)
-        : p(p_), ring(ring_), lane(lane_), hl(hl_), step(step_), chain(chain_) {}
+    __device__ __forceinline__ Feed(const Params& p_, Plan* plan_, uint32_t ring_, int warp_, int lane_,
+                                    int hl_, int step_)
+        : p(p_), plan(plan_), ring(ring_), warp(warp_), lane(lane_), hl(hl_), step(step_), asked(0),
+          answers(0), pushed(0) {}
 
     __device__ __forceinline__ void enter(int n) {  // unit (s, hb)
         nv = visible_of(p, n);
@@ -186,21 +349,41 @@ struct Feed {
         slot = (phys << p.bs_log2) | (tok & ((1 << p.bs_log2) - 1));
     }
 
-    // Tiles first, first + step, ... below te_ of unit (s_, hb_); left_: tiles
-    // up to the range's end, counted from the unit's first one.
+    // Fills the ring from tile `first` of unit (s_, hb_) on, tiles below te_;
+    // left_: tiles from the unit's first one to the range's end.
     __device__ __forceinline__ void begin(int s_, int hb_, int n, int first, int te_, int left_) {
         s = s_;
         hb = hb_;
         i = first;
         te = te_;
         left = left_;
-        n_next = chain && s + 1 < p.S ? context_of(p, s + 1) : 0;
+        n_next = chained() && s + 1 < p.S ? context_of(p, s + 1) : 0;
         more = i < te;
         enter(n);
         lookup();
         stage = 0;
 #pragma unroll
         for (int st = 0; st < NST - 1; ++st) push(st, st);
+    }
+
+    __device__ __forceinline__ bool chained() const { return plan != nullptr && step == 1; }
+
+    // Warp 0 asks for the next range when few tiles are left of this one (not
+    // earlier: a range asked for is a range no other CTA can take).
+    __device__ __forceinline__ void maybe_ask(int tiles_left) {
+        if (warp == 0 && tiles_left <= 3 && asked == answers) {
+            if (lane == 0) ask_range(plan, asked);
+            ++asked;
+        }
+    }
+    // The next range into the queue (whole warp).
+    __device__ __forceinline__ bool next() {
+        maybe_ask(0);
+        int k = answers;
+        const bool got = next_range(p, plan, warp, lane, k, pushed);
+        asked = answers = k;
+        if (got) ++pushed;
+        return got;
     }
 
     // Copies the next tile into ring stage `st` and its row mask into
@@ -224,27 +407,42 @@ struct Feed {
                 cp_async16_zfill(sv + dst, src + to_v, bytes);
             }
             i += step;
-            if (i >= te) {
-                left -= te;
-                more = chain && left > 0;
-                if (more) {
-                    int n;
-                    if (++hb == p.HB) {
-                        hb = 0;
-                        ++s;
-                        n = n_next;
-                        n_next = s + 1 < p.S ? context_of(p, s + 1) : 0;
-                    } else {
-                        n = context_of(p, s);
-                    }
-                    enter(n);
-                    i = 0;
-                    te = min(tiles_of(p, n), left);
-                }
-            }
+            if (i >= te) advance();
+            if (more && chained()) maybe_ask(left - i);
             lookup();
         }
         cp_async_commit();  // empty past the end: the counting stays simple
+    }
+
+    __device__ __forceinline__ void advance() {
+        more = false;
+        if (!chained()) return;
+        left -= te;
+        int n;
+        if (left > 0) {  // the range's next unit
+            i = 0;
+            if (++hb == p.HB) {
+                hb = 0;
+                ++s;
+                n = n_next;
+                n_next = s + 1 < p.S ? context_of(p, s + 1) : 0;
+            } else {
+                n = context_of(p, s);
+            }
+        } else {         // another range
+            const int at = pushed;
+            if (!next()) return;
+            const Range& r = plan->queue[warp][at & 3];
+            s = r.s;
+            hb = r.hb;
+            i = r.tb;
+            left = r.left + r.tb;
+            n = r.n;
+            n_next = s + 1 < p.S ? context_of(p, s + 1) : 0;
+        }
+        more = true;
+        enter(n);
+        te = min(tiles_of(p, n), left);
     }
 };
 
@@ -571,50 +769,91 @@ __device__ __forceinline__ void join_cluster(const Params& p, int s, int kvh, in
     cluster.sync();  // no CTA leaves while another reads its rows
 }
 
+// Writes the finished rows of a unit (the warp's part of the accumulators).
+template <class E, int D, bool kWide>
+__device__ __forceinline__ void write_rows(const Params& p, int s, int kvh, int lane, const Acc<D>& a) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int r = 0; r < (kWide ? 2 : 1); ++r) {
+        const int row = g + 8 * r;
+        if (row < p.G) {
+            const float inv = a.l[r] > 0.f || a.l[r] != a.l[r] ? 1.f / a.l[r] : 0.f;
+            uint16_t* dst = static_cast<uint16_t*>(p.out) +
+                            ((int64_t)s * p.H + (int64_t)kvh * p.G + row) * D + 2 * t;
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j)
+                *reinterpret_cast<uint32_t*>(dst + 8 * j) =
+                    E::from_float2(a.o[j][2 * r] * inv, a.o[j][2 * r + 1] * inv);
+        }
+    }
+}
+
+// Direct: cluster c / cs takes unit c / cs (hw = 1), its CTAs equal parts of
+// the unit's tiles, their warps every fourth tile.
 template <class E, int D, bool kWide, bool kScores>
-__global__ void __launch_bounds__(kThreads, 2) bounded_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, 2) direct_kernel(const __grid_constant__ Params p) {
     // inputs may come from the kernel before this one; the next may become
     // resident once every CTA is here, and waits for this grid's end
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long s_before[kThreads + 1];  // tiles before each thread's sequences
-    __shared__ long long s_warp[kWarps];
     __shared__ float s_m[kMaxGroup], s_inv[kMaxGroup];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int unit = blockIdx.x / p.cs, rank = blockIdx.x % p.cs;
+    const int s = unit / p.Hkv, kvh = unit % p.Hkv;
+    const int raw = __ldg(p.context_lens + s);
+    if ((raw < 0 || raw > p.max_ctx) && kvh == 0 && rank == 0 && tid == 0)
+        pkv::report(p.err, PKV_DEVERR_CONTEXT);
+    const int n = context_of(p, s);
+    const int T = tiles_of(p, n), per = (T + p.cs - 1) / p.cs;
+    const int tb = min(T, rank * per), te = min(T, tb + per);
+
+    Feed<D> feed(p, nullptr, smem_of(smem) + warp * kRingBytes<D>, warp, lane, 0, kWarps);
+    Acc<D> a;
+    feed.begin(s, kvh, n, tb + warp, te, 0);
+    attend<E, D, kWide, kScores>(p, feed, s, kvh, tb + warp, te, lane, a);
+    cp_async_wait<0>();
+    join_splits<D>(p, reinterpret_cast<float*>(smem), warp, lane, a);
+    if (p.cs > 1) {
+        join_cluster<E, D, kWide, kScores>(p, s, kvh, n, tb, te, reinterpret_cast<float*>(smem), warp,
+                                           lane, a, s_m, s_inv);
+        return;
+    }
+    if (warp == 0) write_rows<E, D, kWide>(p, s, kvh, lane, a);
+    if constexpr (kScores) {  // the z of this unit were written by this CTA
+        if (warp == 0 && (lane & 3) == 0) {
+#pragma unroll
+            for (int r = 0; r < (kWide ? 2 : 1); ++r) {
+                s_m[(lane >> 2) + 8 * r] = a.m[r];
+                s_inv[(lane >> 2) + 8 * r] = a.l[r] > 0.f || a.l[r] != a.l[r] ? 1.f / a.l[r] : 0.f;
+            }
+        }
+        __syncthreads();
+        fold_weights(p, s, kvh, 0, n, s_m, s_inv, tid, kThreads);
+    }
+}
+
+// Split: range c = blockIdx.x, then whichever ranges this CTA can take.
+template <class E, int D, bool kWide, bool kScores>
+__global__ void __launch_bounds__(kThreads, 2) split_kernel(const __grid_constant__ Params p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ Plan plan;
     constexpr int NO = D / 8;
     constexpr int R = kWide ? 2 : 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     const int hl = warp % p.hw, split = warp / p.hw;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kRingBytes<D>;
-    const int c = blockIdx.x;
 
-    int s, hb, tb, n;
-    long long left = 0;           // tiles left in this range
-    long long unit0 = 0;          // first tile of the current unit
-    long long range = 1;
-    int end = 0;                  // direct: tiles [tb, end) are this CTA's
-    const int crank = p.direct ? c % p.cs : 0;
-    if (p.direct) {
-        const int unit = c / p.cs;
-        s = unit / p.HB;
-        hb = unit % p.HB;
-        const int raw = __ldg(p.context_lens + s);
-        if ((raw < 0 || raw > p.max_ctx) && hb == 0 && crank == 0 && tid == 0)
-            pkv::report(p.err, PKV_DEVERR_CONTEXT);
-        n = context_of(p, s);
-        const int T = tiles_of(p, n), per = (T + p.cs - 1) / p.cs;
-        tb = min(T, crank * per);
-        end = min(T, tb + per);
-    } else {
-        // tiles before each thread's run of sequences
+    {  // tiles before each thread's run of sequences
         const int per = (p.S + kThreads - 1) / kThreads;
         long long mine = 0;
         for (int i = 0; i < per; ++i) {
             const int q = tid * per + i;
             if (q < p.S) {
                 const int raw = __ldg(p.context_lens + q);
-                if ((raw < 0 || raw > p.max_ctx) && c == 0) pkv::report(p.err, PKV_DEVERR_CONTEXT);
+                if ((raw < 0 || raw > p.max_ctx) && blockIdx.x == 0) pkv::report(p.err, PKV_DEVERR_CONTEXT);
                 mine += tiles_of(p, context_of(p, q));
             }
         }
@@ -624,144 +863,103 @@ __global__ void __launch_bounds__(kThreads, 2) bounded_kernel(Params p) {
             const long long x = __shfl_up_sync(kFull, incl, o);
             if (lane >= o) incl += x;
         }
-        if (lane == 31) s_warp[warp] = incl;
+        if (lane == 31) plan.warp_sum[warp] = incl;
+        if (tid == 0) {
+            plan.abort = 0;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                tc_mbar_init(smem_of(&plan.full[b]), 1);
+                tc_mbar_init(smem_of(&plan.used[b]), kWarps);
+            }
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
         __syncthreads();
         long long base = 0;
-        for (int w = 0; w < warp; ++w) base += s_warp[w];
-        s_before[tid] = base + incl - mine;
-        if (tid == kThreads - 1) s_before[kThreads] = base + incl;
+        for (int w = 0; w < warp; ++w) base += plan.warp_sum[w];
+        plan.before[tid] = base + incl - mine;
+        if (tid == kThreads - 1) {
+            plan.before[kThreads] = base + incl;
+            plan.map.set(p, (base + incl) * p.HB);
+        }
         __syncthreads();
-        const long long total = s_before[kThreads] * p.HB;
-        range = (total + gridDim.x - 1) / gridDim.x;
-        const long long begin = range * c;
-        if (begin >= total) {
-            if (tid == 0) p.info[c].unit = -1;
-            return;
-        }
-        left = min(range, total - begin);
-        // the sequence holding tile `begin`: the thread run, then the sequence
-        const long long want = begin / p.HB;  // in units of one head block's tiles
-        int run = 0;
-#pragma unroll
-        for (int k = 0; k < kThreads / 32; ++k)
-            run += __popc(__ballot_sync(kFull, s_before[32 * k + lane] <= want));
-        run -= 1;  // s_before[0] = 0 <= want; equal entries are empty runs, the last one wins
-        long long before = s_before[run];
-        s = run * per;
-        for (;;) {
-            const int q = s + lane;
-            const int tl = q < p.S && q < (run + 1) * per ? tiles_of(p, context_of(p, q)) : 0;
-            long long in = tl;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long x = __shfl_up_sync(kFull, in, o);
-                if (lane >= o) in += x;
-            }
-            const unsigned past = __ballot_sync(kFull, before + in > want);
-            if (past) {
-                const int at = __ffs(past) - 1;
-                before += __shfl_sync(kFull, in - tl, at);
-                s += at;
-                break;
-            }
-            before += __shfl_sync(kFull, in, 31);
-            s += 32;
-        }
-        n = context_of(p, s);
-        const long long inside = begin - before * p.HB;
-        const int T = tiles_of(p, n);
-        hb = (int)(inside / T);
-        tb = (int)(inside % T);
-        unit0 = begin - tb;
     }
 
-    // with one warp per head the tiles of all units run through the ring
-    // without a break; token splits are joined in the ring's memory, so there
-    // every unit starts anew
-    const bool chain = !p.direct && p.nsplit == 1;
-    Feed<D> feed(p, ring, lane, hl, p.nsplit, chain);
-    for (bool first = true;; first = false) {
-        const int T = tiles_of(p, n);
-        const int te = p.direct ? end : (int)min((long long)T, tb + left);
-        const int kvh = hb * p.hw + hl;
+    Feed<D> feed(p, &plan, smem_of(smem) + warp * kRingBytes<D>, warp, lane, hl, p.nsplit);
+    Range r = range_at(p, plan.before, plan.map, blockIdx.x, lane);
+    bool running = r.left > 0;
+    if (!running) {
+        if (tid == 0) p.info[blockIdx.x].unit = -1;
+    } else if (feed.chained()) {
+        feed.begin(r.s, r.hb, r.n, r.tb, min(tiles_of(p, r.n), r.tb + r.left), r.left + r.tb);
+    }
+    int used = 0;  // ranges taken out of the queue
+    while (running) {
+        // one unit (or the part of it that lies in this range)
+        const int T = tiles_of(p, r.n);
+        const int te = min(T, r.tb + r.left);
+        const int kvh = r.hb * p.hw + hl;
+        const bool last = te - r.tb == r.left;  // of the range
         Acc<D> a;
-        if (!chain || first) feed.begin(s, hb, n, tb + split, te, (int)left + tb);
-        attend<E, D, kWide, kScores>(p, feed, s, kvh, tb + split, te, lane, a);
-        if (!chain) cp_async_wait<0>();
-        if (p.nsplit > 1) join_splits<D>(p, reinterpret_cast<float*>(smem), warp, lane, a);
-        const bool whole = tb == 0 && te == T;
-        if (p.direct && p.cs > 1) {
-            join_cluster<E, D, kWide, kScores>(p, s, hb, n, tb, te, reinterpret_cast<float*>(smem), warp, lane, a, s_m, s_inv);
-            return;
+        if (!feed.chained()) feed.begin(r.s, r.hb, r.n, r.tb + split, te, 0);
+        attend<E, D, kWide, kScores>(p, feed, r.s, kvh, r.tb + split, te, lane, a);
+        if (!feed.chained()) {
+            cp_async_wait<0>();
+            join_splits<D>(p, reinterpret_cast<float*>(smem), warp, lane, a);
         }
+        const bool whole = r.tb == 0 && te == T;
         if (split == 0) {
             if (whole) {
+                write_rows<E, D, kWide>(p, r.s, kvh, lane, a);
+                if constexpr (kScores) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int row = g + 8 * r;
-                    if (row < p.G) {
-                        const int64_t oh = (int64_t)s * p.H + (int64_t)kvh * p.G + row;
-                        const float inv = a.l[r] > 0.f || a.l[r] != a.l[r] ? 1.f / a.l[r] : 0.f;
-                        uint16_t* dst = static_cast<uint16_t*>(p.out) + oh * D + 2 * t;
-#pragma unroll
-                        for (int j = 0; j < NO; ++j)
-                            *reinterpret_cast<uint32_t*>(dst + 8 * j) =
-                                E::from_float2(a.o[j][2 * r] * inv, a.o[j][2 * r + 1] * inv);
-                        if (kScores && t == 0) {
-                            if (p.direct) {
-                                s_m[row] = a.m[r];
-                                s_inv[row] = inv;
-                            } else {
-                                p.row_m[oh] = a.m[r];
-                                p.row_l[oh] = a.l[r];
-                            }
+                    for (int x = 0; x < R; ++x)
+                        if (t == 0 && g + 8 * x < p.G) {
+                            const int64_t oh = (int64_t)r.s * p.H + (int64_t)kvh * p.G + g + 8 * x;
+                            p.row_m[oh] = a.m[x];
+                            p.row_l[oh] = a.l[x];
                         }
-                    }
                 }
             } else {
-                const int64_t piece = 2 * (int64_t)c + (tb == 0 ? 1 : 0);
+                const int64_t piece = 2 * (int64_t)r.c + (r.tb == 0 ? 1 : 0);
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int row = g + 8 * r;
+                for (int x = 0; x < R; ++x) {
+                    const int row = g + 8 * x;
                     if (row < p.G) {
                         const int64_t at = (piece * p.hw + hl) * p.G + row;
                         float* dst = p.part_acc + at * D + 2 * t;
 #pragma unroll
                         for (int j = 0; j < NO; ++j)
                             *reinterpret_cast<float2*>(dst + 8 * j) =
-                                make_float2(a.o[j][2 * r], a.o[j][2 * r + 1]);
+                                make_float2(a.o[j][2 * x], a.o[j][2 * x + 1]);
                         if (t == 0) {
-                            p.part_m[at] = a.m[r];
-                            p.part_l[at] = a.l[r];
+                            p.part_m[at] = a.m[x];
+                            p.part_l[at] = a.l[x];
                         }
                     }
                 }
             }
-        }
-        if (p.direct) {
-            if (kScores) {  // the z of this unit were written by this CTA
-                __syncthreads();
-                fold_weights(p, s, hb, 0, n, s_m, s_inv, tid, kThreads);
+            if (warp == 0 && lane == 0) {
+                const int c1 = plan.map.of(r.unit0 + T - 1);
+                if (kScores && r.tb == 0) p.place[r.s * p.HB + r.hb] = make_int2(r.c, c1);
+                if (last) p.info[r.c] = {r.tb == 0 && te < T ? r.s * p.HB + r.hb : -1, c1};
             }
-            return;
         }
-        if (kScores && tb == 0 && tid == 0)
-            p.place[s * p.HB + hb] = make_int2(c, (int)((unit0 + T - 1) / range));
-        left -= te - tb;
-        if (left == 0) {
-            if (tid == 0) {
-                p.info[c].unit = tb == 0 && te < T ? s * p.HB + hb : -1;
-                p.info[c].c1 = (int)((unit0 + T - 1) / range);
+        if (last) {  // the feed has gone on to the next range, if there is one
+            running = used < feed.pushed;
+            if (running) r = plan.queue[warp][used++ & 3];
+            __syncwarp();
+        } else {
+            r.left -= te - r.tb;
+            r.unit0 += T;
+            r.tb = 0;
+            if (++r.hb == p.HB) {
+                r.hb = 0;
+                r.n = context_of(p, ++r.s);
             }
-            return;
-        }
-        unit0 += T;
-        tb = 0;
-        if (++hb == p.HB) {
-            hb = 0;
-            n = context_of(p, ++s);
         }
     }
+    // every request has been answered: a warp stops at the answer that says no
+    cp_async_wait<0>();
 }
 
 // Row `row` of head hl in the piece that range c has of a unit beginning in c0.
@@ -796,25 +994,24 @@ __device__ __forceinline__ void join_row(const Params& p, int c0, int c1, int hl
     }
 }
 
-// After bounded_kernel.  The first ranges * join CTAs join, per range, the
-// pieces of the unit that begins in it and ends in a later one: a warp per
-// row, or all the CTA's warps on one row (`wpr` of them) where a unit has many
-// pieces.  With scores, `fold` CTAs per unit follow; each takes every fold-th
-// stretch of the unit's tokens, 4 tokens of a head per thread, and folds their
-// weights into the scores.  A stretch is one round of loads: the chain is
-// length and place of the unit -> M, L, z and scores -> store.
+// After split_kernel.  The first ranges * join CTAs join, per range, the pieces
+// of the unit that begins in it and ends in a later one: a warp per row, or all
+// the CTA's warps on one row (`wpr` of them) where a unit has many pieces.  With
+// scores, `fold` CTAs per unit follow; each takes every fold-th stretch of the
+// unit's tokens, 4 tokens of a head per thread, and folds their weights into the
+// scores.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
 template <class E, int D, bool kScores>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(Params p, int ranges, int join, int wpr) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p, int join, int wpr) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     __shared__ float s_m[4 * kMaxGroup], s_inv[4 * kMaxGroup];
     __shared__ __align__(16) float s_o[kJoinWarps][D];
     constexpr int DPL = D / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rows = p.hw * p.G;
+    const int rows = p.hw * p.G, ranges = p.ranges;
     if ((int)blockIdx.x < ranges * join) {
         const int c = blockIdx.x / join;
         const int i = (blockIdx.x % join) * (kJoinWarps / wpr) + warp / wpr;
@@ -923,9 +1120,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(Params p, int ranges
 // ---------------------------------------------------------------------------
 // Visible tokens of a direct call per CTA, and its CTAs in multiples of the
 // resident ones.
-constexpr int kDirectTokens = 512;
+constexpr int kDirectTokens = 1024;
 constexpr int kDirectWaves = 2;
-constexpr int kFoldCtas = 4096;     // of a split call
+constexpr int kFoldCtas = 4096;     // of a split call's join kernel
+constexpr int kCtasPerSm = 2;       // of the attention kernels
 constexpr int kMinUnits = 16;       // of a split call, else fewer KV heads per unit
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -960,12 +1158,22 @@ Layout layout_of(int S, int H, int Hkv, int D, bool scores, int max_ctx) {
 }
 
 using KernelFn = void (*)(Params);
-using JoinFn = void (*)(Params, int, int, int);
+using JoinFn = void (*)(Params, int, int);
 
-template <class E, bool kScores>
+template <class E, bool kScores, bool kDirect>
 KernelFn pick_attend(int D, bool wide) {
-    if (D == 128) return wide ? bounded_kernel<E, 128, true, kScores> : bounded_kernel<E, 128, false, kScores>;
-    return wide ? bounded_kernel<E, 64, true, kScores> : bounded_kernel<E, 64, false, kScores>;
+    if constexpr (kDirect) {
+        if (D == 128) return wide ? direct_kernel<E, 128, true, kScores> : direct_kernel<E, 128, false, kScores>;
+        return wide ? direct_kernel<E, 64, true, kScores> : direct_kernel<E, 64, false, kScores>;
+    } else {
+        if (D == 128) return wide ? split_kernel<E, 128, true, kScores> : split_kernel<E, 128, false, kScores>;
+        return wide ? split_kernel<E, 64, true, kScores> : split_kernel<E, 64, false, kScores>;
+    }
+}
+template <bool kScores, bool kDirect>
+KernelFn pick_attend(pkv_dtype dtype, int D, bool wide) {
+    return dtype == PKV_F16 ? pick_attend<pkv::F16, kScores, kDirect>(D, wide)
+                            : pick_attend<pkv::BF16, kScores, kDirect>(D, wide);
 }
 
 template <bool kScores>
@@ -1072,32 +1280,36 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     p.err = pkv::device_error_word();
     const int64_t most = (int64_t)window + sinks < max_ctx ? (int64_t)window + sinks : max_ctx;
     const bool wide = p.G > 8;
-    KernelFn fn = dtype == PKV_F16
-                      ? (with_scores ? pick_attend<pkv::F16, true>(D, wide) : pick_attend<pkv::F16, false>(D, wide))
-                      : (with_scores ? pick_attend<pkv::BF16, true>(D, wide) : pick_attend<pkv::BF16, false>(D, wide));
     const int smem = D == 128 ? kSmemBytes<128> : kSmemBytes<64>;
-    const int per_sm = resident_of(fn, smem);
-    if (per_sm < 1) return bad(PKV_ERR_CUDA, "the kernel cannot be resident");
-    const int resident = per_sm * pkv::sm_count();
+    KernelFn direct_fn = with_scores ? pick_attend<true, true>(dtype, D, wide) : pick_attend<false, true>(dtype, D, wide);
+    KernelFn split_fn = with_scores ? pick_attend<true, false>(dtype, D, wide) : pick_attend<false, false>(dtype, D, wide);
+    const int sms = pkv::sm_count();
     // direct: the smallest cluster that leaves kDirectTokens per CTA; more CTAs
     // while they still fit the card at once and have a tile per warp
+    const int64_t slots = (int64_t)kCtasPerSm * sms;
     p.cs = 1;
     while (p.cs < kMaxCluster && most > (int64_t)kDirectTokens * p.cs) p.cs *= 2;
-    p.direct = most <= (int64_t)kDirectTokens * p.cs &&
-               (int64_t)S * Hkv * p.cs <= (int64_t)kDirectWaves * resident;
-    if (p.direct)
-        while (p.cs < kMaxCluster && (int64_t)S * Hkv * p.cs * 2 <= resident &&
+    const bool direct = most <= (int64_t)kDirectTokens * p.cs &&
+                        (int64_t)S * Hkv * p.cs <= kDirectWaves * slots;
+    if (direct)
+        while (p.cs < kMaxCluster && (int64_t)S * Hkv * p.cs * 2 <= slots &&
                most > (int64_t)2 * kWarps * kTile * p.cs)
             p.cs *= 2;
-    p.hw = p.direct ? 1 : heads_per_cta(Hkv);
-    while (!p.direct && p.hw > 1 && (int64_t)S * Hkv / p.hw < kMinUnits) p.hw /= 2;
+    p.hw = direct ? 1 : heads_per_cta(Hkv);
+    while (!direct && p.hw > 1 && (int64_t)S * Hkv / p.hw < kMinUnits) p.hw /= 2;
     p.nsplit = kWarps / p.hw;
     p.HB = Hkv / p.hw;
-    // as many CTAs per unit as its longest context has stretches, while the
-    // grid stays within a few times the card
-    const int units = S * p.HB, stretch = 4 * kJoinThreads / p.hw;
+    const int per_sm = resident_of(direct ? direct_fn : split_fn, smem);
+    if (per_sm < 1) return bad(PKV_ERR_CUDA, "the kernel cannot be resident");
+    p.ranges0 = per_sm * sms;
+    if (p.ranges0 > kMaxRanges / (1 + kSmallRanges)) p.ranges0 = kMaxRanges / (1 + kSmallRanges);
+    // small ranges only where changing over costs nothing (a warp per head)
+    p.ranges = p.nsplit == 1 ? p.ranges0 * (1 + kSmallRanges) : p.ranges0;
+    // as many fold CTAs per unit as its longest context has stretches, while
+    // the grid stays within a few times the card
+    const int64_t units = (int64_t)S * p.HB, stretch = 4 * kJoinThreads / p.hw;
     p.fold = (int)((max_ctx + stretch - 1) / stretch);
-    const int most_fold = kFoldCtas / units > 1 ? kFoldCtas / units : 1;
+    const int most_fold = kFoldCtas / units > 1 ? (int)(kFoldCtas / units) : 1;
     if (p.fold > most_fold) p.fold = most_fold;
     if (p.fold < 1) p.fold = 1;
 
@@ -1113,19 +1325,19 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     cfg.dynamicSmemBytes = smem;
     cfg.stream = pkv::as_stream(stream);
     cfg.attrs = attr;
-    cfg.numAttrs = p.direct && p.cs > 1 ? 2 : 1;
-    const int ranges = resident < kMaxRanges ? resident : kMaxRanges;
-    cfg.gridDim = dim3(p.direct ? (unsigned)(S * p.HB * p.cs) : (unsigned)ranges);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p);
-    if (e == cudaSuccess && !p.direct) {
+    cfg.numAttrs = direct && p.cs > 1 ? 2 : 1;
+    cfg.gridDim = dim3(direct ? (unsigned)(S * Hkv * p.cs) : (unsigned)p.ranges);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, direct ? direct_fn : split_fn, p);
+    if (e == cudaSuccess && !direct) {
         // a unit of more than 16 pieces: a CTA per row
-        const int wpr = ranges > 16 * units ? kJoinWarps : 1;
+        const int wpr = p.ranges0 > 16 * units ? kJoinWarps : 1;
         const int join = (p.hw * p.G * wpr + kJoinWarps - 1) / kJoinWarps;
         cfg.dynamicSmemBytes = 0;
+        cfg.numAttrs = 1;
         cfg.blockDim = dim3(kJoinThreads);
-        cfg.gridDim = dim3((unsigned)(ranges * join + (with_scores ? units * p.fold : 0)));
+        cfg.gridDim = dim3((unsigned)(p.ranges * join + (with_scores ? units * p.fold : 0)));
         e = cudaLaunchKernelEx(&cfg, with_scores ? pick_join<true>(dtype, D) : pick_join<false>(dtype, D), p,
-                               ranges, join, wpr);
+                               join, wpr);
     }
     if (e != cudaSuccess) {
         snprintf(msg, sizeof msg, "%s launch", who);
