@@ -336,9 +336,11 @@ size_t pkv_evict_workspace_size(int S, int Hkv, int budget);
  *                 0 and -1
  *   scores_out, positions_out  the same shapes; each may be its input (in
  *                 place) or an array that does not overlap it
- *   context_lens, token_counts  [S] int32: tokens cached (at most MB*bs and
- *                 score_stride) and tokens seen (>= context_lens[s]); others
+ *   context_lens, token_counts  [S] int32: tokens cached (at most
+ *                 max_context_len) and tokens seen (>= context_lens[s]); others
  *                 are clamped and set PKV_DEVERR_CONTEXT
+ *   max_context_len  upper bound of context_lens (0 = MB*bs); at most
+ *                 score_stride
  *   new_context_lens  [S] int32, written; not context_lens itself
  *   budget        >= 1, >= sink_tokens + recent_tokens
  *   workspace     256-byte aligned, pkv_evict_workspace_size bytes; one call
@@ -349,8 +351,9 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
                             const int32_t* positions, const int32_t* block_tables,
                             const int32_t* context_lens, const int32_t* token_counts,
                             float* scores_out, int32_t* positions_out, int32_t* new_context_lens,
-                            int S, int Hkv, int D, int bs, int NB, int MB, int64_t score_stride,
-                            int budget, int recent_tokens, int sink_tokens, pkv_dtype dtype,
+                            int S, int Hkv, int D, int bs, int NB, int MB, int max_context_len,
+                            int64_t score_stride, int budget, int recent_tokens, int sink_tokens,
+                            pkv_dtype dtype,
                             void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------ *

@@ -77,8 +77,8 @@ SIGNATURES = {
     "pkv_paged_attention_decode_accumulate": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
                                                    _I, _I, _I, _I64, _F, _I, _P, _SZ, _P]),
     "pkv_evict_workspace_size": (_SZ, [_I, _I, _I]),
-    "pkv_evict_tokens": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I64,
-                              _I, _I, _I, _I, _P, _SZ, _P]),
+    "pkv_evict_tokens": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
+                              _I64, _I, _I, _I, _I, _P, _SZ, _P]),
     "pkv_compute_slot_mapping": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P]),
     "pkv_reshape_and_cache": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "pkv_copy_blocks": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
@@ -273,13 +273,13 @@ def pkv_evict_workspace_size(S, Hkv, budget) -> int:
 
 def pkv_evict_tokens(k_cache, v_cache, scores, positions, block_tables, context_lens, token_counts,
                      scores_out, positions_out, new_context_lens, S, Hkv, D, bs, NB, MB,
-                     score_stride, budget, recent_tokens, sink_tokens, dtype, workspace,
+                     max_context_len, score_stride, budget, recent_tokens, sink_tokens, dtype, workspace,
                      workspace_bytes, stream=None) -> None:
     st = lib().pkv_evict_tokens(
         ptr(k_cache), ptr(v_cache), ptr(scores), ptr(positions), ptr(block_tables),
         ptr(context_lens), ptr(token_counts), ptr(scores_out), ptr(positions_out),
-        ptr(new_context_lens), S, Hkv, D, bs, NB, MB, score_stride, budget, recent_tokens,
-        sink_tokens, dtype, ptr(workspace), workspace_bytes, stream_handle(stream))
+        ptr(new_context_lens), S, Hkv, D, bs, NB, MB, max_context_len, score_stride, budget,
+        recent_tokens, sink_tokens, dtype, ptr(workspace), workspace_bytes, stream_handle(stream))
     if st:
         check(st, "evict_tokens")
 

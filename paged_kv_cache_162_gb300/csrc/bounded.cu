@@ -81,12 +81,6 @@ constexpr int kRingBytes = kStages<D> * 2 * kTileBytes<D>;  // one warp's ring
 template <int D>
 constexpr int kSmemBytes = kWarps * kRingBytes<D>;
 
-// The unit that begins in a range and ends in a later one, for the join kernel.
-struct RangeInfo {
-    int unit;  // s * HB + hb, -1: none
-    int c1;    // the range where it ends
-};
-
 struct Params {
     void* out;
     const void* q;
@@ -99,10 +93,8 @@ struct Params {
     int hw, nsplit, HB;  // KV heads per CTA, warps per KV head, units per sequence
     int cs;              // direct: CTAs per cluster
     int ranges0, ranges; // split: large ranges, and all of them
-    int fold;            // split: CTAs per unit that fold weights into scores
     float qscale;        // scale * log2(e)
-    RangeInfo* info;     // [ranges]
-    int2* place;         // [S * HB]: first and last range of each unit, accumulate only
+    int2* place;         // [S * HB]: first and last range of each unit
     float* part_m;       // [2 * ranges][hw * G]
     float* part_l;
     float* part_acc;     // [2 * ranges][hw * G][D]
@@ -131,31 +123,40 @@ __device__ __forceinline__ int tiles_of(const Params& p, int n) {
     return t < 1 ? 1 : t;
 }
 
-// How the tiles of a split call are cut: ranges0 large ranges hold
-// kLargeShare / 16 of them, the others the rest, kMinRange tiles or more each
-// (the last one of each kind may hold fewer, or none).
+// How the tiles of a split call are cut: slots of one large range and `n_small`
+// small ones after it, so that a unit has about as many pieces wherever it
+// lies; kLargeShare / 16 of the tiles are in large ranges.  Ranges are numbered
+// by place; CTAs are launched for the large ones first.
 constexpr int kLargeShare = 14;
 constexpr int kSmallRanges = 2;    // per large one
 
 struct RangeMap {
-    long long total, large, small;
-    int n_large;
+    long long total, large, small, slot;
+    int n_large, n_small;
     __device__ __forceinline__ void set(const Params& p, long long total_) {
         total = total_;
         n_large = p.ranges0;
-        const long long in_large = p.ranges > n_large ? total * kLargeShare / 16 : total;
+        n_small = p.ranges / p.ranges0 - 1;
+        const long long in_large = n_small > 0 ? total * kLargeShare / 16 : total;
         large = max((long long)kMinRange, (in_large + n_large - 1) / n_large);
-        const long long rest = total - min(total, large * n_large);
-        const int n_small = max(1, p.ranges - n_large);
-        small = max((long long)kMinRange, (rest + n_small - 1) / n_small);
+        const long long per = (total + n_large - 1) / n_large;
+        small = n_small > 0 ? max((long long)kMinRange, (per - large + n_small - 1) / n_small) : 0;
+        slot = large + n_small * small;
+    }
+    // the range of the id-th CTA launched
+    __device__ __forceinline__ int of_cta(int id) const {
+        if (id < n_large) return id * (1 + n_small);
+        return (id - n_large) / n_small * (1 + n_small) + 1 + (id - n_large) % n_small;
     }
     __device__ __forceinline__ long long begin(int c) const {
-        const long long x = c <= n_large ? large * c : large * n_large + small * (c - n_large);
+        const int k = c % (1 + n_small);
+        const long long x = c / (1 + n_small) * slot + (k ? large + (k - 1) * small : 0);
         return min(x, total);
     }
     __device__ __forceinline__ int of(long long tile) const {
-        const long long edge = large * n_large;
-        return tile < edge ? (int)(tile / large) : n_large + (int)((tile - edge) / small);
+        const int s = (int)(tile / slot);
+        const long long in = tile % slot;
+        return s * (1 + n_small) + (in < large ? 0 : 1 + (int)((in - large) / small));
     }
 };
 
@@ -272,16 +273,13 @@ __device__ __noinline__ bool next_range(const Params& p, Plan* plan, int warp, i
         if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_of(&plan->used[b])) : "memory");
         ++k;
         if (!got) return false;
-        const Range r = range_at(p, plan->before, plan->map, (int)c, lane);
+        const Range r = range_at(p, plan->before, plan->map, plan->map.of_cta((int)c), lane);
         if (r.left > 0) {
             if (lane == 0) plan->queue[warp][at & 3] = r;
             __syncwarp();
             return true;
         }
-        if (warp == 0 && lane == 0) {
-            p.info[c].unit = -1;
-            ask_range(plan, k);
-        }
+        if (warp == 0 && lane == 0) ask_range(plan, k);
         __syncwarp();
     }
 }
@@ -394,6 +392,9 @@ struct Feed {
         if (more) {
             const uint32_t sk = ring + st * 2 * kTileBytes<D>, sv = sk + kTileBytes<D>;
             const int64_t row_elems = (int64_t)p.Hkv * D;
+            // a split call streams more than it could find again in L2; z and the
+            // pieces stay there
+            const uint64_t keep_out = plan ? pkv::policy_evict_first() : pkv::policy_evict_normal();
             const int64_t to_v = static_cast<const uint16_t*>(p.v_cache) - static_cast<const uint16_t*>(p.k_cache);
 #pragma unroll
             for (int j = 0; j < CPL; ++j) {
@@ -403,8 +404,8 @@ struct Feed {
                 const uint16_t* src = k_head + (int64_t)(sl < 0 ? 0 : sl) * row_elems + c * 8;
                 const uint32_t dst = row * ROWB + ((c ^ (row & 7)) * 16);
                 const int bytes = sl < 0 ? 0 : 16;
-                cp_async16_zfill(sk + dst, src, bytes);
-                cp_async16_zfill(sv + dst, src + to_v, bytes);
+                cp_async16_zfill(sk + dst, src, bytes, keep_out);
+                cp_async16_zfill(sv + dst, src + to_v, bytes, keep_out);
             }
             i += step;
             if (i >= te) advance();
@@ -885,13 +886,10 @@ __global__ void __launch_bounds__(kThreads, 2) split_kernel(const __grid_constan
     }
 
     Feed<D> feed(p, &plan, smem_of(smem) + warp * kRingBytes<D>, warp, lane, hl, p.nsplit);
-    Range r = range_at(p, plan.before, plan.map, blockIdx.x, lane);
-    bool running = r.left > 0;
-    if (!running) {
-        if (tid == 0) p.info[blockIdx.x].unit = -1;
-    } else if (feed.chained()) {
+    Range r = range_at(p, plan.before, plan.map, plan.map.of_cta(blockIdx.x), lane);
+    bool running = r.left > 0;  // the same for all warps of the CTA
+    if (running && feed.chained())
         feed.begin(r.s, r.hb, r.n, r.tb, min(tiles_of(p, r.n), r.tb + r.left), r.left + r.tb);
-    }
     int used = 0;  // ranges taken out of the queue
     while (running) {
         // one unit (or the part of it that lies in this range)
@@ -938,11 +936,8 @@ __global__ void __launch_bounds__(kThreads, 2) split_kernel(const __grid_constan
                     }
                 }
             }
-            if (warp == 0 && lane == 0) {
-                const int c1 = plan.map.of(r.unit0 + T - 1);
-                if (kScores && r.tb == 0) p.place[r.s * p.HB + r.hb] = make_int2(r.c, c1);
-                if (last) p.info[r.c] = {r.tb == 0 && te < T ? r.s * p.HB + r.hb : -1, c1};
-            }
+            if (warp == 0 && lane == 0 && r.tb == 0)
+                p.place[r.s * p.HB + r.hb] = make_int2(r.c, plan.map.of(r.unit0 + T - 1));
         }
         if (last) {  // the feed has gone on to the next range, if there is one
             running = used < feed.pushed;
@@ -967,151 +962,264 @@ __device__ __forceinline__ int64_t piece_row(const Params& p, int c, int c0, int
     return ((2 * (int64_t)c + (c == c0 ? 1 : 0)) * p.hw + hl) * p.G + row;
 }
 
-// M and L of one row over the pieces of a cut unit, ranges c0 .. c1: by one
-// thread (kWarp false), or by a warp whose lanes share the pieces.
-template <bool kWarp>
+// (M, L) of two parts of a row as one.
+__device__ __forceinline__ void merge_ml(float& M, float& L, float m, float l) {
+    const float m_new = fmaxf(M, m);
+    const float use = m_new == -INFINITY ? 0.f : m_new;
+    L = L * exp2f(M - use) + l * exp2f(m - use);
+    M = m_new;
+}
+
+// M and L of one row over the pieces of a cut unit, ranges c0 .. c1, by the
+// whole warp.
 __device__ __forceinline__ void join_row(const Params& p, int c0, int c1, int hl, int row, int lane,
                                          float& M, float& L) {
     M = -INFINITY;
     L = 0.f;
-    for (int c = kWarp ? c0 + lane : c0; c <= c1; c += kWarp ? 32 : 1) {
+    for (int c = c0 + lane; c <= c1; c += 32) {
         const int64_t at = piece_row(p, c, c0, hl, row);
-        const float m = p.part_m[at], l = p.part_l[at];
-        const float m_new = fmaxf(M, m);
-        const float use = m_new == -INFINITY ? 0.f : m_new;
-        L = L * exp2f(M - use) + l * exp2f(m - use);
-        M = m_new;
+        merge_ml(M, L, p.part_m[at], p.part_l[at]);
     }
-    if constexpr (kWarp) {
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            const float m = __shfl_xor_sync(kFull, M, o), l = __shfl_xor_sync(kFull, L, o);
-            const float m_new = fmaxf(M, m);
+    for (int o = 16; o >= 1; o >>= 1)
+        merge_ml(M, L, __shfl_xor_sync(kFull, M, o), __shfl_xor_sync(kFull, L, o));
+}
+
+__device__ __forceinline__ float inverse_of(float L) { return L > 0.f || L != L ? 1.f / L : 0.f; }
+
+// Row i of a unit's hw * G over the pieces c, c + step, ... <= c1 (c0: the range
+// where the unit begins), U pieces' loads in flight: (M, L) and the unnormalised
+// output, D / 32 dims per lane.
+template <int D, int U>
+__device__ __forceinline__ void gather_row(const Params& p, int c0, int c, int c1, int step, int i, int lane,
+                                           float& M, float& L, float (&o)[D / 32]) {
+    constexpr int DPL = D / 32;
+    const int rows = p.hw * p.G;
+    M = -INFINITY;
+    L = 0.f;
+#pragma unroll
+    for (int j = 0; j < DPL; ++j) o[j] = 0.f;
+    for (; c <= c1; c += U * step) {
+        float m[U], l[U], x[U][DPL];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int cc = c + u * step;
+            const int64_t at = (2 * (int64_t)cc + (cc == c0 ? 1 : 0)) * rows + i;
+            const bool in = cc <= c1;
+            m[u] = in ? p.part_m[at] : -INFINITY;
+            l[u] = in ? p.part_l[at] : 0.f;
+            const float* src = p.part_acc + at * D + lane * DPL;
+            if constexpr (DPL == 4) {
+                const float4 v = in ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+                x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
+            } else {
+                const float2 v = in ? *reinterpret_cast<const float2*>(src) : make_float2(0.f, 0.f);
+                x[u][0] = v.x; x[u][1] = v.y;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float m_new = fmaxf(M, m[u]);
             const float use = m_new == -INFINITY ? 0.f : m_new;
-            L = L * exp2f(M - use) + l * exp2f(m - use);
+            const float wo = exp2f(M - use), wn = exp2f(m[u] - use);
+            L = L * wo + l[u] * wn;
             M = m_new;
+#pragma unroll
+            for (int j = 0; j < DPL; ++j) o[j] = fmaf(wn, x[u][j], o[j] * wo);
         }
     }
 }
 
-// After split_kernel.  The first ranges * join CTAs join, per range, the pieces
-// of the unit that begins in it and ends in a later one: a warp per row, or all
-// the CTA's warps on one row (`wpr` of them) where a unit has many pieces.  With
-// scores, `fold` CTAs per unit follow; each takes every fold-th stretch of the
-// unit's tokens, 4 tokens of a head per thread, and folds their weights into the
-// scores.
+// Writes row i of unit `unit`.
+template <class E, int D>
+__device__ __forceinline__ void write_row(const Params& p, int unit, int i, int lane, float L,
+                                          const float (&o)[D / 32]) {
+    const float inv = inverse_of(L);
+    const int64_t oh = (int64_t)(unit / p.HB) * p.H + (int64_t)(unit % p.HB) * p.hw * p.G + i;
+    uint16_t* dst = static_cast<uint16_t*>(p.out) + oh * D + lane * (D / 32);
+#pragma unroll
+    for (int j = 0; j < D / 32; j += 2)
+        *reinterpret_cast<uint32_t*>(dst + j) = E::from_float2(o[j] * inv, o[j + 1] * inv);
+}
+
+// Adds the weights of tokens j0 + 4 (32 u + lane) .. + 3, u < RUNS, of KV head
+// kvh of sequence s to their scores, by one warp; `place`: the ranges its unit
+// begins and ends in, hl: the head in it.  z of the first HEADS query heads and
+// the old scores are on their way while M and L are found.
+template <int RUNS, int HEADS>
+__device__ __forceinline__ void fold_stretch(const Params& p, int s, int kvh, int hl, int n, int2 place,
+                                             int j0, int lane) {
+    const int64_t h0 = (int64_t)s * p.H + (int64_t)kvh * p.G;
+    const float* z = p.z + h0 * p.z_stride;
+    float* sc = p.scores + ((int64_t)s * p.Hkv + kvh) * p.score_stride;
+    const bool vec = (reinterpret_cast<uintptr_t>(sc) & 15u) == 0;
+    float4 zz[RUNS][HEADS];
+    float old[RUNS][4];
+#pragma unroll
+    for (int u = 0; u < RUNS; ++u) {
+        const int j = j0 + 4 * (32 * u + lane);
+#pragma unroll
+        for (int r = 0; r < HEADS; ++r)
+            zz[u][r] = j < n && r < p.G ? *reinterpret_cast<const float4*>(z + r * p.z_stride + j)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (vec && j + 4 <= n) {
+            const float4 v = *reinterpret_cast<const float4*>(sc + j);
+            old[u][0] = v.x; old[u][1] = v.y; old[u][2] = v.z; old[u][3] = v.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) old[u][e] = j + e < n ? sc[j + e] : 0.f;
+        }
+    }
+    // M and 1 / L of query head r in lane r
+    float M = 0.f, inv = 0.f;
+    if (place.x == place.y) {
+        if (lane < p.G) {
+            M = p.row_m[h0 + lane];
+            inv = inverse_of(p.row_l[h0 + lane]);
+        }
+    } else if (place.y - place.x < 4) {  // few pieces: a lane per head
+        if (lane < p.G) {
+            float L = 0.f;
+            M = -INFINITY;
+            for (int c = place.x; c <= place.y; ++c) {
+                const int64_t at = piece_row(p, c, place.x, hl, lane);
+                merge_ml(M, L, p.part_m[at], p.part_l[at]);
+            }
+            inv = inverse_of(L);
+        }
+    } else {
+        for (int r = 0; r < p.G; ++r) {
+            float m, l;
+            join_row(p, place.x, place.y, hl, r, lane, m, l);
+            if (lane == r) {
+                M = m;
+                inv = inverse_of(l);
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < RUNS; ++u) {
+        const int j = j0 + 4 * (32 * u + lane);
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+        auto add = [&](const float4& v, int r) {
+            const float m = __shfl_sync(kFull, M, r), i = __shfl_sync(kFull, inv, r);
+            if (i != 0.f) {
+                w[0] = fmaf(exp2f(v.x - m), i, w[0]);
+                w[1] = fmaf(exp2f(v.y - m), i, w[1]);
+                w[2] = fmaf(exp2f(v.z - m), i, w[2]);
+                w[3] = fmaf(exp2f(v.w - m), i, w[3]);
+            }
+        };
+#pragma unroll
+        for (int r = 0; r < HEADS; ++r)
+            if (r < p.G) add(zz[u][r], r);
+        if constexpr (HEADS > 1) {
+#pragma unroll 4
+            for (int r = HEADS; r < p.G; ++r)
+                add(j < n ? *reinterpret_cast<const float4*>(z + r * p.z_stride + j) : make_float4(0.f, 0.f, 0.f, 0.f), r);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) old[u][e] += w[e];
+        if (vec && j + 4 <= n) {
+            *reinterpret_cast<float4*>(sc + j) = make_float4(old[u][0], old[u][1], old[u][2], old[u][3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (j + e < n) sc[j + e] = old[u][e];
+        }
+    }
+}
+
+// After split_kernel, one wave of CTAs that take items: first the joins, then,
+// with scores, the fold.  Either is short chains of loads (is there anything ->
+// where -> the data), so what counts is that a warp has few of them and waits
+// on none to learn that there is nothing to do: it looks at 32 items at once.
+//  join: a row of a unit that lies in several ranges, by a warp, or by the
+//        CTA's warps together (`wide`) where units have many pieces.
+//  fold: 256 tokens (512 with one query head) of a KV head, by a warp.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
-template <class E, int D, bool kScores>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p, int join, int wpr) {
+template <class E, int D, bool kScores, bool kOne>
+__global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const __grid_constant__ Params p, int wide) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    __shared__ float s_m[4 * kMaxGroup], s_inv[4 * kMaxGroup];
-    __shared__ __align__(16) float s_o[kJoinWarps][D];
     constexpr int DPL = D / 32;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rows = p.hw * p.G, ranges = p.ranges;
-    if ((int)blockIdx.x < ranges * join) {
-        const int c = blockIdx.x / join;
-        const int i = (blockIdx.x % join) * (kJoinWarps / wpr) + warp / wpr;
-        if (i >= rows) return;
-        const int hl = i / p.G, row = i % p.G;
-        auto load_piece = [&](int64_t at, float (&x)[DPL]) {
-            const float* src = p.part_acc + at * D + lane * DPL;
-            if constexpr (DPL == 4) {
-                const float4 v = *reinterpret_cast<const float4*>(src);
-                x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-            } else {
-                const float2 v = *reinterpret_cast<const float2*>(src);
-                x[0] = v.x; x[1] = v.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // neighbouring items go to different SMs
+    const int w0 = warp * gridDim.x + blockIdx.x, warps = gridDim.x * kJoinWarps;
+    const int rows = p.hw * p.G;
+    const int joins = p.S * p.HB * rows;  // = S * H
+    if (wide) {
+        __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+        __shared__ __align__(16) float s_o[kJoinWarps][D];
+        for (int i = blockIdx.x; i < joins; i += gridDim.x) {
+            const int2 at = p.place[i / rows];
+            if (at.x == at.y) continue;  // the same for the whole CTA
+            float M, L, o[DPL];
+            gather_row<D, 8>(p, at.x, at.x + warp, at.y, kJoinWarps, i % rows, lane, M, L, o);
+            if (lane == 0) {
+                s_m[warp] = M;
+                s_l[warp] = L;
             }
-        };
-        // most cut units have two pieces, whose places do not depend on the
-        // unit: their loads go out with the look at whether there is one
-        float x0[DPL], x1[DPL];
-        if (wpr == 1 && c + 1 < ranges) {
-            load_piece(piece_row(p, c, c, hl, row), x0);
-            load_piece(piece_row(p, c + 1, c, hl, row), x1);
-        }
-        const RangeInfo ri = p.info[c];
-        if (ri.unit < 0) return;  // the same for all warps of a row
-        float M, L;
-        join_row<true>(p, c, ri.c1, hl, row, lane, M, L);
-        const float use = M == -INFINITY ? 0.f : M;
-        float o[DPL];
-#pragma unroll
-        for (int j = 0; j < DPL; ++j) o[j] = 0.f;
-        auto add = [&](int cc, const float (&x)[DPL]) {
-            const float w = exp2f(p.part_m[piece_row(p, cc, c, hl, row)] - use);
-#pragma unroll
-            for (int j = 0; j < DPL; ++j) o[j] = fmaf(w, x[j], o[j]);
-        };
-        int cc = c + warp % wpr;
-        if (wpr == 1) {
-            add(c, x0);
-            add(c + 1, x1);
-            cc = c + 2;
-        }
-#pragma unroll 8
-        for (; cc <= ri.c1; cc += wpr) {
-            float x[DPL];
-            load_piece(piece_row(p, cc, c, hl, row), x);
-            add(cc, x);
-        }
-        if (wpr > 1) {  // one row per CTA: add the warps' sums
 #pragma unroll
             for (int j = 0; j < DPL; ++j) s_o[warp][lane * DPL + j] = o[j];
             __syncthreads();
-            if (warp != 0) return;
+            if (warp == 0) {
 #pragma unroll
-            for (int w = 1; w < kJoinWarps; ++w)
+                for (int w = 1; w < kJoinWarps; ++w) {
+                    const float m_new = fmaxf(M, s_m[w]);
+                    const float use = m_new == -INFINITY ? 0.f : m_new;
+                    const float wo = exp2f(M - use), wn = exp2f(s_m[w] - use);
+                    L = L * wo + s_l[w] * wn;
+                    M = m_new;
 #pragma unroll
-                for (int j = 0; j < DPL; ++j) o[j] += s_o[w][lane * DPL + j];
+                    for (int j = 0; j < DPL; ++j) o[j] = fmaf(wn, s_o[w][lane * DPL + j], o[j] * wo);
+                }
+                write_row<E, D>(p, i / rows, i % rows, lane, L, o);
+            }
+            __syncthreads();  // the parts have been read
         }
-        const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-        const int64_t oh = (int64_t)(ri.unit / p.HB) * p.H + (int64_t)(ri.unit % p.HB) * rows + i;
-        uint16_t* dst = static_cast<uint16_t*>(p.out) + oh * D + lane * DPL;
-#pragma unroll
-        for (int j = 0; j < DPL; j += 2)
-            *reinterpret_cast<uint32_t*>(dst + j) = E::from_float2(o[j] * inv, o[j + 1] * inv);
-        return;
+    } else {
+        for (int base = w0; base < joins; base += 32 * warps) {
+            const int mine = base + lane * warps;
+            int2 at = make_int2(0, 0);
+            if (mine < joins) at = p.place[mine / rows];
+            for (unsigned todo = __ballot_sync(kFull, at.x != at.y); todo; todo &= todo - 1) {
+                const int src = __ffs(todo) - 1;
+                const int i = base + src * warps;
+                const int c0 = __shfl_sync(kFull, at.x, src), c1 = __shfl_sync(kFull, at.y, src);
+                float M, L, o[DPL];
+                gather_row<D, 4>(p, c0, c0, c1, 1, i % rows, lane, M, L, o);
+                write_row<E, D>(p, i / rows, i % rows, lane, L, o);
+            }
+        }
     }
     if constexpr (kScores) {
-        const int f = blockIdx.x - ranges * join;
-        const int unit = f / p.fold, part = f % p.fold;
-        const int s = unit / p.HB, hb = unit % p.HB;
-        const int2 place = p.place[unit];  // the unit's first and last range
-        const int n = context_of(p, s);
-        const int per = kJoinThreads / p.hw;  // threads per head
-        if (part * 4 * per >= n) return;
-        auto keep = [&](int i, float M, float L) {
-            s_m[i] = M;
-            s_inv[i] = L > 0.f || L != L ? 1.f / L : 0.f;
-        };
-        if (place.x == place.y) {
-            if (tid < rows) {
-                const int64_t oh = (int64_t)s * p.H + (int64_t)hb * rows + tid;
-                keep(tid, p.row_m[oh], p.row_l[oh]);
+        constexpr int RUNS = kOne ? 4 : 2, HEADS = kOne ? 1 : 4, TOKENS = RUNS * 128;
+        const int stretches = (p.max_ctx + TOKENS - 1) / TOKENS;
+        const int heads = p.S * p.Hkv;
+        const long long items = (long long)heads * stretches;
+        // item (stretch, sequence, KV head): the first stretches of all first
+        for (long long base = w0; base < items; base += 32LL * warps) {
+            const long long mine = base + (long long)lane * warps;
+            int u = 0, st = 0, n = 0;
+            int2 place = make_int2(0, 0);
+            if (mine < items) {
+                st = (int)(mine / heads);
+                u = (int)(mine % heads);
+                n = context_of(p, u / p.Hkv);
+                place = p.place[u / p.hw];
             }
-        } else if (place.y - place.x < 4) {  // few pieces: a thread per row
-            if (tid < rows) {
-                float M, L;
-                join_row<false>(p, place.x, place.y, tid / p.G, tid % p.G, lane, M, L);
-                keep(tid, M, L);
-            }
-        } else {
-            for (int i = warp; i < rows; i += kJoinWarps) {
-                float M, L;
-                join_row<true>(p, place.x, place.y, i / p.G, i % p.G, lane, M, L);
-                if (lane == 0) keep(i, M, L);
+            for (unsigned todo = __ballot_sync(kFull, st * TOKENS < n); todo; todo &= todo - 1) {
+                const int src = __ffs(todo) - 1;
+                const int unit = __shfl_sync(kFull, u, src), stretch = __shfl_sync(kFull, st, src);
+                const int len = __shfl_sync(kFull, n, src);
+                const int2 at = make_int2(__shfl_sync(kFull, place.x, src), __shfl_sync(kFull, place.y, src));
+                const int kvh = unit % p.Hkv;
+                fold_stretch<RUNS, HEADS>(p, unit / p.Hkv, kvh, kvh % p.hw, len, at, stretch * TOKENS, lane);
             }
         }
-        __syncthreads();
-        const int hl = tid / per;
-        for (int j = part * 4 * per; j < n; j += p.fold * 4 * per)
-            fold_weights(p, s, hb * p.hw + hl, j, min(n, j + 4 * per), s_m + hl * p.G,
-                         s_inv + hl * p.G, tid % per, per);
     }
 }
 
@@ -1122,14 +1230,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 // resident ones.
 constexpr int kDirectTokens = 1024;
 constexpr int kDirectWaves = 2;
-constexpr int kFoldCtas = 4096;     // of a split call's join kernel
+constexpr int kJoinCtasPerSm = 3;   // of the join kernel
 constexpr int kCtasPerSm = 2;       // of the attention kernels
 constexpr int kMinUnits = 16;       // of a split call, else fewer KV heads per unit
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Layout {
-    size_t info, m, l, acc, place, row_m, row_l, z, total;
+    size_t place, m, l, acc, row_m, row_l, z, total;
     int64_t z_stride;
 };
 
@@ -1140,15 +1248,14 @@ Layout layout_of(int S, int H, int Hkv, int D, bool scores, int max_ctx) {
     const size_t rows = (size_t)2 * kMaxRanges * heads_per_cta(Hkv) * (H / Hkv);
     Layout L;
     size_t o = 0;
-    L.info = o;  o = align256(o + kMaxRanges * sizeof(RangeInfo));
+    L.place = o; o = align256(o + (size_t)S * Hkv * sizeof(int2));
     L.m = o;     o = align256(o + rows * sizeof(float));
     L.l = o;     o = align256(o + rows * sizeof(float));
     L.acc = o;   o = align256(o + rows * D * sizeof(float));
-    L.place = L.row_m = L.row_l = L.z = o;
+    L.row_m = L.row_l = L.z = o;
     L.z_stride = ((int64_t)max_ctx + kTile - 1) / kTile * kTile;
     if (L.z_stride == 0) L.z_stride = kTile;
     if (scores) {
-        o = align256(o + (size_t)S * Hkv * sizeof(int2));
         L.row_m = o; o = align256(o + (size_t)S * H * sizeof(float));
         L.row_l = o; o = align256(o + (size_t)S * H * sizeof(float));
         L.z = o;     o = align256(o + (size_t)S * H * L.z_stride * sizeof(float));
@@ -1158,7 +1265,7 @@ Layout layout_of(int S, int H, int Hkv, int D, bool scores, int max_ctx) {
 }
 
 using KernelFn = void (*)(Params);
-using JoinFn = void (*)(Params, int, int);
+using JoinFn = void (*)(Params, int);
 
 template <class E, bool kScores, bool kDirect>
 KernelFn pick_attend(int D, bool wide) {
@@ -1176,10 +1283,14 @@ KernelFn pick_attend(pkv_dtype dtype, int D, bool wide) {
                             : pick_attend<pkv::BF16, kScores, kDirect>(D, wide);
 }
 
-template <bool kScores>
-JoinFn pick_join(pkv_dtype dtype, int D) {
-    if (dtype == PKV_F16) return D == 128 ? join_kernel<pkv::F16, 128, kScores> : join_kernel<pkv::F16, 64, kScores>;
-    return D == 128 ? join_kernel<pkv::BF16, 128, kScores> : join_kernel<pkv::BF16, 64, kScores>;
+template <class E, int D>
+JoinFn pick_join(bool scores, bool one) {
+    if (!scores) return join_kernel<E, D, false, false>;
+    return one ? join_kernel<E, D, true, true> : join_kernel<E, D, true, false>;
+}
+JoinFn pick_join(pkv_dtype dtype, int D, bool scores, bool one) {
+    if (dtype == PKV_F16) return D == 128 ? pick_join<pkv::F16, 128>(scores, one) : pick_join<pkv::F16, 64>(scores, one);
+    return D == 128 ? pick_join<pkv::BF16, 128>(scores, one) : pick_join<pkv::BF16, 64>(scores, one);
 }
 
 // Resident CTAs per SM of an attention kernel, after allowing it its shared
@@ -1266,7 +1377,6 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     p.sinks = sinks;
     p.qscale = scale * kLog2e;
     char* w = static_cast<char*>(workspace);
-    p.info = reinterpret_cast<RangeInfo*>(w + L.info);
     p.place = reinterpret_cast<int2*>(w + L.place);
     p.part_m = reinterpret_cast<float*>(w + L.m);
     p.part_l = reinterpret_cast<float*>(w + L.l);
@@ -1305,13 +1415,6 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     if (p.ranges0 > kMaxRanges / (1 + kSmallRanges)) p.ranges0 = kMaxRanges / (1 + kSmallRanges);
     // small ranges only where changing over costs nothing (a warp per head)
     p.ranges = p.nsplit == 1 ? p.ranges0 * (1 + kSmallRanges) : p.ranges0;
-    // as many fold CTAs per unit as its longest context has stretches, while
-    // the grid stays within a few times the card
-    const int64_t units = (int64_t)S * p.HB, stretch = 4 * kJoinThreads / p.hw;
-    p.fold = (int)((max_ctx + stretch - 1) / stretch);
-    const int most_fold = kFoldCtas / units > 1 ? (int)(kFoldCtas / units) : 1;
-    if (p.fold > most_fold) p.fold = most_fold;
-    if (p.fold < 1) p.fold = 1;
 
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1329,15 +1432,13 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     cfg.gridDim = dim3(direct ? (unsigned)(S * Hkv * p.cs) : (unsigned)p.ranges);
     cudaError_t e = cudaLaunchKernelEx(&cfg, direct ? direct_fn : split_fn, p);
     if (e == cudaSuccess && !direct) {
-        // a unit of more than 16 pieces: a CTA per row
-        const int wpr = p.ranges0 > 16 * units ? kJoinWarps : 1;
-        const int join = (p.hw * p.G * wpr + kJoinWarps - 1) / kJoinWarps;
+        // units of more than 8 pieces: a CTA per row
+        const int wide = p.ranges > 8 * (int64_t)S * p.HB;
         cfg.dynamicSmemBytes = 0;
         cfg.numAttrs = 1;
         cfg.blockDim = dim3(kJoinThreads);
-        cfg.gridDim = dim3((unsigned)(p.ranges * join + (with_scores ? units * p.fold : 0)));
-        e = cudaLaunchKernelEx(&cfg, with_scores ? pick_join<true>(dtype, D) : pick_join<false>(dtype, D), p,
-                               join, wpr);
+        cfg.gridDim = dim3((unsigned)(kJoinCtasPerSm * sms));
+        e = cudaLaunchKernelEx(&cfg, pick_join(dtype, D, with_scores, p.G == 1), p, wide);
     }
     if (e != cudaSuccess) {
         snprintf(msg, sizeof msg, "%s launch", who);

@@ -39,6 +39,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kFewKeys = 2048;        // a row of fewer is one CTA's
+constexpr int kManyKeys = 4096;       // a row of more is several CTAs'
 constexpr int kSmemKeys = 48 * 1024;  // keys a CTA can hold: 192 KB
 constexpr int kChunk = 128;           // keys a warp takes at once, 4 per lane
 constexpr unsigned kFull = 0xffffffffu;
@@ -110,7 +111,7 @@ __device__ __forceinline__ void store4(T* p, int count, bool vec, const T (&v)[4
 }
 
 template <int D, bool kCluster>
-__global__ void __launch_bounds__(kThreads, 4) evict_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, 5) evict_kernel(Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     extern __shared__ __align__(16) uint32_t s_keys[];
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 4) evict_kernel(Params p) {
     // and moves its score and position, then LPR lanes copy each K or V row.
     constexpr int LPR = D / 8;
     constexpr int PER_STEP = 32 / (2 * LPR);  // movers copied by one warp-wide load
-    constexpr int M = 8;                      // loads in flight per lane
+    constexpr int M = 4;                      // loads in flight per lane
     const int sub = lane / (2 * LPR), part = lane % (2 * LPR);
     uint4* cache = part < LPR ? p.k_cache : p.v_cache;
     const int64_t row_vecs = (int64_t)p.Hkv * LPR;
@@ -506,8 +507,8 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
                             const int32_t* positions, const int32_t* block_tables,
                             const int32_t* context_lens, const int32_t* token_counts,
                             float* scores_out, int32_t* positions_out, int32_t* new_context_lens,
-                            int S, int Hkv, int D, int bs, int NB, int MB, int64_t score_stride,
-                            int budget, int recent_tokens, int sink_tokens, pkv_dtype dtype,
+                            int S, int Hkv, int D, int bs, int NB, int MB, int max_context_len,
+                            int64_t score_stride, int budget, int recent_tokens, int sink_tokens, pkv_dtype dtype,
                             void* workspace, size_t workspace_bytes, void* stream) {
     PKV_TRACE("pkv_evict_tokens");
     pkv::clear_error();
@@ -515,6 +516,10 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
         return pkv::fail(PKV_ERR_INVALID_ARG, "evict_tokens: bad size or dtype");
     if ((D != 64 && D != 128) || (bs != 8 && bs != 16 && bs != 32 && bs != 64))
         return pkv::fail(PKV_ERR_UNSUPPORTED, "evict_tokens: head_dim must be 64/128, block_size 8/16/32/64");
+    if (max_context_len < 0 || max_context_len > (int64_t)MB * bs)
+        return pkv::fail(PKV_ERR_INVALID_ARG, "evict_tokens: max_context_len must be in [0, MB*bs]");
+    if (score_stride < (max_context_len ? max_context_len : (int64_t)MB * bs))
+        return pkv::fail(PKV_ERR_INVALID_ARG, "evict_tokens: score_stride must be at least max_context_len");
     if (budget < 1 || recent_tokens < 0 || sink_tokens < 0 || (int64_t)recent_tokens + sink_tokens > budget)
         return pkv::fail(PKV_ERR_INVALID_ARG, "evict_tokens: budget must be >= 1 and hold the sinks and the recent tokens");
     if ((int64_t)NB * bs > INT32_MAX)
@@ -535,7 +540,7 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
     if (workspace_bytes < pkv_evict_workspace_size(S, Hkv, budget))
         return pkv::fail(PKV_ERR_WORKSPACE, "evict_tokens: workspace too small");
 
-    const int64_t cap = (int64_t)MB * bs < score_stride ? (int64_t)MB * bs : score_stride;
+    const int64_t cap = max_context_len ? max_context_len : (int64_t)MB * bs;
     Params p;
     p.k_cache = static_cast<uint4*>(k_cache);
     p.v_cache = static_cast<uint4*>(v_cache);
@@ -567,7 +572,7 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
     const int rows = S * Hkv;
     int cs = 1;
     while (cs < kMaxCluster && ((rows * cs < 2 * pkv::sm_count() && p.max_ctx / cs > kFewKeys) ||
-                                p.max_ctx / cs > kSmemKeys))
+                                p.max_ctx / cs > kManyKeys))
         cs *= 2;
     const int seg = ((p.max_ctx + cs - 1) / cs + kChunk - 1) / kChunk * kChunk;
     p.seg_cap = seg < kSmemKeys ? seg : kSmemKeys;

@@ -52,10 +52,22 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The same with `bytes` of the 16 read and the rest zero-filled: 0 reads
-// nothing, so `src` need only be an address.
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+// L2 policy for data read once: the first to go when room is needed.
+__device__ __forceinline__ uint64_t policy_evict_first() {
+    uint64_t policy;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
+}
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+    uint64_t policy;
+    asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
+}
+// cp_async16 with `bytes` of the 16 read and the rest zero-filled (0 reads
+// nothing, so `src` need only be an address), under an L2 policy.
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, int bytes, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+                 "r"(bytes), "l"(policy)
                  : "memory");
 }
 

@@ -265,7 +265,7 @@ def paged_attention_decode_accumulate(out, scores, q, k_cache, v_cache, block_ta
 
 def evict_tokens(k_cache, v_cache, scores, positions, block_tables, context_lens, token_counts,
                  new_context_lens, budget, recent_tokens, sink_tokens=0, scores_out=None,
-                 positions_out=None, workspace=None, stream=None):
+                 positions_out=None, max_context_len=0, workspace=None, stream=None):
     """Keeps the `budget` best tokens of every (sequence, KV head) with more
     -- the first sink_tokens positions and the last recent_tokens ones, then
     the highest scores, ties by the lowest index -- and compacts the caches,
@@ -276,7 +276,8 @@ def evict_tokens(k_cache, v_cache, scores, positions, block_tables, context_lens
     sequence's row is all -1); context_lens, token_counts [S] int32: tokens
     cached and tokens seen; new_context_lens [S] int32 receives
     min(context_lens, budget).  scores_out / positions_out: other arrays for
-    the results (default: in place).  The evicted sequences' blocks must be
+    the results (default: in place); max_context_len bounds context_lens (0:
+    MB * bs).  The evicted sequences' blocks must be
     their own (BlockAllocator.unshare); afterwards BlockAllocator.truncate
     releases the blocks past the budget."""
     who = "evict_tokens"
@@ -321,8 +322,8 @@ def evict_tokens(k_cache, v_cache, scores, positions, block_tables, context_lens
     _launch(who, L.lib().pkv_evict_tokens, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(),
             scores.data_ptr(), positions.data_ptr(), block_tables.data_ptr(),
             context_lens.data_ptr(), token_counts.data_ptr(), scores_out.data_ptr(),
-            positions_out.data_ptr(), new_context_lens.data_ptr(), S, Hkv, D, bs, NB, MB, rows[2],
-            budget, recent_tokens, sink_tokens, dtype_code(dt), ws.data_ptr(), ws.numel())
+            positions_out.data_ptr(), new_context_lens.data_ptr(), S, Hkv, D, bs, NB, MB, max_context_len,
+            rows[2], budget, recent_tokens, sink_tokens, dtype_code(dt), ws.data_ptr(), ws.numel())
 
 
 def compute_slot_mapping(slot_mapping, block_tables, seq_idx, pos, block_size, stream=None):
