@@ -20,7 +20,7 @@ import numpy as np
 import torch
 
 from . import _lib as L
-from .allocator import BlockAllocator, plan_step
+from .allocator import BlockAllocator, check_copy_pairs, plan_step
 
 _DTYPES = {torch.float16: L.PKV_F16, torch.bfloat16: L.PKV_BF16}
 _TORCH = {"f16": torch.float16, "bf16": torch.bfloat16}
@@ -139,77 +139,67 @@ def _need(who, tensors, cache):
             _refuse(f"{who}: {name} is on {t.device}, the caches on {dev}")
 
 
-_I32 = torch.int32
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
 
 
-def _launch(who, fn, dev, stream, *args):
-    """fn(*args, stream handle) with device `dev` current (None: torch's
-    current stream on it)."""
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _launch(who, fn, dev, stream, *args)
-    st = fn(*args, L.current_stream_handle(dev) if stream is None else L.stream_handle(stream))
-    if st:
-        L.check(st, who)
-
-
-def _attention_args(who, out, q, k_cache, v_cache, block_tables, context_lens):
-    """Checks what the two attention calls share; returns the sizes."""
-    if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2:
+def _attention_sizes(who, out, q, k_cache, v_cache, block_tables, context_lens):
+    """Checks what the two attention calls share; returns the sizes and the
+    device.  One expression on the way through: these calls take a few
+    microseconds on the GPU, and every attribute counts.  _need then says
+    what is wrong."""
+    shape, cshape, tshape = q.shape, k_cache.shape, block_tables.shape
+    if len(shape) != 3 or len(cshape) != 4 or len(tshape) != 2:
         _refuse(f"{who}: q must be [S, H, D], the caches [NB, bs, Hkv, D], block_tables [S, MB]")
-    shape, cshape = q.shape, k_cache.shape
     S, H, D = shape
     NB, bs, Hkv, Dk = cshape
-    MB = block_tables.shape[1]
     if Dk != D:
         _refuse(f"{who}: q has head_dim {D}, the caches {Dk}")
     dt, dev = k_cache.dtype, k_cache.get_device()
-    # one expression on the way through; _need says what is wrong
     if not (dev >= 0 and q.dtype is dt and out.dtype is dt and v_cache.dtype is dt
             and block_tables.dtype is _I32 and context_lens.dtype is _I32 and out.shape == shape
-            and v_cache.shape == cshape and block_tables.shape[0] == S
-            and context_lens.shape == (S,) and q.is_contiguous() and out.is_contiguous()
-            and k_cache.is_contiguous() and v_cache.is_contiguous()
-            and block_tables.is_contiguous() and context_lens.is_contiguous()
-            and q.get_device() == dev and out.get_device() == dev and v_cache.get_device() == dev
+            and v_cache.shape == cshape and tshape[0] == S and context_lens.shape == (S,)
+            and q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and block_tables.is_contiguous()
+            and context_lens.is_contiguous() and q.get_device() == dev
+            and out.get_device() == dev and v_cache.get_device() == dev
             and block_tables.get_device() == dev and context_lens.get_device() == dev):
         _need(who, (("k_cache", k_cache, dt, None), ("q", q, dt, None), ("out", out, dt, shape),
                     ("v_cache", v_cache, dt, cshape),
-                    ("block_tables", block_tables, _I32, (S, MB)),
+                    ("block_tables", block_tables, _I32, (S, tshape[1])),
                     ("context_lens", context_lens, _I32, (S,))), k_cache)
-    return S, H, D, NB, bs, Hkv, MB, dev
+    return S, H, D, NB, bs, Hkv, tshape[1], dev
 
 
-def _workspace(who, ws, size, device, stream=None):
-    if ws is None:
-        n = size()
-        if n == 0:
-            _refuse(f"{who}: bad workspace arguments (H a multiple of Hkv, at most 16 per group?)")
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
-        if stream is not None:  # keeps its memory until the call's stream has passed
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            ws.record_stream(stream)
-        return ws
-    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device:
-        _refuse(f"{who}: workspace must be a contiguous uint8 tensor on {device}")
+def _workspace(who, nbytes, device, stream=None):
+    """A workspace for one call; its memory stays taken until the call's
+    stream has passed."""
+    if nbytes == 0:
+        _refuse(f"{who}: bad workspace arguments (H a multiple of Hkv, at most 16 per group?)")
+    ws = torch.empty(nbytes, dtype=_U8, device=device)
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        ws.record_stream(stream)
     return ws
 
 
+def _check_workspace(who, ws, dev):
+    if ws.dtype is not _U8 or ws.get_device() != dev or not ws.is_contiguous():
+        _refuse(f"{who}: workspace must be a contiguous uint8 tensor on the caches' device")
+
+
 def new_window_workspace(S, H, Hkv, D, device="cuda") -> torch.Tensor:
-    return _workspace("new_window_workspace", None,
-                      lambda: L.pkv_decode_window_workspace_size(S, H, Hkv, D), device)
+    return _workspace("new_window_workspace", L.pkv_decode_window_workspace_size(S, H, Hkv, D),
+                      device)
 
 
 def new_accumulate_workspace(S, H, Hkv, D, max_context_len, device="cuda") -> torch.Tensor:
-    return _workspace("new_accumulate_workspace", None,
-                      lambda: L.pkv_decode_accumulate_workspace_size(S, H, Hkv, D,
-                                                                     max_context_len), device)
+    return _workspace("new_accumulate_workspace",
+                      L.pkv_decode_accumulate_workspace_size(S, H, Hkv, D, max_context_len), device)
 
 
 def new_evict_workspace(S, Hkv, budget, device="cuda") -> torch.Tensor:
-    return _workspace("new_evict_workspace", None,
-                      lambda: L.pkv_evict_workspace_size(S, Hkv, budget), device)
+    return _workspace("new_evict_workspace", L.pkv_evict_workspace_size(S, Hkv, budget), device)
 
 
 def paged_attention_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, window,
@@ -225,15 +215,27 @@ def paged_attention_decode_window(out, q, k_cache, v_cache, block_tables, contex
     workspace: new_window_workspace(S, H, Hkv, D), kept between calls.
     """
     who = "paged_attention_decode_window"
-    S, H, D, NB, bs, Hkv, MB, dev = _attention_args(who, out, q, k_cache, v_cache, block_tables,
-                                                    context_lens)
-    ws = _workspace(who, workspace, lambda: L.pkv_decode_window_workspace_size(S, H, Hkv, D),
-                    k_cache.device, stream)
-    _launch(who, L.lib().pkv_paged_attention_decode_window, dev, stream, out.data_ptr(),
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-            context_lens.data_ptr(), S, H, Hkv, D, bs, NB, MB, max_context_len, window,
-            sink_tokens, 1.0 / math.sqrt(D) if scale is None else scale, dtype_code(k_cache.dtype),
-            ws.data_ptr(), ws.numel())
+    S, H, D, NB, bs, Hkv, MB, dev = _attention_sizes(who, out, q, k_cache, v_cache, block_tables,
+                                                     context_lens)
+    ws = workspace
+    if ws is None:
+        ws = _workspace(who, L.pkv_decode_window_workspace_size(S, H, Hkv, D), k_cache.device, stream)
+    else:
+        _check_workspace(who, ws, dev)
+
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return paged_attention_decode_window(out, q, k_cache, v_cache, block_tables,
+                                                 context_lens, window, sink_tokens, scale,
+                                                 max_context_len, ws, stream)
+    handle = L.current_stream_handle(dev) if stream is None else L.stream_handle(stream)
+    st = L.lib().pkv_paged_attention_decode_window(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        block_tables.data_ptr(), context_lens.data_ptr(), S, H, Hkv, D, bs, NB, MB,
+        max_context_len, window, sink_tokens, D ** -0.5 if scale is None else scale,
+        dtype_code(k_cache.dtype), ws.data_ptr(), ws.numel(), handle)
+    if st:
+        L.check(st, who)
     return out
 
 
@@ -247,19 +249,32 @@ def paged_attention_decode_accumulate(out, scores, q, k_cache, v_cache, block_ta
     paged_attention_decode_window; workspace: new_accumulate_workspace(S, H,
     Hkv, D, max_context_len)."""
     who = "paged_attention_decode_accumulate"
-    S, H, D, NB, bs, Hkv, MB, dev = _attention_args(who, out, q, k_cache, v_cache, block_tables,
-                                                    context_lens)
-    if not (scores.dtype is torch.float32 and scores.dim() == 3 and scores.shape[:2] == (S, Hkv)
+    S, H, D, NB, bs, Hkv, MB, dev = _attention_sizes(who, out, q, k_cache, v_cache, block_tables,
+                                                     context_lens)
+    rows = scores.shape
+    if not (scores.dtype is _F32 and len(rows) == 3 and rows[0] == S and rows[1] == Hkv
             and scores.is_contiguous() and scores.get_device() == dev):
-        _need(who, (("scores", scores, torch.float32, (S, Hkv, scores.shape[-1])),), k_cache)
-    cap = scores.shape[2]
-    ws = _workspace(who, workspace, lambda: L.pkv_decode_accumulate_workspace_size(
-        S, H, Hkv, D, max_context_len or MB * bs), k_cache.device, stream)
-    _launch(who, L.lib().pkv_paged_attention_decode_accumulate, dev, stream, out.data_ptr(),
-            scores.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            block_tables.data_ptr(), context_lens.data_ptr(), S, H, Hkv, D, bs, NB, MB,
-            max_context_len, cap, 1.0 / math.sqrt(D) if scale is None else scale,
-            dtype_code(k_cache.dtype), ws.data_ptr(), ws.numel())
+        _need(who, (("scores", scores, _F32, (S, Hkv, rows[-1] if len(rows) else 0)),), k_cache)
+    ws = workspace
+    if ws is None:
+        ws = _workspace(who, L.pkv_decode_accumulate_workspace_size(
+            S, H, Hkv, D, max_context_len or MB * bs), k_cache.device, stream)
+    else:
+        _check_workspace(who, ws, dev)
+
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return paged_attention_decode_accumulate(out, scores, q, k_cache, v_cache,
+                                                     block_tables, context_lens, scale,
+                                                     max_context_len, ws, stream)
+    handle = L.current_stream_handle(dev) if stream is None else L.stream_handle(stream)
+    st = L.lib().pkv_paged_attention_decode_accumulate(
+        out.data_ptr(), scores.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, H, Hkv, D, bs,
+        NB, MB, max_context_len, rows[2], D ** -0.5 if scale is None else scale,
+        dtype_code(k_cache.dtype), ws.data_ptr(), ws.numel(), handle)
+    if st:
+        L.check(st, who)
     return out
 
 
@@ -289,10 +304,10 @@ def evict_tokens(k_cache, v_cache, scores, positions, block_tables, context_lens
         scores_out = scores
     if positions_out is None:
         positions_out = positions
-    f32, dt, dev = torch.float32, k_cache.dtype, k_cache.get_device()
+    dt, dev = k_cache.dtype, k_cache.get_device()
     rows = scores.shape
     if not (dev >= 0 and len(rows) == 3 and rows[0] == S and rows[1] == Hkv and v_cache.dtype is dt
-            and scores.dtype is f32 and scores_out.dtype is f32 and positions.dtype is _I32
+            and scores.dtype is _F32 and scores_out.dtype is _F32 and positions.dtype is _I32
             and positions_out.dtype is _I32 and block_tables.dtype is _I32
             and context_lens.dtype is _I32 and token_counts.dtype is _I32
             and new_context_lens.dtype is _I32 and v_cache.shape == k_cache.shape
@@ -310,20 +325,33 @@ def evict_tokens(k_cache, v_cache, scores, positions, block_tables, context_lens
             and new_context_lens.get_device() == dev):
         want = (S, Hkv, rows[-1] if len(rows) else 0)
         _need(who, (("k_cache", k_cache, dt, None), ("v_cache", v_cache, dt, k_cache.shape),
-                    ("scores", scores, f32, want), ("positions", positions, _I32, want),
-                    ("scores_out", scores_out, f32, want),
+                    ("scores", scores, _F32, want), ("positions", positions, _I32, want),
+                    ("scores_out", scores_out, _F32, want),
                     ("positions_out", positions_out, _I32, want),
                     ("block_tables", block_tables, _I32, None),
                     ("context_lens", context_lens, _I32, (S,)),
                     ("token_counts", token_counts, _I32, (S,)),
                     ("new_context_lens", new_context_lens, _I32, (S,))), k_cache)
-    ws = _workspace(who, workspace, lambda: L.pkv_evict_workspace_size(S, Hkv, budget),
-                    k_cache.device, stream)
-    _launch(who, L.lib().pkv_evict_tokens, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(),
-            scores.data_ptr(), positions.data_ptr(), block_tables.data_ptr(),
-            context_lens.data_ptr(), token_counts.data_ptr(), scores_out.data_ptr(),
-            positions_out.data_ptr(), new_context_lens.data_ptr(), S, Hkv, D, bs, NB, MB, max_context_len,
-            rows[2], budget, recent_tokens, sink_tokens, dtype_code(dt), ws.data_ptr(), ws.numel())
+    ws = workspace
+    if ws is None:
+        ws = _workspace(who, L.pkv_evict_workspace_size(S, Hkv, budget), k_cache.device, stream)
+    else:
+        _check_workspace(who, ws, dev)
+
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return evict_tokens(k_cache, v_cache, scores, positions, block_tables, context_lens,
+                                token_counts, new_context_lens, budget, recent_tokens, sink_tokens,
+                                scores_out, positions_out, max_context_len, ws, stream)
+    handle = L.current_stream_handle(dev) if stream is None else L.stream_handle(stream)
+    st = L.lib().pkv_evict_tokens(
+        k_cache.data_ptr(), v_cache.data_ptr(), scores.data_ptr(), positions.data_ptr(),
+        block_tables.data_ptr(), context_lens.data_ptr(), token_counts.data_ptr(),
+        scores_out.data_ptr(), positions_out.data_ptr(), new_context_lens.data_ptr(), S, Hkv, D,
+        bs, NB, MB, max_context_len, rows[2], budget, recent_tokens, sink_tokens,
+        dtype_code(dt), ws.data_ptr(), ws.numel(), handle)
+    if st:
+        L.check(st, who)
 
 
 def compute_slot_mapping(slot_mapping, block_tables, seq_idx, pos, block_size, stream=None):
@@ -661,6 +689,59 @@ class DecodeStep:
         return paged_attention_decode_shared_prefix(
             self.out, self.q, self.k_cache, self.v_cache, self.block_tables, self.context_lens, g,
             self.scale, self.max_context_len, self.partition_tokens, stream=stream)
+
+    def decode_window(self, window, sink_tokens=0, stream=None):
+        """decode() over the first sink_tokens tokens and the last `window`
+        of each context (see paged_attention_decode_window)."""
+        if getattr(self, "_window_ws", None) is None:
+            self._window_ws = new_window_workspace(self.S, self.H, self.H, self.D, self.device)
+        return paged_attention_decode_window(
+            self.out, self.q, self.k_cache, self.v_cache, self.block_tables, self.context_lens,
+            window, sink_tokens, self.scale, self.max_context_len, self._window_ws, stream)
+
+    def decode_accumulate(self, stream=None):
+        """decode() that also adds every token's attention weight to
+        self.scores ([S, H, MB * bs] fp32, made on the first call; see
+        paged_attention_decode_accumulate), which evict() goes by."""
+        if getattr(self, "scores", None) is None:
+            cap = self.MB * self.bs
+            self.scores = torch.zeros((self.S, self.H, cap), device=self.device)
+            self.positions = torch.full((self.S, self.H, cap), -1, dtype=torch.int32,
+                                        device=self.device)
+            self.token_counts = self.context_lens.clone()
+            self._accumulate_ws = new_accumulate_workspace(self.S, self.H, self.H, self.D,
+                                                           self.max_context_len, self.device)
+        return paged_attention_decode_accumulate(
+            self.out, self.scores, self.q, self.k_cache, self.v_cache, self.block_tables,
+            self.context_lens, self.scale, self.max_context_len, self._accumulate_ws, stream)
+
+    def evict(self, budget, recent_tokens, sink_tokens=0, stream=None):
+        """After decode_accumulate: keeps `budget` tokens of every longer
+        sequence (see evict_tokens) and returns the blocks past them to the
+        pool.  Blocks that will be written are copied first where they are
+        shared.  Returns the number of blocks freed."""
+        over = [s for s in range(self.S) if self.context_lens_host[s] > budget]
+        pairs = [self.allocator.unshare(self.tables_host[s],
+                                        min(-(-budget // self.bs), int(self.nblocks_host[s])))
+                 for s in over]
+        pairs = np.concatenate(pairs) if pairs else np.empty((0, 2), dtype=np.int64)
+        if len(pairs):
+            check_copy_pairs(pairs, self.NB)
+            self.block_tables = torch.from_numpy(self.tables_host).to(self.device)
+            copy_blocks(self.k_cache, self.v_cache, torch.from_numpy(pairs).to(self.device), stream)
+        new_lens = torch.empty_like(self.context_lens)
+        evict_tokens(self.k_cache, self.v_cache, self.scores, self.positions, self.block_tables,
+                     self.context_lens, self.token_counts, new_lens, budget, recent_tokens,
+                     sink_tokens, max_context_len=self.max_context_len, stream=stream)
+        self.context_lens = new_lens
+        self.context_lens_host = np.minimum(self.context_lens_host, budget).astype(np.int32)
+        freed = 0
+        for s in over:
+            nb, n = self.allocator.truncate(self.tables_host[s], self.nblocks_host[s], budget, self.bs)
+            self.nblocks_host[s] = nb
+            freed += n
+        self.block_tables = torch.from_numpy(self.tables_host).to(self.device)
+        return freed
 
     def decode(self, stream=None):
         L.pkv_paged_attention_decode(self.out, self.q, self.k_cache, self.v_cache,
