@@ -719,16 +719,21 @@ class DecodeStep:
         """After decode_accumulate: keeps `budget` tokens of every longer
         sequence (see evict_tokens) and returns the blocks past them to the
         pool.  Blocks that will be written are copied first where they are
-        shared.  Returns the number of blocks freed."""
+        shared (OutOfBlocks if the pool has no room for that: nothing is
+        evicted then).  Returns the number of blocks freed."""
         over = [s for s in range(self.S) if self.context_lens_host[s] > budget]
-        pairs = [self.allocator.unshare(self.tables_host[s],
-                                        min(-(-budget // self.bs), int(self.nblocks_host[s])))
-                 for s in over]
-        pairs = np.concatenate(pairs) if pairs else np.empty((0, 2), dtype=np.int64)
-        if len(pairs):
-            check_copy_pairs(pairs, self.NB)
-            self.block_tables = torch.from_numpy(self.tables_host).to(self.device)
-            copy_blocks(self.k_cache, self.v_cache, torch.from_numpy(pairs).to(self.device), stream)
+        pairs = []
+        try:
+            for s in over:
+                n = min(-(-budget // self.bs), int(self.nblocks_host[s]))
+                pairs.append(self.allocator.unshare(self.tables_host[s], n))
+        finally:  # rows that own their blocks now need the contents, also when the pool ran out
+            pairs = np.concatenate(pairs) if pairs else np.empty((0, 2), dtype=np.int64)
+            if len(pairs):
+                check_copy_pairs(pairs, self.NB)
+                self.block_tables = torch.from_numpy(self.tables_host).to(self.device)
+                copy_blocks(self.k_cache, self.v_cache, torch.from_numpy(pairs).to(self.device),
+                            stream)
         new_lens = torch.empty_like(self.context_lens)
         evict_tokens(self.k_cache, self.v_cache, self.scores, self.positions, self.block_tables,
                      self.context_lens, self.token_counts, new_lens, budget, recent_tokens,

@@ -141,6 +141,8 @@ def test_decode_step_methods():
     """DecodeStep: accumulate, evict with shared prompt blocks (copied first),
     decode what is left; the other sequences' blocks are unchanged."""
     w = W.shared_prefix(seed=9, prompts=2, samples=3, prefix=160, tail_lo=1, tail_hi=60, H=4, D=64)
+    more = np.arange(w.NB, w.NB + 40, dtype=np.int32)      # room to copy the shared blocks
+    w.initial_free, w.NB = np.concatenate([more, w.initial_free]), w.NB + 40
     st = device_step(w)
     st.plan()
     st.run()
@@ -164,7 +166,7 @@ def test_decode_step_methods():
     held = [set(t[:n].tolist()) for t, n in zip(st.tables_host, st.nblocks_host)]
     assert all(len(h) == -(-budget // bs) for h in held)
     assert sum(len(h) for h in held) == len(set().union(*held)), "evicted rows own their blocks"
-    assert freed > 0 and st.allocator.num_free + sum(len(h) for h in held) + (w.NB - free) >= free
+    assert freed > 0 and st.allocator.num_free + sum(len(h) for h in held) == w.NB
     ref = np.zeros((S, 4, 64))
     q = st.q.double().cpu().numpy()
     for s in range(S):
@@ -179,3 +181,23 @@ def test_decode_step_methods():
     st.decode()
     close(st.out, ref, "after eviction")
     assert L.pkv_get_device_errors() == 0
+
+
+def test_evict_without_room_for_the_shared_blocks_leaves_a_valid_step():
+    """OutOfBlocks from copy-on-write: blocks copied so far are the rows' own,
+    with their contents, and decoding gives what it gave."""
+    w = W.shared_prefix(seed=9, prompts=2, samples=3, prefix=160, tail_lo=1, tail_hi=60, H=4, D=64)
+    st = device_step(w)
+    st.plan()
+    st.run()
+    want = st.out.clone()
+    st.decode_accumulate()
+    lens = st.context_lens_host.copy()
+    with pytest.raises(L.PkvError) as e:
+        st.evict(96, 20, 4)
+    assert e.value.status == L.PKV_ERR_OOM
+    assert np.array_equal(st.context_lens_host, lens)
+    st.out.zero_()
+    st.decode()
+    assert torch.equal(st.out.view(torch.int16), want.view(torch.int16))
+    assert np.array_equal(st.block_tables.cpu().numpy(), st.tables_host)
