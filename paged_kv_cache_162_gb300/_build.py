@@ -1,4 +1,5 @@
-"""Builds libpagedkv.so in-tree for sm_103a (nvcc, no cmake).
+"""Builds libpagedkv.so in-tree for sm_103a (nvcc, no cmake), and
+_tensor_bind.so, which calls it with torch tensors (g++ against torch).
 
 Each translation unit compiles in parallel; the link uses the shared CUDA
 runtime so the library and PyTorch share one runtime in a process.
@@ -20,10 +21,12 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
+BIND = os.path.join(PKG, "_tensor_bind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CU_SOURCES = ["runtime.cu", "cache_ops.cu", "decode.cu", "bounded.cu", "evict.cu"]
 CXX_SOURCES = ["allocator.cpp", "beam_step.cpp"]
+BIND_SOURCE = "tensor_bind.cpp"
 
 
 def cuda_home() -> str:
@@ -56,18 +59,33 @@ def _defines() -> list[str]:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return False
     built = open(FLAGS).read() if os.path.exists(FLAGS) else ""
     if built != " ".join(_defines()):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     return all(os.path.getmtime(p) <= t for p in _inputs())
+
+
+def _torch_flags():
+    """(compile, link) flags against the torch that will load the module."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(root, "lib")
+    return ([f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             *[x for p in inc for x in ("-isystem", p)]],
+            ["-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"])
 
 
 def _compile(src: str, extra: list[str]) -> str:
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
     inc = ["-I", INCLUDE, "-I", CSRC]
+    if os.path.basename(src) == BIND_SOURCE:
+        inc += _torch_flags()[0]
     if src.endswith(".cu"):
         cmd = [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                "-Xptxas", "-warn-spills", *inc, *extra, "-c", src, "-o", obj]
@@ -88,17 +106,22 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     extra = (["-Xptxas", "-v"] if verbose_ptxas else []) + _defines()
-    srcs = [os.path.join(CSRC, s) for s in CU_SOURCES + CXX_SOURCES]
+    srcs = [os.path.join(CSRC, s) for s in [BIND_SOURCE] + CU_SOURCES + CXX_SOURCES]
     with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-    tmp = LIB + f".tmp{os.getpid()}"
+    bind, objs = objs[0], objs[1:]
     libdir = os.path.join(cuda_home(), "lib64")
-    cmd = [_nvcc(), *ARCH, "-shared", "-cudart", "shared", *objs, "-o", tmp,
-           "-Xlinker", f"-rpath,{libdir}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+    for out, cmd in (
+            (LIB, [_nvcc(), *ARCH, "-shared", "-cudart", "shared", *objs,
+                   "-Xlinker", f"-rpath,{libdir}"]),
+            (BIND, ["g++", "-shared", bind, "-L", PKG, "-l:libpagedkv.so", "-Wl,-rpath,$ORIGIN",
+                    *_torch_flags()[1]])):
+        tmp = out + f".tmp{os.getpid()}"
+        cmd = [*cmd, "-o", tmp]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, out)
     with open(FLAGS, "w") as f:
         f.write(" ".join(_defines()))
     return LIB

@@ -1157,7 +1157,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const __grid_cons
             const int2 at = p.place[i / rows];
             if (at.x == at.y) continue;  // the same for the whole CTA
             float M, L, o[DPL];
-            gather_row<D, 8>(p, at.x, at.x + warp, at.y, kJoinWarps, i % rows, lane, M, L, o);
+            gather_row<D, 6>(p, at.x, at.x + warp, at.y, kJoinWarps, i % rows, lane, M, L, o);
             if (lane == 0) {
                 s_m[warp] = M;
                 s_l[warp] = L;
@@ -1190,7 +1190,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const __grid_cons
                 const int i = base + src * warps;
                 const int c0 = __shfl_sync(kFull, at.x, src), c1 = __shfl_sync(kFull, at.y, src);
                 float M, L, o[DPL];
-                gather_row<D, 4>(p, c0, c0, c1, 1, i % rows, lane, M, L, o);
+                gather_row<D, 2>(p, c0, c0, c1, 1, i % rows, lane, M, L, o);
                 write_row<E, D>(p, i / rows, i % rows, lane, L, o);
             }
         }

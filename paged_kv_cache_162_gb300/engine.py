@@ -119,6 +119,21 @@ def paged_attention_decode_shared_prefix(out, q, k_cache, v_cache, block_tables,
     return out
 
 
+_bind = None
+
+
+def _native():
+    """The module that calls the library with tensors (csrc/tensor_bind.cpp).
+    Its functions answer with the call's status, or -1 for arguments that it
+    leaves to the checks and the ctypes call below."""
+    global _bind
+    if _bind is None:
+        L.lib()
+        from . import _tensor_bind
+        _bind = _tensor_bind
+    return _bind
+
+
 def _refuse(what: str):
     raise L.PkvError(L.PKV_ERR_INVALID_ARG, what)
 
@@ -215,6 +230,13 @@ def paged_attention_decode_window(out, q, k_cache, v_cache, block_tables, contex
     workspace: new_window_workspace(S, H, Hkv, D), kept between calls.
     """
     who = "paged_attention_decode_window"
+    if stream is None and workspace is not None:
+        st = _native().window(out, q, k_cache, v_cache, block_tables, context_lens, window,
+                              sink_tokens, scale, max_context_len, workspace)
+        if st == 0:
+            return out
+        if st > 0:
+            L.check(st, who)
     S, H, D, NB, bs, Hkv, MB, dev = _attention_sizes(who, out, q, k_cache, v_cache, block_tables,
                                                      context_lens)
     ws = workspace
@@ -249,6 +271,13 @@ def paged_attention_decode_accumulate(out, scores, q, k_cache, v_cache, block_ta
     paged_attention_decode_window; workspace: new_accumulate_workspace(S, H,
     Hkv, D, max_context_len)."""
     who = "paged_attention_decode_accumulate"
+    if stream is None and workspace is not None:
+        st = _native().accumulate(out, scores, q, k_cache, v_cache, block_tables, context_lens,
+                                  scale, max_context_len, workspace)
+        if st == 0:
+            return out
+        if st > 0:
+            L.check(st, who)
     S, H, D, NB, bs, Hkv, MB, dev = _attention_sizes(who, out, q, k_cache, v_cache, block_tables,
                                                      context_lens)
     rows = scores.shape
@@ -296,14 +325,22 @@ def evict_tokens(k_cache, v_cache, scores, positions, block_tables, context_lens
     their own (BlockAllocator.unshare); afterwards BlockAllocator.truncate
     releases the blocks past the budget."""
     who = "evict_tokens"
-    if k_cache.dim() != 4 or block_tables.dim() != 2:
-        _refuse(f"{who}: the caches must be [NB, bs, Hkv, D], block_tables [S, MB]")
-    NB, bs, Hkv, D = k_cache.shape
-    S, MB = block_tables.shape
     if scores_out is None:
         scores_out = scores
     if positions_out is None:
         positions_out = positions
+    if stream is None and workspace is not None:
+        st = _native().evict(k_cache, v_cache, scores, positions, block_tables, context_lens,
+                             token_counts, new_context_lens, budget, recent_tokens, sink_tokens,
+                             scores_out, positions_out, max_context_len, workspace)
+        if st == 0:
+            return
+        if st > 0:
+            L.check(st, who)
+    if k_cache.dim() != 4 or block_tables.dim() != 2:
+        _refuse(f"{who}: the caches must be [NB, bs, Hkv, D], block_tables [S, MB]")
+    NB, bs, Hkv, D = k_cache.shape
+    S, MB = block_tables.shape
     dt, dev = k_cache.dtype, k_cache.get_device()
     rows = scores.shape
     if not (dev >= 0 and len(rows) == 3 and rows[0] == S and rows[1] == Hkv and v_cache.dtype is dt
