@@ -677,44 +677,60 @@ __device__ __forceinline__ void fold_weights(const Params& p, int s, int kvh, in
     }
 }
 
-// Joins the CTAs of a cluster that share a unit (hw = 1): every CTA leaves its
-// rows in shared memory, then the rows are dealt out over the cluster's warps,
-// and each CTA folds its own tokens [tb, te) into the scores.
+// What the CTAs of a cluster send one another: 32 dims of a row ("segment") of
+// every CTA to the CTA that joins it, and every row's M and L to all.
+struct ClusterIn {
+    float o[kMaxGroup * 4 * 32];                 // [segment / CS][CTA][32]
+    float m[kMaxCluster][kMaxGroup], l[kMaxCluster][kMaxGroup];
+};
+
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Joins the CTAs of a cluster that share a unit: every CTA writes its rows (warp
+// 0 has them) into the memory of the CTAs that join them, segment i to CTA
+// i % CS; after one barrier each joins what it was sent, and folds its own
+// tokens [tb, te) into the scores.  No CTA reads another's memory, so none has
+// to stay for that.  The caller has arrived once at the cluster's barrier: the
+// wait for it says that all CTAs run.
 template <class E, int D, bool kWide, bool kScores>
 __device__ __forceinline__ void join_cluster(const Params& p, int s, int kvh, int n, int tb, int te,
-                                             float* mem, int warp, int lane, const Acc<D>& a,
+                                             ClusterIn* in, int warp, int lane, const Acc<D>& a,
                                              float* s_m, float* s_inv) {
-    constexpr int NO = D / 8, R = kWide ? 2 : 1, DPL = D / 32;
+    constexpr int NO = D / 8, R = kWide ? 2 : 1, SEGS = D / 32;
     cg::cluster_group cluster = cg::this_cluster();
     const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int g = lane >> 2, t = lane & 3, tid = warp * 32 + lane;
-    float* rows = mem;                      // [G][D]
-    float* ml = mem + kMaxGroup * D;        // [2][16]
+    cluster_wait();
     if (warp == 0) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int row = g + 8 * r;
             if (row < p.G) {
 #pragma unroll
-                for (int j = 0; j < NO; ++j)
-                    *reinterpret_cast<float2*>(rows + row * D + 8 * j + 2 * t) =
-                        make_float2(a.o[j][2 * r], a.o[j][2 * r + 1]);
-                if (t == 0) {
-                    ml[row] = a.m[r];
-                    ml[kMaxGroup + row] = a.l[r];
+                for (int j = 0; j < NO; ++j) {
+                    const int seg = row * SEGS + j / 4;
+                    float* to = cluster.map_shared_rank(&in->o[0], seg % CS) + (seg / CS * CS + rank) * 32 +
+                                8 * (j % 4) + 2 * t;
+                    *reinterpret_cast<float2*>(to) = make_float2(a.o[j][2 * r], a.o[j][2 * r + 1]);
+                }
+                for (int c = t; c < CS; c += 4) {
+                    cluster.map_shared_rank(&in->m[rank][0], c)[row] = a.m[r];
+                    cluster.map_shared_rank(&in->l[rank][0], c)[row] = a.l[r];
                 }
             }
         }
     }
-    cluster.sync();
-    // M and L of a row: lane i reads CTA i's
+    cluster_arrive();
+    cluster_wait();
+    // M and 1 / L of a row, and lane i's weight 2^(m_i - M) for CTA i
     auto row_of = [&](int row, float& M, float& w, float& inv) {
-        float m = -INFINITY, l = 0.f;
-        if (lane < CS) {
-            const float* other = cluster.map_shared_rank(ml, lane);
-            m = other[row];
-            l = other[kMaxGroup + row];
-        }
+        const float m = lane < CS ? in->m[lane][row] : -INFINITY;
+        const float l = lane < CS ? in->l[lane][row] : 0.f;
         M = m;
 #pragma unroll
         for (int o = kMaxCluster / 2; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
@@ -726,34 +742,16 @@ __device__ __forceinline__ void join_cluster(const Params& p, int s, int kvh, in
         L = __shfl_sync(kFull, L, 0);
         inv = L > 0.f || L != L ? 1.f / L : 0.f;
     };
-    for (int row = rank * kWarps + warp; row < p.G; row += CS * kWarps) {
-        float M, w, inv;
+    for (int k = warp; k * CS + rank < p.G * SEGS; k += kWarps) {
+        const int seg = k * CS + rank, row = seg / SEGS;
+        float M, w, inv, o = 0.f;
         row_of(row, M, w, inv);
-        float o[DPL];
-#pragma unroll
-        for (int j = 0; j < DPL; ++j) o[j] = 0.f;
-#pragma unroll
-        for (int i = 0; i < kMaxCluster; ++i) {
-            if (i < CS) {
-                const float wi = __shfl_sync(kFull, w, i);
-                const float* src = cluster.map_shared_rank(rows, i) + row * D + lane * DPL;
-                float v[DPL];
-                if constexpr (DPL == 4) {
-                    const float4 x = *reinterpret_cast<const float4*>(src);
-                    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-                } else {
-                    const float2 x = *reinterpret_cast<const float2*>(src);
-                    v[0] = x.x; v[1] = x.y;
-                }
-#pragma unroll
-                for (int j = 0; j < DPL; ++j) o[j] = fmaf(wi, v[j], o[j]);
-            }
-        }
+        for (int i = 0; i < CS; ++i) o = fmaf(__shfl_sync(kFull, w, i), in->o[(k * CS + i) * 32 + lane], o);
+        o *= inv;
+        const float next = __shfl_down_sync(kFull, o, 1);
         uint16_t* dst = static_cast<uint16_t*>(p.out) +
-                        ((int64_t)s * p.H + (int64_t)kvh * p.G + row) * D + lane * DPL;
-#pragma unroll
-        for (int j = 0; j < DPL; j += 2)
-            *reinterpret_cast<uint32_t*>(dst + j) = E::from_float2(o[j] * inv, o[j + 1] * inv);
+                        ((int64_t)s * p.H + (int64_t)kvh * p.G + row) * D + seg % SEGS * 32 + lane;
+        if ((lane & 1) == 0) *reinterpret_cast<uint32_t*>(dst) = E::from_float2(o, next);
     }
     if constexpr (kScores) {
         for (int row = warp; row < p.G; row += kWarps) {
@@ -767,7 +765,6 @@ __device__ __forceinline__ void join_cluster(const Params& p, int s, int kvh, in
         __syncthreads();
         fold_weights(p, s, kvh, tb * kTile, min(te * kTile, n), s_m, s_inv, tid, kThreads);
     }
-    cluster.sync();  // no CTA leaves while another reads its rows
 }
 
 // Writes the finished rows of a unit (the warp's part of the accumulators).
@@ -799,6 +796,8 @@ __global__ void __launch_bounds__(kThreads, 2) direct_kernel(const __grid_consta
     asm volatile("griddepcontrol.launch_dependents;");
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float s_m[kMaxGroup], s_inv[kMaxGroup];
+    __shared__ ClusterIn in;
+    if (p.cs > 1) cluster_arrive();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int unit = blockIdx.x / p.cs, rank = blockIdx.x % p.cs;
     const int s = unit / p.Hkv, kvh = unit % p.Hkv;
@@ -816,8 +815,7 @@ __global__ void __launch_bounds__(kThreads, 2) direct_kernel(const __grid_consta
     cp_async_wait<0>();
     join_splits<D>(p, reinterpret_cast<float*>(smem), warp, lane, a);
     if (p.cs > 1) {
-        join_cluster<E, D, kWide, kScores>(p, s, kvh, n, tb, te, reinterpret_cast<float*>(smem), warp,
-                                           lane, a, s_m, s_inv);
+        join_cluster<E, D, kWide, kScores>(p, s, kvh, n, tb, te, &in, warp, lane, a, s_m, s_inv);
         return;
     }
     if (warp == 0) write_rows<E, D, kWide>(p, s, kvh, lane, a);

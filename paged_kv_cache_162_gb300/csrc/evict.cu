@@ -110,8 +110,12 @@ __device__ __forceinline__ void store4(T* p, int count, bool vec, const T (&v)[4
     }
 }
 
-template <int D, bool kCluster>
-__global__ void __launch_bounds__(kThreads, 5) evict_kernel(Params p) {
+// kMinCtas: CTAs per SM the registers allow.  Five (48 registers) where rows
+// wait for a place on the card: more of the moves are in flight (256 mixed
+// requests: 219 us, with four 236).  Four (64) where all rows have one: a row is
+// done sooner (64 requests in steady state: 12.0 us, with five 13.9).
+template <int D, bool kCluster, int kMinCtas>
+__global__ void __launch_bounds__(kThreads, kMinCtas) evict_kernel(Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     extern __shared__ __align__(16) uint32_t s_keys[];
@@ -355,8 +359,11 @@ __global__ void __launch_bounds__(kThreads, 5) evict_kernel(Params p) {
     int mover0 = before.gt_back + min(want, ties0) - kept_front(before.eq_front);
     const int all_movers = all.gt_back + min(want, all.eq_front + all.eq_back) - kept_front(all.eq_front);
 
-    int32_t* hole_list = p.holes + (int64_t)row * b;
-    int32_t* mover_list = p.movers + (int64_t)row * b;
+    // the lists: in the histograms' memory where they fit
+    constexpr int kListRoom = BINS;  // one histogram each
+    const bool lists_here = !kCluster && all_movers <= kListRoom;
+    int32_t* hole_list = lists_here ? &s_hist[0][0] : p.holes + (int64_t)row * b;
+    int32_t* mover_list = lists_here ? &s_hist[1][0] : p.movers + (int64_t)row * b;
     int seen = ties0;
     for (int base = w0; base < w1; base += kChunk) {
         const int j = base + 4 * lane;
@@ -472,10 +479,15 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 size_t list_bytes(int S, int Hkv, int budget) { return align256((size_t)S * Hkv * budget * sizeof(int32_t)); }
 
+template <int D, int kMinCtas>
+void (*pick(int cs))(Params) {
+    return cs > 1 ? evict_kernel<D, true, kMinCtas> : evict_kernel<D, false, kMinCtas>;
+}
+
 // Allows the kernel its shared memory (once per device).
 bool ready(void (*fn)(Params), int smem) {
     static std::mutex mu;
-    static struct { void (*fn)(Params); int dev; } done[16];
+    static struct { void (*fn)(Params); int dev; } done[128];
     static int used = 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -489,7 +501,7 @@ bool ready(void (*fn)(Params), int smem) {
         cudaGetLastError();
         return false;
     }
-    if (used < 16) done[used++] = {fn, dev};
+    if (used < 128) done[used++] = {fn, dev};
     return true;
 }
 
@@ -576,8 +588,9 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
         cs *= 2;
     const int seg = ((p.max_ctx + cs - 1) / cs + kChunk - 1) / kChunk * kChunk;
     p.seg_cap = seg < kSmemKeys ? seg : kSmemKeys;
-    void (*fn)(Params) = cs > 1 ? (D == 128 ? evict_kernel<128, true> : evict_kernel<64, true>)
-                                : (D == 128 ? evict_kernel<128, false> : evict_kernel<64, false>);
+    const bool wait = rows * cs > 4 * pkv::sm_count();
+    void (*fn)(Params) = D == 128 ? (wait ? pick<128, 5>(cs) : pick<128, 4>(cs))
+                                  : (wait ? pick<64, 5>(cs) : pick<64, 4>(cs));
     if (!ready(fn, kSmemKeys * 4)) return pkv::fail(PKV_ERR_CUDA, "evict_tokens: shared memory");
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
