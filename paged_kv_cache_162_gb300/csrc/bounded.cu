@@ -66,7 +66,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;
 constexpr int kMaxRanges = 1536;   // CTAs of a split call
-constexpr int kMinRange = 8;       // tiles, more than any ring holds
+constexpr int kMinRange = 8;       // tiles of a large range
+constexpr int kMinSmall = 4;       // and of a small one: a ring is at most two ranges ahead
 constexpr int kMaxGroup = 16;      // query heads per KV head
 constexpr int kMaxCluster = 16;    // CTAs that share a unit in a direct call
 constexpr unsigned kFull = 0xffffffffu;
@@ -125,8 +126,9 @@ __device__ __forceinline__ int tiles_of(const Params& p, int n) {
 
 // How the tiles of a split call are cut: slots of one large range and `n_small`
 // small ones after it, so that a unit has about as many pieces wherever it
-// lies; kLargeShare / 16 of the tiles are in large ranges.  Ranges are numbered
-// by place; CTAs are launched for the large ones first.
+// lies; kLargeShare / 16 of the tiles are in large ranges (all, where the small
+// ones would be shorter than kMinSmall).  Ranges are numbered by place; CTAs are
+// launched for the large ones first.
 constexpr int kLargeShare = 14;
 constexpr int kSmallRanges = 2;    // per large one
 
@@ -137,11 +139,15 @@ struct RangeMap {
         total = total_;
         n_large = p.ranges0;
         n_small = p.ranges / p.ranges0 - 1;
-        const long long in_large = n_small > 0 ? total * kLargeShare / 16 : total;
-        large = max((long long)kMinRange, (in_large + n_large - 1) / n_large);
-        const long long per = (total + n_large - 1) / n_large;
-        small = n_small > 0 ? max((long long)kMinRange, (per - large + n_small - 1) / n_small) : 0;
-        slot = large + n_small * small;
+        const long long per = max((long long)kMinRange, (total + n_large - 1) / n_large);
+        large = per;
+        small = 0;
+        if (n_small > 0) {
+            small = per * (16 - kLargeShare) / 16 / n_small;
+            if (small < kMinSmall) small = 0;  // too little to share out: one range each
+            large = per - n_small * small;
+        }
+        slot = per;
     }
     // the range of the id-th CTA launched
     __device__ __forceinline__ int of_cta(int id) const {
@@ -1411,8 +1417,11 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     if (per_sm < 1) return bad(PKV_ERR_CUDA, "the kernel cannot be resident");
     p.ranges0 = per_sm * sms;
     if (p.ranges0 > kMaxRanges / (1 + kSmallRanges)) p.ranges0 = kMaxRanges / (1 + kSmallRanges);
-    // small ranges only where changing over costs nothing (a warp per head)
-    p.ranges = p.nsplit == 1 ? p.ranges0 * (1 + kSmallRanges) : p.ranges0;
+    // small ranges only where changing over costs nothing (a warp per head), and
+    // where contexts at their bound would have some
+    const int64_t most_tiles = (int64_t)S * p.HB * ((most + kTile - 1) / kTile);
+    const bool share = p.nsplit == 1 && most_tiles / p.ranges0 * (16 - kLargeShare) / 16 / kSmallRanges >= kMinSmall;
+    p.ranges = share ? p.ranges0 * (1 + kSmallRanges) : p.ranges0;
 
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -359,11 +359,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) evict_kernel(Params p) {
     int mover0 = before.gt_back + min(want, ties0) - kept_front(before.eq_front);
     const int all_movers = all.gt_back + min(want, all.eq_front + all.eq_back) - kept_front(all.eq_front);
 
-    // the lists: in the histograms' memory where they fit
-    constexpr int kListRoom = BINS;  // one histogram each
-    const bool lists_here = !kCluster && all_movers <= kListRoom;
-    int32_t* hole_list = lists_here ? &s_hist[0][0] : p.holes + (int64_t)row * b;
-    int32_t* mover_list = lists_here ? &s_hist[1][0] : p.movers + (int64_t)row * b;
+    int32_t* hole_list = p.holes + (int64_t)row * b;
+    int32_t* mover_list = p.movers + (int64_t)row * b;
     int seen = ties0;
     for (int base = w0; base < w1; base += kChunk) {
         const int j = base + 4 * lane;
