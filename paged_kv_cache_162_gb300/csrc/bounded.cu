@@ -974,21 +974,6 @@ __device__ __forceinline__ void merge_ml(float& M, float& L, float m, float l) {
     M = m_new;
 }
 
-// M and L of one row over the pieces of a cut unit, ranges c0 .. c1, by the
-// whole warp.
-__device__ __forceinline__ void join_row(const Params& p, int c0, int c1, int hl, int row, int lane,
-                                         float& M, float& L) {
-    M = -INFINITY;
-    L = 0.f;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-        const int64_t at = piece_row(p, c, c0, hl, row);
-        merge_ml(M, L, p.part_m[at], p.part_l[at]);
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-        merge_ml(M, L, __shfl_xor_sync(kFull, M, o), __shfl_xor_sync(kFull, L, o));
-}
-
 __device__ __forceinline__ float inverse_of(float L) { return L > 0.f || L != L ? 1.f / L : 0.f; }
 
 // Row i of a unit's hw * G over the pieces c, c + step, ... <= c1 (c0: the range
@@ -1046,6 +1031,69 @@ __device__ __forceinline__ void write_row(const Params& p, int unit, int i, int 
         *reinterpret_cast<uint32_t*>(dst + j) = E::from_float2(o[j] * inv, o[j + 1] * inv);
 }
 
+// M and 1 / L of query head `lane` (< G) of a KV head, by one warp: h0 its first
+// query head in row_m and row_l, `place` the ranges of its unit, hl the head in
+// it.  All loads of a round go out together.
+__device__ __forceinline__ void group_ml(const Params& p, int64_t h0, int2 place, int hl, int lane,
+                                         float& M, float& inv) {
+    const int pieces = place.y - place.x + 1;
+    float L = 0.f;
+    M = -INFINITY;
+    if (pieces == 1) {
+        if (lane < p.G) {
+            M = p.row_m[h0 + lane];
+            L = p.row_l[h0 + lane];
+        }
+    } else if (pieces <= 4) {  // four lanes per head, eight heads per round
+        for (int r0 = 0; r0 < p.G; r0 += 8) {
+            const int row = r0 + lane / 4, c = place.x + lane % 4;
+            float m = -INFINITY, l = 0.f;
+            if (row < p.G && c <= place.y) {
+                const int64_t at = piece_row(p, c, place.x, hl, row);
+                m = p.part_m[at];
+                l = p.part_l[at];
+            }
+#pragma unroll
+            for (int o = 1; o <= 2; o <<= 1)
+                merge_ml(m, l, __shfl_xor_sync(kFull, m, o), __shfl_xor_sync(kFull, l, o));
+            const float mr = __shfl_sync(kFull, m, 4 * (lane & 7)), lr = __shfl_sync(kFull, l, 4 * (lane & 7));
+            if (lane / 8 == r0 / 8) {
+                M = mr;
+                L = lr;
+            }
+        }
+    } else {  // the warp on four heads per round
+        for (int r0 = 0; r0 < p.G; r0 += 4) {
+            float m[4], l[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                m[r] = -INFINITY;
+                l[r] = 0.f;
+            }
+            for (int c = place.x + lane; c <= place.y; c += 32) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (r0 + r < p.G) {
+                        const int64_t at = piece_row(p, c, place.x, hl, r0 + r);
+                        merge_ml(m[r], l[r], p.part_m[at], p.part_l[at]);
+                    }
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    merge_ml(m[r], l[r], __shfl_xor_sync(kFull, m[r], o), __shfl_xor_sync(kFull, l[r], o));
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (lane == r0 + r) {
+                    M = m[r];
+                    L = l[r];
+                }
+        }
+    }
+    inv = inverse_of(L);
+}
+
 // Adds the weights of tokens j0 + 4 (32 u + lane) .. + 3, u < RUNS, of KV head
 // kvh of sequence s to their scores, by one warp; `place`: the ranges its unit
 // begins and ends in, hl: the head in it.  z of the first HEADS query heads and
@@ -1074,33 +1122,8 @@ __device__ __forceinline__ void fold_stretch(const Params& p, int s, int kvh, in
             for (int e = 0; e < 4; ++e) old[u][e] = j + e < n ? sc[j + e] : 0.f;
         }
     }
-    // M and 1 / L of query head r in lane r
-    float M = 0.f, inv = 0.f;
-    if (place.x == place.y) {
-        if (lane < p.G) {
-            M = p.row_m[h0 + lane];
-            inv = inverse_of(p.row_l[h0 + lane]);
-        }
-    } else if (place.y - place.x < 4) {  // few pieces: a lane per head
-        if (lane < p.G) {
-            float L = 0.f;
-            M = -INFINITY;
-            for (int c = place.x; c <= place.y; ++c) {
-                const int64_t at = piece_row(p, c, place.x, hl, lane);
-                merge_ml(M, L, p.part_m[at], p.part_l[at]);
-            }
-            inv = inverse_of(L);
-        }
-    } else {
-        for (int r = 0; r < p.G; ++r) {
-            float m, l;
-            join_row(p, place.x, place.y, hl, r, lane, m, l);
-            if (lane == r) {
-                M = m;
-                inv = inverse_of(l);
-            }
-        }
-    }
+    float M, inv;
+    group_ml(p, h0, place, hl, lane, M, inv);
 #pragma unroll
     for (int u = 0; u < RUNS; ++u) {
         const int j = j0 + 4 * (32 * u + lane);
