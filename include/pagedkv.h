@@ -251,6 +251,13 @@ pkv_status pkv_paged_attention_decode_noalloc(
  * above); query head h uses KV head h / (H / Hkv).  The caches are then
  * [NB][bs][Hkv][D], as pkv_reshape_and_cache and pkv_copy_blocks lay them
  * out for H = Hkv.  NB * bs must fit 31 bits; S at most 32767.
+ *
+ * The calls may be captured in a graph; make the first call on a device
+ * before a capture begins.  max_context_len decides how work is spread (a
+ * bound far above the lengths costs some microseconds), so equal inputs give
+ * equal bits for equal bounds.  A wait inside the attention kernels is bounded;
+ * one that runs out sets PKV_DEVERR_TIMEOUT, and the call's results are not
+ * valid.
  * ------------------------------------------------------------------ */
 
 /* Bytes of workspace for pkv_paged_attention_decode_window (0 for invalid
@@ -273,8 +280,8 @@ size_t pkv_decode_window_workspace_size(int S, int H, int Hkv, int D);
  *   other arguments as in pkv_paged_attention_decode.
  * Computation is fp32; attention weights enter P.V as the sum of two 16-bit
  * numbers (relative error 2^-16 at most for bf16); one rounding to dtype at
- * the end.  Equal inputs give equal bits.  A visible V element that is not
- * finite makes its output elements not finite. */
+ * the end.  A visible V element that is not finite makes its output elements
+ * not finite. */
 pkv_status pkv_paged_attention_decode_window(
     void* out, const void* q, const void* k_cache, const void* v_cache,
     const int32_t* block_tables, const int32_t* context_lens,
@@ -300,7 +307,7 @@ size_t pkv_decode_accumulate_workspace_size(int S, int H, int Hkv, int D, int ma
  *   max_context_len  upper bound of context_lens (0 = MB*bs); sizes the
  *                 workspace
  *   other arguments as in pkv_paged_attention_decode_window.  Each score is
- *   added to by one thread in a fixed order: equal inputs give equal bits. */
+ *   added to by one thread in a fixed order. */
 pkv_status pkv_paged_attention_decode_accumulate(
     void* out, float* scores, const void* q, const void* k_cache, const void* v_cache,
     const int32_t* block_tables, const int32_t* context_lens,

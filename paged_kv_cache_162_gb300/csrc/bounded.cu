@@ -23,7 +23,9 @@
 //   P as the sum of two 16-bit numbers (its rounding and the rest): P rounded
 //   once would add an error as large as the output's own rounding.
 // A CTA is four warps: hw heads times 4 / hw token splits, joined in shared
-// memory.
+// memory.  The four read neighbouring data (1 KB of each token row, or 64
+// tokens of one head); a range of its own per warp was slower (window of 64 MHA
+// requests 146 us against 132), a barrier to keep them together no faster.
 //
 // Two ways to spread the units:
 //  * direct: one CTA, or one cluster of CTAs that share the unit's tokens, per
@@ -39,6 +41,19 @@
 //    lengths on the device by every CTA: a call needs no plan kernel, no counter
 //    and no ticket, and as the cuts do not depend on who does which range,
 //    every sum has a fixed order.
+//
+// Measured on GB300 (device time, share of the measured copy rate of 6776 GB/s):
+//   window 1000 + 4 sinks, 64 requests of 128..2048, 32 heads, fp16   128 us  97 %
+//   window 4093 + 7, 96 requests, 32 heads on 8, bf16                 240 us  99 %
+//   accumulate, the 64 requests whole                                 186 us  92 %
+//   accumulate, 8 x 32768                                         657-668 us  97 %
+//   accumulate, 256 requests of 16..4096 (median 512), 32 heads on 8  160 us  79 %
+//   window 4096 of one 32768-token context, 32 heads on 8            8.7 us  29 %
+//   4 requests of at most 100 tokens, 4 heads of 64       2.9 us, with scores 4.1
+// The split kernel reads each byte once (843.9 MB for 843.4) at 84 % of the DRAM
+// peak with its tensor pipe 28 % busy.  About 4 us go before every ring is full
+// (length -> place -> table -> rows), 3 to the last ranges; the second kernel takes
+// 4 us without scores and 12 to 20 with them.  The small calls are that chain.
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -124,7 +139,8 @@ __device__ __forceinline__ int tiles_of(const Params& p, int n) {
     return t < 1 ? 1 : t;
 }
 
-// How the tiles of a split call are cut: slots of one large range and `n_small`
+// How the tiles of a split call are cut (equal ranges alone: the SMs' rates differ
+// and the slowest ended 10 % after the median): slots of one large range and `n_small`
 // small ones after it, so that a unit has about as many pieces wherever it
 // lies; kLargeShare / 16 of the tiles are in large ranges (all, where the small
 // ones would be shorter than kMinSmall).  Ranges are numbered by place; CTAs are
@@ -1230,21 +1246,13 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const __grid_cons
         // item (stretch, sequence, KV head): the first stretches of all first
         for (long long base = w0; base < items; base += 32LL * warps) {
             const long long mine = base + (long long)lane * warps;
-            int u = 0, st = 0, n = 0;
-            int2 place = make_int2(0, 0);
-            if (mine < items) {
-                st = (int)(mine / heads);
-                u = (int)(mine % heads);
-                n = context_of(p, u / p.Hkv);
-                place = p.place[u / p.hw];
-            }
-            for (unsigned todo = __ballot_sync(kFull, st * TOKENS < n); todo; todo &= todo - 1) {
-                const int src = __ffs(todo) - 1;
-                const int unit = __shfl_sync(kFull, u, src), stretch = __shfl_sync(kFull, st, src);
-                const int len = __shfl_sync(kFull, n, src);
-                const int2 at = make_int2(__shfl_sync(kFull, place.x, src), __shfl_sync(kFull, place.y, src));
-                const int kvh = unit % p.Hkv;
-                fold_stretch<RUNS, HEADS>(p, unit / p.Hkv, kvh, kvh % p.hw, len, at, stretch * TOKENS, lane);
+            bool live = false;
+            if (mine < items) live = (int)(mine / heads) * TOKENS < context_of(p, (int)(mine % heads) / p.Hkv);
+            for (unsigned todo = __ballot_sync(kFull, live); todo; todo &= todo - 1) {
+                const long long item = base + (long long)(__ffs(todo) - 1) * warps;
+                const int unit = (int)(item % heads), kvh = unit % p.Hkv;
+                fold_stretch<RUNS, HEADS>(p, unit / p.Hkv, kvh, kvh % p.hw, context_of(p, unit / p.Hkv),
+                                          p.place[unit / p.hw], (int)(item / heads) * TOKENS, lane);
             }
         }
     }
@@ -1253,8 +1261,10 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const __grid_cons
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-// Visible tokens of a direct call per CTA, and its CTAs in multiples of the
-// resident ones.
+// Direct calls: visible tokens per CTA at most, and CTAs in multiples of the
+// resident ones.  16 requests of 2000 tokens, 8 KV heads: direct 26.5 us, split
+// 32.2; 256 requests of 500: direct 90, split 87; a longer share per CTA (2048) loses
+// where few CTAs run (one 32768-token context, scores: 48 us against 36).
 constexpr int kDirectTokens = 1024;
 constexpr int kDirectWaves = 2;
 constexpr int kJoinCtasPerSm = 3;   // of the join kernel

@@ -20,8 +20,18 @@
 //
 // One cluster of 1..8 CTAs per (s, h): each CTA holds a stretch of the row,
 // histograms are summed through distributed shared memory, so few long rows
-// spread over the card.  Bound: 8 bytes read per token for the selection and
-// 2 * 2 * D * 2 bytes per moved token; see the kernel's comment for rates.
+// spread over the card.
+//
+// Bound by memory where tokens move: 8 bytes read and written per token, and
+// per move 2 x 256 bytes (D = 128) read and written, one head of one token row at
+// a time.  Measured on GB300 (device time, share of the copy rate of 6776 GB/s):
+//   256 requests of 16..4096 (median 512) to 500, 32 heads    219 us  83 %
+//   8 x 32768 to 4096, 32 heads                               213 us  77 %
+//   64 requests of 2064 to 2048, 8 heads: 16 moves a row     12.1 us  31 %
+//   4 requests of 50..100 to 48, 4 heads of 64                5.1 us
+// The last two are the chain length -> keys -> histogram -> counts -> lists ->
+// rows, about a microsecond a link.  In the first, DRAM moves 1217 MB at 69 % of its
+// peak, reads and writes of 256 bytes in turn.
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -39,7 +49,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kFewKeys = 2048;        // a row of fewer is one CTA's
-constexpr int kManyKeys = 4096;       // a row of more is several CTAs'
+// A row of more keys is several CTAs': 8 x 32768 to 4096, 32 heads: 213 us with
+// 4096 keys per CTA, 232 with 8192; with 16384, 334: a second wave for a few rows.
+constexpr int kManyKeys = 4096;
 constexpr int kSmemKeys = 48 * 1024;  // keys a CTA can hold: 192 KB
 constexpr int kChunk = 128;           // keys a warp takes at once, 4 per lane
 constexpr unsigned kFull = 0xffffffffu;
@@ -426,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) evict_kernel(Params p) {
     // and moves its score and position, then LPR lanes copy each K or V row.
     constexpr int LPR = D / 8;
     constexpr int PER_STEP = 32 / (2 * LPR);  // movers copied by one warp-wide load
-    constexpr int M = 4;                      // loads in flight per lane
+    constexpr int M = 4;                      // loads in flight per lane (2: +21 %, 6: +9 %, 8: one CTA per SM fewer)
     const int sub = lane / (2 * LPR), part = lane % (2 * LPR);
     uint4* cache = part < LPR ? p.k_cache : p.v_cache;
     const int64_t row_vecs = (int64_t)p.Hkv * LPR;
