@@ -378,7 +378,7 @@ def test_bad_blocks_and_lengths_are_flagged_and_skipped(lens):
         E.paged_attention_decode_window(d["out"], d["q"], d["k"], d["v"], d["tables"], n, 30, 4, c["scale"],
                                         max_context_len=lens[0])
         flags = L.pkv_get_device_errors()
-        assert flags & L.PKV_DEVERR_CONTEXT
+        assert flags == L.PKV_DEVERR_CONTEXT
         if bad < 0:
             assert (d["out"][0] == 0).all()
     new = torch.empty_like(d["lens"])
@@ -568,3 +568,67 @@ def test_evict_equal_scores(value):
         c = evict_case(n, 1, 2, 64, 16, "f16", [n], budget, again=False)
         c["score"][:] = value
         check_evict(c, budget, 0, 0)
+
+
+# ------------------------------------------------------------ random and extreme
+@pytest.mark.parametrize("seed", range(16))
+def test_random_shapes(seed):
+    rng = np.random.default_rng(900 + seed)
+    D, bs = int(rng.choice([64, 128])), int(rng.choice([8, 16, 32, 64]))
+    Hkv = int(rng.choice([1, 2, 3, 4, 5, 6, 8, 12]))
+    G = int(rng.integers(1, 17))
+    S = int(rng.integers(1, 12))
+    top = int(rng.choice([20, 200, 2500]))
+    lens = rng.integers(0, top + 1, S)
+    lens[rng.random(S) < 0.15] = 0
+    dtype = ["f16", "bf16"][seed % 2]
+    c = make(seed, S, Hkv * G, Hkv, D, bs, dtype, lens, MB=max(1, -(-top // bs)) + int(rng.integers(0, 3)))
+    c["scale"] *= float(rng.choice([1.0, 0.1, -1.0, 0.0, 3.0]))
+    check_window(c, int(rng.integers(1, top + 10)), int(rng.integers(0, 40)), max_context_len=int(rng.choice([0, top])))
+    cap = c["MB"] * bs + int(rng.integers(0, 9))
+    check_accumulate(c, cap=cap, seed=seed, max_context_len=int(rng.choice([0, top])))
+    budget = int(rng.integers(1, top + 5))
+    sinks = int(rng.integers(0, budget + 1)) if seed % 3 else 0
+    e = evict_case(seed, S, Hkv, D, bs, dtype, lens, budget, cap=max(cap, -(-top // bs) * bs))
+    check_evict(e, budget, int(rng.integers(0, budget - sinks + 1)), sinks, in_place=bool(seed % 2))
+
+
+def test_the_most_sequences():
+    S = 32767
+    rng = np.random.default_rng(1)
+    lens = rng.integers(0, 4, S)
+    c = make(1, S, 2, 1, 64, 8, "f16", lens, MB=1)
+    check_window(c, 2, 1)
+    check_accumulate(c)
+    e = evict_case(2, S, 1, 64, 8, "f16", lens, 2, cap=8)
+    check_evict(e, 2, 1, 1)
+
+
+def test_one_very_long_context():
+    c = make(2, 1, 3, 1, 64, 64, "bf16", [300001])
+    check_accumulate(c)
+    check_window(c, 2 ** 31 - 1, 2 ** 31 - 1)
+    check_window(c, 250000, 7)
+    check_window(c, 3, 0)
+
+
+@pytest.mark.parametrize("scores_in_place", [True, False])
+def test_evict_with_one_output_in_place(scores_in_place):
+    c = evict_case(31, 3, 2, 64, 16, "bf16", [300, 40, 129], 60)
+    d = dev(c)
+    score, pos = torch.from_numpy(c["score"].copy()).cuda(), torch.from_numpy(c["pos"].copy()).cuda()
+    so = score if scores_in_place else torch.full_like(score, 7.0)
+    po = torch.full_like(pos, -7) if scores_in_place else pos
+    s0, p0 = score.clone(), pos.clone()
+    new = torch.empty_like(d["lens"])
+    E.evict_tokens(d["k"], d["v"], score, pos, d["tables"], d["lens"], torch.from_numpy(c["seen"]).cuda(), new, 60, 10, 4,
+                   scores_out=so, positions_out=po)
+    k, v = c["k"].view(torch.int16).numpy().copy(), c["v"].view(torch.int16).numpy().copy()
+    ws, wp = c["score"].copy(), c["pos"].copy()
+    B.evict(k, v, ws, wp, c["tables"], c["lens"], c["seen"], 60, 10, 4)
+    for s, n in enumerate(c["lens"]):
+        assert np.array_equal(so[s, :, :n].cpu().numpy(), ws[s, :, :n], equal_nan=True)
+        assert np.array_equal(po[s, :, :n].cpu().numpy(), wp[s, :, :n])
+    assert np.array_equal(d["k"].view(torch.int16).cpu().numpy(), k)
+    other, was = (pos, p0) if scores_in_place else (score, s0)
+    assert torch.equal(other.view(torch.int32), was.view(torch.int32)), "an input that is no output stays"
