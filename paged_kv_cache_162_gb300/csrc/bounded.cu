@@ -13,18 +13,19 @@
 //   are written to scratch as they are computed and read back once.
 //
 // How: a unit is one sequence and `hw` neighbouring KV heads; its visible
-// tokens go in tiles of 16.  One warp takes one KV head of a tile: K and V
-// rows come through a cp.async ring in shared memory (16-byte chunks, XOR
-// swizzle by row, rows without a token zero-filled and not read), the group's
-// G <= 16 query heads are the rows of m16n8k16 products on the tensor cores.
+// tokens go in tiles of 16 (D = 64: 32).  One warp takes one KV head of a tile:
+// K and V rows come through a cp.async ring in shared memory (16-byte chunks,
+// XOR swizzle by row, rows without a token zero-filled and not read), the
+// group's G <= 16 query heads are the rows of m16n8k16 products on the tensor
+// cores.
 // Memory is the bound: 512 bytes of K and V per (token, KV head) at D = 128
 // against 32 + 16 products of 16x8x16 per 8 KB tile.
 //   S = Q K^T, then the online softmax on the accumulators, then O += P V with
 //   P as the sum of two 16-bit numbers (its rounding and the rest): P rounded
 //   once would add an error as large as the output's own rounding.
 // A CTA is four warps: hw heads times 4 / hw token splits, joined in shared
-// memory.  The four read neighbouring data (1 KB of each token row, or 64
-// tokens of one head); a range of its own per warp was slower (window of 64 MHA
+// memory.  The four read neighbouring data (4 D values of each token row, or four
+// tiles of one head); a range of its own per warp was slower (window of 64 MHA
 // requests 146 us against 132), a barrier to keep them together no faster.
 //
 // Two ways to spread the units:
@@ -49,7 +50,7 @@
 //   accumulate, 8 x 32768                                         657-668 us  97 %
 //   accumulate, 256 requests of 16..4096 (median 512), 32 heads on 8  160 us  79 %
 //   window 4096 of one 32768-token context, 32 heads on 8            8.7 us  29 %
-//   4 requests of at most 100 tokens, 4 heads of 64       2.9 us, with scores 4.1
+//   4 requests of at most 100 tokens, 4 heads of 64       3.1 us, with scores 3.8
 // The split kernel reads each byte once (843.9 MB for 843.4) at 84 % of the DRAM
 // peak with its tensor pipe 28 % busy.  About 4 us go before every ring is full
 // (length -> place -> table -> rows), 3 to the last ranges; the second kernel takes
@@ -79,7 +80,6 @@ using pkv::Mma;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 16;
 constexpr int kMaxRanges = 1536;   // CTAs of a split call
 constexpr int kMinRange = 8;       // tiles of a large range
 constexpr int kMinSmall = 4;       // and of a small one: a ring is at most two ranges ahead
@@ -88,12 +88,18 @@ constexpr int kMaxCluster = 16;    // CTAs that share a unit in a direct call
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Tokens of a tile: 4 KB of K (or V) either way.  At D = 64 a tile of 16 had as
+// many instructions in its softmax and loop as in its products: 64 requests of
+// 2000 tokens and 16 heads took 90.8 us, with 32 tokens 84.8 (at D = 128 the
+// registers are all taken at 16).
+constexpr int tile_tokens(int D) { return D == 128 ? 16 : 32; }
 template <int D>
-constexpr int kStages = D == 128 ? 3 : 5;
+constexpr int kTile = tile_tokens(D);
+constexpr int kStages = 3;
 template <int D>
-constexpr int kTileBytes = kTile * D * 2;  // K (or V) of one tile and head
+constexpr int kTileBytes = kTile<D> * D * 2;  // K (or V) of one tile and head
 template <int D>
-constexpr int kRingBytes = kStages<D> * 2 * kTileBytes<D>;  // one warp's ring
+constexpr int kRingBytes = kStages * 2 * kTileBytes<D>;  // one warp's ring
 template <int D>
 constexpr int kSmemBytes = kWarps * kRingBytes<D>;
 
@@ -105,6 +111,7 @@ struct Params {
     const int32_t* block_tables;
     const int32_t* context_lens;
     int S, H, Hkv, G, NB, MB, bs_log2, max_ctx;
+    int tile_log2;       // of a tile's tokens
     int window, sinks;   // accumulate: window = max_ctx
     int hw, nsplit, HB;  // KV heads per CTA, warps per KV head, units per sequence
     int cs;              // direct: CTAs per cluster
@@ -135,7 +142,7 @@ __device__ __forceinline__ int visible_of(const Params& p, int n) {
 
 // Tiles of a unit; an empty context has one, which writes zeros.
 __device__ __forceinline__ int tiles_of(const Params& p, int n) {
-    const int t = (visible_of(p, n) + kTile - 1) / kTile;
+    const int t = (visible_of(p, n) + (1 << p.tile_log2) - 1) >> p.tile_log2;
     return t < 1 ? 1 : t;
 }
 
@@ -320,7 +327,8 @@ struct Acc {
 // the units and ranges that follow, so that no end of one drains the ring.
 template <int D>
 struct Feed {
-    static constexpr int NST = kStages<D>;
+    static constexpr int NST = kStages;
+    static constexpr unsigned kAllRows = kTile<D> == 32 ? 0xffffffffu : 0xffffu;
     const Params& p;
     Plan* const plan;         // null: one unit (part) at a time
     const uint32_t ring;
@@ -330,7 +338,7 @@ struct Feed {
     int nv, shift;
     const int32_t* bt;
     const uint16_t* k_head;
-    int slot;                 // cache row of its row lane % 16
+    int slot;                 // cache row of its row lane % kTile
     bool more;
     unsigned mask[NST];       // rows with a token, of the tiles in the ring
     int stage;                // of the oldest tile
@@ -353,12 +361,12 @@ struct Feed {
         if (lane * 128 < p.G * D * 2) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + lane * 128));
     }
 
-    // Row lane % 16 of the next tile: its cache row, or -1 where there is no
+    // Row lane % kTile of the next tile: its cache row, or -1 where there is no
     // token (past the visible ones) or its block id is out of range.  NB * bs
     // fits an int (checked on the host).
     __device__ __forceinline__ void lookup() {
         slot = -1;
-        const int v = i * kTile + (lane & 15);
+        const int v = i * kTile<D> + lane % kTile<D>;
         if (!more || v >= nv) return;
         const int tok = v < p.sinks ? v : v + shift;
         const int phys = __ldg(bt + (tok >> p.bs_log2));
@@ -409,8 +417,8 @@ struct Feed {
     // Copies the next tile into ring stage `st` and its row mask into
     // mask[at], then looks up the one after it.
     __device__ __forceinline__ void push(int st, int at) {
-        constexpr int ROWB = D * 2, CPR = ROWB / 16, CPL = kTile * CPR / 32;
-        mask[at] = __ballot_sync(kFull, slot >= 0) & 0xffffu;
+        constexpr int ROWB = D * 2, CPR = ROWB / 16, CPL = kTile<D> * CPR / 32;
+        mask[at] = __ballot_sync(kFull, slot >= 0) & kAllRows;
         if (more) {
             const uint32_t sk = ring + st * 2 * kTileBytes<D>, sv = sk + kTileBytes<D>;
             const int64_t row_elems = (int64_t)p.Hkv * D;
@@ -476,8 +484,9 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
                                        int te, int lane, Acc<D>& a) {
     constexpr int NK = D / 16, NO = D / 8;
     constexpr int ROWB = D * 2;
-    constexpr int NST = kStages<D>;
+    constexpr int NST = kStages;
     constexpr int R = kWide ? 2 : 1;
+    constexpr int NT = kTile<D> / 8;
     const int g = lane >> 2, t = lane & 3;
 
 #pragma unroll
@@ -509,57 +518,67 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
         __syncwarp();
         const uint32_t sk = feed.ring + stage * 2 * kTileBytes<D>, sv = sk + kTileBytes<D>;
 
-        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        {
+        // S: NT column tiles of 8 tokens
+        float sc[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < NT; j += 2) {
             const int mi = lane >> 3;
-            const int row = (mi >> 1) * 8 + (lane & 7);
+            const int row = 8 * j + (mi >> 1) * 8 + (lane & 7);
 #pragma unroll
             for (int k = 0; k < NK; ++k) {
                 uint32_t b[4];
                 ldsm_x4(b, sk + row * ROWB + (((2 * k + (mi & 1)) ^ (row & 7)) * 16));
-                Mma<E>::run(sc[0], qa[k], b[0], b[1]);
-                Mma<E>::run(sc[1], qa[k], b[2], b[3]);
+                Mma<E>::run(sc[j], qa[k], b[0], b[1]);
+                Mma<E>::run(sc[j + 1], qa[k], b[2], b[3]);
             }
         }
         // logits in log2 units; element e of sc[j] is row g + 8 (e / 2),
         // token 8 j + 2 t + e % 2 of the tile
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int e = 0; e < 2 * R; ++e) {
-                sc[j][e] *= p.qscale;
-                if (rows != 0xffffu && !((rows >> (8 * j + 2 * t + (e & 1))) & 1u))
-                    sc[j][e] = -INFINITY;
-            }
+            for (int e = 0; e < 2 * R; ++e) sc[j][e] *= p.qscale;
+        if (rows != Feed<D>::kAllRows) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2 * R; ++e)
+                    if (!((rows >> (8 * j + 2 * t + (e & 1))) & 1u)) sc[j][e] = -INFINITY;
+        }
         if constexpr (kScores) {
             float* zr = p.z + ((int64_t)s * p.H + (int64_t)kvh * p.G + g) * p.z_stride +
-                        i * kTile + 2 * t;
+                        i * kTile<D> + 2 * t;
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 if (g + 8 * r < p.G) {
                     float* zp = zr + 8 * r * p.z_stride;
-                    *reinterpret_cast<float2*>(zp) = make_float2(sc[0][2 * r], sc[0][2 * r + 1]);
-                    *reinterpret_cast<float2*>(zp + 8) = make_float2(sc[1][2 * r], sc[1][2 * r + 1]);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        *reinterpret_cast<float2*>(zp + 8 * j) = make_float2(sc[j][2 * r], sc[j][2 * r + 1]);
                 }
         }
-        float pr[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
         float corr[2] = {1.f, 1.f};
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float mt = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]),
-                             fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
+            float mt = fmaxf(sc[0][2 * r], sc[0][2 * r + 1]);
+#pragma unroll
+            for (int j = 1; j < NT; ++j) mt = fmaxf(mt, fmaxf(sc[j][2 * r], sc[j][2 * r + 1]));
             mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 1));
             mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 2));
             const float m_new = fmaxf(a.m[r], mt);
             const float m_use = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet
             corr[r] = exp2f(a.m[r] - m_use);
             a.m[r] = m_new;
+            float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < NT; ++j) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) pr[j][2 * r + e] = exp2f(sc[j][2 * r + e] - m_use);
-            a.l[r] = fmaf(a.l[r], corr[r],
-                          (pr[0][2 * r] + pr[0][2 * r + 1]) + (pr[1][2 * r] + pr[1][2 * r + 1]));
+                for (int e = 0; e < 2; ++e) sc[j][2 * r + e] = exp2f(sc[j][2 * r + e] - m_use);
+                sum += sc[j][2 * r] + sc[j][2 * r + 1];
+            }
+            a.l[r] = fmaf(a.l[r], corr[r], sum);
         }
         // most tiles leave every row's maximum as it was
         if (__any_sync(kFull, corr[0] != 1.f || corr[1] != 1.f)) {
@@ -573,21 +592,22 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
                 }
             }
         }
-        // P = its rounding to 16 bits + the rounding of what is left
-        uint32_t ph[4] = {0u, 0u, 0u, 0u}, pl[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int h = 0; h < NT / 2; ++h) {  // 16 tokens each
+            // P = its rounding to 16 bits + the rounding of what is left
+            uint32_t ph[4] = {0u, 0u, 0u, 0u}, pl[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float x = pr[j][2 * r], y = pr[j][2 * r + 1];
-                const uint32_t hi = E::from_float2(x, y);
-                const float2 back = E::to_float2(hi);
-                ph[2 * j + r] = hi;
-                pl[2 * j + r] = E::from_float2(x - back.x, y - back.y);
-            }
-        {
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float x = sc[2 * h + j][2 * r], y = sc[2 * h + j][2 * r + 1];
+                    const uint32_t hi = E::from_float2(x, y);
+                    const float2 back = E::to_float2(hi);
+                    ph[2 * j + r] = hi;
+                    pl[2 * j + r] = E::from_float2(x - back.x, y - back.y);
+                }
             const int mi = lane >> 3;
-            const int row = (mi & 1) * 8 + (lane & 7);
+            const int row = 16 * h + (mi & 1) * 8 + (lane & 7);
 #pragma unroll
             for (int j = 0; j < NO; j += 2) {
                 uint32_t b[4];
@@ -785,7 +805,7 @@ __device__ __forceinline__ void join_cluster(const Params& p, int s, int kvh, in
             }
         }
         __syncthreads();
-        fold_weights(p, s, kvh, tb * kTile, min(te * kTile, n), s_m, s_inv, tid, kThreads);
+        fold_weights(p, s, kvh, tb * kTile<D>, min(te * kTile<D>, n), s_m, s_inv, tid, kThreads);
     }
 }
 
@@ -1290,8 +1310,8 @@ Layout layout_of(int S, int H, int Hkv, int D, bool scores, int max_ctx) {
     L.l = o;     o = align256(o + rows * sizeof(float));
     L.acc = o;   o = align256(o + rows * D * sizeof(float));
     L.row_m = L.row_l = L.z = o;
-    L.z_stride = ((int64_t)max_ctx + kTile - 1) / kTile * kTile;
-    if (L.z_stride == 0) L.z_stride = kTile;
+    const int tile = tile_tokens(D);
+    L.z_stride = max_ctx > 0 ? ((int64_t)max_ctx + tile - 1) / tile * tile : tile;
     if (scores) {
         L.row_m = o; o = align256(o + (size_t)S * H * sizeof(float));
         L.row_l = o; o = align256(o + (size_t)S * H * sizeof(float));
@@ -1426,6 +1446,8 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     p.score_stride = score_stride;
     p.err = pkv::device_error_word();
     const int64_t most = (int64_t)window + sinks < max_ctx ? (int64_t)window + sinks : max_ctx;
+    const int tile = tile_tokens(D);
+    p.tile_log2 = tile == 16 ? 4 : 5;
     const bool wide = p.G > 8;
     const int smem = D == 128 ? kSmemBytes<128> : kSmemBytes<64>;
     KernelFn direct_fn = with_scores ? pick_attend<true, true>(dtype, D, wide) : pick_attend<false, true>(dtype, D, wide);
@@ -1440,7 +1462,7 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
                         (int64_t)S * Hkv * p.cs <= kDirectWaves * slots;
     if (direct)
         while (p.cs < kMaxCluster && (int64_t)S * Hkv * p.cs * 2 <= slots &&
-               most > (int64_t)2 * kWarps * kTile * p.cs)
+               most > (int64_t)2 * kWarps * tile * p.cs)
             p.cs *= 2;
     p.hw = direct ? 1 : heads_per_cta(Hkv);
     while (!direct && p.hw > 1 && (int64_t)S * Hkv / p.hw < kMinUnits) p.hw /= 2;
@@ -1452,7 +1474,7 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     if (p.ranges0 > kMaxRanges / (1 + kSmallRanges)) p.ranges0 = kMaxRanges / (1 + kSmallRanges);
     // small ranges only where changing over costs nothing (a warp per head), and
     // where contexts at their bound would have some
-    const int64_t most_tiles = (int64_t)S * p.HB * ((most + kTile - 1) / kTile);
+    const int64_t most_tiles = (int64_t)S * p.HB * ((most + tile - 1) / tile);
     const bool share = p.nsplit == 1 && most_tiles / p.ranges0 * (16 - kLargeShare) / 16 / kSmallRanges >= kMinSmall;
     p.ranges = share ? p.ranges0 * (1 + kSmallRanges) : p.ranges0;
 
