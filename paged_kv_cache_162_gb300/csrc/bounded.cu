@@ -44,17 +44,17 @@
 //    every sum has a fixed order.
 //
 // Measured on GB300 (device time, share of the measured copy rate of 6776 GB/s):
-//   window 1000 + 4 sinks, 64 requests of 128..2048, 32 heads, fp16   128 us  97 %
-//   window 4093 + 7, 96 requests, 32 heads on 8, bf16                 240 us  99 %
-//   accumulate, the 64 requests whole                                 186 us  92 %
-//   accumulate, 8 x 32768                                         657-668 us  97 %
-//   accumulate, 256 requests of 16..4096 (median 512), 32 heads on 8  160 us  79 %
+//   window 1000 + 4 sinks, 64 requests of 128..2048, 32 heads, fp16   127 us  98 %
+//   window 4093 + 7, 96 requests, 32 heads on 8, bf16                 237 us 100 %
+//   accumulate, the 64 requests whole                                 183 us  93 %
+//   accumulate, 8 x 32768                                             655 us  98 %
+//   accumulate, 256 requests of 16..4096 (median 512), 32 heads on 8  155 us  82 %
 //   window 4096 of one 32768-token context, 32 heads on 8            8.7 us  29 %
 //   4 requests of at most 100 tokens, 4 heads of 64       3.1 us, with scores 3.8
 // The split kernel reads each byte once (843.9 MB for 843.4) at 84 % of the DRAM
 // peak with its tensor pipe 28 % busy.  About 4 us go before every ring is full
 // (length -> place -> table -> rows), 3 to the last ranges; the second kernel takes
-// 4 us without scores and 12 to 20 with them.  The small calls are that chain.
+// 4 us without scores and 10 to 15 with them.  The small calls are that chain.
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -1194,14 +1194,22 @@ __device__ __forceinline__ void fold_stretch(const Params& p, int s, int kvh, in
 }
 
 // After split_kernel, one wave of CTAs that take items: first the joins, then,
-// with scores, the fold.  Either is short chains of loads (is there anything ->
-// where -> the data), so what counts is that a warp has few of them and waits
-// on none to learn that there is nothing to do: it looks at 32 items at once.
+// with scores, the fold.  Either is a short chain of loads (is there anything ->
+// where -> the data), and most possible items do not exist: so the threads of a
+// CTA look at 256 of its share at once, list those that do, and its warps do
+// the listed ones in turn: 155 us for the 256 requests of 16..4096, where warps
+// with items of their own took 160.  Fewer tokens per fold, two or four CTAs per
+// SM: no faster.
 //  join: a row of a unit that lies in several ranges, by a warp, or by the
 //        CTA's warps together (`wide`) where units have many pieces.
 //  fold: 256 tokens (512 with one query head) of a KV head, by a warp.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
+struct Item {
+    int2 place;  // the ranges its unit begins and ends in
+    int at;      // join: output row; fold: sequence * Hkv + KV head
+    int n, j0;   // fold: context (join: 0), first token
+};
 
 template <class E, int D, bool kScores, bool kOne>
 __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const __grid_constant__ Params p, int wide) {
@@ -1209,8 +1217,6 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const __grid_cons
     asm volatile("griddepcontrol.launch_dependents;");
     constexpr int DPL = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // neighbouring items go to different SMs
-    const int w0 = warp * gridDim.x + blockIdx.x, warps = gridDim.x * kJoinWarps;
     const int rows = p.hw * p.G;
     const int joins = p.S * p.HB * rows;  // = S * H
     if (wide) {
@@ -1243,38 +1249,55 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const __grid_cons
             }
             __syncthreads();  // the parts have been read
         }
-    } else {
-        for (int base = w0; base < joins; base += 32 * warps) {
-            const int mine = base + lane * warps;
-            int2 at = make_int2(0, 0);
-            if (mine < joins) at = p.place[mine / rows];
-            for (unsigned todo = __ballot_sync(kFull, at.x != at.y); todo; todo &= todo - 1) {
-                const int src = __ffs(todo) - 1;
-                const int i = base + src * warps;
-                const int c0 = __shfl_sync(kFull, at.x, src), c1 = __shfl_sync(kFull, at.y, src);
-                float M, L, o[DPL];
-                gather_row<D, 2>(p, c0, c0, c1, 1, i % rows, lane, M, L, o);
-                write_row<E, D>(p, i / rows, i % rows, lane, L, o);
-            }
-        }
     }
-    if constexpr (kScores) {
-        constexpr int RUNS = kOne ? 4 : 2, HEADS = kOne ? 1 : 4, TOKENS = RUNS * 128;
-        const int stretches = (p.max_ctx + TOKENS - 1) / TOKENS;
-        const int heads = p.S * p.Hkv;
-        const long long items = (long long)heads * stretches;
-        // item (stretch, sequence, KV head): the first stretches of all first
-        for (long long base = w0; base < items; base += 32LL * warps) {
-            const long long mine = base + (long long)lane * warps;
-            bool live = false;
-            if (mine < items) live = (int)(mine / heads) * TOKENS < context_of(p, (int)(mine % heads) / p.Hkv);
-            for (unsigned todo = __ballot_sync(kFull, live); todo; todo &= todo - 1) {
-                const long long item = base + (long long)(__ffs(todo) - 1) * warps;
-                const int unit = (int)(item % heads), kvh = unit % p.Hkv;
-                fold_stretch<RUNS, HEADS>(p, unit / p.Hkv, kvh, kvh % p.hw, context_of(p, unit / p.Hkv),
-                                          p.place[unit / p.hw], (int)(item / heads) * TOKENS, lane);
+    constexpr int RUNS = kOne ? 4 : 2, HEADS = kOne ? 1 : 4, TOKENS = RUNS * 128;
+    __shared__ int s_count[kJoinWarps];
+    __shared__ Item s_item[kJoinThreads];
+    const int heads = p.S * p.Hkv;
+    const long long listed = wide ? 0 : joins;
+    const long long items = listed + (kScores ? (long long)heads * ((p.max_ctx + TOKENS - 1) / TOKENS) : 0);
+    // neighbouring items go to different SMs
+    for (long long base = blockIdx.x; base < items; base += (long long)kJoinThreads * gridDim.x) {
+        const long long mine = base + (long long)threadIdx.x * gridDim.x;
+        Item it;
+        it.n = 0;  // of a join
+        bool live = false;
+        if (mine < listed) {
+            it.at = (int)mine;
+            it.place = p.place[it.at / rows];
+            live = it.place.x != it.place.y;
+        } else if (kScores && mine < items) {
+            // (stretch, sequence, KV head): the first stretches of all first
+            const long long f = mine - listed;
+            it.at = (int)(f % heads);
+            it.j0 = (int)(f / heads) * TOKENS;
+            it.n = context_of(p, it.at / p.Hkv);
+            live = it.j0 < it.n;
+            it.place = p.place[it.at / p.hw];
+        }
+        const unsigned alive = __ballot_sync(kFull, live);
+        if (lane == 0) s_count[warp] = __popc(alive);
+        __syncthreads();
+        int before = 0, count = 0;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            if (w == warp) before = count;
+            count += s_count[w];
+        }
+        if (live) s_item[before + __popc(alive & ((1u << lane) - 1u))] = it;
+        __syncthreads();
+        for (int k = warp; k < count; k += kJoinWarps) {
+            const Item x = s_item[k];
+            if (x.n == 0) {
+                float M, L, o[DPL];
+                gather_row<D, 2>(p, x.place.x, x.place.x, x.place.y, 1, x.at % rows, lane, M, L, o);
+                write_row<E, D>(p, x.at / rows, x.at % rows, lane, L, o);
+            } else if constexpr (kScores) {
+                const int kvh = x.at % p.Hkv;
+                fold_stretch<RUNS, HEADS>(p, x.at / p.Hkv, kvh, kvh % p.hw, x.n, x.place, x.j0, lane);
             }
         }
+        __syncthreads();  // the list has been read
     }
 }
 
