@@ -25,10 +25,10 @@
 // Bound by memory where tokens move: 8 bytes read and written per token, and
 // per move 2 x 256 bytes (D = 128) read and written, one head of one token row at
 // a time.  Measured on GB300 (device time, share of the copy rate of 6776 GB/s):
-//   256 requests of 16..4096 (median 512) to 500, 32 heads    219 us  83 %
-//   8 x 32768 to 4096, 32 heads                               213 us  77 %
-//   64 requests of 2064 to 2048, 8 heads: 16 moves a row     12.1 us  31 %
-//   4 requests of 50..100 to 48, 4 heads of 64                5.1 us
+//   256 requests of 16..4096 (median 512) to 500, 32 heads    218 us  84 %
+//   8 x 32768 to 4096, 32 heads                               211 us  77 %
+//   64 requests of 2064 to 2048, 8 heads: 16 moves a row     11.3 us  33 %
+//   4 requests of 50..100 to 48, 4 heads of 64                4.9 us
 // The last two are the chain length -> keys -> histogram -> counts -> lists ->
 // rows, about a microsecond a link.  In the first, DRAM moves 1217 MB at 69 % of its
 // peak, reads and writes of 256 bytes in turn.
@@ -373,64 +373,78 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) evict_kernel(Params p) {
 
     int32_t* hole_list = p.holes + (int64_t)row * b;
     int32_t* mover_list = p.movers + (int64_t)row * b;
+    const unsigned lower = (1u << lane) - 1u;
+    // the lane's tokens j + e with in[e] go to the list, in order over the warp
+    auto append = [&](int32_t* list, int& at, int j, const bool (&in)[4]) {
+        unsigned on[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) on[e] = __ballot_sync(kFull, in[e]);
+        if (!(on[0] | on[1] | on[2] | on[3])) return;
+        int to = at;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            to += __popc(on[e] & lower);
+            at += __popc(on[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (in[e]) list[to++] = j + e;
+    };
     int seen = ties0;
     for (int base = w0; base < w1; base += kChunk) {
         const int j = base + 4 * lane;
         uint32_t k[4] = {0u, 0u, 0u, 0u};
         if (j < w1) keys4(j, k);
-        bool kp[4], eq[4];
-        int ties = 0;
+        bool kp[4], eq[4], out[4];
+        unsigned tied[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const bool in = j + e < w1;
             kp[e] = in && (k[e] >> drop) > T;
             eq[e] = in && (k[e] >> drop) == T;
-            ties += eq[e];
+            tied[e] = __ballot_sync(kFull, eq[e]);
         }
-        if (__any_sync(kFull, ties != 0)) {  // ranks of the ties, in order
-            int incl = ties;
+        if (seen < want && (tied[0] | tied[1] | tied[2] | tied[3])) {  // ranks of the ties, in order
+            int r = seen;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(kFull, incl, o);
-                if (lane >= o) incl += y;
+            for (int e = 0; e < 4; ++e) {
+                r += __popc(tied[e] & lower);
+                seen += __popc(tied[e]);
             }
-            int r = seen + incl - ties;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 kp[e] |= eq[e] && r < want;
                 r += eq[e];
             }
-            seen += __shfl_sync(kFull, incl, 31);
         }
-        int found = 0;  // holes, and movers in the upper half
+        if (base < b) {  // holes
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (j + e < w1) found += j + e < b ? (kp[e] ? 0 : 1) : (kp[e] ? 0x10000 : 0);
-        if (!moved_out || !moved_pos) {
+            for (int e = 0; e < 4; ++e) out[e] = j + e < min(w1, b) && !kp[e];
+            append(hole_list, hole0, j, out);
+        }
+        if (base + kChunk > b) {  // movers; the others there are evicted
+            bool all = vec && j >= b && j + 4 <= w1;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (j + e < w1 && j + e >= b && !kp[e]) {  // evicted: nobody reads these any more
-                    if (!moved_out) score_out[j + e] = 0.f;
-                    if (!moved_pos) pos_out[j + e] = -1;
+            for (int e = 0; e < 4; ++e) {
+                out[e] = j + e >= b && j + e < w1 && !kp[e];
+                kp[e] = kp[e] && j + e >= b;
+                all = all && out[e];
+            }
+            if (!moved_out || !moved_pos) {  // nobody reads their scores and positions any more
+                if (all) {
+                    if (!moved_out) *reinterpret_cast<float4*>(score_out + j) = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (!moved_pos) *reinterpret_cast<int4*>(pos_out + j) = make_int4(-1, -1, -1, -1);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (out[e]) {
+                            if (!moved_out) score_out[j + e] = 0.f;
+                            if (!moved_pos) pos_out[j + e] = -1;
+                        }
                 }
+            }
+            append(mover_list, mover0, j, kp);
         }
-        if (!__any_sync(kFull, found != 0)) continue;
-        int incl = found;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kFull, incl, o);
-            if (lane >= o) incl += y;
-        }
-        const int total = __shfl_sync(kFull, incl, 31);
-        int ho = hole0 + ((incl - found) & 0xffff), mo = mover0 + ((incl - found) >> 16);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (j + e >= w1) continue;
-            if (j + e < b && !kp[e]) hole_list[ho++] = j + e;
-            if (j + e >= b && kp[e]) mover_list[mo++] = j + e;
-        }
-        hole0 += total & 0xffff;
-        mover0 += total >> 16;
     }
     sync_row();  // the lists are complete (and no CTA's memory is read after this)
 
