@@ -27,7 +27,7 @@
 // a time.  Measured on GB300 (device time, share of the copy rate of 6776 GB/s):
 //   256 requests of 16..4096 (median 512) to 500, 32 heads    218 us  84 %
 //   8 x 32768 to 4096, 32 heads                               211 us  77 %
-//   64 requests of 2064 to 2048, 8 heads: 16 moves a row     11.3 us  33 %
+//   64 requests of 2064 to 2048, 8 heads: 16 moves a row     10.4 us  36 %
 //   4 requests of 50..100 to 48, 4 heads of 64                4.9 us
 // The last two are the chain length -> keys -> histogram -> counts -> lists ->
 // rows, about a microsecond a link.  In the first, DRAM moves 1217 MB at 69 % of its
@@ -80,8 +80,8 @@ struct Params {
 __device__ __forceinline__ uint32_t key_of(float score, bool safe) {
     if (safe) return 0xffffffffu;
     if (score != score) return 0x007fffffu;          // as -inf
-    const uint32_t u = score == 0.f ? 0u : __float_as_uint(score);
-    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+    const uint32_t u = __float_as_uint(score + 0.f);  // -0 + 0 = +0
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 // How many tokens of a stretch lie below the budget / past it and have a key
@@ -190,10 +190,11 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) evict_kernel(Params p) {
     const int seg = ((n + CS - 1) / CS + kChunk - 1) / kChunk * kChunk;
     const int j0 = min(n, rank * seg), j1 = min(n, j0 + seg);
     const bool in_smem = seg <= p.seg_cap;
-    const int oldest_recent = N - p.recent;
+    // safe: below the sinks, or not below N - recent
+    const unsigned unsafe = max(0, N - p.recent - p.sinks);
     auto make_key = [&](float sc, int stored_pos, int j) -> uint32_t {
         const int q = stored_pos >= 0 ? stored_pos : N - n + j;
-        return key_of(sc, q < p.sinks || q >= oldest_recent);
+        return key_of(sc, (unsigned)(q - p.sinks) >= unsafe);
     };
     // keys of tokens j .. j + 3 (j a multiple of 4 from j0 on, below j1)
     auto keys4 = [&](int j, uint32_t (&k)[4]) {
@@ -323,21 +324,39 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) evict_kernel(Params p) {
     // keys are compared by their digits so far; `want` of those equal to T
     // stay, lowest index first
 
-    // count this warp's stretch [w0, w1)
+    // count this warp's stretch [w0, w1); few instructions per key matter where all
+    // rows are on the card at once (64 requests in steady state: 11.1 -> 10.5 us with
+    // chunks of one kind apart)
     const int per = (seg / kChunk + kWarps - 1) / kWarps * kChunk;
     const int w0 = min(j1, j0 + warp * per), w1 = min(j1, w0 + per);
     Counts mine = {0, 0, 0, 0};
-    for (int j = w0 + 4 * lane; j < w1; j += kChunk) {
-        uint32_t k[4];
-        keys4(j, k);
+    for (int base = w0; base < w1; base += kChunk) {
+        const int j = base + 4 * lane;
+        uint32_t k[4] = {0u, 0u, 0u, 0u};
+        if (j < w1) keys4(j, k);
+        const bool full = base + kChunk <= w1;
+        if (full && base + kChunk <= b) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool in = j + e < w1, front = j + e < b;
-            const int gt = in && (k[e] >> drop) > T, eq = in && (k[e] >> drop) == T;
-            mine.gt_front += front ? gt : 0;
-            mine.gt_back += front ? 0 : gt;
-            mine.eq_front += front ? eq : 0;
-            mine.eq_back += front ? 0 : eq;
+            for (int e = 0; e < 4; ++e) {
+                mine.gt_front += (k[e] >> drop) > T;
+                mine.eq_front += (k[e] >> drop) == T;
+            }
+        } else if (full && base >= b) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                mine.gt_back += (k[e] >> drop) > T;
+                mine.eq_back += (k[e] >> drop) == T;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in = j + e < w1, front = j + e < b;
+                const int gt = in && (k[e] >> drop) > T, eq = in && (k[e] >> drop) == T;
+                mine.gt_front += front ? gt : 0;
+                mine.gt_back += front ? 0 : gt;
+                mine.eq_front += front ? eq : 0;
+                mine.eq_back += front ? 0 : eq;
+            }
         }
     }
     mine.gt_front = __reduce_add_sync(kFull, mine.gt_front);
