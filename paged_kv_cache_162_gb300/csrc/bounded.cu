@@ -49,8 +49,8 @@
 //   accumulate, the 64 requests whole                                 183 us  93 %
 //   accumulate, 8 x 32768                                             655 us  98 %
 //   accumulate, 256 requests of 16..4096 (median 512), 32 heads on 8  155 us  82 %
-//   window 4096 of one 32768-token context, 32 heads on 8            8.7 us  29 %
-//   4 requests of at most 100 tokens, 4 heads of 64       3.1 us, with scores 3.8
+//   window 4096 of one 32768-token context, 32 heads on 8            8.3 us  30 %
+//   4 requests of at most 100 tokens, 4 heads of 64       2.8 us, with scores 3.5
 // The split kernel reads each byte once (843.9 MB for 843.4) at 84 % of the DRAM
 // peak with its tensor pipe 28 % busy.  About 4 us go before every ring is full
 // (length -> place -> table -> rows), 3 to the last ranges; the second kernel takes
@@ -631,21 +631,21 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
 }
 
 // Joins the token splits of each head in shared memory: split 0's warp ends
-// up with the whole.  `ring` is the CTA's ring memory, idle here.
-template <int D>
+// up with the whole.  Every warp's part goes into its own ring, idle here.
+template <int D, bool kWide>
 __device__ __forceinline__ void join_splits(const Params& p, float* ring, int warp, int lane,
                                             Acc<D>& a) {
-    constexpr int NO = D / 8;
+    constexpr int NO = D / 8, R = kWide ? 2 : 1;
     constexpr int kSlice = kRingBytes<D> / 4;  // floats of one warp's ring
-    __syncthreads();
+    __syncwarp();
     if (warp >= p.hw) {
         float* mine = ring + warp * kSlice + lane;
 #pragma unroll
         for (int j = 0; j < NO; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mine[(4 * j + e) * 32] = a.o[j][e];
+            for (int e = 0; e < 2 * R; ++e) mine[(4 * j + e) * 32] = a.o[j][e];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < R; ++r) {
             mine[(4 * NO + r) * 32] = a.m[r];
             mine[(4 * NO + 2 + r) * 32] = a.l[r];
         }
@@ -656,7 +656,7 @@ __device__ __forceinline__ void join_splits(const Params& p, float* ring, int wa
             const float* other = ring + w * kSlice + lane;
             float wa[2], wb[2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
+            for (int r = 0; r < R; ++r) {
                 const float mo = other[(4 * NO + r) * 32], lo = other[(4 * NO + 2 + r) * 32];
                 const float m_new = fmaxf(a.m[r], mo);
                 const float m_use = m_new == -INFINITY ? 0.f : m_new;
@@ -668,11 +668,62 @@ __device__ __forceinline__ void join_splits(const Params& p, float* ring, int wa
 #pragma unroll
             for (int j = 0; j < NO; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 2 * R; ++e)
                     a.o[j][e] = a.o[j][e] * wa[e >> 1] + other[(4 * j + e) * 32] * wb[e >> 1];
         }
     }
     __syncthreads();  // the rings are filled again after this
+}
+
+// The same for a CTA with one head (direct): warp w ends up with columns
+// [w, w + 1) * D / 4 of the rows, in o[.][2 r + column % 2], and with the whole m
+// and l.
+template <int D, bool kWide>
+__device__ __forceinline__ void join_warps(float* ring, int warp, int lane, Acc<D>& a,
+                                           float (&o)[D / 8 / kWarps][kWide ? 4 : 2]) {
+    constexpr int NO = D / 8, R = kWide ? 2 : 1;
+    constexpr int kSlice = kRingBytes<D> / 8;  // float2s of one warp's ring
+    float2* all = reinterpret_cast<float2*>(ring) + lane;
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int j = 0; j < NO; ++j)
+            all[warp * kSlice + (R * j + r) * 32] = make_float2(a.o[j][2 * r], a.o[j][2 * r + 1]);
+        all[warp * kSlice + (R * NO + r) * 32] = make_float2(a.m[r], a.l[r]);
+    }
+    __syncthreads();
+    float2 ml[R][kWarps];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) ml[r][w] = all[w * kSlice + (R * NO + r) * 32];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        float M = ml[r][0].x, L = 0.f;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) M = fmaxf(M, ml[r][w].x);
+        const float use = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            ml[r][w].x = exp2f(ml[r][w].x - use);  // the part's weight
+            L = fmaf(ml[r][w].x, ml[r][w].y, L);
+        }
+        a.m[r] = M;
+        a.l[r] = L;
+    }
+#pragma unroll
+    for (int j = 0; j < NO / kWarps; ++j)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            o[j][2 * r] = o[j][2 * r + 1] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 x = all[w * kSlice + (R * (warp * (NO / kWarps) + j) + r) * 32];
+                o[j][2 * r] = fmaf(ml[r][w].x, x.x, o[j][2 * r]);
+                o[j][2 * r + 1] = fmaf(ml[r][w].x, x.y, o[j][2 * r + 1]);
+            }
+        }
 }
 
 // scores[s, kvh, j] += sum over the group's heads of 2^(z - M) / L for the
@@ -733,37 +784,37 @@ __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Joins the CTAs of a cluster that share a unit: every CTA writes its rows (warp
-// 0 has them) into the memory of the CTAs that join them, segment i to CTA
+// Joins the CTAs of a cluster that share a unit: every CTA writes its rows
+// into the memory of the CTAs that join them, segment i to CTA
 // i % CS; after one barrier each joins what it was sent, and folds its own
 // tokens [tb, te) into the scores.  No CTA reads another's memory, so none has
-// to stay for that.  The caller has arrived once at the cluster's barrier: the
+// to stay for that.  o, m and l are as join_warps leaves them.  The caller has arrived once at the cluster's barrier: the
 // wait for it says that all CTAs run.
 template <class E, int D, bool kWide, bool kScores>
 __device__ __forceinline__ void join_cluster(const Params& p, int s, int kvh, int n, int tb, int te,
                                              ClusterIn* in, int warp, int lane, const Acc<D>& a,
+                                             const float (&mine)[D / 8 / kWarps][kWide ? 4 : 2],
                                              float* s_m, float* s_inv) {
     constexpr int NO = D / 8, R = kWide ? 2 : 1, SEGS = D / 32;
     cg::cluster_group cluster = cg::this_cluster();
     const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int g = lane >> 2, t = lane & 3, tid = warp * 32 + lane;
     cluster_wait();
-    if (warp == 0) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int row = g + 8 * r;
-            if (row < p.G) {
+    for (int r = 0; r < R; ++r) {
+        const int row = g + 8 * r;
+        if (row < p.G) {
 #pragma unroll
-                for (int j = 0; j < NO; ++j) {
-                    const int seg = row * SEGS + j / 4;
-                    float* to = cluster.map_shared_rank(&in->o[0], seg % CS) + (seg / CS * CS + rank) * 32 +
-                                8 * (j % 4) + 2 * t;
-                    *reinterpret_cast<float2*>(to) = make_float2(a.o[j][2 * r], a.o[j][2 * r + 1]);
-                }
-                for (int c = t; c < CS; c += 4) {
-                    cluster.map_shared_rank(&in->m[rank][0], c)[row] = a.m[r];
-                    cluster.map_shared_rank(&in->l[rank][0], c)[row] = a.l[r];
-                }
+            for (int i = 0; i < NO / kWarps; ++i) {
+                const int j = warp * (NO / kWarps) + i, seg = row * SEGS + j / 4;
+                float* to = cluster.map_shared_rank(&in->o[0], seg % CS) + (seg / CS * CS + rank) * 32 +
+                            8 * (j % 4) + 2 * t;
+                *reinterpret_cast<float2*>(to) = make_float2(mine[i][2 * r], mine[i][2 * r + 1]);
+            }
+            const int c = 4 * warp + t;  // kMaxCluster of them
+            if (c < CS) {
+                cluster.map_shared_rank(&in->m[rank][0], c)[row] = a.m[r];
+                cluster.map_shared_rank(&in->l[rank][0], c)[row] = a.l[r];
             }
         }
     }
@@ -855,12 +906,25 @@ __global__ void __launch_bounds__(kThreads, 2) direct_kernel(const __grid_consta
     feed.begin(s, kvh, n, tb + warp, te, 0);
     attend<E, D, kWide, kScores>(p, feed, s, kvh, tb + warp, te, lane, a);
     cp_async_wait<0>();
-    join_splits<D>(p, reinterpret_cast<float*>(smem), warp, lane, a);
+    constexpr int COLS = D / 8 / kWarps;
+    float o[COLS][kWide ? 4 : 2];
+    join_warps<D, kWide>(reinterpret_cast<float*>(smem), warp, lane, a, o);
     if (p.cs > 1) {
-        join_cluster<E, D, kWide, kScores>(p, s, kvh, n, tb, te, &in, warp, lane, a, s_m, s_inv);
+        join_cluster<E, D, kWide, kScores>(p, s, kvh, n, tb, te, &in, warp, lane, a, o, s_m, s_inv);
         return;
     }
-    if (warp == 0) write_rows<E, D, kWide>(p, s, kvh, lane, a);
+#pragma unroll
+    for (int r = 0; r < (kWide ? 2 : 1); ++r) {
+        const int row = (lane >> 2) + 8 * r;
+        if (row < p.G) {
+            const float inv = a.l[r] > 0.f || a.l[r] != a.l[r] ? 1.f / a.l[r] : 0.f;
+            uint16_t* dst = static_cast<uint16_t*>(p.out) +
+                            ((int64_t)s * p.H + (int64_t)kvh * p.G + row) * D + 8 * COLS * warp + 2 * (lane & 3);
+#pragma unroll
+            for (int j = 0; j < COLS; ++j)
+                *reinterpret_cast<uint32_t*>(dst + 8 * j) = E::from_float2(o[j][2 * r] * inv, o[j][2 * r + 1] * inv);
+        }
+    }
     if constexpr (kScores) {  // the z of this unit were written by this CTA
         if (warp == 0 && (lane & 3) == 0) {
 #pragma unroll
@@ -942,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 2) split_kernel(const __grid_constan
         attend<E, D, kWide, kScores>(p, feed, r.s, kvh, r.tb + split, te, lane, a);
         if (!feed.chained()) {
             cp_async_wait<0>();
-            join_splits<D>(p, reinterpret_cast<float*>(smem), warp, lane, a);
+            join_splits<D, kWide>(p, reinterpret_cast<float*>(smem), warp, lane, a);
         }
         const bool whole = r.tb == 0 && te == T;
         if (split == 0) {
