@@ -81,7 +81,10 @@ using pkv::Mma;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxRanges = 1536;   // CTAs of a split call
-constexpr int kMinRange = 8;       // tiles of a large range
+// Tiles of a large range at least: a range of 8 is a chain of unit ends (100
+// requests of 1..64 tokens: 19.9 us with 8, 10.9 with 2; one head of a
+// 30000-token window: 16.5 and 14.0).
+constexpr int kMinRange = 2;
 constexpr int kMinSmall = 4;       // and of a small one: a ring is at most two ranges ahead
 constexpr int kMaxGroup = 16;      // query heads per KV head
 constexpr int kMaxCluster = 16;    // CTAs that share a unit in a direct call
@@ -1369,11 +1372,15 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const __grid_cons
 // Host
 // ---------------------------------------------------------------------------
 // Direct calls: visible tokens per CTA at most, and CTAs in multiples of the
-// resident ones.  16 requests of 2000 tokens, 8 KV heads: direct 26.5 us, split
-// 32.2; 256 requests of 500: direct 90, split 87; a longer share per CTA (2048) loses
-// where few CTAs run (one 32768-token context, scores: 48 us against 36).
+// resident ones.  A wave of CTAs costs 3 us beside its bytes, a split call 6 to 9
+// and with scores 10 to 20, but there it streams while units end.  Windows, direct
+// and split: 100 requests of 1..64, 8 KV heads (2.6 waves) 8.2 and 10.9 us, of
+// 1..1000 40.2 and 41.6, 148 of 1..500 (3.9 waves) 33.4 and 34.5; 256 of 500 (6.7)
+// 90 and 86.  With scores 100 requests of 1..200 19.1 and 20.5, of 1..1000 48.4 and
+// 47.1, 148 of 100..250 32.8 and 30.1.  A longer share per CTA (2048) loses where
+// few CTAs run (one 32768-token context, scores: 48 us against 36).
 constexpr int kDirectTokens = 1024;
-constexpr int kDirectWaves = 2;
+constexpr int direct_waves(bool scores, int64_t most) { return !scores ? 4 : most <= 256 ? 3 : 2; }
 constexpr int kJoinCtasPerSm = 3;   // of the join kernel
 constexpr int kCtasPerSm = 2;       // of the attention kernels
 constexpr int kMinUnits = 16;       // of a split call, else fewer KV heads per unit
@@ -1541,15 +1548,16 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     KernelFn split_fn = with_scores ? pick_attend<true, false>(dtype, D, wide) : pick_attend<false, false>(dtype, D, wide);
     const int sms = pkv::sm_count();
     // direct: the smallest cluster that leaves kDirectTokens per CTA; more CTAs
-    // while they still fit the card at once and have a tile per warp
+    // while they still fit the card at once and have a tile per warp (a cluster's
+    // join costs as much as two more tiles: 150 tokens 4.4 us in one CTA, 5.1 in two)
     const int64_t slots = (int64_t)kCtasPerSm * sms;
     p.cs = 1;
     while (p.cs < kMaxCluster && most > (int64_t)kDirectTokens * p.cs) p.cs *= 2;
     const bool direct = most <= (int64_t)kDirectTokens * p.cs &&
-                        (int64_t)S * Hkv * p.cs <= kDirectWaves * slots;
+                        (int64_t)S * Hkv * p.cs <= direct_waves(with_scores, most) * slots;
     if (direct)
         while (p.cs < kMaxCluster && (int64_t)S * Hkv * p.cs * 2 <= slots &&
-               most > (int64_t)2 * kWarps * tile * p.cs)
+               most > (int64_t)(p.cs == 1 ? 3 : 2) * kWarps * tile * p.cs)
             p.cs *= 2;
     p.hw = direct ? 1 : heads_per_cta(Hkv);
     while (!direct && p.hw > 1 && (int64_t)S * Hkv / p.hw < kMinUnits) p.hw /= 2;
