@@ -143,6 +143,9 @@ __device__ __forceinline__ int visible_of(const Params& p, int n) {
     return most < n ? (int)most : n;
 }
 
+// 1 / L, 0 for a row that sees nothing.
+__device__ __forceinline__ float inverse_of(float L) { return L > 0.f || L != L ? 1.f / L : 0.f; }
+
 // Tiles of a unit; an empty context has one, which writes zeros.
 __device__ __forceinline__ int tiles_of(const Params& p, int n) {
     const int t = (visible_of(p, n) + (1 << p.tile_log2) - 1) >> p.tile_log2;
@@ -730,39 +733,57 @@ __device__ __forceinline__ void join_warps(float* ring, int warp, int lane, Acc<
 }
 
 // scores[s, kvh, j] += sum over the group's heads of 2^(z - M) / L for the
-// tokens j0 <= j < j1 (j0 a multiple of 16) by threads tid, tid + threads, ...:
-// four tokens per thread and round.  s_m and s_inv hold M and 1 / L (0 for an
-// empty row) of the G heads.  Each score is added to by one thread, heads in
-// order.
+// tokens j0 <= j < j1 (j0 a multiple of 16) by `threads` threads.  s_m and s_inv
+// hold M and 1 / L (0 for an empty row) of the G heads.  Four tokens per thread
+// and round; P = 1, 2 or 4 neighbouring threads share them, four heads each, so
+// that all loads of a round go out together (150 tokens, 16 heads, the call: 7.0
+// us, a thread for all heads 8.5).  Every sum has a fixed order.
 __device__ __forceinline__ void fold_weights(const Params& p, int s, int kvh, int j0, int j1,
                                              const float* s_m, const float* s_inv, int tid,
                                              int threads) {
     const float* z = p.z + ((int64_t)s * p.H + (int64_t)kvh * p.G) * p.z_stride;
     float* sc = p.scores + ((int64_t)s * p.Hkv + kvh) * p.score_stride;
     const bool vec = (reinterpret_cast<uintptr_t>(sc) & 15u) == 0;
-    for (int j = j0 + 4 * tid; j < j1; j += 4 * threads) {
-        const bool full = j + 4 <= j1;
+    const int shift = p.G > 8 ? 2 : p.G > 4 ? 1 : 0, P = 1 << shift, part = tid & (P - 1);
+    for (int base = j0; base < j1; base += 4 * (threads >> shift)) {
+        const int j = base + 4 * (tid >> shift);
+        const bool full = vec && j + 4 <= j1;
         float old[4];
-        if (vec && full) {
-            const float4 v = *reinterpret_cast<const float4*>(sc + j);
-            old[0] = v.x; old[1] = v.y; old[2] = v.z; old[3] = v.w;
-        } else {
+        if (part == 0) {
+            if (full) {
+                const float4 x = *reinterpret_cast<const float4*>(sc + j);
+                old[0] = x.x; old[1] = x.y; old[2] = x.z; old[3] = x.w;
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) old[e] = j + e < j1 ? sc[j + e] : 0.f;
-        }
-        float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int r = 0; r < p.G; ++r) {
-            const float4 v = *reinterpret_cast<const float4*>(z + r * p.z_stride + j);
-            const float inv = s_inv[r], m = s_m[r];
-            if (inv != 0.f) {
-                w[0] = fmaf(exp2f(v.x - m), inv, w[0]);
-                w[1] = fmaf(exp2f(v.y - m), inv, w[1]);
-                w[2] = fmaf(exp2f(v.z - m), inv, w[2]);
-                w[3] = fmaf(exp2f(v.w - m), inv, w[3]);
+                for (int e = 0; e < 4; ++e) old[e] = j + e < j1 ? sc[j + e] : 0.f;
             }
         }
-        if (vec && full) {
+        float4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (q * P >= p.G) break;
+            const int r = part + q * P;
+            v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j < j1 && r < p.G) v[q] = *reinterpret_cast<const float4*>(z + r * p.z_stride + j);
+        }
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (q * P >= p.G) break;
+            const int r = part + q * P;
+            const float m = s_m[r], inv = r < p.G ? s_inv[r] : 0.f;
+            if (inv != 0.f) {
+                w[0] = fmaf(exp2f(v[q].x - m), inv, w[0]);
+                w[1] = fmaf(exp2f(v[q].y - m), inv, w[1]);
+                w[2] = fmaf(exp2f(v[q].z - m), inv, w[2]);
+                w[3] = fmaf(exp2f(v[q].w - m), inv, w[3]);
+            }
+        }
+        for (int x = 1; x < P; x <<= 1)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] += __shfl_xor_sync(kFull, w[e], x);
+        if (part != 0) continue;
+        if (full) {
             *reinterpret_cast<float4*>(sc + j) =
                 make_float4(old[0] + w[0], old[1] + w[1], old[2] + w[2], old[3] + w[3]);
         } else {
@@ -823,25 +844,50 @@ __device__ __forceinline__ void join_cluster(const Params& p, int s, int kvh, in
     }
     cluster_arrive();
     cluster_wait();
-    // M and 1 / L of a row, and lane i's weight 2^(m_i - M) for CTA i
-    auto row_of = [&](int row, float& M, float& w, float& inv) {
-        const float m = lane < CS ? in->m[lane][row] : -INFINITY;
-        const float l = lane < CS ? in->l[lane][row] : 0.f;
-        M = m;
+    // M and 1 / L of a row, and the CTAs' weights 2^(m_i - M): with scores, which
+    // need all rows' in every CTA, by a thread per row and before the rest (over
+    // m); without, by the lanes of the warp that joins a segment (a 4096-token
+    // window: 8.2 us, 8.5 the other way)
+    if constexpr (kScores) {
+        if (tid < p.G) {
+            float m[kMaxCluster], l[kMaxCluster], M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int o = kMaxCluster / 2; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-        M = __shfl_sync(kFull, M, 0);
-        w = lane < CS ? exp2f(m - (M == -INFINITY ? 0.f : M)) : 0.f;
-        float L = w * l;
+            for (int i = 0; i < kMaxCluster; ++i) {
+                m[i] = i < CS ? in->m[i][tid] : -INFINITY;
+                l[i] = i < CS ? in->l[i][tid] : 0.f;
+            }
 #pragma unroll
-        for (int o = kMaxCluster / 2; o >= 1; o >>= 1) L += __shfl_xor_sync(kFull, L, o);
-        L = __shfl_sync(kFull, L, 0);
-        inv = L > 0.f || L != L ? 1.f / L : 0.f;
-    };
+            for (int i = 0; i < kMaxCluster; ++i) M = fmaxf(M, m[i]);
+            const float use = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int i = 0; i < kMaxCluster; ++i) {
+                m[i] = exp2f(m[i] - use);
+                L = fmaf(m[i], l[i], L);
+                if (i < CS) in->m[i][tid] = m[i];
+            }
+            s_m[tid] = M;
+            s_inv[tid] = inverse_of(L);
+        }
+        __syncthreads();
+    }
     for (int k = warp; k * CS + rank < p.G * SEGS; k += kWarps) {
         const int seg = k * CS + rank, row = seg / SEGS;
-        float M, w, inv, o = 0.f;
-        row_of(row, M, w, inv);
+        float w, inv, o = 0.f;  // w: of CTA `lane`
+        if constexpr (kScores) {
+            w = lane < CS ? in->m[lane][row] : 0.f;
+            inv = s_inv[row];
+        } else {
+            const float m = lane < CS ? in->m[lane][row] : -INFINITY;
+            float M = m;
+#pragma unroll
+            for (int x = kMaxCluster / 2; x >= 1; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
+            M = __shfl_sync(kFull, M, 0);
+            w = lane < CS ? exp2f(m - (M == -INFINITY ? 0.f : M)) : 0.f;
+            float L = lane < CS ? w * in->l[lane][row] : 0.f;
+#pragma unroll
+            for (int x = kMaxCluster / 2; x >= 1; x >>= 1) L += __shfl_xor_sync(kFull, L, x);
+            inv = inverse_of(__shfl_sync(kFull, L, 0));
+        }
         for (int i = 0; i < CS; ++i) o = fmaf(__shfl_sync(kFull, w, i), in->o[(k * CS + i) * 32 + lane], o);
         o *= inv;
         const float next = __shfl_down_sync(kFull, o, 1);
@@ -849,18 +895,8 @@ __device__ __forceinline__ void join_cluster(const Params& p, int s, int kvh, in
                         ((int64_t)s * p.H + (int64_t)kvh * p.G + row) * D + seg % SEGS * 32 + lane;
         if ((lane & 1) == 0) *reinterpret_cast<uint32_t*>(dst) = E::from_float2(o, next);
     }
-    if constexpr (kScores) {
-        for (int row = warp; row < p.G; row += kWarps) {
-            float M, w, inv;
-            row_of(row, M, w, inv);
-            if (lane == 0) {
-                s_m[row] = M;
-                s_inv[row] = inv;
-            }
-        }
-        __syncthreads();
+    if constexpr (kScores)
         fold_weights(p, s, kvh, tb * kTile<D>, min(te * kTile<D>, n), s_m, s_inv, tid, kThreads);
-    }
 }
 
 // Writes the finished rows of a unit (the warp's part of the accumulators).
@@ -871,7 +907,7 @@ __device__ __forceinline__ void write_rows(const Params& p, int s, int kvh, int 
     for (int r = 0; r < (kWide ? 2 : 1); ++r) {
         const int row = g + 8 * r;
         if (row < p.G) {
-            const float inv = a.l[r] > 0.f || a.l[r] != a.l[r] ? 1.f / a.l[r] : 0.f;
+            const float inv = inverse_of(a.l[r]);
             uint16_t* dst = static_cast<uint16_t*>(p.out) +
                             ((int64_t)s * p.H + (int64_t)kvh * p.G + row) * D + 2 * t;
 #pragma unroll
@@ -920,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 2) direct_kernel(const __grid_consta
     for (int r = 0; r < (kWide ? 2 : 1); ++r) {
         const int row = (lane >> 2) + 8 * r;
         if (row < p.G) {
-            const float inv = a.l[r] > 0.f || a.l[r] != a.l[r] ? 1.f / a.l[r] : 0.f;
+            const float inv = inverse_of(a.l[r]);
             uint16_t* dst = static_cast<uint16_t*>(p.out) +
                             ((int64_t)s * p.H + (int64_t)kvh * p.G + row) * D + 8 * COLS * warp + 2 * (lane & 3);
 #pragma unroll
@@ -933,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, 2) direct_kernel(const __grid_consta
 #pragma unroll
             for (int r = 0; r < (kWide ? 2 : 1); ++r) {
                 s_m[(lane >> 2) + 8 * r] = a.m[r];
-                s_inv[(lane >> 2) + 8 * r] = a.l[r] > 0.f || a.l[r] != a.l[r] ? 1.f / a.l[r] : 0.f;
+                s_inv[(lane >> 2) + 8 * r] = inverse_of(a.l[r]);
             }
         }
         __syncthreads();
@@ -1076,8 +1112,6 @@ __device__ __forceinline__ void merge_ml(float& M, float& L, float m, float l) {
     L = L * exp2f(M - use) + l * exp2f(m - use);
     M = m_new;
 }
-
-__device__ __forceinline__ float inverse_of(float L) { return L > 0.f || L != L ? 1.f / L : 0.f; }
 
 // Row i of a unit's hw * G over the pieces c, c + step, ... <= c1 (c0: the range
 // where the unit begins), U pieces' loads in flight: (M, L) and the unnormalised
@@ -1549,7 +1583,8 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     const int sms = pkv::sm_count();
     // direct: the smallest cluster that leaves kDirectTokens per CTA; more CTAs
     // while they still fit the card at once and have a tile per warp (a cluster's
-    // join costs as much as two more tiles: 150 tokens 4.4 us in one CTA, 5.1 in two)
+    // join costs as much as two or, of many rows, three more tiles: 150 tokens 4.4 us
+    // in one CTA, 5.1 in two; 220 tokens, 8 query heads a head: 5.2 and 6.0)
     const int64_t slots = (int64_t)kCtasPerSm * sms;
     p.cs = 1;
     while (p.cs < kMaxCluster && most > (int64_t)kDirectTokens * p.cs) p.cs *= 2;
@@ -1557,7 +1592,7 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
                         (int64_t)S * Hkv * p.cs <= direct_waves(with_scores, most) * slots;
     if (direct)
         while (p.cs < kMaxCluster && (int64_t)S * Hkv * p.cs * 2 <= slots &&
-               most > (int64_t)(p.cs == 1 ? 3 : 2) * kWarps * tile * p.cs)
+               most > (int64_t)(p.cs > 1 ? 2 : p.G > 4 ? 4 : 3) * kWarps * tile * p.cs)
             p.cs *= 2;
     p.hw = direct ? 1 : heads_per_cta(Hkv);
     while (!direct && p.hw > 1 && (int64_t)S * Hkv / p.hw < kMinUnits) p.hw /= 2;
