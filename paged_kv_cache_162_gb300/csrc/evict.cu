@@ -45,8 +45,14 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kManyThreads = 256;
+// CTAs of 128 threads for short rows, longer ones where the rows do not all fit
+// the card at once: 512 rows of 65..130 tokens 5.8 us (256 threads 6.2), 2048 8.2
+// (12.1), 3472 of 303 31.7 (40.0); but 128 rows of 130..260 6.5 (6.0).
+constexpr int kSmallThreads = 128;
+constexpr int kSmallCtas = 8;         // per SM
+constexpr int kSmallKeys = 160;
+constexpr int kSmallKeysWaiting = 320;
 constexpr int kMaxCluster = 8;
 constexpr int kFewKeys = 2048;        // a row of fewer is one CTA's
 // A row of more keys is several CTAs': 8 x 32768 to 4096, 32 heads: 213 us with
@@ -126,14 +132,15 @@ __device__ __forceinline__ void store4(T* p, int count, bool vec, const T (&v)[4
 // wait for a place on the card: more of the moves are in flight (256 mixed
 // requests: 219 us, with four 236).  Four (64) where all rows have one: a row is
 // done sooner (64 requests in steady state: 12.0 us, with five 13.9).
-template <int D, bool kCluster, int kMinCtas>
+template <int D, bool kCluster, int kThreads, int kMinCtas>
 __global__ void __launch_bounds__(kThreads, kMinCtas) evict_kernel(Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     extern __shared__ __align__(16) uint32_t s_keys[];
+    constexpr int kWarps = kThreads / 32;
     // digits of 11 bits, or of 8 in a cluster, where every CTA reads every
-    // histogram
-    constexpr int BITS = kCluster ? 8 : 11, PASSES = (31 + BITS) / BITS;
+    // histogram, and for a few keys, which a second digit mostly tells apart
+    constexpr int BITS = kCluster || kThreads < 256 ? 8 : 11, PASSES = (31 + BITS) / BITS;
     constexpr int BINS = 1 << BITS, BPT = BINS / kThreads;  // bins per thread
     __shared__ __align__(16) int s_hist[2][BINS];
     __shared__ int s_sum[kWarps];
@@ -521,9 +528,11 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 size_t list_bytes(int S, int Hkv, int budget) { return align256((size_t)S * Hkv * budget * sizeof(int32_t)); }
 
-template <int D, int kMinCtas>
-void (*pick(int cs))(Params) {
-    return cs > 1 ? evict_kernel<D, true, kMinCtas> : evict_kernel<D, false, kMinCtas>;
+template <int D>
+void (*pick(int cs, bool small, bool wait))(Params) {
+    if (small) return evict_kernel<D, false, kSmallThreads, kSmallCtas>;
+    if (cs > 1) return wait ? evict_kernel<D, true, kManyThreads, 5> : evict_kernel<D, true, kManyThreads, 4>;
+    return wait ? evict_kernel<D, false, kManyThreads, 5> : evict_kernel<D, false, kManyThreads, 4>;
 }
 
 // Allows the kernel its shared memory (once per device).
@@ -631,8 +640,8 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
     const int seg = ((p.max_ctx + cs - 1) / cs + kChunk - 1) / kChunk * kChunk;
     p.seg_cap = seg < kSmemKeys ? seg : kSmemKeys;
     const bool wait = rows * cs > 4 * pkv::sm_count();
-    void (*fn)(Params) = D == 128 ? (wait ? pick<128, 5>(cs) : pick<128, 4>(cs))
-                                  : (wait ? pick<64, 5>(cs) : pick<64, 4>(cs));
+    const bool small = cs == 1 && p.max_ctx <= (rows > 5 * pkv::sm_count() ? kSmallKeysWaiting : kSmallKeys);
+    void (*fn)(Params) = D == 128 ? pick<128>(cs, small, wait) : pick<64>(cs, small, wait);
     if (!ready(fn, kSmemKeys * 4)) return pkv::fail(PKV_ERR_CUDA, "evict_tokens: shared memory");
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -643,7 +652,7 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * cs));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(small ? kSmallThreads : kManyThreads);
     cfg.dynamicSmemBytes = (size_t)p.seg_cap * 4;
     cfg.stream = pkv::as_stream(stream);
     cfg.attrs = attr;
