@@ -45,14 +45,15 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kManyThreads = 256;
-// CTAs of 128 threads for short rows, longer ones where the rows do not all fit
-// the card at once: 512 rows of 65..130 tokens 5.8 us (256 threads 6.2), 2048 8.2
-// (12.1), 3472 of 303 31.7 (40.0); but 128 rows of 130..260 6.5 (6.0).
-constexpr int kSmallThreads = 128;
-constexpr int kSmallCtas = 8;         // per SM
+// Threads of a CTA: 256, or
+// 128 for short rows, longer ones where the rows do not all fit the card at
+// once: 512 rows of 65..130 tokens 5.8 us (256 threads 6.2), 2048 8.2 (12.1), 3472
+// of 303 31.7 (40.0); but 128 rows of 130..260 6.5 (6.0);
 constexpr int kSmallKeys = 160;
 constexpr int kSmallKeysWaiting = 320;
+// 512 where there is room for it and a CTA may have this many moves: 128 rows of
+// 500..1000 to 500 10.1 us (256 threads 15.7); but 128 of 484..500 to 484 5.4 (4.8).
+constexpr int kManyMoves = 256;
 constexpr int kMaxCluster = 8;
 constexpr int kFewKeys = 2048;        // a row of fewer is one CTA's
 // A row of more keys is several CTAs': 8 x 32768 to 4096, 32 heads: 213 us with
@@ -128,10 +129,11 @@ __device__ __forceinline__ void store4(T* p, int count, bool vec, const T (&v)[4
     }
 }
 
-// kMinCtas: CTAs per SM the registers allow.  Five (48 registers) where rows
-// wait for a place on the card: more of the moves are in flight (256 mixed
-// requests: 219 us, with four 236).  Four (64) where all rows have one: a row is
-// done sooner (64 requests in steady state: 12.0 us, with five 13.9).
+// kMinCtas: CTAs per SM the registers allow, of 256 threads four or five.  Five
+// (48 registers) where rows wait for a place on the card: more of the moves are in
+// flight (256 mixed requests: 219 us, with four 236).  Four (64) where all rows
+// have one: a row is done sooner (64 requests in steady state: 12.0 us, with five
+// 13.9).
 template <int D, bool kCluster, int kThreads, int kMinCtas>
 __global__ void __launch_bounds__(kThreads, kMinCtas) evict_kernel(Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) evict_kernel(Params p) {
     // digits of 11 bits, or of 8 in a cluster, where every CTA reads every
     // histogram, and for a few keys, which a second digit mostly tells apart
     constexpr int BITS = kCluster || kThreads < 256 ? 8 : 11, PASSES = (31 + BITS) / BITS;
-    constexpr int BINS = 1 << BITS, BPT = BINS / kThreads;  // bins per thread
+    constexpr int BINS = 1 << BITS, BPT = BINS > kThreads ? BINS / kThreads : 1;  // bins per thread
     __shared__ __align__(16) int s_hist[2][BINS];
     __shared__ int s_sum[kWarps];
     __shared__ int s_pick[3];
@@ -154,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) evict_kernel(Params p) {
         if constexpr (kCluster) cluster.sync(); else __syncthreads();
     };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool has_bins = BPT * kThreads == BINS || tid < BINS;
     const int row = blockIdx.x / CS;
     const int s = row / p.Hkv, h = row % p.Hkv;
 
@@ -161,7 +164,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) evict_kernel(Params p) {
     int N = __ldg(p.token_counts + s);
     auto clear = [&](int which) {
 #pragma unroll
-        for (int i = 0; i < BPT; ++i) s_hist[which][i * kThreads + tid] = 0;
+        for (int i = 0; i < BPT; ++i)
+            if (has_bins) s_hist[which][i * kThreads + tid] = 0;
     };
     clear(0);
     clear(1);
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) evict_kernel(Params p) {
         int c[BPT], sum = 0;
 #pragma unroll
         for (int i = 0; i < BPT; ++i) c[i] = 0;
-        for (int r = 0; r < CS; ++r) {
+        for (int r = 0; has_bins && r < CS; ++r) {
             const int* hist = &s_hist[pass & 1][BPT * tid];
             if constexpr (kCluster) hist = cluster.map_shared_rank(hist, r);
             if constexpr (BPT == 8) {
@@ -529,10 +533,11 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 size_t list_bytes(int S, int Hkv, int budget) { return align256((size_t)S * Hkv * budget * sizeof(int32_t)); }
 
 template <int D>
-void (*pick(int cs, bool small, bool wait))(Params) {
-    if (small) return evict_kernel<D, false, kSmallThreads, kSmallCtas>;
-    if (cs > 1) return wait ? evict_kernel<D, true, kManyThreads, 5> : evict_kernel<D, true, kManyThreads, 4>;
-    return wait ? evict_kernel<D, false, kManyThreads, 5> : evict_kernel<D, false, kManyThreads, 4>;
+void (*pick(int cs, int threads, bool wait))(Params) {
+    if (threads == 128) return evict_kernel<D, false, 128, 8>;
+    if (threads == 512) return cs > 1 ? evict_kernel<D, true, 512, 2> : evict_kernel<D, false, 512, 2>;
+    if (cs > 1) return wait ? evict_kernel<D, true, 256, 5> : evict_kernel<D, true, 256, 4>;
+    return wait ? evict_kernel<D, false, 256, 5> : evict_kernel<D, false, 256, 4>;
 }
 
 // Allows the kernel its shared memory (once per device).
@@ -640,8 +645,11 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
     const int seg = ((p.max_ctx + cs - 1) / cs + kChunk - 1) / kChunk * kChunk;
     p.seg_cap = seg < kSmemKeys ? seg : kSmemKeys;
     const bool wait = rows * cs > 4 * pkv::sm_count();
-    const bool small = cs == 1 && p.max_ctx <= (rows > 5 * pkv::sm_count() ? kSmallKeysWaiting : kSmallKeys);
-    void (*fn)(Params) = D == 128 ? pick<128>(cs, small, wait) : pick<64>(cs, small, wait);
+    const int sms = pkv::sm_count();
+    const int moves = p.max_ctx - budget < budget ? p.max_ctx - budget : budget;  // of a row at most
+    const int threads = cs == 1 && p.max_ctx <= (rows > 5 * sms ? kSmallKeysWaiting : kSmallKeys) ? 128
+                        : rows * cs <= 2 * sms && moves / cs >= kManyMoves ? 512 : 256;
+    void (*fn)(Params) = D == 128 ? pick<128>(cs, threads, wait) : pick<64>(cs, threads, wait);
     if (!ready(fn, kSmemKeys * 4)) return pkv::fail(PKV_ERR_CUDA, "evict_tokens: shared memory");
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -652,7 +660,7 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * cs));
-    cfg.blockDim = dim3(small ? kSmallThreads : kManyThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = (size_t)p.seg_cap * 4;
     cfg.stream = pkv::as_stream(stream);
     cfg.attrs = attr;
