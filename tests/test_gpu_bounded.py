@@ -632,3 +632,37 @@ def test_evict_with_one_output_in_place(scores_in_place):
     assert np.array_equal(d["k"].view(torch.int16).cpu().numpy(), k)
     other, was = (pos, p0) if scores_in_place else (score, s0)
     assert torch.equal(other.view(torch.int32), was.view(torch.int32)), "an input that is no output stays"
+
+
+# ------------------------------------------------- every form a call can take
+@pytest.mark.parametrize("S,H,Hkv,D,lo,hi", [
+    (100, 8, 8, 128, 0, 40),       # waves of direct CTAs
+    (140, 16, 8, 64, 100, 250),    # the same, split with scores
+    (300, 16, 8, 64, 0, 64),       # split, ranges of two tiles, a warp per head
+    (900, 6, 2, 128, 1, 30),       # two warps per head
+    (700, 5, 5, 64, 1, 70),        # four
+    (1, 64, 4, 128, 220, 220),     # one CTA per head, four threads fold a token
+    (2, 40, 5, 64, 600, 700),      # clusters, two threads
+    (3, 30, 3, 128, 1900, 2100)])
+def test_forms_of_attention(S, H, Hkv, D, lo, hi):
+    rng = np.random.default_rng(S + H)
+    lens = rng.integers(lo, hi + 1, S)
+    c = make(S + D, S, H, Hkv, D, 16, "bf16" if D == 128 else "f16", lens)
+    check_window(c, hi, 0)
+    check_window(c, max(1, hi // 2), 3)
+    check_accumulate(c, cap=c["MB"] * 16 + 4 * (S % 2))
+
+
+@pytest.mark.parametrize("S,Hkv,D,lo,hi,budget", [
+    (100, 7, 64, 300, 420, 200),       # rows that wait for a place
+    (110, 7, 128, 200, 300, 90),       # the same with short rows
+    (30, 4, 128, 100, 150, 140),       # short rows
+    (16, 8, 64, 400, 1000, 480),       # room for larger CTAs, many moves
+    (2, 3, 128, 6000, 9000, 3001),     # clusters of them
+    (2, 2, 64, 6000, 9000, 8800)])     # clusters, few moves
+def test_forms_of_eviction(S, Hkv, D, lo, hi, budget):
+    rng = np.random.default_rng(S + hi)
+    lens = rng.integers(lo, hi + 1, S)
+    lens[0] = hi
+    c = evict_case(S + D, S, Hkv, D, 32, "f16", lens, budget)
+    check_evict(c, budget, budget // 3, 5, in_place=bool(S % 4))
