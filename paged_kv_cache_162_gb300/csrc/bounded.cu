@@ -51,8 +51,8 @@
 //   accumulate, 256 requests of 16..4096 (median 512), 32 heads on 8  155 us  82 %
 //   window 4096 of one 32768-token context, 32 heads on 8            8.3 us  30 %
 //   4 requests of at most 100 tokens, 4 heads of 64       2.8 us, with scores 3.5
-// The split kernel reads each byte once (843.9 MB for 843.4) at 84 % of the DRAM
-// peak with its tensor pipe 28 % busy.  About 4 us go before every ring is full
+// The split kernel moves each byte once (847.5 MB for 843.4) at 83 % of the DRAM
+// peak with its tensor pipe 26 % busy.  About 4 us go before every ring is full
 // (length -> place -> table -> rows), 3 to the last ranges; the second kernel takes
 // 4 us without scores and 10 to 15 with them.  The small calls are that chain.
 #include <cooperative_groups.h>

@@ -30,7 +30,7 @@
 //   64 requests of 2064 to 2048, 8 heads: 16 moves a row     10.4 us  36 %
 //   4 requests of 50..100 to 48, 4 heads of 64                4.9 us
 // The last two are the chain length -> keys -> histogram -> counts -> lists ->
-// rows, about a microsecond a link.  In the first, DRAM moves 1217 MB at 69 % of its
+// rows, about a microsecond a link.  In the first, DRAM moves 1217 MB at 70 % of its
 // peak, reads and writes of 256 bytes in turn.
 #include <cooperative_groups.h>
 
