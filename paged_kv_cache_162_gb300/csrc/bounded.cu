@@ -173,14 +173,16 @@ struct RangeMap {
         small = 0;
         if (n_small > 0) {
             small = per * (16 - kLargeShare) / 16 / n_small;
-            if (small < kMinSmall) small = 0;  // too little to share out: one range each
+            // too little to share out: one range each, and numbers without gaps (a
+            // unit's pieces are those of all ranges from its first to its last)
+            if (small < kMinSmall) small = n_small = 0;
             large = per - n_small * small;
         }
         slot = per;
     }
     // the range of the id-th CTA launched
     __device__ __forceinline__ int of_cta(int id) const {
-        if (id < n_large) return id * (1 + n_small);
+        if (id < n_large || n_small == 0) return id * (1 + n_small);  // n_large and up, no small ones: empty
         return (id - n_large) / n_small * (1 + n_small) + 1 + (id - n_large) % n_small;
     }
     __device__ __forceinline__ long long begin(int c) const {

@@ -666,3 +666,15 @@ def test_forms_of_eviction(S, Hkv, D, lo, hi, budget):
     lens[0] = hi
     c = evict_case(S + D, S, Hkv, D, 32, "f16", lens, budget)
     check_evict(c, budget, budget // 3, 5, in_place=bool(S % 4))
+
+
+@pytest.mark.parametrize("S,H,Hkv,D,hi", [(60, 64, 32, 128, 400), (70, 32, 32, 64, 900), (300, 16, 8, 128, 300)])
+def test_lengths_far_below_the_bound_on_a_used_workspace(S, H, Hkv, D, hi):
+    """Small ranges for the bound, but none for the lengths: a unit's pieces
+    are those of its ranges, not what lies between them in the workspace."""
+    rng = np.random.default_rng(S)
+    c = make(S + D, S, H, Hkv, D, 16, "bf16", rng.integers(0, hi + 1, S), MB=64)
+    ws = E.new_window_workspace(S, H, Hkv, D)
+    check_window(c, 1024, 0, workspace=ws.fill_(255))
+    ws = E.new_accumulate_workspace(S, H, Hkv, D, 1024)
+    check_accumulate(c, workspace=ws.fill_(255))
