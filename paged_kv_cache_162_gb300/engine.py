@@ -185,17 +185,21 @@ def _attention_sizes(who, out, q, k_cache, v_cache, block_tables, context_lens):
     return S, H, D, NB, bs, Hkv, tshape[1], dev
 
 
+def _as_stream(stream, device):
+    """`stream`, a torch stream or a handle, as a torch stream."""
+    return torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+
+
 def _workspace(who, nbytes, device, stream=None):
-    """A workspace for one call; its memory stays taken until the call's
-    stream has passed."""
+    """A workspace for one call on `stream` (None: the current one), out of
+    the memory of that stream: what another stream has given back may still
+    be in use there, and what this call gives back is its stream's again."""
     if nbytes == 0:
         _refuse(f"{who}: bad workspace arguments (H a multiple of Hkv, at most 16 per group?)")
-    ws = torch.empty(nbytes, dtype=_U8, device=device)
-    if stream is not None:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=device)
-        ws.record_stream(stream)
-    return ws
+    if stream is None:
+        return torch.empty(nbytes, dtype=_U8, device=device)
+    with torch.cuda.stream(_as_stream(stream, device)):
+        return torch.empty(nbytes, dtype=_U8, device=device)
 
 
 def _check_workspace(who, ws, dev):

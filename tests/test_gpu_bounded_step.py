@@ -1,0 +1,45 @@
+"""Bounded-cache calls on streams of their own, and DecodeStep's over more
+than one cycle, against the 64-bit definitions."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import bounded as B
+from paged_kv_cache_162_gb300 import _lib as L
+from paged_kv_cache_162_gb300 import engine as E
+from tests.test_gpu_bounded import check_out, dev, f64, make, weight_error
+
+pytestmark = pytest.mark.gpu
+
+
+def keep_busy(rounds=40):
+    """Work of some milliseconds on the current stream."""
+    a = torch.randn(4096, 4096, device="cuda")
+    for _ in range(rounds):
+        a = a @ a * 1e-2
+    return a
+
+
+def test_scratch_is_not_shared_with_another_stream():
+    """A call that makes its own scratch on the current stream gives the
+    memory back while its kernels wait; a call with stream= right after it
+    must not get the same memory."""
+    c = [make(31 + i, 6, 8, 4, 128, 16, "f16", [1500, 700, 2000, 1, 0, 999]) for i in range(2)]
+    side = torch.cuda.Stream()
+    refs = [B.attend(f64(x["q"]), f64(x["k"]), f64(x["v"]), x["tables"], x["lens"], x["scale"]) for x in c]
+    for _ in range(4):
+        d = [dev(x) for x in c]
+        scores = [torch.zeros(6, 4, c[0]["MB"] * 16, device="cuda") for _ in c]
+        torch.cuda.synchronize()
+        keep_busy()
+        for x, y, z, stream in zip(c, d, scores, (None, side)):
+            E.paged_attention_decode_accumulate(y["out"], z, y["q"], y["k"], y["v"], y["tables"], y["lens"],
+                                                x["scale"], stream=stream)
+        torch.cuda.synchronize()
+        for x, y, z, (ref, weights, mag) in zip(c, d, scores, refs):
+            w = weight_error(x)
+            check_out(x, y["out"], ref, mag, w)
+            want = B.accumulate(np.zeros(z.shape), weights, 4)
+            # two query heads per KV head, from zero: (w + 2 e) of what was added, once rounded
+            assert np.all(np.abs(f64(z.cpu()) - want) <= (w + 3 * 2.0 ** -24) * want + 2.0 ** -126)
+    assert L.pkv_get_device_errors() == 0
