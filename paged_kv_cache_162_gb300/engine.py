@@ -12,6 +12,7 @@ The step, in the order a serving loop runs it ("3.3 页面级显存管理" 3.3.2
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import time
@@ -188,6 +189,23 @@ def _attention_sizes(who, out, q, k_cache, v_cache, block_tables, context_lens):
 def _as_stream(stream, device):
     """`stream`, a torch stream or a handle, as a torch stream."""
     return torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+
+
+@contextlib.contextmanager
+def _on(stream, device):
+    """Torch's work inside runs on `stream` (None: the current one), after
+    what the current stream holds by now; what the current stream gets later
+    runs after it."""
+    if stream is None:
+        yield
+        return
+    stream, current = _as_stream(stream, device), torch.cuda.current_stream(device)
+    stream.wait_stream(current)
+    try:
+        with torch.cuda.stream(stream):
+            yield
+    finally:
+        current.wait_stream(stream)
 
 
 def _workspace(who, nbytes, device, stream=None):
@@ -735,7 +753,8 @@ class DecodeStep:
         """decode() over the first sink_tokens tokens and the last `window`
         of each context (see paged_attention_decode_window)."""
         if getattr(self, "_window_ws", None) is None:
-            self._window_ws = new_window_workspace(self.S, self.H, self.H, self.D, self.device)
+            with _on(stream, self.device):
+                self._window_ws = new_window_workspace(self.S, self.H, self.H, self.D, self.device)
         return paged_attention_decode_window(
             self.out, self.q, self.k_cache, self.v_cache, self.block_tables, self.context_lens,
             window, sink_tokens, self.scale, self.max_context_len, self._window_ws, stream)
@@ -746,12 +765,13 @@ class DecodeStep:
         paged_attention_decode_accumulate), which evict() goes by."""
         if getattr(self, "scores", None) is None:
             cap = self.MB * self.bs
-            self.scores = torch.zeros((self.S, self.H, cap), device=self.device)
-            self.positions = torch.full((self.S, self.H, cap), -1, dtype=torch.int32,
-                                        device=self.device)
-            self.token_counts = self.context_lens.clone()
-            self._accumulate_ws = new_accumulate_workspace(self.S, self.H, self.H, self.D,
-                                                           self.max_context_len, self.device)
+            with _on(stream, self.device):
+                self.scores = torch.zeros((self.S, self.H, cap), device=self.device)
+                self.positions = torch.full((self.S, self.H, cap), -1, dtype=torch.int32,
+                                            device=self.device)
+                self.token_counts = self.context_lens.clone()
+                self._accumulate_ws = new_accumulate_workspace(self.S, self.H, self.H, self.D,
+                                                               self.max_context_len, self.device)
         return paged_attention_decode_accumulate(
             self.out, self.scores, self.q, self.k_cache, self.v_cache, self.block_tables,
             self.context_lens, self.scale, self.max_context_len, self._accumulate_ws, stream)
@@ -761,7 +781,14 @@ class DecodeStep:
         sequence (see evict_tokens) and returns the blocks past them to the
         pool.  Blocks that will be written are copied first where they are
         shared (OutOfBlocks if the pool has no room for that: nothing is
-        evicted then).  Returns the number of blocks freed."""
+        evicted then).  With a stream, the eviction runs there after what the
+        current stream holds, and the current stream goes on after it.
+        Returns the number of blocks freed."""
+        with _on(stream, self.device):
+            return self._evict(budget, recent_tokens, sink_tokens)
+
+    def _evict(self, budget, recent_tokens, sink_tokens):
+        """evict() on the current stream, temporary tensors and all."""
         over = [s for s in range(self.S) if self.context_lens_host[s] > budget]
         pairs = []
         try:
@@ -773,12 +800,11 @@ class DecodeStep:
             if len(pairs):
                 check_copy_pairs(pairs, self.NB)
                 self.block_tables = torch.from_numpy(self.tables_host).to(self.device)
-                copy_blocks(self.k_cache, self.v_cache, torch.from_numpy(pairs).to(self.device),
-                            stream)
+                copy_blocks(self.k_cache, self.v_cache, torch.from_numpy(pairs).to(self.device))
         new_lens = torch.empty_like(self.context_lens)
         evict_tokens(self.k_cache, self.v_cache, self.scores, self.positions, self.block_tables,
                      self.context_lens, self.token_counts, new_lens, budget, recent_tokens,
-                     sink_tokens, max_context_len=self.max_context_len, stream=stream)
+                     sink_tokens, max_context_len=self.max_context_len)
         self.context_lens = new_lens
         self.context_lens_host = np.minimum(self.context_lens_host, budget).astype(np.int32)
         freed = 0

@@ -2,9 +2,12 @@
 memory belongs to, what a step keeps between calls, and what is refused."""
 import contextlib
 
+import numpy as np
 import pytest
 import torch
 
+import workloads as W
+from oracle import bounded as B
 from paged_kv_cache_162_gb300 import engine as E
 
 
@@ -46,8 +49,10 @@ class Streams:
     @contextlib.contextmanager
     def on(self, stream):
         before, self.now = self.now, stream
-        yield
-        self.now = before
+        try:
+            yield
+        finally:
+            self.now = before
 
 
 @pytest.mark.parametrize("given", [77, FakeStream(77)])
@@ -59,3 +64,82 @@ def test_a_call_s_workspace_comes_from_its_own_stream(monkeypatch, given):
     assert streams.made == [("empty", 77)]
     E._workspace("call", 1024, torch.device("cpu"))
     assert streams.made[1:] == [("empty", 0)]
+
+
+# ------------------------------------------------------- DecodeStep on the CPU
+def cpu_step(**kw):
+    """A planned DecodeStep on the CPU: two requests of three sequences that share their prompt's blocks."""
+    args = dict(seed=9, prompts=2, samples=3, prefix=160, tail_lo=1, tail_hi=60, H=2, D=64)
+    w = W.shared_prefix(**{**args, **kw})
+    w.initial_free = np.concatenate([np.arange(w.NB, w.NB + 60, dtype=np.int32), w.initial_free])
+    w.NB += 60
+    st = E.DecodeStep(dtype=w.dtype, S=w.S, H=w.H, D=w.D, bs=w.bs, NB=w.NB, MB=w.MB, scale=w.scale,
+                      ctx_before=w.ctx_before, n_new=w.n_new, tables_pre=w.tables_pre, nblocks_pre=w.nblocks_pre,
+                      initial_free=w.initial_free, blocks=w.blocks, k_blocks=w.k_blocks, v_blocks=w.v_blocks, q=w.q,
+                      new_k=w.new_k, new_v=w.new_v, seq_idx=w.seq_idx, pos=w.pos, fill_bits=int(W.POISON[w.dtype]),
+                      device="cpu")
+    st.plan()
+    return st
+
+
+class FakeKernels:
+    """The calls that DecodeStep makes, by the 64-bit definitions on CPU tensors; what each was given."""
+
+    def __init__(self, monkeypatch, streams=None):
+        self.calls, self.streams = [], streams
+        for name in ("paged_attention_decode_window", "paged_attention_decode_accumulate", "evict_tokens",
+                     "copy_blocks"):
+            monkeypatch.setattr(E, name, getattr(self, name))
+
+    def note(self, name, stream):
+        at = None if self.streams is None else self.streams.now.cuda_stream
+        self.calls.append((name, at if stream is None else getattr(stream, "cuda_stream", stream)))
+
+    def paged_attention_decode_window(self, out, *args):
+        self.note("window", args[-1])
+        return out
+
+    def paged_attention_decode_accumulate(self, out, scores, q, k, v, bt, lens, scale, most, ws, stream=None):
+        self.note("accumulate", stream)
+        S, Hkv = scores.shape[:2]
+        assert ws.numel() >= E.L.pkv_decode_accumulate_workspace_size(S, q.shape[1], Hkv, q.shape[2], most)
+        assert int(lens.max()) <= most
+        _, weights, _ = B.attend(*(x.double().numpy() for x in (q, k, v)), bt.numpy(), lens.numpy(), scale)
+        scores.numpy()[:] = B.accumulate(scores.numpy(), weights, Hkv)
+        return out
+
+    def evict_tokens(self, k, v, scores, pos, bt, lens, seen, new, budget, recent, sinks=0, max_context_len=0,
+                     stream=None):
+        self.note("evict", stream)
+        s, p = scores.numpy(), pos.numpy()
+        new.numpy()[:] = B.evict(k.view(torch.int16).numpy(), v.view(torch.int16).numpy(), s, p, bt.numpy(),
+                                 lens.numpy(), seen.numpy(), budget, recent, sinks)
+
+    def copy_blocks(self, k, v, pairs, stream=None):
+        self.note("copy", stream)
+        for src, dst in pairs.tolist():
+            k[dst], v[dst] = k[src].clone(), v[src].clone()
+
+
+def test_a_step_s_calls_keep_to_the_stream_they_are_given(monkeypatch):
+    """Scores zeroed, tables uploaded and temporary tensors made on another
+    stream than the kernels' would race with them."""
+    st = cpu_step()
+    streams = Streams(monkeypatch)
+    kernels = FakeKernels(monkeypatch, streams)
+    side = FakeStream(5)
+    for call, expect in ((lambda: st.decode_window(30, 4, stream=side), ["window"]),
+                         (lambda: st.decode_accumulate(stream=side), ["accumulate"]),
+                         (lambda: st.evict(96, 20, 4, stream=side), ["copy", "evict"])):
+        streams.made.clear()
+        kernels.calls.clear()
+        main = streams.now
+        main.waited.clear()
+        side.waited.clear()
+        call()
+        assert kernels.calls == [(name, 5) for name in expect]
+        assert streams.made and {at for _, at in streams.made} == {5}, streams.made
+        assert side.waited == [0] and main.waited == [5]
+        assert streams.now is main
+    st.evict(80, 20, 4)                       # without one, all on the current stream and nothing to wait for
+    assert kernels.calls[-1] == ("evict", 0) and side.waited == [0]

@@ -4,9 +4,11 @@ import numpy as np
 import pytest
 import torch
 
+import workloads as W
 from oracle import bounded as B
 from paged_kv_cache_162_gb300 import _lib as L
 from paged_kv_cache_162_gb300 import engine as E
+from tests.gpu_harness import device_step
 from tests.test_gpu_bounded import check_out, dev, f64, make, weight_error
 
 pytestmark = pytest.mark.gpu
@@ -42,4 +44,52 @@ def test_scratch_is_not_shared_with_another_stream():
             want = B.accumulate(np.zeros(z.shape), weights, 4)
             # two query heads per KV head, from zero: (w + 2 e) of what was added, once rounded
             assert np.all(np.abs(f64(z.cpu()) - want) <= (w + 3 * 2.0 ** -24) * want + 2.0 ** -126)
+    assert L.pkv_get_device_errors() == 0
+
+
+def shared_step(**kw):
+    """A step of two requests of three sequences that share their prompt's
+    blocks, planned and run, with room in the pool to copy them."""
+    args = dict(seed=9, prompts=2, samples=3, prefix=160, tail_lo=1, tail_hi=60, H=4, D=64)
+    w = W.shared_prefix(**{**args, **kw})
+    w.initial_free = np.concatenate([np.arange(w.NB, w.NB + 80, dtype=np.int32), w.initial_free])
+    w.NB += 80
+    st = device_step(w)
+    st.plan()
+    st.run()
+    return st
+
+
+def bits(st):
+    torch.cuda.synchronize()
+    return [x.view(torch.int16 if x.element_size() == 2 else torch.int32).cpu()
+            for x in (st.out, st.k_cache, st.v_cache, st.scores, st.positions, st.block_tables, st.context_lens,
+                      st.token_counts)]
+
+
+def test_step_on_another_stream():
+    """Both streams busy before every call, and no synchronisation but the
+    calls' own: the results are those of one stream."""
+    def cycle(stream):
+        st = shared_step()
+        torch.cuda.synchronize()
+        for _ in range(2):
+            if stream is not None:
+                with torch.cuda.stream(stream):
+                    keep_busy()
+            keep_busy()
+            st.decode_accumulate(stream=stream)
+        freed = st.evict(96, 20, 4, stream=stream)
+        junk = [torch.full((1 << 16,), 255, dtype=torch.uint8, device="cuda") for _ in range(64)]
+        st.decode()
+        after = st.out.clone()
+        st.decode_window(30, 4, stream=stream)
+        got = bits(st) + [after.view(torch.int16).cpu()]
+        del junk
+        return freed, got
+    freed, want = cycle(None)
+    assert freed > 0
+    for _ in range(3):
+        got_freed, got = cycle(torch.cuda.Stream())
+        assert got_freed == freed and all(torch.equal(a, b) for a, b in zip(got, want))
     assert L.pkv_get_device_errors() == 0
