@@ -783,7 +783,8 @@ class DecodeStep:
         shared (OutOfBlocks if the pool has no room for that: nothing is
         evicted then).  With a stream, the eviction runs there after what the
         current stream holds, and the current stream goes on after it.
-        Returns the number of blocks freed."""
+        block_tables and context_lens are updated where they are: a captured
+        graph reads the new ones.  Returns the number of blocks freed."""
         with _on(stream, self.device):
             return self._evict(budget, recent_tokens, sink_tokens)
 
@@ -799,20 +800,20 @@ class DecodeStep:
             pairs = np.concatenate(pairs) if pairs else np.empty((0, 2), dtype=np.int64)
             if len(pairs):
                 check_copy_pairs(pairs, self.NB)
-                self.block_tables = torch.from_numpy(self.tables_host).to(self.device)
+                self.block_tables.copy_(torch.from_numpy(self.tables_host))
                 copy_blocks(self.k_cache, self.v_cache, torch.from_numpy(pairs).to(self.device))
         new_lens = torch.empty_like(self.context_lens)
         evict_tokens(self.k_cache, self.v_cache, self.scores, self.positions, self.block_tables,
                      self.context_lens, self.token_counts, new_lens, budget, recent_tokens,
                      sink_tokens, max_context_len=self.max_context_len)
-        self.context_lens = new_lens
+        self.context_lens.copy_(new_lens)
         self.context_lens_host = np.minimum(self.context_lens_host, budget).astype(np.int32)
         freed = 0
         for s in over:
             nb, n = self.allocator.truncate(self.tables_host[s], self.nblocks_host[s], budget, self.bs)
             self.nblocks_host[s] = nb
             freed += n
-        self.block_tables = torch.from_numpy(self.tables_host).to(self.device)
+        self.block_tables.copy_(torch.from_numpy(self.tables_host))
         return freed
 
     def decode(self, stream=None):

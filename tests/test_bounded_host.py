@@ -143,3 +143,16 @@ def test_a_step_s_calls_keep_to_the_stream_they_are_given(monkeypatch):
         assert streams.now is main
     st.evict(80, 20, 4)                       # without one, all on the current stream and nothing to wait for
     assert kernels.calls[-1] == ("evict", 0) and side.waited == [0]
+
+
+# ------------------------------------------------- what a step keeps between calls
+def test_eviction_updates_the_step_s_tensors_in_place(monkeypatch):
+    """A graph captured before holds the addresses of the tables and lengths."""
+    st = cpu_step()
+    FakeKernels(monkeypatch)
+    tables, lens = st.block_tables, st.context_lens
+    st.decode_accumulate()
+    assert st.evict(96, 20, 4) > 0
+    assert st.block_tables is tables and st.context_lens is lens
+    assert np.array_equal(tables.numpy(), st.tables_host) and np.array_equal(lens.numpy(), st.context_lens_host)
+    assert lens.max() == 96 and (tables.numpy()[:, 6:] == -1).all()

@@ -93,3 +93,26 @@ def test_step_on_another_stream():
         got_freed, got = cycle(torch.cuda.Stream())
         assert got_freed == freed and all(torch.equal(a, b) for a, b in zip(got, want))
     assert L.pkv_get_device_errors() == 0
+
+
+def test_captured_decode_follows_an_eviction():
+    """A graph captured before evict() decodes what is left after it."""
+    st = shared_step()
+    st.decode_accumulate()
+    st.decode_window(60, 4)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        st.decode_window(60, 4)
+    torch.cuda.synchronize()
+    st.evict(96, 20, 4)
+    junk = [torch.full((1 << 12,), 77, dtype=torch.int32, device="cuda") for _ in range(64)]
+    st.decode_window(60, 4)
+    want = st.out.clone()
+    st.out.zero_()
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(st.out.view(torch.int16), want.view(torch.int16))
+    assert L.pkv_get_device_errors() == 0
+    del junk
