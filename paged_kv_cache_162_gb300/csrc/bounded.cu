@@ -62,6 +62,7 @@
 #include <cstdio>
 #include <mutex>
 
+#include "bounded_place.h"
 #include "pagedkv.h"
 #include "pkv_device.cuh"
 #include "pkv_mma.cuh"
@@ -1327,7 +1328,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const __grid_cons
         __shared__ __align__(16) float s_o[kJoinWarps][D];
         for (int i = blockIdx.x; i < joins; i += gridDim.x) {
             const int2 at = p.place[i / rows];
-            if (at.x == at.y) continue;  // the same for the whole CTA
+            if (pkv::pieces_of(at.x, at.y, p.ranges) < 2) continue;  // the same for the whole CTA
             float M, L, o[DPL];
             gather_row<D, 6>(p, at.x, at.x + warp, at.y, kJoinWarps, i % rows, lane, M, L, o);
             if (lane == 0) {
@@ -1368,15 +1369,15 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const __grid_cons
         if (mine < listed) {
             it.at = (int)mine;
             it.place = p.place[it.at / rows];
-            live = it.place.x != it.place.y;
+            live = pkv::pieces_of(it.place.x, it.place.y, p.ranges) > 1;
         } else if (kScores && mine < items) {
             // (stretch, sequence, KV head): the first stretches of all first
             const long long f = mine - listed;
             it.at = (int)(f % heads);
             it.j0 = (int)(f / heads) * TOKENS;
             it.n = context_of(p, it.at / p.Hkv);
-            live = it.j0 < it.n;
             it.place = p.place[it.at / p.hw];
+            live = it.j0 < it.n && pkv::pieces_of(it.place.x, it.place.y, p.ranges) > 0;
         }
         const unsigned alive = __ballot_sync(kFull, live);
         if (lane == 0) s_count[warp] = __popc(alive);

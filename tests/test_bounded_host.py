@@ -1,6 +1,9 @@
 """The host side of the bounded-cache calls without a GPU: which stream their
 memory belongs to, what a step keeps between calls, and what is refused."""
 import contextlib
+import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -156,3 +159,26 @@ def test_eviction_updates_the_step_s_tensors_in_place(monkeypatch):
     assert st.block_tables is tables and st.context_lens is lens
     assert np.array_equal(tables.numpy(), st.tables_host) and np.array_equal(lens.numpy(), st.context_lens_host)
     assert lens.max() == 96 and (tables.numpy()[:, 6:] == -1).all()
+
+
+# --------------------------------------------------- what a wait that ran out leaves
+def test_entries_that_nobody_wrote_name_no_pieces(tmp_path):
+    """After a wait that ran out the join finds any contents in the workspace
+    and must not look for pieces outside the call's."""
+    csrc = os.path.join(os.path.dirname(E.__file__), "csrc")
+    src, so = tmp_path / "place.cpp", tmp_path / "place.so"
+    src.write_text('#include "bounded_place.h"\n'
+                   'extern "C" int pieces(int x, int y, int r) { return pkv::pieces_of(x, y, r); }\n')
+    subprocess.run(["g++", "-shared", "-fPIC", "-I", csrc, str(src), "-o", str(so)], check=True)
+    pieces = ctypes.CDLL(str(so)).pieces
+    for ranges in (1, 304, 1536):
+        for x in range(0, ranges, 7):
+            assert [pieces(x, y, ranges) for y in (x, ranges - 1)] == [1, ranges - x]
+        top, low = 2 ** 31 - 1, -2 ** 31
+        for x, y in ((-1, -1), (low, top), (top, low), (low, low), (top, top), (0, ranges), (0, top), (1, 0), (-1, 0),
+                     (low, 0), (0x7f7f7f7f, 0x7f7f7f7f), (ranges, ranges), (0, -1)):
+            assert pieces(x, y, ranges) == 0, (x, y, ranges)
+    # the kernel asks it wherever it reads an entry
+    with open(os.path.join(csrc, "bounded.cu")) as f:
+        kernel = f.read()
+    assert kernel.count("= p.place[") == kernel.count("pkv::pieces_of(") == 3
