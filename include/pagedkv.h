@@ -348,7 +348,8 @@ size_t pkv_evict_workspace_size(int S, int Hkv, int budget);
  *                 are clamped and set PKV_DEVERR_CONTEXT
  *   max_context_len  upper bound of context_lens (0 = MB*bs); at most
  *                 score_stride
- *   new_context_lens  [S] int32, written; not context_lens itself
+ *   new_context_lens  [S] int32, written; overlaps neither context_lens nor
+ *                 token_counts
  *   budget        >= 1, >= sink_tokens + recent_tokens
  *   workspace     256-byte aligned, pkv_evict_workspace_size bytes; one call
  *                 at a time may use it

@@ -600,9 +600,14 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
         return pkv::fail(PKV_ERR_INVALID_ARG, "evict_tokens: null pointer");
     if (!pkv::aligned16(k_cache) || !pkv::aligned16(v_cache))
         return pkv::fail(PKV_ERR_INVALID_ARG, "evict_tokens: cache pointers must be 16-byte aligned");
-    // every head of a sequence reads its length
-    if (new_context_lens == context_lens)
-        return pkv::fail(PKV_ERR_INVALID_ARG, "evict_tokens: new_context_lens must not be context_lens");
+    // every head of a sequence reads its length and its count; one of them writes the new length
+    auto overlap = [&](const int32_t* in) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(in), y = reinterpret_cast<uintptr_t>(new_context_lens);
+        return (x < y ? y - x : x - y) < (uintptr_t)S * sizeof(int32_t);
+    };
+    if (overlap(context_lens) || overlap(token_counts))
+        return pkv::fail(PKV_ERR_INVALID_ARG,
+                         "evict_tokens: new_context_lens must not overlap context_lens or token_counts");
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return pkv::fail(PKV_ERR_INVALID_ARG, "evict_tokens: workspace must be a 256-byte aligned device pointer");
     if (workspace_bytes < pkv_evict_workspace_size(S, Hkv, budget))

@@ -11,6 +11,7 @@ import torch
 
 import workloads as W
 from oracle import bounded as B
+from paged_kv_cache_162_gb300 import _lib as L
 from paged_kv_cache_162_gb300 import engine as E
 
 
@@ -182,3 +183,27 @@ def test_entries_that_nobody_wrote_name_no_pieces(tmp_path):
     with open(os.path.join(csrc, "bounded.cu")) as f:
         kernel = f.read()
     assert kernel.count("= p.place[") == kernel.count("pkv::pieces_of(") == 3
+
+
+# ------------------------------------------------------------------ refusals
+def evict_args(**kw):
+    a = dict(k_cache=256, v_cache=256, scores=256, positions=256, block_tables=256, context_lens=1024,
+             token_counts=2048, scores_out=256, positions_out=256, new_context_lens=4096, S=5, Hkv=4, D=128, bs=16,
+             NB=8, MB=4, max_context_len=0, score_stride=64, budget=32, recent_tokens=8, sink_tokens=4,
+             dtype=L.PKV_BF16, workspace=256, workspace_bytes=1 << 40, stream=0)
+    a.update(kw)
+    return a
+
+
+@pytest.mark.parametrize("new", [1024, 2048, 1024 + 16, 2048 + 16, 1024 - 16, 2048 - 16, 2048 + 4])
+def test_evict_refuses_lengths_written_over_what_it_reads(new):
+    """Heads and CTAs of a row read its length and its token count while one of them writes the new length."""
+    with pytest.raises(L.PkvError, match="must not overlap") as e:
+        L.pkv_evict_tokens(**evict_args(new_context_lens=new))
+    assert e.value.status == L.PKV_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("new", [1024 + 20, 2048 - 20, 2048 + 20])
+def test_evict_takes_lengths_next_to_what_it_reads(new):
+    with pytest.raises(L.PkvError, match="workspace too small"):  # the next check
+        L.pkv_evict_tokens(**evict_args(new_context_lens=new, workspace_bytes=10))
