@@ -807,7 +807,10 @@ class DecodeStep:
                      self.context_lens, self.token_counts, new_lens, budget, recent_tokens,
                      sink_tokens, max_context_len=self.max_context_len)
         self.context_lens.copy_(new_lens)
-        self.context_lens_host = np.minimum(self.context_lens_host, budget).astype(np.int32)
+        if hasattr(self, "beam_ctx"):  # the native search goes by this array
+            self.context_lens_host = np.minimum(self.beam_ctx, budget, out=self.beam_ctx)
+        else:
+            self.context_lens_host = np.minimum(self.context_lens_host, budget).astype(np.int32)
         freed = 0
         for s in over:
             nb, n = self.allocator.truncate(self.tables_host[s], self.nblocks_host[s], budget, self.bs)

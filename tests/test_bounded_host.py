@@ -13,6 +13,7 @@ import workloads as W
 from oracle import bounded as B
 from paged_kv_cache_162_gb300 import _lib as L
 from paged_kv_cache_162_gb300 import engine as E
+from tests.bounded_rows import Rows
 
 
 # ---------------------------------------------------------------- streams
@@ -207,3 +208,84 @@ def test_evict_refuses_lengths_written_over_what_it_reads(new):
 def test_evict_takes_lengths_next_to_what_it_reads(new):
     with pytest.raises(L.PkvError, match="workspace too small"):  # the next check
         L.pkv_evict_tokens(**evict_args(new_context_lens=new, workspace_bytes=10))
+
+
+# ------------------------------------------------------------- beam search
+class FakeEvent:
+    def record(self, stream=None):
+        pass
+
+    def synchronize(self):
+        pass
+
+
+def on_cpu(st, monkeypatch):
+    """Lets beam_step run on the CPU: its buffers, and the native step by the allocator's own calls."""
+    S, MB, H, D, bs = st.S, st.MB, st.H, st.D, st.bs
+
+    class Native:
+        def step(self, parents, q, key, value, stream):
+            parents = np.ctypeslib.as_array((ctypes.c_int32 * S).from_address(parents)).copy()
+            pos = st.beam_ctx[parents]
+            st.allocator.fork(st.tables_host, st.nblocks_host, parents)
+            pairs = st.allocator.append_batch(st.tables_host, st.nblocks_host, pos, np.ones(S, np.int32), bs)
+            k, v = (t.view(torch.int16).numpy() for t in (st.k_cache, st.v_cache))
+            for a, b in pairs:
+                k[b], v[b] = k[a], v[a]
+            tok = st._beam_dev_u16.numpy().reshape(3, S, H, D)
+            for s in range(S):
+                block = st.tables_host[s, pos[s] // bs]
+                k[block, pos[s] % bs], v[block, pos[s] % bs] = tok[1, s], tok[2, s]
+            st.beam_ctx[:] = pos + 1
+            st._beam_views[0].numpy()[:], st._beam_views[1].numpy()[:] = st.tables_host, st.beam_ctx
+            return 0, 0
+
+        def close(self):
+            pass
+
+    def buffers():
+        st._beam_slots = [dict(stg_np=np.zeros(64, np.uint8), u16=torch.empty(3 * S * H * D, dtype=torch.int16),
+                               done=FakeEvent(), used=False) for _ in range(2)]
+        st._beam_dev_u16 = torch.empty(3 * S * H * D, dtype=torch.int16)
+        st._beam_turn, st._beam_inputs_bytes, st._beam_stg_base = 0, 64, [0, 1 << 40]
+        st._beam_views = (torch.empty(S, MB, dtype=torch.int32), torch.empty(S, dtype=torch.int32),
+                          torch.empty(S, dtype=torch.int32), torch.empty(S, dtype=torch.int32))
+        groups = getattr(st, "beam_groups", None)
+        st._beam_G = 0 if groups is None else len(groups)
+        st.max_context_len = MB * bs
+        st._beam_native = Native()
+
+    monkeypatch.setattr(st, "_beam_buffers", buffers)
+    return st
+
+
+def beam_tokens(st, rng):
+    """q, K and V of a step's new tokens: bit patterns, and their values."""
+    b = W.normal_bits(np.random.Generator(np.random.SFC64(int(rng.integers(1 << 30)))), (3, st.S, st.H, st.D), W.F16)
+    return b, b.view(np.float16).astype(np.float64)
+
+
+def step_rows(st):
+    return Rows(st.k_cache.double().numpy(), st.v_cache.double().numpy(), st.tables_host, st.context_lens_host,
+                st.scale)
+
+
+def test_a_beam_search_goes_on_from_the_evicted_lengths(monkeypatch):
+    """The native search has lengths of its own: a token appended past them
+    would leave rows that nobody wrote inside the context."""
+    rng = np.random.default_rng(3)
+    Streams(monkeypatch)
+    FakeKernels(monkeypatch)
+    st = on_cpu(cpu_step(H=1), monkeypatch)
+    for t in (st.k_cache, st.v_cache):
+        t.view(-1, 1, st.D)[:] = 0.25                   # whatever a row holds that nobody writes
+    step = lambda: st.beam_step(np.arange(st.S), *(beam_tokens(st, rng)[0][i] for i in (1, 2, 0)))  # noqa: E731
+    step()
+    st.decode_accumulate()
+    st.evict(160, 20, 4)
+    assert (st.context_lens_host == 160).all() and (st.beam_ctx == 160).all()
+    tables = st.tables_host.copy()
+    step()
+    assert (st.context_lens.numpy() == 161).all() and (st.context_lens_host == 161).all()
+    assert (st.nblocks_host == 11).all() and np.array_equal(st.tables_host[:, :10], tables[:, :10])
+    assert (st.tables_host[:, 10] >= 0).all()
