@@ -634,7 +634,8 @@ class DecodeStep:
         (pkv_beam_step).  new_k/new_v/q: [S, H, D] 16-bit values, either
         host arrays of uint16 bit patterns (uploaded first) or device
         tensors (used in place, as a model on the device would produce
-        them).  Returns the (src, dst) copy pairs of the step."""
+        them).  Scores and positions of decode_accumulate follow the parents.
+        Returns the (src, dst) copy pairs of the step."""
         S, MB, H, D, bs = self.S, self.MB, self.H, self.D, self.bs
         if not hasattr(self, "beam_ctx"):
             self.beam_ctx = np.ascontiguousarray(self.context_lens_host, dtype=np.int32).copy()
@@ -674,6 +675,9 @@ class DecodeStep:
         P, at = self._beam_native.step(par.ctypes.data, tq.data_ptr(), tk.data_ptr(), tv.data_ptr(),
                                        sh)
         self.last_native_seconds = time.perf_counter() - t0
+        if getattr(self, "scores", None) is not None:
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+                self._scores_follow(par)
         # the pairs sit in the staging buffer the step used
         k = 0 if 0 <= at - self._beam_stg_base[0] < self._beam_inputs_bytes else 1
         o = at - self._beam_stg_base[k]
@@ -685,6 +689,17 @@ class DecodeStep:
         (self.block_tables, self.context_lens, self.pos,
          self.seq_idx) = self._beam_views
         return pairs
+
+    def _scores_follow(self, parents):
+        """After a beam step, on the current stream: every sequence has its
+        parent's scores and positions, and one more token than its parent."""
+        moved = np.flatnonzero(parents != np.arange(self.S))
+        if len(moved):
+            to = torch.from_numpy(moved).to(self.device)
+            of = torch.from_numpy(parents[moved].astype(np.int64)).to(self.device)
+            for t in (self.scores, self.positions, self.token_counts):
+                t.index_copy_(0, to, t.index_select(0, of))
+        self.token_counts.add_(1)
 
     def pack_inputs(self, on_host=()):
         """Move the step's inputs (q, new K/V, block tables, context lengths,

@@ -84,6 +84,8 @@ def cpu_step(**kw):
                       new_k=w.new_k, new_v=w.new_v, seq_idx=w.seq_idx, pos=w.pos, fill_bits=int(W.POISON[w.dtype]),
                       device="cpu")
     st.plan()
+    for t in (st.k_cache, st.v_cache):       # as if every row had been written
+        t.copy_(torch.randn(t.shape, generator=torch.Generator().manual_seed(1)))
     return st
 
 
@@ -289,3 +291,37 @@ def test_a_beam_search_goes_on_from_the_evicted_lengths(monkeypatch):
     assert (st.context_lens.numpy() == 161).all() and (st.context_lens_host == 161).all()
     assert (st.nblocks_host == 11).all() and np.array_equal(st.tables_host[:, :10], tables[:, :10])
     assert (st.tables_host[:, 10] >= 0).all()
+
+
+@pytest.mark.parametrize("start", [0, 2])
+def test_scores_positions_and_ages_follow_a_beam_search(monkeypatch, start):
+    """Three cycles of beam steps, accumulated weights and eviction, token by
+    token: every beam has its parent's rows, and new tokens their true ages."""
+    rng = np.random.default_rng(start)
+    Streams(monkeypatch)
+    FakeKernels(monkeypatch)
+    st = on_cpu(cpu_step(), monkeypatch)
+    rows, S = step_rows(st), st.S
+
+    def step():
+        parents = rng.integers(0, S, S)
+        b, x = beam_tokens(st, rng)
+        st.beam_step(parents, b[1], b[2], b[0])
+        rows.beam_step(parents, x[1], x[2])
+        return x[0]
+    for _ in range(start):                   # a search that had begun before the first scores
+        step()
+    q = st.q.double().numpy()
+    st.decode_accumulate()
+    rows.attend(q, add=True)
+    rows.check_state(st, 1e-6)
+    for cycle in range(3):
+        rows.take_scores(st)
+        st.evict(100, 30, 4)
+        rows.evict(100, 30, 4)
+        rows.check_state(st, 0)
+        for _ in range(12 + 5 * cycle):
+            q = step()
+            st.decode_accumulate()
+            rows.attend(q, add=True)
+        rows.check_state(st, 1e-4)

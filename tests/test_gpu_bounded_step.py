@@ -8,7 +8,8 @@ import workloads as W
 from oracle import bounded as B
 from paged_kv_cache_162_gb300 import _lib as L
 from paged_kv_cache_162_gb300 import engine as E
-from tests.gpu_harness import device_step
+from tests.bounded_rows import Rows
+from tests.gpu_harness import assert_attention_close, device_step
 from tests.test_gpu_bounded import check_out, dev, f64, make, weight_error
 
 pytestmark = pytest.mark.gpu
@@ -116,3 +117,45 @@ def test_captured_decode_follows_an_eviction():
     assert torch.equal(st.out.view(torch.int16), want.view(torch.int16))
     assert L.pkv_get_device_errors() == 0
     del junk
+
+
+@pytest.mark.parametrize("dtype,D,streamed", [("f16", 64, False), ("f16", 64, True), ("bf16", 128, False)])
+def test_cycles_of_beam_search_and_eviction(dtype, D, streamed):
+    """Beam steps, accumulated weights and evictions in turn, token by token:
+    caches, positions and lengths exact, attention within the library's bar,
+    scores within 1e-4 (24 steps of weights of at most 1, each within 2e-6)."""
+    rng = np.random.default_rng(D + streamed)
+    st = shared_step(dtype=dtype, D=D)
+    S, H = st.S, st.H
+    stream = torch.cuda.Stream() if streamed else None
+    if streamed:
+        torch.cuda.synchronize()
+    rows = Rows(st.k_cache.double().cpu().numpy(), st.v_cache.double().cpu().numpy(), st.tables_host,
+                st.context_lens_host, st.scale)
+
+    def attended(q):
+        torch.cuda.synchronize()
+        assert_attention_close(st.out.double().cpu().numpy(), rows.attend(q, add=True), "accumulate")
+
+    q = st.q.double().cpu().numpy()
+    st.decode_accumulate(stream=stream)
+    attended(q)
+    for cycle in range(3):
+        rows.take_scores(st)
+        assert st.evict(100, 30, 4, stream=stream) > 0
+        rows.evict(100, 30, 4)
+        torch.cuda.synchronize()
+        rows.check_state(st, 0)
+        for _ in range(8 + 5 * cycle):
+            parents = rng.integers(0, S, S)
+            tok = [torch.from_numpy(rng.standard_normal((S, H, D))).to(st.dtype) for _ in range(3)]
+            bits16 = [t.view(torch.int16).numpy().view(np.uint16) for t in tok]
+            q, k, v = (t.double().numpy() for t in tok)
+            st.beam_step(parents, bits16[1], bits16[2], bits16[0], stream=stream)
+            rows.beam_step(parents, k, v)
+            torch.cuda.synchronize()
+            assert_attention_close(st.out.double().cpu().numpy(), rows.attend(q), "beam step")
+            st.decode_accumulate(stream=stream)
+            attended(q)
+        rows.check_state(st, 1e-4)
+    assert L.pkv_get_device_errors() == 0
