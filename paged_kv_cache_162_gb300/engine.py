@@ -508,6 +508,7 @@ class DecodeStep:
         # shared-prefix groups [G, 3] int32 on the device for run(fused=True)
         # (the workspace must then have the shared-prefix size)
         self.prefix_groups = None
+        self._evicted = False  # since plan(): rows own their blocks, tokens have moved
 
     def plan(self):
         """Host allocator: tables and copy-on-write pairs for this step.
@@ -517,6 +518,7 @@ class DecodeStep:
             if name == "_beam_native" and old is not None:
                 torch.cuda.synchronize(self.device)  # its staging buffers may still be in flight
                 old.close()
+        self._evicted = False
         self.allocator = BlockAllocator(self.NB, self.initial_free)
         ids, counts = np.unique(self.tables_pre[self.tables_pre >= 0], return_counts=True)
         for b, c in zip(ids.tolist(), counts.tolist()):
@@ -759,7 +761,15 @@ class DecodeStep:
     def decode_shared_prefix(self, prefix_groups, stream=None):
         """decode() with the prefix of each group read once (see
         paged_attention_decode_shared_prefix); prefix_groups [G, 3] int32."""
-        g = torch.as_tensor(np.asarray(prefix_groups, dtype=np.int32)).to(self.device)
+        prefix_groups = np.asarray(prefix_groups, dtype=np.int32)
+        if self._evicted:
+            for first, n, tokens in prefix_groups.reshape(-1, 3).tolist():
+                rows = self.tables_host[max(first, 0):max(first + n, 0), :-(-tokens // self.bs)]
+                held = self.context_lens_host[max(first, 0):max(first + n, 0)]
+                if (rows != rows[:1]).any() or (held < tokens).any():
+                    _refuse("decode_shared_prefix: after evict() the sequences from "
+                            f"{first} on no longer share {tokens} tokens")
+        g = torch.as_tensor(prefix_groups).to(self.device)
         return paged_attention_decode_shared_prefix(
             self.out, self.q, self.k_cache, self.v_cache, self.block_tables, self.context_lens, g,
             self.scale, self.max_context_len, self.partition_tokens, stream=stream)
@@ -799,13 +809,17 @@ class DecodeStep:
         evicted then).  With a stream, the eviction runs there after what the
         current stream holds, and the current stream goes on after it.
         block_tables and context_lens are updated where they are: a captured
-        graph reads the new ones.  Returns the number of blocks freed."""
+        graph reads the new ones.  Evicted rows own their blocks: prefix_groups
+        and beam_groups are dropped, and a beam search that has begun with
+        groups is refused.  Returns the number of blocks freed."""
         with _on(stream, self.device):
             return self._evict(budget, recent_tokens, sink_tokens)
 
     def _evict(self, budget, recent_tokens, sink_tokens):
         """evict() on the current stream, temporary tensors and all."""
         over = [s for s in range(self.S) if self.context_lens_host[s] > budget]
+        if over and hasattr(self, "beam_ctx") and self._beam_G:
+            _refuse("evict: the beam search reads prefix groups that evicted sequences would no longer share")
         pairs = []
         try:
             for s in over:
@@ -831,6 +845,9 @@ class DecodeStep:
             nb, n = self.allocator.truncate(self.tables_host[s], self.nblocks_host[s], budget, self.bs)
             self.nblocks_host[s] = nb
             freed += n
+        if over:
+            self._evicted = True
+            self.prefix_groups = self.beam_groups = None
         self.block_tables.copy_(torch.from_numpy(self.tables_host))
         return freed
 
@@ -866,12 +883,15 @@ class StepGraph:
     fused: run the step through pkv_decode_step (DecodeStep.run).
     The step runs once eagerly before capture so that every per-device
     set-up of the library happens outside the capture.  replay() enqueues
-    the whole step on the capture stream with one launch.
+    the whole step on the capture stream with one launch.  It replays the step
+    as it was captured, prefix groups included: after DecodeStep.evict a step
+    with groups is captured anew.
     """
 
     def __init__(self, step: DecodeStep, stream: torch.cuda.Stream, h2d=(), d2h=(), fused=False):
         self.step = step
         self.stream = stream
+        self._groups = step.prefix_groups  # read by every replay
         with torch.cuda.stream(stream):
             step.run(fused=fused)
         stream.synchronize()

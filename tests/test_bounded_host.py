@@ -325,3 +325,52 @@ def test_scores_positions_and_ages_follow_a_beam_search(monkeypatch, start):
             st.decode_accumulate()
             rows.attend(q, add=True)
         rows.check_state(st, 1e-4)
+
+
+def test_prefix_groups_end_with_an_eviction(monkeypatch):
+    """Evicted sequences own their blocks and hold other tokens per head: no group reads them through its first member."""
+    FakeKernels(monkeypatch)
+    seen = []
+    monkeypatch.setattr(E, "paged_attention_decode_shared_prefix", lambda *a, **kw: seen.append(a[6].tolist()))
+    st = cpu_step()
+    groups = [[0, 3, 160], [3, 3, 160]]
+    st.prefix_groups, st.beam_groups = torch.tensor(groups, dtype=torch.int32), groups
+    st.decode_accumulate()
+    st.decode_shared_prefix(groups)
+    lens = st.context_lens_host.copy()
+    assert st.evict(int(lens.max()), 20, 4) == 0       # nothing over the budget: all as before
+    assert st.prefix_groups is not None and st.beam_groups is groups
+    st.decode_shared_prefix(groups)
+    assert seen == [groups, groups]
+    budget = int(lens[:3].max())                       # sequences of the second request alone
+    assert (lens[3:] > budget).any() or (lens[:3] > (budget := int(lens[3:].max()))).any()
+    st.evict(budget, 20, 4)
+    assert st.prefix_groups is None and st.beam_groups is None
+    whole = 0 if (lens[:3] <= budget).all() else 1     # the request that kept its blocks
+    st.decode_shared_prefix(groups[whole:whole + 1])
+    with pytest.raises(L.PkvError, match="no longer share"):
+        st.decode_shared_prefix(groups[1 - whole:2 - whole])
+    st.decode_shared_prefix(np.empty((0, 3)))
+    st.evict(96, 20, 4)
+    for i in (0, 1):
+        with pytest.raises(L.PkvError, match="no longer share"):
+            st.decode_shared_prefix(groups[i:i + 1])
+    st.plan()
+    st.decode_shared_prefix(groups)
+    assert seen[2:] == [groups[whole:whole + 1], [], groups]
+
+
+def test_a_beam_search_with_groups_is_not_evicted(monkeypatch):
+    rng = np.random.default_rng(5)
+    Streams(monkeypatch)
+    FakeKernels(monkeypatch)
+    st = on_cpu(cpu_step(), monkeypatch)
+    st.beam_groups = [[0, 3, 160], [3, 3, 160]]
+    b, _ = beam_tokens(st, rng)
+    st.beam_step(np.arange(st.S), b[1], b[2], b[0])
+    st.decode_accumulate()
+    tables, lens, free = st.tables_host.copy(), st.context_lens_host.copy(), st.allocator.num_free
+    with pytest.raises(L.PkvError, match="prefix groups"):
+        st.evict(96, 20, 4)
+    assert np.array_equal(st.tables_host, tables) and np.array_equal(st.context_lens_host, lens)
+    assert st.allocator.num_free == free
