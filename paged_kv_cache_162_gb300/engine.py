@@ -509,6 +509,7 @@ class DecodeStep:
         # (the workspace must then have the shared-prefix size)
         self.prefix_groups = None
         self._evicted = False  # since plan(): rows own their blocks, tokens have moved
+        self._accumulate_ws, self._accumulate_bound = None, 0
 
     def plan(self):
         """Host allocator: tables and copy-on-write pairs for this step.
@@ -788,18 +789,29 @@ class DecodeStep:
         """decode() that also adds every token's attention weight to
         self.scores ([S, H, MB * bs] fp32, made on the first call; see
         paged_attention_decode_accumulate), which evict() goes by."""
-        if getattr(self, "scores", None) is None:
-            cap = self.MB * self.bs
+        if getattr(self, "scores", None) is None or self.max_context_len > self._accumulate_bound:
             with _on(stream, self.device):
-                self.scores = torch.zeros((self.S, self.H, cap), device=self.device)
-                self.positions = torch.full((self.S, self.H, cap), -1, dtype=torch.int32,
-                                            device=self.device)
-                self.token_counts = self.context_lens.clone()
-                self._accumulate_ws = new_accumulate_workspace(self.S, self.H, self.H, self.D,
-                                                               self.max_context_len, self.device)
+                self._make_scores()
         return paged_attention_decode_accumulate(
             self.out, self.scores, self.q, self.k_cache, self.v_cache, self.block_tables,
             self.context_lens, self.scale, self.max_context_len, self._accumulate_ws, stream)
+
+    def _make_scores(self):
+        """What decode_accumulate keeps, on the current stream: the rows of a
+        step that has none, and a workspace for the bound (a beam search
+        raises it)."""
+        if getattr(self, "scores", None) is None:
+            rows = (self.S, self.H, self.MB * self.bs)
+            self.scores = torch.zeros(rows, device=self.device)
+            self.positions = torch.full(rows, -1, dtype=torch.int32, device=self.device)
+            self.token_counts = self.context_lens.clone()
+        if self.max_context_len > self._accumulate_bound:
+            old = self._accumulate_ws
+            self._accumulate_ws = new_accumulate_workspace(self.S, self.H, self.H, self.D,
+                                                           self.max_context_len, self.device)
+            self._accumulate_bound = self.max_context_len
+            if old is not None and old.is_cuda:  # the call before may still be in it
+                old.record_stream(torch.cuda.current_stream(self.device))
 
     def evict(self, budget, recent_tokens, sink_tokens=0, stream=None):
         """After decode_accumulate: keeps `budget` tokens of every longer

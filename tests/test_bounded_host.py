@@ -374,3 +374,21 @@ def test_a_beam_search_with_groups_is_not_evicted(monkeypatch):
         st.evict(96, 20, 4)
     assert np.array_equal(st.tables_host, tables) and np.array_equal(st.context_lens_host, lens)
     assert st.allocator.num_free == free
+
+
+def test_weights_go_on_when_a_beam_search_raises_the_bound(monkeypatch):
+    """beam_step allows contexts up to the table's end: a workspace for less is refused."""
+    rng = np.random.default_rng(6)
+    Streams(monkeypatch)
+    FakeKernels(monkeypatch)                 # its accumulate checks the workspace
+    st = on_cpu(cpu_step(tail_lo=33, tail_hi=33, bs=32, D=128), monkeypatch)
+    st.decode_accumulate()
+    ws = st._accumulate_ws
+    st.decode_accumulate()
+    assert st._accumulate_ws is ws and st.MB * st.bs > st.max_context_len + 16
+    b, _ = beam_tokens(st, rng)
+    st.beam_step(np.arange(st.S), b[1], b[2], b[0])
+    st.decode_accumulate()
+    ws = st._accumulate_ws
+    st.decode_accumulate()
+    assert st._accumulate_ws is ws
