@@ -829,6 +829,10 @@ class DecodeStep:
 
     def _evict(self, budget, recent_tokens, sink_tokens):
         """evict() on the current stream, temporary tensors and all."""
+        if getattr(self, "scores", None) is None:
+            _refuse("evict: there are no scores to go by (decode_accumulate makes them)")
+        if budget < 1 or recent_tokens < 0 or sink_tokens < 0 or recent_tokens + sink_tokens > budget:
+            _refuse("evict: budget must be >= 1 and hold the sinks and the recent tokens")
         over = [s for s in range(self.S) if self.context_lens_host[s] > budget]
         if over and hasattr(self, "beam_ctx") and self._beam_G:
             _refuse("evict: the beam search reads prefix groups that evicted sequences would no longer share")

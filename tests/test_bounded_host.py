@@ -392,3 +392,22 @@ def test_weights_go_on_when_a_beam_search_raises_the_bound(monkeypatch):
     ws = st._accumulate_ws
     st.decode_accumulate()
     assert st._accumulate_ws is ws
+
+
+def test_a_step_refuses_an_eviction_before_anything_moves(monkeypatch):
+    """Without scores, or with arguments that evict_tokens refuses, no block has been copied or freed."""
+    kernels = FakeKernels(monkeypatch)
+    st = cpu_step()
+    tables, free = st.tables_host.copy(), st.allocator.num_free
+
+    def refused(match, *args):
+        with pytest.raises(L.PkvError, match=match) as e:
+            st.evict(*args)
+        assert e.value.status == L.PKV_ERR_INVALID_ARG
+        assert np.array_equal(st.tables_host, tables) and st.allocator.num_free == free
+    refused("no scores", 96, 20, 4)
+    st.decode_accumulate()
+    for args in ((0, 0, 0), (-3, 0, 0), (96, -1, 0), (96, 20, -1), (96, 93, 4)):
+        refused("budget must be", *args)
+    assert kernels.calls == [("accumulate", None)]
+    st.evict(96, 92, 4)
