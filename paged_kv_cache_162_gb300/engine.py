@@ -509,17 +509,20 @@ class DecodeStep:
         # (the workspace must then have the shared-prefix size)
         self.prefix_groups = None
         self._evicted = False  # since plan(): rows own their blocks, tokens have moved
+        self.scores = self.positions = self.token_counts = None  # of decode_accumulate
         self._accumulate_ws, self._accumulate_bound = None, 0
 
     def plan(self):
         """Host allocator: tables and copy-on-write pairs for this step.
-        A new plan also starts a new beam search (beam_step)."""
+        A new plan also starts a new beam search (beam_step), and new scores
+        (decode_accumulate) over the lengths from before any eviction; the
+        caches keep what an eviction has moved."""
         for name in ("beam_ctx", "_beam_native"):
             old = self.__dict__.pop(name, None)
             if name == "_beam_native" and old is not None:
                 torch.cuda.synchronize(self.device)  # its staging buffers may still be in flight
                 old.close()
-        self._evicted = False
+        self._forget_scores()
         self.allocator = BlockAllocator(self.NB, self.initial_free)
         ids, counts = np.unique(self.tables_pre[self.tables_pre >= 0], return_counts=True)
         for b, c in zip(ids.tolist(), counts.tolist()):
@@ -531,6 +534,19 @@ class DecodeStep:
         self.block_tables = torch.from_numpy(tables).to(self.device)
         self.pairs = torch.from_numpy(np.ascontiguousarray(pairs)).to(self.device)
         return tables, nb, pairs
+
+    def _forget_scores(self):
+        """Ends what decode_accumulate and evict() have begun: a step planned
+        anew has no scores, and its lengths are those of its tables."""
+        if self.scores is None:
+            return
+        if self.device.type == "cuda":
+            torch.cuda.synchronize(self.device)  # a kernel may still be in them
+        self.scores = self.positions = self.token_counts = None
+        if self._evicted:
+            self._evicted = False
+            self.context_lens_host = (self.ctx_before + self.n_new).astype(np.int32)
+            self.context_lens.copy_(torch.from_numpy(self.context_lens_host))
 
     def run(self, stream=None, attention=True, write=True, fused=False):
         """The device part of the step: copy_blocks, slot mapping, cache
@@ -678,7 +694,7 @@ class DecodeStep:
         P, at = self._beam_native.step(par.ctypes.data, tq.data_ptr(), tk.data_ptr(), tv.data_ptr(),
                                        sh)
         self.last_native_seconds = time.perf_counter() - t0
-        if getattr(self, "scores", None) is not None:
+        if self.scores is not None:
             with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
                 self._scores_follow(par)
         # the pairs sit in the staging buffer the step used
@@ -789,7 +805,7 @@ class DecodeStep:
         """decode() that also adds every token's attention weight to
         self.scores ([S, H, MB * bs] fp32, made on the first call; see
         paged_attention_decode_accumulate), which evict() goes by."""
-        if getattr(self, "scores", None) is None or self.max_context_len > self._accumulate_bound:
+        if self.scores is None or self.max_context_len > self._accumulate_bound:
             with _on(stream, self.device):
                 self._make_scores()
         return paged_attention_decode_accumulate(
@@ -800,7 +816,7 @@ class DecodeStep:
         """What decode_accumulate keeps, on the current stream: the rows of a
         step that has none, and a workspace for the bound (a beam search
         raises it)."""
-        if getattr(self, "scores", None) is None:
+        if self.scores is None:
             rows = (self.S, self.H, self.MB * self.bs)
             self.scores = torch.zeros(rows, device=self.device)
             self.positions = torch.full(rows, -1, dtype=torch.int32, device=self.device)
@@ -829,7 +845,7 @@ class DecodeStep:
 
     def _evict(self, budget, recent_tokens, sink_tokens):
         """evict() on the current stream, temporary tensors and all."""
-        if getattr(self, "scores", None) is None:
+        if self.scores is None:
             _refuse("evict: there are no scores to go by (decode_accumulate makes them)")
         if budget < 1 or recent_tokens < 0 or sink_tokens < 0 or recent_tokens + sink_tokens > budget:
             _refuse("evict: budget must be >= 1 and hold the sinks and the recent tokens")

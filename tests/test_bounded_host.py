@@ -411,3 +411,30 @@ def test_a_step_refuses_an_eviction_before_anything_moves(monkeypatch):
         refused("budget must be", *args)
     assert kernels.calls == [("accumulate", None)]
     st.evict(96, 92, 4)
+
+
+def test_a_new_plan_starts_over(monkeypatch):
+    """plan() makes the tables from before the step: no lengths, scores, positions or ages of an eviction outlive it."""
+    FakeKernels(monkeypatch)
+    st = cpu_step()
+    lens, tables = st.context_lens_host.copy(), st.tables_host.copy()
+    k, v = st.k_cache.clone(), st.v_cache.clone()
+    st.decode_accumulate()
+    first = st.scores.clone()
+    st.plan()                                # no eviction yet
+    assert st.scores is None and np.array_equal(st.context_lens.numpy(), lens)
+    st.decode_accumulate()
+    assert torch.equal(st.scores, first)
+    held = st.context_lens
+    st.evict(96, 20, 4)
+    st.plan()
+    st.k_cache.copy_(k), st.v_cache.copy_(v)
+    assert st.context_lens is held and np.array_equal(held.numpy(), lens)
+    assert np.array_equal(st.context_lens_host, lens) and np.array_equal(st.tables_host, tables)
+    with pytest.raises(L.PkvError, match="no scores"):
+        st.evict(96, 20, 4)
+    st.decode_accumulate()
+    assert torch.equal(st.scores, first) and np.array_equal(st.token_counts.numpy(), lens)
+    assert (st.positions == -1).all()
+    st.evict(96, 20, 4)
+    assert (st.context_lens_host == 96).all()
