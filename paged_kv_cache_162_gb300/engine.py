@@ -552,9 +552,13 @@ class DecodeStep:
         """The device part of the step: copy_blocks, slot mapping, cache
         write, decode.  fused=True runs the last three as pkv_decode_step
         (fewer kernels, the same results), with the shared-prefix decode
-        when self.prefix_groups is set."""
+        when self.prefix_groups is set.  After evict() the step's copies and
+        writes would go to blocks that are other rows' by now: only
+        write=False then."""
         if self.block_tables is None:
             self.plan()
+        if write and self._evicted:
+            _refuse("run: the step was written before an eviction moved it (plan() starts over)")
         if fused and write and attention:
             if self.pairs.shape[0]:
                 copy_blocks(self.k_cache, self.v_cache, self.pairs, stream)

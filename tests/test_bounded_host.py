@@ -438,3 +438,27 @@ def test_a_new_plan_starts_over(monkeypatch):
     assert (st.positions == -1).all()
     st.evict(96, 20, 4)
     assert (st.context_lens_host == 96).all()
+
+
+def test_a_step_is_not_written_again_after_an_eviction(monkeypatch):
+    """Its copy pairs and slots name blocks that have gone back to the pool."""
+    kernels = FakeKernels(monkeypatch)
+    monkeypatch.setattr(E, "compute_slot_mapping", lambda *a: kernels.calls.append(("slots", None)))
+    monkeypatch.setattr(E, "reshape_and_cache", lambda *a: kernels.calls.append(("write", None)))
+    monkeypatch.setattr(E.DecodeStep, "decode", lambda st, stream=None: kernels.calls.append(("decode", None)))
+    monkeypatch.setattr(E.L, "pkv_decode_step", lambda *a: kernels.calls.append(("step", None)))
+    st = cpu_step()
+    st.run()
+    st.decode_accumulate()
+    st.run()
+    st.evict(96, 20, 4)
+    done = len(kernels.calls)
+    for kw in ({}, dict(fused=True), dict(attention=False)):
+        with pytest.raises(L.PkvError, match="plan\\(\\) starts over"):
+            st.run(**kw)
+    assert len(kernels.calls) == done
+    st.run(write=False)
+    st.run(write=False, fused=True)
+    assert kernels.calls[done:] == [("decode", None)] * 2
+    st.plan()
+    st.run()
