@@ -208,6 +208,16 @@ def _on(stream, device):
         current.wait_stream(stream)
 
 
+def _no_capture(who, stream, device):
+    """Refuses while the current stream or `stream` is being captured."""
+    if not torch.cuda.is_initialized():
+        return
+    with torch.cuda.stream(None if stream is None else _as_stream(stream, device)):
+        capturing = torch.cuda.is_current_stream_capturing()
+    if capturing or torch.cuda.is_current_stream_capturing():
+        _refuse(f"{who} cannot be captured in a graph")
+
+
 def _workspace(who, nbytes, device, stream=None):
     """A workspace for one call on `stream` (None: the current one), out of
     the memory of that stream: what another stream has given back may still
@@ -808,8 +818,11 @@ class DecodeStep:
     def decode_accumulate(self, stream=None):
         """decode() that also adds every token's attention weight to
         self.scores ([S, H, MB * bs] fp32, made on the first call; see
-        paged_attention_decode_accumulate), which evict() goes by."""
+        paged_attention_decode_accumulate), which evict() goes by.  May be
+        captured in a graph after a first call outside it."""
         if self.scores is None or self.max_context_len > self._accumulate_bound:
+            # captured, every replay would zero the scores
+            _no_capture("the first decode_accumulate, which makes the scores,", stream, self.device)
             with _on(stream, self.device):
                 self._make_scores()
         return paged_attention_decode_accumulate(
@@ -844,6 +857,7 @@ class DecodeStep:
         graph reads the new ones.  Evicted rows own their blocks: prefix_groups
         and beam_groups are dropped, and a beam search that has begun with
         groups is refused.  Returns the number of blocks freed."""
+        _no_capture("evict, whose tables are the host's,", stream, self.device)
         with _on(stream, self.device):
             return self._evict(budget, recent_tokens, sink_tokens)
 

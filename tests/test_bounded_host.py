@@ -38,7 +38,10 @@ class Streams:
         monkeypatch.setattr(torch.cuda, "stream", self.on)
         monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.now)
         monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: FakeStream(handle))
-        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+        self.captured = ()                   # handles of streams that are being captured
+        monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing",
+                            lambda: self.now.cuda_stream in self.captured)
         monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
         for name in ("empty", "zeros", "full", "empty_like"):
             monkeypatch.setattr(torch, name, self.logged(name, getattr(torch, name)))
@@ -53,7 +56,7 @@ class Streams:
 
     @contextlib.contextmanager
     def on(self, stream):
-        before, self.now = self.now, stream
+        before, self.now = self.now, stream or self.now
         try:
             yield
         finally:
@@ -462,3 +465,27 @@ def test_a_step_is_not_written_again_after_an_eviction(monkeypatch):
     assert kernels.calls[done:] == [("decode", None)] * 2
     st.plan()
     st.run()
+
+
+@pytest.mark.parametrize("captured,given", [(0, None), (5, 5), (0, 5)])
+def test_what_a_graph_would_repeat_is_not_captured(monkeypatch, captured, given):
+    """A captured first decode_accumulate would zero the scores on every replay; evict decides on the host."""
+    streams = Streams(monkeypatch)
+    kernels = FakeKernels(monkeypatch)
+    side = None if given is None else FakeStream(given)
+    st = cpu_step()
+    free, tables = st.allocator.num_free, st.tables_host.copy()
+    streams.captured = (captured,)
+    with pytest.raises(L.PkvError, match="cannot be captured"):
+        st.decode_accumulate(stream=side)
+    assert st.scores is None
+    streams.captured = ()
+    st.decode_accumulate(stream=side)
+    streams.captured = (captured,)
+    st.decode_accumulate(stream=side)        # this may be
+    waited = len(streams.now.waited), 0 if side is None else len(side.waited)
+    with pytest.raises(L.PkvError, match="cannot be captured"):
+        st.evict(96, 20, 4, stream=side)
+    assert np.array_equal(st.tables_host, tables) and st.allocator.num_free == free
+    assert (len(streams.now.waited), 0 if side is None else len(side.waited)) == waited
+    assert [name for name, _ in kernels.calls] == ["accumulate"] * 2

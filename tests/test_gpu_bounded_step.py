@@ -159,3 +159,27 @@ def test_cycles_of_beam_search_and_eviction(dtype, D, streamed):
             attended(q)
         rows.check_state(st, 1e-4)
     assert L.pkv_get_device_errors() == 0
+
+
+def test_captured_weights_add_up():
+    """decode_accumulate captured after a first call: every replay adds the
+    same weights; a first call or an eviction inside a capture is refused."""
+    st, side = shared_step(), torch.cuda.Stream()
+    with pytest.raises(L.PkvError, match="cannot be captured"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):
+            st.decode_accumulate()
+    assert st.scores is None
+    st.decode_accumulate()
+    torch.cuda.synchronize()
+    once = st.scores.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        st.decode_accumulate()
+        with pytest.raises(L.PkvError, match="cannot be captured"):
+            st.evict(96, 20, 4)
+    for k in (2, 3):
+        graph.replay()
+        torch.cuda.synchronize()
+        # k sums of one weight, each rounded to fp32
+        assert torch.allclose(st.scores, k * once, rtol=3 * 2.0 ** -24, atol=0)
+    assert L.pkv_get_device_errors() == 0
