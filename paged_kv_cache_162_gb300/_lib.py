@@ -10,6 +10,7 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -169,6 +170,18 @@ def stream_handle(stream) -> int | None:
     return stream.cuda_stream
 
 
+def int32(value, name: str) -> int:
+    """`value` as an int; refuses what ctypes would cut to 32 bits."""
+    value = operator.index(value)
+    if not -(1 << 31) <= value < 1 << 31:
+        raise PkvError(PKV_ERR_INVALID_ARG, f"{name} = {value} does not fit 32 bits")
+    return value
+
+
+def _int32s(*values) -> bool:
+    return all(-(1 << 31) <= v < 1 << 31 for v in values)
+
+
 def check(status: int, what: str = "") -> None:
     if status != PKV_OK:
         msg = lib().pkv_last_error_string().decode(errors="replace")
@@ -236,6 +249,8 @@ def pkv_paged_attention_decode_noalloc(out, q, k_cache, v_cache, block_tables, c
 
 
 def pkv_decode_window_workspace_size(S, H, Hkv, D) -> int:
+    if not _int32s(S, H, Hkv, D):
+        return 0
     return int(lib().pkv_decode_window_workspace_size(S, H, Hkv, D))
 
 
@@ -245,13 +260,16 @@ def pkv_paged_attention_decode_window(out, q, k_cache, v_cache, block_tables, co
                                       stream=None) -> None:
     st = lib().pkv_paged_attention_decode_window(
         ptr(out), ptr(q), ptr(k_cache), ptr(v_cache), ptr(block_tables), ptr(context_lens), S, H,
-        Hkv, D, bs, NB, MB, max_context_len, window, sink_tokens, scale, dtype, ptr(workspace),
-        workspace_bytes, stream_handle(stream))
+        Hkv, D, bs, NB, MB, int32(max_context_len, "max_context_len"), int32(window, "window"),
+        int32(sink_tokens, "sink_tokens"), scale, dtype, ptr(workspace), workspace_bytes,
+        stream_handle(stream))
     if st:
         check(st, "paged_attention_decode_window")
 
 
 def pkv_decode_accumulate_workspace_size(S, H, Hkv, D, max_context_len) -> int:
+    if not _int32s(S, H, Hkv, D, max_context_len):
+        return 0
     return int(lib().pkv_decode_accumulate_workspace_size(S, H, Hkv, D, max_context_len))
 
 
@@ -261,13 +279,15 @@ def pkv_paged_attention_decode_accumulate(out, scores, q, k_cache, v_cache, bloc
                                           stream=None) -> None:
     st = lib().pkv_paged_attention_decode_accumulate(
         ptr(out), ptr(scores), ptr(q), ptr(k_cache), ptr(v_cache), ptr(block_tables),
-        ptr(context_lens), S, H, Hkv, D, bs, NB, MB, max_context_len, score_stride, scale, dtype,
-        ptr(workspace), workspace_bytes, stream_handle(stream))
+        ptr(context_lens), S, H, Hkv, D, bs, NB, MB, int32(max_context_len, "max_context_len"),
+        score_stride, scale, dtype, ptr(workspace), workspace_bytes, stream_handle(stream))
     if st:
         check(st, "paged_attention_decode_accumulate")
 
 
 def pkv_evict_workspace_size(S, Hkv, budget) -> int:
+    if not _int32s(S, Hkv, budget):
+        return 0
     return int(lib().pkv_evict_workspace_size(S, Hkv, budget))
 
 
@@ -278,8 +298,10 @@ def pkv_evict_tokens(k_cache, v_cache, scores, positions, block_tables, context_
     st = lib().pkv_evict_tokens(
         ptr(k_cache), ptr(v_cache), ptr(scores), ptr(positions), ptr(block_tables),
         ptr(context_lens), ptr(token_counts), ptr(scores_out), ptr(positions_out),
-        ptr(new_context_lens), S, Hkv, D, bs, NB, MB, max_context_len, score_stride, budget,
-        recent_tokens, sink_tokens, dtype, ptr(workspace), workspace_bytes, stream_handle(stream))
+        ptr(new_context_lens), S, Hkv, D, bs, NB, MB, int32(max_context_len, "max_context_len"),
+        score_stride, int32(budget, "budget"), int32(recent_tokens, "recent_tokens"),
+        int32(sink_tokens, "sink_tokens"), dtype, ptr(workspace), workspace_bytes,
+        stream_handle(stream))
     if st:
         check(st, "evict_tokens")
 

@@ -12,7 +12,7 @@ import ctypes
 
 import numpy as np
 
-from ._lib import PKV_ERR_INVALID_ARG, OutOfBlocks, PkvError, check, lib  # noqa: F401
+from ._lib import PKV_ERR_INVALID_ARG, OutOfBlocks, PkvError, check, int32, lib  # noqa: F401
 
 
 def _need_i32(a: np.ndarray, what: str) -> None:
@@ -143,9 +143,10 @@ class BlockAllocator:
         _need_i32(row, "row")
         if int(num_blocks) > len(row):
             raise PkvError(PKV_ERR_INVALID_ARG, "truncate: num_blocks is past the row")
-        nb, freed = ctypes.c_int32(int(num_blocks)), ctypes.c_int32(0)
-        check(lib().pkv_alloc_truncate(self._h, row.ctypes.data, ctypes.addressof(nb), int(tokens),
-                                       int(block_size), ctypes.addressof(freed)), "alloc_truncate")
+        nb, freed = ctypes.c_int32(int32(num_blocks, "num_blocks")), ctypes.c_int32(0)
+        check(lib().pkv_alloc_truncate(self._h, row.ctypes.data, ctypes.addressof(nb),
+                                       int32(tokens, "tokens"), int32(block_size, "block_size"),
+                                       ctypes.addressof(freed)), "alloc_truncate")
         return int(nb.value), int(freed.value)
 
     def release_window(self, row: np.ndarray, num_blocks: int, context_len: int, window: int,
@@ -157,10 +158,11 @@ class BlockAllocator:
         if int(num_blocks) > len(row):
             raise PkvError(PKV_ERR_INVALID_ARG, "release_window: num_blocks is past the row")
         freed = ctypes.c_int32(0)
-        check(lib().pkv_alloc_release_window(self._h, row.ctypes.data, int(num_blocks),
-                                             int(context_len), int(window), int(sink_tokens),
-                                             int(block_size), ctypes.addressof(freed)),
-              "alloc_release_window")
+        check(lib().pkv_alloc_release_window(
+            self._h, row.ctypes.data, int32(num_blocks, "num_blocks"),
+            int32(context_len, "context_len"), int32(window, "window"),
+            int32(sink_tokens, "sink_tokens"), int32(block_size, "block_size"),
+            ctypes.addressof(freed)), "alloc_release_window")
         return int(freed.value)
 
     def refcount(self, block: int) -> int:

@@ -170,6 +170,7 @@ def _attention_sizes(who, out, q, k_cache, v_cache, block_tables, context_lens):
     NB, bs, Hkv, Dk = cshape
     if Dk != D:
         _refuse(f"{who}: q has head_dim {D}, the caches {Dk}")
+    L.int32(max(*shape, *cshape, *tshape), f"{who}: the largest extent")
     dt, dev = k_cache.dtype, k_cache.get_device()
     if not (dev >= 0 and q.dtype is dt and out.dtype is dt and v_cache.dtype is dt
             and block_tables.dtype is _I32 and context_lens.dtype is _I32 and out.shape == shape
@@ -271,6 +272,8 @@ def paged_attention_decode_window(out, q, k_cache, v_cache, block_tables, contex
             L.check(st, who)
     S, H, D, NB, bs, Hkv, MB, dev = _attention_sizes(who, out, q, k_cache, v_cache, block_tables,
                                                      context_lens)
+    window, sink_tokens, max_context_len = (L.int32(window, "window"), L.int32(sink_tokens, "sink_tokens"),
+                                            L.int32(max_context_len, "max_context_len"))
     ws = workspace
     if ws is None:
         ws = _workspace(who, L.pkv_decode_window_workspace_size(S, H, Hkv, D), k_cache.device, stream)
@@ -312,6 +315,7 @@ def paged_attention_decode_accumulate(out, scores, q, k_cache, v_cache, block_ta
             L.check(st, who)
     S, H, D, NB, bs, Hkv, MB, dev = _attention_sizes(who, out, q, k_cache, v_cache, block_tables,
                                                      context_lens)
+    max_context_len = L.int32(max_context_len, "max_context_len")
     rows = scores.shape
     if not (scores.dtype is _F32 and len(rows) == 3 and rows[0] == S and rows[1] == Hkv
             and scores.is_contiguous() and scores.get_device() == dev):
@@ -373,6 +377,10 @@ def evict_tokens(k_cache, v_cache, scores, positions, block_tables, context_lens
         _refuse(f"{who}: the caches must be [NB, bs, Hkv, D], block_tables [S, MB]")
     NB, bs, Hkv, D = k_cache.shape
     S, MB = block_tables.shape
+    L.int32(max(*k_cache.shape, S, MB), f"{who}: the largest extent")
+    budget, recent_tokens, sink_tokens, max_context_len = (
+        L.int32(budget, "budget"), L.int32(recent_tokens, "recent_tokens"),
+        L.int32(sink_tokens, "sink_tokens"), L.int32(max_context_len, "max_context_len"))
     dt, dev = k_cache.dtype, k_cache.get_device()
     rows = scores.shape
     if not (dev >= 0 and len(rows) == 3 and rows[0] == S and rows[1] == Hkv and v_cache.dtype is dt

@@ -13,6 +13,7 @@ import workloads as W
 from oracle import bounded as B
 from paged_kv_cache_162_gb300 import _lib as L
 from paged_kv_cache_162_gb300 import engine as E
+from paged_kv_cache_162_gb300.allocator import BlockAllocator
 from tests.bounded_rows import Rows
 
 
@@ -489,3 +490,67 @@ def test_what_a_graph_would_repeat_is_not_captured(monkeypatch, captured, given)
     assert np.array_equal(st.tables_host, tables) and st.allocator.num_free == free
     assert (len(streams.now.waited), 0 if side is None else len(side.waited)) == waited
     assert [name for name, _ in kernels.calls] == ["accumulate"] * 2
+
+
+# ------------------------------------------------------- numbers past 32 bits
+FAR = [2 ** 32 + 8, 2 ** 31, -2 ** 31 - 1, 2 ** 40]
+
+
+def window_args(**kw):
+    a = dict(out=16, q=16, k_cache=16, v_cache=16, block_tables=16, context_lens=16, S=2, H=8, Hkv=4, D=128, bs=16,
+             NB=8, MB=4, max_context_len=0, window=8, sink_tokens=2, scale=0.1, dtype=L.PKV_F16, workspace=256,
+             workspace_bytes=10, stream=0)
+    a.update(kw)
+    return a
+
+
+@pytest.mark.parametrize("far", FAR)
+def test_numbers_past_32_bits_are_refused_not_cut(far):
+    """2**32 + 8 is no window of 8."""
+    def refused(call, *args, **kw):
+        with pytest.raises(L.PkvError, match="does not fit 32 bits") as e:
+            call(*args, **kw)
+        assert e.value.status == L.PKV_ERR_INVALID_ARG
+    for name in ("window", "sink_tokens", "max_context_len"):
+        refused(L.pkv_paged_attention_decode_window, **window_args(**{name: far}))
+    a = window_args(scores=16, score_stride=64, max_context_len=far)
+    del a["window"], a["sink_tokens"]
+    refused(L.pkv_paged_attention_decode_accumulate, **a)
+    for name in ("budget", "recent_tokens", "sink_tokens", "max_context_len"):
+        refused(L.pkv_evict_tokens, **evict_args(**{name: far}))
+    assert L.pkv_decode_window_workspace_size(far, 8, 8, 64) == 0
+    assert L.pkv_decode_accumulate_workspace_size(1, 8, 8, 64, far) == 0
+    assert L.pkv_evict_workspace_size(1, 8, far) == 0
+    # the tensor calls (their own checks come first on the CPU: what they pass on is checked next)
+    k, q = torch.zeros(4, 16, 2, 64, dtype=torch.float16), torch.zeros(1, 2, 64, dtype=torch.float16)
+    t, n, sc = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2, 64)
+    huge = torch.zeros(1, 1, dtype=torch.int32).expand(1, 2 ** 31)
+    for name, tables in (("window", t), ("sink_tokens", t), ("max_context_len", t), (None, huge)):
+        kw = dict(window=4, **({} if name in (None, "window") else {name: far}))
+        kw.update({name: far} if name == "window" else {})
+        with pytest.MonkeyPatch.context() as m:
+            m.setattr(E, "_need", lambda *a: None)
+            refused(E.paged_attention_decode_window, q.clone(), q, k, k, tables, n, **kw)
+            if name in (None, "max_context_len"):
+                kw.pop("window")
+                refused(E.paged_attention_decode_accumulate, q.clone(), sc, q, k, k, tables, n, **kw)
+    for name in ("budget", "recent_tokens", "sink_tokens", "max_context_len"):
+        kw = {**dict(budget=8, recent_tokens=2), name: far}
+        refused(E.evict_tokens, k, k, sc, sc.int(), t, n, n, n.clone(), **kw)
+    refused(E.evict_tokens, k, k, sc, sc.int(), huge, n, n, n.clone(), 8, 2)
+
+
+@pytest.mark.parametrize("far", FAR)
+def test_the_allocator_does_not_cut_numbers(far):
+    a = BlockAllocator(8)
+    row = np.array(a.alloc(4), np.int32)
+    before = row.copy()
+    calls = [lambda: a.truncate(row, 4, far, 16), lambda: a.truncate(row, 4, 16, far)]
+    calls += [lambda kw=kw: a.release_window(row, **{**dict(num_blocks=4, context_len=64, window=8, sink_tokens=0,
+                                                            block_size=16), **kw})
+              for kw in ({"context_len": far}, {"window": far}, {"sink_tokens": far}, {"block_size": far})]
+    for call in calls:
+        with pytest.raises(L.PkvError, match="does not fit 32 bits"):
+            call()
+    assert np.array_equal(row, before) and a.num_free == 4
+    assert a.truncate(row, np.int64(4), np.int64(33), np.int32(16)) == (3, 1)   # numpy's integers are taken
