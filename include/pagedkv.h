@@ -291,7 +291,8 @@ pkv_status pkv_paged_attention_decode_window(
 
 /* Bytes of workspace for pkv_paged_attention_decode_accumulate (0 for
  * invalid arguments): the logits of every query head take 4 * S * H *
- * max_context_len of them. */
+ * max_context_len of them.  max_context_len >= 1 is the bound that the call
+ * goes by: MB*bs where the call is given 0. */
 size_t pkv_decode_accumulate_workspace_size(int S, int H, int Hkv, int D, int max_context_len);
 
 /* Decode attention that also adds every token's attention weight to a

@@ -1668,7 +1668,7 @@ pkv_status pkv_paged_attention_decode_window(
 }
 
 size_t pkv_decode_accumulate_workspace_size(int S, int H, int Hkv, int D, int max_context_len) {
-    if (!workspace_args_ok(S, H, Hkv, D) || max_context_len < 0 || max_context_len > INT32_MAX - 64)
+    if (!workspace_args_ok(S, H, Hkv, D) || max_context_len < 1 || max_context_len > INT32_MAX - 64)
         return 0;
     return layout_of(S, H, Hkv, D, true, max_context_len).total;
 }

@@ -242,6 +242,9 @@ def new_window_workspace(S, H, Hkv, D, device="cuda") -> torch.Tensor:
 
 
 def new_accumulate_workspace(S, H, Hkv, D, max_context_len, device="cuda") -> torch.Tensor:
+    """max_context_len: the call's, or MB * bs where the call is given 0."""
+    if max_context_len < 1:
+        _refuse("new_accumulate_workspace: max_context_len must be at least 1 (MB * bs for a call given 0)")
     return _workspace("new_accumulate_workspace",
                       L.pkv_decode_accumulate_workspace_size(S, H, Hkv, D, max_context_len), device)
 

@@ -554,3 +554,13 @@ def test_the_allocator_does_not_cut_numbers(far):
             call()
     assert np.array_equal(row, before) and a.num_free == 4
     assert a.truncate(row, np.int64(4), np.int64(33), np.int32(16)) == (3, 1)   # numpy's integers are taken
+
+
+def test_no_workspace_for_a_context_of_zero():
+    """A call takes 0 as MB * bs: a workspace made for 0 would be too small for it."""
+    assert L.pkv_decode_accumulate_workspace_size(2, 8, 4, 128, 0) == 0
+    assert L.pkv_decode_accumulate_workspace_size(2, 8, 4, 128, 1) > 0
+    for n in (0, -1):
+        with pytest.raises(L.PkvError, match="MB \\* bs") as e:
+            E.new_accumulate_workspace(2, 8, 4, 128, n, device="cpu")
+        assert e.value.status == L.PKV_ERR_INVALID_ARG
