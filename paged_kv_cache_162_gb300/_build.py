@@ -1,5 +1,8 @@
 """Builds libpagedkv.so in-tree for sm_103a (nvcc, no cmake), and
-_tensor_bind.so, which calls it with torch tensors (g++ against torch).
+_tensor_bind.so, which calls it with torch tensors (g++ against torch).  The
+library needs no torch: without one, or where the module does not compile
+against it, the library is built all the same and engine.py calls it through
+ctypes.
 
 Each translation unit compiles in parallel; the link uses the shared CUDA
 runtime so the library and PyTorch share one runtime in a process.
@@ -10,7 +13,9 @@ every C-ABI call (for profilers); the default build has none.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -52,20 +57,45 @@ def _inputs():
 
 
 FLAGS = os.path.join(BUILD, "flags.txt")
+BIND_FLAGS = os.path.join(BUILD, "bind_flags.txt")
 
 
 def _defines() -> list[str]:
     return ["-DPKV_NVTX"] if os.environ.get("PKV_NVTX", "") not in ("", "0") else []
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
+def _torch_version() -> str:
+    """The installed torch's version, without importing it; "" without one."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return ""
+    with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
+        found = re.search(r"^__version__ = '([^']+)'", f.read(), re.M)
+    return found.group(1) if found else ""
+
+
+def _current(out: str, flags: str, want: str) -> bool:
+    """`out` was built with the flags `want`, after the last change of any source."""
+    if not os.path.exists(out) or not os.path.exists(flags):
         return False
-    built = open(FLAGS).read() if os.path.exists(FLAGS) else ""
-    if built != " ".join(_defines()):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
+    with open(flags) as f:
+        if f.read() != want:
+            return False
+    t = os.path.getmtime(out)
     return all(os.path.getmtime(p) <= t for p in _inputs())
+
+
+def _lib_current() -> bool:
+    return _current(LIB, FLAGS, " ".join(_defines()))
+
+
+def _bind_current() -> bool:
+    torch = _torch_version()
+    return not torch or _current(BIND, BIND_FLAGS, torch)
+
+
+def up_to_date() -> bool:
+    return _lib_current() and _bind_current()
 
 
 def _torch_flags():
@@ -77,6 +107,7 @@ def _torch_flags():
     inc = [os.path.join(root, "include"), sysconfig.get_paths()["include"]]
     lib = os.path.join(root, "lib")
     return ([f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             f'-DPKV_TORCH_VERSION="{torch.__version__}"',
              *[x for p in inc for x in ("-isystem", p)]],
             ["-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"])
 
@@ -101,29 +132,46 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _link(out: str, cmd: list[str]) -> None:
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = [*cmd, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+
+
+def _no_bind(error: Exception) -> None:
+    """Says why there is no _tensor_bind.so; one of another build would not do."""
+    if os.path.exists(BIND):
+        os.remove(BIND)
+    sys.stderr.write(f"_tensor_bind.so was not built; calls go through ctypes: {error}\n")
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and up_to_date():
+    lib, bind = force or not _lib_current(), force or not _bind_current()
+    if not lib and not bind:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     extra = (["-Xptxas", "-v"] if verbose_ptxas else []) + _defines()
-    srcs = [os.path.join(CSRC, s) for s in [BIND_SOURCE] + CU_SOURCES + CXX_SOURCES]
-    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    srcs = [os.path.join(CSRC, s) for s in CU_SOURCES + CXX_SOURCES] if lib else []
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        bind_obj = ex.submit(_compile, os.path.join(CSRC, BIND_SOURCE), extra) if bind and _torch_version() else None
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-    bind, objs = objs[0], objs[1:]
-    libdir = os.path.join(cuda_home(), "lib64")
-    for out, cmd in (
-            (LIB, [_nvcc(), *ARCH, "-shared", "-cudart", "shared", *objs,
-                   "-Xlinker", f"-rpath,{libdir}"]),
-            (BIND, ["g++", "-shared", bind, "-L", PKG, "-l:libpagedkv.so", "-Wl,-rpath,$ORIGIN",
-                    *_torch_flags()[1]])):
-        tmp = out + f".tmp{os.getpid()}"
-        cmd = [*cmd, "-o", tmp]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, out)
-    with open(FLAGS, "w") as f:
-        f.write(" ".join(_defines()))
+    if lib:
+        libdir = os.path.join(cuda_home(), "lib64")
+        _link(LIB, [_nvcc(), *ARCH, "-shared", "-cudart", "shared", *objs, "-Xlinker", f"-rpath,{libdir}"])
+        with open(FLAGS, "w") as f:
+            f.write(" ".join(_defines()))
+    if bind_obj is not None:
+        try:
+            _link(BIND, ["g++", "-shared", bind_obj.result(), "-L", PKG, "-l:libpagedkv.so", "-Wl,-rpath,$ORIGIN",
+                         *_torch_flags()[1]])
+        except Exception as e:  # whatever torch, its headers or g++ make of it
+            _no_bind(e)
+        else:
+            with open(BIND_FLAGS, "w") as f:
+                f.write(_torch_version())
     return LIB
 
 

@@ -217,4 +217,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_bind", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tensor_bind() { return PyModule_Create(&module); }
+// torch_version: the torch that this was built against, the only one that it may be used with.
+PyMODINIT_FUNC PyInit__tensor_bind() {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", PKV_TORCH_VERSION) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

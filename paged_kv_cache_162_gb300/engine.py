@@ -120,6 +120,11 @@ def paged_attention_decode_shared_prefix(out, q, k_cache, v_cache, block_tables,
     return out
 
 
+class _AskCtypes:
+    """Stands for _tensor_bind where there is none for this torch: every call is left to ctypes."""
+    window = accumulate = evict = staticmethod(lambda *args: -1)
+
+
 _bind = None
 
 
@@ -130,8 +135,11 @@ def _native():
     global _bind
     if _bind is None:
         L.lib()
-        from . import _tensor_bind
-        _bind = _tensor_bind
+        try:
+            from . import _tensor_bind as found
+        except ImportError:  # not built, or for a torch with other symbols
+            found = None
+        _bind = found if found and found.torch_version == torch.__version__ else _AskCtypes
     return _bind
 
 

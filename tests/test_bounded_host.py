@@ -564,3 +564,58 @@ def test_no_workspace_for_a_context_of_zero():
         with pytest.raises(L.PkvError, match="MB \\* bs") as e:
             E.new_accumulate_workspace(2, 8, 4, 128, n, device="cpu")
         assert e.value.status == L.PKV_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ the build
+def a_build(tmp_path, monkeypatch, bad=()):
+    """The build with its files under tmp_path and its commands recorded, not run; those that name something in
+    `bad` fail."""
+    from paged_kv_cache_162_gb300 import _build
+    ran = []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        fails = any(b in " ".join(cmd) for b in bad)
+        if not fails:
+            with open(cmd[cmd.index("-o") + 1], "w") as f:
+                f.write("built")
+        return subprocess.CompletedProcess(cmd, int(fails), "", "no such header" if fails else "")
+    for name in ("BUILD", "LIB", "BIND", "FLAGS", "BIND_FLAGS"):
+        monkeypatch.setattr(_build, name, str(tmp_path / name.lower()), raising=False)
+    monkeypatch.setattr(_build.subprocess, "run", run)
+    return _build, ran
+
+
+def test_the_library_is_built_where_the_binding_is_not(tmp_path, monkeypatch, capfd):
+    """A C user has nvcc and no torch, or a torch that the binding does not compile against."""
+    build, ran = a_build(tmp_path, monkeypatch, bad=["tensor_bind.cpp"])
+    (tmp_path / "bind").write_text("of another build")
+    assert build.build() == build.LIB and os.path.exists(build.LIB)
+    assert not os.path.exists(build.BIND)              # no stale one either
+    assert "no such header" in capfd.readouterr().err and not build.up_to_date()
+    monkeypatch.setattr(build, "_torch_version", lambda: "")
+    assert build.up_to_date()                          # without a torch nothing is missing
+    os.remove(build.LIB)
+    ran.clear()
+    build.build()
+    assert os.path.exists(build.LIB) and not any("tensor_bind" in " ".join(c) for c in ran)
+
+
+def test_the_binding_is_built_again_for_another_torch(tmp_path, monkeypatch):
+    build, ran = a_build(tmp_path, monkeypatch)
+    build.build()
+    assert build.up_to_date() and os.path.exists(build.BIND)
+    ran.clear()
+    monkeypatch.setattr(build, "_torch_version", lambda: "9.9")
+    assert not build.up_to_date()
+    build.build()
+    assert build.up_to_date() and len(ran) == 2 and not any(".cu" in " ".join(c[:-1]) for c in ran)
+
+
+def test_a_binding_of_another_torch_is_not_used(monkeypatch):
+    monkeypatch.setattr(E, "_bind", None)
+    native = E._native()
+    assert native.torch_version == torch.__version__   # this tree's is for this torch
+    monkeypatch.setattr(E, "_bind", None)
+    monkeypatch.setattr(torch, "__version__", "1.0")
+    assert E._native().window(1, 2, 3) == E._native().evict() == -1
