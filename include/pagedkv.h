@@ -279,8 +279,8 @@ size_t pkv_decode_window_workspace_size(int S, int H, int Hkv, int D);
  *                 needed; one call at a time may use it
  *   other arguments as in pkv_paged_attention_decode.
  * Computation is fp32; attention weights enter P.V as the sum of two 16-bit
- * numbers (relative error 2^-16 at most for bf16); one rounding to dtype at
- * the end.  A visible V element that is not finite makes its output elements
+ * numbers (relative error at most 2^-16 in bf16, in fp16 2^-22 or 2^-40 of the
+ * row's largest weight); one rounding to dtype at the end.  A visible V element that is not finite makes its output elements
  * not finite. */
 pkv_status pkv_paged_attention_decode_window(
     void* out, const void* q, const void* k_cache, const void* v_cache,

@@ -147,6 +147,20 @@ __device__ __forceinline__ int visible_of(const Params& p, int n) {
 // 1 / L, 0 for a row that sees nothing.
 __device__ __forceinline__ float inverse_of(float L) { return L > 0.f || L != L ? 1.f / L : 0.f; }
 
+// What a weight of 1 is in P.V.  In fp16 a weight below 2^-25 would be nothing and
+// one below 2^-14 lose digits, and a long context's can all be: one token of
+// logit 0 among 2^20 of -18 has 1.6 % of the weight lost.  In units of 2^-15 (the
+// largest weight is 1: 32768 of 65504) the same happens below 2^-40.  bf16 has the
+// range of fp32.
+template <class E>
+constexpr float kWeightUnits = 1.f;
+template <>
+constexpr float kWeightUnits<pkv::F16> = 32768.f;
+
+// What makes a row of P.V the output: 1 / L, and the units of the weights.
+template <class E>
+__device__ __forceinline__ float output_scale(float L) { return inverse_of(L) * (1.f / kWeightUnits<E>); }
+
 // Tiles of a unit; an empty context has one, which writes zeros.
 __device__ __forceinline__ int tiles_of(const Params& p, int n) {
     const int t = (visible_of(p, n) + (1 << p.tile_log2) - 1) >> p.tile_log2;
@@ -609,7 +623,7 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float x = sc[2 * h + j][2 * r], y = sc[2 * h + j][2 * r + 1];
+                    const float x = sc[2 * h + j][2 * r] * kWeightUnits<E>, y = sc[2 * h + j][2 * r + 1] * kWeightUnits<E>;
                     const uint32_t hi = E::from_float2(x, y);
                     const float2 back = E::to_float2(hi);
                     ph[2 * j + r] = hi;
@@ -891,6 +905,7 @@ __device__ __forceinline__ void join_cluster(const Params& p, int s, int kvh, in
             for (int x = kMaxCluster / 2; x >= 1; x >>= 1) L += __shfl_xor_sync(kFull, L, x);
             inv = inverse_of(__shfl_sync(kFull, L, 0));
         }
+        inv *= 1.f / kWeightUnits<E>;
         for (int i = 0; i < CS; ++i) o = fmaf(__shfl_sync(kFull, w, i), in->o[(k * CS + i) * 32 + lane], o);
         o *= inv;
         const float next = __shfl_down_sync(kFull, o, 1);
@@ -910,7 +925,7 @@ __device__ __forceinline__ void write_rows(const Params& p, int s, int kvh, int 
     for (int r = 0; r < (kWide ? 2 : 1); ++r) {
         const int row = g + 8 * r;
         if (row < p.G) {
-            const float inv = inverse_of(a.l[r]);
+            const float inv = output_scale<E>(a.l[r]);
             uint16_t* dst = static_cast<uint16_t*>(p.out) +
                             ((int64_t)s * p.H + (int64_t)kvh * p.G + row) * D + 2 * t;
 #pragma unroll
@@ -959,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 2) direct_kernel(const __grid_consta
     for (int r = 0; r < (kWide ? 2 : 1); ++r) {
         const int row = (lane >> 2) + 8 * r;
         if (row < p.G) {
-            const float inv = inverse_of(a.l[r]);
+            const float inv = output_scale<E>(a.l[r]);
             uint16_t* dst = static_cast<uint16_t*>(p.out) +
                             ((int64_t)s * p.H + (int64_t)kvh * p.G + row) * D + 8 * COLS * warp + 2 * (lane & 3);
 #pragma unroll
@@ -1163,7 +1178,7 @@ __device__ __forceinline__ void gather_row(const Params& p, int c0, int c, int c
 template <class E, int D>
 __device__ __forceinline__ void write_row(const Params& p, int unit, int i, int lane, float L,
                                           const float (&o)[D / 32]) {
-    const float inv = inverse_of(L);
+    const float inv = output_scale<E>(L);
     const int64_t oh = (int64_t)(unit / p.HB) * p.H + (int64_t)(unit % p.HB) * p.hw * p.G + i;
     uint16_t* dst = static_cast<uint16_t*>(p.out) + oh * D + lane * (D / 32);
 #pragma unroll

@@ -183,3 +183,42 @@ def test_captured_weights_add_up():
         # k sums of one weight, each rounded to fp32
         assert torch.allclose(st.scores, k * once, rtol=3 * 2.0 ** -24, atol=0)
     assert L.pkv_get_device_errors() == 0
+
+
+@pytest.mark.parametrize("D,H,Hkv,n", [(64, 2, 2, 700), (128, 12, 1, 5000), (64, 3, 1, 40000), (128, 20, 4, 20000),
+                                       (64, 4, 4, 60000)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_many_small_weights_are_not_lost(dtype, D, H, Hkv, n):
+    """One token of logit 0 and V = 0, the others of logit -18 and V = 1000:
+    the output is made of weights of 1.5e-8, below half the smallest fp16
+    number.  check_out's bound without its term for those: a weight is the
+    sum of two 16-bit numbers in units of 2^-15, 2^-40 absolute at most."""
+    c = make(n, 1, H, Hkv, D, 16, dtype, [n])
+    top = int(B.rows_of(c["tables"][0], [n // 3], 16)[0])
+    for name, rest, one in (("k", -18.0, 0.0), ("v", 1000.0, 0.0)):
+        c[name][:] = 0
+        rows = c[name].view(-1, Hkv, D)
+        rows[:, :, slice(0, 1) if name == "k" else slice(None)] = rest
+        rows[top] = one
+    c["q"][:] = 0
+    c["q"][:, :, 0] = 8.0
+    c["scale"] = 0.125
+    d = dev(c)
+    scores = torch.zeros(1, Hkv, c["MB"] * 16, device="cuda")
+    ref, weights, mag = B.attend(f64(c["q"]), f64(c["k"]), f64(c["v"]), c["tables"], c["lens"], c["scale"])
+    assert ref.min() > 0.9 * n * 1.5e-5
+    u = torch.finfo(c["q"].dtype).eps / 2
+    tiny = 2.0 ** -25 if dtype == "f16" else 0.0     # a subnormal output's rounding
+    tol = u * np.abs(ref) + (1 + u) * (mag * (weight_error(c) + u * u) + n * 2.0 ** -40 * 1000) + tiny
+    for call in ("window", "accumulate"):
+        d["out"].fill_(float("nan"))
+        if call == "window":
+            E.paged_attention_decode_window(d["out"], d["q"], d["k"], d["v"], d["tables"], d["lens"], n, 0, c["scale"])
+        else:
+            E.paged_attention_decode_accumulate(d["out"], scores, d["q"], d["k"], d["v"], d["tables"], d["lens"],
+                                                c["scale"])
+        err = np.abs(f64(d["out"].cpu()) - ref)
+        assert np.all(err <= tol), f"{call}: {err.max():.3g} of {ref.max():.3g}"
+    want = B.accumulate(np.zeros(scores.shape), weights, Hkv)
+    w = weight_error(c) + (H // Hkv + 1) * 2.0 ** -24
+    assert np.all(np.abs(f64(scores.cpu()) - want) <= w * want + 2.0 ** -126)
