@@ -250,7 +250,8 @@ pkv_status pkv_paged_attention_decode_noalloc(
  * multiple of Hkv, at most 16 query heads per KV head (PKV_ERR_UNSUPPORTED
  * above); query head h uses KV head h / (H / Hkv).  The caches are then
  * [NB][bs][Hkv][D], as pkv_reshape_and_cache and pkv_copy_blocks lay them
- * out for H = Hkv.  NB * bs must fit 31 bits; S at most 32767.
+ * out for H = Hkv.  NB * bs must fit 31 bits; S at most 32767; contexts of
+ * attention at most 2^31 - 1025 tokens, of eviction 2^30 - 1.
  *
  * The calls may be captured in a graph; make the first call on a device
  * before a capture begins.  max_context_len decides how work is spread (a

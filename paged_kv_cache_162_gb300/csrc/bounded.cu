@@ -1436,6 +1436,8 @@ constexpr int direct_waves(bool scores, int64_t most) { return !scores ? 4 : mos
 constexpr int kJoinCtasPerSm = 3;   // of the join kernel
 constexpr int kCtasPerSm = 2;       // of the attention kernels
 constexpr int kMinUnits = 16;       // of a split call, else fewer KV heads per unit
+// Longest context: token numbers go up to the end of a fold's 512 past it.
+constexpr int kMaxContext = INT32_MAX - 1024;
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -1544,9 +1546,9 @@ pkv_status run_bounded(const char* who, void* out, const void* q, const void* k_
     if (S > 32767 || (int64_t)S * H > INT32_MAX / kMaxCluster)
         return bad(PKV_ERR_INVALID_ARG, "at most 32767 sequences, and 2^27 heads in all of them");
     const int64_t cap = (int64_t)MB * bs;
-    const int64_t max_ctx = max_context_len == 0 ? (cap < INT32_MAX - 64 ? cap : INT32_MAX - 64) : max_context_len;
-    if (max_ctx < 0 || max_ctx > cap || max_ctx > INT32_MAX - 64)
-        return bad(PKV_ERR_INVALID_ARG, "max_context_len must be in [0, MB*bs]");
+    const int64_t max_ctx = max_context_len == 0 ? (cap < kMaxContext ? cap : kMaxContext) : max_context_len;
+    if (max_ctx < 0 || max_ctx > cap || max_ctx > kMaxContext)
+        return bad(PKV_ERR_INVALID_ARG, "max_context_len must be in [0, MB*bs], below 2^31 - 1024");
     if (S == 0) return PKV_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || (with_scores && !scores))
         return bad(PKV_ERR_INVALID_ARG, "null pointer");
@@ -1683,7 +1685,7 @@ pkv_status pkv_paged_attention_decode_window(
 }
 
 size_t pkv_decode_accumulate_workspace_size(int S, int H, int Hkv, int D, int max_context_len) {
-    if (!workspace_args_ok(S, H, Hkv, D) || max_context_len < 1 || max_context_len > INT32_MAX - 64)
+    if (!workspace_args_ok(S, H, Hkv, D) || max_context_len < 1 || max_context_len > kMaxContext)
         return 0;
     return layout_of(S, H, Hkv, D, true, max_context_len).total;
 }

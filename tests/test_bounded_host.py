@@ -619,3 +619,19 @@ def test_a_binding_of_another_torch_is_not_used(monkeypatch):
     monkeypatch.setattr(E, "_bind", None)
     monkeypatch.setattr(torch, "__version__", "1.0")
     assert E._native().window(1, 2, 3) == E._native().evict() == -1
+
+
+@pytest.mark.parametrize("most,status", [(2 ** 31 - 1, L.PKV_ERR_INVALID_ARG), (2 ** 31 - 1024, L.PKV_ERR_INVALID_ARG),
+                                         (2 ** 31 - 65, L.PKV_ERR_INVALID_ARG), (2 ** 31 - 1025, L.PKV_ERR_WORKSPACE)])
+def test_contexts_whose_token_numbers_would_pass_31_bits(most, status):
+    """The fold of the weights counts its tokens in stretches of up to 512: the last one must not wrap."""
+    a = window_args(MB=1 << 26, bs=64, max_context_len=most)
+    with pytest.raises(L.PkvError) as e:
+        L.pkv_paged_attention_decode_window(**a)
+    assert e.value.status == status
+    del a["window"], a["sink_tokens"]
+    with pytest.raises(L.PkvError) as e:
+        L.pkv_paged_attention_decode_accumulate(**a, scores=16, score_stride=1 << 32)
+    assert e.value.status == status
+    size = L.pkv_decode_accumulate_workspace_size(1, 2, 1, 64, most)
+    assert (size == 0) == (status == L.PKV_ERR_INVALID_ARG)
