@@ -824,9 +824,14 @@ class DecodeStep:
             self.out, self.q, self.k_cache, self.v_cache, self.block_tables, self.context_lens, g,
             self.scale, self.max_context_len, self.partition_tokens, stream=stream)
 
+    def _need_plan(self, who):
+        if self.block_tables is None:
+            _refuse(f"{who}: the step has no tables yet (plan() makes them)")
+
     def decode_window(self, window, sink_tokens=0, stream=None):
         """decode() over the first sink_tokens tokens and the last `window`
         of each context (see paged_attention_decode_window)."""
+        self._need_plan("decode_window")
         if getattr(self, "_window_ws", None) is None:
             with _on(stream, self.device):
                 self._window_ws = new_window_workspace(self.S, self.H, self.H, self.D, self.device)
@@ -839,6 +844,7 @@ class DecodeStep:
         self.scores ([S, H, MB * bs] fp32, made on the first call; see
         paged_attention_decode_accumulate), which evict() goes by.  May be
         captured in a graph after a first call outside it."""
+        self._need_plan("decode_accumulate")
         if self.scores is None or self.max_context_len > self._accumulate_bound:
             # captured, every replay would zero the scores
             _no_capture("the first decode_accumulate, which makes the scores,", stream, self.device)

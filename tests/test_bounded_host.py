@@ -635,3 +635,14 @@ def test_contexts_whose_token_numbers_would_pass_31_bits(most, status):
     assert e.value.status == status
     size = L.pkv_decode_accumulate_workspace_size(1, 2, 1, 64, most)
     assert (size == 0) == (status == L.PKV_ERR_INVALID_ARG)
+
+
+def test_a_step_without_a_plan_has_no_tables(monkeypatch):
+    kernels = FakeKernels(monkeypatch)
+    st = cpu_step()
+    st.block_tables = None                   # as __init__ leaves it
+    for call in (lambda: st.decode_window(8), st.decode_accumulate, lambda: st.evict(8, 2)):
+        with pytest.raises(L.PkvError) as e:
+            call()
+        assert e.value.status == L.PKV_ERR_INVALID_ARG
+    assert not kernels.calls and st.scores is None
