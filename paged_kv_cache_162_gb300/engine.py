@@ -539,7 +539,7 @@ class DecodeStep:
         self.prefix_groups = None
         self._evicted = False  # since plan(): rows own their blocks, tokens have moved
         self.scores = self.positions = self.token_counts = None  # of decode_accumulate
-        self._accumulate_ws, self._accumulate_bound = None, 0
+        self._scored = False   # since plan(): they hold weights
 
     def plan(self):
         """Host allocator: tables and copy-on-write pairs for this step.
@@ -567,11 +567,7 @@ class DecodeStep:
     def _forget_scores(self):
         """Ends what decode_accumulate and evict() have begun: a step planned
         anew has no scores, and its lengths are those of its tables."""
-        if self.scores is None:
-            return
-        if self.device.type == "cuda":
-            torch.cuda.synchronize(self.device)  # a kernel may still be in them
-        self.scores = self.positions = self.token_counts = None
+        self._scored = False
         if self._evicted:
             self._evicted = False
             self.context_lens_host = (self.ctx_before + self.n_new).astype(np.int32)
@@ -727,7 +723,7 @@ class DecodeStep:
         P, at = self._beam_native.step(par.ctypes.data, tq.data_ptr(), tk.data_ptr(), tv.data_ptr(),
                                        sh)
         self.last_native_seconds = time.perf_counter() - t0
-        if self.scores is not None:
+        if self._scored:
             with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
                 self._scores_follow(par)
         # the pairs sit in the staging buffer the step used
@@ -841,35 +837,34 @@ class DecodeStep:
 
     def decode_accumulate(self, stream=None):
         """decode() that also adds every token's attention weight to
-        self.scores ([S, H, MB * bs] fp32, made on the first call; see
-        paged_attention_decode_accumulate), which evict() goes by.  May be
-        captured in a graph after a first call outside it."""
+        self.scores ([S, H, MB * bs] fp32, zero before the first call after
+        plan(); see paged_attention_decode_accumulate), which evict() goes by.
+        May be captured in a graph after a first call outside it."""
         self._need_plan("decode_accumulate")
-        if self.scores is None or self.max_context_len > self._accumulate_bound:
+        if not self._scored:
             # captured, every replay would zero the scores
             _no_capture("the first decode_accumulate, which makes the scores,", stream, self.device)
             with _on(stream, self.device):
-                self._make_scores()
+                self._begin_scores()
         return paged_attention_decode_accumulate(
             self.out, self.scores, self.q, self.k_cache, self.v_cache, self.block_tables,
             self.context_lens, self.scale, self.max_context_len, self._accumulate_ws, stream)
 
-    def _make_scores(self):
-        """What decode_accumulate keeps, on the current stream: the rows of a
-        step that has none, and a workspace for the bound (a beam search
-        raises it)."""
+    def _begin_scores(self):
+        """No weights yet, on the current stream.  The tensors stay where they
+        are and the workspace is for the longest context that the tables
+        allow: a captured graph holds their addresses."""
+        rows = (self.S, self.H, self.MB * self.bs)
         if self.scores is None:
-            rows = (self.S, self.H, self.MB * self.bs)
             self.scores = torch.zeros(rows, device=self.device)
             self.positions = torch.full(rows, -1, dtype=torch.int32, device=self.device)
             self.token_counts = self.context_lens.clone()
-        if self.max_context_len > self._accumulate_bound:
-            old = self._accumulate_ws
-            self._accumulate_ws = new_accumulate_workspace(self.S, self.H, self.H, self.D,
-                                                           self.max_context_len, self.device)
-            self._accumulate_bound = self.max_context_len
-            if old is not None and old.is_cuda:  # the call before may still be in it
-                old.record_stream(torch.cuda.current_stream(self.device))
+            self._accumulate_ws = new_accumulate_workspace(self.S, self.H, self.H, self.D, rows[2], self.device)
+        else:
+            self.scores.zero_()
+            self.positions.fill_(-1)
+            self.token_counts.copy_(self.context_lens)
+        self._scored = True
 
     def evict(self, budget, recent_tokens, sink_tokens=0, stream=None):
         """After decode_accumulate: keeps `budget` tokens of every longer
@@ -888,7 +883,7 @@ class DecodeStep:
 
     def _evict(self, budget, recent_tokens, sink_tokens):
         """evict() on the current stream, temporary tensors and all."""
-        if self.scores is None:
+        if not self._scored:
             _refuse("evict: there are no scores to go by (decode_accumulate makes them)")
         if budget < 1 or recent_tokens < 0 or sink_tokens < 0 or recent_tokens + sink_tokens > budget:
             _refuse("evict: budget must be >= 1 and hold the sinks and the recent tokens")

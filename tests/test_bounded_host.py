@@ -41,6 +41,7 @@ class Streams:
         monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: FakeStream(handle))
         self.captured = ()                   # handles of streams that are being captured
         monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+        monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: None)
         monkeypatch.setattr(torch.cuda, "is_current_stream_capturing",
                             lambda: self.now.cuda_stream in self.captured)
         monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
@@ -426,7 +427,7 @@ def test_a_new_plan_starts_over(monkeypatch):
     st.decode_accumulate()
     first = st.scores.clone()
     st.plan()                                # no eviction yet
-    assert st.scores is None and np.array_equal(st.context_lens.numpy(), lens)
+    assert np.array_equal(st.context_lens.numpy(), lens)
     st.decode_accumulate()
     assert torch.equal(st.scores, first)
     held = st.context_lens
@@ -646,3 +647,26 @@ def test_a_step_without_a_plan_has_no_tables(monkeypatch):
             call()
         assert e.value.status == L.PKV_ERR_INVALID_ARG
     assert not kernels.calls and st.scores is None
+
+
+def test_a_captured_call_s_memory_stays(monkeypatch):
+    """A captured decode_accumulate holds the addresses of the scores and of
+    its workspace: neither a raised bound nor a new plan may free them."""
+    rng = np.random.default_rng(6)
+    Streams(monkeypatch)
+    FakeKernels(monkeypatch)
+    st = on_cpu(cpu_step(tail_lo=33, tail_hi=33, bs=32, D=128), monkeypatch)
+    st.decode_accumulate()
+    held = [x.data_ptr() for x in (st.scores, st.positions, st.token_counts, st._accumulate_ws)]
+    first = st.scores.clone()
+    b, _ = beam_tokens(st, rng)
+    st.beam_step(rng.integers(0, st.S, st.S), b[1], b[2], b[0])
+    st.decode_accumulate()
+    st.evict(96, 20, 4)
+    k, v = st.k_cache, st.v_cache
+    st.plan()
+    st.decode_accumulate()
+    assert held == [x.data_ptr() for x in (st.scores, st.positions, st.token_counts, st._accumulate_ws)]
+    assert (st.positions == -1).all() and torch.equal(st.token_counts, st.context_lens)
+    assert (st.scores[:, :, 193:] == 0).all() and torch.allclose(st.scores.sum(-1), first.sum(-1), atol=1e-4)
+    assert k is st.k_cache and v is st.v_cache
