@@ -139,7 +139,7 @@ def _native():
             from . import _tensor_bind as found
         except ImportError:  # not built, or for a torch with other symbols
             found = None
-        _bind = found if found and found.torch_version == torch.__version__ else _AskCtypes
+        _bind = found if getattr(found, "torch_version", None) == torch.__version__ else _AskCtypes
     return _bind
 
 

@@ -670,3 +670,11 @@ def test_a_captured_call_s_memory_stays(monkeypatch):
     assert (st.positions == -1).all() and torch.equal(st.token_counts, st.context_lens)
     assert (st.scores[:, :, 193:] == 0).all() and torch.allclose(st.scores.sum(-1), first.sum(-1), atol=1e-4)
     assert k is st.k_cache and v is st.v_cache
+
+
+def test_a_binding_that_names_no_torch_is_not_used(monkeypatch):
+    import paged_kv_cache_162_gb300 as P
+    monkeypatch.setattr(E, "_bind", None)
+    monkeypatch.setitem(__import__("sys").modules, "paged_kv_cache_162_gb300._tensor_bind", object())
+    monkeypatch.setattr(P, "_tensor_bind", object(), raising=False)
+    assert E._native().window() == -1
