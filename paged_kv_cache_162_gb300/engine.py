@@ -953,9 +953,9 @@ class StepGraph:
     fused: run the step through pkv_decode_step (DecodeStep.run).
     The step runs once eagerly before capture so that every per-device
     set-up of the library happens outside the capture.  replay() enqueues
-    the whole step on the capture stream with one launch.  It replays the step
-    as it was captured, prefix groups included: after DecodeStep.evict a step
-    with groups is captured anew.
+    the whole step on the capture stream with one launch, as it was captured:
+    block copies, writes and prefix groups included.  Like DecodeStep.run it is
+    refused after an eviction; a step planned anew is captured anew.
     """
 
     def __init__(self, step: DecodeStep, stream: torch.cuda.Stream, h2d=(), d2h=(), fused=False):
@@ -981,6 +981,8 @@ class StepGraph:
 
         One driver call: switching torch's current stream around
         CUDAGraph.replay() costs more host time per step than the launch."""
+        if self.step._evicted:
+            _refuse("replay: the step was written before an eviction moved it (plan it and capture it anew)")
         r = self._launch(self._exec, self._stream)
         if r != 0:
             raise L.PkvError(L.PKV_ERR_CUDA, f"cuGraphLaunch failed (CUresult {r})")

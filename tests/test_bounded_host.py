@@ -678,3 +678,19 @@ def test_a_binding_that_names_no_torch_is_not_used(monkeypatch):
     monkeypatch.setitem(__import__("sys").modules, "paged_kv_cache_162_gb300._tensor_bind", object())
     monkeypatch.setattr(P, "_tensor_bind", object(), raising=False)
     assert E._native().window() == -1
+
+
+def test_a_captured_step_is_not_replayed_after_an_eviction(monkeypatch):
+    """The graph holds the step's block copies and writes, like run()."""
+    FakeKernels(monkeypatch)
+    launched = []
+    graph = E.StepGraph.__new__(E.StepGraph)             # capturing needs a GPU
+    graph.step, graph._exec, graph._stream = cpu_step(), None, None
+    graph._launch = lambda *a: launched.append(a) or 0
+    graph.replay()
+    graph.step.decode_accumulate()
+    graph.replay()
+    graph.step.evict(96, 20, 4)
+    with pytest.raises(L.PkvError, match="capture it anew"):
+        graph.replay()
+    assert len(launched) == 2
