@@ -22,7 +22,8 @@
 // against 32 + 16 products of 16x8x16 per 8 KB tile.
 //   S = Q K^T, then the online softmax on the accumulators, then O += P V with
 //   P as the sum of two 16-bit numbers (its rounding and the rest): P rounded
-//   once would add an error as large as the output's own rounding.
+//   once would add an error as large as the output's own rounding.  In fp16 P is in
+//   units of 2^-15 (kWeightUnits).
 // A CTA is four warps: hw heads times 4 / hw token splits, joined in shared
 // memory.  The four read neighbouring data (4 D values of each token row, or four
 // tiles of one head); a range of its own per warp was slower (window of 64 MHA
@@ -44,13 +45,13 @@
 //    every sum has a fixed order.
 //
 // Measured on GB300 (device time, share of the measured copy rate of 6776 GB/s):
-//   window 1000 + 4 sinks, 64 requests of 128..2048, 32 heads, fp16   127 us  98 %
-//   window 4093 + 7, 96 requests, 32 heads on 8, bf16                 237 us 100 %
-//   accumulate, the 64 requests whole                                 183 us  93 %
-//   accumulate, 8 x 32768                                             655 us  98 %
-//   accumulate, 256 requests of 16..4096 (median 512), 32 heads on 8  155 us  82 %
+//   window 1000 + 4 sinks, 64 requests of 128..2048, 32 heads, fp16   129 us  97 %
+//   window 4093 + 7, 96 requests, 32 heads on 8, bf16                 240 us  99 %
+//   accumulate, the 64 requests whole                                 186 us  92 %
+//   accumulate, 8 x 32768                                             663 us  97 %
+//   accumulate, 256 requests of 16..4096 (median 512), 32 heads on 8  156 us  81 %
 //   window 4096 of one 32768-token context, 32 heads on 8            8.3 us  30 %
-//   4 requests of at most 100 tokens, 4 heads of 64       2.8 us, with scores 3.5
+//   4 requests of at most 100 tokens, 4 heads of 64       3.0 us, with scores 3.4
 // The split kernel moves each byte once (847.5 MB for 843.4) at 83 % of the DRAM
 // peak with its tensor pipe 26 % busy.  About 4 us go before every ring is full
 // (length -> place -> table -> rows), 3 to the last ranges; the second kernel takes
@@ -1318,7 +1319,7 @@ __device__ __forceinline__ void fold_stretch(const Params& p, int s, int kvh, in
 // CTA look at 256 of its share at once, list those that do, and its warps do
 // the listed ones in turn: 155 us for the 256 requests of 16..4096, where warps
 // with items of their own took 160.  Fewer tokens per fold, two or four CTAs per
-// SM: no faster.
+// SM: no faster (at three the score forms spill 4 to 28 bytes, at two nothing).
 //  join: a row of a unit that lies in several ranges, by a warp, or by the
 //        CTA's warps together (`wide`) where units have many pieces.
 //  fold: 256 tokens (512 with one query head) of a KV head, by a warp.

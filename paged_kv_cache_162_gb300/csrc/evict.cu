@@ -25,12 +25,13 @@
 // Bound by memory where tokens move: 8 bytes read and written per token, and
 // per move 2 x 256 bytes (D = 128) read and written, one head of one token row at
 // a time.  Measured on GB300 (device time, share of the copy rate of 6776 GB/s):
-//   256 requests of 16..4096 (median 512) to 500, 32 heads    218 us  84 %
-//   8 x 32768 to 4096, 32 heads                               211 us  77 %
+//   256 requests of 16..4096 (median 512) to 500, 32 heads    220 us  83 %
+//   8 x 32768 to 4096, 32 heads                               210 us  78 %
 //   64 requests of 2064 to 2048, 8 heads: 16 moves a row     10.4 us  36 %
 //   4 requests of 50..100 to 48, 4 heads of 64                4.9 us
 // The last two are the chain length -> keys -> histogram -> counts -> lists ->
-// rows, about a microsecond a link.  In the first, DRAM moves 1217 MB at 70 % of its
+// rows, about a microsecond a link; in the steady state two or three of its sweeps of
+// the row find nothing that the handful of keys in the first digit's bin do not say.  In the first, DRAM moves 1217 MB at 70 % of its
 // peak, reads and writes of 256 bytes in turn.
 #include <cooperative_groups.h>
 
