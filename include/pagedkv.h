@@ -281,8 +281,8 @@ size_t pkv_decode_window_workspace_size(int S, int H, int Hkv, int D);
  *   other arguments as in pkv_paged_attention_decode.
  * Computation is fp32; attention weights enter P.V as the sum of two 16-bit
  * numbers (relative error at most 2^-16 in bf16, in fp16 2^-22 or 2^-40 of the
- * row's largest weight); one rounding to dtype at the end.  A visible V element that is not finite makes its output elements
- * not finite. */
+ * row's largest weight); one rounding to dtype at the end.  A visible V
+ * element that is not finite makes its output elements not finite. */
 pkv_status pkv_paged_attention_decode_window(
     void* out, const void* q, const void* k_cache, const void* v_cache,
     const int32_t* block_tables, const int32_t* context_lens,

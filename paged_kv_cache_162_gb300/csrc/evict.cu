@@ -31,8 +31,9 @@
 //   4 requests of 50..100 to 48, 4 heads of 64                4.9 us
 // The last two are the chain length -> keys -> histogram -> counts -> lists ->
 // rows, about a microsecond a link; in the steady state two or three of its sweeps of
-// the row find nothing that the handful of keys in the first digit's bin do not say.  In the first, DRAM moves 1217 MB at 70 % of its
-// peak, reads and writes of 256 bytes in turn.
+// the row find nothing that the few keys in the first digit's bin do not say.  In the
+// first, DRAM moves 1217 MB at 70 % of its peak, reads and writes of 256 bytes in
+// turn.
 #include <cooperative_groups.h>
 
 #include <climits>
