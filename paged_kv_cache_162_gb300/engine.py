@@ -48,6 +48,21 @@ def new_workspace(S, H, D, max_context_len, partition_tokens=0, device="cuda") -
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _as_stream(stream, device):
+    """`stream`, a torch stream or a handle, as a torch stream."""
+    return torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+
+
+def _scratch(nbytes, device, stream=None) -> torch.Tensor:
+    """Memory for one call on `stream` (None: the current one), out of the
+    memory of that stream: what another stream has given back may still be in
+    use there, and what this call gives back is its stream's again."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(_as_stream(stream, device)):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale=None,
                            max_context_len=0, partition_tokens=0, workspace=None, stream=None):
     """out[s,h] = softmax(scale q[s,h] K^T) V over each sequence's paged context.
@@ -61,8 +76,10 @@ def paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens,
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if workspace is None:
-        workspace = new_workspace(S, H, D, max_context_len or MB * bs, partition_tokens,
-                                  q.device)
+        n = workspace_size(S, H, D, max_context_len or MB * bs, partition_tokens)
+        if n == 0:
+            raise L.PkvError(L.PKV_ERR_INVALID_ARG, "bad workspace arguments")
+        workspace = _scratch(n, q.device, stream)
     L.pkv_paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens, S, H, D, bs,
                                  NB, MB, max_context_len, scale, dtype_code(q.dtype),
                                  partition_tokens, workspace, workspace.numel(), stream)
@@ -88,7 +105,7 @@ def decode_step(out, q, key, value, k_cache, v_cache, block_tables, context_lens
         mc = max_context_len or MB * bs
         n = (L.pkv_decode_shared_prefix_workspace_size(S, H, D, G, mc, partition_tokens) if G
              else workspace_size(S, H, D, mc, partition_tokens))
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(n, q.device, stream)
     L.pkv_decode_step(out, q, key, value, k_cache, v_cache, block_tables, context_lens, seq_idx,
                       pos, slot_mapping, prefix_groups, G, T, S, H, D, bs, NB, MB,
                       max_context_len, scale, dtype_code(q.dtype), partition_tokens, workspace,
@@ -111,7 +128,7 @@ def paged_attention_decode_shared_prefix(out, q, k_cache, v_cache, block_tables,
     if workspace is None:
         mcl = max_context_len or MB * bs
         need = L.pkv_decode_shared_prefix_workspace_size(S, H, D, G, mcl, partition_tokens)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, q.device, stream)
     L.pkv_paged_attention_decode_shared_prefix(out, q, k_cache, v_cache, block_tables,
                                                context_lens, prefix_groups, G, S, H, D, bs, NB, MB,
                                                max_context_len, scale, dtype_code(q.dtype),
@@ -195,11 +212,6 @@ def _attention_sizes(who, out, q, k_cache, v_cache, block_tables, context_lens):
     return S, H, D, NB, bs, Hkv, tshape[1], dev
 
 
-def _as_stream(stream, device):
-    """`stream`, a torch stream or a handle, as a torch stream."""
-    return torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
-
-
 @contextlib.contextmanager
 def _on(stream, device):
     """Torch's work inside runs on `stream` (None: the current one), after
@@ -228,15 +240,10 @@ def _no_capture(who, stream, device):
 
 
 def _workspace(who, nbytes, device, stream=None):
-    """A workspace for one call on `stream` (None: the current one), out of
-    the memory of that stream: what another stream has given back may still
-    be in use there, and what this call gives back is its stream's again."""
+    """_scratch for a call of this section."""
     if nbytes == 0:
         _refuse(f"{who}: bad workspace arguments (H a multiple of Hkv, at most 16 per group?)")
-    if stream is None:
-        return torch.empty(nbytes, dtype=_U8, device=device)
-    with torch.cuda.stream(_as_stream(stream, device)):
-        return torch.empty(nbytes, dtype=_U8, device=device)
+    return _scratch(nbytes, device, stream)
 
 
 def _check_workspace(who, ws, dev):
@@ -815,7 +822,8 @@ class DecodeStep:
                 if (rows != rows[:1]).any() or (held < tokens).any():
                     _refuse("decode_shared_prefix: after evict() the sequences from "
                             f"{first} on no longer share {tokens} tokens")
-        g = torch.as_tensor(prefix_groups).to(self.device)
+        with _on(stream, self.device):  # the groups are read, and given back, on that stream
+            g = torch.as_tensor(prefix_groups).to(self.device)
         return paged_attention_decode_shared_prefix(
             self.out, self.q, self.k_cache, self.v_cache, self.block_tables, self.context_lens, g,
             self.scale, self.max_context_len, self.partition_tokens, stream=stream)

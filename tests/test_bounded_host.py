@@ -694,3 +694,26 @@ def test_a_captured_step_is_not_replayed_after_an_eviction(monkeypatch):
     with pytest.raises(L.PkvError, match="capture it anew"):
         graph.replay()
     assert len(launched) == 2
+
+
+def test_the_other_calls_scratch_is_their_stream_s_too(monkeypatch):
+    """Decode, the fused step and the shared-prefix decode without a workspace, and DecodeStep's groups."""
+    st = cpu_step()
+    streams = Streams(monkeypatch)
+    launched = []
+    for name in ("pkv_paged_attention_decode", "pkv_decode_step", "pkv_paged_attention_decode_shared_prefix"):
+        monkeypatch.setattr(E.L, name, lambda *a, name=name: launched.append((name, a[-1])))
+    side = FakeStream(5)
+    a = (st.out, st.q, st.k_cache, st.v_cache, st.block_tables, st.context_lens)
+    g = torch.tensor([[0, 3, 160]], dtype=torch.int32)
+    E.paged_attention_decode(*a, stream=side)
+    E.decode_step(*a[:2], st.new_k, st.new_v, *a[2:], st.seq_idx, st.pos, st.slot_mapping, stream=side)
+    E.decode_step(*a[:2], st.new_k, st.new_v, *a[2:], st.seq_idx, st.pos, st.slot_mapping, g, stream=side)
+    E.paged_attention_decode_shared_prefix(*a, g, stream=side)
+    assert streams.made == [("empty", 5)] * 4 and [s for _, s in launched] == [side] * 4
+    streams.made.clear()
+    st.decode_shared_prefix([[0, 3, 160]], stream=side)
+    assert streams.made == [("to", 5), ("empty", 5)] and side.waited == [0] and streams.now.waited == [5]
+    streams.made.clear()
+    E.paged_attention_decode(*a)
+    assert streams.made == [("empty", 0)]
