@@ -79,7 +79,7 @@ def paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens,
         n = workspace_size(S, H, D, max_context_len or MB * bs, partition_tokens)
         if n == 0:
             raise L.PkvError(L.PKV_ERR_INVALID_ARG, "bad workspace arguments")
-        workspace = _scratch(n, q.device, stream)
+        workspace = _scratch(n, k_cache.device, stream)
     L.pkv_paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens, S, H, D, bs,
                                  NB, MB, max_context_len, scale, dtype_code(q.dtype),
                                  partition_tokens, workspace, workspace.numel(), stream)
@@ -105,7 +105,7 @@ def decode_step(out, q, key, value, k_cache, v_cache, block_tables, context_lens
         mc = max_context_len or MB * bs
         n = (L.pkv_decode_shared_prefix_workspace_size(S, H, D, G, mc, partition_tokens) if G
              else workspace_size(S, H, D, mc, partition_tokens))
-        workspace = _scratch(n, q.device, stream)
+        workspace = _scratch(n, k_cache.device, stream)
     L.pkv_decode_step(out, q, key, value, k_cache, v_cache, block_tables, context_lens, seq_idx,
                       pos, slot_mapping, prefix_groups, G, T, S, H, D, bs, NB, MB,
                       max_context_len, scale, dtype_code(q.dtype), partition_tokens, workspace,
@@ -128,7 +128,7 @@ def paged_attention_decode_shared_prefix(out, q, k_cache, v_cache, block_tables,
     if workspace is None:
         mcl = max_context_len or MB * bs
         need = L.pkv_decode_shared_prefix_workspace_size(S, H, D, G, mcl, partition_tokens)
-        workspace = _scratch(need, q.device, stream)
+        workspace = _scratch(need, k_cache.device, stream)
     L.pkv_paged_attention_decode_shared_prefix(out, q, k_cache, v_cache, block_tables,
                                                context_lens, prefix_groups, G, S, H, D, bs, NB, MB,
                                                max_context_len, scale, dtype_code(q.dtype),

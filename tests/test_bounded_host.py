@@ -717,3 +717,19 @@ def test_the_other_calls_scratch_is_their_stream_s_too(monkeypatch):
     streams.made.clear()
     E.paged_attention_decode(*a)
     assert streams.made == [("empty", 0)]
+
+
+def test_scratch_is_where_the_caches_are(monkeypatch):
+    """Queries may be in pinned host memory; the kernels' scratch may not."""
+    st = cpu_step()
+    made = []
+    monkeypatch.setattr(E, "_scratch", lambda n, device, stream=None: made.append(device) or torch.empty(1))
+    for name in ("pkv_paged_attention_decode", "pkv_decode_step", "pkv_paged_attention_decode_shared_prefix"):
+        monkeypatch.setattr(E.L, name, lambda *a: None)
+    k = st.k_cache.to("meta")                # stands for another device than the queries'
+    a = (st.out, st.q, k, k, st.block_tables, st.context_lens)
+    g = torch.tensor([[0, 3, 160]], dtype=torch.int32)
+    E.paged_attention_decode(*a)
+    E.decode_step(*a[:2], st.new_k, st.new_v, *a[2:], st.seq_idx, st.pos, st.slot_mapping)
+    E.paged_attention_decode_shared_prefix(*a, g)
+    assert made == [torch.device("meta")] * 3
