@@ -367,6 +367,113 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
                             void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------ *
+ * Appending with the position rotation, and the cache held in 4 bits
+ *
+ * The keys of a rotary model are cached rotated.  These calls rotate a step's
+ * queries and keys on the way and write K and V into their slots: into the
+ * 16-bit caches, or into a cache that holds 4 bits per element.  Grouped
+ * heads as in the section above.  Not on the pages.
+ *
+ * The 4-bit cache: K and V pools of uint8 [NB][Hkv][bs][RB], RB =
+ * pkv_cache_q4_row_bytes(D) = D/2 + D/16.  A row's elements go in groups of
+ * 64; element i of a group reads as centre + step * (code - 8), code 0..15:
+ *   step = (max - min) / 15, centre = (8 max + 7 min) / 15 of the group, each
+ *   rounded once to dtype; code = round((x - centre) / step) + 8 within 0..15
+ *   (halves to even), 8 where step is 0 (or, in bf16, below 2^-126: then 0 is
+ *   stored).
+ * An element is off by at most step / 2 and what rounding step and centre
+ * moves the ends: 8 u |step| + u |centre|, u = 2^-11 (fp16), 2^-8 (bf16).  A
+ * group with an element that is not finite reads as NaN.  (An fp16 K whose
+ * rotation passes 65504 may make a centre, and its group, infinite.)
+ * Order of a (block, head) in memory: for every 8 tokens their 8 rows of D/2
+ * code bytes (byte j: elements 2j, in the low nibble, and 2j + 1; the 16-byte
+ * chunk c of row r at place c ^ (r/2)%4 for D = 128, c ^ (r/4)%2 for D = 64),
+ * then their 8 rows of D/64 pairs (step, centre).  The pools are 16-byte
+ * aligned; a pool is read with the dtype it was written with.
+ * ------------------------------------------------------------------ */
+
+/* RB: bytes per (token, KV head) of a 4-bit K (or V) pool; 0 for a D that is
+ * not 64 or 128. */
+size_t pkv_cache_q4_row_bytes(int D);
+
+/* Writes T new tokens.  Token t belongs at position pos[t] of sequence
+ * seq_idx[t]; its slot is found as by pkv_compute_slot_mapping and written to
+ * slot_mapping[t].  Its rotary position is rotary_pos[t] (NULL: pos[t]; after
+ * an eviction a token's place lies below its position).  With (cos_i, sin_i)
+ * of that row of the table, every query and K row's first rotary_dim = R dims
+ * become
+ *   (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i),  i < R/2,
+ *   (a, b) = dims (i, i + R/2), or (2i, 2i + 1) when `interleaved`;
+ * products and sums in fp32, each rounded, and one rounding to dtype (K of the
+ * 4-bit form: none before it is quantised).  V is not rotated.
+ * A token with pos[t] < 0 is padding: slot -1, nothing else is written for it.
+ * The same where the slot is not to be found or is out of range (the bits of
+ * pkv_compute_slot_mapping and pkv_reshape_and_cache), or the rotary position
+ * outside [0, table_rows) (slot -1, PKV_DEVERR_POSITION).  Slots must be
+ * distinct within a call.
+ *   key, value   [T][Hkv][D] dtype, rows of a token contiguous, tokens
+ *                key_stride / value_stride elements apart (multiples of 8,
+ *                below 2^30): slices of one projection need no copy
+ *   query, query_out  [T][H][D] with strides of their own; H = 0: no queries,
+ *                both NULL.  query_out may be query (with its stride); else it
+ *                overlaps neither query nor key nor value
+ *   rotary_table [table_rows][R] fp32: R/2 cosines, then R/2 sines; NULL when
+ *                R = 0 (no rotation)
+ *   rotary_dim   R: a multiple of 16, at most D
+ *   slot_mapping [T] int64, written */
+pkv_status pkv_rotate_and_cache(
+    const void* key, int64_t key_stride, const void* value, int64_t value_stride,
+    const void* query, int64_t query_stride, void* query_out, int64_t query_out_stride,
+    void* k_cache, void* v_cache, const int32_t* block_tables, const int32_t* seq_idx,
+    const int32_t* pos, const int32_t* rotary_pos, const float* rotary_table, int table_rows,
+    int rotary_dim, int interleaved, int64_t* slot_mapping, int T, int S, int H, int Hkv, int D,
+    int bs, int NB, int MB, pkv_dtype dtype, void* stream);
+
+/* The same into 4-bit caches. */
+pkv_status pkv_rotate_and_cache_q4(
+    const void* key, int64_t key_stride, const void* value, int64_t value_stride,
+    const void* query, int64_t query_stride, void* query_out, int64_t query_out_stride,
+    void* k_cache, void* v_cache, const int32_t* block_tables, const int32_t* seq_idx,
+    const int32_t* pos, const int32_t* rotary_pos, const float* rotary_table, int table_rows,
+    int rotary_dim, int interleaved, int64_t* slot_mapping, int T, int S, int H, int Hkv, int D,
+    int bs, int NB, int MB, pkv_dtype dtype, void* stream);
+
+/* Reads the K and V rows of T slots of 4-bit caches, as the 16-bit values that
+ * they stand for: the cached prefix of a prompt's next chunk, a sequence on its
+ * way into a 16-bit cache.  Rows of negative slots are left as they were; a slot
+ * of NB*bs or more too, with PKV_DEVERR_SLOT.  A slot may be read twice.
+ *   key, value  [T][Hkv][D] dtype, written, not overlapping; strides as in
+ *               pkv_rotate_and_cache
+ *   slot_mapping  [T] int64 */
+pkv_status pkv_gather_cache_q4(void* key, int64_t key_stride, void* value, int64_t value_stride,
+                               const void* k_cache, const void* v_cache,
+                               const int64_t* slot_mapping, int T, int Hkv, int D, int bs, int NB,
+                               pkv_dtype dtype, void* stream);
+
+/* Bytes of workspace for pkv_paged_attention_decode_q4 (0 for invalid
+ * arguments); it does not depend on the context lengths. */
+size_t pkv_decode_q4_workspace_size(int S, int H, int Hkv, int D);
+
+/* Single-query decode attention over 4-bit caches: what
+ * pkv_paged_attention_decode computes, with grouped heads, from the values
+ * that the caches stand for.  Arguments, limits and the promises about capture,
+ * equal bits and bounded waits as in pkv_paged_attention_decode_window, whose
+ * window it has not; the workspace needs pkv_decode_q4_workspace_size bytes. */
+pkv_status pkv_paged_attention_decode_q4(
+    void* out, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens,
+    int S, int H, int Hkv, int D, int bs, int NB, int MB, int max_context_len, float scale,
+    pkv_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* pkv_copy_blocks and pkv_swap_blocks for 4-bit caches: the same calls on
+ * blocks of Hkv * bs * RB bytes. */
+pkv_status pkv_copy_blocks_q4(void* k_cache, void* v_cache, const int64_t* block_mapping, int P,
+                              int Hkv, int D, int bs, int NB, void* stream);
+pkv_status pkv_swap_blocks_q4(void* gpu_k, void* gpu_v, void* host_k, void* host_v,
+                              const int64_t* block_mapping, int P, int Hkv, int D, int bs,
+                              int NB_gpu, int NB_host, int direction, void* stream);
+
+/* ------------------------------------------------------------------ *
  * Cache maintenance kernels
  * ------------------------------------------------------------------ */
 

@@ -29,7 +29,7 @@ LIB = os.path.join(PKG, "libpagedkv.so")
 BIND = os.path.join(PKG, "_tensor_bind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-CU_SOURCES = ["runtime.cu", "cache_ops.cu", "decode.cu", "bounded.cu", "evict.cu"]
+CU_SOURCES = ["runtime.cu", "cache_ops.cu", "decode.cu", "bounded.cu", "evict.cu", "rotary.cu", "q4_decode.cu"]
 CXX_SOURCES = ["allocator.cpp", "beam_step.cpp"]
 BIND_SOURCE = "tensor_bind.cpp"
 

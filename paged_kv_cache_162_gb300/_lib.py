@@ -80,6 +80,17 @@ SIGNATURES = {
     "pkv_evict_workspace_size": (_SZ, [_I, _I, _I]),
     "pkv_evict_tokens": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
                               _I64, _I, _I, _I, _I, _P, _SZ, _P]),
+    "pkv_cache_q4_row_bytes": (_SZ, [_I]),
+    "pkv_rotate_and_cache": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I,
+                                  _I, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "pkv_rotate_and_cache_q4": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P,
+                                     _I, _I, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "pkv_gather_cache_q4": (_I, [_P, _I64, _P, _I64, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "pkv_decode_q4_workspace_size": (_SZ, [_I, _I, _I, _I]),
+    "pkv_paged_attention_decode_q4": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I,
+                                           _P, _SZ, _P]),
+    "pkv_copy_blocks_q4": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "pkv_swap_blocks_q4": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "pkv_compute_slot_mapping": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P]),
     "pkv_reshape_and_cache": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "pkv_copy_blocks": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
@@ -304,6 +315,67 @@ def pkv_evict_tokens(k_cache, v_cache, scores, positions, block_tables, context_
         stream_handle(stream))
     if st:
         check(st, "evict_tokens")
+
+
+def pkv_cache_q4_row_bytes(D) -> int:
+    return int(lib().pkv_cache_q4_row_bytes(int32(D, "D")))
+
+
+def _rotate_and_cache(name, key, key_stride, value, value_stride, query, query_stride, query_out, query_out_stride,
+                      k_cache, v_cache, block_tables, seq_idx, pos, rotary_pos, rotary_table, table_rows, rotary_dim,
+                      interleaved, slot_mapping, T, S, H, Hkv, D, bs, NB, MB, dtype, stream=None) -> None:
+    st = getattr(lib(), name)(
+        ptr(key), key_stride, ptr(value), value_stride, ptr(query), query_stride, ptr(query_out), query_out_stride,
+        ptr(k_cache), ptr(v_cache), ptr(block_tables), ptr(seq_idx), ptr(pos), ptr(rotary_pos), ptr(rotary_table),
+        table_rows, rotary_dim, int(interleaved), ptr(slot_mapping), T, S, H, Hkv, D, bs, NB, MB, int(dtype),
+        stream_handle(stream))
+    if st:
+        check(st, name[4:])
+
+
+def pkv_rotate_and_cache(*args, stream=None) -> None:
+    """The arguments of pkv_rotate_and_cache, in its order."""
+    _rotate_and_cache("pkv_rotate_and_cache", *args, stream=stream)
+
+
+def pkv_rotate_and_cache_q4(*args, stream=None) -> None:
+    """The same into 4-bit caches."""
+    _rotate_and_cache("pkv_rotate_and_cache_q4", *args, stream=stream)
+
+
+def pkv_gather_cache_q4(key, key_stride, value, value_stride, k_cache, v_cache, slot_mapping, T, Hkv, D, bs, NB,
+                        dtype, stream=None) -> None:
+    st = lib().pkv_gather_cache_q4(ptr(key), key_stride, ptr(value), value_stride, ptr(k_cache), ptr(v_cache),
+                                   ptr(slot_mapping), T, Hkv, D, bs, NB, int(dtype), stream_handle(stream))
+    if st:
+        check(st, "gather_cache_q4")
+
+
+def pkv_decode_q4_workspace_size(S, H, Hkv, D) -> int:
+    if not _int32s(S, H, Hkv, D):
+        return 0
+    return int(lib().pkv_decode_q4_workspace_size(S, H, Hkv, D))
+
+
+def pkv_paged_attention_decode_q4(out, q, k_cache, v_cache, block_tables, context_lens, S, H, Hkv, D, bs, NB, MB,
+                                  max_context_len, scale, dtype, workspace, workspace_bytes, stream=None) -> None:
+    st = lib().pkv_paged_attention_decode_q4(
+        ptr(out), ptr(q), ptr(k_cache), ptr(v_cache), ptr(block_tables), ptr(context_lens), S, H, Hkv, D, bs, NB, MB,
+        int32(max_context_len, "max_context_len"), scale, int(dtype), ptr(workspace), workspace_bytes,
+        stream_handle(stream))
+    if st:
+        check(st, "paged_attention_decode_q4")
+
+
+def pkv_copy_blocks_q4(k_cache, v_cache, block_mapping, P, Hkv, D, bs, NB, stream=None) -> None:
+    check(lib().pkv_copy_blocks_q4(ptr(k_cache), ptr(v_cache), ptr(block_mapping), P, Hkv, D, bs, NB,
+                                   stream_handle(stream)), "copy_blocks_q4")
+
+
+def pkv_swap_blocks_q4(gpu_k, gpu_v, host_k, host_v, block_mapping, P, Hkv, D, bs, NB_gpu, NB_host, direction,
+                       stream=None) -> None:
+    check(lib().pkv_swap_blocks_q4(ptr(gpu_k), ptr(gpu_v), ptr(host_k), ptr(host_v), ptr(block_mapping), P, Hkv, D,
+                                   bs, NB_gpu, NB_host, int(direction), stream_handle(stream)), "swap_blocks_q4")
 
 
 def pkv_compute_slot_mapping(slot_mapping, block_tables, seq_idx, pos, T, S, MB, bs,

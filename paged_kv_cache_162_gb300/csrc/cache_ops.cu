@@ -12,6 +12,7 @@
 // 16-byte loads and stores.
 #include "pagedkv.h"
 #include "pkv_device.cuh"
+#include "q4.cuh"
 
 namespace {
 
@@ -120,6 +121,51 @@ cudaError_t launch_pdl(void (*fn)(KArgs...), dim3 grid, int threads, cudaStream_
     return cudaLaunchKernelEx(&cfg, fn, static_cast<KArgs>(args)...);
 }
 
+// 16-byte vectors of a block of a 4-bit K (or V) cache; its units of 8 tokens
+// are multiples of 16 bytes.
+int64_t vecs_per_block_q4(int Hkv, int D, int bs) { return (int64_t)Hkv * bs * pkv::q4::row_bytes(D) / 16; }
+
+// The copies of pkv_copy_blocks, of blocks of vec_per_block 16-byte vectors.
+pkv_status copy_blocks(void* k_cache, void* v_cache, const int64_t* block_mapping, int P, int64_t vec_per_block,
+                       int NB, void* stream) {
+    if (P == 0) return PKV_OK;
+    if (!k_cache || !v_cache || !block_mapping)
+        return pkv::fail(PKV_ERR_INVALID_ARG, "copy_blocks: null pointer");
+    if (!pkv::aligned16(k_cache) || !pkv::aligned16(v_cache))
+        return pkv::fail(PKV_ERR_INVALID_ARG, "copy_blocks: pointers must be 16-byte aligned");
+    if (P > 65535 * 64) return pkv::fail(PKV_ERR_INVALID_ARG, "copy_blocks: too many pairs");
+    dim3 grid(P, copy_splits(vec_per_block));
+    cudaError_t e = launch_pdl(copy_blocks_kernel, grid, 256, pkv::as_stream(stream),
+                               static_cast<uint4*>(k_cache), static_cast<uint4*>(v_cache),
+                               static_cast<const uint4*>(k_cache), static_cast<const uint4*>(v_cache),
+                               block_mapping, vec_per_block, NB, NB, pkv::device_error_word());
+    return e == cudaSuccess ? PKV_OK : pkv::cuda_fail(e, "copy_blocks launch");
+}
+
+// And of pkv_swap_blocks.
+pkv_status swap_blocks(void* gpu_k, void* gpu_v, void* host_k, void* host_v, const int64_t* block_mapping, int P,
+                       int64_t vec_per_block, int NB_gpu, int NB_host, int direction, void* stream) {
+    if (P == 0) return PKV_OK;
+    if (P > 65535 * 64) return pkv::fail(PKV_ERR_INVALID_ARG, "swap_blocks: too many pairs");
+    if (!gpu_k || !gpu_v || !host_k || !host_v || !block_mapping)
+        return pkv::fail(PKV_ERR_INVALID_ARG, "swap_blocks: null pointer");
+    if (!pkv::aligned16(gpu_k) || !pkv::aligned16(gpu_v) || !pkv::aligned16(host_k) || !pkv::aligned16(host_v))
+        return pkv::fail(PKV_ERR_INVALID_ARG, "swap_blocks: pointers must be 16-byte aligned");
+    void* dk = device_view_of_host(host_k);
+    void* dv = device_view_of_host(host_v);
+    if (!dk || !dv)
+        return pkv::fail(PKV_ERR_INVALID_ARG, "swap_blocks: host caches must be page-locked host memory the device can address");
+    dim3 grid(P, copy_splits(vec_per_block));
+    uint4 *gk = static_cast<uint4*>(gpu_k), *gv = static_cast<uint4*>(gpu_v);
+    uint4 *hk = static_cast<uint4*>(dk), *hv = static_cast<uint4*>(dv);
+    const bool out = direction == PKV_SWAP_OUT;
+    cudaError_t e = launch_pdl(copy_blocks_kernel, grid, 256, pkv::as_stream(stream),
+                               out ? hk : gk, out ? hv : gv, out ? gk : hk, out ? gv : hv,
+                               block_mapping, vec_per_block, out ? NB_gpu : NB_host,
+                               out ? NB_host : NB_gpu, pkv::device_error_word());
+    return e == cudaSuccess ? PKV_OK : pkv::cuda_fail(e, "swap_blocks launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -171,19 +217,17 @@ pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const int64_t* block_ma
     if (P < 0 || H <= 0 || NB < 0 || (dtype != PKV_F16 && dtype != PKV_BF16))
         return pkv::fail(PKV_ERR_INVALID_ARG, "copy_blocks: bad size or dtype");
     if (!supported(D, bs)) return pkv::fail(PKV_ERR_UNSUPPORTED, "copy_blocks: unsupported head_dim/block_size");
-    if (P == 0) return PKV_OK;
-    if (!k_cache || !v_cache || !block_mapping)
-        return pkv::fail(PKV_ERR_INVALID_ARG, "copy_blocks: null pointer");
-    if (!pkv::aligned16(k_cache) || !pkv::aligned16(v_cache))
-        return pkv::fail(PKV_ERR_INVALID_ARG, "copy_blocks: pointers must be 16-byte aligned");
-    if (P > 65535 * 64) return pkv::fail(PKV_ERR_INVALID_ARG, "copy_blocks: too many pairs");
-    const int64_t vec_per_block = (int64_t)bs * H * D / 8;
-    dim3 grid(P, copy_splits(vec_per_block));
-    cudaError_t e = launch_pdl(copy_blocks_kernel, grid, 256, pkv::as_stream(stream),
-                               static_cast<uint4*>(k_cache), static_cast<uint4*>(v_cache),
-                               static_cast<const uint4*>(k_cache), static_cast<const uint4*>(v_cache),
-                               block_mapping, vec_per_block, NB, NB, pkv::device_error_word());
-    return e == cudaSuccess ? PKV_OK : pkv::cuda_fail(e, "copy_blocks launch");
+    return copy_blocks(k_cache, v_cache, block_mapping, P, (int64_t)bs * H * D / 8, NB, stream);
+}
+
+pkv_status pkv_copy_blocks_q4(void* k_cache, void* v_cache, const int64_t* block_mapping, int P,
+                              int Hkv, int D, int bs, int NB, void* stream) {
+    PKV_TRACE("pkv_copy_blocks_q4");
+    pkv::clear_error();
+    if (P < 0 || Hkv <= 0 || NB < 0)
+        return pkv::fail(PKV_ERR_INVALID_ARG, "copy_blocks_q4: bad size");
+    if (!supported(D, bs)) return pkv::fail(PKV_ERR_UNSUPPORTED, "copy_blocks_q4: unsupported head_dim/block_size");
+    return copy_blocks(k_cache, v_cache, block_mapping, P, vecs_per_block_q4(Hkv, D, bs), NB, stream);
 }
 
 pkv_status pkv_swap_blocks(void* gpu_k, void* gpu_v, void* host_k, void* host_v,
@@ -195,26 +239,20 @@ pkv_status pkv_swap_blocks(void* gpu_k, void* gpu_v, void* host_k, void* host_v,
         (direction != PKV_SWAP_OUT && direction != PKV_SWAP_IN))
         return pkv::fail(PKV_ERR_INVALID_ARG, "swap_blocks: bad size, dtype or direction");
     if (!supported(D, bs)) return pkv::fail(PKV_ERR_UNSUPPORTED, "swap_blocks: unsupported head_dim/block_size");
-    if (P == 0) return PKV_OK;
-    if (P > 65535 * 64) return pkv::fail(PKV_ERR_INVALID_ARG, "swap_blocks: too many pairs");
-    if (!gpu_k || !gpu_v || !host_k || !host_v || !block_mapping)
-        return pkv::fail(PKV_ERR_INVALID_ARG, "swap_blocks: null pointer");
-    if (!pkv::aligned16(gpu_k) || !pkv::aligned16(gpu_v) || !pkv::aligned16(host_k) || !pkv::aligned16(host_v))
-        return pkv::fail(PKV_ERR_INVALID_ARG, "swap_blocks: pointers must be 16-byte aligned");
-    void* dk = device_view_of_host(host_k);
-    void* dv = device_view_of_host(host_v);
-    if (!dk || !dv)
-        return pkv::fail(PKV_ERR_INVALID_ARG, "swap_blocks: host caches must be page-locked host memory the device can address");
-    const int64_t vec_per_block = (int64_t)bs * H * D / 8;
-    dim3 grid(P, copy_splits(vec_per_block));
-    uint4 *gk = static_cast<uint4*>(gpu_k), *gv = static_cast<uint4*>(gpu_v);
-    uint4 *hk = static_cast<uint4*>(dk), *hv = static_cast<uint4*>(dv);
-    const bool out = direction == PKV_SWAP_OUT;
-    cudaError_t e = launch_pdl(copy_blocks_kernel, grid, 256, pkv::as_stream(stream),
-                               out ? hk : gk, out ? hv : gv, out ? gk : hk, out ? gv : hv,
-                               block_mapping, vec_per_block, out ? NB_gpu : NB_host,
-                               out ? NB_host : NB_gpu, pkv::device_error_word());
-    return e == cudaSuccess ? PKV_OK : pkv::cuda_fail(e, "swap_blocks launch");
+    return swap_blocks(gpu_k, gpu_v, host_k, host_v, block_mapping, P, (int64_t)bs * H * D / 8, NB_gpu,
+                       NB_host, direction, stream);
+}
+
+pkv_status pkv_swap_blocks_q4(void* gpu_k, void* gpu_v, void* host_k, void* host_v,
+                              const int64_t* block_mapping, int P, int Hkv, int D, int bs,
+                              int NB_gpu, int NB_host, int direction, void* stream) {
+    PKV_TRACE("pkv_swap_blocks_q4");
+    pkv::clear_error();
+    if (P < 0 || Hkv <= 0 || NB_gpu < 0 || NB_host < 0 || (direction != PKV_SWAP_OUT && direction != PKV_SWAP_IN))
+        return pkv::fail(PKV_ERR_INVALID_ARG, "swap_blocks_q4: bad size or direction");
+    if (!supported(D, bs)) return pkv::fail(PKV_ERR_UNSUPPORTED, "swap_blocks_q4: unsupported head_dim/block_size");
+    return swap_blocks(gpu_k, gpu_v, host_k, host_v, block_mapping, P, vecs_per_block_q4(Hkv, D, bs), NB_gpu,
+                       NB_host, direction, stream);
 }
 
 }  // extern "C"

@@ -192,6 +192,148 @@ PyObject* evict(PyObject*, PyObject* const* args, Py_ssize_t n) {
         budget, recent, sinks, code(c.type), ws->data_ptr(), (size_t)ws->numel(), stream));
 }
 
+// rows of tokens [T, heads, D] of type t, each token's contiguous; the
+// elements from one token to the next
+const at::Tensor* token_rows(Args& a, int i, at::ScalarType t, int64_t T, int64_t heads, int64_t D, int64_t* stride) {
+    const at::Tensor* x = a.ok ? tensor(a.v[i]) : nullptr;
+    if (!x || !x->is_cuda() || x->scalar_type() != t || x->dim() != 3 || x->size(0) != T ||
+        (heads >= 0 && x->size(1) != heads) || x->size(2) != D || x->numel() == 0 || x->stride(2) != 1 ||
+        (x->size(1) > 1 && x->stride(1) != D) || !small(*x) || x->get_device() != a.dev) {
+        a.ok = false;
+        return nullptr;
+    }
+    *stride = T > 1 ? x->stride(0) : x->size(1) * D;
+    return x;
+}
+
+// 4-bit caches [NB, Hkv, bs, RB] of head_dim D, arguments ik and iv.
+struct Caches4 {
+    const at::Tensor *k, *v;
+    int NB, Hkv, bs;
+    bool take(Args& a, int ik, int iv, int64_t D) {
+        k = a.take(ik, at::kByte, 4);
+        v = a.take(iv, at::kByte, 4);
+        if (!a.ok || v->sizes() != k->sizes() || !small(*k) || D < 0 || D > 128 ||
+            (size_t)k->size(3) != pkv_cache_q4_row_bytes((int)D))
+            return a.ok = false;
+        NB = (int)k->size(0);
+        Hkv = (int)k->size(1);
+        bs = (int)k->size(2);
+        return true;
+    }
+};
+
+// The 16-bit type, the first extent and the head_dim of o, a tensor of three dims.
+bool rows_like(PyObject* o, at::ScalarType* type, int64_t* T, int64_t* D) {
+    const at::Tensor* x = tensor(o);
+    if (!x || x->dim() != 3 || (x->scalar_type() != at::kHalf && x->scalar_type() != at::kBFloat16)) return false;
+    *type = x->scalar_type();
+    *T = x->size(0);
+    *D = x->size(2);
+    return true;
+}
+
+// rotate(q4, key, value, k_cache, v_cache, block_tables, seq_idx, pos,
+//        slot_mapping, rotary_table, query, query_out, rotary_pos, interleaved)
+PyObject* rotate(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    at::ScalarType type;
+    int64_t T, D;
+    if (n != 14 || !PyBool_Check(args[0]) || !PyBool_Check(args[13]) || !rows_like(args[1], &type, &T, &D))
+        return answer(kAskPython);
+    Args a{args};
+    const bool q4 = args[0] == Py_True;
+    int NB, bs, Hkv;
+    const at::Tensor *k, *v;
+    if (q4) {
+        Caches4 c;
+        if (!c.take(a, 3, 4, D)) return answer(kAskPython);
+        k = c.k, v = c.v, NB = c.NB, bs = c.bs, Hkv = c.Hkv;
+    } else {
+        k = a.take(3, type, 4);
+        v = a.take(4, type, 4);
+        if (!a.ok || v->sizes() != k->sizes() || !small(*k) || k->size(3) != D) return answer(kAskPython);
+        NB = (int)k->size(0);
+        bs = (int)k->size(1);
+        Hkv = (int)k->size(2);
+    }
+    int64_t ks = 0, vs = 0, qs = 0, qos = 0;
+    const at::Tensor* key = token_rows(a, 1, type, T, Hkv, D, &ks);
+    const at::Tensor* value = token_rows(a, 2, type, T, Hkv, D, &vs);
+    const at::Tensor* tables = a.take(5, at::kInt, 2);
+    const at::Tensor* seq = a.take(6, at::kInt, 1);
+    const at::Tensor* pos = a.take(7, at::kInt, 1);
+    const at::Tensor* slots = a.take(8, at::kLong, 1);
+    const at::Tensor* table = args[9] == Py_None ? nullptr : a.take(9, at::kFloat, 2);
+    const at::Tensor* turn = args[12] == Py_None ? nullptr : a.take(12, at::kInt, 1);
+    const at::Tensor *query = nullptr, *query_out = nullptr;
+    if (args[10] != Py_None) {
+        query = token_rows(a, 10, type, T, -1, D, &qs);
+        query_out = token_rows(a, 11, type, T, query ? query->size(1) : 0, D, &qos);
+    } else if (args[11] != Py_None) {
+        return answer(kAskPython);
+    }
+    void* stream = a.stream();
+    if (!a.ok || seq->size(0) != T || pos->size(0) != T || slots->size(0) != T || (turn && turn->size(0) != T) ||
+        !small(*tables) || (table && !small(*table)))
+        return answer(kAskPython);
+    auto call = q4 ? pkv_rotate_and_cache_q4 : pkv_rotate_and_cache;
+    return answer(call(
+        key->data_ptr(), ks, value->data_ptr(), vs, query ? query->data_ptr() : nullptr, qs,
+        query_out ? query_out->data_ptr() : nullptr, qos, k->data_ptr(), v->data_ptr(),
+        static_cast<const int32_t*>(tables->data_ptr()), static_cast<const int32_t*>(seq->data_ptr()),
+        static_cast<const int32_t*>(pos->data_ptr()),
+        turn ? static_cast<const int32_t*>(turn->data_ptr()) : nullptr,
+        table ? static_cast<const float*>(table->data_ptr()) : nullptr, table ? (int)table->size(0) : 0,
+        table ? (int)table->size(1) : 0, args[13] == Py_True, static_cast<int64_t*>(slots->data_ptr()), (int)T,
+        (int)tables->size(0), query ? (int)query->size(1) : 0, Hkv, (int)D, bs, NB, (int)tables->size(1), code(type),
+        stream));
+}
+
+// gather(key, value, k_cache, v_cache, slot_mapping)
+PyObject* gather(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    at::ScalarType type;
+    int64_t T, D, ks = 0, vs = 0;
+    if (n != 5 || !rows_like(args[0], &type, &T, &D)) return answer(kAskPython);
+    Args a{args};
+    Caches4 c;
+    if (!c.take(a, 2, 3, D)) return answer(kAskPython);
+    const at::Tensor* key = token_rows(a, 0, type, T, c.Hkv, D, &ks);
+    const at::Tensor* value = token_rows(a, 1, type, T, c.Hkv, D, &vs);
+    const at::Tensor* slots = a.take(4, at::kLong, 1);
+    void* stream = a.stream();
+    if (!a.ok || slots->size(0) != T) return answer(kAskPython);
+    return answer(pkv_gather_cache_q4(key->data_ptr(), ks, value->data_ptr(), vs, c.k->data_ptr(), c.v->data_ptr(),
+                                      static_cast<const int64_t*>(slots->data_ptr()), (int)T, c.Hkv, (int)D, c.bs,
+                                      c.NB, code(type), stream));
+}
+
+// decode_q4(out, q, k_cache, v_cache, block_tables, context_lens, scale,
+//           max_context_len, workspace)
+PyObject* decode_q4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    at::ScalarType type;
+    int64_t S, D;
+    if (n != 9 || !rows_like(args[1], &type, &S, &D)) return answer(kAskPython);
+    Args a{args};
+    Caches4 c;
+    if (!c.take(a, 2, 3, D)) return answer(kAskPython);
+    const at::Tensor* q = a.take(1, type, 3);
+    const at::Tensor* out = a.take(0, type, 3);
+    const at::Tensor* tables = a.take(4, at::kInt, 2);
+    const at::Tensor* lens = a.take(5, at::kInt, 1);
+    const float scale = a.scale(6, D);
+    const int most = a.integer(7);
+    const at::Tensor* ws = a.take(8, at::kByte, 1);
+    void* stream = a.stream();
+    if (!a.ok || out->sizes() != q->sizes() || tables->size(0) != S || lens->size(0) != S || !small(*q) ||
+        !small(*tables))
+        return answer(kAskPython);
+    return answer(pkv_paged_attention_decode_q4(
+        out->data_ptr(), q->data_ptr(), c.k->data_ptr(), c.v->data_ptr(),
+        static_cast<const int32_t*>(tables->data_ptr()), static_cast<const int32_t*>(lens->data_ptr()), (int)S,
+        (int)q->size(1), c.Hkv, (int)D, c.bs, c.NB, (int)tables->size(1), most, scale, code(type), ws->data_ptr(),
+        (size_t)ws->numel(), stream));
+}
+
 // C++ exceptions (torch's device query) end here.
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject* self, PyObject* const* args, Py_ssize_t n) {
@@ -211,6 +353,9 @@ PyMethodDef methods[] = {
     {"window", entry<window>(), METH_FASTCALL, "pkv_paged_attention_decode_window with tensors"},
     {"accumulate", entry<accumulate>(), METH_FASTCALL, "pkv_paged_attention_decode_accumulate with tensors"},
     {"evict", entry<evict>(), METH_FASTCALL, "pkv_evict_tokens with tensors"},
+    {"rotate", entry<rotate>(), METH_FASTCALL, "pkv_rotate_and_cache and pkv_rotate_and_cache_q4 with tensors"},
+    {"gather", entry<gather>(), METH_FASTCALL, "pkv_gather_cache_q4 with tensors"},
+    {"decode_q4", entry<decode_q4>(), METH_FASTCALL, "pkv_paged_attention_decode_q4 with tensors"},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

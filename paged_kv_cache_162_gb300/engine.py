@@ -139,7 +139,7 @@ def paged_attention_decode_shared_prefix(out, q, k_cache, v_cache, block_tables,
 
 class _AskCtypes:
     """Stands for _tensor_bind where there is none for this torch: every call is left to ctypes."""
-    window = accumulate = evict = staticmethod(lambda *args: -1)
+    window = accumulate = evict = rotate = gather = decode_q4 = staticmethod(lambda *args: -1)
 
 
 _bind = None
@@ -178,6 +178,20 @@ def _need(who, tensors, cache):
                     f"{'' if t.is_contiguous() else ' (not contiguous)'}")
         if t.device != dev and not (name in ("q", "out") and t.device.type == "cpu" and t.is_pinned()):
             _refuse(f"{who}: {name} is on {t.device}, the caches on {dev}")
+
+
+def _token_rows(who, name, t, dtype, shape, dev) -> int:
+    """Refuses unless t is [T, heads, D] of that type and shape with each
+    token's rows contiguous, on device `dev` or in pinned host memory; the
+    elements from one token to the next."""
+    if t.dtype != dtype or t.shape != shape:
+        _refuse(f"{who}: {name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    T, heads, D = shape
+    if T * heads * D and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+        _refuse(f"{who}: {name}: the {heads} x {D} elements of a token must be contiguous, got strides {t.stride()}")
+    if t.device != dev and not (t.device.type == "cpu" and t.is_pinned()):
+        _refuse(f"{who}: {name} is on {t.device}, the caches on {dev}")
+    return t.stride(0) if T > 1 else heads * D
 
 
 _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
@@ -449,6 +463,193 @@ def evict_tokens(k_cache, v_cache, scores, positions, block_tables, context_lens
         L.check(st, who)
 
 
+def new_rotary_table(positions, rotary_dim, base=10000.0, device="cuda") -> torch.Tensor:
+    """The rotary table of rotate_and_cache for positions 0 .. positions - 1:
+    [positions, rotary_dim] fp32, the cosines of the rotary_dim / 2 angles
+    position * base^(-2i / rotary_dim), then their sines.  The angles are taken
+    in 64 bits: in 32 those of far positions are off by whole steps."""
+    if positions < 1 or rotary_dim < 2 or rotary_dim % 2:
+        _refuse("new_rotary_table: positions >= 1 and an even rotary_dim >= 2")
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * float(base) ** (-i / rotary_dim)
+    return torch.cat([angle.cos(), angle.sin()], -1).float()
+
+
+def rotate_and_cache(key, value, k_cache, v_cache, block_tables, seq_idx, pos, slot_mapping, rotary_table=None,
+                     query=None, query_out=None, rotary_pos=None, interleaved=False, stream=None):
+    """compute_slot_mapping + the rotary position encoding of a step's queries
+    and keys + reshape_and_cache, in one kernel (see pkv_rotate_and_cache).
+
+    key, value: [T, Hkv, D] and query: [T, H, D], each token's rows contiguous,
+    tokens any multiple of 8 elements apart (slices of one projection);
+    caches: [NB, bs, Hkv, D]; block_tables [S, MB], seq_idx, pos [T] int32
+    (pos -1: padding, left alone); slot_mapping [T] int64 receives the slots.
+    rotary_table [positions, rotary_dim] fp32 (new_rotary_table; None: no
+    rotation) is read at rotary_pos [T] int32 (None: pos).  query_out receives
+    the queries (None: in place) and is returned."""
+    return _rotate("rotate_and_cache", False, key, value, k_cache, v_cache, block_tables, seq_idx, pos, slot_mapping,
+                   rotary_table, query, query_out, rotary_pos, interleaved, stream)
+
+
+def new_cache_q4(NB, bs, Hkv, D, device="cuda") -> torch.Tensor:
+    """A K (or V) pool held in 4 bits, all elements 0: uint8 [NB, Hkv, bs, RB]
+    with RB = D/2 + D/16 bytes per (token, KV head).  Written by
+    rotate_and_cache_q4, read by paged_attention_decode_q4 and
+    gather_cache_q4; its bytes are laid out as include/pagedkv.h says."""
+    RB = L.pkv_cache_q4_row_bytes(D)
+    if RB == 0 or bs not in (8, 16, 32, 64) or NB < 1 or Hkv < 1:
+        _refuse("new_cache_q4: head_dim must be 64/128, block_size 8/16/32/64, NB and Hkv at least 1")
+    return torch.zeros((NB, Hkv, bs, RB), dtype=_U8, device=device)
+
+
+def rotate_and_cache_q4(key, value, k_cache, v_cache, block_tables, seq_idx, pos, slot_mapping, rotary_table=None,
+                        query=None, query_out=None, rotary_pos=None, interleaved=False, stream=None):
+    """rotate_and_cache into 4-bit caches (new_cache_q4): K is quantised from
+    its rotated values in fp32."""
+    return _rotate("rotate_and_cache_q4", True, key, value, k_cache, v_cache, block_tables, seq_idx, pos,
+                   slot_mapping, rotary_table, query, query_out, rotary_pos, interleaved, stream)
+
+
+def _cache_sizes(who, cache, D, q4):
+    """(NB, bs, Hkv) of a cache for head_dim D."""
+    if cache.dim() != 4:
+        _refuse(f"{who}: the caches must be [NB, {'Hkv, bs, RB' if q4 else 'bs, Hkv, D'}]")
+    if not q4:
+        NB, bs, Hkv, Dk = cache.shape
+        if Dk != D:
+            _refuse(f"{who}: key has head_dim {D}, the caches {Dk}")
+        return NB, bs, Hkv
+    NB, Hkv, bs, RB = cache.shape
+    want = L.pkv_cache_q4_row_bytes(D)
+    if want == 0:
+        raise L.PkvError(L.PKV_ERR_UNSUPPORTED, f"{who}: head_dim must be 64 or 128, got {D}")
+    if RB != want or cache.dtype != _U8:
+        _refuse(f"{who}: 4-bit caches must be uint8 [NB, Hkv, bs, {want}] for head_dim {D}, got {cache.dtype} "
+                f"{tuple(cache.shape)}")
+    return NB, bs, Hkv
+
+
+def _rotate(who, q4, key, value, k_cache, v_cache, block_tables, seq_idx, pos, slot_mapping, rotary_table, query,
+            query_out, rotary_pos, interleaved, stream):
+    if query_out is None:
+        query_out = query
+    if stream is None:
+        st = _native().rotate(q4, key, value, k_cache, v_cache, block_tables, seq_idx, pos, slot_mapping, rotary_table,
+                              query, query_out, rotary_pos, interleaved)
+        if st == 0:
+            return query_out
+        if st > 0:
+            L.check(st, who)
+    if key.dim() != 3 or block_tables.dim() != 2 or (query is not None and query.dim() != 3):
+        _refuse(f"{who}: key must be [T, Hkv, D], query [T, H, D], block_tables [S, MB]")
+    T, Hkv, D = key.shape
+    dt, dev = key.dtype, k_cache.device
+    code = dtype_code(dt)
+    NB, bs, heads = _cache_sizes(who, k_cache, D, q4)
+    if heads != Hkv:
+        _refuse(f"{who}: key has {Hkv} heads, the caches {heads}")
+    if query is None and query_out is not None:
+        _refuse(f"{who}: query_out without query")
+    cdt = _U8 if q4 else dt
+    _need(who, [("k_cache", k_cache, cdt, None), ("v_cache", v_cache, cdt, k_cache.shape),
+                ("block_tables", block_tables, _I32, None), ("seq_idx", seq_idx, _I32, (T,)),
+                ("pos", pos, _I32, (T,)), ("slot_mapping", slot_mapping, torch.int64, (T,))]
+          + ([("rotary_pos", rotary_pos, _I32, (T,))] if rotary_pos is not None else [])
+          + ([("rotary_table", rotary_table, _F32, None)] if rotary_table is not None else []), k_cache)
+    rows, R = 0, 0
+    if rotary_table is not None:
+        if rotary_table.dim() != 2:
+            _refuse(f"{who}: rotary_table must be [positions, rotary_dim]")
+        rows, R = rotary_table.shape
+    ks, vs = _token_rows(who, "key", key, dt, key.shape, dev), _token_rows(who, "value", value, dt, key.shape, dev)
+    H, qs, qos = 0, 0, 0
+    if query is not None:
+        H = query.shape[1]
+        if H == 0:
+            _refuse(f"{who}: query has no heads")
+        qs = _token_rows(who, "query", query, dt, (T, H, D), dev)
+        qos = _token_rows(who, "query_out", query_out, dt, (T, H, D), dev)
+    S, MB = block_tables.shape
+    L.int32(max(T, H, S, MB, rows, R, *k_cache.shape), f"{who}: the largest extent")
+    with torch.cuda.device(dev):
+        (L.pkv_rotate_and_cache_q4 if q4 else L.pkv_rotate_and_cache)(
+            key, ks, value, vs, query, qs, query_out, qos, k_cache, v_cache, block_tables, seq_idx, pos, rotary_pos,
+            rotary_table, rows, R, bool(interleaved), slot_mapping, T, S, H, Hkv, D, bs, NB, MB, code, stream=stream)
+    return query_out
+
+
+def gather_cache_q4(key, value, k_cache, v_cache, slot_mapping, stream=None):
+    """Reads the rows of slot_mapping [T] int64 out of 4-bit caches into key
+    and value [T, Hkv, D] (strides as in rotate_and_cache), as the 16-bit
+    values that they stand for; rows of negative slots are left as they were.
+    For the cached prefix of a prompt's next chunk, or a sequence on its way
+    into a 16-bit cache (reshape_and_cache)."""
+    who = "gather_cache_q4"
+    if stream is None:
+        st = _native().gather(key, value, k_cache, v_cache, slot_mapping)
+        if st == 0:
+            return key, value
+        if st > 0:
+            L.check(st, who)
+    if key.dim() != 3:
+        _refuse(f"{who}: key must be [T, Hkv, D]")
+    T, Hkv, D = key.shape
+    dt, dev = key.dtype, k_cache.device
+    code = dtype_code(dt)
+    NB, bs, heads = _cache_sizes(who, k_cache, D, True)
+    if heads != Hkv:
+        _refuse(f"{who}: key has {Hkv} heads, the caches {heads}")
+    _need(who, (("k_cache", k_cache, _U8, None), ("v_cache", v_cache, _U8, k_cache.shape),
+                ("slot_mapping", slot_mapping, torch.int64, (T,))), k_cache)
+    ks, vs = _token_rows(who, "key", key, dt, key.shape, dev), _token_rows(who, "value", value, dt, key.shape, dev)
+    L.int32(max(T, *k_cache.shape), f"{who}: the largest extent")
+    with torch.cuda.device(dev):
+        L.pkv_gather_cache_q4(key, ks, value, vs, k_cache, v_cache, slot_mapping, T, Hkv, D, bs, NB, code, stream)
+    return key, value
+
+
+def new_q4_workspace(S, H, Hkv, D, device="cuda") -> torch.Tensor:
+    return _workspace("new_q4_workspace", L.pkv_decode_q4_workspace_size(S, H, Hkv, D), device)
+
+
+def paged_attention_decode_q4(out, q, k_cache, v_cache, block_tables, context_lens, scale=None, max_context_len=0,
+                              workspace=None, stream=None):
+    """Decode attention of each sequence's newest token over its whole context
+    in 4-bit caches (new_cache_q4).  q, out: [S, H, D] with H a multiple of Hkv
+    (at most 16 query heads per KV head), of the type the caches were written
+    with; block_tables [S, MB], context_lens [S] int32.  workspace:
+    new_q4_workspace(S, H, Hkv, D), kept between calls."""
+    who = "paged_attention_decode_q4"
+    if stream is None and workspace is not None:
+        st = _native().decode_q4(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
+                                 workspace)
+        if st == 0:
+            return out
+        if st > 0:
+            L.check(st, who)
+    if q.dim() != 3 or block_tables.dim() != 2:
+        _refuse(f"{who}: q must be [S, H, D], block_tables [S, MB]")
+    S, H, D = q.shape
+    code = dtype_code(q.dtype)
+    NB, bs, Hkv = _cache_sizes(who, k_cache, D, True)
+    MB = block_tables.shape[1]
+    L.int32(max(S, H, MB, *k_cache.shape), f"{who}: the largest extent")
+    max_context_len = L.int32(max_context_len, "max_context_len")
+    _need(who, (("k_cache", k_cache, _U8, None), ("v_cache", v_cache, _U8, k_cache.shape),
+                ("q", q, q.dtype, None), ("out", out, q.dtype, q.shape),
+                ("block_tables", block_tables, _I32, (S, MB)), ("context_lens", context_lens, _I32, (S,))), k_cache)
+    ws, dev = workspace, k_cache.get_device()
+    if ws is None:
+        ws = _workspace(who, L.pkv_decode_q4_workspace_size(S, H, Hkv, D), k_cache.device, stream)
+    else:
+        _check_workspace(who, ws, dev)
+    with torch.cuda.device(dev):
+        L.pkv_paged_attention_decode_q4(out, q, k_cache, v_cache, block_tables, context_lens, S, H, Hkv, D, bs, NB,
+                                        MB, max_context_len, D ** -0.5 if scale is None else scale, code, ws,
+                                        ws.numel(), stream)
+    return out
+
+
 def compute_slot_mapping(slot_mapping, block_tables, seq_idx, pos, block_size, stream=None):
     L.pkv_compute_slot_mapping(slot_mapping, block_tables, seq_idx, pos, seq_idx.numel(),
                                block_tables.shape[0], block_tables.shape[1], block_size, stream)
@@ -462,9 +663,26 @@ def reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, stream=None):
                             dtype_code(key.dtype), stream)
 
 
+def _q4_head_dim(who, cache) -> int:
+    """head_dim of a 4-bit cache [NB, Hkv, bs, RB]."""
+    for D in (64, 128):
+        if cache.dim() == 4 and cache.shape[3] == L.pkv_cache_q4_row_bytes(D):
+            return D
+    _refuse(f"{who}: not a 4-bit cache: uint8 {tuple(cache.shape)}")
+
+
 def copy_blocks(k_cache, v_cache, block_mapping, stream=None):
-    NB, bs, H, D = k_cache.shape
+    """Block copies (src, dst) [P, 2] int64 within 16-bit caches [NB, bs, H,
+    D], or within 4-bit ones (new_cache_q4)."""
     P = block_mapping.shape[0] if block_mapping is not None else 0
+    if k_cache.dtype == _U8:
+        D = _q4_head_dim("copy_blocks", k_cache)
+        NB, Hkv, bs, _ = k_cache.shape
+        if v_cache.dtype != _U8 or v_cache.shape != k_cache.shape:
+            _refuse("copy_blocks: k_cache and v_cache differ in type or shape")
+        L.pkv_copy_blocks_q4(k_cache, v_cache, block_mapping, P, Hkv, D, bs, NB, stream)
+        return
+    NB, bs, H, D = k_cache.shape
     L.pkv_copy_blocks(k_cache, v_cache, block_mapping, P, H, D, bs, NB,
                       dtype_code(k_cache.dtype), stream)
 
@@ -472,9 +690,19 @@ def copy_blocks(k_cache, v_cache, block_mapping, stream=None):
 def swap_blocks(gpu_k, gpu_v, host_k, host_v, block_mapping, direction, stream=None):
     """GPU <-> pinned-host block copies (CPU swap).  block_mapping [P, 2]
     int64 on the device: (gpu block, host block) pairs for swap-out,
-    (host block, gpu block) pairs for swap-in."""
-    NBg, bs, H, D = gpu_k.shape
+    (host block, gpu block) pairs for swap-in.  16-bit caches, or 4-bit ones on
+    both sides."""
     P = block_mapping.shape[0]
+    if gpu_k.dtype == _U8:
+        D = _q4_head_dim("swap_blocks", gpu_k)
+        NBg, Hkv, bs, _ = gpu_k.shape
+        if any(x.dtype != _U8 or x.dim() != 4 or x.shape[1:] != gpu_k.shape[1:] for x in (gpu_v, host_k, host_v)) \
+                or gpu_v.shape != gpu_k.shape or host_v.shape != host_k.shape:
+            _refuse("swap_blocks: the 4-bit caches differ in type or shape")
+        L.pkv_swap_blocks_q4(gpu_k, gpu_v, host_k, host_v, block_mapping, P, Hkv, D, bs, NBg, host_k.shape[0],
+                             direction, stream)
+        return
+    NBg, bs, H, D = gpu_k.shape
     L.pkv_swap_blocks(gpu_k, gpu_v, host_k, host_v, block_mapping, P, H, D, bs, NBg,
                       host_k.shape[0], dtype_code(gpu_k.dtype), direction, stream)
 
