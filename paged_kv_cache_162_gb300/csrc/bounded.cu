@@ -95,6 +95,20 @@ constexpr int kRingBytes = kStages * 2 * kTileBytes<D>;  // one warp's ring
 template <int D>
 constexpr int kSmemBytes = kWarps * kRingBytes<D>;
 
+// What a weight of 1 is in P.V.  In fp16 a weight below 2^-25 would be nothing and
+// one below 2^-14 lose digits, and a long context's can all be: one token of
+// logit 0 among 2^20 of -18 has 1.6 % of the weight lost.  In units of 2^-15 (the
+// largest weight is 1: 32768 of 65504) the same happens below 2^-40.  bf16 has the
+// range of fp32.
+template <class E>
+constexpr float kWeightUnits = 1.f;
+template <>
+constexpr float kWeightUnits<pkv::F16> = 32768.f;
+
+// What makes a row of P.V the output: 1 / L, and the units of the weights.
+template <class E>
+__device__ __forceinline__ float output_scale(float L) { return inverse_of(L) * (1.f / kWeightUnits<E>); }
+
 // Running softmax of one warp over its tiles: rows lane/4 and lane/4 + 8 of
 // the accumulators, (m, l) per row.
 template <int D>
@@ -834,6 +848,265 @@ __global__ void __launch_bounds__(kThreads, 2) split_kernel(const __grid_constan
     cp_async_wait<0>();
 }
 
+// Row `row` of head hl in the piece that range c has of a unit beginning in c0.
+__device__ __forceinline__ int64_t piece_row(const Params& p, int c, int c0, int hl, int row) {
+    return ((2 * (int64_t)c + (c == c0 ? 1 : 0)) * p.hw + hl) * p.G + row;
+}
+
+// (M, L) of two parts of a row as one.
+__device__ __forceinline__ void merge_ml(float& M, float& L, float m, float l) {
+    const float m_new = fmaxf(M, m);
+    const float use = m_new == -INFINITY ? 0.f : m_new;
+    L = L * exp2f(M - use) + l * exp2f(m - use);
+    M = m_new;
+}
+
+// Writes row i of unit `unit`.
+template <class E, int D>
+__device__ __forceinline__ void write_row(const Params& p, int unit, int i, int lane, float L,
+                                          const float (&o)[D / 32]) {
+    const float inv = output_scale<E>(L);
+    const int64_t oh = (int64_t)(unit / p.HB) * p.H + (int64_t)(unit % p.HB) * p.hw * p.G + i;
+    uint16_t* dst = static_cast<uint16_t*>(p.out) + oh * D + lane * (D / 32);
+#pragma unroll
+    for (int j = 0; j < D / 32; j += 2)
+        *reinterpret_cast<uint32_t*>(dst + j) = E::from_float2(o[j] * inv, o[j + 1] * inv);
+}
+
+// M and 1 / L of query head `lane` (< G) of a KV head, by one warp: h0 its first
+// query head in row_m and row_l, `place` the ranges of its unit, hl the head in
+// it.  All loads of a round go out together.
+__device__ __forceinline__ void group_ml(const Params& p, int64_t h0, int2 place, int hl, int lane,
+                                         float& M, float& inv) {
+    const int pieces = place.y - place.x + 1;
+    float L = 0.f;
+    M = -INFINITY;
+    if (pieces == 1) {
+        if (lane < p.G) {
+            M = p.row_m[h0 + lane];
+            L = p.row_l[h0 + lane];
+        }
+    } else if (pieces <= 4) {  // four lanes per head, eight heads per round
+        for (int r0 = 0; r0 < p.G; r0 += 8) {
+            const int row = r0 + lane / 4, c = place.x + lane % 4;
+            float m = -INFINITY, l = 0.f;
+            if (row < p.G && c <= place.y) {
+                const int64_t at = piece_row(p, c, place.x, hl, row);
+                m = p.part_m[at];
+                l = p.part_l[at];
+            }
+#pragma unroll
+            for (int o = 1; o <= 2; o <<= 1)
+                merge_ml(m, l, __shfl_xor_sync(kFull, m, o), __shfl_xor_sync(kFull, l, o));
+            const float mr = __shfl_sync(kFull, m, 4 * (lane & 7)), lr = __shfl_sync(kFull, l, 4 * (lane & 7));
+            if (lane / 8 == r0 / 8) {
+                M = mr;
+                L = lr;
+            }
+        }
+    } else {  // the warp on four heads per round
+        for (int r0 = 0; r0 < p.G; r0 += 4) {
+            float m[4], l[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                m[r] = -INFINITY;
+                l[r] = 0.f;
+            }
+            for (int c = place.x + lane; c <= place.y; c += 32) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (r0 + r < p.G) {
+                        const int64_t at = piece_row(p, c, place.x, hl, r0 + r);
+                        merge_ml(m[r], l[r], p.part_m[at], p.part_l[at]);
+                    }
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    merge_ml(m[r], l[r], __shfl_xor_sync(kFull, m[r], o), __shfl_xor_sync(kFull, l[r], o));
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (lane == r0 + r) {
+                    M = m[r];
+                    L = l[r];
+                }
+        }
+    }
+    inv = inverse_of(L);
+}
+
+// Adds the weights of tokens j0 + 4 (32 u + lane) .. + 3, u < RUNS, of KV head
+// kvh of sequence s to their scores, by one warp; `place`: the ranges its unit
+// begins and ends in, hl: the head in it.  z of the first HEADS query heads and
+// the old scores are on their way while M and L are found.
+template <int RUNS, int HEADS>
+__device__ __forceinline__ void fold_stretch(const Params& p, int s, int kvh, int hl, int n, int2 place,
+                                             int j0, int lane) {
+    const int64_t h0 = (int64_t)s * p.H + (int64_t)kvh * p.G;
+    const float* z = p.z + h0 * p.z_stride;
+    float* sc = p.scores + ((int64_t)s * p.Hkv + kvh) * p.score_stride;
+    const bool vec = (reinterpret_cast<uintptr_t>(sc) & 15u) == 0;
+    float4 zz[RUNS][HEADS];
+    float old[RUNS][4];
+#pragma unroll
+    for (int u = 0; u < RUNS; ++u) {
+        const int j = j0 + 4 * (32 * u + lane);
+#pragma unroll
+        for (int r = 0; r < HEADS; ++r)
+            zz[u][r] = j < n && r < p.G ? *reinterpret_cast<const float4*>(z + r * p.z_stride + j)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (vec && j + 4 <= n) {
+            const float4 v = *reinterpret_cast<const float4*>(sc + j);
+            old[u][0] = v.x; old[u][1] = v.y; old[u][2] = v.z; old[u][3] = v.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) old[u][e] = j + e < n ? sc[j + e] : 0.f;
+        }
+    }
+    float M, inv;
+    group_ml(p, h0, place, hl, lane, M, inv);
+#pragma unroll
+    for (int u = 0; u < RUNS; ++u) {
+        const int j = j0 + 4 * (32 * u + lane);
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+        auto add = [&](const float4& v, int r) {
+            const float m = __shfl_sync(kFull, M, r), i = __shfl_sync(kFull, inv, r);
+            if (i != 0.f) {
+                w[0] = fmaf(exp2f(v.x - m), i, w[0]);
+                w[1] = fmaf(exp2f(v.y - m), i, w[1]);
+                w[2] = fmaf(exp2f(v.z - m), i, w[2]);
+                w[3] = fmaf(exp2f(v.w - m), i, w[3]);
+            }
+        };
+#pragma unroll
+        for (int r = 0; r < HEADS; ++r)
+            if (r < p.G) add(zz[u][r], r);
+        if constexpr (HEADS > 1) {
+#pragma unroll 4
+            for (int r = HEADS; r < p.G; ++r)
+                add(j < n ? *reinterpret_cast<const float4*>(z + r * p.z_stride + j) : make_float4(0.f, 0.f, 0.f, 0.f), r);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) old[u][e] += w[e];
+        if (vec && j + 4 <= n) {
+            *reinterpret_cast<float4*>(sc + j) = make_float4(old[u][0], old[u][1], old[u][2], old[u][3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (j + e < n) sc[j + e] = old[u][e];
+        }
+    }
+}
+
+// After split_kernel, one wave of CTAs that take items: first the joins, then,
+// with scores, the fold.  Either is a short chain of loads (is there anything ->
+// where -> the data), and most possible items do not exist: so the threads of a
+// CTA look at 256 of its share at once, list those that do, and its warps do
+// the listed ones in turn: 155 us for the 256 requests of 16..4096, where warps
+// with items of their own took 160.  Fewer tokens per fold, two or four CTAs per
+// SM: no faster (at three the score forms spill 4 to 28 bytes, at two nothing).
+//  join: a row of a unit that lies in several ranges, by a warp, or by the
+//        CTA's warps together (`wide`) where units have many pieces.
+//  fold: 256 tokens (512 with one query head) of a KV head, by a warp.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+struct Item {
+    int2 place;  // the ranges its unit begins and ends in
+    int at;      // join: output row; fold: sequence * Hkv + KV head
+    int n, j0;   // fold: context (join: 0), first token
+};
+
+template <class E, int D, bool kScores, bool kOne>
+__global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const __grid_constant__ Params p, int wide) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    constexpr int DPL = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = p.hw * p.G;
+    const int joins = p.S * p.HB * rows;  // = S * H
+    if (wide) {
+        __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+        __shared__ __align__(16) float s_o[kJoinWarps][D];
+        for (int i = blockIdx.x; i < joins; i += gridDim.x) {
+            const int2 at = p.place[i / rows];
+            if (pkv::pieces_of(at.x, at.y, p.ranges) < 2) continue;  // the same for the whole CTA
+            float M, L, o[DPL];
+            gather_row<D, 6>(p, at.x, at.x + warp, at.y, kJoinWarps, i % rows, lane, M, L, o);
+            if (lane == 0) {
+                s_m[warp] = M;
+                s_l[warp] = L;
+            }
+#pragma unroll
+            for (int j = 0; j < DPL; ++j) s_o[warp][lane * DPL + j] = o[j];
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int w = 1; w < kJoinWarps; ++w) {
+                    const float m_new = fmaxf(M, s_m[w]);
+                    const float use = m_new == -INFINITY ? 0.f : m_new;
+                    const float wo = exp2f(M - use), wn = exp2f(s_m[w] - use);
+                    L = L * wo + s_l[w] * wn;
+                    M = m_new;
+#pragma unroll
+                    for (int j = 0; j < DPL; ++j) o[j] = fmaf(wn, s_o[w][lane * DPL + j], o[j] * wo);
+                }
+                write_row<E, D>(p, i / rows, i % rows, lane, L, o);
+            }
+            __syncthreads();  // the parts have been read
+        }
+    }
+    constexpr int RUNS = kOne ? 4 : 2, HEADS = kOne ? 1 : 4, TOKENS = RUNS * 128;
+    __shared__ int s_count[kJoinWarps];
+    __shared__ Item s_item[kJoinThreads];
+    const int heads = p.S * p.Hkv;
+    const long long listed = wide ? 0 : joins;
+    const long long items = listed + (kScores ? (long long)heads * ((p.max_ctx + TOKENS - 1) / TOKENS) : 0);
+    // neighbouring items go to different SMs
+    for (long long base = blockIdx.x; base < items; base += (long long)kJoinThreads * gridDim.x) {
+        const long long mine = base + (long long)threadIdx.x * gridDim.x;
+        Item it;
+        it.n = 0;  // of a join
+        bool live = false;
+        if (mine < listed) {
+            it.at = (int)mine;
+            it.place = p.place[it.at / rows];
+            live = pkv::pieces_of(it.place.x, it.place.y, p.ranges) > 1;
+        } else if (kScores && mine < items) {
+            // (stretch, sequence, KV head): the first stretches of all first
+            const long long f = mine - listed;
+            it.at = (int)(f % heads);
+            it.j0 = (int)(f / heads) * TOKENS;
+            it.n = context_of(p, it.at / p.Hkv);
+            it.place = p.place[it.at / p.hw];
+            live = it.j0 < it.n && pkv::pieces_of(it.place.x, it.place.y, p.ranges) > 0;
+        }
+        const unsigned alive = __ballot_sync(kFull, live);
+        if (lane == 0) s_count[warp] = __popc(alive);
+        __syncthreads();
+        int before = 0, count = 0;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            if (w == warp) before = count;
+            count += s_count[w];
+        }
+        if (live) s_item[before + __popc(alive & ((1u << lane) - 1u))] = it;
+        __syncthreads();
+        for (int k = warp; k < count; k += kJoinWarps) {
+            const Item x = s_item[k];
+            if (x.n == 0) {
+                float M, L, o[DPL];
+                gather_row<D, 2>(p, x.place.x, x.place.x, x.place.y, 1, x.at % rows, lane, M, L, o);
+                write_row<E, D>(p, x.at / rows, x.at % rows, lane, L, o);
+            } else if constexpr (kScores) {
+                const int kvh = x.at % p.Hkv;
+                fold_stretch<RUNS, HEADS>(p, x.at / p.Hkv, kvh, kvh % p.hw, x.n, x.place, x.j0, lane);
+            }
+        }
+        __syncthreads();  // the list has been read
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
@@ -847,6 +1120,7 @@ __global__ void __launch_bounds__(kThreads, 2) split_kernel(const __grid_constan
 // few CTAs run (one 32768-token context, scores: 48 us against 36).
 constexpr int kDirectTokens = 1024;
 constexpr int direct_waves(bool scores, int64_t most) { return !scores ? 4 : most <= 256 ? 3 : 2; }
+constexpr int kJoinCtasPerSm = 3;   // of the join kernel
 constexpr int kCtasPerSm = 2;       // of the attention kernels
 struct Layout {
     size_t place, m, l, acc, row_m, row_l, z, total;
@@ -873,6 +1147,8 @@ Layout layout_of(int S, int H, int Hkv, int D, bool scores, int max_ctx) {
     L.total = o;
     return L;
 }
+
+using JoinFn = void (*)(Params, int);
 
 template <class E, bool kScores, bool kDirect>
 KernelFn pick_attend(int D, bool wide) {
