@@ -1,118 +1,929 @@
 // Decode attention over a cache held in 4 bits (q4.cuh).
 //
-// One CTA takes one query head of one sequence; its warps take tokens in turn,
-// D / 32 elements per lane, with a running maximum and sum per warp that are
-// joined at the end.
+// For sequence s, query head h of KV head g, context n, groups r of 64 dims:
+//   z_j = scale sum_r (step_jr sum_{d in r} q_d c_jd + centre_jr sum_{d in r} q_d),  c = code - 8
+//   out_d = sum_j p_j (step_jr c_jd + centre_jr),  p = softmax z.
+// So the codes go into the products as they are, exact in fp16, and the steps
+// and centres are applied outside of them, in fp32: to the group's part of a
+// logit, and to the weight, of which each group of V has its own, p_j step_jr.
+//
+// Units, tiles, ranges and the two ways to spread them (direct, split) are
+// unit_ranges.cuh's.  A unit is one sequence and `hw` neighbouring KV heads, one
+// warp takes one head of a 32-token tile: 4 units of 8 tokens of K and of V, each
+// one asynchronous bulk copy into the warp's ring (a (block, head) is one run of
+// the pool), an mbarrier per stage.
+//
+// The products are m16n8k16 in fp16 with the cache as the 16 rows and the query
+// heads as the 8 columns, S^T = K Q^T and O^T = V^T P^T: a group of up to 8 query
+// heads fills them with half the products that heads as rows would take, and
+// accumulators of half the size (more than 8 heads: two column blocks).
+//  * K: ldmatrix gives a lane 8 codes of one token, 32 bits; q is loaded in the
+//    order that makes of them two fragments.  q is 16-bit: bf16 is made fp16 by
+//    a power of two per head, exact but for elements below 2^-24 of the largest.
+//  * V: transposing ldmatrix of 16-bit pieces, 4 codes of one token each, gives a
+//    lane 4 codes of two neighbouring tokens: the pairs that the product's k wants.
+//  * Codes to fp16: a nibble at bits 0 or 4 of a half under the exponent of 1024
+//    or 64 is that number + code; one subtraction takes it to -8 .. 7: 5 integer
+//    and 4 fp16 instructions per 8 codes.
+//  * P^T comes out of S^T's accumulators by movmatrix.  A weight times its step is
+//    rounded to fp16 once, 2^-11 of itself (the output's own rounding in fp16, an
+//    eighth of it in bf16).  Both factors are bounded by powers of two (2^kLazy, and
+//    the running maximum of the steps), and the units make 2^15 of their
+//    product: what falls below 2^-24 is 2^-39 of the largest.
+//  * The running maximum moves only when a logit passes it by more than kLazy: one
+//    vote per tile instead of three exchanges per head.
+#include <cooperative_groups.h>
+
 #include <climits>
 #include <cmath>
 #include <cstdio>
+#include <type_traits>
 
 #include "pagedkv.h"
 #include "pkv_device.cuh"
+#include "pkv_mma.cuh"
 #include "q4.cuh"
+#include "unit_ranges.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace {
 
 namespace q4 = pkv::q4;
+using pkv::ldsm_x4;
+using pkv::ldsm_x4_trans;
 
-constexpr unsigned kFull = 0xffffffffu;
-constexpr int kWarps = 4;
-constexpr int kMaxGroup = 16;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTile = 32;  // tokens: a lane looks up one
+constexpr int kStages = 3;
+constexpr int kMaxRanges = 1824;  // CTAs of a split call
+constexpr float kLazy = 6.f;      // log2 of what a weight may pass 1 by
+constexpr float kUnits = 256.f;   // 2^(15 - 1 - kLazy): a step is below 2^(E + 1)
 
-struct Params {
-    char* out;
-    const char* q;
-    const char *k_cache, *v_cache;
-    const int32_t *block_tables, *context_lens;
-    int S, H, Hkv, G, NB, MB, bs_log2, max_ctx;
-    float qscale;  // scale * log2(e)
-    int* err;
+// One tile's K (or V): 4 units.
+template <int D>
+constexpr int kTileBytes = kTile / q4::kUnit * q4::kUnitBytes<D>;
+template <int D>
+constexpr int kRingBytes = kStages * 2 * kTileBytes<D>;  // one warp's ring
+template <int D>
+constexpr int kSmemBytes = kWarps * kRingBytes<D>;
+// CTAs per SM that the registers are for
+template <int D, bool kWide>
+constexpr int kCtas = kWide ? 2 : (D == 128 ? 3 : 4);
+
+__device__ __forceinline__ float exp2_of(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// An 8x8 block of 16-bit elements, two of a row per lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+// The codes 4e and 16 + 4e bits up in x, e = 0..3, as pairs of fp16, minus 8.
+__device__ __forceinline__ void codes_of(uint32_t x, uint32_t (&h)[4]) {
+    const uint32_t y = x >> 8;
+    h[0] = hsub2((x & 0x000f000fu) | 0x64006400u, 0x64086408u);  // 1024 + c - 1032
+    h[1] = hsub2((x & 0x00f000f0u) | 0x54005400u, 0x54805480u);  // 64 + c - 72
+    h[2] = hsub2((y & 0x000f000fu) | 0x64006400u, 0x64086408u);
+    h[3] = hsub2((y & 0x00f000f0u) | 0x54005400u, 0x54805480u);
+}
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const char* src, int bytes, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+// The (step, centre) pairs of a row, one per group.
+template <int NG>
+__device__ __forceinline__ void pairs_at(uint32_t from, uint32_t (&pair)[NG]) {
+    if constexpr (NG == 2)
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(pair[0]), "=r"(pair[1]) : "r"(from) : "memory");
+    else
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(pair[0]) : "r"(from) : "memory");
+}
+
+// One warp's tiles on their way through its ring, `step` apart, each looked up
+// one tile ahead of its copies and copied kStages - 1 tiles ahead of its use.
+// With a plan and step 1 it goes on into the units and ranges that follow.
+template <int D>
+struct Feed {
+    static constexpr int NST = kStages;
+    static constexpr int UB = q4::kUnitBytes<D>;
+    const Params& p;
+    Plan* const plan;          // null: one unit (part) at a time
+    int* const abort;
+    const uint32_t ring, bars; // bars: an mbarrier per stage
+    const int warp, lane, hl;  // hl: head of the CTA's hw that this warp takes
+    const int step;
+    int s, hb, n_next, i, te, left;  // the next tile to copy, and its unit; left: from its tile 0 to the range's end
+    int nv;
+    const int32_t* bt;
+    int64_t src;               // first byte of the unit of 8 that its token `lane` is in
+    bool there, more;          // there: that token exists
+    unsigned mask[NST];        // tokens of the tiles in the ring
+    int into, from;            // stages of the next copy and of the oldest tile
+    unsigned phase;            // bit st: parity of stage st's copy that is waited for next
+    int asked, answers, pushed;
+
+    __device__ __forceinline__ Feed(const Params& p_, Plan* plan_, int* abort_, uint32_t ring_, uint32_t bars_,
+                                    int warp_, int lane_, int hl_, int step_)
+        : p(p_), plan(plan_), abort(abort_), ring(ring_), bars(bars_), warp(warp_), lane(lane_), hl(hl_),
+          step(step_), into(0), from(0), phase(0), asked(0), answers(0), pushed(0) {
+        if (lane == 0)
+            for (int st = 0; st < NST; ++st) tc_mbar_init(bars + 8 * st, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ void enter(int n) {  // unit (s, hb)
+        nv = n;
+        bt = p.block_tables + (int64_t)s * p.MB;
+        const char* q = static_cast<const char*>(p.q) +
+                        ((int64_t)s * p.H + (int64_t)(hb * p.hw + hl) * p.G) * D * 2;
+        if (lane * 128 < p.G * D * 2) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + lane * 128));
+    }
+
+    __device__ __forceinline__ void lookup() {
+        there = false;
+        const int64_t tok = (int64_t)i * kTile + lane;
+        if (!more || tok >= nv) return;
+        const int phys = __ldg(bt + (tok >> p.bs_log2));
+        if ((unsigned)phys >= (unsigned)p.NB) {
+            pkv::report(p.err, PKV_DEVERR_BLOCK_ID);
+            return;
+        }
+        there = true;
+        src = q4::unit_at<D>((phys << p.bs_log2) | ((int)tok & ((1 << p.bs_log2) - 1)), hb * p.hw + hl, p.Hkv, p.bs_log2);
+    }
+
+    __device__ __forceinline__ void begin(int s_, int hb_, int n, int first, int te_, int left_) {
+        s = s_;
+        hb = hb_;
+        i = first;
+        te = te_;
+        left = left_;
+        n_next = chained() && s + 1 < p.S ? context_of(p, s + 1) : 0;
+        more = i < te;
+        enter(n);
+        lookup();
+#pragma unroll
+        for (int st = 0; st < NST - 1; ++st) push(st);
+    }
+
+    __device__ __forceinline__ bool chained() const { return plan != nullptr && step == 1; }
+
+    __device__ __forceinline__ void maybe_ask(int tiles_left) {
+        if (warp == 0 && tiles_left <= 3 && asked == answers) {
+            if (lane == 0) ask_range(plan, asked);
+            ++asked;
+        }
+    }
+    __device__ __forceinline__ bool next() {
+        maybe_ask(0);
+        int k = answers;
+        const bool got = next_range(p, plan, warp, lane, k, pushed);
+        asked = answers = k;
+        if (got) ++pushed;
+        return got;
+    }
+
+    // Copies the next tile into the ring, its tokens' mask into mask[at], then
+    // looks up the one after it.
+    __device__ __forceinline__ void push(int at) {
+        mask[at] = __ballot_sync(kFull, there);
+        if (!more) return;
+        const uint32_t bar = bars + 8 * into, sk = ring + into * 2 * kTileBytes<D>, sv = sk + kTileBytes<D>;
+        if (lane == 0)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                         "r"(__popc(mask[at] & 0x01010101u) * 2 * UB)
+                         : "memory");
+        __syncwarp();
+        if (there && (lane & 7) == 0) {
+            const uint64_t policy = plan ? pkv::policy_evict_first() : pkv::policy_evict_normal();
+            bulk_copy(sk + (lane >> 3) * UB, static_cast<const char*>(p.k_cache) + src, UB, bar, policy);
+            bulk_copy(sv + (lane >> 3) * UB, static_cast<const char*>(p.v_cache) + src, UB, bar, policy);
+        }
+        into = into + 1 == NST ? 0 : into + 1;
+        i += step;
+        if (i >= te) advance();
+        if (more && chained()) maybe_ask(left - i);
+        lookup();
+    }
+
+    // Waits for the oldest tile.
+    __device__ __forceinline__ void wait() {
+        if (!tc_mbar_wait(bars + 8 * from, phase >> from & 1u, abort)) {
+            pkv::report(p.err, PKV_DEVERR_TIMEOUT);
+            *(volatile int*)abort = 1;
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ void done() {
+        phase ^= 1u << from;
+        from = from + 1 == NST ? 0 : from + 1;
+#pragma unroll
+        for (int st = 0; st < NST - 1; ++st) mask[st] = mask[st + 1];
+        __syncwarp();  // this stage is filled again by the next push
+    }
+
+    __device__ __forceinline__ void advance() {
+        more = false;
+        if (!chained()) return;
+        left -= te;
+        int n;
+        if (left > 0) {  // the range's next unit
+            i = 0;
+            if (++hb == p.HB) {
+                hb = 0;
+                ++s;
+                n = n_next;
+                n_next = s + 1 < p.S ? context_of(p, s + 1) : 0;
+            } else {
+                n = context_of(p, s);
+            }
+        } else {         // another range
+            const int at = pushed;
+            if (!next()) return;
+            const Range& r = plan->queue[warp][at & 3];
+            s = r.s;
+            hb = r.hb;
+            i = r.tb;
+            left = r.left + r.tb;
+            n = r.n;
+            n_next = s + 1 < p.S ? context_of(p, s + 1) : 0;
+        }
+        more = true;
+        enter(n);
+        te = min(tiles_of(p, n), left);
+    }
 };
 
-// D / 32 elements of row `row` of a unit, elements D / 32 * lane and up.
-template <class E, int D>
-__device__ __forceinline__ void row_of(const char* unit, int row, int lane, float (&x)[D / 32]) {
-    constexpr int N = D / 32;
-    const int d = N * lane;
-    const char* code = unit + row * q4::code_bytes(D) + 16 * q4::chunk_place<D>(row, d / 32) + d % 32 / 2;
-    const float2 sm = E::to_float2(*reinterpret_cast<const uint32_t*>(unit + q4::kUnitCodes<D> +
-                                                                      row * q4::pair_bytes(D) + 4 * (d / 64)));
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        x[i] = fmaf(sm.x, (float)((((unsigned char)code[i / 2] >> (4 * (i & 1))) & 15) - 8), sm.y);
+// What a warp has of its unit: lane (g, t) = (lane / 4, lane % 4) has, of the
+// heads 8 x + 2 t + h (x: column block, h = 0, 1), the dims 32 i + 4 g + e, and
+// the heads' m and l.
+template <int D, int X>
+struct Acc {
+    float o[X][D / 32][2][4];
+    float m[X][2], l[X][2];
+    __device__ __forceinline__ float& at(int x, int i, int e, int h) { return o[x][i][e >> 1][2 * (e & 1) + h]; }
+};
+
+// Sum over the lanes with the same t.
+__device__ __forceinline__ float sum_rows(float x) {
+    x += __shfl_xor_sync(kFull, x, 4);
+    x += __shfl_xor_sync(kFull, x, 8);
+    return x + __shfl_xor_sync(kFull, x, 16);
+}
+__device__ __forceinline__ float max_rows(float x) {
+    x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+    return fmaxf(x, __shfl_xor_sync(kFull, x, 16));
 }
 
-template <class E, int D>
-__global__ void __launch_bounds__(32 * kWarps) attend_kernel(const __grid_constant__ Params p) {
+// One warp: KV head kvh of sequence s, its tiles first, first + step, ... below
+// te out of the feed.  X: blocks of 8 query heads.
+template <class E, int D, int X>
+__device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, int kvh, int first, int te, int lane,
+                                       Acc<D, X>& a) {
+    constexpr int NI = D / 32, NG = D / q4::kGroup, UB = q4::kUnitBytes<D>, UC = q4::kUnitCodes<D>;
+    constexpr int SUB = kTile / 16;
+    constexpr bool kHalf = std::is_same<E, pkv::F16>::value;
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) a.o[x][i][0][c] = a.o[x][i][1][c] = 0.f;
+        a.m[x][0] = a.m[x][1] = -INFINITY;
+        a.l[x][0] = a.l[x][1] = 0.f;
+    }
+    if (first >= te) return;
+
+    // The queries as columns: lane (g, t) has head 8 x + g, and of chunk i the
+    // dims 32 i + 8 t + e and + 4, e = 0 .. 3, as the codes come.
+    uint32_t qb[X][NI][4];
+    float qs[X][2], qsum[X][NG][2];  // of heads 8 x + 2 t + h: units of its logits, sums over the groups
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+        const int head = 8 * x + g;
+        const uint16_t* q = static_cast<const uint16_t*>(p.q) + ((int64_t)s * p.H + (int64_t)kvh * p.G + head) * D + 8 * t;
+        float f[NI][8], unit = 1.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const uint4 raw = head < p.G ? __ldg(reinterpret_cast<const uint4*>(q + 32 * i)) : make_uint4(0u, 0u, 0u, 0u);
+            pkv::unpack8<E>(raw, f[i]);
+        }
+        if (!kHalf) {
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[i][e]));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+            // the power of two at or below the largest, and its inverse: both normal numbers
+            const uint32_t ex = min(max(__float_as_uint(top) & 0x7f800000u, 0x00800000u), 0x7e800000u);
+            const float down = __uint_as_float((254u << 23) - ex);
+            unit = __uint_as_float(ex);
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[i][e] *= down;
+        }
+        float part[NG];
+#pragma unroll
+        for (int r = 0; r < NG; ++r) part[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                qb[x][i][e] = pkv::F16::from_float2(f[i][e], f[i][e + 4]);
+                const float2 back = pkv::F16::to_float2(qb[x][i][e]);
+                part[i / 2] += back.x + back.y;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < NG; ++r) {
+            part[r] += __shfl_xor_sync(kFull, part[r], 1);
+            part[r] += __shfl_xor_sync(kFull, part[r], 2);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // head 2 t + h is in lanes 4 (2 t + h) ..
+            qs[x][h] = __shfl_sync(kFull, unit, 4 * (2 * t + h)) * p.qscale;
+#pragma unroll
+            for (int r = 0; r < NG; ++r) qsum[x][r][h] = __shfl_sync(kFull, part[r], 4 * (2 * t + h));
+        }
+    }
+
+    float centres[X][NG][2];  // sum of p times V's centres, this lane's tokens
+#pragma unroll
+    for (int x = 0; x < X; ++x)
+#pragma unroll
+        for (int r = 0; r < NG; ++r) centres[x][r][0] = centres[x][r][1] = 0.f;
+    float wu = 0.f;           // units of the weights: kUnits / 2^E; 0: no step seen yet
+    float step_most = 0.f;    // 2^(E + 1)
+
+    // this lane's address in ldmatrix: matrix lane / 8, row lane % 8; x4 is two
+    // chunks of two units
+    const int mrow = lane & 7, munit = (lane >> 3) & 1, mchunk = lane >> 4;
+    uint32_t at[NG];
+#pragma unroll
+    for (int r = 0; r < NG; ++r)
+        at[r] = munit * UB + mrow * q4::code_bytes(D) + 16 * q4::chunk_place<D>(mrow, 2 * r + mchunk);
+    const uint32_t pair_at = UC + g * q4::pair_bytes(D);
+
+    for (int i = first; i < te; i += feed.step) {
+        feed.push(Feed<D>::NST - 1);
+        const unsigned rows = feed.mask[0] >> g;  // bit 8 u: token 8 u + g
+        const uint32_t sk = feed.ring + feed.from * 2 * kTileBytes<D>, sv = sk + kTileBytes<D>;
+        feed.wait();
+
+        // z[x][sub][c]: token 16 sub + 8 (c / 2) + g, head 8 x + 2 t + c % 2
+        float z[X][SUB][4];
+#pragma unroll
+        for (int sub = 0; sub < SUB; ++sub) {
+            const uint32_t ku = sk + 2 * sub * UB;
+            float dot[X][NG][4];
+#pragma unroll
+            for (int x = 0; x < X; ++x)
+#pragma unroll
+                for (int r = 0; r < NG; ++r) dot[x][r][0] = dot[x][r][1] = dot[x][r][2] = dot[x][r][3] = 0.f;
+#pragma unroll
+            for (int r = 0; r < NG; ++r) {
+                uint32_t k[4], h0[4], h1[4];
+                ldsm_x4(k, ku + at[r]);  // chunks 2 r, 2 r + 1
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    codes_of(k[2 * c], h0);      // token g
+                    codes_of(k[2 * c + 1], h1);  // token g + 8
+                    const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
+#pragma unroll
+                    for (int x = 0; x < X; ++x) {
+                        pkv::Mma<pkv::F16>::run(dot[x][r], a0, qb[x][2 * r + c][0], qb[x][2 * r + c][1]);
+                        pkv::Mma<pkv::F16>::run(dot[x][r], a1, qb[x][2 * r + c][2], qb[x][2 * r + c][3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t pair[NG];
+                pairs_at<NG>(ku + u * UB + pair_at, pair);
+#pragma unroll
+                for (int x = 0; x < X; ++x)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float v = 0.f;
+#pragma unroll
+                        for (int r = 0; r < NG; ++r) {
+                            const float2 sc = E::to_float2(pair[r]);
+                            v = fmaf(sc.x, dot[x][r][2 * u + h], v);
+                            v = fmaf(sc.y, qsum[x][r][h], v);
+                        }
+                        z[x][sub][2 * u + h] = v * qs[x][h];
+                    }
+            }
+        }
+        // V's steps and centres
+        uint32_t vpair[SUB][2][NG];
+#pragma unroll
+        for (int sub = 0; sub < SUB; ++sub)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) pairs_at<NG>(sv + (2 * sub + u) * UB + pair_at, vpair[sub][u]);
+        if (feed.mask[0] != kFull) {  // nothing where there is no token
+#pragma unroll
+            for (int sub = 0; sub < SUB; ++sub)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (!((rows >> (16 * sub + 8 * u)) & 1u)) {
+#pragma unroll
+                        for (int x = 0; x < X; ++x) z[x][sub][2 * u] = z[x][sub][2 * u + 1] = -INFINITY;
+#pragma unroll
+                        for (int r = 0; r < NG; ++r) vpair[sub][u][r] = 0u;
+                    }
+        }
+
+        // does a maximum move?
+        float most = 0.f;
+#pragma unroll
+        for (int sub = 0; sub < SUB; ++sub)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int r = 0; r < NG; ++r) most = fmaxf(most, E::to_float2(vpair[sub][u][r]).x);
+        float top[X][2];
+        bool moves = most >= step_most && most > 0.f;
+#pragma unroll
+        for (int x = 0; x < X; ++x)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v = fmaxf(z[x][0][h], z[x][0][2 + h]);
+#pragma unroll
+                for (int sub = 1; sub < SUB; ++sub) v = fmaxf(v, fmaxf(z[x][sub][h], z[x][sub][2 + h]));
+                top[x][h] = v;
+                moves = moves || v > a.m[x][h] + kLazy;
+            }
+        if (__any_sync(kFull, moves)) {
+            most = max_rows(most);
+            float fewer = 1.f;
+            if (most >= step_most && most > 0.f) {  // the same for the whole warp
+                const uint32_t ex = min(max(__float_as_uint(most) & 0x7f800000u, 0x08000000u), 0x7e800000u);
+                const float now = kUnits * __uint_as_float((254u << 23) - ex);
+                fewer = wu > 0.f ? now / wu : 1.f;
+                wu = now;
+                step_most = __uint_as_float(ex + 0x00800000u);
+            }
+#pragma unroll
+            for (int x = 0; x < X; ++x)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float v = fmaxf(max_rows(top[x][h]), a.m[x][h]);
+                    const float old = v == -INFINITY ? 1.f : exp2_of(a.m[x][h] - v);
+                    a.m[x][h] = v;
+                    a.l[x][h] *= old;
+#pragma unroll
+                    for (int r = 0; r < NG; ++r) centres[x][r][h] *= old;
+#pragma unroll
+                    for (int c = 0; c < NI; ++c)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) a.at(x, c, e, h) *= old * fewer;
+                }
+        }
+
+#pragma unroll
+        for (int sub = 0; sub < SUB; ++sub) {
+            // the weights times V's steps, as columns
+            uint32_t pb[X][NG][2];
+#pragma unroll
+            for (int x = 0; x < X; ++x)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float w[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float use = a.m[x][h] == -INFINITY ? 0.f : a.m[x][h];
+                        w[h] = exp2_of(z[x][sub][2 * u + h] - use);
+                        a.l[x][h] += w[h];
+                    }
+#pragma unroll
+                    for (int r = 0; r < NG; ++r) {
+                        const float2 sc = E::to_float2(vpair[sub][u][r]);
+                        const float su = sc.x * wu;
+                        centres[x][r][0] = fmaf(w[0], sc.y, centres[x][r][0]);
+                        centres[x][r][1] = fmaf(w[1], sc.y, centres[x][r][1]);
+                        pb[x][r][u] = transposed(pkv::F16::from_float2(w[0] * su, w[1] * su));
+                    }
+                }
+            const uint32_t vu = sv + 2 * sub * UB;
+#pragma unroll
+            for (int r = 0; r < NG; ++r) {
+                uint32_t v[4], h0[4], h1[4];
+                ldsm_x4_trans(v, vu + at[r]);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    codes_of(v[2 * c], h0);      // tokens 2 t, 2 t + 1
+                    codes_of(v[2 * c + 1], h1);  // and 8 more
+                    const uint32_t a0[4] = {h0[0], h0[1], h1[0], h1[1]}, a1[4] = {h0[2], h0[3], h1[2], h1[3]};
+#pragma unroll
+                    for (int x = 0; x < X; ++x) {
+                        pkv::Mma<pkv::F16>::run(a.o[x][2 * r + c][0], a0, pb[x][r][0], pb[x][r][1]);
+                        pkv::Mma<pkv::F16>::run(a.o[x][2 * r + c][1], a1, pb[x][r][0], pb[x][r][1]);
+                    }
+                }
+            }
+        }
+        feed.done();
+    }
+    const float back = wu > 0.f ? 1.f / wu : 0.f;  // a power of two
+#pragma unroll
+    for (int x = 0; x < X; ++x)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            a.l[x][h] = sum_rows(a.l[x][h]);
+#pragma unroll
+            for (int r = 0; r < NG; ++r) {
+                const float c = sum_rows(centres[x][r][h]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a.at(x, 2 * r + k, e, h) = fmaf(a.at(x, 2 * r + k, e, h), back, c);
+            }
+        }
+}
+
+// A warp's part of its unit in shared memory: rows [16][D], m and l.
+template <int D>
+struct Part {
+    float o[kMaxGroup][D];
+    float m[kMaxGroup], l[kMaxGroup];
+};
+static_assert(sizeof(Part<128>) <= kRingBytes<128> && sizeof(Part<64>) <= kRingBytes<64>, "a part takes its warp's ring");
+
+template <int D, int X>
+__device__ __forceinline__ void put_part(Part<D>* to, int lane, Acc<D, X>& a) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int x = 0; x < X; ++x)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = 8 * x + 2 * t + h;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+                *reinterpret_cast<float4*>(&to->o[row][32 * i + 4 * g]) =
+                    make_float4(a.at(x, i, 0, h), a.at(x, i, 1, h), a.at(x, i, 2, h), a.at(x, i, 3, h));
+            if (g == 0) {
+                to->m[row] = a.m[x][h];
+                to->l[row] = a.l[x][h];
+            }
+        }
+}
+
+// The weights 2^(m - M) of a row's parts from the CTA's warps w0, w0 + step, ...,
+// its M and L.
+template <int D>
+__device__ __forceinline__ float row_weights(const char* smem, int w0, int step, int row, float (&w)[kWarps], float& L) {
+    float l[kWarps];
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        const bool in = w0 + i * step < kWarps;
+        const Part<D>* part = reinterpret_cast<const Part<D>*>(smem + (in ? w0 + i * step : w0) * kRingBytes<D>);
+        w[i] = in ? part->m[row] : -INFINITY;
+        l[i] = in ? part->l[row] : 0.f;
+    }
+    float M = w[0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) M = fmaxf(M, w[i]);
+    const float use = M == -INFINITY ? 0.f : M;
+    L = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        w[i] = exp2f(w[i] - use);
+        L = fmaf(w[i], l[i], L);
+    }
+    return M;
+}
+
+// Four dims of a row out of those parts.
+template <int D>
+__device__ __forceinline__ float4 row_sum(const char* smem, int w0, int step, int row, int d, const float (&w)[kWarps]) {
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i)
+        if (w0 + i * step < kWarps) {
+            const Part<D>* part = reinterpret_cast<const Part<D>*>(smem + (w0 + i * step) * kRingBytes<D>);
+            const float4 v = *reinterpret_cast<const float4*>(&part->o[row][d]);
+            sum.x = fmaf(w[i], v.x, sum.x);
+            sum.y = fmaf(w[i], v.y, sum.y);
+            sum.z = fmaf(w[i], v.z, sum.z);
+            sum.w = fmaf(w[i], v.w, sum.w);
+        }
+    return sum;
+}
+
+// Joins the token splits of each head (split): split 0's warp ends up with the
+// whole.
+template <int D, int X>
+__device__ __forceinline__ void join_splits(const Params& p, char* smem, int warp, int lane, Acc<D, X>& a) {
+    const int g = lane >> 2, t = lane & 3;
+    __syncwarp();
+    put_part<D, X>(reinterpret_cast<Part<D>*>(smem + warp * kRingBytes<D>), lane, a);
+    __syncthreads();
+    if (warp < p.hw) {
+#pragma unroll
+        for (int x = 0; x < X; ++x)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = 8 * x + 2 * t + h;
+                float w[kWarps], L;
+                a.m[x][h] = row_weights<D>(smem, warp, p.hw, row, w, L);
+                a.l[x][h] = L;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const float4 v = row_sum<D>(smem, warp, p.hw, row, 32 * i + 4 * g, w);
+                    a.at(x, i, 0, h) = v.x;
+                    a.at(x, i, 1, h) = v.y;
+                    a.at(x, i, 2, h) = v.z;
+                    a.at(x, i, 3, h) = v.w;
+                }
+            }
+    }
+    // the rings are filled again, by the asynchronous copies, after this
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+}
+
+template <class E>
+__device__ __forceinline__ uint2 pack4(const float4& v, float f) {
+    return make_uint2(E::from_float2(v.x * f, v.y * f), E::from_float2(v.z * f, v.w * f));
+}
+
+// What the CTAs of a cluster send one another: 32 dims of a row ("segment") of
+// every CTA to the CTA that joins it, and every row's M and L to all.
+struct ClusterIn {
+    float o[kMaxGroup * 4 * 32];                 // [segment / CS][CTA][32]
+    float m[kMaxCluster][kMaxGroup], l[kMaxCluster][kMaxGroup];
+};
+
+// Direct: cluster c / cs takes unit c / cs (hw = 1), its CTAs equal parts of
+// the unit's tiles, their warps every fourth tile.
+template <class E, int D, bool kWide>
+__global__ void __launch_bounds__(kThreads, kCtas<D, kWide>) direct_kernel(const __grid_constant__ Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    constexpr int N = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, kvh = h / p.G;
-    int n = p.context_lens[s];
-    if (n < 0 || n > p.max_ctx) {
-        if (h == 0 && threadIdx.x == 0) pkv::report(p.err, PKV_DEVERR_CONTEXT);
-        n = n < 0 ? 0 : p.max_ctx;
-    }
-    const int64_t oh = ((int64_t)s * p.H + h) * D;
-    float q[N], o[N], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const float2 x = E::to_float2(*reinterpret_cast<const uint32_t*>(p.q + 2 * (oh + N * lane + i)));
-        q[i] = x.x;
-        q[i + 1] = x.y;
-        o[i] = o[i + 1] = 0.f;
-    }
-    for (int j = warp; j < n; j += kWarps) {
-        const int phys = p.block_tables[(int64_t)s * p.MB + (j >> p.bs_log2)];
-        if ((unsigned)phys >= (unsigned)p.NB) {
-            if (lane == 0) pkv::report(p.err, PKV_DEVERR_BLOCK_ID);
-            continue;
-        }
-        const int slot = (phys << p.bs_log2) | (j & ((1 << p.bs_log2) - 1));
-        const int64_t unit = q4::unit_at<D>(slot, kvh, p.Hkv, p.bs_log2);
-        float k[N], v[N], z = 0.f;
-        row_of<E, D>(p.k_cache + unit, slot & 7, lane, k);
-        row_of<E, D>(p.v_cache + unit, slot & 7, lane, v);
-#pragma unroll
-        for (int i = 0; i < N; ++i) z = fmaf(q[i], k[i], z);
-#pragma unroll
-        for (int x = 16; x >= 1; x >>= 1) z += __shfl_xor_sync(kFull, z, x);
-        z *= p.qscale;
-        const float m_new = fmaxf(m, z), use = m_new == -INFINITY ? 0.f : m_new;
-        const float old = exp2f(m - use), w = exp2f(z - use);
-        m = m_new;
-        l = fmaf(l, old, w);
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = fmaf(w, v[i], o[i] * old);
-    }
-    __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
-    s_m[warp] = m;
-    s_l[warp] = l;
-#pragma unroll
-    for (int i = 0; i < N; ++i) s_o[warp][N * lane + i] = o[i];
+    constexpr int X = kWide ? 2 : 1, SEGS = D / 32;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ ClusterIn in;
+    __shared__ __align__(8) unsigned long long full[kWarps][kStages];
+    __shared__ int abort;
+    if (p.cs > 1) cluster_arrive();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) abort = 0;
     __syncthreads();
-    if (warp != 0) return;
-    float M = s_m[0];
-    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
-    const float use = M == -INFINITY ? 0.f : M;
-    float L = 0.f, r[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-        const float x = exp2f(s_m[w] - use);
-        L = fmaf(x, s_l[w], L);
-#pragma unroll
-        for (int i = 0; i < N; ++i) r[i] = fmaf(x, s_o[w][N * lane + i], r[i]);
+    const int unit = blockIdx.x / p.cs, rank = blockIdx.x % p.cs;
+    const int s = unit / p.Hkv, kvh = unit % p.Hkv;
+    const int raw = __ldg(p.context_lens + s);
+    if ((raw < 0 || raw > p.max_ctx) && kvh == 0 && rank == 0 && tid == 0) pkv::report(p.err, PKV_DEVERR_CONTEXT);
+    const int n = context_of(p, s);
+    const int T = tiles_of(p, n), per = (T + p.cs - 1) / p.cs;
+    const int tb = min(T, rank * per), te = min(T, tb + per);
+
+    Feed<D> feed(p, nullptr, &abort, smem_of(smem) + warp * kRingBytes<D>, smem_of(&full[warp][0]), warp, lane, 0, kWarps);
+    Acc<D, X> a;
+    feed.begin(s, kvh, n, tb + warp, te, 0);
+    attend<E, D, X>(p, feed, s, kvh, tb + warp, te, lane, a);
+    __syncwarp();
+    put_part<D, X>(reinterpret_cast<Part<D>*>(smem + warp * kRingBytes<D>), lane, a);
+    __syncthreads();
+    uint16_t* out = static_cast<uint16_t*>(p.out) + ((int64_t)s * p.H + (int64_t)kvh * p.G) * D;
+    if (p.cs == 1) {
+        for (int k = tid; k < p.G * (D / 4); k += kThreads) {
+            const int row = k / (D / 4), d = k % (D / 4) * 4;
+            float w[kWarps], L;
+            row_weights<D>(smem, 0, 1, row, w, L);
+            *reinterpret_cast<uint2*>(out + row * D + d) = pack4<E>(row_sum<D>(smem, 0, 1, row, d, w), inverse_of(L));
+        }
+        return;
     }
-    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+    // every CTA sends its rows to the CTAs that join them, segment i to CTA i % CS
+    cg::cluster_group cluster = cg::this_cluster();
+    const int CS = (int)cluster.num_blocks();
+    cluster_wait();  // all CTAs run
+    for (int seg = warp; seg < p.G * SEGS; seg += kWarps) {
+        const int row = seg / SEGS, d = seg % SEGS * 32 + lane;
+        float w[kWarps], L, sum = 0.f;
+        const float M = row_weights<D>(smem, 0, 1, row, w, L);
 #pragma unroll
-    for (int i = 0; i < N; i += 2)
-        *reinterpret_cast<uint32_t*>(p.out + 2 * (oh + N * lane + i)) = E::from_float2(r[i] * inv, r[i + 1] * inv);
+        for (int i = 0; i < kWarps; ++i)
+            sum = fmaf(w[i], reinterpret_cast<const Part<D>*>(smem + i * kRingBytes<D>)->o[row][d], sum);
+        cluster.map_shared_rank(&in.o[0], seg % CS)[(seg / CS * CS + rank) * 32 + lane] = sum;
+        if (seg % SEGS == 0 && lane < CS) {
+            cluster.map_shared_rank(&in.m[rank][0], lane)[row] = M;
+            cluster.map_shared_rank(&in.l[rank][0], lane)[row] = L;
+        }
+    }
+    cluster_arrive();
+    cluster_wait();
+    for (int k = warp; k * CS + rank < p.G * SEGS; k += kWarps) {
+        const int seg = k * CS + rank, row = seg / SEGS;
+        const float m = lane < CS ? in.m[lane][row] : -INFINITY;
+        float M = m;
+#pragma unroll
+        for (int x = kMaxCluster / 2; x >= 1; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
+        M = __shfl_sync(kFull, M, 0);
+        const float w = lane < CS ? exp2f(m - (M == -INFINITY ? 0.f : M)) : 0.f;
+        float L = lane < CS ? w * in.l[lane][row] : 0.f;
+#pragma unroll
+        for (int x = kMaxCluster / 2; x >= 1; x >>= 1) L += __shfl_xor_sync(kFull, L, x);
+        const float inv = inverse_of(__shfl_sync(kFull, L, 0));
+        float o = 0.f;
+        for (int i = 0; i < CS; ++i) o = fmaf(__shfl_sync(kFull, w, i), in.o[(k * CS + i) * 32 + lane], o);
+        o *= inv;
+        const float next = __shfl_down_sync(kFull, o, 1);
+        if ((lane & 1) == 0)
+            *reinterpret_cast<uint32_t*>(out + row * D + seg % SEGS * 32 + lane) = E::from_float2(o, next);
+    }
 }
 
-constexpr int kMaxContext = INT32_MAX - 1024;
+// Split: range c = blockIdx.x, then whichever ranges this CTA can take.
+template <class E, int D, bool kWide>
+__global__ void __launch_bounds__(kThreads, kCtas<D, kWide>) split_kernel(const __grid_constant__ Params p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    extern __shared__ __align__(128) char smem[];
+    __shared__ Plan plan;
+    __shared__ __align__(8) unsigned long long full[kWarps][kStages];
+    constexpr int X = kWide ? 2 : 1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int hl = warp % p.hw, split = warp / p.hw;
+    make_plan(p, plan, tid);
+
+    Feed<D> feed(p, &plan, &plan.abort, smem_of(smem) + warp * kRingBytes<D>, smem_of(&full[warp][0]), warp, lane, hl,
+                 p.nsplit);
+    Range r = range_at(p, plan.before, plan.map, plan.map.of_cta(blockIdx.x), lane);
+    bool running = r.left > 0;  // the same for all warps of the CTA
+    if (running && feed.chained())
+        feed.begin(r.s, r.hb, r.n, r.tb, min(tiles_of(p, r.n), r.tb + r.left), r.left + r.tb);
+    int used = 0;  // ranges taken out of the queue
+    while (running) {
+        // one unit (or the part of it that lies in this range)
+        const int T = tiles_of(p, r.n);
+        const int te = min(T, r.tb + r.left);
+        const int kvh = r.hb * p.hw + hl;
+        const bool last = te - r.tb == r.left;  // of the range
+        Acc<D, X> a;
+        if (!feed.chained()) feed.begin(r.s, r.hb, r.n, r.tb + split, te, 0);
+        attend<E, D, X>(p, feed, r.s, kvh, r.tb + split, te, lane, a);
+        if (!feed.chained()) join_splits<D, X>(p, smem, warp, lane, a);
+        const bool whole = r.tb == 0 && te == T;
+        if (split == 0) {
+            // finished rows, or a piece
+            const int64_t piece = ((2 * (int64_t)r.c + (r.tb == 0 ? 1 : 0)) * p.hw + hl) * p.G;
+            const int64_t oh = (int64_t)r.s * p.H + (int64_t)kvh * p.G;
+#pragma unroll
+            for (int x = 0; x < X; ++x)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = 8 * x + 2 * t + h;
+                    if (row >= p.G) continue;
+                    const float inv = inverse_of(a.l[x][h]);
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        const float4 v = make_float4(a.at(x, i, 0, h), a.at(x, i, 1, h), a.at(x, i, 2, h), a.at(x, i, 3, h));
+                        const int d = 32 * i + 4 * g;
+                        if (whole)
+                            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (oh + row) * D + d) = pack4<E>(v, inv);
+                        else
+                            *reinterpret_cast<float4*>(p.part_acc + (piece + row) * D + d) = v;
+                    }
+                    if (!whole && g == 0) {
+                        p.part_m[piece + row] = a.m[x][h];
+                        p.part_l[piece + row] = a.l[x][h];
+                    }
+                }
+            if (warp == 0 && lane == 0 && r.tb == 0)
+                p.place[r.s * p.HB + r.hb] = make_int2(r.c, plan.map.of(r.unit0 + T - 1));
+        }
+        if (last) {  // the feed has gone on to the next range, if there is one
+            running = used < feed.pushed;
+            if (running) r = plan.queue[warp][used++ & 3];
+            __syncwarp();
+        } else {
+            r.left -= te - r.tb;
+            r.unit0 += T;
+            r.tb = 0;
+            if (++r.hb == p.HB) {
+                r.hb = 0;
+                r.n = context_of(p, ++r.s);
+            }
+        }
+    }
+}
+
+// After split_kernel: the rows of units that lie in several ranges, a warp per
+// row, or (`many`: units of many pieces) the warps of a CTA.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+
+template <class E, int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p, int many) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    constexpr int DPL = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = p.hw * p.G, joins = p.S * p.HB * rows;  // = S * H
+    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+    __shared__ __align__(16) float s_o[kJoinWarps][D];
+    const int first = many ? blockIdx.x : blockIdx.x + warp * gridDim.x;  // neighbouring rows go to different SMs
+    const int step = many ? gridDim.x : kJoinWarps * gridDim.x;
+    for (int i = first; i < joins; i += step) {
+        const int unit = i / rows;
+        const int2 at = p.place[unit];
+        if (pkv::pieces_of(at.x, at.y, p.ranges) < 2) continue;  // many: the same for the whole CTA
+        float M, L, o[DPL];
+        if (many) {
+            gather_row<D, 6>(p, at.x, at.x + warp, at.y, kJoinWarps, i % rows, lane, M, L, o);
+            if (lane == 0) {
+                s_m[warp] = M;
+                s_l[warp] = L;
+            }
+#pragma unroll
+            for (int j = 0; j < DPL; ++j) s_o[warp][lane * DPL + j] = o[j];
+            __syncthreads();
+            if (warp == 0)
+#pragma unroll
+                for (int w = 1; w < kJoinWarps; ++w) {
+                    const float m_new = fmaxf(M, s_m[w]);
+                    const float use = m_new == -INFINITY ? 0.f : m_new;
+                    const float wo = exp2f(M - use), wn = exp2f(s_m[w] - use);
+                    L = L * wo + s_l[w] * wn;
+                    M = m_new;
+#pragma unroll
+                    for (int j = 0; j < DPL; ++j) o[j] = fmaf(wn, s_o[w][lane * DPL + j], o[j] * wo);
+                }
+        } else {
+            gather_row<D, 2>(p, at.x, at.x, at.y, 1, i % rows, lane, M, L, o);
+        }
+        if (!many || warp == 0) {
+            const float inv = inverse_of(L);
+            const int64_t oh = (int64_t)(unit / p.HB) * p.H + (int64_t)(unit % p.HB) * rows + i % rows;
+            uint16_t* dst = static_cast<uint16_t*>(p.out) + oh * D + lane * DPL;
+#pragma unroll
+            for (int j = 0; j < DPL; j += 2)
+                *reinterpret_cast<uint32_t*>(dst + j) = E::from_float2(o[j] * inv, o[j + 1] * inv);
+        }
+        if (many) __syncthreads();  // the parts have been read
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+constexpr int kDirectTokens = 1024;  // per CTA of a direct call
+constexpr int kDirectWaves = 4;
+constexpr int kJoinCtasPerSm = 3;
+
+struct Layout {
+    size_t place, m, l, acc, total;
+};
+
+Layout layout_of(int S, int H, int Hkv, int D) {
+    const size_t rows = (size_t)2 * kMaxRanges * heads_per_cta(Hkv) * (H / Hkv);
+    Layout L;
+    size_t o = 0;
+    L.place = o; o = align256(o + (size_t)S * Hkv * sizeof(int2));
+    L.m = o;     o = align256(o + rows * sizeof(float));
+    L.l = o;     o = align256(o + rows * sizeof(float));
+    L.acc = o;   o = align256(o + rows * D * sizeof(float));
+    L.total = o;
+    return L;
+}
+
+template <class E, int D>
+KernelFn pick(bool direct, bool wide) {
+    if (direct) return wide ? direct_kernel<E, D, true> : direct_kernel<E, D, false>;
+    return wide ? split_kernel<E, D, true> : split_kernel<E, D, false>;
+}
+KernelFn pick(pkv_dtype dtype, int D, bool direct, bool wide) {
+    if (dtype == PKV_F16) return D == 128 ? pick<pkv::F16, 128>(direct, wide) : pick<pkv::F16, 64>(direct, wide);
+    return D == 128 ? pick<pkv::BF16, 128>(direct, wide) : pick<pkv::BF16, 64>(direct, wide);
+}
+void (*pick_join(pkv_dtype dtype, int D))(Params, int) {
+    if (dtype == PKV_F16) return D == 128 ? join_kernel<pkv::F16, 128> : join_kernel<pkv::F16, 64>;
+    return D == 128 ? join_kernel<pkv::BF16, 128> : join_kernel<pkv::BF16, 64>;
+}
 
 bool workspace_args_ok(int S, int H, int Hkv, int D) {
     return S >= 0 && H > 0 && Hkv > 0 && H % Hkv == 0 && H / Hkv <= kMaxGroup && (D == 64 || D == 128);
@@ -124,7 +935,7 @@ extern "C" {
 
 size_t pkv_decode_q4_workspace_size(int S, int H, int Hkv, int D) {
     if (!workspace_args_ok(S, H, Hkv, D)) return 0;
-    return 256;
+    return layout_of(S, H, Hkv, D).total;
 }
 
 pkv_status pkv_paged_attention_decode_q4(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -146,7 +957,7 @@ pkv_status pkv_paged_attention_decode_q4(void* out, const void* q, const void* k
     if (H / Hkv > kMaxGroup) return bad(PKV_ERR_UNSUPPORTED, "at most 16 query heads per KV head");
     if (!(scale == scale) || std::isinf(scale)) return bad(PKV_ERR_INVALID_ARG, "scale must be finite");
     if ((int64_t)NB * bs > INT32_MAX) return bad(PKV_ERR_INVALID_ARG, "NB * bs must fit 31 bits");
-    if (S > 32767 || (int64_t)S * H > INT32_MAX / 16)
+    if (S > 32767 || (int64_t)S * H > INT32_MAX / kMaxCluster)
         return bad(PKV_ERR_INVALID_ARG, "at most 32767 sequences, and 2^27 heads in all of them");
     const int64_t cap = (int64_t)MB * bs;
     const int64_t max_ctx = max_context_len == 0 ? (cap < kMaxContext ? cap : kMaxContext) : max_context_len;
@@ -159,13 +970,14 @@ pkv_status pkv_paged_attention_decode_q4(void* out, const void* q, const void* k
         return bad(PKV_ERR_INVALID_ARG, "token and cache pointers must be 16-byte aligned");
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return bad(PKV_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
-    if (workspace_bytes < pkv_decode_q4_workspace_size(S, H, Hkv, D))
-        return bad(PKV_ERR_WORKSPACE, "workspace too small");
-    Params p;
-    p.out = static_cast<char*>(out);
-    p.q = static_cast<const char*>(q);
-    p.k_cache = static_cast<const char*>(k_cache);
-    p.v_cache = static_cast<const char*>(v_cache);
+    const Layout L = layout_of(S, H, Hkv, D);
+    if (workspace_bytes < L.total) return bad(PKV_ERR_WORKSPACE, "workspace too small");
+
+    Params p = {};
+    p.out = out;
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
     p.block_tables = block_tables;
     p.context_lens = context_lens;
     p.S = S;
@@ -176,20 +988,64 @@ pkv_status pkv_paged_attention_decode_q4(void* out, const void* q, const void* k
     p.MB = MB;
     p.bs_log2 = bs == 8 ? 3 : (bs == 16 ? 4 : (bs == 32 ? 5 : 6));
     p.max_ctx = (int)max_ctx;
+    p.window = INT32_MAX;  // every token is visible
+    p.sinks = 0;
     p.qscale = scale * kLog2e;
+    char* w = static_cast<char*>(workspace);
+    p.place = reinterpret_cast<int2*>(w + L.place);
+    p.part_m = reinterpret_cast<float*>(w + L.m);
+    p.part_l = reinterpret_cast<float*>(w + L.l);
+    p.part_acc = reinterpret_cast<float*>(w + L.acc);
     p.err = pkv::device_error_word();
-    void (*fn)(Params) = dtype == PKV_F16 ? (D == 128 ? attend_kernel<pkv::F16, 128> : attend_kernel<pkv::F16, 64>)
-                                          : (D == 128 ? attend_kernel<pkv::BF16, 128> : attend_kernel<pkv::BF16, 64>);
-    cudaLaunchAttribute attr[1];
+    p.tile_log2 = 5;
+    const bool wide = p.G > 8;
+    const int smem = D == 128 ? kSmemBytes<128> : kSmemBytes<64>;
+    const int sms = pkv::sm_count();
+    const KernelFn direct_fn = pick(dtype, D, true, wide), split_fn = pick(dtype, D, false, wide);
+    const int per_sm = resident_of(split_fn, smem), direct_sm = resident_of(direct_fn, smem);
+    if (per_sm < 1 || direct_sm < 1) return bad(PKV_ERR_CUDA, "the kernel cannot be resident");
+    // direct: the smallest cluster that leaves kDirectTokens per CTA; more CTAs
+    // while they still fit the card at once and have two tiles per warp
+    const int64_t slots = (int64_t)direct_sm * sms;
+    p.cs = 1;
+    while (p.cs < kMaxCluster && max_ctx > (int64_t)kDirectTokens * p.cs) p.cs *= 2;
+    const bool direct = max_ctx <= (int64_t)kDirectTokens * p.cs && (int64_t)S * Hkv * p.cs <= kDirectWaves * slots;
+    if (direct)
+        while (p.cs < kMaxCluster && (int64_t)S * Hkv * p.cs * 2 <= slots && max_ctx > (int64_t)2 * kWarps * kTile * p.cs)
+            p.cs *= 2;
+    p.hw = direct ? 1 : heads_per_cta(Hkv);
+    while (!direct && p.hw > 1 && (int64_t)S * Hkv / p.hw < kMinUnits) p.hw /= 2;
+    p.nsplit = kWarps / p.hw;
+    p.HB = Hkv / p.hw;
+    p.ranges0 = per_sm * sms;
+    if (p.ranges0 > kMaxRanges / (1 + kSmallRanges)) p.ranges0 = kMaxRanges / (1 + kSmallRanges);
+    const int64_t most_tiles = (int64_t)S * p.HB * ((max_ctx + kTile - 1) / kTile);
+    const bool share = p.nsplit == 1 && most_tiles / p.ranges0 * (16 - kLargeShare) / 16 / kSmallRanges >= kMinSmall;
+    p.ranges = share ? p.ranges0 * (1 + kSmallRanges) : p.ranges0;
+
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cs;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(S * H));
-    cfg.blockDim = dim3(32 * kWarps);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = pkv::as_stream(stream);
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p);
+    cfg.numAttrs = direct && p.cs > 1 ? 2 : 1;
+    cfg.gridDim = dim3(direct ? (unsigned)(S * Hkv * p.cs) : (unsigned)p.ranges);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, direct ? direct_fn : split_fn, p);
+    if (e == cudaSuccess && !direct) {
+        const int many = p.ranges > 8 * (int64_t)S * p.HB;  // units of more than 8 pieces
+        cfg.dynamicSmemBytes = 0;
+        cfg.numAttrs = 1;
+        cfg.blockDim = dim3(kJoinThreads);
+        cfg.gridDim = dim3((unsigned)(kJoinCtasPerSm * sms));
+        e = cudaLaunchKernelEx(&cfg, pick_join(dtype, D), p, many);
+    }
     return e == cudaSuccess ? PKV_OK : pkv::cuda_fail(e, "paged_attention_decode_q4 launch");
 }
 

@@ -48,7 +48,7 @@ CASES = [
     dict(S=2, H=3, Hkv=3, D=64, bs=16, dtype="bf16", new=[17, 4], R=48, pad=1),
     dict(S=2, H=3, Hkv=1, D=64, bs=16, dtype="bf16", new=[17, 4], R=32, interleaved=True, shift=1000),
     dict(S=2, H=7, Hkv=7, D=128, bs=8, dtype="f16", new=[5, 6], R=0, pad=2),
-    dict(S=1, H=100, Hkv=20, D=128, bs=16, dtype="bf16", new=[3], before=[100000], R=112, base=500000.0),
+    dict(S=1, H=100, Hkv=20, D=128, bs=16, dtype="bf16", new=[3], before=[30000], R=112, base=500000.0),
     dict(S=40, H=8, Hkv=2, D=64, bs=8, dtype="f16", new=[1] * 40, before=list(range(0, 80, 2))),
 ]
 
