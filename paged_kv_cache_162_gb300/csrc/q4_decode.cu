@@ -8,28 +8,32 @@
 // logit, and to the weight, of which each group of V has its own, p_j step_jr.
 //
 // Units, tiles, ranges and the two ways to spread them (direct, split) are
-// unit_ranges.cuh's.  A unit is one sequence and `hw` neighbouring KV heads, one
-// warp takes one head of a 32-token tile: 4 units of 8 tokens of K and of V, each
-// one asynchronous bulk copy into the warp's ring (a (block, head) is one run of
-// the pool), an mbarrier per stage.
+// unit_ranges.cuh's.  A unit is one sequence and `hw` neighbouring KV heads; one
+// warp takes one head, two 32-token tiles per stage of its ring: 8 runs of 8
+// tokens of K and of V, each one asynchronous bulk copy (a (block, head) is one
+// run of the pool) by a lane of its own, an mbarrier per stage.
 //
 // The products are m16n8k16 in fp16 with the cache as the 16 rows and the query
 // heads as the 8 columns, S^T = K Q^T and O^T = V^T P^T: a group of up to 8 query
 // heads fills them with half the products that heads as rows would take, and
 // accumulators of half the size (more than 8 heads: two column blocks).
+//  * Codes to fp16: a nibble at bits 0 or 4 of a half is, as a subnormal number,
+//    2^-24 or 2^-20 times the code: 5 instructions per 8 codes.  The 8 that a code
+//    is to lose comes off the sums: K's products start from -8 sum q; V's are
+//    corrected every 32 tokens by a product of the same weights with -8 (not at
+//    the end: sums that grow with the context would lose digits).
 //  * K: ldmatrix gives a lane 8 codes of one token, 32 bits; q is loaded in the
-//    order that makes of them two fragments.  q is 16-bit: bf16 is made fp16 by
-//    a power of two per head, exact but for elements below 2^-24 of the largest.
+//    order that makes of them two fragments.  A power of two per head makes q
+//    fp16 with the codes' units taken out, exact but for elements below 2^-32 of
+//    the largest.
 //  * V: transposing ldmatrix of 16-bit pieces, 4 codes of one token each, gives a
 //    lane 4 codes of two neighbouring tokens: the pairs that the product's k wants.
-//  * Codes to fp16: a nibble at bits 0 or 4 of a half under the exponent of 1024
-//    or 64 is that number + code; one subtraction takes it to -8 .. 7: 5 integer
-//    and 4 fp16 instructions per 8 codes.
-//  * P^T comes out of S^T's accumulators by movmatrix.  A weight times its step is
-//    rounded to fp16 once, 2^-11 of itself (the output's own rounding in fp16, an
-//    eighth of it in bf16).  Both factors are bounded by powers of two (2^kLazy, and
-//    the running maximum of the steps), and the units make 2^15 of their
-//    product: what falls below 2^-24 is 2^-39 of the largest.
+//  * P^T comes out of S^T's accumulators by movmatrix.  A weight times its step
+//    enters the product as fp16, rounded by 2^-11 of itself: an eighth of a bf16
+//    output's own rounding.  For fp16 outputs, whose rounding is no larger, what is
+//    left enters as a second number.  Both factors are bounded by powers of two
+//    (2^kLazy, and the running maximum of the steps), and the units make 2^15 of
+//    their product: what falls below 2^-24 is 2^-39 of the largest.
 //  * The running maximum moves only when a logit passes it by more than kLazy: one
 //    vote per tile instead of three exchanges per head.
 #include <cooperative_groups.h>
@@ -53,22 +57,39 @@ namespace q4 = pkv::q4;
 using pkv::ldsm_x4;
 using pkv::ldsm_x4_trans;
 
-constexpr int kTile = 32;  // tokens: a lane looks up one
-constexpr int kStages = 3;
+constexpr int kTile = 32;         // tokens of a pass through the softmax
+constexpr int kSpan = 2;          // tiles of a stage
+constexpr int kRuns = kSpan * kTile / q4::kUnit;  // runs of 8 tokens in it
+template <int D>
+constexpr int kStages = D == 128 ? 2 : 3;
 constexpr int kMaxRanges = 1824;  // CTAs of a split call
 constexpr float kLazy = 6.f;      // log2 of what a weight may pass 1 by
 constexpr float kUnits = 256.f;   // 2^(15 - 1 - kLazy): a step is below 2^(E + 1)
 
-// One tile's K (or V): 4 units.
+// K (or V) of one stage.
 template <int D>
-constexpr int kTileBytes = kTile / q4::kUnit * q4::kUnitBytes<D>;
+constexpr int kHalfBytes = kRuns * q4::kUnitBytes<D>;
 template <int D>
-constexpr int kRingBytes = kStages * 2 * kTileBytes<D>;  // one warp's ring
+constexpr int kRingBytes = kStages<D> * 2 * kHalfBytes<D>;  // one warp's ring
 template <int D>
 constexpr int kSmemBytes = kWarps * kRingBytes<D>;
 // CTAs per SM that the registers are for
-template <int D, bool kWide>
-constexpr int kCtas = kWide ? 2 : (D == 128 ? 3 : 4);
+template <int D, class C>
+constexpr int kCtas = C::X == 2 ? 2 : (D == 64 ? 4 : 3);
+
+// What the 8 columns of a product are: 8 query heads, or, for groups of up to 4,
+// (head, group of 64 dims): then one chain of products gives a logit's parts side
+// by side, one column block carries the weights of both groups, and a lane has
+// one head to take through the softmax instead of two.
+struct Narrow {
+    static constexpr bool kNarrow = true;
+    static constexpr int X = 1, HL = 1;  // column blocks, heads per lane and block
+};
+template <int kBlocks>
+struct Heads {
+    static constexpr bool kNarrow = false;
+    static constexpr int X = kBlocks, HL = 2;
+};
 
 __device__ __forceinline__ float exp2_of(float x) {
     float y;
@@ -83,19 +104,17 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     return y;
 }
 
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&x);
-}
-
-// The codes 4e and 16 + 4e bits up in x, e = 0..3, as pairs of fp16, minus 8.
+// The codes 4e and 16 + 4e bits up in x, e = 0..3, as pairs of fp16: times 2^-24
+// for even e, times 2^-20 for odd.
+constexpr float kEven = 0x1p-24f, kOdd = 0x1p-20f;
 __device__ __forceinline__ void codes_of(uint32_t x, uint32_t (&h)[4]) {
     const uint32_t y = x >> 8;
-    h[0] = hsub2((x & 0x000f000fu) | 0x64006400u, 0x64086408u);  // 1024 + c - 1032
-    h[1] = hsub2((x & 0x00f000f0u) | 0x54005400u, 0x54805480u);  // 64 + c - 72
-    h[2] = hsub2((y & 0x000f000fu) | 0x64006400u, 0x64086408u);
-    h[3] = hsub2((y & 0x00f000f0u) | 0x54005400u, 0x54805480u);
+    h[0] = x & 0x000f000fu;
+    h[1] = x & 0x00f000f0u;
+    h[2] = y & 0x000f000fu;
+    h[3] = y & 0x00f000f0u;
 }
+constexpr uint32_t kMinus8Even = 0x80088008u, kMinus8Odd = 0x80808080u;  // -8 in these units
 
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const char* src, int bytes, uint32_t bar, uint64_t policy) {
     asm volatile(
@@ -113,33 +132,41 @@ __device__ __forceinline__ void pairs_at(uint32_t from, uint32_t (&pair)[NG]) {
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(pair[0]) : "r"(from) : "memory");
 }
 
-// One warp's tiles on their way through its ring, `step` apart, each looked up
-// one tile ahead of its copies and copied kStages - 1 tiles ahead of its use.
-// With a plan and step 1 it goes on into the units and ranges that follow.
+// One warp's tiles on their way through its ring: stages of `span` tiles, `step`
+// tiles apart, each looked up one stage ahead of its copies and copied one less
+// than the ring has ahead of its use.  Chained (a plan, and all tiles are this
+// warp's) it goes on into the units and ranges that follow.
 template <int D>
 struct Feed {
-    static constexpr int NST = kStages;
+    static constexpr int NST = kStages<D>;
     static constexpr int UB = q4::kUnitBytes<D>;
     const Params& p;
     Plan* const plan;          // null: one unit (part) at a time
     int* const abort;
     const uint32_t ring, bars; // bars: an mbarrier per stage
     const int warp, lane, hl;  // hl: head of the CTA's hw that this warp takes
-    const int step;
-    int s, hb, n_next, i, te, left;  // the next tile to copy, and its unit; left: from its tile 0 to the range's end
+    const int span, step;
+    const bool chained;
+    const uint64_t policy;
+    const char* const cache;   // lanes 0..7 copy K's runs, 8..15 V's
+    int s, hb, n_next, i, te, left;  // the next stage's first tile, and its unit; left: from its tile 0 to the range's end
     int nv;
     const int32_t* bt;
-    int64_t src;               // first byte of the unit of 8 that its token `lane` is in
-    bool there, more;          // there: that token exists
-    unsigned mask[NST];        // tokens of the tiles in the ring
-    int into, from;            // stages of the next copy and of the oldest tile
+    int64_t src;               // first byte of the stage's run lane % 8
+    bool there, more;          // there: that run has tokens
+    int has[NST];              // of the stages in the ring: runs with tokens, and tokens << 8
+    int into, from;            // stages of the next copy and of the oldest one
     unsigned phase;            // bit st: parity of stage st's copy that is waited for next
     int asked, answers, pushed;
 
     __device__ __forceinline__ Feed(const Params& p_, Plan* plan_, int* abort_, uint32_t ring_, uint32_t bars_,
-                                    int warp_, int lane_, int hl_, int step_)
+                                    int warp_, int lane_, int hl_, int span_, int nsplit)
         : p(p_), plan(plan_), abort(abort_), ring(ring_), bars(bars_), warp(warp_), lane(lane_), hl(hl_),
-          step(step_), into(0), from(0), phase(0), asked(0), answers(0), pushed(0) {
+          span(span_), step(span_ * nsplit), chained(plan_ != nullptr && nsplit == 1),
+          // a split call streams more than it could find again in L2
+          policy(plan_ ? pkv::policy_evict_first() : pkv::policy_evict_normal()),
+          cache(static_cast<const char*>(lane_ < kRuns ? p_.k_cache : p_.v_cache)), into(0), from(0), phase(0),
+          asked(0), answers(0), pushed(0) {
         if (lane == 0)
             for (int st = 0; st < NST; ++st) tc_mbar_init(bars + 8 * st, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -155,17 +182,24 @@ struct Feed {
         if (lane * 128 < p.G * D * 2) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + lane * 128));
     }
 
+    // Tokens of the next stage.
+    __device__ __forceinline__ int tokens() const {
+        const int64_t end = min((int64_t)min(i + span, te) * kTile, (int64_t)nv);
+        return (int)max(end - (int64_t)i * kTile, (int64_t)0);
+    }
+
     __device__ __forceinline__ void lookup() {
         there = false;
-        const int64_t tok = (int64_t)i * kTile + lane;
-        if (!more || tok >= nv) return;
+        const int run = lane & (kRuns - 1);
+        if (!more || lane >= 2 * kRuns || run * q4::kUnit >= tokens()) return;
+        const int tok = i * kTile + run * q4::kUnit;
         const int phys = __ldg(bt + (tok >> p.bs_log2));
         if ((unsigned)phys >= (unsigned)p.NB) {
             pkv::report(p.err, PKV_DEVERR_BLOCK_ID);
             return;
         }
         there = true;
-        src = q4::unit_at<D>((phys << p.bs_log2) | ((int)tok & ((1 << p.bs_log2) - 1)), hb * p.hw + hl, p.Hkv, p.bs_log2);
+        src = q4::unit_at<D>((phys << p.bs_log2) | (tok & ((1 << p.bs_log2) - 1)), hb * p.hw + hl, p.Hkv, p.bs_log2);
     }
 
     __device__ __forceinline__ void begin(int s_, int hb_, int n, int first, int te_, int left_) {
@@ -174,7 +208,7 @@ struct Feed {
         i = first;
         te = te_;
         left = left_;
-        n_next = chained() && s + 1 < p.S ? context_of(p, s + 1) : 0;
+        n_next = chained && s + 1 < p.S ? context_of(p, s + 1) : 0;
         more = i < te;
         enter(n);
         lookup();
@@ -182,10 +216,8 @@ struct Feed {
         for (int st = 0; st < NST - 1; ++st) push(st);
     }
 
-    __device__ __forceinline__ bool chained() const { return plan != nullptr && step == 1; }
-
     __device__ __forceinline__ void maybe_ask(int tiles_left) {
-        if (warp == 0 && tiles_left <= 3 && asked == answers) {
+        if (warp == 0 && tiles_left <= 2 * kSpan && asked == answers) {
             if (lane == 0) ask_range(plan, asked);
             ++asked;
         }
@@ -199,48 +231,50 @@ struct Feed {
         return got;
     }
 
-    // Copies the next tile into the ring, its tokens' mask into mask[at], then
-    // looks up the one after it.
+    // Copies the next stage into the ring, what it has into has[at], then looks
+    // up the one after it.
     __device__ __forceinline__ void push(int at) {
-        mask[at] = __ballot_sync(kFull, there);
+        const unsigned runs = __ballot_sync(kFull, there) & ((1u << kRuns) - 1u);
         if (!more) return;
-        const uint32_t bar = bars + 8 * into, sk = ring + into * 2 * kTileBytes<D>, sv = sk + kTileBytes<D>;
+        has[at] = (int)runs | tokens() << 8;
+        const uint32_t bar = bars + 8 * into;
         if (lane == 0)
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
-                         "r"(__popc(mask[at] & 0x01010101u) * 2 * UB)
+                         "r"(__popc(runs) * 2 * UB)
                          : "memory");
         __syncwarp();
-        if (there && (lane & 7) == 0) {
-            const uint64_t policy = plan ? pkv::policy_evict_first() : pkv::policy_evict_normal();
-            bulk_copy(sk + (lane >> 3) * UB, static_cast<const char*>(p.k_cache) + src, UB, bar, policy);
-            bulk_copy(sv + (lane >> 3) * UB, static_cast<const char*>(p.v_cache) + src, UB, bar, policy);
-        }
+        if (there)  // lanes 0..15: K's runs, then V's
+            bulk_copy(ring + into * 2 * kHalfBytes<D> + lane * UB, cache + src, UB, bar, policy);
         into = into + 1 == NST ? 0 : into + 1;
         i += step;
         if (i >= te) advance();
-        if (more && chained()) maybe_ask(left - i);
+        if (more && chained) maybe_ask(left - i);
         lookup();
     }
 
-    // Waits for the oldest tile.
-    __device__ __forceinline__ void wait() {
-        if (!tc_mbar_wait(bars + 8 * from, phase >> from & 1u, abort)) {
+    __device__ __noinline__ void wait_on(uint32_t bar, uint32_t parity) {
+        if (!tc_mbar_wait(bar, parity, abort)) {
             pkv::report(p.err, PKV_DEVERR_TIMEOUT);
             *(volatile int*)abort = 1;
         }
+    }
+    // Waits for the oldest stage.
+    __device__ __forceinline__ void wait() {
+        const uint32_t bar = bars + 8 * from, parity = phase >> from & 1u;
+        if (!tc_mbar_try(bar, parity)) wait_on(bar, parity);
         __syncwarp();
     }
     __device__ __forceinline__ void done() {
         phase ^= 1u << from;
         from = from + 1 == NST ? 0 : from + 1;
 #pragma unroll
-        for (int st = 0; st < NST - 1; ++st) mask[st] = mask[st + 1];
+        for (int st = 0; st < NST - 1; ++st) has[st] = has[st + 1];
         __syncwarp();  // this stage is filled again by the next push
     }
 
     __device__ __forceinline__ void advance() {
         more = false;
-        if (!chained()) return;
+        if (!chained) return;
         left -= te;
         int n;
         if (left > 0) {  // the range's next unit
@@ -270,14 +304,16 @@ struct Feed {
     }
 };
 
-// What a warp has of its unit: lane (g, t) = (lane / 4, lane % 4) has, of the
-// heads 8 x + 2 t + h (x: column block, h = 0, 1), the dims 32 i + 4 g + e, and
-// the heads' m and l.
-template <int D, int X>
+// What a warp has of its unit: lane (g, t) = (lane / 4, lane % 4) has, of its
+// heads (head_of), the dims 32 i + 4 g + e, and the heads' m and l.
+template <int D, class C>
 struct Acc {
-    float o[X][D / 32][2][4];
-    float m[X][2], l[X][2];
-    __device__ __forceinline__ float& at(int x, int i, int e, int h) { return o[x][i][e >> 1][2 * (e & 1) + h]; }
+    float o[C::X][D / 32][2][4];
+    float m[C::X][C::HL], l[C::X][C::HL];
+    __device__ __forceinline__ float& at(int x, int i, int e, int h) {
+        return o[x][i][e >> 1][2 * (e & 1) + (C::kNarrow ? i / 2 : h)];
+    }
+    static __device__ __forceinline__ int head_of(int x, int t, int h) { return C::kNarrow ? t : 8 * x + 2 * t + h; }
 };
 
 // Sum over the lanes with the same t.
@@ -293,13 +329,16 @@ __device__ __forceinline__ float max_rows(float x) {
 }
 
 // One warp: KV head kvh of sequence s, its tiles first, first + step, ... below
-// te out of the feed.  X: blocks of 8 query heads.
-template <class E, int D, int X>
+// te out of the feed.
+template <class E, int D, class C>
 __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, int kvh, int first, int te, int lane,
-                                       Acc<D, X>& a) {
+                                       Acc<D, C>& a) {
     constexpr int NI = D / 32, NG = D / q4::kGroup, UB = q4::kUnitBytes<D>, UC = q4::kUnitCodes<D>;
-    constexpr int SUB = kTile / 16;
+    constexpr int SUB = kTile / 16, X = C::X, HL = C::HL;
+    constexpr int CH = C::kNarrow ? 1 : NG;  // chains of products of a logit, and columns of weights
     constexpr bool kHalf = std::is_same<E, pkv::F16>::value;
+    constexpr int PARTS = kHalf ? 2 : 1;     // numbers that make a weight
+    constexpr float kProduct = 0x1p-11f;     // of a code and the largest query elements' power of two
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int x = 0; x < X; ++x) {
@@ -307,52 +346,51 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
         for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) a.o[x][i][0][c] = a.o[x][i][1][c] = 0.f;
-        a.m[x][0] = a.m[x][1] = -INFINITY;
-        a.l[x][0] = a.l[x][1] = 0.f;
+#pragma unroll
+        for (int h = 0; h < HL; ++h) {
+            a.m[x][h] = -INFINITY;
+            a.l[x][h] = 0.f;
+        }
     }
     if (first >= te) return;
 
-    // The queries as columns: lane (g, t) has head 8 x + g, and of chunk i the
+    // The queries as columns: lane (g, t) has column g's head, and of chunk i the
     // dims 32 i + 8 t + e and + 4, e = 0 .. 3, as the codes come.
     uint32_t qb[X][NI][4];
-    float qs[X][2], qsum[X][NG][2];  // of heads 8 x + 2 t + h: units of its logits, sums over the groups
+    float qs[X][HL], qsum[X][NG][HL];  // of the lane's heads: units of its logits, sums over the groups
 #pragma unroll
     for (int x = 0; x < X; ++x) {
-        const int head = 8 * x + g;
+        const int head = C::kNarrow ? g >> 1 : 8 * x + g;
         const uint16_t* q = static_cast<const uint16_t*>(p.q) + ((int64_t)s * p.H + (int64_t)kvh * p.G + head) * D + 8 * t;
-        float f[NI][8], unit = 1.f;
+        float f[NI][8], top = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const uint4 raw = head < p.G ? __ldg(reinterpret_cast<const uint4*>(q + 32 * i)) : make_uint4(0u, 0u, 0u, 0u);
             pkv::unpack8<E>(raw, f[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[i][e]));
         }
-        if (!kHalf) {
-            float top = 0.f;
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[i][e]));
-            top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-            // the power of two at or below the largest, and its inverse: both normal numbers
-            const uint32_t ex = min(max(__float_as_uint(top) & 0x7f800000u, 0x00800000u), 0x7e800000u);
-            const float down = __uint_as_float((254u << 23) - ex);
-            unit = __uint_as_float(ex);
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[i][e] *= down;
-        }
-        float part[NG];
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+        // the power of two at or below the largest; its inverse times what the codes'
+        // units ask for makes the query fp16, below 2^14 (past 2^112 only bf16's
+        // last powers are left, and their logits' units would not be finite); a
+        // negative scale is the query's sign
+        const uint32_t ex = min(max(__float_as_uint(top) & 0x7f800000u, 0x08000000u), 0x77800000u);
+        const float unit = __uint_as_float(ex);
+        const float down = p.qscale < 0.f ? -__uint_as_float((254u << 23) - ex) : __uint_as_float((254u << 23) - ex);
+        float part[NG];  // sums over the groups, in units of the products'
 #pragma unroll
         for (int r = 0; r < NG; ++r) part[r] = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
+            const bool mine = !C::kNarrow || (g & 1) == i / 2;  // narrow: column g has group g % 2
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                qb[x][i][e] = pkv::F16::from_float2(f[i][e], f[i][e + 4]);
+                const float up = down * ((e & 1 ? 0x1p20f : 0x1p24f) * kProduct);
+                qb[x][i][e] = mine ? pkv::F16::from_float2(f[i][e] * up, f[i][e + 4] * up) : 0u;
                 const float2 back = pkv::F16::to_float2(qb[x][i][e]);
-                part[i / 2] += back.x + back.y;
+                part[i / 2] = fmaf(back.x + back.y, e & 1 ? kOdd : kEven, part[i / 2]);
             }
         }
 #pragma unroll
@@ -360,19 +398,26 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
             part[r] += __shfl_xor_sync(kFull, part[r], 1);
             part[r] += __shfl_xor_sync(kFull, part[r], 2);
         }
+        // column c is in lanes 4 c ..; no logit's unit is 0: nothing times -infinity
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // head 2 t + h is in lanes 4 (2 t + h) ..
-            qs[x][h] = __shfl_sync(kFull, unit, 4 * (2 * t + h)) * p.qscale;
+        for (int h = 0; h < HL; ++h) {
+            qs[x][h] = fmaxf(__shfl_sync(kFull, unit, 4 * (2 * t + h)) * (fabsf(p.qscale) * (1.f / kProduct)), 0x1p-126f);
 #pragma unroll
-            for (int r = 0; r < NG; ++r) qsum[x][r][h] = __shfl_sync(kFull, part[r], 4 * (2 * t + h));
+            for (int r = 0; r < NG; ++r)
+                qsum[x][r][h] = __shfl_sync(kFull, part[r], 4 * (2 * t + (C::kNarrow ? r : h)));
         }
     }
 
-    float centres[X][NG][2];  // sum of p times V's centres, this lane's tokens
+    float centres[X][NG][HL];  // sum of p times V's centres, this lane's tokens
+    float less[X][HL];         // -m, 0 for none yet
 #pragma unroll
     for (int x = 0; x < X; ++x)
 #pragma unroll
-        for (int r = 0; r < NG; ++r) centres[x][r][0] = centres[x][r][1] = 0.f;
+        for (int h = 0; h < HL; ++h) {
+            less[x][h] = 0.f;
+#pragma unroll
+            for (int r = 0; r < NG; ++r) centres[x][r][h] = 0.f;
+        }
     float wu = 0.f;           // units of the weights: kUnits / 2^E; 0: no step seen yet
     float step_most = 0.f;    // 2^(E + 1)
 
@@ -387,20 +432,35 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
 
     for (int i = first; i < te; i += feed.step) {
         feed.push(Feed<D>::NST - 1);
-        const unsigned rows = feed.mask[0] >> g;  // bit 8 u: token 8 u + g
-        const uint32_t sk = feed.ring + feed.from * 2 * kTileBytes<D>, sv = sk + kTileBytes<D>;
+        const int has = feed.has[0], count = has >> 8;
+        const uint32_t stage = feed.ring + feed.from * 2 * kHalfBytes<D>;
         feed.wait();
+#pragma unroll 1
+      for (int tile = 0; tile == 0 || tile * kTile < count; ++tile) {
+        const uint32_t sk = stage + tile * (kTile / q4::kUnit) * UB, sv = sk + kHalfBytes<D>;
+        // tokens 8 u + g of the tile, bit u
+        const int seen = count - tile * kTile - g;
+        unsigned rows = (unsigned)has >> (4 * tile) & 15u;
+        const bool some = rows != 15u || count < (tile + 1) * kTile;  // not all of the tile's tokens
+        if (some)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (8 * u >= seen) rows &= ~(1u << u);
 
-        // z[x][sub][c]: token 16 sub + 8 (c / 2) + g, head 8 x + 2 t + c % 2
-        float z[X][SUB][4];
+        // v[x][sub][u][h]: logit of token 16 sub + 8 u + g in units of qs
+        float v[X][SUB][2][HL];
 #pragma unroll
         for (int sub = 0; sub < SUB; ++sub) {
             const uint32_t ku = sk + 2 * sub * UB;
-            float dot[X][NG][4];
+            float dot[X][CH][4];  // element 2 u + h: column 2 t + h
 #pragma unroll
             for (int x = 0; x < X; ++x)
 #pragma unroll
-                for (int r = 0; r < NG; ++r) dot[x][r][0] = dot[x][r][1] = dot[x][r][2] = dot[x][r][3] = 0.f;
+                for (int r = 0; r < CH; ++r)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)  // the 8 that every code is to lose
+                        dot[x][r][h] = dot[x][r][2 + h] = C::kNarrow ? (h < NG ? -8.f * qsum[x][h][0] : 0.f)
+                                                                     : -8.f * qsum[x][r][h % HL];
 #pragma unroll
             for (int r = 0; r < NG; ++r) {
                 uint32_t k[4], h0[4], h1[4];
@@ -412,8 +472,8 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
                     const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
 #pragma unroll
                     for (int x = 0; x < X; ++x) {
-                        pkv::Mma<pkv::F16>::run(dot[x][r], a0, qb[x][2 * r + c][0], qb[x][2 * r + c][1]);
-                        pkv::Mma<pkv::F16>::run(dot[x][r], a1, qb[x][2 * r + c][2], qb[x][2 * r + c][3]);
+                        pkv::Mma<pkv::F16>::run(dot[x][r % CH], a0, qb[x][2 * r + c][0], qb[x][2 * r + c][1]);
+                        pkv::Mma<pkv::F16>::run(dot[x][r % CH], a1, qb[x][2 * r + c][2], qb[x][2 * r + c][3]);
                     }
                 }
             }
@@ -424,15 +484,15 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
 #pragma unroll
                 for (int x = 0; x < X; ++x)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float v = 0.f;
+                    for (int h = 0; h < HL; ++h) {
+                        float sum = 0.f;
 #pragma unroll
                         for (int r = 0; r < NG; ++r) {
                             const float2 sc = E::to_float2(pair[r]);
-                            v = fmaf(sc.x, dot[x][r][2 * u + h], v);
-                            v = fmaf(sc.y, qsum[x][r][h], v);
+                            sum = fmaf(sc.x, dot[x][r % CH][2 * u + (C::kNarrow ? r : h)], sum);
+                            sum = fmaf(sc.y, qsum[x][r][h], sum);
                         }
-                        z[x][sub][2 * u + h] = v * qs[x][h];
+                        v[x][sub][u][h] = sum;
                     }
             }
         }
@@ -442,14 +502,16 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
         for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
             for (int u = 0; u < 2; ++u) pairs_at<NG>(sv + (2 * sub + u) * UB + pair_at, vpair[sub][u]);
-        if (feed.mask[0] != kFull) {  // nothing where there is no token
+        if (some) {  // nothing where there is no token
 #pragma unroll
             for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
-                    if (!((rows >> (16 * sub + 8 * u)) & 1u)) {
+                    if (!((rows >> (2 * sub + u)) & 1u)) {
 #pragma unroll
-                        for (int x = 0; x < X; ++x) z[x][sub][2 * u] = z[x][sub][2 * u + 1] = -INFINITY;
+                        for (int x = 0; x < X; ++x)
+#pragma unroll
+                            for (int h = 0; h < HL; ++h) v[x][sub][u][h] = -INFINITY;
 #pragma unroll
                         for (int r = 0; r < NG; ++r) vpair[sub][u][r] = 0u;
                     }
@@ -463,17 +525,17 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int r = 0; r < NG; ++r) most = fmaxf(most, E::to_float2(vpair[sub][u][r]).x);
-        float top[X][2];
+        float top[X][HL];
         bool moves = most >= step_most && most > 0.f;
 #pragma unroll
         for (int x = 0; x < X; ++x)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float v = fmaxf(z[x][0][h], z[x][0][2 + h]);
+            for (int h = 0; h < HL; ++h) {
+                float y = fmaxf(v[x][0][0][h], v[x][0][1][h]);
 #pragma unroll
-                for (int sub = 1; sub < SUB; ++sub) v = fmaxf(v, fmaxf(z[x][sub][h], z[x][sub][2 + h]));
-                top[x][h] = v;
-                moves = moves || v > a.m[x][h] + kLazy;
+                for (int sub = 1; sub < SUB; ++sub) y = fmaxf(y, fmaxf(v[x][sub][0][h], v[x][sub][1][h]));
+                top[x][h] = y * qs[x][h];
+                moves = moves || top[x][h] > a.m[x][h] + kLazy;
             }
         if (__any_sync(kFull, moves)) {
             most = max_rows(most);
@@ -488,10 +550,11 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
 #pragma unroll
             for (int x = 0; x < X; ++x)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float v = fmaxf(max_rows(top[x][h]), a.m[x][h]);
-                    const float old = v == -INFINITY ? 1.f : exp2_of(a.m[x][h] - v);
-                    a.m[x][h] = v;
+                for (int h = 0; h < HL; ++h) {
+                    const float y = fmaxf(max_rows(top[x][h]), a.m[x][h]);
+                    const float old = y == -INFINITY ? 1.f : exp2_of(a.m[x][h] - y);
+                    a.m[x][h] = y;
+                    less[x][h] = y == -INFINITY ? 0.f : -y;
                     a.l[x][h] *= old;
 #pragma unroll
                     for (int r = 0; r < NG; ++r) centres[x][r][h] *= old;
@@ -502,55 +565,91 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
                 }
         }
 
+        float eight[X][CH][4];  // -8 times the columns' weights: rows of even e, of odd e
+#pragma unroll
+        for (int x = 0; x < X; ++x)
+#pragma unroll
+            for (int r = 0; r < CH; ++r) eight[x][r][0] = eight[x][r][1] = eight[x][r][2] = eight[x][r][3] = 0.f;
 #pragma unroll
         for (int sub = 0; sub < SUB; ++sub) {
             // the weights times V's steps, as columns
-            uint32_t pb[X][NG][2];
+            uint32_t pb[X][CH][PARTS][2];
 #pragma unroll
             for (int x = 0; x < X; ++x)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    float w[2];
+                    float w[HL];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float use = a.m[x][h] == -INFINITY ? 0.f : a.m[x][h];
-                        w[h] = exp2_of(z[x][sub][2 * u + h] - use);
+                    for (int h = 0; h < HL; ++h) {
+                        w[h] = exp2_of(fmaf(v[x][sub][u][h], qs[x][h], less[x][h]));
                         a.l[x][h] += w[h];
                     }
+                    float su[NG];
 #pragma unroll
                     for (int r = 0; r < NG; ++r) {
                         const float2 sc = E::to_float2(vpair[sub][u][r]);
-                        const float su = sc.x * wu;
-                        centres[x][r][0] = fmaf(w[0], sc.y, centres[x][r][0]);
-                        centres[x][r][1] = fmaf(w[1], sc.y, centres[x][r][1]);
-                        pb[x][r][u] = transposed(pkv::F16::from_float2(w[0] * su, w[1] * su));
+                        su[r] = sc.x * wu;
+#pragma unroll
+                        for (int h = 0; h < HL; ++h) centres[x][r][h] = fmaf(w[h], sc.y, centres[x][r][h]);
+                    }
+#pragma unroll
+                    for (int r = 0; r < CH; ++r) {
+                        const float w0 = w[0] * su[r];
+                        const float w1 = C::kNarrow ? (NG == 2 ? w[0] * su[NG - 1] : 0.f) : w[HL - 1] * su[r];
+                        const uint32_t hi = pkv::F16::from_float2(w0, w1);
+                        pb[x][r][0][u] = transposed(hi);
+                        if (PARTS == 2) {  // and what the rounding left
+                            const float2 back = pkv::F16::to_float2(hi);
+                            pb[x][r][PARTS - 1][u] = transposed(pkv::F16::from_float2(w0 - back.x, w1 - back.y));
+                        }
                     }
                 }
+            const uint32_t minus8[4] = {kMinus8Even, kMinus8Odd, kMinus8Even, kMinus8Odd};
+#pragma unroll
+            for (int x = 0; x < X; ++x)
+#pragma unroll
+                for (int r = 0; r < CH; ++r)
+#pragma unroll
+                    for (int y = 0; y < PARTS; ++y)
+                        pkv::Mma<pkv::F16>::run(eight[x][r], minus8, pb[x][r][y][0], pb[x][r][y][1]);
             const uint32_t vu = sv + 2 * sub * UB;
 #pragma unroll
             for (int r = 0; r < NG; ++r) {
-                uint32_t v[4], h0[4], h1[4];
-                ldsm_x4_trans(v, vu + at[r]);
+                uint32_t k[4], h0[4], h1[4];
+                ldsm_x4_trans(k, vu + at[r]);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    codes_of(v[2 * c], h0);      // tokens 2 t, 2 t + 1
-                    codes_of(v[2 * c + 1], h1);  // and 8 more
+                    codes_of(k[2 * c], h0);      // tokens 2 t, 2 t + 1
+                    codes_of(k[2 * c + 1], h1);  // and 8 more
                     const uint32_t a0[4] = {h0[0], h0[1], h1[0], h1[1]}, a1[4] = {h0[2], h0[3], h1[2], h1[3]};
 #pragma unroll
-                    for (int x = 0; x < X; ++x) {
-                        pkv::Mma<pkv::F16>::run(a.o[x][2 * r + c][0], a0, pb[x][r][0], pb[x][r][1]);
-                        pkv::Mma<pkv::F16>::run(a.o[x][2 * r + c][1], a1, pb[x][r][0], pb[x][r][1]);
-                    }
+                    for (int x = 0; x < X; ++x)
+#pragma unroll
+                        for (int y = 0; y < PARTS; ++y) {
+                            const uint32_t(&b)[2] = pb[x][r % CH][y];
+                            pkv::Mma<pkv::F16>::run(a.o[x][2 * r + c][0], a0, b[0], b[1]);
+                            pkv::Mma<pkv::F16>::run(a.o[x][2 * r + c][1], a1, b[0], b[1]);
+                        }
                 }
             }
         }
+#pragma unroll
+        for (int x = 0; x < X; ++x)
+#pragma unroll
+            for (int c = 0; c < NI; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int h = 0; h < HL; ++h)
+                        a.at(x, c, e, h) += eight[x][(c / 2) % CH][2 * (e & 1) + (C::kNarrow ? c / 2 : h)];
+      }
         feed.done();
     }
     const float back = wu > 0.f ? 1.f / wu : 0.f;  // a power of two
 #pragma unroll
     for (int x = 0; x < X; ++x)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < HL; ++h) {
             a.l[x][h] = sum_rows(a.l[x][h]);
 #pragma unroll
             for (int r = 0; r < NG; ++r) {
@@ -558,7 +657,7 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) a.at(x, 2 * r + k, e, h) = fmaf(a.at(x, 2 * r + k, e, h), back, c);
+                    for (int e = 0; e < 4; ++e) a.at(x, 2 * r + k, e, h) = fmaf(a.at(x, 2 * r + k, e, h), back * (e & 1 ? 0x1p20f : 0x1p24f), c);
             }
         }
 }
@@ -571,14 +670,14 @@ struct Part {
 };
 static_assert(sizeof(Part<128>) <= kRingBytes<128> && sizeof(Part<64>) <= kRingBytes<64>, "a part takes its warp's ring");
 
-template <int D, int X>
-__device__ __forceinline__ void put_part(Part<D>* to, int lane, Acc<D, X>& a) {
+template <int D, class C>
+__device__ __forceinline__ void put_part(Part<D>* to, int lane, Acc<D, C>& a) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int x = 0; x < X; ++x)
+    for (int x = 0; x < C::X; ++x)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int row = 8 * x + 2 * t + h;
+        for (int h = 0; h < C::HL; ++h) {
+            const int row = a.head_of(x, t, h);
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
                 *reinterpret_cast<float4*>(&to->o[row][32 * i + 4 * g]) =
@@ -634,18 +733,18 @@ __device__ __forceinline__ float4 row_sum(const char* smem, int w0, int step, in
 
 // Joins the token splits of each head (split): split 0's warp ends up with the
 // whole.
-template <int D, int X>
-__device__ __forceinline__ void join_splits(const Params& p, char* smem, int warp, int lane, Acc<D, X>& a) {
+template <int D, class C>
+__device__ __forceinline__ void join_splits(const Params& p, char* smem, int warp, int lane, Acc<D, C>& a) {
     const int g = lane >> 2, t = lane & 3;
     __syncwarp();
-    put_part<D, X>(reinterpret_cast<Part<D>*>(smem + warp * kRingBytes<D>), lane, a);
+    put_part<D, C>(reinterpret_cast<Part<D>*>(smem + warp * kRingBytes<D>), lane, a);
     __syncthreads();
     if (warp < p.hw) {
 #pragma unroll
-        for (int x = 0; x < X; ++x)
+        for (int x = 0; x < C::X; ++x)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = 8 * x + 2 * t + h;
+            for (int h = 0; h < C::HL; ++h) {
+                const int row = a.head_of(x, t, h);
                 float w[kWarps], L;
                 a.m[x][h] = row_weights<D>(smem, warp, p.hw, row, w, L);
                 a.l[x][h] = L;
@@ -678,14 +777,14 @@ struct ClusterIn {
 
 // Direct: cluster c / cs takes unit c / cs (hw = 1), its CTAs equal parts of
 // the unit's tiles, their warps every fourth tile.
-template <class E, int D, bool kWide>
-__global__ void __launch_bounds__(kThreads, kCtas<D, kWide>) direct_kernel(const __grid_constant__ Params p) {
+template <class E, int D, class C>
+__global__ void __launch_bounds__(kThreads, kCtas<D, C>) direct_kernel(const __grid_constant__ Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    constexpr int X = kWide ? 2 : 1, SEGS = D / 32;
+    constexpr int SEGS = D / 32;
     extern __shared__ __align__(128) char smem[];
     __shared__ ClusterIn in;
-    __shared__ __align__(8) unsigned long long full[kWarps][kStages];
+    __shared__ __align__(8) unsigned long long full[kWarps][kStages<D>];
     __shared__ int abort;
     if (p.cs > 1) cluster_arrive();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -699,12 +798,15 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, kWide>) direct_kernel(const
     const int T = tiles_of(p, n), per = (T + p.cs - 1) / p.cs;
     const int tb = min(T, rank * per), te = min(T, tb + per);
 
-    Feed<D> feed(p, nullptr, &abort, smem_of(smem) + warp * kRingBytes<D>, smem_of(&full[warp][0]), warp, lane, 0, kWarps);
-    Acc<D, X> a;
-    feed.begin(s, kvh, n, tb + warp, te, 0);
-    attend<E, D, X>(p, feed, s, kvh, tb + warp, te, lane, a);
+    // stages of one tile where two would leave warps without any
+    const int span = te - tb > kWarps ? kSpan : 1, first = tb + warp * span;
+    Feed<D> feed(p, nullptr, &abort, smem_of(smem) + warp * kRingBytes<D>, smem_of(&full[warp][0]), warp, lane, 0, span,
+                 kWarps);
+    Acc<D, C> a;
+    feed.begin(s, kvh, n, first, te, 0);
+    attend<E, D, C>(p, feed, s, kvh, first, te, lane, a);
     __syncwarp();
-    put_part<D, X>(reinterpret_cast<Part<D>*>(smem + warp * kRingBytes<D>), lane, a);
+    put_part<D, C>(reinterpret_cast<Part<D>*>(smem + warp * kRingBytes<D>), lane, a);
     __syncthreads();
     uint16_t* out = static_cast<uint16_t*>(p.out) + ((int64_t)s * p.H + (int64_t)kvh * p.G) * D;
     if (p.cs == 1) {
@@ -757,24 +859,23 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, kWide>) direct_kernel(const
 }
 
 // Split: range c = blockIdx.x, then whichever ranges this CTA can take.
-template <class E, int D, bool kWide>
-__global__ void __launch_bounds__(kThreads, kCtas<D, kWide>) split_kernel(const __grid_constant__ Params p) {
+template <class E, int D, class C>
+__global__ void __launch_bounds__(kThreads, kCtas<D, C>) split_kernel(const __grid_constant__ Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     extern __shared__ __align__(128) char smem[];
     __shared__ Plan plan;
-    __shared__ __align__(8) unsigned long long full[kWarps][kStages];
-    constexpr int X = kWide ? 2 : 1;
+    __shared__ __align__(8) unsigned long long full[kWarps][kStages<D>];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     const int hl = warp % p.hw, split = warp / p.hw;
     make_plan(p, plan, tid);
 
     Feed<D> feed(p, &plan, &plan.abort, smem_of(smem) + warp * kRingBytes<D>, smem_of(&full[warp][0]), warp, lane, hl,
-                 p.nsplit);
+                 kSpan, p.nsplit);
     Range r = range_at(p, plan.before, plan.map, plan.map.of_cta(blockIdx.x), lane);
     bool running = r.left > 0;  // the same for all warps of the CTA
-    if (running && feed.chained())
+    if (running && feed.chained)
         feed.begin(r.s, r.hb, r.n, r.tb, min(tiles_of(p, r.n), r.tb + r.left), r.left + r.tb);
     int used = 0;  // ranges taken out of the queue
     while (running) {
@@ -783,20 +884,21 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, kWide>) split_kernel(const 
         const int te = min(T, r.tb + r.left);
         const int kvh = r.hb * p.hw + hl;
         const bool last = te - r.tb == r.left;  // of the range
-        Acc<D, X> a;
-        if (!feed.chained()) feed.begin(r.s, r.hb, r.n, r.tb + split, te, 0);
-        attend<E, D, X>(p, feed, r.s, kvh, r.tb + split, te, lane, a);
-        if (!feed.chained()) join_splits<D, X>(p, smem, warp, lane, a);
+        Acc<D, C> a;
+        const int first = r.tb + kSpan * split;
+        if (!feed.chained) feed.begin(r.s, r.hb, r.n, first, te, 0);
+        attend<E, D, C>(p, feed, r.s, kvh, first, te, lane, a);
+        if (!feed.chained) join_splits<D, C>(p, smem, warp, lane, a);
         const bool whole = r.tb == 0 && te == T;
         if (split == 0) {
             // finished rows, or a piece
             const int64_t piece = ((2 * (int64_t)r.c + (r.tb == 0 ? 1 : 0)) * p.hw + hl) * p.G;
             const int64_t oh = (int64_t)r.s * p.H + (int64_t)kvh * p.G;
 #pragma unroll
-            for (int x = 0; x < X; ++x)
+            for (int x = 0; x < C::X; ++x)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int row = 8 * x + 2 * t + h;
+                for (int h = 0; h < C::HL; ++h) {
+                    const int row = a.head_of(x, t, h);
                     if (row >= p.G) continue;
                     const float inv = inverse_of(a.l[x][h]);
 #pragma unroll
@@ -912,13 +1014,14 @@ Layout layout_of(int S, int H, int Hkv, int D) {
 }
 
 template <class E, int D>
-KernelFn pick(bool direct, bool wide) {
-    if (direct) return wide ? direct_kernel<E, D, true> : direct_kernel<E, D, false>;
-    return wide ? split_kernel<E, D, true> : split_kernel<E, D, false>;
+KernelFn pick(bool direct, int G) {
+    if (G <= 4) return direct ? direct_kernel<E, D, Narrow> : split_kernel<E, D, Narrow>;
+    if (G <= 8) return direct ? direct_kernel<E, D, Heads<1>> : split_kernel<E, D, Heads<1>>;
+    return direct ? direct_kernel<E, D, Heads<2>> : split_kernel<E, D, Heads<2>>;
 }
-KernelFn pick(pkv_dtype dtype, int D, bool direct, bool wide) {
-    if (dtype == PKV_F16) return D == 128 ? pick<pkv::F16, 128>(direct, wide) : pick<pkv::F16, 64>(direct, wide);
-    return D == 128 ? pick<pkv::BF16, 128>(direct, wide) : pick<pkv::BF16, 64>(direct, wide);
+KernelFn pick(pkv_dtype dtype, int D, bool direct, int G) {
+    if (dtype == PKV_F16) return D == 128 ? pick<pkv::F16, 128>(direct, G) : pick<pkv::F16, 64>(direct, G);
+    return D == 128 ? pick<pkv::BF16, 128>(direct, G) : pick<pkv::BF16, 64>(direct, G);
 }
 void (*pick_join(pkv_dtype dtype, int D))(Params, int) {
     if (dtype == PKV_F16) return D == 128 ? join_kernel<pkv::F16, 128> : join_kernel<pkv::F16, 64>;
@@ -998,10 +1101,9 @@ pkv_status pkv_paged_attention_decode_q4(void* out, const void* q, const void* k
     p.part_acc = reinterpret_cast<float*>(w + L.acc);
     p.err = pkv::device_error_word();
     p.tile_log2 = 5;
-    const bool wide = p.G > 8;
     const int smem = D == 128 ? kSmemBytes<128> : kSmemBytes<64>;
     const int sms = pkv::sm_count();
-    const KernelFn direct_fn = pick(dtype, D, true, wide), split_fn = pick(dtype, D, false, wide);
+    const KernelFn direct_fn = pick(dtype, D, true, p.G), split_fn = pick(dtype, D, false, p.G);
     const int per_sm = resident_of(split_fn, smem), direct_sm = resident_of(direct_fn, smem);
     if (per_sm < 1 || direct_sm < 1) return bad(PKV_ERR_CUDA, "the kernel cannot be resident");
     // direct: the smallest cluster that leaves kDirectTokens per CTA; more CTAs

@@ -67,18 +67,20 @@ def attend_case(seed, S, H, Hkv, D, bs, dtype, lens, MB=None, spread=1.0):
 def attend_reference(c):
     """(out, bound) [S, H, D] in 64 bits.  The bound, with u = half a step of the
     output type and e = 2^-24:
-     * a logit z_j = scale sum_r (step_r sum_d q_d c_d + centre_r sum_d q_d): the
-       products are exact, the sums of 64 in fp32 with truncation, 2 e each, and
-       a few more roundings: 144 e Z, Z = scale max_j sum_d |q_d| (step |c_d| + |centre|);
-       a bf16 q as fp16 loses what is below 2^-24 of the head's largest: e Zq, Zq with
+     * a logit z_j = scale sum_r (step_r (sum_d q_d code_d - 8 sum_d q_d) + centre_r
+       sum_d q_d): the products are exact, the sums of 64 in fp32 with truncation, 2 e
+       each, partial sums at most sum_d |q_d| (|code_d - 8| + 16), and a few more
+       roundings: 144 e Z, Z = scale max_j sum_d |q_d| (step (|code_d - 8| + 16) + |centre|);
+       a q as fp16 loses what is below 2^-24 of the head's largest: e Zq, Zq with
        that largest for every q_d.  A weight errs by twice that (the maximum errs too)
        and 2^-22 of the exponential; the normaliser by as much; n / 8 sums per lane
        and n / 16 products' sums with 4 e each:
          w = 4 (144 e Z + e Zq) + 2^-21 + (n / 8 + 100) 4 e
-     * a weight times V's step is rounded to fp16: 2^-11 relative, or 2^-33 of the
-       largest step where it is below 2^-14 in units of 2^-8 (at most 8 codes up).
-       With A = sum_j p_j (step_j |c_j| + |centre_j|):
-         |out - ref| <= u |ref| + (1 + u) (A (2^-11 + w) + n 2^-30 max step) + 2^-25"""
+     * a weight times V's step enters as one fp16 number (bf16 output: rounded by r =
+       2^-11) or as two (fp16: r = 2^-22), or 2^-33 of the largest step off where it
+       is below 2^-14 in units of 2^-8 (at most 8 codes up).
+       With A = sum_j p_j (step_j |code_j - 8| + |centre_j|), A' the same with 16 more codes:
+         |out - ref| <= u |ref| + (1 + u) (A r + A' w + n 2^-30 max step) + 2^-25"""
     S, H, Hkv, D, bs, dtype = (c[x] for x in ("S", "H", "Hkv", "D", "bs", "dtype"))
     G, u = H // Hkv, U[dtype]
     out, bound = np.zeros((S, H, D)), np.zeros((S, H, D))
@@ -97,7 +99,8 @@ def attend_reference(c):
         rows = c["tables"][i, pos // bs].astype(np.int64) * bs + pos % bs
         (ks, ka, kc), (vs, va, vc) = (tuple(y[rows].transpose(1, 0, 2) for y in x) for x in kv)
         k, v = ka + ks * kc, va + vs * vc
-        kmag, vmag = np.abs(ka) + ks * np.abs(kc), np.abs(va) + vs * np.abs(vc)
+        kmag, vmag = np.abs(ka) + ks * (np.abs(kc) + 16), np.abs(va) + vs * np.abs(vc)
+        r16 = 2.0 ** -22 if dtype == "f16" else 2.0 ** -11
         qq = q[i].reshape(Hkv, G, D)
         z = c["scale"] * (qq @ k.transpose(0, 2, 1))
         p = np.exp(z - z.max(-1, keepdims=True))
@@ -105,8 +108,8 @@ def attend_reference(c):
         Z = abs(c["scale"]) * (np.abs(qq) @ kmag.transpose(0, 2, 1)).max(-1)
         Zq = abs(c["scale"]) * (np.abs(qq).max(-1) * kmag.sum(-1).max(-1)[:, None])
         w = 4 * (144 * E32 * Z + E32 * Zq) + 2.0 ** -21 + (n / 8 + 100) * 4 * E32
-        A, r = p @ vmag, p @ v
-        b = u * np.abs(r) + (1 + u) * (A * (2.0 ** -11 + w[..., None]) + n * 2.0 ** -30 * vs.max()) + 2.0 ** -25
+        A, A16, r = p @ vmag, p @ (vmag + 16 * vs), p @ v
+        b = u * np.abs(r) + (1 + u) * (A * r16 + A16 * w[..., None] + n * 2.0 ** -30 * vs.max()) + 2.0 ** -25
         out[i], bound[i] = r.reshape(H, D), b.reshape(H, D)
     return out, bound
 
