@@ -71,12 +71,6 @@ template <int D>
 constexpr int kHalfBytes = kRuns * q4::kUnitBytes<D>;
 template <int D>
 constexpr int kRingBytes = kStages<D> * 2 * kHalfBytes<D>;  // one warp's ring
-template <int D>
-constexpr int kSmemBytes = kWarps * kRingBytes<D>;
-// CTAs per SM that the registers are for
-template <int D, class C>
-constexpr int kCtas = C::X == 2 ? 2 : (D == 64 ? 4 : 3);
-
 // What the 8 columns of a product are: 8 query heads, or, for groups of up to 4,
 // (head, group of 64 dims): then one chain of products gives a logit's parts side
 // by side, one column block carries the weights of both groups, and a lane has
@@ -90,6 +84,14 @@ struct Heads {
     static constexpr bool kNarrow = false;
     static constexpr int X = kBlocks, HL = 2;
 };
+
+// CTAs per SM that the registers are for
+template <int D, class C>
+constexpr int kCtas = C::X == 2 ? 2 : (D == 64 ? 4 : 3);
+
+// Warps of a direct call's CTAs: 4, or, for few units, as many as an SM takes.
+template <int D, class C>
+constexpr int kManyWarps = C::X == 2 ? 8 : (D == 128 ? 12 : 16);
 
 __device__ __forceinline__ float exp2_of(float x) {
     float y;
@@ -150,10 +152,10 @@ struct Feed {
     const uint64_t policy;
     const char* const cache;   // lanes 0..7 copy K's runs, 8..15 V's
     int s, hb, n_next, i, te, left;  // the next stage's first tile, and its unit; left: from its tile 0 to the range's end
-    int nv;
+    int rest, count;           // the unit's tokens from that tile on, the stage's tokens
     const int32_t* bt;
-    int64_t src;               // first byte of the stage's run lane % 8
-    bool there, more;          // there: that run has tokens
+    int tok, phys;             // of the stage's run lane % 8: first token, and its block (-1: no run)
+    bool more;
     int has[NST];              // of the stages in the ring: runs with tokens, and tokens << 8
     int into, from;            // stages of the next copy and of the oldest one
     unsigned phase;            // bit st: parity of stage st's copy that is waited for next
@@ -174,32 +176,22 @@ struct Feed {
         __syncwarp();
     }
 
-    __device__ __forceinline__ void enter(int n) {  // unit (s, hb)
-        nv = n;
+    __device__ __forceinline__ void enter(int n) {  // unit (s, hb), at its tile i
+        rest = n - i * kTile;
         bt = p.block_tables + (int64_t)s * p.MB;
         const char* q = static_cast<const char*>(p.q) +
                         ((int64_t)s * p.H + (int64_t)(hb * p.hw + hl) * p.G) * D * 2;
         if (lane * 128 < p.G * D * 2) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + lane * 128));
     }
 
-    // Tokens of the next stage.
-    __device__ __forceinline__ int tokens() const {
-        const int64_t end = min((int64_t)min(i + span, te) * kTile, (int64_t)nv);
-        return (int)max(end - (int64_t)i * kTile, (int64_t)0);
-    }
-
+    // The next stage's blocks; they are used when it is pushed.
     __device__ __forceinline__ void lookup() {
-        there = false;
-        const int run = lane & (kRuns - 1);
-        if (!more || lane >= 2 * kRuns || run * q4::kUnit >= tokens()) return;
-        const int tok = i * kTile + run * q4::kUnit;
-        const int phys = __ldg(bt + (tok >> p.bs_log2));
-        if ((unsigned)phys >= (unsigned)p.NB) {
-            pkv::report(p.err, PKV_DEVERR_BLOCK_ID);
-            return;
-        }
-        there = true;
-        src = q4::unit_at<D>((phys << p.bs_log2) | (tok & ((1 << p.bs_log2) - 1)), hb * p.hw + hl, p.Hkv, p.bs_log2);
+        phys = -1;
+        if (!more) return;
+        count = max(min(min(te - i, span) * kTile, rest), 0);
+        const int first = (lane & (kRuns - 1)) * q4::kUnit;
+        tok = i * kTile + first;
+        if (lane < 2 * kRuns && first < count) phys = __ldg(bt + (tok >> p.bs_log2)) & INT32_MAX;
     }
 
     __device__ __forceinline__ void begin(int s_, int hb_, int n, int first, int te_, int left_) {
@@ -210,6 +202,7 @@ struct Feed {
         left = left_;
         n_next = chained && s + 1 < p.S ? context_of(p, s + 1) : 0;
         more = i < te;
+        count = tok = 0;
         enter(n);
         lookup();
 #pragma unroll
@@ -234,19 +227,29 @@ struct Feed {
     // Copies the next stage into the ring, what it has into has[at], then looks
     // up the one after it.
     __device__ __forceinline__ void push(int at) {
-        const unsigned runs = __ballot_sync(kFull, there) & ((1u << kRuns) - 1u);
         if (!more) return;
-        has[at] = (int)runs | tokens() << 8;
+        const bool there = (unsigned)phys < (unsigned)p.NB;
+        if (!there && phys >= 0) pkv::report(p.err, PKV_DEVERR_BLOCK_ID);
+        const unsigned runs = __ballot_sync(kFull, there) & ((1u << kRuns) - 1u);
+        has[at] = (int)runs | count << 8;
         const uint32_t bar = bars + 8 * into;
         if (lane == 0)
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
                          "r"(__popc(runs) * 2 * UB)
                          : "memory");
         __syncwarp();
-        if (there)  // lanes 0..15: K's runs, then V's
-            bulk_copy(ring + into * 2 * kHalfBytes<D> + lane * UB, cache + src, UB, bar, policy);
+        // lanes 0..15: K's runs, then V's.  The runs of a block (of a tile at most: tiles
+        // are where blocks may end) are one piece.
+        const int units = p.bs_log2 - 3, whole = 1 << min(units, 2);
+        if (there && (lane & (whole - 1)) == 0) {
+            // the pool's units of 8 tokens fit an int (checked on the host)
+            const int unit = ((phys * p.Hkv + hb * p.hw + hl) << units) | ((tok >> 3) & ((1 << units) - 1));
+            const int n = min(whole, (count - (lane & (kRuns - 1)) * q4::kUnit + q4::kUnit - 1) / q4::kUnit);
+            bulk_copy(ring + into * 2 * kHalfBytes<D> + lane * UB, cache + (int64_t)unit * UB, n * UB, bar, policy);
+        }
         into = into + 1 == NST ? 0 : into + 1;
         i += step;
+        rest -= step * kTile;
         if (i >= te) advance();
         if (more && chained) maybe_ask(left - i);
         lookup();
@@ -435,6 +438,11 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
         const int has = feed.has[0], count = has >> 8;
         const uint32_t stage = feed.ring + feed.from * 2 * kHalfBytes<D>;
         feed.wait();
+        float eight[X][CH][4];  // -8 times the stage's weights in the columns: rows of even e, of odd e
+#pragma unroll
+        for (int x = 0; x < X; ++x)
+#pragma unroll
+            for (int r = 0; r < CH; ++r) eight[x][r][0] = eight[x][r][1] = eight[x][r][2] = eight[x][r][3] = 0.f;
 #pragma unroll 1
       for (int tile = 0; tile == 0 || tile * kTile < count; ++tile) {
         const uint32_t sk = stage + tile * (kTile / q4::kUnit) * UB, sv = sk + kHalfBytes<D>;
@@ -448,39 +456,47 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
                 if (8 * u >= seen) rows &= ~(1u << u);
 
         // v[x][sub][u][h]: logit of token 16 sub + 8 u + g in units of qs
-        float v[X][SUB][2][HL];
+        float v[X][SUB][2][HL], dot[SUB][X][CH][4];  // dot: element 2 u + h is column 2 t + h
 #pragma unroll
-        for (int sub = 0; sub < SUB; ++sub) {
-            const uint32_t ku = sk + 2 * sub * UB;
-            float dot[X][CH][4];  // element 2 u + h: column 2 t + h
+        for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
             for (int x = 0; x < X; ++x)
 #pragma unroll
                 for (int r = 0; r < CH; ++r)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)  // the 8 that every code is to lose
-                        dot[x][r][h] = dot[x][r][2 + h] = C::kNarrow ? (h < NG ? -8.f * qsum[x][h][0] : 0.f)
-                                                                     : -8.f * qsum[x][r][h % HL];
+                        dot[sub][x][r][h] = dot[sub][x][r][2 + h] =
+                            C::kNarrow ? (h < NG ? -8.f * qsum[x][h % NG][0] : 0.f) : -8.f * qsum[x][r][h % HL];
 #pragma unroll
-            for (int r = 0; r < NG; ++r) {
-                uint32_t k[4], h0[4], h1[4];
-                ldsm_x4(k, ku + at[r]);  // chunks 2 r, 2 r + 1
+        for (int r = 0; r < NG; ++r) {
+            uint32_t k[SUB][4];  // chunks 2 r, 2 r + 1
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    codes_of(k[2 * c], h0);      // token g
-                    codes_of(k[2 * c + 1], h1);  // token g + 8
-                    const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
+            for (int sub = 0; sub < SUB; ++sub) ldsm_x4(k[sub], sk + at[r] + 2 * sub * UB);
 #pragma unroll
-                    for (int x = 0; x < X; ++x) {
-                        pkv::Mma<pkv::F16>::run(dot[x][r % CH], a0, qb[x][2 * r + c][0], qb[x][2 * r + c][1]);
-                        pkv::Mma<pkv::F16>::run(dot[x][r % CH], a1, qb[x][2 * r + c][2], qb[x][2 * r + c][3]);
-                    }
+            for (int c = 0; c < 2; ++c) {
+                uint32_t h0[SUB][4], h1[SUB][4];
+#pragma unroll
+                for (int sub = 0; sub < SUB; ++sub) {
+                    codes_of(k[sub][2 * c], h0[sub]);      // token g
+                    codes_of(k[sub][2 * c + 1], h1[sub]);  // token g + 8
                 }
+#pragma unroll
+                for (int e = 0; e < 4; e += 2)
+#pragma unroll
+                    for (int sub = 0; sub < SUB; ++sub) {
+                        const uint32_t f[4] = {h0[sub][e], h1[sub][e], h0[sub][e + 1], h1[sub][e + 1]};
+#pragma unroll
+                        for (int x = 0; x < X; ++x)
+                            pkv::Mma<pkv::F16>::run(dot[sub][x][r % CH], f, qb[x][2 * r + c][e], qb[x][2 * r + c][e + 1]);
+                    }
             }
+        }
+#pragma unroll
+        for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 uint32_t pair[NG];
-                pairs_at<NG>(ku + u * UB + pair_at, pair);
+                pairs_at<NG>(sk + pair_at + (2 * sub + u) * UB, pair);
 #pragma unroll
                 for (int x = 0; x < X; ++x)
 #pragma unroll
@@ -489,19 +505,18 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
 #pragma unroll
                         for (int r = 0; r < NG; ++r) {
                             const float2 sc = E::to_float2(pair[r]);
-                            sum = fmaf(sc.x, dot[x][r % CH][2 * u + (C::kNarrow ? r : h)], sum);
+                            sum = fmaf(sc.x, dot[sub][x][r % CH][2 * u + (C::kNarrow ? r : h)], sum);
                             sum = fmaf(sc.y, qsum[x][r][h], sum);
                         }
                         v[x][sub][u][h] = sum;
                     }
             }
-        }
         // V's steps and centres
         uint32_t vpair[SUB][2][NG];
 #pragma unroll
         for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) pairs_at<NG>(sv + (2 * sub + u) * UB + pair_at, vpair[sub][u]);
+            for (int u = 0; u < 2; ++u) pairs_at<NG>(sv + pair_at + (2 * sub + u) * UB, vpair[sub][u]);
         if (some) {  // nothing where there is no token
 #pragma unroll
             for (int sub = 0; sub < SUB; ++sub)
@@ -562,18 +577,18 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
                     for (int c = 0; c < NI; ++c)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) a.at(x, c, e, h) *= old * fewer;
+#pragma unroll
+                    for (int r = 0; r < CH; ++r)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (C::kNarrow || c % 2 == h) eight[x][r][c] *= old * fewer;
                 }
         }
 
-        float eight[X][CH][4];  // -8 times the columns' weights: rows of even e, of odd e
+        // the weights times V's steps, as columns
+        uint32_t pb[SUB][X][CH][PARTS][2];
 #pragma unroll
-        for (int x = 0; x < X; ++x)
-#pragma unroll
-            for (int r = 0; r < CH; ++r) eight[x][r][0] = eight[x][r][1] = eight[x][r][2] = eight[x][r][3] = 0.f;
-#pragma unroll
-        for (int sub = 0; sub < SUB; ++sub) {
-            // the weights times V's steps, as columns
-            uint32_t pb[X][CH][PARTS][2];
+        for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
             for (int x = 0; x < X; ++x)
 #pragma unroll
@@ -597,42 +612,46 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
                         const float w0 = w[0] * su[r];
                         const float w1 = C::kNarrow ? (NG == 2 ? w[0] * su[NG - 1] : 0.f) : w[HL - 1] * su[r];
                         const uint32_t hi = pkv::F16::from_float2(w0, w1);
-                        pb[x][r][0][u] = transposed(hi);
+                        pb[sub][x][r][0][u] = transposed(hi);
                         if (PARTS == 2) {  // and what the rounding left
                             const float2 back = pkv::F16::to_float2(hi);
-                            pb[x][r][PARTS - 1][u] = transposed(pkv::F16::from_float2(w0 - back.x, w1 - back.y));
+                            pb[sub][x][r][PARTS - 1][u] = transposed(pkv::F16::from_float2(w0 - back.x, w1 - back.y));
                         }
                     }
                 }
-            const uint32_t minus8[4] = {kMinus8Even, kMinus8Odd, kMinus8Even, kMinus8Odd};
+        const uint32_t minus8[4] = {kMinus8Even, kMinus8Odd, kMinus8Even, kMinus8Odd};
 #pragma unroll
-            for (int x = 0; x < X; ++x)
-#pragma unroll
-                for (int r = 0; r < CH; ++r)
-#pragma unroll
-                    for (int y = 0; y < PARTS; ++y)
-                        pkv::Mma<pkv::F16>::run(eight[x][r], minus8, pb[x][r][y][0], pb[x][r][y][1]);
-            const uint32_t vu = sv + 2 * sub * UB;
+        for (int sub = 0; sub < SUB; ++sub) {
 #pragma unroll
             for (int r = 0; r < NG; ++r) {
-                uint32_t k[4], h0[4], h1[4];
-                ldsm_x4_trans(k, vu + at[r]);
+                uint32_t k[4], f[4][4];
+                ldsm_x4_trans(k, sv + at[r] + 2 * sub * UB);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
+                    uint32_t h0[4], h1[4];
                     codes_of(k[2 * c], h0);      // tokens 2 t, 2 t + 1
                     codes_of(k[2 * c + 1], h1);  // and 8 more
-                    const uint32_t a0[4] = {h0[0], h0[1], h1[0], h1[1]}, a1[4] = {h0[2], h0[3], h1[2], h1[3]};
 #pragma unroll
-                    for (int x = 0; x < X; ++x)
-#pragma unroll
-                        for (int y = 0; y < PARTS; ++y) {
-                            const uint32_t(&b)[2] = pb[x][r % CH][y];
-                            pkv::Mma<pkv::F16>::run(a.o[x][2 * r + c][0], a0, b[0], b[1]);
-                            pkv::Mma<pkv::F16>::run(a.o[x][2 * r + c][1], a1, b[0], b[1]);
-                        }
+                    for (int e = 0; e < 2; ++e) {
+                        f[2 * c + e][0] = h0[2 * e];
+                        f[2 * c + e][1] = h0[2 * e + 1];
+                        f[2 * c + e][2] = h1[2 * e];
+                        f[2 * c + e][3] = h1[2 * e + 1];
+                    }
                 }
+#pragma unroll
+                for (int x = 0; x < X; ++x)
+#pragma unroll
+                    for (int y = 0; y < PARTS; ++y) {
+                        const uint32_t(&b)[2] = pb[sub][x][r % CH][y];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            pkv::Mma<pkv::F16>::run(a.o[x][2 * r + c / 2][c & 1], f[c], b[0], b[1]);
+                        if (r < CH) pkv::Mma<pkv::F16>::run(eight[x][r % CH], minus8, b[0], b[1]);
+                    }
             }
         }
+      }
 #pragma unroll
         for (int x = 0; x < X; ++x)
 #pragma unroll
@@ -642,7 +661,6 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
 #pragma unroll
                     for (int h = 0; h < HL; ++h)
                         a.at(x, c, e, h) += eight[x][(c / 2) % CH][2 * (e & 1) + (C::kNarrow ? c / 2 : h)];
-      }
         feed.done();
     }
     const float back = wu > 0.f ? 1.f / wu : 0.f;  // a power of two
@@ -689,25 +707,25 @@ __device__ __forceinline__ void put_part(Part<D>* to, int lane, Acc<D, C>& a) {
         }
 }
 
-// The weights 2^(m - M) of a row's parts from the CTA's warps w0, w0 + step, ...,
-// its M and L.
-template <int D>
-__device__ __forceinline__ float row_weights(const char* smem, int w0, int step, int row, float (&w)[kWarps], float& L) {
-    float l[kWarps];
+// The weights 2^(m - M) of a row's parts from the warps w0, w0 + step, ... of a
+// CTA's N, its M and L.
+template <int D, int N>
+__device__ __forceinline__ float row_weights(const char* smem, int w0, int step, int row, float (&w)[N], float& L) {
+    float l[N];
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        const bool in = w0 + i * step < kWarps;
+    for (int i = 0; i < N; ++i) {
+        const bool in = w0 + i * step < N;
         const Part<D>* part = reinterpret_cast<const Part<D>*>(smem + (in ? w0 + i * step : w0) * kRingBytes<D>);
         w[i] = in ? part->m[row] : -INFINITY;
         l[i] = in ? part->l[row] : 0.f;
     }
     float M = w[0];
 #pragma unroll
-    for (int i = 1; i < kWarps; ++i) M = fmaxf(M, w[i]);
+    for (int i = 1; i < N; ++i) M = fmaxf(M, w[i]);
     const float use = M == -INFINITY ? 0.f : M;
     L = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < N; ++i) {
         w[i] = exp2f(w[i] - use);
         L = fmaf(w[i], l[i], L);
     }
@@ -715,12 +733,12 @@ __device__ __forceinline__ float row_weights(const char* smem, int w0, int step,
 }
 
 // Four dims of a row out of those parts.
-template <int D>
-__device__ __forceinline__ float4 row_sum(const char* smem, int w0, int step, int row, int d, const float (&w)[kWarps]) {
+template <int D, int N>
+__device__ __forceinline__ float4 row_sum(const char* smem, int w0, int step, int row, int d, const float (&w)[N]) {
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i)
-        if (w0 + i * step < kWarps) {
+    for (int i = 0; i < N; ++i)
+        if (w0 + i * step < N) {
             const Part<D>* part = reinterpret_cast<const Part<D>*>(smem + (w0 + i * step) * kRingBytes<D>);
             const float4 v = *reinterpret_cast<const float4*>(&part->o[row][d]);
             sum.x = fmaf(w[i], v.x, sum.x);
@@ -746,11 +764,11 @@ __device__ __forceinline__ void join_splits(const Params& p, char* smem, int war
             for (int h = 0; h < C::HL; ++h) {
                 const int row = a.head_of(x, t, h);
                 float w[kWarps], L;
-                a.m[x][h] = row_weights<D>(smem, warp, p.hw, row, w, L);
+                a.m[x][h] = row_weights<D, kWarps>(smem, warp, p.hw, row, w, L);
                 a.l[x][h] = L;
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
-                    const float4 v = row_sum<D>(smem, warp, p.hw, row, 32 * i + 4 * g, w);
+                    const float4 v = row_sum<D, kWarps>(smem, warp, p.hw, row, 32 * i + 4 * g, w);
                     a.at(x, i, 0, h) = v.x;
                     a.at(x, i, 1, h) = v.y;
                     a.at(x, i, 2, h) = v.z;
@@ -770,21 +788,24 @@ __device__ __forceinline__ uint2 pack4(const float4& v, float f) {
 
 // What the CTAs of a cluster send one another: 32 dims of a row ("segment") of
 // every CTA to the CTA that joins it, and every row's M and L to all.
+template <int D, class C>
 struct ClusterIn {
-    float o[kMaxGroup * 4 * 32];                 // [segment / CS][CTA][32]
-    float m[kMaxCluster][kMaxGroup], l[kMaxCluster][kMaxGroup];
+    static constexpr int ROWS = C::kNarrow ? 4 : 8 * C::X, SEGS = ROWS * (D / 32);
+    // [segment / CS][CTA][32]; the last CTAs of a cluster may have one segment less
+    float o[(SEGS + kMaxCluster - 1) / kMaxCluster * kMaxCluster][32];
+    float m[kMaxCluster][ROWS], l[kMaxCluster][ROWS];
 };
 
 // Direct: cluster c / cs takes unit c / cs (hw = 1), its CTAs equal parts of
-// the unit's tiles, their warps every fourth tile.
-template <class E, int D, class C>
-__global__ void __launch_bounds__(kThreads, kCtas<D, C>) direct_kernel(const __grid_constant__ Params p) {
+// the unit's tiles, their W warps a stage each in turn.
+template <class E, int D, class C, int W>
+__global__ void __launch_bounds__(32 * W, W == kWarps ? kCtas<D, C> : 1) direct_kernel(const __grid_constant__ Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     constexpr int SEGS = D / 32;
     extern __shared__ __align__(128) char smem[];
-    __shared__ ClusterIn in;
-    __shared__ __align__(8) unsigned long long full[kWarps][kStages<D>];
+    __shared__ ClusterIn<D, C> in;
+    __shared__ __align__(8) unsigned long long full[W][kStages<D>];
     __shared__ int abort;
     if (p.cs > 1) cluster_arrive();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -799,9 +820,9 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, C>) direct_kernel(const __g
     const int tb = min(T, rank * per), te = min(T, tb + per);
 
     // stages of one tile where two would leave warps without any
-    const int span = te - tb > kWarps ? kSpan : 1, first = tb + warp * span;
+    const int span = te - tb > W ? kSpan : 1, first = tb + warp * span;
     Feed<D> feed(p, nullptr, &abort, smem_of(smem) + warp * kRingBytes<D>, smem_of(&full[warp][0]), warp, lane, 0, span,
-                 kWarps);
+                 W);
     Acc<D, C> a;
     feed.begin(s, kvh, n, first, te, 0);
     attend<E, D, C>(p, feed, s, kvh, first, te, lane, a);
@@ -810,11 +831,11 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, C>) direct_kernel(const __g
     __syncthreads();
     uint16_t* out = static_cast<uint16_t*>(p.out) + ((int64_t)s * p.H + (int64_t)kvh * p.G) * D;
     if (p.cs == 1) {
-        for (int k = tid; k < p.G * (D / 4); k += kThreads) {
+        for (int k = tid; k < p.G * (D / 4); k += 32 * W) {
             const int row = k / (D / 4), d = k % (D / 4) * 4;
-            float w[kWarps], L;
-            row_weights<D>(smem, 0, 1, row, w, L);
-            *reinterpret_cast<uint2*>(out + row * D + d) = pack4<E>(row_sum<D>(smem, 0, 1, row, d, w), inverse_of(L));
+            float w[W], L;
+            row_weights<D, W>(smem, 0, 1, row, w, L);
+            *reinterpret_cast<uint2*>(out + row * D + d) = pack4<E>(row_sum<D, W>(smem, 0, 1, row, d, w), inverse_of(L));
         }
         return;
     }
@@ -822,14 +843,14 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, C>) direct_kernel(const __g
     cg::cluster_group cluster = cg::this_cluster();
     const int CS = (int)cluster.num_blocks();
     cluster_wait();  // all CTAs run
-    for (int seg = warp; seg < p.G * SEGS; seg += kWarps) {
+    for (int seg = warp; seg < p.G * SEGS; seg += W) {
         const int row = seg / SEGS, d = seg % SEGS * 32 + lane;
-        float w[kWarps], L, sum = 0.f;
-        const float M = row_weights<D>(smem, 0, 1, row, w, L);
+        float w[W], L, sum = 0.f;
+        const float M = row_weights<D, W>(smem, 0, 1, row, w, L);
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i)
+        for (int i = 0; i < W; ++i)
             sum = fmaf(w[i], reinterpret_cast<const Part<D>*>(smem + i * kRingBytes<D>)->o[row][d], sum);
-        cluster.map_shared_rank(&in.o[0], seg % CS)[(seg / CS * CS + rank) * 32 + lane] = sum;
+        cluster.map_shared_rank(&in.o[0][0], seg % CS)[(seg / CS * CS + rank) * 32 + lane] = sum;
         if (seg % SEGS == 0 && lane < CS) {
             cluster.map_shared_rank(&in.m[rank][0], lane)[row] = M;
             cluster.map_shared_rank(&in.l[rank][0], lane)[row] = L;
@@ -837,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, C>) direct_kernel(const __g
     }
     cluster_arrive();
     cluster_wait();
-    for (int k = warp; k * CS + rank < p.G * SEGS; k += kWarps) {
+    for (int k = warp; k * CS + rank < p.G * SEGS; k += W) {
         const int seg = k * CS + rank, row = seg / SEGS;
         const float m = lane < CS ? in.m[lane][row] : -INFINITY;
         float M = m;
@@ -850,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, C>) direct_kernel(const __g
         for (int x = kMaxCluster / 2; x >= 1; x >>= 1) L += __shfl_xor_sync(kFull, L, x);
         const float inv = inverse_of(__shfl_sync(kFull, L, 0));
         float o = 0.f;
-        for (int i = 0; i < CS; ++i) o = fmaf(__shfl_sync(kFull, w, i), in.o[(k * CS + i) * 32 + lane], o);
+        for (int i = 0; i < CS; ++i) o = fmaf(__shfl_sync(kFull, w, i), in.o[k * CS + i][lane], o);
         o *= inv;
         const float next = __shfl_down_sync(kFull, o, 1);
         if ((lane & 1) == 0)
@@ -938,9 +959,10 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, C>) split_kernel(const __gr
 // row, or (`many`: units of many pieces) the warps of a CTA.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinCtasPerSm = 5;
 
 template <class E, int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p, int many) {
+__global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) join_kernel(const __grid_constant__ Params p, int many) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     constexpr int DPL = D / 32;
@@ -995,7 +1017,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 // ---------------------------------------------------------------------------
 constexpr int kDirectTokens = 1024;  // per CTA of a direct call
 constexpr int kDirectWaves = 4;
-constexpr int kJoinCtasPerSm = 3;
+constexpr int kManyTokens = 640;     // per warp of a CTA that fills its SM
 
 struct Layout {
     size_t place, m, l, acc, total;
@@ -1013,15 +1035,25 @@ Layout layout_of(int S, int H, int Hkv, int D) {
     return L;
 }
 
-template <class E, int D>
-KernelFn pick(bool direct, int G) {
-    if (G <= 4) return direct ? direct_kernel<E, D, Narrow> : split_kernel<E, D, Narrow>;
-    if (G <= 8) return direct ? direct_kernel<E, D, Heads<1>> : split_kernel<E, D, Heads<1>>;
-    return direct ? direct_kernel<E, D, Heads<2>> : split_kernel<E, D, Heads<2>>;
+// A kernel, its warps, and the shared memory of their rings.
+struct Pick {
+    KernelFn fn;
+    int warps, smem;
+};
+enum Kind { kSplit, kDirect, kDirectMany };
+template <class E, int D, class C>
+Pick pick(Kind kind) {
+    constexpr int many = kManyWarps<D, C>;
+    if (kind == kDirectMany) return {direct_kernel<E, D, C, many>, many, many * kRingBytes<D>};
+    return {kind == kSplit ? split_kernel<E, D, C> : direct_kernel<E, D, C, kWarps>, kWarps, kWarps * kRingBytes<D>};
 }
-KernelFn pick(pkv_dtype dtype, int D, bool direct, int G) {
-    if (dtype == PKV_F16) return D == 128 ? pick<pkv::F16, 128>(direct, G) : pick<pkv::F16, 64>(direct, G);
-    return D == 128 ? pick<pkv::BF16, 128>(direct, G) : pick<pkv::BF16, 64>(direct, G);
+template <class E, int D>
+Pick pick(Kind kind, int G) {
+    return G <= 4 ? pick<E, D, Narrow>(kind) : G <= 8 ? pick<E, D, Heads<1>>(kind) : pick<E, D, Heads<2>>(kind);
+}
+Pick pick(pkv_dtype dtype, int D, Kind kind, int G) {
+    if (dtype == PKV_F16) return D == 128 ? pick<pkv::F16, 128>(kind, G) : pick<pkv::F16, 64>(kind, G);
+    return D == 128 ? pick<pkv::BF16, 128>(kind, G) : pick<pkv::BF16, 64>(kind, G);
 }
 void (*pick_join(pkv_dtype dtype, int D))(Params, int) {
     if (dtype == PKV_F16) return D == 128 ? join_kernel<pkv::F16, 128> : join_kernel<pkv::F16, 64>;
@@ -1060,6 +1092,8 @@ pkv_status pkv_paged_attention_decode_q4(void* out, const void* q, const void* k
     if (H / Hkv > kMaxGroup) return bad(PKV_ERR_UNSUPPORTED, "at most 16 query heads per KV head");
     if (!(scale == scale) || std::isinf(scale)) return bad(PKV_ERR_INVALID_ARG, "scale must be finite");
     if ((int64_t)NB * bs > INT32_MAX) return bad(PKV_ERR_INVALID_ARG, "NB * bs must fit 31 bits");
+    if ((int64_t)NB * bs / q4::kUnit * Hkv > INT32_MAX)
+        return bad(PKV_ERR_INVALID_ARG, "NB * bs * Hkv must fit 34 bits");
     if (S > 32767 || (int64_t)S * H > INT32_MAX / kMaxCluster)
         return bad(PKV_ERR_INVALID_ARG, "at most 32767 sequences, and 2^27 heads in all of them");
     const int64_t cap = (int64_t)MB * bs;
@@ -1101,20 +1135,30 @@ pkv_status pkv_paged_attention_decode_q4(void* out, const void* q, const void* k
     p.part_acc = reinterpret_cast<float*>(w + L.acc);
     p.err = pkv::device_error_word();
     p.tile_log2 = 5;
-    const int smem = D == 128 ? kSmemBytes<128> : kSmemBytes<64>;
     const int sms = pkv::sm_count();
-    const KernelFn direct_fn = pick(dtype, D, true, p.G), split_fn = pick(dtype, D, false, p.G);
-    const int per_sm = resident_of(split_fn, smem), direct_sm = resident_of(direct_fn, smem);
-    if (per_sm < 1 || direct_sm < 1) return bad(PKV_ERR_CUDA, "the kernel cannot be resident");
-    // direct: the smallest cluster that leaves kDirectTokens per CTA; more CTAs
-    // while they still fit the card at once and have two tiles per warp
-    const int64_t slots = (int64_t)direct_sm * sms;
+    const int64_t units = (int64_t)S * Hkv;
+    // few units: clusters of CTAs that fill an SM each, unless their warps' shares
+    // would be longer than kManyTokens
+    Pick use = pick(dtype, D, kDirectMany, p.G);
     p.cs = 1;
-    while (p.cs < kMaxCluster && max_ctx > (int64_t)kDirectTokens * p.cs) p.cs *= 2;
-    const bool direct = max_ctx <= (int64_t)kDirectTokens * p.cs && (int64_t)S * Hkv * p.cs <= kDirectWaves * slots;
-    if (direct)
-        while (p.cs < kMaxCluster && (int64_t)S * Hkv * p.cs * 2 <= slots && max_ctx > (int64_t)2 * kWarps * kTile * p.cs)
-            p.cs *= 2;
+    while (p.cs < kMaxCluster && units * p.cs * 2 <= sms && max_ctx > (int64_t)use.warps * kTile * p.cs) p.cs *= 2;
+    bool direct = units * p.cs <= sms && max_ctx > (int64_t)kWarps * kTile &&
+                  max_ctx <= (int64_t)kManyTokens * use.warps * p.cs;
+    if (!direct) {
+        // the smallest cluster that leaves kDirectTokens per CTA; more CTAs while they
+        // still fit the card at once and have two tiles per warp
+        use = pick(dtype, D, kDirect, p.G);
+        const int64_t slots = (int64_t)resident_of(use.fn, use.smem) * sms;
+        p.cs = 1;
+        while (p.cs < kMaxCluster && max_ctx > (int64_t)kDirectTokens * p.cs) p.cs *= 2;
+        direct = max_ctx <= (int64_t)kDirectTokens * p.cs && units * p.cs <= kDirectWaves * slots;
+        if (direct)
+            while (p.cs < kMaxCluster && units * p.cs * 2 <= slots && max_ctx > (int64_t)2 * kWarps * kTile * p.cs)
+                p.cs *= 2;
+    }
+    if (!direct) use = pick(dtype, D, kSplit, p.G);
+    const int per_sm = resident_of(use.fn, use.smem, 32 * use.warps);
+    if (per_sm < 1) return bad(PKV_ERR_CUDA, "the kernel cannot be resident");
     p.hw = direct ? 1 : heads_per_cta(Hkv);
     while (!direct && p.hw > 1 && (int64_t)S * Hkv / p.hw < kMinUnits) p.hw /= 2;
     p.nsplit = kWarps / p.hw;
@@ -1133,19 +1177,21 @@ pkv_status pkv_paged_attention_decode_q4(void* out, const void* q, const void* k
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(32 * use.warps);
+    cfg.dynamicSmemBytes = use.smem;
     cfg.stream = pkv::as_stream(stream);
     cfg.attrs = attr;
     cfg.numAttrs = direct && p.cs > 1 ? 2 : 1;
     cfg.gridDim = dim3(direct ? (unsigned)(S * Hkv * p.cs) : (unsigned)p.ranges);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, direct ? direct_fn : split_fn, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, use.fn, p);
     if (e == cudaSuccess && !direct) {
         const int many = p.ranges > 8 * (int64_t)S * p.HB;  // units of more than 8 pieces
         cfg.dynamicSmemBytes = 0;
         cfg.numAttrs = 1;
         cfg.blockDim = dim3(kJoinThreads);
-        cfg.gridDim = dim3((unsigned)(kJoinCtasPerSm * sms));
+        // one wave, of no more CTAs than there are rows for
+        const int64_t ctas = many ? (int64_t)S * H : ((int64_t)S * H + kJoinWarps - 1) / kJoinWarps;
+        cfg.gridDim = dim3((unsigned)(ctas < kJoinCtasPerSm * sms ? ctas : kJoinCtasPerSm * sms));
         e = cudaLaunchKernelEx(&cfg, pick_join(dtype, D), p, many);
     }
     return e == cudaSuccess ? PKV_OK : pkv::cuda_fail(e, "paged_attention_decode_q4 launch");

@@ -11,10 +11,11 @@
 // needs to land on the same one.
 //
 // Memory is the bound: a row is read once and written once; a 4-bit row is
-// 288 (D = 128: 576) bytes per 8 tokens.  One CTA takes a token, D / 16
-// neighbouring threads one row of it; a thread holds two chunks of 8 dims that
+// 288 (D = 128: 576) bytes per 8 tokens.  One CTA takes a few tokens, D / 16
+// neighbouring threads a row at a time; a thread holds two chunks of 8 dims that
 // rotate with one another (dims 8j and R/2 + 8j, or 16 neighbouring dims when
-// interleaved), so nothing is exchanged, and keeps its 8 angles for all its rows.
+// interleaved), so nothing is exchanged.  The next row is on its way while one is
+// turned; its angles come out of L1, where the first row of the token left them.
 #include <cmath>
 #include <cstdio>
 
@@ -36,10 +37,12 @@ struct AppendParams {
     const int32_t *block_tables, *seq_idx, *pos, *rotary_pos;
     const float* table;  // [table_rows][R]: R / 2 cos, R / 2 sin
     int64_t* slots;
-    int S, H, Hkv, bs_log2, MB, R, table_rows, interleaved;
+    int T, S, H, Hkv, bs_log2, MB, R, table_rows, interleaved;
+    int per_cta;         // tokens, at most kMaxTokens
     int64_t num_slots;
     int* err;
 };
+constexpr int kMaxTokens = 8;
 
 __device__ __forceinline__ void st16(char* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }
 
@@ -106,57 +109,78 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     constexpr int LPR = D / 16;  // threads per row
-    const int tid = threadIdx.x, lane = tid & 31, j = tid % LPR;
-    const int64_t t = blockIdx.x;
-    const int place = p.pos[t], seq = p.seq_idx[t];
-    const int turn_at = p.rotary_pos ? p.rotary_pos[t] : place;
+    __shared__ int64_t s_slot[kMaxTokens];  // negative: nothing is written for the token
+    __shared__ int s_turn[kMaxTokens];
+    const int tid = threadIdx.x, j = tid % LPR;
+    const int64_t t0 = (int64_t)blockIdx.x * p.per_cta;
+    const int tokens = (int)min((int64_t)p.per_cta, p.T - t0);
 
-    // rows: K of every KV head, V, then the queries
+    // rows of a token: K of every KV head, V, then the queries
     const int kv = 2 * p.Hkv, rows = kv + p.H, step = blockDim.x / LPR;
     int ca, cb;
     chunks_of(j, p.R, p.interleaved, ca, cb);
+    int k = 0, r = tid / LPR;  // the thread's token and row
+    auto settle = [&]() {
+        while (r >= rows && k < tokens) {
+            r -= rows;
+            ++k;
+        }
+    };
+    settle();
     uint4 va, vb;
-    auto load = [&](int r) {
-        if (r >= rows) return;
+    auto load = [&]() {
+        if (k >= tokens) return;
+        const int64_t t = t0 + k;
         const char* from = r < p.Hkv ? p.key + t * p.key_stride + (int64_t)r * D * 2
                            : r < kv  ? p.value + t * p.value_stride + (int64_t)(r - p.Hkv) * D * 2
                                      : p.query + t * p.query_stride + (int64_t)(r - kv) * D * 2;
         va = pkv::ld_stream(from + 16 * ca);
         vb = pkv::ld_stream(from + 16 * cb);
     };
-    int r = tid / LPR;
-    if (place >= 0) load(r);  // on its way while the slot is found
-
-    int64_t slot = pkv::slot_of(p.block_tables, seq, place, p.S, p.MB, 1 << p.bs_log2, tid == 0 ? p.err : nullptr);
-    if (slot >= 0 && p.R && (unsigned)turn_at >= (unsigned)p.table_rows) {
-        if (tid == 0) pkv::report(p.err, PKV_DEVERR_POSITION);
-        slot = -1;
+    if (tid < tokens) {
+        const int64_t t = t0 + tid;
+        const int place = p.pos[t], seq = p.seq_idx[t];
+        const int turn_at = p.rotary_pos ? p.rotary_pos[t] : place;
+        int64_t slot = pkv::slot_of(p.block_tables, seq, place, p.S, p.MB, 1 << p.bs_log2, p.err);
+        if (slot >= 0 && p.R && (unsigned)turn_at >= (unsigned)p.table_rows) {
+            pkv::report(p.err, PKV_DEVERR_POSITION);
+            slot = -1;
+        }
+        p.slots[t] = slot;
+        if (slot >= p.num_slots) {
+            pkv::report(p.err, PKV_DEVERR_SLOT);
+            slot = -1;
+        }
+        s_slot[tid] = slot;
+        s_turn[tid] = turn_at;
     }
-    if (tid == 0) p.slots[t] = slot;
-    if (slot < 0) return;
-    if (slot >= p.num_slots) {
-        if (tid == 0) pkv::report(p.err, PKV_DEVERR_SLOT);
-        return;
-    }
+    load();
+    __syncthreads();
     const bool turns = 16 * j < p.R;
-    float cs[8], sn[8];
-    if (turns) {
-        const float* at = p.table + (int64_t)turn_at * p.R + 8 * j;
-        const float4 c0 = __ldg(reinterpret_cast<const float4*>(at)), c1 = __ldg(reinterpret_cast<const float4*>(at) + 1);
-        const float4 s0 = __ldg(reinterpret_cast<const float4*>(at + p.R / 2)),
-                     s1 = __ldg(reinterpret_cast<const float4*>(at + p.R / 2) + 1);
-        cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w;
-        cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
-        sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w;
-        sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
-    }
 
     // whole warps go round together: the threads of a row exchange its bounds
-    for (int r0 = r - lane / LPR; r0 < rows; r0 += step, r += step) {
-        float a[8], b[8];
+    while (__any_sync(kFull, k < tokens)) {
+        const bool in = k < tokens;
+        const int64_t t = t0 + k, slot = in ? s_slot[k] : -1;
+        const int row_of = r;
         uint4 xa = va, xb = vb;
-        load(r + step);
-        const bool rotates = turns && r < rows && (r < p.Hkv || r >= kv);
+        const bool rotates = turns && slot >= 0 && (r < p.Hkv || r >= kv);
+        float cs[8], sn[8];
+        if (rotates) {
+            const float* at = p.table + (int64_t)s_turn[k] * p.R + 8 * j;
+            const float4 c0 = __ldg(reinterpret_cast<const float4*>(at)), c1 = __ldg(reinterpret_cast<const float4*>(at) + 1);
+            const float4 s0 = __ldg(reinterpret_cast<const float4*>(at + p.R / 2)),
+                         s1 = __ldg(reinterpret_cast<const float4*>(at + p.R / 2) + 1);
+            cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w;
+            cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
+            sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w;
+            sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
+        }
+        r += step;
+        settle();
+        load();
+        const bool is_kv = in && row_of < kv;
+        float a[8], b[8];
         if (rotates || kQ4) {
             pkv::unpack8<E>(xa, a);
             pkv::unpack8<E>(xb, b);
@@ -165,7 +189,7 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
             if (p.interleaved) rotate<true>(a, b, cs, sn);
             else rotate<false>(a, b, cs, sn);
         }
-        if (kQ4 && r0 < kv) {
+        if (kQ4 && __any_sync(kFull, is_kv)) {
             // bounds of the row's groups: a chunk lies in group chunk / 8
             float lo[2], hi[2], bad[2];
             bounds_of(a, lo[0], hi[0], bad[0]);
@@ -202,9 +226,10 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
                 m[g] = back.y;
                 inv[g] = s[g] > 0.f ? 1.f / s[g] : 0.f;
             }
-            if (r < kv) {
-                const int head = r < p.Hkv ? r : r - p.Hkv, row = (int)(slot & 7);
-                char* unit = (r < p.Hkv ? p.k_cache : p.v_cache) + q4::unit_at<D>((int)slot, head, p.Hkv, p.bs_log2);
+            if (is_kv) {
+                if (slot < 0) continue;
+                const int head = row_of < p.Hkv ? row_of : row_of - p.Hkv, row = (int)(slot & 7);
+                char* unit = (row_of < p.Hkv ? p.k_cache : p.v_cache) + q4::unit_at<D>((int)slot, head, p.Hkv, p.bs_log2);
                 char* codes = unit + row * q4::code_bytes(D);
                 *reinterpret_cast<uint32_t*>(codes + 16 * q4::chunk_place<D>(row, ca >> 2) + 4 * (ca & 3)) =
                     codes_of(a, second[0] ? s[1] : s[0], second[0] ? m[1] : m[0], second[0] ? inv[1] : inv[0]);
@@ -216,14 +241,14 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
                 continue;
             }
         }
-        if (r >= rows) continue;
+        if (slot < 0) continue;
         if (rotates) {
             xa = pkv::pack8<E>(a);
             xb = pkv::pack8<E>(b);
         }
-        char* to = r < p.Hkv ? p.k_cache + (slot * p.Hkv + r) * D * 2
-                   : r < kv  ? p.v_cache + (slot * p.Hkv + r - p.Hkv) * D * 2
-                             : p.query_out + t * p.query_out_stride + (int64_t)(r - kv) * D * 2;
+        char* to = row_of < p.Hkv ? p.k_cache + (slot * p.Hkv + row_of) * D * 2
+                   : row_of < kv  ? p.v_cache + (slot * p.Hkv + row_of - p.Hkv) * D * 2
+                                  : p.query_out + t * p.query_out_stride + (int64_t)(row_of - kv) * D * 2;
         st16(to + 16 * ca, xa);
         st16(to + 16 * cb, xb);
     }
@@ -234,13 +259,13 @@ struct GatherParams {
     int64_t key_stride, value_stride;  // bytes per token
     const char *k_cache, *v_cache;
     const int64_t* slots;
-    int T, Hkv, bs_log2;
+    int T, Hkv, bs_log2, splits;
     int64_t num_slots;
     int* err;
 };
 
-// One CTA reads 8 tokens' K and V rows of every KV head: D / 16 threads per row,
-// neighbouring tokens of one head (one run of the pool when their slots are
+// `splits` CTAs read 8 tokens' K and V rows of every KV head: D / 16 threads per
+// row, neighbouring tokens of one head (one run of the pool when their slots are
 // neighbours too) by neighbouring rows' threads.
 template <class E, int D>
 __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ GatherParams p) {
@@ -248,9 +273,9 @@ __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ Gat
     asm volatile("griddepcontrol.launch_dependents;");
     constexpr int LPR = D / 16;
     const int j = threadIdx.x % LPR, step = blockDim.x / LPR;
-    const int64_t t0 = (int64_t)blockIdx.x * 8;
+    const int64_t t0 = (int64_t)(blockIdx.x / p.splits) * 8;
     const int rows = 16 * p.Hkv;
-    for (int r = threadIdx.x / LPR; r < rows; r += step) {
+    for (int r = blockIdx.x % p.splits * step + threadIdx.x / LPR; r < rows; r += step * p.splits) {
         const int64_t t = t0 + r % 8;
         if (t >= p.T) continue;
         const int64_t slot = p.slots[t];
@@ -372,6 +397,7 @@ pkv_status append(const char* who, const void* key, int64_t key_stride, const vo
     p.rotary_pos = rotary_pos;
     p.table = table;
     p.slots = slots;
+    p.T = T;
     p.S = S;
     p.H = H;
     p.Hkv = Hkv;
@@ -385,9 +411,13 @@ pkv_status append(const char* who, const void* key, int64_t key_stride, const vo
     void (*fn)(AppendParams) =
         dtype == PKV_F16 ? (D == 128 ? append_kernel<pkv::F16, 128, kQ4> : append_kernel<pkv::F16, 64, kQ4>)
                          : (D == 128 ? append_kernel<pkv::BF16, 128, kQ4> : append_kernel<pkv::BF16, 64, kQ4>);
-    const int want = (H + 2 * Hkv) * (D / 16);
-    const int threads = want >= 256 ? 256 : (want + 31) / 32 * 32;
-    const cudaError_t e = launch(fn, T, threads, stream, p);
+    // few tokens: a CTA each; many: CTAs of several, so that the chain position ->
+    // block -> slot is paid once for all their rows
+    const int64_t want = (int64_t)(H + 2 * Hkv) * (D / 16);
+    p.per_cta = 1;
+    while (p.per_cta < kMaxTokens && T >= 16 * p.per_cta * pkv::sm_count()) p.per_cta *= 2;
+    const int threads = want * p.per_cta >= 256 ? 256 : (int)(want * p.per_cta + 31) / 32 * 32;
+    const cudaError_t e = launch(fn, ((int64_t)T + p.per_cta - 1) / p.per_cta, threads, stream, p);
     if (e == cudaSuccess) return PKV_OK;
     snprintf(msg, sizeof msg, "%s launch", who);
     return pkv::cuda_fail(e, msg);
@@ -463,7 +493,12 @@ pkv_status pkv_gather_cache_q4(void* key, int64_t key_stride, void* value, int64
     p.err = pkv::device_error_word();
     void (*fn)(GatherParams) = dtype == PKV_F16 ? (D == 128 ? gather_kernel<pkv::F16, 128> : gather_kernel<pkv::F16, 64>)
                                                 : (D == 128 ? gather_kernel<pkv::BF16, 128> : gather_kernel<pkv::BF16, 64>);
-    const cudaError_t e = launch(fn, ((int64_t)T + 7) / 8, 256, stream, p);
+    // few tokens: more CTAs for their heads
+    const int64_t groups = ((int64_t)T + 7) / 8;
+    const int passes = (16 * Hkv * (D / 16) + 255) / 256;
+    p.splits = 1;
+    while (p.splits * 2 <= passes && groups * p.splits * 2 <= 8 * pkv::sm_count()) p.splits *= 2;
+    const cudaError_t e = launch(fn, groups * p.splits, 256, stream, p);
     return e == cudaSuccess ? PKV_OK : pkv::cuda_fail(e, "gather_cache_q4 launch");
 }
 

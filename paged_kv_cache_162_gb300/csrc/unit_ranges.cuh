@@ -347,7 +347,7 @@ using KernelFn = void (*)(Params);
 
 // Resident CTAs per SM of an attention kernel, after allowing it its shared
 // memory (once per kernel and device); 0 if it cannot run.
-int resident_of(KernelFn fn, int smem) {
+int resident_of(KernelFn fn, int smem, int threads = kThreads) {
     static std::mutex mu;
     static struct { KernelFn fn; int dev; int n; } cache[128];
     static int used = 0;
@@ -362,7 +362,7 @@ int resident_of(KernelFn fn, int smem) {
     int n = 0;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
         cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, kThreads, smem) != cudaSuccess) {
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
