@@ -9,9 +9,9 @@
 //
 // Units, tiles, ranges and the two ways to spread them (direct, split) are
 // unit_ranges.cuh's.  A unit is one sequence and `hw` neighbouring KV heads; one
-// warp takes one head, two 32-token tiles per stage of its ring: 8 runs of 8
-// tokens of K and of V, each one asynchronous bulk copy (a (block, head) is one
-// run of the pool) by a lane of its own, an mbarrier per stage.
+// warp takes one head of a 64-token tile: 8 runs of 8 tokens of K and of V, in one
+// asynchronous bulk copy per block (a (block, head) is one run of the pool) by a
+// lane of its own, an mbarrier per stage of the warp's ring.
 //
 // The products are m16n8k16 in fp16 with the cache as the 16 rows and the query
 // heads as the 8 columns, S^T = K Q^T and O^T = V^T P^T: a group of up to 8 query
@@ -20,7 +20,7 @@
 //  * Codes to fp16: a nibble at bits 0 or 4 of a half is, as a subnormal number,
 //    2^-24 or 2^-20 times the code: 5 instructions per 8 codes.  The 8 that a code
 //    is to lose comes off the sums: K's products start from -8 sum q; V's are
-//    corrected every 32 tokens by a product of the same weights with -8 (not at
+//    corrected every tile by a product of the same weights with -8 (not at
 //    the end: sums that grow with the context would lose digits).
 //  * K: ldmatrix gives a lane 8 codes of one token, 32 bits; q is loaded in the
 //    order that makes of them two fragments.  A power of two per head makes q
@@ -57,9 +57,8 @@ namespace q4 = pkv::q4;
 using pkv::ldsm_x4;
 using pkv::ldsm_x4_trans;
 
-constexpr int kTile = 32;         // tokens of a pass through the softmax
-constexpr int kSpan = 2;          // tiles of a stage
-constexpr int kRuns = kSpan * kTile / q4::kUnit;  // runs of 8 tokens in it
+constexpr int kTile = 64;                    // tokens of a stage
+constexpr int kRuns = kTile / q4::kUnit;     // runs of 8 tokens in it
 template <int D>
 constexpr int kStages = D == 128 ? 2 : 3;
 constexpr int kMaxRanges = 1824;  // CTAs of a split call
@@ -78,11 +77,13 @@ constexpr int kRingBytes = kStages<D> * 2 * kHalfBytes<D>;  // one warp's ring
 struct Narrow {
     static constexpr bool kNarrow = true;
     static constexpr int X = 1, HL = 1;  // column blocks, heads per lane and block
+    static constexpr int PASS = 64;      // tokens that go through the softmax together
 };
 template <int kBlocks>
 struct Heads {
     static constexpr bool kNarrow = false;
     static constexpr int X = kBlocks, HL = 2;
+    static constexpr int PASS = 32;      // (the registers are for no more)
 };
 
 // CTAs per SM that the registers are for
@@ -134,9 +135,8 @@ __device__ __forceinline__ void pairs_at(uint32_t from, uint32_t (&pair)[NG]) {
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(pair[0]) : "r"(from) : "memory");
 }
 
-// One warp's tiles on their way through its ring: stages of `span` tiles, `step`
-// tiles apart, each looked up one stage ahead of its copies and copied one less
-// than the ring has ahead of its use.  Chained (a plan, and all tiles are this
+// One warp's tiles on their way through its ring, `step` apart, each looked up one
+// tile ahead of its copies and copied kStages - 1 ahead of its use.  Chained (a plan, and all tiles are this
 // warp's) it goes on into the units and ranges that follow.
 template <int D>
 struct Feed {
@@ -147,14 +147,14 @@ struct Feed {
     int* const abort;
     const uint32_t ring, bars; // bars: an mbarrier per stage
     const int warp, lane, hl;  // hl: head of the CTA's hw that this warp takes
-    const int span, step;
+    const int step;
     const bool chained;
     const uint64_t policy;
     const char* const cache;   // lanes 0..7 copy K's runs, 8..15 V's
-    int s, hb, n_next, i, te, left;  // the next stage's first tile, and its unit; left: from its tile 0 to the range's end
-    int rest, count;           // the unit's tokens from that tile on, the stage's tokens
+    int s, hb, n_next, i, te, left;  // the next tile, and its unit; left: from its tile 0 to the range's end
+    int rest, count;           // the unit's tokens from that tile on, the tile's tokens
     const int32_t* bt;
-    int tok, phys;             // of the stage's run lane % 8: first token, and its block (-1: no run)
+    int tok, phys;             // of the tile's run lane % 8: first token, and its block (-1: no run)
     bool more;
     int has[NST];              // of the stages in the ring: runs with tokens, and tokens << 8
     int into, from;            // stages of the next copy and of the oldest one
@@ -162,12 +162,12 @@ struct Feed {
     int asked, answers, pushed;
 
     __device__ __forceinline__ Feed(const Params& p_, Plan* plan_, int* abort_, uint32_t ring_, uint32_t bars_,
-                                    int warp_, int lane_, int hl_, int span_, int nsplit)
+                                    int warp_, int lane_, int hl_, int step_)
         : p(p_), plan(plan_), abort(abort_), ring(ring_), bars(bars_), warp(warp_), lane(lane_), hl(hl_),
-          span(span_), step(span_ * nsplit), chained(plan_ != nullptr && nsplit == 1),
+          step(step_), chained(plan_ != nullptr && step_ == 1),
           // a split call streams more than it could find again in L2
           policy(plan_ ? pkv::policy_evict_first() : pkv::policy_evict_normal()),
-          cache(static_cast<const char*>(lane_ < kRuns ? p_.k_cache : p_.v_cache)), into(0), from(0), phase(0),
+          cache(static_cast<const char*>(lane_ < 8 ? p_.k_cache : p_.v_cache)), into(0), from(0), phase(0),
           asked(0), answers(0), pushed(0) {
         if (lane == 0)
             for (int st = 0; st < NST; ++st) tc_mbar_init(bars + 8 * st, 1);
@@ -184,14 +184,14 @@ struct Feed {
         if (lane * 128 < p.G * D * 2) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + lane * 128));
     }
 
-    // The next stage's blocks; they are used when it is pushed.
+    // The next tile's blocks; they are used when it is pushed.
     __device__ __forceinline__ void lookup() {
         phys = -1;
         if (!more) return;
-        count = max(min(min(te - i, span) * kTile, rest), 0);
-        const int first = (lane & (kRuns - 1)) * q4::kUnit;
+        count = max(min(kTile, rest), 0);
+        const int first = (lane & 7) * q4::kUnit;
         tok = i * kTile + first;
-        if (lane < 2 * kRuns && first < count) phys = __ldg(bt + (tok >> p.bs_log2)) & INT32_MAX;
+        if (lane < 16 && first < count) phys = __ldg(bt + (tok >> p.bs_log2)) & INT32_MAX;
     }
 
     __device__ __forceinline__ void begin(int s_, int hb_, int n, int first, int te_, int left_) {
@@ -210,7 +210,7 @@ struct Feed {
     }
 
     __device__ __forceinline__ void maybe_ask(int tiles_left) {
-        if (warp == 0 && tiles_left <= 2 * kSpan && asked == answers) {
+        if (warp == 0 && tiles_left <= 2 && asked == answers) {
             if (lane == 0) ask_range(plan, asked);
             ++asked;
         }
@@ -224,8 +224,8 @@ struct Feed {
         return got;
     }
 
-    // Copies the next stage into the ring, what it has into has[at], then looks
-    // up the one after it.
+    // Copies the next tile into the ring, what it has into has[at], then looks up
+    // the one after it.
     __device__ __forceinline__ void push(int at) {
         if (!more) return;
         const bool there = (unsigned)phys < (unsigned)p.NB;
@@ -238,14 +238,13 @@ struct Feed {
                          "r"(__popc(runs) * 2 * UB)
                          : "memory");
         __syncwarp();
-        // lanes 0..15: K's runs, then V's.  The runs of a block (of a tile at most: tiles
-        // are where blocks may end) are one piece.
-        const int units = p.bs_log2 - 3, whole = 1 << min(units, 2);
+        // lanes 0..7: K's runs, 8..15: V's.  The runs of a block are one piece.
+        const int units = p.bs_log2 - 3, whole = 1 << units;
         if (there && (lane & (whole - 1)) == 0) {
             // the pool's units of 8 tokens fit an int (checked on the host)
             const int unit = ((phys * p.Hkv + hb * p.hw + hl) << units) | ((tok >> 3) & ((1 << units) - 1));
-            const int n = min(whole, (count - (lane & (kRuns - 1)) * q4::kUnit + q4::kUnit - 1) / q4::kUnit);
-            bulk_copy(ring + into * 2 * kHalfBytes<D> + lane * UB, cache + (int64_t)unit * UB, n * UB, bar, policy);
+            const int n = min(whole, (count - (lane & 7) * q4::kUnit + q4::kUnit - 1) / q4::kUnit);
+            bulk_copy(ring + (2 * into + (lane >> 3)) * kHalfBytes<D> + (lane & 7) * UB, cache + (int64_t)unit * UB, n * UB, bar, policy);
         }
         into = into + 1 == NST ? 0 : into + 1;
         i += step;
@@ -337,8 +336,8 @@ template <class E, int D, class C>
 __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, int kvh, int first, int te, int lane,
                                        Acc<D, C>& a) {
     constexpr int NI = D / 32, NG = D / q4::kGroup, UB = q4::kUnitBytes<D>, UC = q4::kUnitCodes<D>;
-    constexpr int SUB = kTile / 16, X = C::X, HL = C::HL;
-    constexpr int CH = C::kNarrow ? 1 : NG;  // chains of products of a logit, and columns of weights
+    constexpr int SUB = C::PASS / 16, X = C::X, HL = C::HL;
+    constexpr int CH = C::kNarrow ? 1 : NG;  // columns of weights per group
     constexpr bool kHalf = std::is_same<E, pkv::F16>::value;
     constexpr int PARTS = kHalf ? 2 : 1;     // numbers that make a weight
     constexpr float kProduct = 0x1p-11f;     // of a code and the largest query elements' power of two
@@ -444,29 +443,29 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
 #pragma unroll
             for (int r = 0; r < CH; ++r) eight[x][r][0] = eight[x][r][1] = eight[x][r][2] = eight[x][r][3] = 0.f;
 #pragma unroll 1
-      for (int tile = 0; tile == 0 || tile * kTile < count; ++tile) {
-        const uint32_t sk = stage + tile * (kTile / q4::kUnit) * UB, sv = sk + kHalfBytes<D>;
-        // tokens 8 u + g of the tile, bit u
-        const int seen = count - tile * kTile - g;
-        unsigned rows = (unsigned)has >> (4 * tile) & 15u;
-        const bool some = rows != 15u || count < (tile + 1) * kTile;  // not all of the tile's tokens
+      for (int pass = 0; pass == 0 || (C::PASS < kTile && pass * C::PASS < count); ++pass) {
+        constexpr int RUNS = C::PASS / q4::kUnit;
+        const uint32_t sk = stage + pass * RUNS * UB, sv = sk + kHalfBytes<D>;
+        // tokens 8 u + g of the pass, bit u
+        constexpr unsigned all = (1u << RUNS) - 1u;
+        unsigned rows = (unsigned)has >> (RUNS * pass) & all;
+        const bool some = rows != all || count < (pass + 1) * C::PASS;  // not all of the tokens
         if (some)
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (8 * u >= seen) rows &= ~(1u << u);
+            for (int u = 0; u < RUNS; ++u)
+                if (8 * u + g >= count - pass * C::PASS) rows &= ~(1u << u);
 
         // v[x][sub][u][h]: logit of token 16 sub + 8 u + g in units of qs
-        float v[X][SUB][2][HL], dot[SUB][X][CH][4];  // dot: element 2 u + h is column 2 t + h
+        float v[X][SUB][2][HL], dot[SUB][X][NG][4];  // dot: element 2 u + h is column 2 t + h
 #pragma unroll
         for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
             for (int x = 0; x < X; ++x)
 #pragma unroll
-                for (int r = 0; r < CH; ++r)
+                for (int r = 0; r < NG; ++r)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)  // the 8 that every code is to lose
-                        dot[sub][x][r][h] = dot[sub][x][r][2 + h] =
-                            C::kNarrow ? (h < NG ? -8.f * qsum[x][h % NG][0] : 0.f) : -8.f * qsum[x][r][h % HL];
+                    for (int h = 0; h < 2; ++h)  // the 8 that every code is to lose (narrow: column r is group r's)
+                        dot[sub][x][r][h] = dot[sub][x][r][2 + h] = -8.f * qsum[x][r][h % HL];
 #pragma unroll
         for (int r = 0; r < NG; ++r) {
             uint32_t k[SUB][4];  // chunks 2 r, 2 r + 1
@@ -487,7 +486,7 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
                         const uint32_t f[4] = {h0[sub][e], h1[sub][e], h0[sub][e + 1], h1[sub][e + 1]};
 #pragma unroll
                         for (int x = 0; x < X; ++x)
-                            pkv::Mma<pkv::F16>::run(dot[sub][x][r % CH], f, qb[x][2 * r + c][e], qb[x][2 * r + c][e + 1]);
+                            pkv::Mma<pkv::F16>::run(dot[sub][x][r], f, qb[x][2 * r + c][e], qb[x][2 * r + c][e + 1]);
                     }
             }
         }
@@ -505,7 +504,7 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
 #pragma unroll
                         for (int r = 0; r < NG; ++r) {
                             const float2 sc = E::to_float2(pair[r]);
-                            sum = fmaf(sc.x, dot[sub][x][r % CH][2 * u + (C::kNarrow ? r : h)], sum);
+                            sum = fmaf(sc.x, dot[sub][x][r][2 * u + (C::kNarrow ? r : h)], sum);
                             sum = fmaf(sc.y, qsum[x][r][h], sum);
                         }
                         v[x][sub][u][h] = sum;
@@ -548,7 +547,8 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
             for (int h = 0; h < HL; ++h) {
                 float y = fmaxf(v[x][0][0][h], v[x][0][1][h]);
 #pragma unroll
-                for (int sub = 1; sub < SUB; ++sub) y = fmaxf(y, fmaxf(v[x][sub][0][h], v[x][sub][1][h]));
+                for (int sub = 1; sub < SUB; ++sub)
+                    y = fmaxf(y, fmaxf(v[x][sub][0][h], v[x][sub][1][h]));
                 top[x][h] = y * qs[x][h];
                 moves = moves || top[x][h] > a.m[x][h] + kLazy;
             }
@@ -819,10 +819,8 @@ __global__ void __launch_bounds__(32 * W, W == kWarps ? kCtas<D, C> : 1) direct_
     const int T = tiles_of(p, n), per = (T + p.cs - 1) / p.cs;
     const int tb = min(T, rank * per), te = min(T, tb + per);
 
-    // stages of one tile where two would leave warps without any
-    const int span = te - tb > W ? kSpan : 1, first = tb + warp * span;
-    Feed<D> feed(p, nullptr, &abort, smem_of(smem) + warp * kRingBytes<D>, smem_of(&full[warp][0]), warp, lane, 0, span,
-                 W);
+    const int first = tb + warp;
+    Feed<D> feed(p, nullptr, &abort, smem_of(smem) + warp * kRingBytes<D>, smem_of(&full[warp][0]), warp, lane, 0, W);
     Acc<D, C> a;
     feed.begin(s, kvh, n, first, te, 0);
     attend<E, D, C>(p, feed, s, kvh, first, te, lane, a);
@@ -893,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, C>) split_kernel(const __gr
     make_plan(p, plan, tid);
 
     Feed<D> feed(p, &plan, &plan.abort, smem_of(smem) + warp * kRingBytes<D>, smem_of(&full[warp][0]), warp, lane, hl,
-                 kSpan, p.nsplit);
+                 p.nsplit);
     Range r = range_at(p, plan.before, plan.map, plan.map.of_cta(blockIdx.x), lane);
     bool running = r.left > 0;  // the same for all warps of the CTA
     if (running && feed.chained)
@@ -906,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, C>) split_kernel(const __gr
         const int kvh = r.hb * p.hw + hl;
         const bool last = te - r.tb == r.left;  // of the range
         Acc<D, C> a;
-        const int first = r.tb + kSpan * split;
+        const int first = r.tb + split;
         if (!feed.chained) feed.begin(r.s, r.hb, r.n, first, te, 0);
         attend<E, D, C>(p, feed, r.s, kvh, first, te, lane, a);
         if (!feed.chained) join_splits<D, C>(p, smem, warp, lane, a);
@@ -1134,7 +1132,7 @@ pkv_status pkv_paged_attention_decode_q4(void* out, const void* q, const void* k
     p.part_l = reinterpret_cast<float*>(w + L.l);
     p.part_acc = reinterpret_cast<float*>(w + L.acc);
     p.err = pkv::device_error_word();
-    p.tile_log2 = 5;
+    p.tile_log2 = 6;
     const int sms = pkv::sm_count();
     const int64_t units = (int64_t)S * Hkv;
     // few units: clusters of CTAs that fill an SM each, unless their warps' shares
