@@ -57,7 +57,7 @@ namespace q4 = pkv::q4;
 using pkv::ldsm_x4;
 using pkv::ldsm_x4_trans;
 
-constexpr int kTile = 64;                    // tokens of a stage
+constexpr int kTile = 64;                    // tokens of a stage at most; short contexts go in tiles of 32
 constexpr int kRuns = kTile / q4::kUnit;     // runs of 8 tokens in it
 template <int D>
 constexpr int kStages = D == 128 ? 2 : 3;
@@ -74,10 +74,11 @@ constexpr int kRingBytes = kStages<D> * 2 * kHalfBytes<D>;  // one warp's ring
 // (head, group of 64 dims): then one chain of products gives a logit's parts side
 // by side, one column block carries the weights of both groups, and a lane has
 // one head to take through the softmax instead of two.
+template <int kPass>
 struct Narrow {
     static constexpr bool kNarrow = true;
     static constexpr int X = 1, HL = 1;  // column blocks, heads per lane and block
-    static constexpr int PASS = 64;      // tokens that go through the softmax together
+    static constexpr int PASS = kPass;   // tokens that go through the softmax together
 };
 template <int kBlocks>
 struct Heads {
@@ -90,9 +91,9 @@ struct Heads {
 template <int D, class C>
 constexpr int kCtas = C::X == 2 ? 2 : (D == 64 ? 4 : 3);
 
-// Warps of a direct call's CTAs: 4, or, for few units, as many as an SM takes.
+// Warps of a direct call's CTAs: 4, or, for few units, half of what an SM takes.
 template <int D, class C>
-constexpr int kManyWarps = C::X == 2 ? 8 : (D == 128 ? 12 : 16);
+constexpr int kManyWarps = C::X == 2 ? 4 : (D == 128 ? 6 : 8);
 
 __device__ __forceinline__ float exp2_of(float x) {
     float y;
@@ -177,7 +178,7 @@ struct Feed {
     }
 
     __device__ __forceinline__ void enter(int n) {  // unit (s, hb), at its tile i
-        rest = n - i * kTile;
+        rest = n - (i << p.tile_log2);
         bt = p.block_tables + (int64_t)s * p.MB;
         const char* q = static_cast<const char*>(p.q) +
                         ((int64_t)s * p.H + (int64_t)(hb * p.hw + hl) * p.G) * D * 2;
@@ -188,9 +189,9 @@ struct Feed {
     __device__ __forceinline__ void lookup() {
         phys = -1;
         if (!more) return;
-        count = max(min(kTile, rest), 0);
+        count = max(min(1 << p.tile_log2, rest), 0);
         const int first = (lane & 7) * q4::kUnit;
-        tok = i * kTile + first;
+        tok = (i << p.tile_log2) + first;
         if (lane < 16 && first < count) phys = __ldg(bt + (tok >> p.bs_log2)) & INT32_MAX;
     }
 
@@ -248,7 +249,7 @@ struct Feed {
         }
         into = into + 1 == NST ? 0 : into + 1;
         i += step;
-        rest -= step * kTile;
+        rest -= step << p.tile_log2;
         if (i >= te) advance();
         if (more && chained) maybe_ask(left - i);
         lookup();
@@ -799,7 +800,7 @@ struct ClusterIn {
 // Direct: cluster c / cs takes unit c / cs (hw = 1), its CTAs equal parts of
 // the unit's tiles, their W warps a stage each in turn.
 template <class E, int D, class C, int W>
-__global__ void __launch_bounds__(32 * W, W == kWarps ? kCtas<D, C> : 1) direct_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(32 * W, W == kWarps ? kCtas<D, C> : 2) direct_kernel(const __grid_constant__ Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     constexpr int SEGS = D / 32;
@@ -1013,9 +1014,15 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) join_kernel(cons
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-constexpr int kDirectTokens = 1024;  // per CTA of a direct call
-constexpr int kDirectWaves = 4;
-constexpr int kManyTokens = 640;     // per warp of a CTA that fills its SM
+// Direct calls.  Measured, us, 32 query heads on 8, D = 128 (direct with four
+// warps, with kManyWarps, split):
+//   1 context of 4096 6.9, 7.0, 12.0; of 32768 19.5, 18.6, 21.6; of 131072 64, 61, 37
+//   4 of 8192 15.6, 12.8, 20.8; of 32768 44, 36, 38;  32 of 1024 13.9, 11.2, 20.8;
+//   of 4096 42, 35, 39;  64 of 128..2048 26.6, 28.2, 26.4;  100 of 1..500 13.9, -, 16.9;
+//   256 of 1..200 20.8, -, 21.8
+constexpr int kDirectTokens = 1024;  // the longest context that four warps take
+constexpr int kDirectWaves = 4;      // of their CTAs
+constexpr int kManyTokens = 704;     // per warp of a CTA of kManyWarps
 
 struct Layout {
     size_t place, m, l, acc, total;
@@ -1041,17 +1048,22 @@ struct Pick {
 enum Kind { kSplit, kDirect, kDirectMany };
 template <class E, int D, class C>
 Pick pick(Kind kind) {
-    constexpr int many = kManyWarps<D, C>;
-    if (kind == kDirectMany) return {direct_kernel<E, D, C, many>, many, many * kRingBytes<D>};
-    return {kind == kSplit ? split_kernel<E, D, C> : direct_kernel<E, D, C, kWarps>, kWarps, kWarps * kRingBytes<D>};
+    if constexpr (C::kNarrow && C::PASS < kTile) return {direct_kernel<E, D, C, kWarps>, kWarps, kWarps * kRingBytes<D>};
+    else {
+        constexpr int many = kManyWarps<D, C>;
+        if (kind == kDirectMany) return {direct_kernel<E, D, C, many>, many, many * kRingBytes<D>};
+        return {kind == kSplit ? split_kernel<E, D, C> : direct_kernel<E, D, C, kWarps>, kWarps, kWarps * kRingBytes<D>};
+    }
 }
 template <class E, int D>
-Pick pick(Kind kind, int G) {
-    return G <= 4 ? pick<E, D, Narrow>(kind) : G <= 8 ? pick<E, D, Heads<1>>(kind) : pick<E, D, Heads<2>>(kind);
+Pick pick(Kind kind, int G, bool brief) {
+    if (G <= 4) return brief ? pick<E, D, Narrow<32>>(kDirect) : pick<E, D, Narrow<64>>(kind);
+    return G <= 8 ? pick<E, D, Heads<1>>(kind) : pick<E, D, Heads<2>>(kind);
 }
-Pick pick(pkv_dtype dtype, int D, Kind kind, int G) {
-    if (dtype == PKV_F16) return D == 128 ? pick<pkv::F16, 128>(kind, G) : pick<pkv::F16, 64>(kind, G);
-    return D == 128 ? pick<pkv::BF16, 128>(kind, G) : pick<pkv::BF16, 64>(kind, G);
+// brief: direct, tiles of 32
+Pick pick(pkv_dtype dtype, int D, Kind kind, int G, bool brief = false) {
+    if (dtype == PKV_F16) return D == 128 ? pick<pkv::F16, 128>(kind, G, brief) : pick<pkv::F16, 64>(kind, G, brief);
+    return D == 128 ? pick<pkv::BF16, 128>(kind, G, brief) : pick<pkv::BF16, 64>(kind, G, brief);
 }
 void (*pick_join(pkv_dtype dtype, int D))(Params, int) {
     if (dtype == PKV_F16) return D == 128 ? join_kernel<pkv::F16, 128> : join_kernel<pkv::F16, 64>;
@@ -1132,29 +1144,35 @@ pkv_status pkv_paged_attention_decode_q4(void* out, const void* q, const void* k
     p.part_l = reinterpret_cast<float*>(w + L.l);
     p.part_acc = reinterpret_cast<float*>(w + L.acc);
     p.err = pkv::device_error_word();
-    p.tile_log2 = 6;
     const int sms = pkv::sm_count();
     const int64_t units = (int64_t)S * Hkv;
-    // few units: clusters of CTAs that fill an SM each, unless their warps' shares
-    // would be longer than kManyTokens
+    // Few units, of more than a few tiles: clusters of CTAs of which an SM takes two,
+    // unless their warps' shares would be longer than kManyTokens.  Clusters grow
+    // while there is an SM per CTA and a tile per warp, to two CTAs per SM where
+    // their warps have four tiles.
     Pick use = pick(dtype, D, kDirectMany, p.G);
+    p.tile_log2 = 6;
     p.cs = 1;
-    while (p.cs < kMaxCluster && units * p.cs * 2 <= sms && max_ctx > (int64_t)use.warps * kTile * p.cs) p.cs *= 2;
-    bool direct = units * p.cs <= sms && max_ctx > (int64_t)kWarps * kTile &&
-                  max_ctx <= (int64_t)kManyTokens * use.warps * p.cs;
+    while (p.cs < kMaxCluster && units * p.cs * 2 <= 2 * sms &&
+           max_ctx > (int64_t)use.warps * kTile * p.cs * (units * p.cs * 2 <= sms ? 1 : 4))
+        p.cs *= 2;
+    bool direct = units <= 2 * sms && max_ctx >= kDirectTokens && max_ctx <= (int64_t)kManyTokens * use.warps * p.cs;
     if (!direct) {
-        // the smallest cluster that leaves kDirectTokens per CTA; more CTAs while they
-        // still fit the card at once and have two tiles per warp
-        use = pick(dtype, D, kDirect, p.G);
+        // Short contexts: a CTA of four warps per unit, or, while they fit the card at
+        // once, clusters with a tile per warp.
+        const bool brief = max_ctx <= kWarps * kTile;
+        use = pick(dtype, D, kDirect, p.G, brief);
+        p.tile_log2 = brief ? 5 : 6;
         const int64_t slots = (int64_t)resident_of(use.fn, use.smem) * sms;
         p.cs = 1;
-        while (p.cs < kMaxCluster && max_ctx > (int64_t)kDirectTokens * p.cs) p.cs *= 2;
-        direct = max_ctx <= (int64_t)kDirectTokens * p.cs && units * p.cs <= kDirectWaves * slots;
-        if (direct)
-            while (p.cs < kMaxCluster && units * p.cs * 2 <= slots && max_ctx > (int64_t)2 * kWarps * kTile * p.cs)
-                p.cs *= 2;
+        direct = max_ctx <= kDirectTokens && units <= kDirectWaves * slots;
+        while (direct && p.cs < kMaxCluster && units * p.cs * 2 <= slots && max_ctx > (int64_t)kWarps * kTile * p.cs)
+            p.cs *= 2;
     }
-    if (!direct) use = pick(dtype, D, kSplit, p.G);
+    if (!direct) {
+        use = pick(dtype, D, kSplit, p.G);
+        p.tile_log2 = 6;
+    }
     const int per_sm = resident_of(use.fn, use.smem, 32 * use.warps);
     if (per_sm < 1) return bad(PKV_ERR_CUDA, "the kernel cannot be resident");
     p.hw = direct ? 1 : heads_per_cta(Hkv);
