@@ -42,7 +42,7 @@ struct AppendParams {
     int64_t num_slots;
     int* err;
 };
-constexpr int kMaxTokens = 8;
+constexpr int kMaxTokens = 4;
 
 __device__ __forceinline__ void st16(char* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }
 
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
         load();
         const bool is_kv = in && row_of < kv;
         float a[8], b[8];
-        if (rotates || kQ4) {
+        if (rotates || (kQ4 && is_kv)) {
             pkv::unpack8<E>(xa, a);
             pkv::unpack8<E>(xb, b);
         }
