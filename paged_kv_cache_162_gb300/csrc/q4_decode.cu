@@ -537,9 +537,8 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
 #pragma unroll
         for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int r = 0; r < NG; ++r) most = fmaxf(most, E::to_float2(vpair[sub][u][r]).x);
+            for (int r = 0; r < NG; ++r)
+                most = pkv::max3(most, E::to_float2(vpair[sub][0][r]).x, E::to_float2(vpair[sub][1][r]).x);
         float top[X][HL];
         bool moves = most >= step_most && most > 0.f;
 #pragma unroll
@@ -548,8 +547,7 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
             for (int h = 0; h < HL; ++h) {
                 float y = fmaxf(v[x][0][0][h], v[x][0][1][h]);
 #pragma unroll
-                for (int sub = 1; sub < SUB; ++sub)
-                    y = fmaxf(y, fmaxf(v[x][sub][0][h], v[x][sub][1][h]));
+                for (int sub = 1; sub < SUB; ++sub) y = pkv::max3(y, v[x][sub][0][h], v[x][sub][1][h]);
                 top[x][h] = y * qs[x][h];
                 moves = moves || top[x][h] > a.m[x][h] + kLazy;
             }
@@ -676,7 +674,7 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) a.at(x, 2 * r + k, e, h) = fmaf(a.at(x, 2 * r + k, e, h), back * (e & 1 ? 0x1p20f : 0x1p24f), c);
+                    for (int e = 0; e < 4; ++e) a.at(x, 2 * r + k, e, h) = fmaf(a.at(x, 2 * r + k, e, h) * (e & 1 ? 0x1p20f : 0x1p24f), back, c);
             }
         }
 }

@@ -76,14 +76,16 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float
 
 // (least, greatest) of a chunk; `bad` is NaN where an element is not finite, else 0.
 __device__ __forceinline__ void bounds_of(const float (&x)[8], float& lo, float& hi, float& bad) {
-    lo = hi = x[0];
-    bad = __fmul_rn(x[0], 0.f);
+    lo = fminf(x[0], x[1]);
+    hi = fmaxf(x[0], x[1]);
+    bad = 0.f;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-        bad = fmaf(x[i], 0.f, bad);
+    for (int i = 2; i < 8; i += 2) {
+        lo = pkv::min3(lo, x[i], x[i + 1]);
+        hi = pkv::max3(hi, x[i], x[i + 1]);
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bad = fmaf(x[i], 0.f, bad);
 }
 
 // The codes of a chunk.  (x - centre) / step by a product with 1 / step and one
@@ -92,12 +94,18 @@ __device__ __forceinline__ void bounds_of(const float (&x)[8], float& lo, float&
 __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float step, float centre, float inv) {
     uint32_t c = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float d = __fsub_rn(x[i], centre);
-        const float t0 = __fmul_rn(d, inv);
-        const float t = fminf(fmaxf(fmaf(fmaf(-t0, step, d), inv, t0), -8.f), 7.f);
-        // 1.5 * 2^23 + 8: the sum's last bits are the nearest integer (to even) + 8
-        c |= (__float_as_uint(__fadd_rn(t, 12582920.f)) & 15u) << (4 * i);
+    for (int h = 0; h < 2; ++h) {
+        float four = 0.f;  // four codes as one number below 2^16
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            const float d = __fsub_rn(x[4 * h + i], centre);
+            const float t0 = __fmul_rn(d, inv);
+            const float t = fminf(fmaxf(fmaf(fmaf(-t0, step, d), inv, t0), -8.f), 7.f);
+            // 1.5 * 2^23 is where the numbers are whole: the nearest one (to even)
+            const float whole = __fadd_rn(__fadd_rn(t, 12582912.f), -12582904.f);  // + 8
+            four = fmaf(four, 16.f, whole);
+        }
+        c |= (__float_as_uint(__fadd_rn(four, 8388608.f)) & 0xffffu) << (16 * h);
     }
     return c;
 }
@@ -416,7 +424,9 @@ pkv_status append(const char* who, const void* key, int64_t key_stride, const vo
     const int64_t want = (int64_t)(H + 2 * Hkv) * (D / 16);
     p.per_cta = 1;
     while (p.per_cta < kMaxTokens && T >= 16 * p.per_cta * pkv::sm_count()) p.per_cta *= 2;
-    const int threads = want * p.per_cta >= 256 ? 256 : (int)(want * p.per_cta + 31) / 32 * 32;
+    // (the 4-bit form, 75 registers a thread: 24 warps of smaller CTAs fit an SM better)
+    const int most = kQ4 && p.per_cta > 1 ? 128 : 256;
+    const int threads = want * p.per_cta >= most ? most : (int)(want * p.per_cta + 31) / 32 * 32;
     const cudaError_t e = launch(fn, ((int64_t)T + p.per_cta - 1) / p.per_cta, threads, stream, p);
     if (e == cudaSuccess) return PKV_OK;
     snprintf(msg, sizeof msg, "%s launch", who);

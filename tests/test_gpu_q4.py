@@ -53,6 +53,10 @@ def test_few_short_contexts(dtype, D, bs, Hkv, G):
     (3, 3, 2, 64, 16, "f16", 20000),
     (5, 2, 9, 128, 64, "bf16", 18000),
     (2, 4, 1, 128, 16, "f16", 33000),
+    (2, 2, 7, 128, 16, "f16", 3000),     # 5 to 8 query heads per KV head
+    (3, 1, 5, 64, 8, "bf16", 6000),
+    (1, 1, 1, 128, 16, "f16", 70000),    # too long for the clusters: split
+    (1, 2, 6, 64, 64, "bf16", 95000),
 ])
 def test_long_contexts(S, Hkv, G, D, bs, dtype, hi):
     rng = np.random.default_rng(hi)
@@ -69,6 +73,10 @@ def test_long_contexts(S, Hkv, G, D, bs, dtype, hi):
     (2500, 1, 3, 64, 16, "bf16", 60),
     (900, 3, 10, 64, 32, "f16", 64),
     (160, 16, 1, 128, 16, "bf16", 400),
+    (80, 4, 6, 128, 16, "bf16", 1300),
+    (80, 4, 2, 64, 8, "f16", 1300),
+    (200, 2, 1, 64, 16, "f16", 1100),
+    (45, 8, 10, 64, 32, "f16", 1100),
 ])
 def test_many_sequences(S, Hkv, G, D, bs, dtype, hi):
     """Enough units that tiles are cut into ranges; empty sequences in between."""
@@ -97,7 +105,7 @@ def test_scales(scale):
 
 
 @pytest.mark.parametrize("dtype,k_exp,q_exp", [("f16", 8, -8), ("f16", -10, 9), ("bf16", 40, -40), ("bf16", -50, 50),
-                                               ("bf16", 60, -90)])
+                                               ("bf16", 60, -90), ("bf16", 110, -110), ("bf16", -100, 100)])
 def test_far_from_one(dtype, k_exp, q_exp):
     """Steps, centres and queries of far other sizes; steps that differ by orders from token to token."""
     c = C.attend_case(16, 3, 12, 3, 64, 16, dtype, [200, 40, 1000], spread=3.0 if dtype == "bf16" else 1.0)
@@ -211,3 +219,12 @@ def test_copy_and_swap_blocks(D):
     torch.cuda.synchronize()
     assert torch.equal(k, want_k) and torch.equal(v, want_v)
     assert L.pkv_get_device_errors() == 0
+
+
+def test_values_near_the_end_of_bf16():
+    """V of 2^113: a weight's units and a code's together must not leave fp32."""
+    c = C.attend_case(22, 2, 4, 2, 128, 16, "bf16", [70, 20], spread=0.0)
+    step, centre, code = Q.parts(c["v"], 128)
+    step, centre = (Q.narrow(Q.widen(x, "bf16") * 2.0 ** 113, "bf16") for x in (step, centre))
+    c["v"] = Q.pack(step, centre, code)
+    check(c, run(c))
