@@ -78,18 +78,6 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
     return v;
 }
 
-// The least and the greatest of three (a NaN only where all are).
-__device__ __forceinline__ float min3(float a, float b, float c) {
-    float d;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 __device__ __forceinline__ void report(int* err, int bits) {
     if (err) atomicOr(err, bits);
 }

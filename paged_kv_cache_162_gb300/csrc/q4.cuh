@@ -36,6 +36,18 @@ constexpr int kUnitBytes = kUnit * row_bytes(D);
 template <int D>
 constexpr int kUnitCodes = kUnit * code_bytes(D);
 
+// The least and the greatest of three (a NaN only where all are).
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Where row r (0..7) of a unit has its 16-byte chunk c.
 template <int D>
 __device__ __forceinline__ int chunk_place(int r, int c) {

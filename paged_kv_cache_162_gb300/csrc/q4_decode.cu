@@ -538,7 +538,7 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
         for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
             for (int r = 0; r < NG; ++r)
-                most = pkv::max3(most, E::to_float2(vpair[sub][0][r]).x, E::to_float2(vpair[sub][1][r]).x);
+                most = q4::max3(most, E::to_float2(vpair[sub][0][r]).x, E::to_float2(vpair[sub][1][r]).x);
         float top[X][HL];
         bool moves = most >= step_most && most > 0.f;
 #pragma unroll
@@ -547,7 +547,7 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
             for (int h = 0; h < HL; ++h) {
                 float y = fmaxf(v[x][0][0][h], v[x][0][1][h]);
 #pragma unroll
-                for (int sub = 1; sub < SUB; ++sub) y = pkv::max3(y, v[x][sub][0][h], v[x][sub][1][h]);
+                for (int sub = 1; sub < SUB; ++sub) y = q4::max3(y, v[x][sub][0][h], v[x][sub][1][h]);
                 top[x][h] = y * qs[x][h];
                 moves = moves || top[x][h] > a.m[x][h] + kLazy;
             }

@@ -81,8 +81,8 @@ __device__ __forceinline__ void bounds_of(const float (&x)[8], float& lo, float&
     bad = 0.f;
 #pragma unroll
     for (int i = 2; i < 8; i += 2) {
-        lo = pkv::min3(lo, x[i], x[i + 1]);
-        hi = pkv::max3(hi, x[i], x[i + 1]);
+        lo = q4::min3(lo, x[i], x[i + 1]);
+        hi = q4::max3(hi, x[i], x[i + 1]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) bad = fmaf(x[i], 0.f, bad);
