@@ -155,7 +155,7 @@ struct Feed {
     int s, hb, n_next, i, te, left;  // the next tile, and its unit; left: from its tile 0 to the range's end
     int rest, count;           // the unit's tokens from that tile on, the tile's tokens
     const int32_t* bt;
-    int tok, phys;             // of the tile's run lane % 8: first token, and its block (-1: no run)
+    int tok, phys;             // of the tile's run lane % 8: first token, and its block, if wanted()
     bool more;
     int has[NST];              // of the stages in the ring: runs with tokens, and tokens << 8
     int into, from;            // stages of the next copy and of the oldest one
@@ -187,13 +187,13 @@ struct Feed {
 
     // The next tile's blocks; they are used when it is pushed.
     __device__ __forceinline__ void lookup() {
-        phys = -1;
         if (!more) return;
         count = max(min(1 << p.tile_log2, rest), 0);
-        const int first = (lane & 7) * q4::kUnit;
-        tok = (i << p.tile_log2) + first;
-        if (lane < 16 && first < count) phys = __ldg(bt + (tok >> p.bs_log2)) & INT32_MAX;
+        tok = (i << p.tile_log2) + (lane & 7) * q4::kUnit;
+        // (not touched here: whatever uses it would wait for it)
+        if (wanted()) phys = __ldg(bt + (tok >> p.bs_log2));
     }
+    __device__ __forceinline__ bool wanted() const { return lane < 16 && (lane & 7) * q4::kUnit < count; }
 
     __device__ __forceinline__ void begin(int s_, int hb_, int n, int first, int te_, int left_) {
         s = s_;
@@ -203,7 +203,7 @@ struct Feed {
         left = left_;
         n_next = chained && s + 1 < p.S ? context_of(p, s + 1) : 0;
         more = i < te;
-        count = tok = 0;
+        count = tok = phys = 0;
         enter(n);
         lookup();
 #pragma unroll
@@ -229,8 +229,8 @@ struct Feed {
     // the one after it.
     __device__ __forceinline__ void push(int at) {
         if (!more) return;
-        const bool there = (unsigned)phys < (unsigned)p.NB;
-        if (!there && phys >= 0) pkv::report(p.err, PKV_DEVERR_BLOCK_ID);
+        const bool want = wanted(), there = want && (unsigned)phys < (unsigned)p.NB;
+        if (want && !there) pkv::report(p.err, PKV_DEVERR_BLOCK_ID);
         const unsigned runs = __ballot_sync(kFull, there) & ((1u << kRuns) - 1u);
         has[at] = (int)runs | count << 8;
         const uint32_t bar = bars + 8 * into;
