@@ -202,7 +202,7 @@ struct Feed {
         te = te_;
         left = left_;
         n_next = chained && s + 1 < p.S ? context_of(p, s + 1) : 0;
-        more = i < te;
+        more = i < te && !*(volatile int*)abort;
         count = tok = phys = 0;
         enter(n);
         lookup();
@@ -255,17 +255,29 @@ struct Feed {
         lookup();
     }
 
-    __device__ __noinline__ void wait_on(uint32_t bar, uint32_t parity) {
-        if (!tc_mbar_wait(bar, parity, abort)) {
-            pkv::report(p.err, PKV_DEVERR_TIMEOUT);
-            *(volatile int*)abort = 1;
-        }
-    }
-    // Waits for the oldest stage.
-    __device__ __forceinline__ void wait() {
-        const uint32_t bar = bars + 8 * from, parity = phase >> from & 1u;
-        if (!tc_mbar_try(bar, parity)) wait_on(bar, parity);
+    // The whole warp waits for stage `from`.  When that runs out it gives what else may
+    // be on its way into this CTA's memory some more time.
+    static __device__ __noinline__ bool wait_on(uint32_t bars, int from, unsigned phase, int* abort, int* err,
+                                                uint32_t answer, uint32_t answer_parity) {
+        if (__all_sync(kFull, tc_mbar_wait(bars + 8 * from, phase >> from & 1u, abort))) return true;
+        pkv::report(err, PKV_DEVERR_TIMEOUT);
+        *(volatile int*)abort = 1;
+        auto drain = [](uint32_t bar, uint32_t parity) {
+            for (int k = 0; k < 4096; ++k)
+                if (tc_mbar_try(bar, parity)) return;
+        };
+        for (int st = 0; st < NST; ++st) drain(bars + 8 * st, phase >> st & 1u);
+        if (answer) drain(answer, answer_parity);
         __syncwarp();
+        return false;
+    }
+    // Waits for the oldest stage; false: in vain, and nothing is copied any more.
+    __device__ __forceinline__ bool wait() {
+        if (__all_sync(kFull, tc_mbar_try(bars + 8 * from, phase >> from & 1u))) return true;
+        const uint32_t answer = plan && warp == 0 && asked != answers ? smem_of(&plan->full[answers & 1]) : 0u;
+        if (wait_on(bars, from, phase, abort, p.err, answer, (answers >> 1) & 1)) return true;
+        more = false;
+        return false;
     }
     __device__ __forceinline__ void done() {
         phase ^= 1u << from;
@@ -437,7 +449,7 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
         feed.push(Feed<D>::NST - 1);
         const int has = feed.has[0], count = has >> 8;
         const uint32_t stage = feed.ring + feed.from * 2 * kHalfBytes<D>;
-        feed.wait();
+        if (!feed.wait()) break;
         float eight[X][CH][4];  // -8 times the stage's weights in the columns: rows of even e, of odd e
 #pragma unroll
         for (int x = 0; x < X; ++x)
