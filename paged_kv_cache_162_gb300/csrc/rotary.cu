@@ -16,6 +16,16 @@
 // rotate with one another (dims 8j and R/2 + 8j, or 16 neighbouring dims when
 // interleaved), so nothing is exchanged.  The next row is on its way while one is
 // turned; its angles come out of L1, where the first row of the token left them.
+// (Two to four rows on their way: 149 to 173 us where one takes 140; the registers
+// cost more warps than the rows in flight bring.)
+//
+// Measured, D = 128: 16 prompts of 320..1727 tokens, 32 + 32 + 32 heads in fp16,
+// interleaved: 135 us, 5.96 TB/s of what it has to move, 88 % of a plain copy's rate.
+// 20 thousand tokens of 8 KV heads into 4 bits, with 32 query heads turned by 64
+// dims: 96 us, 4.5 TB/s, bound by instructions issued (the codes are 8 per element,
+// and half the threads wait while the other half's dims turn).  4-bit rows of 64
+// contexts back to fp16: 233 us, 6.26 TB/s, 92 %.  250 decoding sequences: 3.6 us,
+// 3.9 in 4 bits; a handful of tokens 3.2: launch, position -> block -> slot, row.
 #include <cmath>
 #include <cstdio>
 
@@ -42,6 +52,8 @@ struct AppendParams {
     int64_t num_slots;
     int* err;
 };
+// 2, 4, 8 tokens per CTA: 140, 135.5, 140 us in 16 bits, 119, 118, 126 in 4 (with
+// their gather); more leave the last wave of CTAs emptier.
 constexpr int kMaxTokens = 4;
 
 __device__ __forceinline__ void st16(char* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }
@@ -74,44 +86,42 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float
     }
 }
 
-// (least, greatest) of a chunk; `bad` is NaN where an element is not finite, else 0.
-__device__ __forceinline__ void bounds_of(const float (&x)[8], float& lo, float& hi, float& bad) {
-    lo = fminf(x[0], x[1]);
-    hi = fmaxf(x[0], x[1]);
-    bad = 0.f;
+// Least and greatest of a chunk, NaN where an element is.
+__device__ __forceinline__ void bounds_of(const float (&x)[8], float& lo, float& hi) {
+    lo = q4::min_nan(x[0], x[1]);
+    hi = q4::max_nan(x[0], x[1]);
 #pragma unroll
     for (int i = 2; i < 8; i += 2) {
-        lo = q4::min3(lo, x[i], x[i + 1]);
-        hi = q4::max3(hi, x[i], x[i + 1]);
+        lo = q4::min_nan(lo, x[i], x[i + 1]);
+        hi = q4::max_nan(hi, x[i], x[i + 1]);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) bad = fmaf(x[i], 0.f, bad);
 }
 
 // The codes of a chunk.  (x - centre) / step by a product with 1 / step and one
 // correction: where the quotient lies halfway between two codes, which rows of
 // 16-bit values often do, a product alone would fall to either side.
 __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float step, float centre, float inv) {
+    // at 1.5 * 2^23 the numbers are whole: the sum is the nearest one (to even), and
+    // its bits are kWhole + code.  What kWhole adds to the word comes off at the end.
+    constexpr uint32_t kWhole = 0x4b400000u;
     uint32_t c = 0;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float four = 0.f;  // four codes as one number below 2^16
-#pragma unroll
-        for (int i = 3; i >= 0; --i) {
-            const float d = __fsub_rn(x[4 * h + i], centre);
-            const float t0 = __fmul_rn(d, inv);
-            const float t = fminf(fmaxf(fmaf(fmaf(-t0, step, d), inv, t0), -8.f), 7.f);
-            // 1.5 * 2^23 is where the numbers are whole: the nearest one (to even)
-            const float whole = __fadd_rn(__fadd_rn(t, 12582912.f), -12582904.f);  // + 8
-            four = fmaf(four, 16.f, whole);
-        }
-        c |= (__float_as_uint(__fadd_rn(four, 8388608.f)) & 0xffffu) << (16 * h);
+    for (int i = 7; i >= 0; --i) {
+        const float d = __fsub_rn(x[i], centre);
+        const float t0 = __fmul_rn(d, inv);
+        const float t = fminf(fmaxf(fmaf(fmaf(-t0, step, d), inv, t0), -8.f), 7.f);
+        c = 16u * c + __float_as_uint(__fadd_rn(t, 12582920.f));
     }
-    return c;
+    return c - 0x11111111u * kWhole;
 }
 
+// The 4-bit form in CTAs of 128 threads, 7 to an SM (20 thousand tokens and their
+// gather: 122 us with 6, 118 with 7, 121 with 8, whose 64 registers are too few).
+template <bool kQ4>
+constexpr int kAppendThreads = kQ4 ? 128 : 256;
+
 template <class E, int D, bool kQ4>
-__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads<kQ4>, kQ4 ? 7 : 1) append_kernel(const __grid_constant__ AppendParams p) {
     // inputs may come from the kernel before this one; the next kernel may
     // become resident once every CTA is past this point
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -198,41 +208,52 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
             else rotate<false>(a, b, cs, sn);
         }
         if (kQ4 && __any_sync(kFull, is_kv)) {
-            // bounds of the row's groups: a chunk lies in group chunk / 8
-            float lo[2], hi[2], bad[2];
-            bounds_of(a, lo[0], hi[0], bad[0]);
-            bounds_of(b, lo[1], hi[1], bad[1]);
-            const bool second[2] = {D == 128 && ca >= 8, D == 128 && cb >= 8};
-            float s[2] = {0.f, 0.f}, m[2] = {0.f, 0.f}, inv[2] = {0.f, 0.f};
-            uint32_t pair[2] = {0u, 0u};
+            // bounds of the row's groups.  A chunk lies in group chunk / 8; the first half
+            // of the row's threads goes on with group 0, the second with group 1.
+            float lo[2], hi[2];
+            bounds_of(a, lo[0], hi[0]);
+            bounds_of(b, lo[1], hi[1]);
+            const int mine = j / 4;  // a group is four threads' share
+            const bool own[2] = {D == 64 || ca / 8 == mine, D == 64 || cb / 8 == mine};
+            float l, h;
+            if (D == 64) {
+                l = q4::min_nan(lo[0], lo[1]);
+                h = q4::max_nan(hi[0], hi[1]);
+            } else {
+                l = q4::min_nan(own[0] ? lo[0] : INFINITY, own[1] ? lo[1] : INFINITY);
+                h = q4::max_nan(own[0] ? hi[0] : -INFINITY, own[1] ? hi[1] : -INFINITY);
+                const float l1 = q4::min_nan(own[0] ? INFINITY : lo[0], own[1] ? INFINITY : lo[1]);
+                const float h1 = q4::max_nan(own[0] ? -INFINITY : hi[0], own[1] ? -INFINITY : hi[1]);
+                l = q4::min_nan(l, __shfl_xor_sync(kFull, l1, 4));
+                h = q4::max_nan(h, __shfl_xor_sync(kFull, h1, 4));
+            }
 #pragma unroll
-            for (int g = 0; g < D / q4::kGroup; ++g) {
-                float l = INFINITY, h = -INFINITY, n = 0.f;
+            for (int o = 1; o < 4; o <<= 1) {
+                l = q4::min_nan(l, __shfl_xor_sync(kFull, l, o));
+                h = q4::max_nan(h, __shfl_xor_sync(kFull, h, o));
+            }
+            const float n = fmaf(l, 0.f, h * 0.f);  // NaN where an element is not finite
+            // in sixteenths, so that no sum overflows
+            l *= 0.0625f;
+            h *= 0.0625f;
+            const float range = __fmul_rn(__fsub_rn(h, l), 1.f / 15.f) * 16.f + n;
+            const float mid = __fmul_rn(__fadd_rn(8.f * h, __fmul_rn(7.f, l)), 1.f / 15.f) * 16.f + n;
+            uint32_t pair = E::from_float2(range, mid);
+            // a step so small that 1 / step could overflow: the group reads as its centre
+            if (E::to_float2(pair).x < 0x1p-126f) pair &= 0xffff0000u;
+            const float2 sm = E::to_float2(pair);  // step, centre
+            const float inv = sm.x > 0.f ? q4::reciprocal(sm.x) : 0.f;
+            float2 sm_of[2] = {sm, sm};
+            float inv_of[2] = {inv, inv};
+            if (D == 128) {
+                const float2 other = E::to_float2(__shfl_xor_sync(kFull, pair, 4));
+                const float inv_other = __shfl_xor_sync(kFull, inv, 4);
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-                    if (second[x] == (g == 1)) {
-                        l = fminf(l, lo[x]);
-                        h = fmaxf(h, hi[x]);
-                        n += bad[x];
+                    if (!own[x]) {
+                        sm_of[x] = other;
+                        inv_of[x] = inv_other;
                     }
-#pragma unroll
-                for (int o = 1; o < LPR; o <<= 1) {
-                    l = fminf(l, __shfl_xor_sync(kFull, l, o));
-                    h = fmaxf(h, __shfl_xor_sync(kFull, h, o));
-                    n += __shfl_xor_sync(kFull, n, o);
-                }
-                // in sixteenths, so that no sum overflows
-                l *= 0.0625f;
-                h *= 0.0625f;
-                const float range = __fmul_rn(__fsub_rn(h, l), 1.f / 15.f) * 16.f + n;
-                const float mid = __fmul_rn(__fadd_rn(8.f * h, __fmul_rn(7.f, l)), 1.f / 15.f) * 16.f + n;
-                pair[g] = E::from_float2(range, mid);
-                // a step so small that 1 / step could overflow: the group reads as its centre
-                if (E::to_float2(pair[g]).x < 0x1p-126f) pair[g] &= 0xffff0000u;
-                const float2 back = E::to_float2(pair[g]);
-                s[g] = back.x;
-                m[g] = back.y;
-                inv[g] = s[g] > 0.f ? 1.f / s[g] : 0.f;
             }
             if (is_kv) {
                 if (slot < 0) continue;
@@ -240,12 +261,11 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
                 char* unit = (row_of < p.Hkv ? p.k_cache : p.v_cache) + q4::unit_at<D>((int)slot, head, p.Hkv, p.bs_log2);
                 char* codes = unit + row * q4::code_bytes(D);
                 *reinterpret_cast<uint32_t*>(codes + 16 * q4::chunk_place<D>(row, ca >> 2) + 4 * (ca & 3)) =
-                    codes_of(a, second[0] ? s[1] : s[0], second[0] ? m[1] : m[0], second[0] ? inv[1] : inv[0]);
+                    codes_of(a, sm_of[0].x, sm_of[0].y, inv_of[0]);
                 *reinterpret_cast<uint32_t*>(codes + 16 * q4::chunk_place<D>(row, cb >> 2) + 4 * (cb & 3)) =
-                    codes_of(b, second[1] ? s[1] : s[0], second[1] ? m[1] : m[0], second[1] ? inv[1] : inv[0]);
-                if (j < D / q4::kGroup)
-                    *reinterpret_cast<uint32_t*>(unit + q4::kUnitCodes<D> + row * q4::pair_bytes(D) + 4 * j) =
-                        j ? pair[1] : pair[0];
+                    codes_of(b, sm_of[1].x, sm_of[1].y, inv_of[1]);
+                if (j % 4 == 0)
+                    *reinterpret_cast<uint32_t*>(unit + q4::kUnitCodes<D> + row * q4::pair_bytes(D) + j) = pair;
                 continue;
             }
         }
@@ -424,8 +444,7 @@ pkv_status append(const char* who, const void* key, int64_t key_stride, const vo
     const int64_t want = (int64_t)(H + 2 * Hkv) * (D / 16);
     p.per_cta = 1;
     while (p.per_cta < kMaxTokens && T >= 16 * p.per_cta * pkv::sm_count()) p.per_cta *= 2;
-    // (the 4-bit form, 75 registers a thread: 24 warps of smaller CTAs fit an SM better)
-    const int most = kQ4 && p.per_cta > 1 ? 128 : 256;
+    constexpr int most = kAppendThreads<kQ4>;
     const int threads = want * p.per_cta >= most ? most : (int)(want * p.per_cta + 31) / 32 * 32;
     const cudaError_t e = launch(fn, ((int64_t)T + p.per_cta - 1) / p.per_cta, threads, stream, p);
     if (e == cudaSuccess) return PKV_OK;
