@@ -458,7 +458,8 @@ size_t pkv_decode_q4_workspace_size(int S, int H, int Hkv, int D);
  * pkv_paged_attention_decode computes, with grouped heads, from the values
  * that the caches stand for.  Arguments, limits and the promises about capture,
  * equal bits and bounded waits as in pkv_paged_attention_decode_window, whose
- * window it has not; the workspace needs pkv_decode_q4_workspace_size bytes. */
+ * window it has not; the workspace needs pkv_decode_q4_workspace_size bytes.
+ * Queries lie below 2^113 (a larger one makes its row NaN). */
 pkv_status pkv_paged_attention_decode_q4(
     void* out, const void* q, const void* k_cache, const void* v_cache,
     const int32_t* block_tables, const int32_t* context_lens,

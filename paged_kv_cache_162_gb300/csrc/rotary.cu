@@ -56,6 +56,15 @@ struct AppendParams {
 // their gather); more leave the last wave of CTAs emptier.
 constexpr int kMaxTokens = 4;
 
+// 16 bytes that are read once.  Not on the read-only path: queries may be turned in
+// place.  (A store to where a load was depends on what it brought.)
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
 __device__ __forceinline__ void st16(char* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }
 
 // The two chunks of 8 dims that thread j of a row holds.
@@ -152,8 +161,8 @@ __global__ void __launch_bounds__(kAppendThreads<kQ4>, kQ4 ? 7 : 1) append_kerne
         const char* from = r < p.Hkv ? p.key + t * p.key_stride + (int64_t)r * D * 2
                            : r < kv  ? p.value + t * p.value_stride + (int64_t)(r - p.Hkv) * D * 2
                                      : p.query + t * p.query_stride + (int64_t)(r - kv) * D * 2;
-        va = pkv::ld_stream(from + 16 * ca);
-        vb = pkv::ld_stream(from + 16 * cb);
+        va = ld_once(from + 16 * ca);
+        vb = ld_once(from + 16 * cb);
     };
     if (tid < tokens) {
         const int64_t t = t0 + tid;
