@@ -313,3 +313,30 @@ def test_rotary_table():
     ref = np.concatenate([np.cos(angle), np.sin(angle)], -1)
     # the angle in 64 bits is off by 2^-51 of itself, 2^-34 at 1e5, on either side; fp32 rounds by 2^-25
     assert np.abs(t - ref).max() <= 2.0 ** -25 + 2.0 ** -32
+
+
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("kw", [
+    dict(S=3, H=3, Hkv=1, D=64, bs=16, dtype="f16", new=[2600, 1, 1000], pad=30),         # two tokens per CTA
+    dict(S=2, H=8, Hkv=2, D=128, bs=32, dtype="bf16", new=[5000, 503], R=64, pad=4, fused=True),  # four
+    dict(S=1, H=33, Hkv=3, D=128, bs=8, dtype="bf16", new=[4901], interleaved=True),
+])
+def test_many_tokens_are_as_few_at_a_time(kw, q4):
+    """CTAs of several tokens write what CTAs of one write, bit for bit."""
+    c = C.append_case(9, **kw)
+    got = []
+    for step in (c["T"], 700):
+        d = C.append_on_gpu(c)
+        shape = (c["NB"], c["bs"], c["Hkv"], c["D"])
+        k, v = (E.new_cache_q4(c["NB"], c["bs"], c["Hkv"], c["D"]) if q4 else
+                torch.zeros(shape, dtype=C.DT[c["dtype"]], device="cuda") for _ in range(2))
+        for at in range(0, c["T"], step):
+            part = {x: d[x] if d[x] is None or x in ("tables", "table") else d[x][at:at + step] for x in d}
+            call(c, part, q4, k, v, None)
+        got.append((k, v, d["query"], d["slots"]))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    live = c["pos"] >= 0
+    assert np.array_equal(got[0][3].cpu().numpy(), Q.slots(c["tables"], c["seq"], c["pos"], c["bs"]))
+    qref, qmag = C.rotated(c, "query", np.float64)
+    check16(C.bits_of(got[0][2])[live], qref[live], qmag[live], c["dtype"])
+    assert L.pkv_get_device_errors() == 0
