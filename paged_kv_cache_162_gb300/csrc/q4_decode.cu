@@ -154,8 +154,8 @@ __device__ __forceinline__ void pairs_at(uint32_t from, uint32_t (&pair)[NG]) {
 }
 
 // One warp's tiles on their way through its ring, `step` apart, each looked up one
-// tile ahead of its copies and copied kStages - 1 ahead of its use.  Chained (a plan, and all tiles are this
-// warp's) it goes on into the units and ranges that follow.
+// tile ahead of its copies and copied kStages - 1 ahead of its use.  Chained (a plan,
+// and all tiles are this warp's) it goes on into the units and ranges that follow.
 template <int D>
 struct Feed {
     static constexpr int NST = kStages<D>;
@@ -262,7 +262,8 @@ struct Feed {
             // the pool's units of 8 tokens fit an int (checked on the host)
             const int unit = ((phys * p.Hkv + hb * p.hw + hl) << units) | ((tok >> 3) & ((1 << units) - 1));
             const int n = min(whole, (count - (lane & 7) * q4::kUnit + q4::kUnit - 1) / q4::kUnit);
-            bulk_copy(ring + (2 * into + (lane >> 3)) * kHalfBytes<D> + (lane & 7) * UB, cache + (int64_t)unit * UB, n * UB, bar, policy);
+            bulk_copy(ring + (2 * into + (lane >> 3)) * kHalfBytes<D> + (lane & 7) * UB, cache + (int64_t)unit * UB, n * UB,
+                      bar, policy);
         }
         into = into + 1 == NST ? 0 : into + 1;
         i += step;
@@ -393,11 +394,13 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
 #pragma unroll
     for (int x = 0; x < X; ++x) {
         const int head = C::kNarrow ? g >> 1 : 8 * x + g;
-        const uint16_t* q = static_cast<const uint16_t*>(p.q) + ((int64_t)s * p.H + (int64_t)kvh * p.G + head) * D + 8 * t;
+        const uint16_t* q =
+            static_cast<const uint16_t*>(p.q) + ((int64_t)s * p.H + (int64_t)kvh * p.G + head) * D + 8 * t;
         float f[NI][8], top = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const uint4 raw = head < p.G ? __ldg(reinterpret_cast<const uint4*>(q + 32 * i)) : make_uint4(0u, 0u, 0u, 0u);
+            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+            if (head < p.G) raw = __ldg(reinterpret_cast<const uint4*>(q + 32 * i));
             pkv::unpack8<E>(raw, f[i]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[i][e]));
@@ -433,7 +436,8 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
         // column c is in lanes 4 c ..; no logit's unit is 0: nothing times -infinity
 #pragma unroll
         for (int h = 0; h < HL; ++h) {
-            qs[x][h] = fmaxf(__shfl_sync(kFull, unit, 4 * (2 * t + h)) * (fabsf(p.qscale) * (1.f / kProduct)), 0x1p-126f);
+            qs[x][h] =
+                fmaxf(__shfl_sync(kFull, unit, 4 * (2 * t + h)) * (fabsf(p.qscale) * (1.f / kProduct)), 0x1p-126f);
 #pragma unroll
             for (int r = 0; r < NG; ++r)
                 qsum[x][r][h] = __shfl_sync(kFull, part[r], 4 * (2 * t + (C::kNarrow ? r : h)));
@@ -703,7 +707,10 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) a.at(x, 2 * r + k, e, h) = fmaf(a.at(x, 2 * r + k, e, h) * (e & 1 ? 0x1p20f : 0x1p24f), back, c);
+                    for (int e = 0; e < 4; ++e) {
+                        float& o = a.at(x, 2 * r + k, e, h);
+                        o = fmaf(o * (e & 1 ? 0x1p20f : 0x1p24f), back, c);
+                    }
             }
         }
 }
@@ -714,7 +721,8 @@ struct Part {
     float o[kMaxGroup][D];
     float m[kMaxGroup], l[kMaxGroup];
 };
-static_assert(sizeof(Part<128>) <= kRingBytes<128> && sizeof(Part<64>) <= kRingBytes<64>, "a part takes its warp's ring");
+static_assert(sizeof(Part<128>) <= kRingBytes<128> && sizeof(Part<64>) <= kRingBytes<64>,
+              "a part takes its warp's ring");
 
 template <int D, class C>
 __device__ __forceinline__ void put_part(Part<D>* to, int lane, Acc<D, C>& a) {
