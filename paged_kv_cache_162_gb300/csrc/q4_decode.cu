@@ -40,7 +40,7 @@
 // Measured, D = 128 (in brackets what the bytes take at a plain copy's rate, 6.78
 // TB/s): 32 contexts of 4001..16384, 32 heads in fp16, 263 us (222); 32 of 32768, 8
 // KV heads of 4 query heads in bf16, 200 (178), of 16384 106 (89): what a token adds
-// runs at 95 % of that rate.  256 of 16..4096 60 (36); one of 32768 19 (6); a handful
+// runs at 95 % of that rate.  256 of 16..4096 60 (36); one of 32768 14.5 (6); a handful
 // of short ones 3.2.  Bounds, long batches: the SMs' issue (the tensor pipe 44 %
 // busy, the ALU, which unpacks, 52 %) beside DRAM at 73 % of its peak.  Mixed lengths:
 // that and the ends, 5 us until the rings are full, CTAs of an SM that end up to 10
@@ -55,6 +55,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdio>
+#include <mutex>
 #include <type_traits>
 
 #include "pagedkv.h"
@@ -108,7 +109,8 @@ struct Heads {
 template <int D, class C>
 constexpr int kCtas = C::X == 2 ? 2 : (D == 64 ? 4 : 3);
 
-// Warps of a direct call's CTAs: 4, or, for few units, half of what an SM takes.
+// Warps of a direct call's CTAs: 4, or, for few units, half of what an SM takes, or
+// (twice as many) all of it.
 template <int D, class C>
 constexpr int kManyWarps = C::X == 2 ? 4 : (D == 128 ? 6 : 8);
 
@@ -828,14 +830,14 @@ template <int D, class C>
 struct ClusterIn {
     static constexpr int ROWS = C::kNarrow ? 4 : 8 * C::X, SEGS = ROWS * (D / 32);
     // [segment / CS][CTA][32]; the last CTAs of a cluster may have one segment less
-    float o[(SEGS + kMaxCluster - 1) / kMaxCluster * kMaxCluster][32];
+    float o[SEGS + kMaxCluster - 1][32];
     float m[kMaxCluster][ROWS], l[kMaxCluster][ROWS];
 };
 
 // Direct: cluster c / cs takes unit c / cs (hw = 1), its CTAs equal parts of
 // the unit's tiles, their W warps a stage each in turn.
 template <class E, int D, class C, int W>
-__global__ void __launch_bounds__(32 * W, W == kWarps ? kCtas<D, C> : 2) direct_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(32 * W, W == kWarps ? kCtas<D, C> : W == kManyWarps<D, C> ? 2 : 1) direct_kernel(const __grid_constant__ Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     constexpr int SEGS = D / 32;
@@ -1049,15 +1051,20 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) join_kernel(cons
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-// Direct calls.  Measured, us, 32 query heads on 8, D = 128 (direct with four
-// warps, with kManyWarps, split):
-//   1 context of 4096 6.9, 7.0, 12.0; of 32768 19.5, 18.6, 21.6; of 131072 64, 61, 37
-//   4 of 8192 15.6, 12.8, 20.8; of 32768 44, 36, 38;  32 of 1024 13.9, 11.2, 20.8;
-//   of 4096 42, 35, 39;  64 of 128..2048 26.6, 28.2, 26.4;  100 of 1..500 13.9, -, 16.9;
-//   256 of 1..200 20.8, -, 21.8
+// Direct calls.  Measured, us, 32 query heads on 8, D = 128 (with CTAs that fill an
+// SM, that fill half of one, split):
+//   1 context of 4096 7.0, 7.0, 12.3; of 32768 14.5, 18.4, 21.6; of 65536 23.4, 32.1,
+//   25.4; of 100000 32.4, 46.5, 35.8 (131072: split 37)
+//   4 of 8192 12.2, 12.5, 21.2; of 32768 32.7, 34.0, 37.1;  8 of 16384 32.6, 33.9, 38.1
+//   16 of 1024 7.6, 8.0, 16.7; of 4096 17.4, 19.3, 26.1;  19 of 4096 18.2, 19.9, 28.9
+//   32 (two units per SM) of 1024 -, 11.0, 20.8; of 4096 -, 33, 39
+// and with four warps (split beside them): 32 of 1024 13.9, of 4096 42; 64 of 128..2048
+// 26.6 (26.4); 100 of 1..500 13.9 (16.9); 256 of 1..200 20.8 (21.8).
+// A cluster of 16 CTAs that fill an SM each finds room 7 times, of 12 8 times: eight
+// units are better off with 12 (32768 tokens: 14.5 us; with 16 23.4, in two waves).
 constexpr int kDirectTokens = 1024;  // the longest context that four warps take
 constexpr int kDirectWaves = 4;      // of their CTAs
-constexpr int kManyTokens = 704;     // per warp of a CTA of kManyWarps
+constexpr int kManyTokens = 704;     // per warp of the larger CTAs
 
 struct Layout {
     size_t place, m, l, acc, total;
@@ -1080,13 +1087,42 @@ struct Pick {
     KernelFn fn;
     int warps, smem;
 };
-enum Kind { kSplit, kDirect, kDirectMany };
+enum Kind { kSplit, kDirect, kDirectMany, kDirectWhole };
+// Clusters of cs of its CTAs that run at once (once per kernel, size and device).
+int clusters_of(const Pick& use, int cs) {
+    static std::mutex mu;
+    static struct { KernelFn fn; int dev, cs, n; } cache[256];
+    static int used = 0;
+    int dev = 0;
+    if (resident_of(use.fn, use.smem, 32 * use.warps) < 1 || cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lk(mu);
+    for (int i = 0; i < used; ++i)
+        if (cache[i].fn == use.fn && cache[i].dev == dev && cache[i].cs == cs) return cache[i].n;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cs;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cs);
+    cfg.blockDim = dim3(32 * use.warps);
+    cfg.dynamicSmemBytes = use.smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, use.fn, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (used < 256) cache[used++] = {use.fn, dev, cs, n};
+    return n;
+}
 template <class E, int D, class C>
 Pick pick(Kind kind) {
     if constexpr (C::kNarrow && C::PASS < kTile) return {direct_kernel<E, D, C, kWarps>, kWarps, kWarps * kRingBytes<D>};
     else {
         constexpr int many = kManyWarps<D, C>;
         if (kind == kDirectMany) return {direct_kernel<E, D, C, many>, many, many * kRingBytes<D>};
+        if (kind == kDirectWhole) return {direct_kernel<E, D, C, 2 * many>, 2 * many, 2 * many * kRingBytes<D>};
         return {kind == kSplit ? split_kernel<E, D, C> : direct_kernel<E, D, C, kWarps>, kWarps, kWarps * kRingBytes<D>};
     }
 }
@@ -1181,17 +1217,19 @@ pkv_status pkv_paged_attention_decode_q4(void* out, const void* q, const void* k
     p.err = pkv::device_error_word();
     const int sms = pkv::sm_count();
     const int64_t units = (int64_t)S * Hkv;
-    // Few units, of more than a few tiles: clusters of CTAs of which an SM takes two,
-    // unless their warps' shares would be longer than kManyTokens.  Clusters grow
-    // while there is an SM per CTA and a tile per warp, to two CTAs per SM where
-    // their warps have four tiles.
-    Pick use = pick(dtype, D, kDirectMany, p.G);
+    // Few units, of more than a few tiles: CTAs that fill an SM, or, for up to two units
+    // per SM, half of one, unless their warps' shares would be longer than kManyTokens.
+    // Clusters grow while every fourth of their warps has a tile (1100 tokens: 7.5 us
+    // where each has one, 6.1) and all run at once.
+    Pick use = pick(dtype, D, units <= sms ? kDirectWhole : kDirectMany, p.G);
+    bool direct = units <= 2 * sms && max_ctx >= kDirectTokens;
     p.tile_log2 = 6;
     p.cs = 1;
-    while (p.cs < kMaxCluster && units * p.cs * 2 <= 2 * sms &&
-           max_ctx > (int64_t)use.warps * kTile * p.cs * (units * p.cs * 2 <= sms ? 1 : 4))
-        p.cs *= 2;
-    bool direct = units <= 2 * sms && max_ctx >= kDirectTokens && max_ctx <= (int64_t)kManyTokens * use.warps * p.cs;
+    for (int cs : {2, 4, 8, 12, 16})
+        if (direct && units * cs <= sms && max_ctx > (int64_t)use.warps * (kTile / 4) * p.cs &&
+            clusters_of(use, cs) >= units)
+            p.cs = cs;
+    direct = direct && max_ctx <= (int64_t)kManyTokens * use.warps * p.cs;
     if (!direct) {
         // Short contexts: a CTA of four warps per unit, or, while they fit the card at
         // once, clusters with a tile per warp.
