@@ -31,9 +31,13 @@
 //  * P^T comes out of S^T's accumulators by movmatrix.  A weight times its step
 //    enters the product as fp16, rounded by 2^-11 of itself: an eighth of a bf16
 //    output's own rounding.  For fp16 outputs, whose rounding is no larger, what is
-//    left enters as a second number.  Both factors are bounded by powers of two
-//    (2^kLazy, and the running maximum of the steps), and the units make 2^15 of
-//    their product: what falls below 2^-24 is 2^-39 of the largest.
+//    left enters as a second number.  The products' units are each head's and
+//    group's own and follow the largest of its products, which lies in 2^8 .. 2^15:
+//    what falls below 2^-24 is 2^-32 of the largest.  (Units by the steps alone, the
+//    same for all, take no vote on the products and are 1 % faster with up to 4 heads,
+//    2 to 5 % with more, 10 % where 16 heads have one tile per warp.  But a group whose
+//    steps are 2^30 below the other's, or a row with one such token of no weight, keeps
+//    no digits in them.)
 //  * The running maximum moves only when a logit passes it by more than kLazy: one
 //    vote per tile instead of three exchanges per head.
 //
@@ -77,11 +81,14 @@ constexpr int kRuns = kTile / q4::kUnit;     // runs of 8 tokens in it
 template <int D>
 constexpr int kStages = D == 128 ? 2 : 3;  // what 3 (4) CTAs per SM leave room for
 constexpr int kMaxRanges = 1824;  // CTAs of a split call
-// log2 of what a weight may pass 1 by.  It costs the weights' products that many bits
-// of range (the units below), and spares a scaling of every sum wherever a maximum
-// creeps up.
+// log2 of what a weight may pass 1 by: it spares a scaling of every sum wherever a
+// maximum creeps up.
 constexpr float kLazy = 6.f;
-constexpr float kUnits = 256.f;   // 2^(15 - 1 - kLazy): a step is below 2^(E + 1)
+// A weight's product with a step, in the units it enters fp16 with, stays below
+// kProductMost; units that have to be new make the largest kUnits to 2 kUnits, so that
+// the weights have as much room again.
+constexpr float kProductMost = 0x1p15f, kUnits = 256.f;
+constexpr float kUnitMost = 0x1p119f;  // of the units: the least step they are for is 2^-111
 
 // K (or V) of one stage.
 template <int D>
@@ -456,8 +463,13 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
 #pragma unroll
             for (int r = 0; r < NG; ++r) centres[x][r][h] = 0.f;
         }
-    float wu = 0.f;           // units of the weights: kUnits / 2^E; 0: no step seen yet
-    float step_most = 0.f;    // 2^(E + 1)
+    float wu[X][NG][HL];       // units of the weights' products with the steps: powers of two
+#pragma unroll
+    for (int x = 0; x < X; ++x)
+#pragma unroll
+        for (int r = 0; r < NG; ++r)
+#pragma unroll
+            for (int h = 0; h < HL; ++h) wu[x][r][h] = kUnitMost;
 
     // this lane's address in ldmatrix: matrix lane / 8, row lane % 8; x4 is two
     // chunks of two units
@@ -568,14 +580,8 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
         }
 
         // does a maximum move?
-        float most = 0.f;
-#pragma unroll
-        for (int sub = 0; sub < SUB; ++sub)
-#pragma unroll
-            for (int r = 0; r < NG; ++r)
-                most = q4::max3(most, E::to_float2(vpair[sub][0][r]).x, E::to_float2(vpair[sub][1][r]).x);
         float top[X][HL];
-        bool moves = most >= step_most && most > 0.f;
+        bool moves = false;
 #pragma unroll
         for (int x = 0; x < X; ++x)
 #pragma unroll
@@ -586,73 +592,104 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
                 top[x][h] = y * qs[x][h];
                 moves = moves || top[x][h] > a.m[x][h] + kLazy;
             }
+        // the sums of a head's group, and what is to come off them, by f
+        auto scale_sums = [&](int x, int r, int h, float f) {
+#pragma unroll
+            for (int c = 2 * r; c < 2 * r + 2; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a.at(x, c, e, h) *= f;
+            eight[x][r % CH][C::kNarrow ? r : h] *= f;
+            eight[x][r % CH][2 + (C::kNarrow ? r : h)] *= f;
+        };
         if (__any_sync(kFull, moves)) {
-            most = max_rows(most);
-            float fewer = 1.f;
-            if (most >= step_most && most > 0.f) {  // the same for the whole warp
-                const uint32_t ex = min(max(__float_as_uint(most) & 0x7f800000u, 0x08000000u), 0x7e800000u);
-                const float now = kUnits * __uint_as_float((254u << 23) - ex);
-                fewer = wu > 0.f ? now / wu : 1.f;
-                wu = now;
-                step_most = __uint_as_float(ex + 0x00800000u);
-            }
 #pragma unroll
             for (int x = 0; x < X; ++x)
 #pragma unroll
                 for (int h = 0; h < HL; ++h) {
                     const float y = fmaxf(max_rows(top[x][h]), a.m[x][h]);
-                    const float old = y == -INFINITY ? 1.f : exp2_of(a.m[x][h] - y);
+                    const float by = y == -INFINITY ? 0.f : y - a.m[x][h], old = exp2_of(-by);
                     a.m[x][h] = y;
                     less[x][h] = y == -INFINITY ? 0.f : -y;
                     a.l[x][h] *= old;
 #pragma unroll
-                    for (int r = 0; r < NG; ++r) centres[x][r][h] *= old;
-#pragma unroll
-                    for (int c = 0; c < NI; ++c)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) a.at(x, c, e, h) *= old * fewer;
-#pragma unroll
-                    for (int r = 0; r < CH; ++r)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (C::kNarrow || c % 2 == h) eight[x][r][c] *= old * fewer;
+                    for (int r = 0; r < NG; ++r) {
+                        centres[x][r][h] *= old;
+                        // the products so far keep their size: the units rise by as much, up to
+                        // the next power of two
+                        const int at = __float_as_int(wu[x][r][h]);
+                        const int up = min((int)ceilf(fminf(by, 300.f)), (__float_as_int(kUnitMost) - at) >> 23);
+                        wu[x][r][h] = __int_as_float(at + (up << 23));
+                        scale_sums(x, r, h, exp2_of((float)up - by));
+                    }
                 }
         }
 
-        // the weights times V's steps, as columns
+        // the weights, in the logits' place, and their products with V's steps, as columns
         uint32_t pb[SUB][X][CH][PARTS][2];
+        auto products = [&](int sub, int x, int u, int r) {
+            const float(&w)[HL] = v[x][sub][u];
+            const float s0 = E::to_float2(vpair[sub][u][r]).x;
+            const float w0 = w[0] * wu[x][r][0] * s0;
+            const float w1 = C::kNarrow ? (NG == 2 ? w[0] * wu[x][NG - 1][0] * E::to_float2(vpair[sub][u][NG - 1]).x : 0.f)
+                                        : w[HL - 1] * wu[x][r][HL - 1] * s0;
+            const uint32_t hi = pkv::F16::from_float2(w0, w1);
+            pb[sub][x][r][0][u] = transposed(hi);
+            if (PARTS == 2) {  // and what the rounding left
+                const float2 back = pkv::F16::to_float2(hi);
+                pb[sub][x][r][PARTS - 1][u] = transposed(pkv::F16::from_float2(w0 - back.x, w1 - back.y));
+            }
+            return *reinterpret_cast<const __half2*>(&hi);
+        };
+        __half2 most = __float2half2_rn(0.f);
 #pragma unroll
         for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
             for (int x = 0; x < X; ++x)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    float w[HL];
 #pragma unroll
                     for (int h = 0; h < HL; ++h) {
-                        w[h] = exp2_of(fmaf(v[x][sub][u][h], qs[x][h], less[x][h]));
-                        a.l[x][h] += w[h];
+                        float& w = v[x][sub][u][h];
+                        w = exp2_of(fmaf(w, qs[x][h], less[x][h]));
+                        a.l[x][h] += w;
+#pragma unroll
+                        for (int r = 0; r < NG; ++r)
+                            centres[x][r][h] = fmaf(w, E::to_float2(vpair[sub][u][r]).y, centres[x][r][h]);
                     }
-                    float su[NG];
+#pragma unroll
+                    for (int r = 0; r < CH; ++r) most = __hmax2(most, products(sub, x, u, r));
+                }
+        const float2 large = __half22float2(most);
+        if (__any_sync(kFull, fmaxf(large.x, large.y) >= kProductMost)) {  // new units
+#pragma unroll
+            for (int x = 0; x < X; ++x)
+#pragma unroll
+                for (int h = 0; h < HL; ++h)
 #pragma unroll
                     for (int r = 0; r < NG; ++r) {
-                        const float2 sc = E::to_float2(vpair[sub][u][r]);
-                        su[r] = sc.x * wu;
+                        float y = 0.f;
 #pragma unroll
-                        for (int h = 0; h < HL; ++h) centres[x][r][h] = fmaf(w[h], sc.y, centres[x][r][h]);
+                        for (int sub = 0; sub < SUB; ++sub)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+                                y = fmaxf(y, v[x][sub][u][h] * E::to_float2(vpair[sub][u][r]).x);
+                        y = max_rows(y);
+                        const uint32_t ex = min(max(__float_as_uint(y) & 0x7f800000u, 0x08000000u), 0x7e800000u);
+                        const int was = __float_as_int(wu[x][r][h]);
+                        const int now = y * wu[x][r][h] >= kProductMost
+                                            ? __float_as_int(kUnits * __uint_as_float((254u << 23) - ex)) : was;
+                        wu[x][r][h] = __int_as_float(now);
+                        scale_sums(x, r, h, __int_as_float(max(now - was + (127 << 23), 0)));  // now / was
                     }
 #pragma unroll
-                    for (int r = 0; r < CH; ++r) {
-                        const float w0 = w[0] * su[r];
-                        const float w1 = C::kNarrow ? (NG == 2 ? w[0] * su[NG - 1] : 0.f) : w[HL - 1] * su[r];
-                        const uint32_t hi = pkv::F16::from_float2(w0, w1);
-                        pb[sub][x][r][0][u] = transposed(hi);
-                        if (PARTS == 2) {  // and what the rounding left
-                            const float2 back = pkv::F16::to_float2(hi);
-                            pb[sub][x][r][PARTS - 1][u] = transposed(pkv::F16::from_float2(w0 - back.x, w1 - back.y));
-                        }
-                    }
-                }
+            for (int sub = 0; sub < SUB; ++sub)
+#pragma unroll
+                for (int x = 0; x < X; ++x)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int r = 0; r < CH; ++r) products(sub, x, u, r);
+        }
         const uint32_t minus8[4] = {kMinus8Even, kMinus8Odd, kMinus8Even, kMinus8Odd};
 #pragma unroll
         for (int sub = 0; sub < SUB; ++sub) {
@@ -697,7 +734,6 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
                         a.at(x, c, e, h) += eight[x][(c / 2) % CH][2 * (e & 1) + (C::kNarrow ? c / 2 : h)];
         feed.done();
     }
-    const float back = wu > 0.f ? 1.f / wu : 0.f;  // a power of two
 #pragma unroll
     for (int x = 0; x < X; ++x)
 #pragma unroll
@@ -705,7 +741,7 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
             a.l[x][h] = sum_rows(a.l[x][h]);
 #pragma unroll
             for (int r = 0; r < NG; ++r) {
-                const float c = sum_rows(centres[x][r][h]);
+                const float c = sum_rows(centres[x][r][h]), back = 1.f / wu[x][r][h];  // a power of two
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll

@@ -64,7 +64,7 @@ def attend_case(seed, S, H, Hkv, D, bs, dtype, lens, MB=None, spread=1.0):
                 v=pool_for(rng, NB, bs, Hkv, D, dtype, live, spread))
 
 
-def attend_reference(c):
+def attend_reference(c, own_units=False):
     """(out, bound) [S, H, D] in 64 bits.  The bound, with u = half a step of the
     output type and e = 2^-24:
      * a logit z_j = scale sum_r (step_r (sum_d q_d code_d - 8 sum_d q_d) + centre_r
@@ -80,7 +80,14 @@ def attend_reference(c):
        2^-11) or as two (fp16: r = 2^-22), or 2^-33 of the largest step off where it
        is below 2^-14 in units of 2^-8 (at most 8 codes up).
        With A = sum_j p_j (step_j |code_j - 8| + |centre_j|), A' the same with 16 more codes:
-         |out - ref| <= u |ref| + (1 + u) (A r + A' w + n 2^-30 max step) + 2^-25"""
+         |out - ref| <= u |ref| + (1 + u) (A r + A' w + n 2^-30 max step) + 2^-25
+       own_units, for inputs where that is far too much: the units of the weights are
+       each head's and group's own, so that what a weight is small beside is the
+       largest p_j step_j of that head and group; Z and Zq are each token's own, with 4 e
+       max |z| for the exponent's sum; below the least normal number a rounding is 2^-25
+       (fp16) or 2^-134 (bf16):
+         |out - ref| <= u |ref| + (1 + u) (A r + sum_j p_j (a_j + A16) w_j + n 2^-30 max_j p_j step_j)
+       and that, a_j = step_j (|code_j - 8| + 16) + |centre_j|, A16 = sum_j p_j a_j"""
     S, H, Hkv, D, bs, dtype = (c[x] for x in ("S", "H", "Hkv", "D", "bs", "dtype"))
     G, u = H // Hkv, U[dtype]
     out, bound = np.zeros((S, H, D)), np.zeros((S, H, D))
@@ -109,7 +116,16 @@ def attend_reference(c):
         Zq = abs(c["scale"]) * (np.abs(qq).max(-1) * kmag.sum(-1).max(-1)[:, None])
         w = 4 * (144 * E32 * Z + E32 * Zq) + 2.0 ** -21 + (n / 8 + 100) * 4 * E32
         A, A16, r = p @ vmag, p @ (vmag + 16 * vs), p @ v
-        b = u * np.abs(r) + (1 + u) * (A * r16 + A16 * w[..., None] + n * 2.0 ** -30 * vs.max()) + 2.0 ** -25
+        if own_units:
+            Z = abs(c["scale"]) * (np.abs(qq) @ kmag.transpose(0, 2, 1))
+            Zq = abs(c["scale"]) * np.abs(qq).max(-1)[..., None] * kmag.sum(-1)[:, None]
+            w = 2 * (144 * E32 * Z + E32 * Zq) + 4 * E32 * np.abs(z).max() + 2.0 ** -21 + (n / 8 + 100) * 4 * E32
+            off = (p * w) @ (vmag + 16 * vs) + (p * w).sum(-1, keepdims=True) * A16
+            small = n * 2.0 ** -30 * np.stack([(p[..., None] * vs[:, None, :, g:g + 64]).max(2) for g in range(0, D, 64)], 2)
+            small = small.reshape(Hkv, G, D)
+            b = u * np.abs(r) + (1 + u) * (A * r16 + off + small) + (2.0 ** -25 if dtype == "f16" else 2.0 ** -134)
+        else:
+            b = u * np.abs(r) + (1 + u) * (A * r16 + A16 * w[..., None] + n * 2.0 ** -30 * vs.max()) + 2.0 ** -25
         out[i], bound[i] = r.reshape(H, D), b.reshape(H, D)
     return out, bound
 
