@@ -63,6 +63,14 @@ def _scratch(nbytes, device, stream=None) -> torch.Tensor:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def _no_q4(who, *caches):
+    """Refuses 4-bit caches (new_cache_q4) in a call on 16-bit ones, which would
+    reach past their smaller blocks."""
+    for c in caches:
+        if c.dtype is torch.uint8:
+            _refuse(f"{who}: takes 16-bit caches, not 4-bit ones (uint8 {tuple(c.shape)})")
+
+
 def paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale=None,
                            max_context_len=0, partition_tokens=0, workspace=None, stream=None):
     """out[s,h] = softmax(scale q[s,h] K^T) V over each sequence's paged context.
@@ -70,6 +78,7 @@ def paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens,
     q, out: [S, H, D]; caches: [NB, bs, H, D]; block_tables [S, MB] int32;
     context_lens [S] int32 (all on the device).
     """
+    _no_q4("paged_attention_decode", k_cache, v_cache)
     S, H, D = q.shape
     NB, bs = k_cache.shape[0], k_cache.shape[1]
     MB = block_tables.shape[1]
@@ -94,6 +103,7 @@ def decode_step(out, q, key, value, k_cache, v_cache, block_tables, context_lens
     fewer kernels (see pkv_decode_step): the new tokens (key/value [T, H, D],
     seq_idx/pos [T] int32) are written into the caches, slot_mapping [T]
     int64 receives their slots, then out = attention over every context."""
+    _no_q4("decode_step", k_cache, v_cache)
     S, H, D = q.shape
     NB, bs = k_cache.shape[0], k_cache.shape[1]
     MB = block_tables.shape[1]
@@ -119,6 +129,7 @@ def paged_attention_decode_shared_prefix(out, q, k_cache, v_cache, block_tables,
     """paged_attention_decode where groups of sequences share a prefix
     (prefix_groups [G, 3] int32 on the device: first sequence, members,
     prefix tokens); the prefix is read once per group (tensor cores)."""
+    _no_q4("paged_attention_decode_shared_prefix", k_cache, v_cache)
     S, H, D = q.shape
     NB, bs = k_cache.shape[0], k_cache.shape[1]
     MB = block_tables.shape[1]
@@ -657,6 +668,7 @@ def compute_slot_mapping(slot_mapping, block_tables, seq_idx, pos, block_size, s
 
 
 def reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, stream=None):
+    _no_q4("reshape_and_cache", k_cache, v_cache)
     T, H, D = key.shape
     NB, bs = k_cache.shape[0], k_cache.shape[1]
     L.pkv_reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, T, H, D, bs, NB,
@@ -682,6 +694,7 @@ def copy_blocks(k_cache, v_cache, block_mapping, stream=None):
             _refuse("copy_blocks: k_cache and v_cache differ in type or shape")
         L.pkv_copy_blocks_q4(k_cache, v_cache, block_mapping, P, Hkv, D, bs, NB, stream)
         return
+    _no_q4("copy_blocks", v_cache)
     NB, bs, H, D = k_cache.shape
     L.pkv_copy_blocks(k_cache, v_cache, block_mapping, P, H, D, bs, NB,
                       dtype_code(k_cache.dtype), stream)
@@ -702,6 +715,7 @@ def swap_blocks(gpu_k, gpu_v, host_k, host_v, block_mapping, direction, stream=N
         L.pkv_swap_blocks_q4(gpu_k, gpu_v, host_k, host_v, block_mapping, P, Hkv, D, bs, NBg, host_k.shape[0],
                              direction, stream)
         return
+    _no_q4("swap_blocks", gpu_v, host_k, host_v)
     NBg, bs, H, D = gpu_k.shape
     L.pkv_swap_blocks(gpu_k, gpu_v, host_k, host_v, block_mapping, P, H, D, bs, NBg,
                       host_k.shape[0], dtype_code(gpu_k.dtype), direction, stream)
