@@ -692,6 +692,8 @@ def copy_blocks(k_cache, v_cache, block_mapping, stream=None):
         NB, Hkv, bs, _ = k_cache.shape
         if v_cache.dtype != _U8 or v_cache.shape != k_cache.shape:
             _refuse("copy_blocks: k_cache and v_cache differ in type or shape")
+        if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+            _refuse("copy_blocks: 4-bit caches must be contiguous")
         L.pkv_copy_blocks_q4(k_cache, v_cache, block_mapping, P, Hkv, D, bs, NB, stream)
         return
     _no_q4("copy_blocks", v_cache)
@@ -712,6 +714,8 @@ def swap_blocks(gpu_k, gpu_v, host_k, host_v, block_mapping, direction, stream=N
         if any(x.dtype != _U8 or x.dim() != 4 or x.shape[1:] != gpu_k.shape[1:] for x in (gpu_v, host_k, host_v)) \
                 or gpu_v.shape != gpu_k.shape or host_v.shape != host_k.shape:
             _refuse("swap_blocks: the 4-bit caches differ in type or shape")
+        if not all(x.is_contiguous() for x in (gpu_k, gpu_v, host_k, host_v)):
+            _refuse("swap_blocks: 4-bit caches must be contiguous")
         L.pkv_swap_blocks_q4(gpu_k, gpu_v, host_k, host_v, block_mapping, P, Hkv, D, bs, NBg, host_k.shape[0],
                              direction, stream)
         return

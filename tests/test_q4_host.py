@@ -58,3 +58,19 @@ def test_copies_and_swaps_of_16_bit_blocks_refuse_4_bit_pools(called):
     E.copy_blocks(k, v, pairs), E.swap_blocks(k, v, k, v, pairs, L.PKV_SWAP_IN)
     E.copy_blocks(k4, v4, pairs), E.swap_blocks(k4, v4, k4, v4, pairs, L.PKV_SWAP_IN)
     assert called == ["pkv_copy_blocks", "pkv_swap_blocks", "pkv_copy_blocks_q4", "pkv_swap_blocks_q4"]
+
+
+def test_copies_of_4_bit_blocks_refuse_pools_with_gaps(called):
+    """K and V interleaved in one tensor: the blocks do not follow one another."""
+    both = torch.zeros(4, 2, 2, 16, 36, dtype=torch.uint8)
+    k, v = both[:, 0], both[:, 1]
+    whole, pairs = caches(True), torch.zeros(1, 2, dtype=torch.int64)
+    for args in ((k, v), (whole[0], v)):
+        with pytest.raises(L.PkvError, match="copy_blocks.*contiguous"):
+            E.copy_blocks(*args, pairs)
+    for i in range(4):
+        args = [*whole, *whole]
+        args[i] = k
+        with pytest.raises(L.PkvError, match="swap_blocks.*contiguous"):
+            E.swap_blocks(*args, pairs, L.PKV_SWAP_OUT)
+    assert not called
