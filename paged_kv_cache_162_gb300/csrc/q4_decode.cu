@@ -861,7 +861,10 @@ __device__ __forceinline__ uint2 pack4(const float4& v, float f) {
 }
 
 // What the CTAs of a cluster send one another: 32 dims of a row ("segment") of
-// every CTA to the CTA that joins it, and every row's M and L to all.
+// every CTA to the CTA that joins it, and every row's M and L to all.  Behind the
+// rings, and only in calls with clusters: those have one CTA per SM, or few, and the
+// others would lose one to it (8 query heads per KV head, 256 units of 4096 tokens, one
+// CTA of six warps per SM and two: 48.8 and 35.8 us).
 template <int D, class C>
 struct ClusterIn {
     static constexpr int ROWS = C::kNarrow ? 4 : 8 * C::X, SEGS = ROWS * (D / 32);
@@ -870,17 +873,24 @@ struct ClusterIn {
     float m[kMaxCluster][ROWS], l[kMaxCluster][ROWS];
 };
 
+// CTAs of a direct call's W warps that an SM takes, without clusters
+template <int D, class C, int W>
+constexpr int kDirectCtas = W == kWarps ? kCtas<D, C> : W == kManyWarps<D, C> ? 2 : 1;
+constexpr int kSmemPerSm = 228 * 1024, kSmemReserved = 1024;  // the system's, per CTA
+
 // Direct: cluster c / cs takes unit c / cs (hw = 1), its CTAs equal parts of
 // the unit's tiles, their W warps a stage each in turn.
 template <class E, int D, class C, int W>
-__global__ void __launch_bounds__(32 * W, W == kWarps ? kCtas<D, C> : W == kManyWarps<D, C> ? 2 : 1) direct_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(32 * W, kDirectCtas<D, C, W>) direct_kernel(const __grid_constant__ Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     constexpr int SEGS = D / 32;
     extern __shared__ __align__(128) char smem[];
-    __shared__ ClusterIn<D, C> in;
     __shared__ __align__(8) unsigned long long full[W][kStages<D>];
     __shared__ int abort;
+    static_assert(kDirectCtas<D, C, W> * (W * kRingBytes<D> + sizeof full + sizeof abort + kSmemReserved) <= kSmemPerSm,
+                  "the CTAs that the registers are for");
+    ClusterIn<D, C>& in = *reinterpret_cast<ClusterIn<D, C>*>(smem + W * kRingBytes<D>);  // cs > 1
     if (p.cs > 1) cluster_arrive();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) abort = 0;
@@ -1093,9 +1103,12 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) join_kernel(cons
 //   25.4; of 100000 32.4, 46.5, 35.8 (131072: split 37)
 //   4 of 8192 12.2, 12.5, 21.2; of 32768 32.7, 34.0, 37.1;  8 of 16384 32.6, 33.9, 38.1
 //   16 of 1024 7.6, 8.0, 16.7; of 4096 17.4, 19.3, 26.1;  19 of 4096 18.2, 19.9, 28.9
-//   32 (two units per SM) of 1024 -, 11.0, 20.8; of 4096 -, 33, 39
-// and with four warps (split beside them): 32 of 1024 13.9, of 4096 42; 64 of 128..2048
-// 26.6 (26.4); 100 of 1..500 13.9 (16.9); 256 of 1..200 20.8 (21.8).
+//   32 (two units per SM) of 1024 -, 11.0, 21.2; of 4096 -, 33, 38
+//   and with 64 query heads: 32 of 1024 -, 13.4, 23.9; of 4096 -, 37.8, 44.4; D = 64: 32 of
+//   1024 -, 9.0, 22.3; of 5600 -, 30.9, 44.2
+// and with four warps (split beside them): 32 of 1024 13.9, of 4096 44; 64 of 128..2048
+// 26.9 (28.5); 100 of 1..500 14.0 (17.8); 220 of 1..1000 38.2 (43.5), with 64 query heads
+// 45.4 (52.3); 256 of 1..200 20.9 (22.5).
 // A cluster of 16 CTAs that fill an SM each finds room 7 times, of 12 8 times: eight
 // units are better off with 12 (32768 tokens: 14.5 us; with 16 23.4, in two waves).
 constexpr int kDirectTokens = 1024;  // the longest context that four warps take
@@ -1118,11 +1131,16 @@ Layout layout_of(int S, int H, int Hkv, int D) {
     return L;
 }
 
-// A kernel, its warps, and the shared memory of their rings.
+// A kernel, its warps, the shared memory of their rings, and what a cluster adds.
 struct Pick {
     KernelFn fn;
-    int warps, smem;
+    int warps, rings, more;
+    int smem(int cs) const { return rings + (cs > 1 ? more : 0); }
 };
+// Its CTAs that an SM takes, in clusters of cs.
+int resident_of(const Pick& use, int cs) {
+    return resident_of(use.fn, use.smem(cs), 32 * use.warps, use.rings + use.more);
+}
 enum Kind { kSplit, kDirect, kDirectMany, kDirectWhole };
 // Clusters of cs of its CTAs that run at once (once per kernel, size and device).
 int clusters_of(const Pick& use, int cs) {
@@ -1130,7 +1148,7 @@ int clusters_of(const Pick& use, int cs) {
     static struct { KernelFn fn; int dev, cs, n; } cache[256];
     static int used = 0;
     int dev = 0;
-    if (resident_of(use.fn, use.smem, 32 * use.warps) < 1 || cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (resident_of(use, cs) < 1 || cudaGetDevice(&dev) != cudaSuccess) return 0;
     std::lock_guard<std::mutex> lk(mu);
     for (int i = 0; i < used; ++i)
         if (cache[i].fn == use.fn && cache[i].dev == dev && cache[i].cs == cs) return cache[i].n;
@@ -1141,7 +1159,7 @@ int clusters_of(const Pick& use, int cs) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cs);
     cfg.blockDim = dim3(32 * use.warps);
-    cfg.dynamicSmemBytes = use.smem;
+    cfg.dynamicSmemBytes = use.smem(cs);
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
@@ -1154,12 +1172,14 @@ int clusters_of(const Pick& use, int cs) {
 }
 template <class E, int D, class C>
 Pick pick(Kind kind) {
-    if constexpr (C::kNarrow && C::PASS < kTile) return {direct_kernel<E, D, C, kWarps>, kWarps, kWarps * kRingBytes<D>};
+    constexpr int ring = kRingBytes<D>, more = sizeof(ClusterIn<D, C>);
+    if constexpr (C::kNarrow && C::PASS < kTile) return {direct_kernel<E, D, C, kWarps>, kWarps, kWarps * ring, more};
     else {
         constexpr int many = kManyWarps<D, C>;
-        if (kind == kDirectMany) return {direct_kernel<E, D, C, many>, many, many * kRingBytes<D>};
-        if (kind == kDirectWhole) return {direct_kernel<E, D, C, 2 * many>, 2 * many, 2 * many * kRingBytes<D>};
-        return {kind == kSplit ? split_kernel<E, D, C> : direct_kernel<E, D, C, kWarps>, kWarps, kWarps * kRingBytes<D>};
+        if (kind == kDirectMany) return {direct_kernel<E, D, C, many>, many, many * ring, more};
+        if (kind == kDirectWhole) return {direct_kernel<E, D, C, 2 * many>, 2 * many, 2 * many * ring, more};
+        if (kind == kSplit) return {split_kernel<E, D, C>, kWarps, kWarps * ring, 0};
+        return {direct_kernel<E, D, C, kWarps>, kWarps, kWarps * ring, more};
     }
 }
 template <class E, int D>
@@ -1272,9 +1292,9 @@ pkv_status pkv_paged_attention_decode_q4(void* out, const void* q, const void* k
         const bool brief = max_ctx <= kWarps * kTile;
         use = pick(dtype, D, kDirect, p.G, brief);
         p.tile_log2 = brief ? 5 : 6;
-        const int64_t slots = (int64_t)resident_of(use.fn, use.smem) * sms;
         p.cs = 1;
-        direct = max_ctx <= kDirectTokens && units <= kDirectWaves * slots;
+        direct = max_ctx <= kDirectTokens && units <= (int64_t)kDirectWaves * resident_of(use, 1) * sms;
+        const int64_t slots = (int64_t)resident_of(use, 2) * sms;
         while (direct && p.cs < kMaxCluster && units * p.cs * 2 <= slots && max_ctx > (int64_t)kWarps * kTile * p.cs)
             p.cs *= 2;
     }
@@ -1282,7 +1302,7 @@ pkv_status pkv_paged_attention_decode_q4(void* out, const void* q, const void* k
         use = pick(dtype, D, kSplit, p.G);
         p.tile_log2 = 6;
     }
-    const int per_sm = resident_of(use.fn, use.smem, 32 * use.warps);
+    const int per_sm = resident_of(use, p.cs);
     if (per_sm < 1) return bad(PKV_ERR_CUDA, "the kernel cannot be resident");
     p.hw = direct ? 1 : heads_per_cta(Hkv);
     while (!direct && p.hw > 1 && (int64_t)S * Hkv / p.hw < kMinUnits) p.hw /= 2;
@@ -1303,7 +1323,7 @@ pkv_status pkv_paged_attention_decode_q4(void* out, const void* q, const void* k
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(32 * use.warps);
-    cfg.dynamicSmemBytes = use.smem;
+    cfg.dynamicSmemBytes = use.smem(p.cs);
     cfg.stream = pkv::as_stream(stream);
     cfg.attrs = attr;
     cfg.numAttrs = direct && p.cs > 1 ? 2 : 1;

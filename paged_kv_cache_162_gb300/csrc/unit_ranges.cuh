@@ -345,11 +345,12 @@ int heads_per_cta(int Hkv) { return Hkv % 4 == 0 ? 4 : (Hkv % 2 == 0 ? 2 : 1); }
 
 using KernelFn = void (*)(Params);
 
-// Resident CTAs per SM of an attention kernel, after allowing it its shared
-// memory (once per kernel and device); 0 if it cannot run.
-int resident_of(KernelFn fn, int smem, int threads = kThreads) {
+// Resident CTAs per SM of an attention kernel with smem bytes of shared memory,
+// after allowing it `most` (0: as many), once per kernel, size and device; 0 if it
+// cannot run.
+int resident_of(KernelFn fn, int smem, int threads = kThreads, int most = 0) {
     static std::mutex mu;
-    static struct { KernelFn fn; int dev; int n; } cache[128];
+    static struct { KernelFn fn; int dev, smem, n; } cache[256];
     static int used = 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -358,15 +359,15 @@ int resident_of(KernelFn fn, int smem, int threads = kThreads) {
     }
     std::lock_guard<std::mutex> lk(mu);
     for (int i = 0; i < used; ++i)
-        if (cache[i].fn == fn && cache[i].dev == dev) return cache[i].n;
+        if (cache[i].fn == fn && cache[i].dev == dev && cache[i].smem == smem) return cache[i].n;
     int n = 0;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most > smem ? most : smem) != cudaSuccess ||
         cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
-    if (used < 128) cache[used++] = {fn, dev, n};
+    if (used < 256) cache[used++] = {fn, dev, smem, n};
     return n;
 }
 
