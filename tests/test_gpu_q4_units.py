@@ -86,3 +86,14 @@ def test_weights_that_climb_while_steps_fall(G, split, climbs):
     ups = np.zeros((c["k"].shape[0] * bs, 1, 1))
     ups[rows, 0, 0] = -powers
     check(scaled(c, ups.reshape(-1, bs, 1, 1)))
+
+
+@pytest.mark.parametrize("G", [2, 5, 11])
+def test_the_largest_queries(G):
+    """Up to 2^113 (not itself): the elements' units, and the logits'."""
+    c = C.attend_case(35, 2, G, 1, 64, 16, "bf16", [90, 700], spread=0.0)
+    q = Q.widen(c["q"], "bf16").reshape(2, G, 64)
+    q *= 1.99 * 2.0 ** 112 / np.abs(q).max(-1, keepdims=True)
+    step, centre, code = Q.parts(c["k"], 64)
+    step, centre = (Q.narrow(Q.widen(x, "bf16") * 2.0 ** -112, "bf16") for x in (step, centre))
+    check(dict(c, q=Q.narrow(q, "bf16"), k=Q.pack(step, centre, code)))
