@@ -377,13 +377,18 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores,
  * The 4-bit cache: K and V pools of uint8 [NB][Hkv][bs][RB], RB =
  * pkv_cache_q4_row_bytes(D) = D/2 + D/16.  A row's elements go in groups of
  * 64; element i of a group reads as centre + step * (code - 8), code 0..15:
- *   step = (max - min) / 15, centre = (8 max + 7 min) / 15 of the group, each
- *   rounded once to dtype; code = round((x - centre) / step) + 8 within 0..15
- *   (halves to even), 8 where step is 0 (or, in bf16, below 2^-126: then 0 is
- *   stored).
- * An element is off by at most step / 2 and what rounding step and centre
- * moves the ends: 8 u |step| + u |centre|, u = 2^-11 (fp16), 2^-8 (bf16).  A
- * group with an element that is not finite reads as NaN.  (An fp16 K whose
+ *   step = (max - min) / 15, centre = (8 max + 7 min) / 15 of the group, in fp32
+ *   (every sum and product rounded, the division a product with fp32's 1/15; no
+ *   sum overflows), then rounded to dtype: as the quotients rounded once, but
+ *   where those are within 2^-21 of halfway between two of the type's numbers;
+ *   code = round((x - centre) / step) + 8 within 0..15 (halves to even), 8 where
+ *   step is 0 (or, in bf16, below 2^-126: then 0 is stored).
+ * An element is off by at most
+ *   (1/2 + 2^-18) step + u (8 step + |centre|) + a,
+ * half a step and what rounding step and centre moves the ends: u = 2^-11 + 2^-21
+ * (fp16), 2^-8 + 2^-21 (bf16); a = 2^-21 (fp16: steps and centres below its normal
+ * numbers), 2^-122 (bf16: steps stored as 0).  A group with an element that is not
+ * finite reads as NaN.  (An fp16 K whose
  * rotation passes 65504 may make a centre, and its group, infinite.)
  * Order of a (block, head) in memory: for every 8 tokens their 8 rows of D/2
  * code bytes (byte j: elements 2j, in the low nibble, and 2j + 1; the 16-byte

@@ -340,3 +340,21 @@ def test_many_tokens_are_as_few_at_a_time(kw, q4):
     qref, qmag = C.rotated(c, "query", np.float64)
     check16(C.bits_of(got[0][2])[live], qref[live], qmag[live], c["dtype"])
     assert L.pkv_get_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_steps_and_centres_beside_the_64_bit_quotients(dtype):
+    """Groups whose quotients lie halfway between two 16-bit numbers, or whose ends are far apart in
+    size: within what the header says of the rounding, which here knows of no fp32."""
+    from test_q4_cpu import check_rounding, ends_apart
+    x = ends_apart(np.random.default_rng(9), dtype, 4096).reshape(2048, 1, 128)
+    k, v = E.new_cache_q4(128, 16, 1, 128), E.new_cache_q4(128, 16, 1, 128)
+    rows = C.tensor(Q.narrow(x, dtype), dtype).cuda()
+    at = torch.arange(2048, dtype=torch.int32, device="cuda")
+    slots = torch.empty(2048, dtype=torch.int64, device="cuda")
+    E.rotate_and_cache_q4(rows, rows, k, v, torch.arange(128, dtype=torch.int32, device="cuda")[None],
+                          torch.zeros_like(at), at, slots)
+    for cache in (k, v):
+        step, centre, code = (y.reshape(2048, 1, -1) for y in Q.parts(cache.cpu().numpy(), 128))
+        check_rounding(x, step, centre, code, dtype)
+    assert L.pkv_get_device_errors() == 0

@@ -320,3 +320,61 @@ def test_the_workloads_lay_the_cache_out_alike():
         pool = M._pack(x, torch.bfloat16).view(3, 2, 8, Q.row_bytes(D))
         v = Q.values(pool.numpy(), D, "bf16")
         assert np.array_equal(v, M._unpack(pool, D, torch.bfloat16).double().numpy())
+
+
+# ---------------------------------------------------------------- how step and centre are rounded
+def ends_apart(rng, dtype, n):
+    """Rows [n, 64] that both 16-bit types hold, with ends far apart in size and, in part, with
+    max - min or 8 max + 7 min at 15 times a number halfway between two of the type's."""
+    bits = 11 if dtype == "f16" else 8
+    x = np.zeros((n, 64))
+    half = (2 * rng.integers(1 << (bits - 1), 1 << bits, n) + 1) * 15.0     # times 2^-k below
+    hi = np.floor(half * rng.uniform(0.01, 0.99, n) / 2 ** (17 - bits)) * 2 ** (17 - bits)
+    x[:, 0], x[:, 1] = hi, hi - half
+    wide = np.exp2(rng.integers(-6, 7, n))
+    x[::3, 0], x[::3, 1] = rng.integers(1, 200, x[::3].shape[0]) * wide[::3], -rng.integers(1, 200, x[::3].shape[0]) / 64
+    x = Q.widen(Q.narrow(x / 512, dtype), dtype)
+    lo, hi = x.min(-1, keepdims=True), x.max(-1, keepdims=True)
+    mid = Q.widen(Q.narrow(lo + (hi - lo) * rng.uniform(0, 1, (n, 64)), dtype), dtype)
+    mid[:, :2] = x[:, :2]
+    return np.clip(mid, lo, hi)
+
+
+def rounding_bound(step, centre, dtype):
+    """What include/pagedkv.h says that an element may be off by."""
+    u = C.U[dtype] + 2.0 ** -21
+    return step * (0.5 + 2.0 ** -18) + u * (8 * step + np.abs(centre)) + (2.0 ** -21 if dtype == "f16" else 2.0 ** -122)
+
+
+def check_rounding(x, step, centre, code, dtype):
+    """step, centre (bits) and codes of rows x: the 64-bit quotients rounded once, but for those within
+    2^-21 of halfway, which may go to either side; values within the bound."""
+    g = x.reshape(x.shape[:-1] + (-1, 64))
+    hi, lo = g.max(-1), g.min(-1)
+    size = np.maximum(np.abs(hi), np.abs(lo))
+    for got, exact, slack in ((step, (hi - lo) / 15, (hi - lo) / 15 * 2.0 ** -21),
+                              (centre, (8 * hi + 7 * lo) / 15, size * 2.0 ** -21)):
+        below, above = (Q.widen(Q.narrow(exact + s, dtype), dtype) for s in (-slack, slack))
+        value = Q.widen(got, dtype)
+        assert ((below <= value) & (value <= above)).all()
+    s, a = (np.repeat(Q.widen(y, dtype), 64, -1).reshape(x.shape) for y in (step, centre))
+    assert (np.abs(a + s * (code - 8) - x) <= rounding_bound(s, a, dtype)).all()
+    return (step != Q.narrow((hi - lo) / 15, dtype)).sum()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_step_and_centre_are_those_of_fp32_numbers(dtype):
+    """A product with fp32's 1/15, rounded again to 16 bits: a quotient halfway between two 16-bit
+    numbers may go to either, and every element keeps the stated bound."""
+    rng = np.random.default_rng(8)
+    x = ends_apart(rng, dtype, 6000)
+    assert check_rounding(x, *Q.quantise(x, dtype, np.float32), dtype) > 0
+    assert check_rounding(x, *Q.quantise(x, dtype), dtype) == 0
+    # steps and centres below fp16's normal numbers, down to a step of 0
+    small = rng.standard_normal((3000, 64)) * np.exp2(rng.integers(-24, -12, (3000, 1)))
+    small = Q.widen(Q.narrow(small, "f16"), "f16")
+    for wide in (np.float32, np.float64):
+        step, centre, code = Q.quantise(small, "f16", wide)
+        s, a = (np.repeat(Q.widen(y, "f16"), 64, -1) for y in (step, centre))
+        assert (step == 0).any()
+        assert (np.abs(a + s * (code - 8) - small) <= rounding_bound(s, a, "f16")).all()
