@@ -412,10 +412,12 @@ size_t pkv_cache_q4_row_bytes(int D);
  * products and sums in fp32, each rounded, and one rounding to dtype (K of the
  * 4-bit form: none before it is quantised).  V is not rotated.
  * A token with pos[t] < 0 is padding: slot -1, nothing else is written for it.
- * The same where the slot is not to be found or is out of range (the bits of
- * pkv_compute_slot_mapping and pkv_reshape_and_cache), or the rotary position
- * outside [0, table_rows) (slot -1, PKV_DEVERR_POSITION).  Slots must be
- * distinct within a call.
+ * The same where the slot is not to be found (the bits of
+ * pkv_compute_slot_mapping), or the rotary position outside [0, table_rows)
+ * (PKV_DEVERR_POSITION).  A slot of NB*bs or more (a block id that the pool does
+ * not have) is written to slot_mapping as it was found, as by
+ * pkv_compute_slot_mapping; nothing else is written for its token, and
+ * PKV_DEVERR_SLOT is set.  Slots must be distinct within a call.
  *   key, value   [T][Hkv][D] dtype, rows of a token contiguous, tokens
  *                key_stride / value_stride elements apart (multiples of 8,
  *                below 2^30): slices of one projection need no copy
