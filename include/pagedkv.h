@@ -466,7 +466,10 @@ size_t pkv_decode_q4_workspace_size(int S, int H, int Hkv, int D);
  * that the caches stand for.  Arguments, limits and the promises about capture,
  * equal bits and bounded waits as in pkv_paged_attention_decode_window, whose
  * window it has not; the workspace needs pkv_decode_q4_workspace_size bytes.
- * Queries lie below 2^113 (a larger one makes its row NaN). */
+ * The weights, times V's steps, enter the products as fp16: rounded by 2^-11 of
+ * themselves for bf16 outputs, by 2^-22 (two numbers) for fp16 ones, and by 2^-33 of
+ * the largest of the same head and group at least; logits, sums and the normaliser
+ * are fp32.  Queries lie below 2^113 (a larger one may make its row NaN). */
 pkv_status pkv_paged_attention_decode_q4(
     void* out, const void* q, const void* k_cache, const void* v_cache,
     const int32_t* block_tables, const int32_t* context_lens,

@@ -24,8 +24,8 @@
 //    the end: sums that grow with the context would lose digits).
 //  * K: ldmatrix gives a lane 8 codes of one token, 32 bits; q is loaded in the
 //    order that makes of them two fragments.  A power of two per head makes q
-//    fp16 with the codes' units taken out, exact but for elements below 2^-32 of
-//    the largest.
+//    fp16 with the codes' units taken out, exact but for elements below 2^-23 (fp16)
+//    or 2^-26 (bf16) of the largest: what they lose is below 2^-34 of it.
 //  * V: transposing ldmatrix of 16-bit pieces, 4 codes of one token each, gives a
 //    lane 4 codes of two neighbouring tokens: the pairs that the product's k wants.
 //  * P^T comes out of S^T's accumulators by movmatrix.  A weight times its step
@@ -417,8 +417,8 @@ __device__ __forceinline__ void attend(const Params& p, Feed<D>& feed, int s, in
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
         // the power of two at or below the largest; its inverse times what the codes'
-        // units ask for makes the query fp16, below 2^14 (past 2^112 only bf16's
-        // last powers are left, and their logits' units would not be finite); a
+        // units ask for makes the query fp16, below 2^14 (it stops at 2^112: queries of
+        // 2^113 are bf16's last powers, and their logits' units would not be finite); a
         // negative scale is the query's sign
         const uint32_t ex = min(max(__float_as_uint(top) & 0x7f800000u, 0x08000000u), 0x77800000u);
         const float unit = __uint_as_float(ex);
