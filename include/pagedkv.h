@@ -469,7 +469,8 @@ size_t pkv_decode_q4_workspace_size(int S, int H, int Hkv, int D);
  * The weights, times V's steps, enter the products as fp16: rounded by 2^-11 of
  * themselves for bf16 outputs, by 2^-22 (two numbers) for fp16 ones, and by 2^-33 of
  * the largest of the same head and group at least; logits, sums and the normaliser
- * are fp32.  Queries lie below 2^113 (a larger one may make its row NaN). */
+ * are fp32.  Queries lie below 2^113 (a larger one may make its row NaN), and
+ * NB * bs * Hkv below 2^34. */
 pkv_status pkv_paged_attention_decode_q4(
     void* out, const void* q, const void* k_cache, const void* v_cache,
     const int32_t* block_tables, const int32_t* context_lens,

@@ -30,8 +30,10 @@
 //    lane 4 codes of two neighbouring tokens: the pairs that the product's k wants.
 //  * P^T comes out of S^T's accumulators by movmatrix.  A weight times its step
 //    enters the product as fp16, rounded by 2^-11 of itself: an eighth of a bf16
-//    output's own rounding.  For fp16 outputs, whose rounding is no larger, what is
-//    left enters as a second number.  The products' units are each head's and
+//    output's own rounding (a second number makes bf16 calls 8 to 20 % slower, and no
+//    more exact: 1.6e-3 off 64 bits either way, which is the outputs' rounding).  For
+//    fp16 outputs, whose rounding is no larger, what is left does enter as a second
+//    number.  The products' units are each head's and
 //    group's own and follow the largest of its products, which lies in 2^8 .. 2^15:
 //    what falls below 2^-24 is 2^-32 of the largest.  (Units by the steps alone, the
 //    same for all, take no vote on the products and are 1 % faster with up to 4 heads,
@@ -41,19 +43,23 @@
 //  * The running maximum moves only when a logit passes it by more than kLazy: one
 //    vote per tile instead of three exchanges per head.
 //
-// Measured, D = 128 (in brackets what the bytes take at a plain copy's rate, 6.78
-// TB/s): 32 contexts of 4001..16384, 32 heads in fp16, 263 us (222); 32 of 32768, 8
-// KV heads of 4 query heads in bf16, 200 (178), of 16384 106 (89): what a token adds
-// runs at 95 % of that rate.  256 of 16..4096 60 (36); one of 32768 14.5 (6); a handful
-// of short ones 3.2.  Bounds, long batches: the SMs' issue (the tensor pipe 44 %
-// busy, the ALU, which unpacks, 52 %) beside DRAM at 73 % of its peak.  Mixed lengths:
-// that and the ends, 5 us until the rings are full, CTAs of an SM that end up to 10
-// us apart, as its older warps go first, and the join, 4 to 8 us.  Few units: the
-// chain of a warp's tile, 1.2 us per 64 tokens.  None of these gained: stages of 32
-// tokens (73 us where these take 65.5), passes of 16 tokens with a fourth CTA per SM
-// (77 for 67), two CTAs of 255 registers per SM (the same), three or four stages for
-// few units (the same), ranges of one tile (116 for 110), ranges by a CTA's turn on
-// its SM (113 to 119 for 110).
+// Measured, D = 128 (in brackets what the bytes take at a plain copy's rate, 6.80
+// TB/s): 32 contexts of 4001..16384, 32 heads in fp16, 266 us (221); 32 of 32768, 8
+// KV heads of 4 query heads in bf16, 204 (178), of 16384 108 (89): what a token adds
+// runs at 93 % of that rate.  256 of 16..4096 60 (35); one of 32768 14.5 (6); a handful
+// of short ones 3.4.  With 8 and with 16 query heads per KV head, whose products, weights
+// and registers are more: 32 of 16384 126 and 184 (89), 256 of 16..4096 70 and 106 (36,
+// 37), one of 32768 17.3 and 25.9 (6).  What bounds it: nothing is busy all the time.
+// Long batches have DRAM at 72 % of its peak, the tensor pipe at 43 %, the ALU, which
+// unpacks, at 51 %, and issue at 54 %; a warp's chain of products waits for the pipes,
+// and 12 warps are what the registers hold (the forms of D = 128 spill 8 to 60 bytes
+// at that).  Mixed lengths: that and the ends, 5 us until the rings are full, CTAs of
+// an SM that end up to 10 us apart, as its older warps go first, and the join, 4 to 8
+// us.  Few units: eight of them fill 96 SMs of 152 with twelve warps, whose next tiles
+// cost 2.4 us each.  None of these gained: stages of 32 tokens (73 us where these take
+// 65.5), passes of 16 tokens with a fourth CTA per SM (77 for 67), two CTAs of 255
+// registers per SM (the same), three or four stages for few units (the same), ranges
+// of one tile (116 for 110), ranges by a CTA's turn on its SM (113 to 119 for 110).
 #include <cooperative_groups.h>
 
 #include <climits>

@@ -22,10 +22,12 @@
 // Measured, D = 128: 16 prompts of 320..1727 tokens, 32 + 32 + 32 heads in fp16,
 // interleaved: 135 us, 5.96 TB/s of what it has to move, 88 % of a plain copy's rate.
 // 20 thousand tokens of 8 KV heads into 4 bits, with 32 query heads turned by 64
-// dims: 96 us, 4.5 TB/s, bound by instructions issued (the codes are 8 per element,
-// and half the threads wait while the other half's dims turn).  4-bit rows of 64
-// contexts back to fp16: 233 us, 6.26 TB/s, 92 %.  250 decoding sequences: 3.6 us,
-// 3.9 in 4 bits; a handful of tokens 3.2: launch, position -> block -> slot, row.
+// dims: 98 us, 4.4 TB/s (64 us at a plain copy's rate).  It issues on 64 % of the cycles
+// (8 instructions per element for the codes; half the threads wait while the other
+// half's dims turn), has DRAM at 49 % of its peak, and for the rest waits for rows: one
+// of 32 bytes on its way per thread is 28 KB per SM.  4-bit rows of 64 contexts back to
+// fp16: 234 us, 6.25 TB/s, 92 %.  250 decoding sequences: 3.7 us, 5.0 in 4 bits; a
+// handful of tokens 2.7 to 3.4: launch, position -> block -> slot, row.
 #include <cmath>
 #include <cstdio>
 
