@@ -130,3 +130,25 @@ def test_two_units_per_sm(S, Hkv, G, D, dtype, hi):
     ref, bound = C.attend_reference(c)
     assert (np.abs(Q.widen(C.bits_of(out), dtype) - ref) <= bound).all()
     assert L.pkv_get_device_errors() == 0
+
+
+def test_large_and_small_ranges_captured():
+    """Launch control in a replayed graph, after the lengths have changed."""
+    rng = np.random.default_rng(7)
+    lens = rng.integers(38000, 47001, 64)
+    lens[5] = 47000
+    c = shared_case(44, 64, 4, 2, 64, 32, "bf16", lens)
+    d = C.on_gpu(c)
+    ws = E.new_q4_workspace(64, 8, 4, 64)
+    out = run(c, d, ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        E.paged_attention_decode_q4(out, d["q"], d["k"], d["v"], d["tables"], d["lens"], c["scale"], workspace=ws)
+    for low in (38000, 1):
+        now = rng.integers(low, 47001, 64)
+        now[9] = 47000
+        d["lens"].copy_(torch.from_numpy(now))
+        out.fill_(3)
+        g.replay()
+        torch.cuda.synchronize()
+        check(dict(c, lens=now.astype(np.int32)), out)
